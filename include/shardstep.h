@@ -59,6 +59,8 @@ extern "C" {
 #define SHARDSTEP_DTYPE_F16 2 /* IEEE half: gradients under fp16 loss scaling */
 
 #define SHARDSTEP_MAX_ND 64 /* largest N_d a kernel accepts */
+#define SHARDSTEP_MAX_GROUPS 8    /* hyper-parameter groups of one tensors_adamw_step */
+#define SHARDSTEP_MOMENT_BLOCK 256 /* elements that share a scale of the 8-bit moments */
 
 /* ------------------------------------------------------------ types */
 
@@ -731,6 +733,182 @@ int shardstep_ckpt_verify(const char* path);
  * it exceeds cap). */
 int fsdp_reshard_plan(int64_t total, int32_t old_nd, int32_t new_nd, int32_t new_rank,
                       shardstep_ckpt_piece_t* pieces, int32_t cap, int32_t* n_pieces);
+
+/* ------------------------------------------------- losses over tokens */
+
+/* The loss that starts a tuning step, straight from the logits of a language
+ * model, forward and (where `grad` is given) backward in the same call.  The
+ * gradient leaves multiplied by grad_scale (e.g. 1/M of [P1] section "Naïve
+ * Data Parallelism") and by the gradient scaler's loss scale ([P2] section
+ * 3.5), which stays on the device.  Per token i with logits x, id y:
+ *     a = (x_y - max x) - log(sum exp(x - max x)),   logps[i] = a
+ *     d loss / d x = c (1[y] - softmax x),           c = d loss / d a
+ * Statistics, terms and c are fp32, sums over tokens double; the gradient is
+ * rounded once to the logits' type.  A token of weight 0 takes no part: its
+ * logits and id are not read, its logps entry and gradient row are 0.  An id
+ * outside [0, vocab) makes its token's log probability NaN, and the loss with
+ * it. */
+typedef struct {
+    const void* logits;       /* device, row i at logits + i * row_stride       */
+    int64_t row_stride;       /* elements, >= vocab                              */
+    int32_t dtype;            /* SHARDSTEP_DTYPE_BF16, _F16 or _F32              */
+    int32_t id_bytes;         /* 4 or 8: int32 or int64 ids                      */
+    const void* ids;          /* device, n_tokens                                */
+    int64_t n_tokens;         /* 0 .. 2^31 - 1                                   */
+    int64_t vocab;            /* 1 .. 2^31 - 1                                   */
+    const float* weights;     /* device, n_tokens, or NULL: ones                 */
+    const float* ref_logps;   /* device, n_tokens: the reference model's         */
+    float* logps;             /* device, n_tokens, written                       */
+    void* grad;               /* device, rows of `dtype`, or NULL: forward only; */
+                              /* the logits themselves (same stride) are allowed */
+    int64_t grad_stride;      /* elements, >= vocab                              */
+    float grad_scale;
+    float norm;               /* divisor of the loss; 0: the sum of the weights  */
+                              /* (policy), the number of pairs (preference)      */
+    const float* loss_scale;  /* device fp32 word or NULL                        */
+    float* stats;             /* device, 4 fp32, written (preference: 3 of them) */
+    void* workspace;          /* device, 8-byte aligned, its head zeroed once    */
+    int64_t workspace_bytes;  /* >= token_loss_workspace_bytes(...)              */
+} shardstep_token_loss_t;
+
+/* Bytes of the workspace for up to n_tokens tokens in n_pairs pairs (0, 0 for
+ * the policy loss, which needs its head alone); -1 for negative arguments.
+ * The caller zeroes the workspace once; calls that may run at the same time
+ * need workspaces of their own. */
+int64_t token_loss_workspace_bytes(int64_t n_tokens, int32_t n_pairs);
+
+/* token_policy_loss -- device, one launch.  Per token, W = norm or sum w:
+ *     u = exp(a - old), policy = -min(u A, clip(u, 1 - clip_low, 1 + clip_high) A)
+ *     d = ref - a, kl = expm1(d) - d                (kl_coef 0: not formed, ref unused)
+ *     stats = sum over tokens of w / W * {policy + kl_coef kl, policy, kl,
+ *             1 where the clip holds the policy term, else 0}
+ *     c = w / W ((clip holds ? 0 : -u A) - kl_coef expm1(d))
+ * All weights 0: stats and gradient are 0.
+ *   old_logps, advantages   device, n_tokens fp32.
+ *   clip_low in [0, 1], clip_high >= 0, kl_coef >= 0, all finite.
+ * Errors: INVALID, CUDA. */
+int token_policy_loss(const shardstep_token_loss_t* args, const float* old_logps,
+                      const float* advantages, float clip_low, float clip_high, float kl_coef,
+                      void* stream);
+
+/* token_preference_loss -- device, two launches per 1024 pairs (one forward
+ * only).  The tokens are 2 * n_pairs sequences back to back, chosen and
+ * rejected of each pair in turn.  Per sequence s and pair q:
+ *     r_s = sum over its tokens of w (a - ref)
+ *     h_q = beta (r_chosen - r_rejected)
+ *     loss_q = (1 - ls) softplus(-h) + ls softplus(h),   W = norm or n_pairs
+ *     stats = sum over pairs of {loss_q, h_q, 1 where h_q > 0} / W   (3 words)
+ *     c = +-(beta / W) w (ls sigmoid(h) - (1 - ls) sigmoid(-h))
+ *   seq_lens[2 * n_pairs]  host, tokens of each sequence (>= 0), sum n_tokens.
+ *   log_ratios             device, 2 * n_pairs fp32, written: r_s.
+ *   beta finite, label_smoothing in [0, 0.5].
+ * Errors: INVALID, CUDA. */
+int token_preference_loss(const shardstep_token_loss_t* args, const int64_t* seq_lens,
+                          int32_t n_pairs, float beta, float label_smoothing,
+                          float* log_ratios, void* stream);
+
+/* -------------------------------------------------- lists of tensors */
+
+/* AdamW over many separately allocated tensors, and the global gradient norm
+ * before it: the replicated update where the parameters are a model's tensors
+ * and not one flat buffer ([P1] section "Naïve Data Parallelism": after the
+ * all-reduce every rank runs the same optimizer step on all of its
+ * parameters).  The list is passed by value with each launch (up to 400
+ * tensors per launch of the step, 1200 of the norm; longer lists take several
+ * launches), so nothing is copied to the device and nothing is kept. */
+typedef struct {
+    float* master;     /* device, numel fp32, updated in place               */
+    void* m;           /* device, numel fp32, or numel uint8 codes (8 bits)  */
+    void* v;           /* likewise                                           */
+    float* m_scale;    /* device, ceil(numel / 256) fp32; 8 bits only        */
+    float* v_scale;    /* likewise                                           */
+    void* param;       /* device, numel elements of param_dtype, or NULL     */
+    int64_t numel;     /* >= 0                                               */
+    int32_t group;     /* index of its hyper-parameters                      */
+    int32_t pad_;
+} shardstep_tensor_t;
+
+/* tensors_adamw_step -- device, one launch per 400 tensors.  Per element, in
+ * fp32, one rounding per operation:
+ *     g = grad * *grad_coef                 (grad itself where grad_coef is NULL)
+ *     p, m, v as in fsdp_rs_avg_adamw_cast at N_d = 1
+ *     param = param_dtype(p), round to nearest even
+ * state_bits 32: m and v are fp32 arrays; the bits of fsdp_rs_avg_adamw_cast
+ * on g.  state_bits 8: m and r = sqrt(v) are held as one code per element with
+ * one fp32 scale per 256 consecutive elements of the tensor (the last block
+ * may be shorter):
+ *     m = e4m3(code_m) * m_scale,  r = root(code_v) * v_scale,  v = r * r
+ *     (update; r' = sqrt(v'), and p' is formed from m' and r' unrounded)
+ *     m_scale' = max|m'| / 448,      code_m' = e4m3(m' * (448 / max|m'|))
+ *     v_scale' = max r' / 1.9375,    code_v' = root(r' * (1.9375 / max r'))
+ * e4m3: 4 exponent and 3 mantissa bits and a sign, nearest even.  root: an
+ * unsigned float of 4 exponent and 4 mantissa bits, code c > 0 standing for
+ * (1 + (c & 15) / 16) * 2^((c >> 4) - 15) and code 0 for 0; to nearest, ties
+ * up, and at least code 1 for r' > 0.  A block whose largest magnitude is
+ * below 2^-100 is stored as zeros; one that holds an inf or NaN gets a
+ * non-finite scale, so the fault is not lost (pass `skip` to leave such a step
+ * out).
+ *   grads[n]     host array of device pointers, tensors[i].numel elements of
+ *                grad_dtype each.
+ *   tensors[n]   host array; n >= 0.  Tensors of numel 0 may hold NULLs.
+ *   grad_dtype   SHARDSTEP_DTYPE_BF16, _F16 or _F32, for all gradients.
+ *   param_dtype  SHARDSTEP_DTYPE_BF16 or _F16, for all non-NULL param.
+ *   state_bits   32 or 8.
+ *   hp[n_groups] host: the hyper-parameters and step t >= 1 of each group,
+ *                1 <= n_groups <= SHARDSTEP_MAX_GROUPS.
+ *   grad_coef    device fp32 word or NULL, e.g. the clipping factor that
+ *                tensors_grad_norm leaves (loss scale divided out).
+ *   skip         device word or NULL: non-zero at launch, nothing changes.
+ * No array may overlap another that is written (gradients may overlap one
+ * another).  Any element alignment; a tensor whose arrays are all 16-byte
+ * aligned takes the vector path.
+ * Errors: INVALID, CAPACITY (n_groups), CUDA. */
+int tensors_adamw_step(const void* const* grads, const shardstep_tensor_t* tensors, int32_t n,
+                       int32_t grad_dtype, int32_t param_dtype, int32_t state_bits,
+                       const shardstep_adamw_t* hp, int32_t n_groups, const float* grad_coef,
+                       const uint32_t* skip, void* stream);
+
+/* tensors_state_adamw_step -- tensors_adamw_step with each group's scalars
+ * read on the device from states[g] (host array of device pointers; each at a
+ * step >= 1), so that a CUDA graph can capture it. */
+int tensors_state_adamw_step(const void* const* grads, const shardstep_tensor_t* tensors,
+                             int32_t n, int32_t grad_dtype, int32_t param_dtype,
+                             int32_t state_bits, const shardstep_adamw_state_t* const* states,
+                             int32_t n_groups, const float* grad_coef, const uint32_t* skip,
+                             void* stream);
+
+/* tensors_moments_decode / _encode -- device, one launch.  The 8-bit moments
+ * of n elements in blocks of 256 to fp32 (m_out = m, v_out = r * r) and back
+ * (r = sqrt(v)), e.g. for a checkpoint in 32 bits.  Inputs and outputs must
+ * not overlap.  Errors: INVALID, CUDA. */
+int tensors_moments_decode(const uint8_t* m, const float* m_scale, const uint8_t* v,
+                           const float* v_scale, int64_t n, float* m_out, float* v_out,
+                           void* stream);
+int tensors_moments_encode(const float* m_in, const float* v_in, int64_t n, uint8_t* m,
+                           float* m_scale, uint8_t* v, float* v_scale, void* stream);
+
+/* tensors_grad_norm -- device, one launch per 1200 tensors.  With s =
+ * *loss_scale (1 where NULL):
+ *     out[0] = norm   = sqrt(sum over all tensors of g^2) / s
+ *     out[1] = factor = min(1, max_norm / (norm + 1e-6)) / s
+ * so that tensors_adamw_step with grad_coef = out + 1 clips and unscales in
+ * its own pass.  Squares are summed in fp32 per thread and in double beyond
+ * that, in an order that depends on the sizes alone.  When norm is inf or NaN
+ * (also when a square passes fp32's range, |g| > 1.8e19) *found_inf becomes 1;
+ * it is never cleared here (fsdp_grad_scaler_update does).
+ *   grads[n], numels[n]  host arrays; NULL allowed where numel is 0.
+ *   max_norm             > 0 (infinity: no clipping).
+ *   loss_scale, found_inf  device words or NULL.
+ *   out                  device, 2 fp32.
+ *   workspace            device, 8-byte aligned, tensors_norm_workspace_bytes()
+ *                        bytes, zeroed once by the caller; calls that may run
+ *                        at the same time need workspaces of their own.
+ * An empty list launches one block: norm 0, factor min(1, max_norm/1e-6)/s.
+ * Errors: INVALID, CUDA. */
+int64_t tensors_norm_workspace_bytes(void);
+int tensors_grad_norm(const void* const* grads, const int64_t* numels, int32_t n, int32_t dtype,
+                      float max_norm, const float* loss_scale, float* out, uint32_t* found_inf,
+                      void* workspace, void* stream);
 
 /* ------------------------------------------------------------ misc */
 

@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 from dataclasses import dataclass
+from typing import NamedTuple
 
 from . import _capi
 from ._capi import ShardstepError, AdamWHP, MAX_ND
@@ -30,6 +31,9 @@ __all__ = [
     "fsdp_accumulate_rs_avg_adamw_cast", "fsdp_state_accumulate_rs_avg_adamw_cast",
     "ddp_bucket_allreduce_avg_adamw_cast", "set_tma_wait_ns", "check_mean_division",
     "fsdp_shard_pieces", "fsdp2_rs_avg_adamw_cast", "Fsdp2Step",
+    "LossWorkspace", "PolicyLoss", "policy_loss", "PreferenceLoss", "preference_loss",
+    "TensorList", "NormWorkspace", "grad_norm_clip", "TensorAdamW", "moments_decode",
+    "moments_encode",
 ]
 
 
@@ -760,6 +764,406 @@ def ddp_allreduce_as_ready(rank_grads, bucket_offsets, out, ready: BucketReadine
         ddp_bucket_allreduce_avg(rank_grads, bucket_offsets, out, first=b, count=1,
                                  stream=stream)
     return out
+
+
+# ---------------------------------------------------- losses over tokens
+
+class LossWorkspace:
+    """Device workspace of the token losses, kept from call to call so that a
+    call allocates nothing once it is large enough.  It carries no results;
+    calls that may run at the same time (on different streams) need
+    workspaces of their own."""
+
+    def __init__(self, device="cuda"):
+        self.device = device
+        self.buf = None
+
+    def at_least(self, nbytes: int):
+        import torch
+        if self.buf is None or self.buf.numel() * 8 < nbytes:
+            self.buf = torch.zeros((nbytes + 7) // 8, dtype=torch.int64, device=self.device)
+        return self.buf
+
+
+class PolicyLoss(NamedTuple):
+    stats: object      # fp32 [4]: loss, policy term, KL term, clipped fraction
+    logps: object      # fp32 [N]: the ids' log probabilities
+    grad: object       # d loss / d logits, or None
+
+
+class PreferenceLoss(NamedTuple):
+    stats: object       # fp32 [3]: loss, margin, fraction of positive margins
+    log_ratios: object  # fp32 [2 P]: per sequence, sum of w (logp - ref_logp)
+    logps: object       # fp32 [N]
+    grad: object        # d loss / d logits, or None
+
+
+def _f32_word(t, what):
+    import torch
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or not t.is_cuda or t.numel() < 1:
+        raise ValueError(f"{what} must be a CUDA fp32 word")
+    return t.data_ptr()
+
+
+def _per_token(t, n, what, optional=False):
+    """Device address of an fp32 array of n tokens."""
+    import torch
+    if t is None and optional:
+        return None
+    if t is None or t.dtype != torch.float32 or t.numel() != n or not t.is_cuda \
+            or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous CUDA fp32 tensor of {n} elements")
+    return t.data_ptr()
+
+
+def _token_args(logits, ids, weights, ref_logps, grad, grad_scale, loss_scale, norm, workspace,
+                pairs):
+    """The checks both losses share; allocates their outputs.  Returns the C
+    arguments, the statistics, the log probabilities and the workspace buffer
+    (which the caller holds until the launch)."""
+    import torch
+    if logits.dim() != 2 or not logits.is_cuda:
+        raise ValueError("logits must be a CUDA matrix [tokens, vocabulary]")
+    n, v = logits.shape
+    if n > 0 and logits.stride(1) != 1 and v > 1:
+        raise ValueError("a row of the logits must be contiguous")
+    if ids.dtype not in (torch.int64, torch.int32) or ids.numel() != n or not ids.is_cuda \
+            or not ids.is_contiguous():
+        raise ValueError(f"ids must be contiguous CUDA int64 or int32 with {n} elements")
+    if grad is not None and (grad.shape != logits.shape or grad.dtype != logits.dtype
+                             or not grad.is_cuda or (n > 0 and v > 1 and grad.stride(1) != 1)):
+        raise ValueError("grad must have the logits' shape and dtype, rows contiguous")
+    if grad is not None and n > 1 and grad.stride(0) < v or n > 1 and logits.stride(0) < v:
+        raise ValueError("the rows of logits or grad overlap")
+    out = torch.empty(n + 4, dtype=torch.float32, device=logits.device)
+    stats, logps = out[:4], out[4:]
+    if n == 0:
+        stats.zero_()
+    ws = workspace if workspace is not None else LossWorkspace(logits.device)
+    need = _capi.lib().token_loss_workspace_bytes(n, pairs)
+    buf = ws.at_least(need)
+    args = _capi.TokenLoss(
+        logits.data_ptr(), max(logits.stride(0), v), _dtype_code(logits), ids.element_size(),
+        ids.data_ptr(), n, v, _per_token(weights, n, "weights", True),
+        _per_token(ref_logps, n, "ref_logps", True), logps.data_ptr(),
+        grad.data_ptr() if grad is not None else None,
+        max(grad.stride(0), v) if grad is not None else v, float(grad_scale),
+        0.0 if norm is None else float(norm), _f32_word(loss_scale, "loss_scale"),
+        stats.data_ptr(), buf.data_ptr(), buf.numel() * 8)
+    if norm is not None and not norm > 0:
+        raise ValueError("norm must be > 0 (None: the sum of the weights, or the pairs)")
+    return args, stats, logps, buf
+
+
+def policy_loss(logits, ids, old_logps, advantages, *, ref_logps=None, weights=None,
+                clip_low: float = 0.2, clip_high: float = 0.2, kl_coef: float = 0.0, grad=None,
+                grad_scale: float = 1.0, loss_scale=None, norm=None, workspace=None,
+                stream=None) -> PolicyLoss:
+    """The clipped policy loss of ``logits`` [N, V] (bf16, fp16 or fp32, rows
+    of any stride) on the tokens ``ids`` [N], with a KL term against
+    ``ref_logps`` when ``kl_coef`` > 0, in one launch:
+
+        u = exp(logp - old_logps)
+        loss = sum w (-min(u A, clip(u, 1 - clip_low, 1 + clip_high) A)
+                      + kl_coef (exp(d) - 1 - d)) / norm,   d = ref_logps - logp
+
+    ``weights`` [N] fp32 (None: ones): a token of weight 0 is not read; its
+    logp and gradient are 0.  ``norm`` divides the loss (None: the sum of the
+    weights; give the global count when micro-batches share one mean).
+    ``grad`` (None: forward only; may be ``logits``) receives d loss / d logits
+    times ``grad_scale`` times the device word ``loss_scale`` (a
+    ``GradScaler.scale``)."""
+    args, stats, logps, held = _token_args(logits, ids, weights, ref_logps, grad, grad_scale,
+                                           loss_scale, norm, workspace, 0)
+    n = args.n_tokens
+    _capi.check("token_policy_loss", _capi.lib().token_policy_loss(
+        ctypes.byref(args), _per_token(old_logps, n, "old_logps"),
+        _per_token(advantages, n, "advantages"), clip_low, clip_high, kl_coef,
+        _stream(stream, logits.device)))
+    return PolicyLoss(stats, logps, grad)
+
+
+def preference_loss(logits, ids, seq_lens, ref_logps, *, beta: float = 0.1,
+                    label_smoothing: float = 0.0, weights=None, grad=None,
+                    grad_scale: float = 1.0, loss_scale=None, norm=None, workspace=None,
+                    stream=None) -> PreferenceLoss:
+    """The preference loss of pairs of sequences packed back to back (chosen,
+    rejected, chosen, ...; ``seq_lens``: their lengths, on the host) from the
+    ``logits`` [N, V] of their tokens ``ids`` [N]:
+
+        r = sum over a sequence of w (logp - ref_logps)
+        h = beta (r_chosen - r_rejected)
+        loss = sum over pairs of ((1 - ls) softplus(-h) + ls softplus(h)) / norm
+
+    ``weights`` [N] fp32 (0: not read, e.g. a prompt; 1 / length for averaged
+    log ratios); ``norm`` None: the number of pairs.  ``grad``, ``grad_scale``
+    and ``loss_scale`` as in ``policy_loss``."""
+    import torch
+    lens = _capi.i64_array(seq_lens)
+    if len(seq_lens) % 2:
+        raise ValueError("seq_lens must hold chosen and rejected lengths in turn")
+    pairs = len(seq_lens) // 2
+    args, stats, logps, held = _token_args(logits, ids, weights, ref_logps, grad, grad_scale,
+                                           loss_scale, norm, workspace, pairs)
+    ratios = torch.empty(2 * pairs, dtype=torch.float32, device=logits.device)
+    if args.n_tokens == 0:
+        ratios.zero_()
+    _capi.check("token_preference_loss", _capi.lib().token_preference_loss(
+        ctypes.byref(args), lens, pairs, beta, label_smoothing, ratios.data_ptr(),
+        _stream(stream, logits.device)))
+    return PreferenceLoss(stats[:3], ratios, logps, grad)
+
+
+# ------------------------------------------------------ lists of tensors
+
+class TensorList:
+    """Gradient tensors checked once: contiguous CUDA tensors of one dtype on
+    one device.  It keeps them alive and takes their addresses when made;
+    each call checks only that none has moved, so that a step over many small
+    tensors costs little host time."""
+
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+        _need_cuda(*self.tensors)
+        for t in self.tensors:
+            if t.dtype != self.tensors[0].dtype or t.device != self.tensors[0].device:
+                raise ValueError("one dtype and one device per list")
+        self.dtype = _dtype_code(self.tensors[0]) if self.tensors else _capi.DTYPE_BF16
+        self.device = self.tensors[0].device if self.tensors else None
+        self.numels = [t.numel() for t in self.tensors]
+        self.addrs = [t.data_ptr() for t in self.tensors]
+        self._numels = _capi.i64_array(self.numels)
+        self._ptrs = _capi.ptr_array(self.addrs)
+
+    def __len__(self):
+        return len(self.tensors)
+
+    def check(self):
+        if [t.data_ptr() for t in self.tensors] != self.addrs:
+            raise ValueError("a tensor moved since this TensorList was made")
+        return self
+
+
+def _tensor_list(x):
+    return x.check() if isinstance(x, TensorList) else TensorList(x)
+
+
+class NormWorkspace:
+    """Device workspace of ``grad_norm_clip`` (zeroed once, left ready by each
+    call); calls that may run at the same time need workspaces of their
+    own."""
+
+    def __init__(self, device="cuda"):
+        import torch
+        self.buf = torch.zeros(_capi.lib().tensors_norm_workspace_bytes() // 8,
+                               dtype=torch.int64, device=device)
+
+
+def grad_norm_clip(grads, max_norm: float, *, loss_scale=None, found_inf=None, out=None,
+                   workspace=None, stream=None):
+    """The global 2-norm of the gradient tensors ``grads`` (a list or a
+    ``TensorList``) and the factor that clips them, in one launch (per 1200
+    tensors).  Returns ``out`` (fp32 [2] on the device): the norm with the
+    device word ``loss_scale`` divided out, and min(1, max_norm / (norm +
+    1e-6)) / loss_scale, which ``TensorAdamW.step(grad_coef=out[1:])``
+    applies in its own pass.  A non-finite norm sets ``found_inf`` (an int32
+    device word, e.g. ``GradScaler.found_inf``)."""
+    import torch
+    grads = _tensor_list(grads)
+    if not len(grads) and out is None:
+        raise ValueError("an empty list needs out")
+    dev = grads.device if len(grads) else out.device
+    if out is None:
+        out = torch.empty(2, dtype=torch.float32, device=dev)
+    elif out.dtype != torch.float32 or out.numel() != 2 or not out.is_cuda \
+            or not out.is_contiguous():
+        raise ValueError("out must be a contiguous CUDA fp32 tensor of 2 elements")
+    if found_inf is not None and (found_inf.element_size() != 4 or not found_inf.is_cuda):
+        raise ValueError("found_inf must be a 4-byte CUDA word")
+    ws = workspace if workspace is not None else NormWorkspace(dev)
+    _capi.check("tensors_grad_norm", _capi.lib().tensors_grad_norm(
+        grads._ptrs, grads._numels, len(grads), grads.dtype, max_norm,
+        _f32_word(loss_scale, "loss_scale"), out.data_ptr(),
+        found_inf.data_ptr() if found_inf is not None else None, ws.buf.data_ptr(),
+        _stream(stream, dev)))
+    return out
+
+
+def _moment_args(m, m_scale, v, v_scale, m32, v32):
+    import torch
+    _need_cuda(m, m_scale, v, v_scale, m32, v32)
+    n = m.numel()
+    blocks = -(-n // _capi.MOMENT_BLOCK)
+    if any(t.dtype != torch.uint8 or t.numel() != n for t in (m, v)):
+        raise ValueError("codes must be uint8 with the same numel")
+    if any(t.dtype != torch.float32 or t.numel() != blocks for t in (m_scale, v_scale)):
+        raise ValueError("scales must be fp32, one per 256 elements")
+    if any(t.dtype != torch.float32 or t.numel() != n for t in (m32, v32)):
+        raise ValueError("moments must be fp32 with the codes' numel")
+    return n
+
+
+def moments_decode(m, m_scale, v, v_scale, out=None, stream=None):
+    """8-bit moments (codes and scales in blocks of 256) -> fp32 (m, v)."""
+    import torch
+    if out is None:
+        out = (torch.empty(m.numel(), dtype=torch.float32, device=m.device),
+               torch.empty(m.numel(), dtype=torch.float32, device=m.device))
+    n = _moment_args(m, m_scale, v, v_scale, *out)
+    _capi.check("tensors_moments_decode", _capi.lib().tensors_moments_decode(
+        m.data_ptr(), m_scale.data_ptr(), v.data_ptr(), v_scale.data_ptr(), n,
+        out[0].data_ptr(), out[1].data_ptr(), _stream(stream, m.device)))
+    return out
+
+
+def moments_encode(m32, v32, m, m_scale, v, v_scale, stream=None):
+    """fp32 moments -> 8-bit codes and scales in blocks of 256, in place."""
+    n = _moment_args(m, m_scale, v, v_scale, m32, v32)
+    _capi.check("tensors_moments_encode", _capi.lib().tensors_moments_encode(
+        m32.data_ptr(), v32.data_ptr(), n, m.data_ptr(), m_scale.data_ptr(), v.data_ptr(),
+        v_scale.data_ptr(), _stream(stream, m.device)))
+
+
+class TensorAdamW:
+    """AdamW over a list of parameter tensors (bf16 or fp16, one dtype) with
+    an fp32 master copy and moments in ``state_bits`` = 32 or 8 bits: one
+    launch per step for up to 400 tensors.
+
+    The state sits in flat buffers, tensor t at elements
+    [offsets[t], offsets[t] + numel) with every tensor starting on a multiple
+    of 256: ``master`` (fp32, from the parameters' values), ``m`` and ``v``
+    (fp32, or uint8 codes with ``m_scale`` / ``v_scale``, one fp32 per 256
+    elements).  ``hp`` is one ``AdamW`` or a list of up to 8, ``groups[t]``
+    each tensor's index into it (e.g. no weight decay for norm vectors).
+    ``t`` counts the steps; ``device_step_state`` moves the count to the
+    device for ``step_on_device``, which a CUDA graph can capture."""
+
+    def __init__(self, params, hp, groups=None, state_bits: int = 32, stream=None):
+        import torch
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits must be 8 or 32")
+        self.params = list(params)
+        if not self.params:
+            raise ValueError("need at least one parameter tensor")
+        _need_cuda(*self.params)
+        dt, dev = self.params[0].dtype, self.params[0].device
+        if dt not in (torch.bfloat16, torch.float16) or any(
+                p.dtype != dt or p.device != dev for p in self.params):
+            raise ValueError("parameters must be all bf16 or all fp16, on one device")
+        self.hps = list(hp) if isinstance(hp, (list, tuple)) else [hp]
+        if not 1 <= len(self.hps) <= _capi.MAX_GROUPS:
+            raise ValueError(f"1 to {_capi.MAX_GROUPS} hyper-parameter groups")
+        self.groups = [0] * len(self.params) if groups is None else [int(g) for g in groups]
+        if len(self.groups) != len(self.params) or any(
+                not 0 <= g < len(self.hps) for g in self.groups):
+            raise ValueError("groups must give each parameter an index into hp")
+        self.state_bits, self.t, self.states = state_bits, 0, None
+        self.numels = [p.numel() for p in self.params]
+        blk = _capi.MOMENT_BLOCK
+        self.offsets, pos = [], 0
+        for n in self.numels:
+            self.offsets.append(pos)
+            pos += -(-n // blk) * blk
+        self.flat = pos
+        self.master = torch.zeros(pos, dtype=torch.float32, device=dev)
+        for p, o, n in zip(self.params, self.offsets, self.numels):
+            self.master[o:o + n].copy_(p.reshape(-1))
+        code = torch.float32 if state_bits == 32 else torch.uint8
+        self.m = torch.zeros(pos, dtype=code, device=dev)
+        self.v = torch.zeros(pos, dtype=code, device=dev)
+        self.m_scale = self.v_scale = None
+        if state_bits == 8:
+            self.m_scale = torch.zeros(pos // blk, dtype=torch.float32, device=dev)
+            self.v_scale = torch.zeros(pos // blk, dtype=torch.float32, device=dev)
+        self._param_code = _dtype_code(self.params[0])
+        self._table = (_capi.Tensor * len(self.params))()
+        self._addrs = None
+
+    def view(self, buf, t):
+        """Tensor t's piece of a flat buffer of the state, in its shape."""
+        o, n = self.offsets[t], self.numels[t]
+        return buf[o:o + n].view(self.params[t].shape)
+
+    def _call(self, grads):
+        """The list of this call's gradients, checked against the parameters,
+        with the table of the state's addresses brought up to date where a
+        buffer or a parameter has moved."""
+        state = [self.master, self.m, self.v] + (
+            [self.m_scale, self.v_scale] if self.state_bits == 8 else [])
+        addrs = [b.data_ptr() for b in state] + [p.data_ptr() for p in self.params]
+        if addrs != self._addrs:
+            _need_cuda(*state)
+            es = 4 if self.state_bits == 32 else 1
+            for t, row in enumerate(self._table):
+                o = self.offsets[t]
+                row.master = addrs[0] + 4 * o
+                row.m, row.v = addrs[1] + es * o, addrs[2] + es * o
+                if self.state_bits == 8:
+                    row.m_scale = addrs[3] + 4 * (o // _capi.MOMENT_BLOCK)
+                    row.v_scale = addrs[4] + 4 * (o // _capi.MOMENT_BLOCK)
+                row.param = addrs[len(state) + t]
+                row.numel, row.group = self.numels[t], self.groups[t]
+            self._addrs = addrs
+        grads = _tensor_list(grads)
+        if grads.numels != self.numels:
+            raise ValueError("gradients must match the parameters one by one")
+        if grads.device != self.master.device:
+            raise ValueError("gradients on another device than the parameters")
+        return grads
+
+    def _words(self, grad_coef, skip):
+        if skip is not None and (skip.element_size() != 4 or not skip.is_cuda):
+            raise ValueError("skip must be a 4-byte CUDA word")
+        return (_f32_word(grad_coef, "grad_coef"), skip.data_ptr() if skip is not None else None)
+
+    def step(self, grads, grad_coef=None, skip=None, stream=None):
+        """One step on ``grads`` (a list or a ``TensorList``, one tensor per
+        parameter): g = grad * ``grad_coef`` (a device fp32 word, e.g. the
+        factor of ``grad_norm_clip``); a non-zero device word ``skip`` leaves
+        everything unchanged on the device.  The host's count advances either
+        way; with device step states it is the device's count that advances,
+        unless skipped."""
+        if self.states is not None:
+            return self.step_on_device(grads, grad_coef, skip, stream)
+        grads = self._call(grads)
+        hp = (AdamWHP * len(self.hps))(*[h.at_step(self.t + 1) for h in self.hps])
+        _capi.check("tensors_adamw_step", _capi.lib().tensors_adamw_step(
+            grads._ptrs, self._table, len(self.params), grads.dtype, self._param_code,
+            self.state_bits, hp, len(self.hps), *self._words(grad_coef, skip), _stream(stream, self.master.device)))
+        self.t += 1
+
+    def device_step_state(self):
+        """Moves the step count to the device, one ``AdamWState`` per group."""
+        self.states = [AdamWState(h, self.t, device=self.master.device) for h in self.hps]
+        return self.states
+
+    def step_on_device(self, grads, grad_coef=None, skip=None, stream=None):
+        """``step`` with the count advanced (unless ``skip``) and the scalars
+        derived on the device: the same launches every call."""
+        grads = self._call(grads)
+        for s in self.states:
+            s.advance(skip=skip, stream=stream)
+        _capi.check("tensors_state_adamw_step", _capi.lib().tensors_state_adamw_step(
+            grads._ptrs, self._table, len(self.params), grads.dtype, self._param_code,
+            self.state_bits, _capi.ptr_array([s.buf.data_ptr() for s in self.states]), len(self.states),
+            *self._words(grad_coef, skip), _stream(stream, self.master.device)))
+
+    def moments(self, out=None, stream=None):
+        """The moments as flat fp32 buffers (m, v): the state's own at 32 bits,
+        decoded (into ``out`` if given) at 8."""
+        if self.state_bits == 32:
+            return self.m, self.v
+        return moments_decode(self.m, self.m_scale, self.v, self.v_scale, out=out, stream=stream)
+
+    def load_moments(self, m32, v32, stream=None):
+        """Sets the moments from flat fp32 buffers laid out like ``master``."""
+        if self.state_bits == 32:
+            self.m.copy_(m32)
+            self.v.copy_(v32)
+        else:
+            moments_encode(m32, v32, self.m, self.m_scale, self.v, self.v_scale, stream=stream)
 
 
 # ---------------------------------------------------------------- ledger

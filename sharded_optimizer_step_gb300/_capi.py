@@ -28,6 +28,8 @@ DTYPE_BF16 = 0
 DTYPE_F32 = 1
 DTYPE_F16 = 2
 MAX_ND = 64
+MAX_GROUPS = 8
+MOMENT_BLOCK = 256
 COMM_KINDS = {"reduce_scatter": 0, "all_gather": 1, "all_reduce": 2, "ddp": 2,
               "zero1": 3, "zero2": 4, "zero3": 5}
 
@@ -54,6 +56,20 @@ class CkptInfo(ctypes.Structure):
 class CkptPiece(ctypes.Structure):
     _fields_ = [("old_rank", c_i32), ("pad_", c_i32), ("old_offset", c_i64),
                 ("new_offset", c_i64), ("count", c_i64)]
+
+
+class Tensor(ctypes.Structure):
+    _fields_ = [("master", c_vp), ("m", c_vp), ("v", c_vp), ("m_scale", c_vp),
+                ("v_scale", c_vp), ("param", c_vp), ("numel", c_i64), ("group", c_i32),
+                ("pad_", c_i32)]
+
+
+class TokenLoss(ctypes.Structure):
+    _fields_ = [("logits", c_vp), ("row_stride", c_i64), ("dtype", c_i32), ("id_bytes", c_i32),
+                ("ids", c_vp), ("n_tokens", c_i64), ("vocab", c_i64), ("weights", c_vp),
+                ("ref_logps", c_vp), ("logps", c_vp), ("grad", c_vp), ("grad_stride", c_i64),
+                ("grad_scale", c_f32), ("norm", c_f32), ("loss_scale", c_vp), ("stats", c_vp),
+                ("workspace", c_vp), ("workspace_bytes", c_i64)]
 
 
 # name -> (restype, argtypes), exactly the declarations of include/shardstep.h
@@ -120,6 +136,20 @@ SIGNATURES = {
     "shardstep_adamw_state_advance": (c_i32, [c_vp, ctypes.POINTER(AdamWHP), c_vp, c_vp]),
     "fsdp_state_scaled_rs_avg_adamw_cast": (c_i32, [c_vp, c_i32, c_i32, c_i32, c_i64, c_vp, c_vp,
                                                     c_vp, c_vp, c_vp, c_vp, c_vp, c_vp]),
+    "token_loss_workspace_bytes": (c_i64, [c_i64, c_i32]),
+    "token_policy_loss": (c_i32, [ctypes.POINTER(TokenLoss), c_vp, c_vp, c_f32, c_f32, c_f32,
+                                  c_vp]),
+    "token_preference_loss": (c_i32, [ctypes.POINTER(TokenLoss), c_vp, c_i32, c_f32, c_f32,
+                                      c_vp, c_vp]),
+    "tensors_adamw_step": (c_i32, [c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, c_vp, c_i32, c_vp,
+                                   c_vp, c_vp]),
+    "tensors_state_adamw_step": (c_i32, [c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, c_vp, c_i32,
+                                         c_vp, c_vp, c_vp]),
+    "tensors_moments_decode": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_i64, c_vp, c_vp, c_vp]),
+    "tensors_moments_encode": (c_i32, [c_vp, c_vp, c_i64, c_vp, c_vp, c_vp, c_vp, c_vp]),
+    "tensors_norm_workspace_bytes": (c_i64, []),
+    "tensors_grad_norm": (c_i32, [c_vp, c_vp, c_i32, c_i32, c_f32, c_vp, c_vp, c_vp, c_vp,
+                                  c_vp]),
     "fsdp_state_rs_avg_adamw_cast": (c_i32, [c_vp, c_i32, c_i32, c_i32, c_i64, c_vp, c_vp, c_vp,
                                              c_vp, c_vp, c_vp]),
 }

@@ -15,7 +15,8 @@ OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libshardstep.so")
 
 SOURCES = ["step.cu", "step_tma.cu", "copy.cu", "accum_step.cu", "fsdp2_step.cu", "state.cu",
-           "api.cpp", "ckpt.cpp", "ready.cpp"]
+           "tensors.cu", "token_loss.cu",
+           "api.cpp", "tuning_api.cpp", "ckpt.cpp", "ready.cpp"]
 HEADERS = ["common.cuh", "internal.h"]
 ARCH = "103a"
 

@@ -271,6 +271,15 @@ int ready_fail(int code, const char* fmt, ...) {
 
 int ready_ok() { return ok(); }
 
+void record_kernel(const char* fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_last_kernel, sizeof g_last_kernel, fmt, ap);
+    va_end(ap);
+}
+
+AdamScalars host_adam_scalars(const shardstep_adamw_t& hp) { return adam_scalars(hp); }
+
 int device_sms() {
     static std::atomic<int> cache[256];
     int dev = 0;

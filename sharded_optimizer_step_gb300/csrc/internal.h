@@ -247,4 +247,145 @@ cudaError_t launch_accum_rs_adamw_cast(const PtrTable& acc, const PtrTable& last
                                        float* v, uint16_t* out, const AdamScalars& c,
                                        const MeanOp& mo, bool vec, cudaStream_t stream);
 
+// ------------------------------------------------- lists of tensors
+// (tensors.cu; host side in tuning_api.cpp)
+
+// The AdamW hyper-parameter groups of one launch.
+constexpr int kMaxGroups = SHARDSTEP_MAX_GROUPS;
+// Tensors of one launch: the table travels as a kernel parameter, whose limit
+// is 32764 bytes; the smaller capacity keeps the parameter block of the usual
+// short lists small.
+constexpr int kTensorsSmall = 32;
+constexpr int kTensorsLarge = 400;
+// Elements that share one scale of the 8-bit moments.
+constexpr int kMomentBlock = SHARDSTEP_MOMENT_BLOCK;
+
+template <int CAP>
+struct TensorTable {
+    const void* grad[CAP];
+    float* master[CAP];
+    void* m[CAP];
+    void* v[CAP];
+    float* m_scale[CAP];
+    float* v_scale[CAP];
+    void* param[CAP];
+    int64_t n[CAP];
+    uint32_t b0[CAP + 1];   // first block of each tensor; b0[count] = the launch's blocks
+    uint16_t group[CAP];
+    uint8_t vec[CAP];       // every array of the tensor takes 16-byte accesses
+    int32_t count;
+};
+struct GroupScalars {
+    AdamScalars c[kMaxGroups];
+};
+// Elements one block of the list kernels covers.
+constexpr int kListChunk32 = 2048;
+constexpr int kListChunk8 = 8 * kMomentBlock;
+
+template <int CAP>
+cudaError_t launch_tensors_adamw(const TensorTable<CAP>& t, int grad_type, int param_type,
+                                 int bits, const GroupScalars& gs, const float* coef,
+                                 const unsigned int* skip, cudaStream_t stream);
+cudaError_t launch_moments_decode(const uint8_t* m, const float* m_scale, const uint8_t* v,
+                                  const float* v_scale, int64_t n, float* m_out, float* v_out,
+                                  bool vec, cudaStream_t stream);
+cudaError_t launch_moments_encode(const float* m_in, const float* v_in, int64_t n, uint8_t* m,
+                                  float* m_scale, uint8_t* v, float* v_scale, bool vec,
+                                  cudaStream_t stream);
+
+template <int CAP>
+struct NormTable {
+    const void* p[CAP];
+    int64_t n[CAP];
+    uint32_t b0[CAP + 1];   // first chunk of each tensor; b0[count] = the launch's chunks
+    uint8_t vec[CAP];
+    int32_t count;
+};
+constexpr int kNormSmall = 64;
+constexpr int kNormLarge = 1200;
+constexpr int kNormChunk = 8192;      // elements of one chunk
+constexpr int kNormMaxBlocks = 1024;  // partial sums in the workspace
+// The norm's workspace: an arrival counter, then one double per block.
+struct NormWork {
+    unsigned int arrived;
+    unsigned int pad_[3];
+    double partial[kNormMaxBlocks];
+};
+struct NormArgs {
+    NormWork* ws;
+    const float* scale;       // may be null: 1
+    float max_norm;
+    float* out;               // {norm, factor}
+    unsigned int* found;      // may be null
+    int first, last;          // this launch starts / ends the call
+};
+template <int CAP>
+cudaError_t launch_tensors_norm(const NormTable<CAP>& t, int type, const NormArgs& a, int blocks,
+                                cudaStream_t stream);
+
+// ---------------------------------------------------- losses over tokens
+// (token_loss.cu; host side in tuning_api.cpp)
+
+constexpr int kLossMaxBlocks = 1024;
+// The workspace of the token losses; the preference loss's per-token and
+// per-sequence words follow it.
+struct LossWork {
+    unsigned int arrived;
+    unsigned int pad_[3];
+    double total[4];                        // carried from launch to launch
+    double partial[kLossMaxBlocks][4];      // the blocks' sums
+};
+struct TokenArgs {
+    const void* x;          // logits, row i at x + i * x_stride
+    int64_t x_stride;       // elements
+    void* grad;             // or null: forward only
+    int64_t g_stride;
+    const void* ids;
+    int ids64;
+    const float* w;         // or null: ones
+    const float* ref;
+    float* logps;
+    int64_t n, v;
+    float grad_scale;
+    const float* loss_scale;  // or null
+    float norm;               // 0: the sum of the weights (policy)
+    float* stats;
+    LossWork* ws;
+};
+struct PolicyArgs {
+    const float* old;
+    const float* adv;
+    float lo, hi, kl;
+};
+// The sequences of one launch of the preference loss: pairs 2 p, 2 p + 1 are
+// its rows [start[2 p], start[2 p + 1]) and [start[2 p + 1], start[2 p + 2]).
+constexpr int kPairsPerLaunch = 1024;
+struct PairTable {
+    int32_t start[2 * kPairsPerLaunch + 1];
+    int32_t pairs;
+};
+struct PreferenceArgs {
+    float beta, smoothing;
+    float* log_ratios;      // 2 per pair
+    float* row_max;         // per token
+    float* row_inv;         // per token: 1 / sum exp(x - max)
+    float* term;            // per token: w (a - ref)
+    float* coef;            // per sequence: d loss / d a at weight 1
+    int first, last;        // this launch starts / ends the call
+};
+cudaError_t launch_policy_loss(const TokenArgs& a, const PolicyArgs& p, int dtype,
+                               cudaStream_t stream);
+cudaError_t launch_preference_forward(const TokenArgs& a, const PreferenceArgs& p,
+                                      const PairTable& t, int dtype, cudaStream_t stream);
+cudaError_t launch_preference_backward(const TokenArgs& a, const PreferenceArgs& p,
+                                       const PairTable& t, int dtype, cudaStream_t stream);
+
+// Host helpers of api.cpp for the other translation units: the last error of
+// the calling thread, the name shardstep_last_kernel reports, the per-step
+// scalars.
+int ready_fail(int code, const char* fmt, ...);
+int ready_ok();
+void record_kernel(const char* fmt, ...);
+AdamScalars host_adam_scalars(const shardstep_adamw_t& hp);
+
 }  // namespace shardstep
