@@ -159,6 +159,9 @@ int set_tma_stage_limit(int stages);
 // The TMA-staged kernels' wait limit in ns (0: the default of two seconds);
 // read at each launch.  Returns the previous limit.
 int64_t set_tma_wait_ns(int64_t ns);
+unsigned long long tma_wait_limit();
+// The status word of the staged loss kernels (token_loss.cu).
+cudaError_t read_loss_status(unsigned int* status, bool clear);
 cudaError_t launch_rs_adamw_cast_tma(const PtrTable& tab, int nd, int grad_type, int64_t S,
                                      float* master, float* m, float* v, uint16_t* out,
                                      const AdamScalars& c, const MeanOp& mo,
@@ -329,11 +332,14 @@ cudaError_t launch_tensors_norm(const NormTable<CAP>& t, int type, const NormArg
 constexpr int kLossMaxBlocks = 1024;
 // The workspace of the token losses; the preference loss's per-token and
 // per-sequence words follow it.
+constexpr int kPairsPerLaunch = 1024;
 struct LossWork {
     unsigned int arrived;
     unsigned int pad_[3];
     double total[4];                        // carried from launch to launch
     double partial[kLossMaxBlocks][4];      // the blocks' sums
+    unsigned int rows_done[kPairsPerLaunch];  // of each pair; zero between launches
+    double pair_loss[kPairsPerLaunch][3];     // of each pair: loss, margin, margin > 0
 };
 struct TokenArgs {
     const void* x;          // logits, row i at x + i * x_stride
@@ -359,7 +365,6 @@ struct PolicyArgs {
 };
 // The sequences of one launch of the preference loss: pairs 2 p, 2 p + 1 are
 // its rows [start[2 p], start[2 p + 1]) and [start[2 p + 1], start[2 p + 2]).
-constexpr int kPairsPerLaunch = 1024;
 struct PairTable {
     int32_t start[2 * kPairsPerLaunch + 1];
     int32_t pairs;
@@ -367,18 +372,25 @@ struct PairTable {
 struct PreferenceArgs {
     float beta, smoothing;
     float* log_ratios;      // 2 per pair
-    float* row_max;         // per token
-    float* row_inv;         // per token: 1 / sum exp(x - max)
+    float* row_ref;         // per token: what its exponents refer to
+    float* row_sum;         // per token: the sum of its exponentials
     float* term;            // per token: w (a - ref)
+    int32_t* seq;           // per token: its sequence within the launch
     float* coef;            // per sequence: d loss / d a at weight 1
     int first, last;        // this launch starts / ends the call
 };
-cudaError_t launch_policy_loss(const TokenArgs& a, const PolicyArgs& p, int dtype,
+// Whether a row of v elements fits the staged kernels' shared memory.
+bool loss_row_fits(int64_t v, int dtype);
+// staged: rows go through shared memory (they fit, and the gradient's rows,
+// if any, start at the logits' rows' offsets from 16-byte boundaries).
+cudaError_t launch_policy_loss(const TokenArgs& a, const PolicyArgs& p, int dtype, bool staged,
                                cudaStream_t stream);
 cudaError_t launch_preference_forward(const TokenArgs& a, const PreferenceArgs& p,
-                                      const PairTable& t, int dtype, cudaStream_t stream);
+                                      const PairTable& t, int dtype, bool staged,
+                                      cudaStream_t stream);
 cudaError_t launch_preference_backward(const TokenArgs& a, const PreferenceArgs& p,
-                                       const PairTable& t, int dtype, cudaStream_t stream);
+                                       const PairTable& t, int dtype, bool staged,
+                                      cudaStream_t stream);
 
 // Host helpers of api.cpp for the other translation units: the last error of
 // the calling thread, the name shardstep_last_kernel reports, the per-step

@@ -1,26 +1,43 @@
 // Losses over a language model's logits, forward and backward: the clipped
 // policy loss with a KL term and the preference loss of paired sequences.
 //
-// With x a token's logits, y its id: mx = max x, S = sum exp(x - mx),
-// a = (x_y - mx) - log S.  The maximum is subtracted before the scaling to
-// base 2, so rows of the type's lowest value and rows with -inf entries are
-// right, and a is formed from differences, which keeps the digits that
-// x_y - (mx + log S) would lose.  Both losses have d loss / d x =
-// c (1[y] - softmax x) with one c per row, so a row is read for S, then again
-// for its gradient.  Statistics, terms and coefficients are fp32, sums over
-// tokens double; the gradient is rounded once, to the logits' type.
+// With x a token's logits and y its id, the row's exponentials refer to the
+// id's own logit, rounded to a whole power of two: e_j = 2^(x_j log2 e - R),
+// R = rint(x_y log2 e).  Their sum S is at least about 1 (the id's own term),
+// no maximum has to be known before the first term, and the log probability
+// a = ln 2 (x_y log2 e - R) - log S is formed from small numbers.  Where that
+// range does not do (S past 2^120, x_y infinite or huge, a NaN) the row is
+// summed again against its true maximum, which is subtracted before anything
+// is scaled, so rows of the type's lowest value and rows with -inf are right.
+// Both losses have d loss / d x = c (1[y] - softmax x) with one c per row.
+// Statistics, terms and coefficients are fp32, sums over tokens double; the
+// gradient is rounded once, to the logits' type.
+//
+// The staged kernels move a row through shared memory once: bulk copies bring
+// it in 16 KB chunks, 512 threads sum it, form the row's terms, overwrite it in
+// place with the gradient, and bulk copies store it, while the next rows are on
+// their way.  Each logit is read once and each gradient written once, the
+// least there is, and the kernel is bound by that traffic.  A row that does
+// not fit (or whose gradient lies at another offset from a 16-byte boundary)
+// takes the plain kernels, which read it again for the gradient (from L2).
 #include "common.cuh"
+#include "tma.cuh"
 
 namespace shardstep {
 namespace {
 
-constexpr int kRowThreads = 512;
-constexpr int kRowWarps = kRowThreads / 32;
+constexpr int kRowThreads = 512;              // threads of a plain kernel's block
+constexpr unsigned kFull = 0xFFFFFFFFu;
 // log2 e as the sum of two floats: the first alone is 1.3e-8 off, always to
 // the same side, which a sum over a sequence's tokens would gather up.
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLog2eLo = 1.9259629911e-8f;
-constexpr unsigned kFull = 0xFFFFFFFFu;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kFastLogit = 32768.0f;        // |x_y| below this: R and its products are fine
+constexpr float kFastSum = 0x1p120f;
+
+// Status of this device's staged loss launches (0 = no wait ran out).
+__device__ unsigned int g_loss_status = 0;
 
 __device__ __forceinline__ float exp2_approx(float x) {
     float y;
@@ -43,56 +60,121 @@ __device__ __forceinline__ void store1(void* p, int64_t i, float x) {
         static_cast<uint16_t*>(p)[i] = f32_to_bf16(x);
 }
 template <int GT>
+constexpr __host__ __device__ int elem_bytes() {
+    return GT == kGradF32 ? 4 : 2;
+}
+template <int GT>
 __device__ __forceinline__ const char* row_of(const void* x, int64_t i, int64_t stride) {
-    return static_cast<const char*>(x) + i * stride * (GT == kGradF32 ? 4 : 2);
+    return static_cast<const char*>(x) + i * stride * elem_bytes<GT>();
 }
 
-// A partial softmax sum: s = sum exp(x - m) over the elements seen, m their
-// maximum.  An m of -inf (nothing seen but -inf) refers to 0 instead, so that
-// no inf - inf arises; NaN elements reach s.
-struct Soft {
-    float m, s;
+// The T threads that work on one row, with a named barrier of their own.
+template <int T>
+struct TeamShared {
+    float part[2][T / 32];
+    double dpart[T / 32];
 };
-__device__ __forceinline__ float soft_ref(float m) { return m == -INFINITY ? 0.0f : m; }
-__device__ __forceinline__ float soft_exp(float x, float ref) {
-    const float d = __fsub_rn(x, ref);
+template <int T>
+struct Team {
+    int bar, tid;
+    TeamShared<T>* sh;
+
+    __device__ __forceinline__ void sync() const {
+        asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(T) : "memory");
+    }
+    // The same, true for all where any thread passes true.
+    __device__ __forceinline__ bool sync_or(bool any) const {
+        int r;
+        asm volatile(
+            "{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n bar.red.or.pred q, %2, %3, p;\n"
+            " selp.s32 %0, 1, 0, q;\n}\n"
+            : "=r"(r)
+            : "r"(static_cast<int>(any)), "r"(bar), "n"(T)
+            : "memory");
+        return r != 0;
+    }
+    // Sums and maxima over the team in a fixed order; every thread gets the
+    // result.  *any: in, this thread's; out, of all threads.  `turn` alternates
+    // between calls, so that one barrier per call is enough.
+    __device__ __forceinline__ float sum(float x, bool* any, int turn) const {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) x = __fadd_rn(x, __shfl_xor_sync(kFull, x, d));
+        if ((tid & 31) == 0) sh->part[turn][tid >> 5] = x;
+        *any = sync_or(*any);
+        x = sh->part[turn][tid & (T / 32 - 1)];
+#pragma unroll
+        for (int d = T / 64; d > 0; d >>= 1) x = __fadd_rn(x, __shfl_xor_sync(kFull, x, d));
+        return x;
+    }
+    __device__ __forceinline__ float max(float x) const {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, d));
+        sync();
+        if ((tid & 31) == 0) sh->part[0][tid >> 5] = x;
+        sync();
+        for (int w = 0; w < T / 32; ++w) x = fmaxf(x, sh->part[0][w]);
+        sync();
+        return x;
+    }
+    __device__ __forceinline__ double sum(double x) const {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(kFull, x, d);
+        sync();
+        if ((tid & 31) == 0) sh->dpart[tid >> 5] = x;
+        sync();
+        x = 0.0;
+        for (int w = 0; w < T / 32; ++w) x += sh->dpart[w];
+        sync();
+        return x;
+    }
+};
+
+// --------------------------------------------------- a row's exponentials
+
+// How a row's exponentials are formed: fast, 2^(x log2 e - ref); else
+// 2^((x - ref) log2 e) with ref the row's maximum (0 for a row of -inf).
+struct RowRef {
+    float ref;
+    bool fast;
+};
+__device__ __forceinline__ float row_exp(float x, RowRef r) {
+    if (r.fast) return exp2_approx(__fmaf_rn(x, kLog2e, __fmaf_rn(x, kLog2eLo, -r.ref)));
+    const float d = __fsub_rn(x, r.ref);
     return exp2_approx(__fmaf_rn(d, kLog2e, __fmul_rn(d, kLog2eLo)));
 }
-__device__ __forceinline__ Soft soft_join(Soft a, Soft b) {
-    const float m = fmaxf(a.m, b.m);
-    const float r = soft_ref(m);
-    return Soft{m, __fadd_rn(__fmul_rn(a.s, soft_exp(a.m, r)), __fmul_rn(b.s, soft_exp(b.m, r)))};
+__device__ __forceinline__ RowRef fast_ref(float xy) {
+    return RowRef{rintf(__fmul_rn(xy, kLog2e)), fabsf(xy) < kFastLogit};
+}
+// The id's log probability.
+__device__ __forceinline__ float row_logp(float xy, RowRef r, float sum) {
+    if (!r.fast) return __fsub_rn(__fsub_rn(xy, r.ref), logf(sum));
+    const float t = __fmaf_rn(xy, kLog2e, __fmaf_rn(xy, kLog2eLo, -r.ref));
+    return __fmaf_rn(t, kLn2, -logf(sum));
 }
 
-// All threads get the block's join, formed in a fixed order.
-__device__ __forceinline__ Soft block_soft(Soft a) {
-    __shared__ Soft part[kRowWarps];
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
-        a = soft_join(a, Soft{__shfl_xor_sync(kFull, a.m, d), __shfl_xor_sync(kFull, a.s, d)});
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = a;
-    __syncthreads();
-    a = part[threadIdx.x & (kRowWarps - 1)];
-#pragma unroll
-    for (int d = kRowWarps / 2; d > 0; d >>= 1)
-        a = soft_join(a, Soft{__shfl_xor_sync(kFull, a.m, d), __shfl_xor_sync(kFull, a.s, d)});
-    return a;
+// The sum against the true maximum, from global memory: rows that the fast
+// form does not cover.  The products of x - max stay in range whatever x is.
+struct SlowRow {
+    RowRef r;
+    float sum;
+};
+template <int GT, int T>
+__device__ __forceinline__ SlowRow slow_row(const char* x, int64_t v, const Team<T>& team) {
+    float m = -INFINITY;
+    for (int64_t j = team.tid; j < v; j += T) m = fmaxf(m, load1<GT>(x, j));
+    m = team.max(m);
+    const RowRef r{m == -INFINITY ? 0.0f : m, false};
+    float s = 0.0f;
+    for (int64_t j = team.tid; j < v; j += T) s = __fadd_rn(s, row_exp(load1<GT>(x, j), r));
+    bool none = false;
+    team.sync();
+    s = team.sum(s, &none, 0);
+    team.sync();
+    if (m == -INFINITY) s = NAN;   // nothing but -inf (or NaN): no distribution
+    return SlowRow{r, s};
 }
 
-// Thread 0 gets the block's sum in a fixed order.
-__device__ __forceinline__ double block_sum(double x) {
-    __shared__ double part[kRowWarps];
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) x += __shfl_down_sync(kFull, x, d);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = x;
-    __syncthreads();
-    double s = 0.0;
-    if (threadIdx.x == 0)
-        for (int w = 0; w < kRowWarps; ++w) s += part[w];
-    return s;
-}
+// -------------------------------------------------------- terms of a token
 
 // The row's id, or -1 where it lies outside the vocabulary: the token's log
 // probability is then NaN, and so is the loss.
@@ -101,55 +183,11 @@ __device__ __forceinline__ int64_t token_id(const TokenArgs& a, int64_t i) {
                               : static_cast<const int32_t*>(a.ids)[i];
     return y >= 0 && y < a.v ? y : -1;
 }
-
-template <int GT>
-__device__ __forceinline__ Soft row_soft(const char* x, int64_t v) {
-    Soft a{-INFINITY, 0.0f};
-    for (int64_t j = threadIdx.x; j < v; j += kRowThreads) {
-        const float f = load1<GT>(x, j);
-        const float m = fmaxf(a.m, f);
-        const float r = soft_ref(m);
-        a.s = __fadd_rn(__fmul_rn(a.s, soft_exp(a.m, r)), soft_exp(f, r));
-        a.m = m;
-    }
-    return block_soft(a);
+__device__ __forceinline__ float token_weight(const TokenArgs& a, int64_t i) {
+    return a.w != nullptr ? a.w[i] : 1.0f;
 }
-
-// grad = c (1[y] - exp(x - ref) inv), rounded once.
-template <int GT>
-__device__ __forceinline__ void row_grad(const char* x, char* g, int64_t v, int64_t y, float ref,
-                                         float inv, float c) {
-    const float f = -__fmul_rn(c, inv);
-    for (int64_t j = threadIdx.x; j < v; j += kRowThreads) {
-        float d = __fmul_rn(soft_exp(load1<GT>(x, j), ref), f);
-        if (j == y) d = __fadd_rn(d, c);
-        store1<GT>(g, j, d);
-    }
-}
-template <int GT>
-__device__ __forceinline__ void row_zero(char* g, int64_t v) {
-    for (int64_t j = threadIdx.x; j < v; j += kRowThreads) store1<GT>(g, j, 0.0f);
-}
-
-// The blocks' sums (thread 0's t) added up by the block that arrives last, in
-// block order; true there, with the sums in the workspace's total.
-__device__ __forceinline__ bool join_blocks(LossWork* ws, const double* t, bool first) {
-    __shared__ bool last;
-    if (threadIdx.x == 0) {
-        for (int k = 0; k < 4; ++k) ws->partial[blockIdx.x][k] = t[k];
-        __threadfence();
-        last = atomicInc(&ws->arrived, gridDim.x - 1) == gridDim.x - 1;
-    }
-    __syncthreads();
-    if (!last) return false;
-    __threadfence();
-    if (threadIdx.x < 4) {
-        double s = first ? 0.0 : ws->total[threadIdx.x];
-        for (unsigned b = 0; b < gridDim.x; ++b) s += __ldcg(&ws->partial[b][threadIdx.x]);
-        ws->total[threadIdx.x] = s;
-    }
-    __syncthreads();
-    return true;
+__device__ __forceinline__ float out_scale(const TokenArgs& a) {
+    return a.loss_scale != nullptr ? __fmul_rn(a.grad_scale, __ldg(a.loss_scale)) : a.grad_scale;
 }
 
 // One token's policy terms from its log probability:
@@ -178,70 +216,63 @@ __device__ __forceinline__ PolicyTerms policy_terms(float lp, float old, float a
 }
 
 // The divisor of the means: given, or the sum of the weights, which every
-// block adds up by itself in the same order.
-__device__ __forceinline__ float weight_sum(const TokenArgs& a) {
-    __shared__ float total;
+// team adds up by itself in the same order.
+template <int T>
+__device__ __forceinline__ float weight_sum(const TokenArgs& a, const Team<T>& team) {
     if (a.norm != 0.0f) return a.norm;
     if (a.w == nullptr) return static_cast<float>(a.n);
     double s = 0.0;
-    for (int64_t i = threadIdx.x; i < a.n; i += kRowThreads) s += static_cast<double>(a.w[i]);
-    s = block_sum(s);
-    if (threadIdx.x == 0) total = __double2float_rn(s);
-    __syncthreads();
-    return total;
+#pragma unroll 8
+    for (int64_t i = team.tid; i < a.n; i += T) s += static_cast<double>(a.w[i]);
+    return __double2float_rn(team.sum(s));
 }
 
-template <int GT>
-__global__ void __launch_bounds__(kRowThreads)
-    policy_rows(const TokenArgs a, const PolicyArgs p) {
-    pdl_enter();
-    const float norm = weight_sum(a);
-    const float out_scale =
-        a.loss_scale != nullptr ? __fmul_rn(a.grad_scale, __ldg(a.loss_scale)) : a.grad_scale;
-    double sums[4] = {0.0, 0.0, 0.0, 0.0};
-    for (int64_t i = blockIdx.x; i < a.n; i += gridDim.x) {
-        const char* x = row_of<GT>(a.x, i, a.x_stride);
-        char* g = const_cast<char*>(row_of<GT>(a.grad, i, a.g_stride));
-        const float w = a.w != nullptr ? a.w[i] : 1.0f;
-        if (w == 0.0f) {   // not read at all: whatever it holds takes no part
-            if (threadIdx.x == 0) a.logps[i] = 0.0f;
-            if (a.grad != nullptr) row_zero<GT>(g, a.v);
-            continue;
-        }
-        const int64_t y = token_id(a, i);
-        const float xy = y >= 0 ? load1<GT>(x, y) : NAN;
-        const Soft s = row_soft<GT>(x, a.v);
-        const float lp = __fsub_rn(__fsub_rn(xy, s.m), logf(s.s));
-        const PolicyTerms t =
-            policy_terms(lp, p.old[i], p.adv[i], p.kl != 0.0f ? a.ref[i] : 0.0f, p);
-        const float k = __fdiv_rn(w, norm);
-        if (threadIdx.x == 0) {
-            a.logps[i] = lp;
-            const double kd = k;
-            sums[0] += kd * __fadd_rn(t.policy, __fmul_rn(p.kl, t.kl));
-            sums[1] += kd * t.policy;
-            sums[2] += kd * t.kl;
-            sums[3] += kd * t.clipped;
-        }
-        if (a.grad != nullptr)
-            row_grad<GT>(x, g, a.v, y, soft_ref(s.m), __fdiv_rn(1.0f, s.s),
-                         __fmul_rn(__fmul_rn(t.slope, k), out_scale));
+// The blocks' sums (thread 0's t) added up by the block that arrives last, in a
+// fixed order; true there, with the sums in the workspace's total.  Every
+// thread of the block calls it.
+__device__ __forceinline__ bool join_blocks(LossWork* ws, const double* t) {
+    __shared__ bool last;
+    if (threadIdx.x == 0) {
+        for (int k = 0; k < 4; ++k) ws->partial[blockIdx.x][k] = t[k];
+        __threadfence();
+        last = atomicInc(&ws->arrived, gridDim.x - 1) == gridDim.x - 1;
     }
-    if (join_blocks(a.ws, sums, true) && threadIdx.x < 4)
-        a.stats[threadIdx.x] = __double2float_rn(a.ws->total[threadIdx.x]);
+    __syncthreads();
+    if (!last) return false;
+    __threadfence();
+    const unsigned k = threadIdx.x >> 5;      // a warp per sum
+    if (k < 4) {
+        double s = 0.0;
+#pragma unroll 8
+        for (unsigned b = threadIdx.x & 31; b < gridDim.x; b += 32)
+            s += __ldcg(&ws->partial[b][k]);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
+        if ((threadIdx.x & 31) == 0) ws->total[k] = s;
+    }
+    __syncthreads();
+    return true;
 }
 
-// The sequence that a row of the launch belongs to.
-__device__ __forceinline__ int find_sequence(const PairTable& t, int row) {
+__device__ __forceinline__ void add_policy(double* sums, const PolicyTerms& t,
+                                           const PolicyArgs& p, float k) {
+    const double kd = k;
+    sums[0] += kd * __fadd_rn(t.policy, __fmul_rn(p.kl, t.kl));
+    sums[1] += kd * t.policy;
+    sums[2] += kd * t.kl;
+    sums[3] += kd * t.clipped;
+}
+
+// The sequence of the launch that row i belongs to.
+__device__ __forceinline__ int find_sequence(const PairTable& t, int64_t i) {
     int lo = 0, hi = 2 * t.pairs - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (t.start[mid] <= row) lo = mid;
+        if (t.start[mid] <= i) lo = mid;
         else hi = mid - 1;
     }
     return lo;
 }
-
 __device__ __forceinline__ float softplus(float x) {
     return __fadd_rn(fmaxf(x, 0.0f), log1pf(expf(-fabsf(x))));
 }
@@ -249,141 +280,903 @@ __device__ __forceinline__ float sigmoid(float x) {
     return __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-x)));
 }
 
+// A pair's loss and slope from its tokens' terms, added up in a fixed order by
+// one warp.
+__device__ __forceinline__ void finish_pair(const TokenArgs& a, const PreferenceArgs& p,
+                                            const PairTable& t, int q) {
+    const int lane = threadIdx.x & 31;
+    float r[2];
+    for (int h = 0; h < 2; ++h) {
+        double s = 0.0;
+        const int end = t.start[2 * q + h + 1];
+        for (int i = t.start[2 * q + h] + lane; i < end; i += 8 * 32) {
+            float x[8];          // in flight together
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = i + 32 * k < end ? __ldcg(p.term + i + 32 * k) : 0.0f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) s += static_cast<double>(x[k]);
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
+        r[h] = __double2float_rn(s);
+    }
+    if (lane != 0) return;
+    const float h = __fmul_rn(p.beta, __fsub_rn(r[0], r[1]));
+    const float ls = p.smoothing, us = __fsub_rn(1.0f, ls);
+    p.log_ratios[2 * q] = r[0];
+    p.log_ratios[2 * q + 1] = r[1];
+    const float dh = __fsub_rn(__fmul_rn(ls, sigmoid(h)), __fmul_rn(us, sigmoid(-h)));
+    const float c = __fmul_rn(dh, __fdiv_rn(p.beta, a.norm));
+    p.coef[2 * q] = c;
+    p.coef[2 * q + 1] = -c;
+    a.ws->pair_loss[q][0] = __fadd_rn(__fmul_rn(us, softplus(-h)), __fmul_rn(ls, softplus(h)));
+    a.ws->pair_loss[q][1] = h;
+    a.ws->pair_loss[q][2] = h > 0.0f ? 1.0 : 0.0;
+}
+
+// `rows` more rows of pair q are done, their terms written by this warp's lane
+// 0: the warp that brings the pair's count to its rows finishes the pair.
+__device__ __forceinline__ void rows_done(const TokenArgs& a, const PreferenceArgs& p,
+                                          const PairTable& t, int q, unsigned rows) {
+    unsigned before = 0;
+    if ((threadIdx.x & 31) == 0)
+        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;"
+                     : "=r"(before)
+                     : "l"(&a.ws->rows_done[q]), "r"(rows)
+                     : "memory");
+    before = __shfl_sync(kFull, before, 0);
+    __syncwarp();
+    if (before + rows != static_cast<unsigned>(t.start[2 * q + 2] - t.start[2 * q])) return;
+    if ((threadIdx.x & 31) == 0) a.ws->rows_done[q] = 0;
+    finish_pair(a, p, t, q);
+}
+
+// Pairs without a token, which no row finishes.
+__device__ __forceinline__ void empty_pairs(const TokenArgs& a, const PreferenceArgs& p,
+                                            const PairTable& t) {
+    for (int q = blockIdx.x; q < t.pairs; q += gridDim.x)
+        if (t.start[2 * q + 2] == t.start[2 * q]) finish_pair(a, p, t, q);
+}
+
+// The pairs' losses, added up by the last block in pair order per lane.
+// Every thread of the block calls it.
+__device__ __forceinline__ void preference_stats(const TokenArgs& a, const PreferenceArgs& p,
+                                                 const PairTable& t) {
+    __shared__ bool last;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        __threadfence();
+        last = atomicInc(&a.ws->arrived, gridDim.x - 1) == gridDim.x - 1;
+        __threadfence();
+    }
+    __syncthreads();
+    if (!last || threadIdx.x >= 32) return;
+    for (int k = 0; k < 3; ++k) {
+        double s = 0.0;
+        for (int q = threadIdx.x; q < t.pairs; q += 32) s += __ldcg(&a.ws->pair_loss[q][k]);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
+        if (threadIdx.x == 0) {
+            s += p.first ? 0.0 : a.ws->total[k];
+            a.ws->total[k] = s;
+            if (p.last) a.stats[k] = __double2float_rn(__ddiv_rn(s, static_cast<double>(a.norm)));
+        }
+    }
+}
+
+// What the backward pass needs of a row; a negative sum marks the slow form.
+__device__ __forceinline__ void save_row(const PreferenceArgs& p, int64_t i, RowRef r, float sum) {
+    p.row_ref[i] = r.ref;
+    p.row_sum[i] = r.fast ? sum : -sum;
+}
+
+// The id's own gradient, c (1 - e_y / S), as (c / S) (S - e_y): the difference
+// is that of the other tokens' terms, and exactly 0 where there are none.
+__device__ __forceinline__ float own_grad(float e, float sum, float cs) {
+    return __fmul_rn(__fsub_rn(sum, e), cs);
+}
+
+// ------------------------------------------------------- the plain kernels
+
+template <int GT>
+__device__ __forceinline__ float plain_sum(const char* x, int64_t v, float xy, RowRef* r,
+                                           const Team<kRowThreads>& team) {
+    *r = fast_ref(xy);
+    float s = 0.0f;
+    if (r->fast)
+        for (int64_t j = threadIdx.x; j < v; j += kRowThreads)
+            s = __fadd_rn(s, row_exp(load1<GT>(x, j), *r));
+    bool none = false;
+    team.sync();
+    s = team.sum(s, &none, 0);
+    if (!r->fast || !(s < kFastSum)) {
+        const SlowRow q = slow_row<GT>(x, v, team);
+        *r = q.r;
+        s = q.sum;
+    }
+    return s;
+}
+// grad = c (1[y] - e / S), rounded once.
+template <int GT>
+__device__ __forceinline__ void plain_grad(const char* x, char* g, int64_t v, int64_t y, RowRef r,
+                                           float sum, float c) {
+    const float cs = __fdiv_rn(c, sum);
+    for (int64_t j = threadIdx.x; j < v; j += kRowThreads) {
+        const float e = row_exp(load1<GT>(x, j), r);
+        store1<GT>(g, j, j == y ? own_grad(e, sum, cs) : -__fmul_rn(e, cs));
+    }
+}
+template <int GT>
+__device__ __forceinline__ void plain_zero(char* g, int64_t v) {
+    for (int64_t j = threadIdx.x; j < v; j += kRowThreads) store1<GT>(g, j, 0.0f);
+}
+
+template <int GT>
+__global__ void __launch_bounds__(kRowThreads)
+    policy_rows(const TokenArgs a, const PolicyArgs p) {
+    __shared__ TeamShared<kRowThreads> sh;
+    const Team<kRowThreads> team{1, static_cast<int>(threadIdx.x), &sh};
+    pdl_enter();
+    const float norm = weight_sum(a, team), scale = out_scale(a);
+    double sums[4] = {0.0, 0.0, 0.0, 0.0};
+    for (int64_t i = blockIdx.x; i < a.n; i += gridDim.x) {
+        const char* x = row_of<GT>(a.x, i, a.x_stride);
+        char* g = const_cast<char*>(row_of<GT>(a.grad, i, a.g_stride));
+        const float w = token_weight(a, i);
+        if (w == 0.0f) {   // not read at all: whatever it holds takes no part
+            if (threadIdx.x == 0) a.logps[i] = 0.0f;
+            if (a.grad != nullptr) plain_zero<GT>(g, a.v);
+            continue;
+        }
+        const int64_t y = token_id(a, i);
+        const float xy = y >= 0 ? load1<GT>(x, y) : NAN;
+        RowRef r;
+        const float s = plain_sum<GT>(x, a.v, xy, &r, team);
+        const float lp = row_logp(xy, r, s);
+        const PolicyTerms t =
+            policy_terms(lp, p.old[i], p.adv[i], p.kl != 0.0f ? a.ref[i] : 0.0f, p);
+        const float k = __fdiv_rn(w, norm);
+        if (threadIdx.x == 0) {
+            a.logps[i] = lp;
+            add_policy(sums, t, p, k);
+        }
+        if (a.grad != nullptr)
+            plain_grad<GT>(x, g, a.v, y, r, s, __fmul_rn(__fmul_rn(t.slope, k), scale));
+    }
+    if (join_blocks(a.ws, sums) && threadIdx.x < 4)
+        a.stats[threadIdx.x] = __double2float_rn(a.ws->total[threadIdx.x]);
+}
+
 template <int GT>
 __global__ void __launch_bounds__(kRowThreads)
     preference_forward(const TokenArgs a, const PreferenceArgs p,
                        const __grid_constant__ PairTable t) {
+    __shared__ TeamShared<kRowThreads> sh;
+    const Team<kRowThreads> team{1, static_cast<int>(threadIdx.x), &sh};
     pdl_enter();
-    const int row0 = t.start[0], rows = t.start[2 * t.pairs] - row0;
-    for (int r = blockIdx.x; r < rows; r += gridDim.x) {
-        const int64_t i = row0 + r;
-        const float w = a.w != nullptr ? a.w[i] : 1.0f;
-        if (w == 0.0f) {
-            if (threadIdx.x == 0) {
-                a.logps[i] = 0.0f;
-                p.term[i] = 0.0f;
-            }
-            continue;
+    if (threadIdx.x < 32) empty_pairs(a, p, t);
+    const int64_t end = t.start[2 * t.pairs];
+    for (int64_t i = t.start[0] + static_cast<int64_t>(blockIdx.x); i < end; i += gridDim.x) {
+        const float w = token_weight(a, i);
+        const int seq = find_sequence(t, i);
+        float lp = 0.0f, term = 0.0f;
+        if (w != 0.0f) {
+            const char* x = row_of<GT>(a.x, i, a.x_stride);
+            const int64_t y = token_id(a, i);
+            const float xy = y >= 0 ? load1<GT>(x, y) : NAN;
+            RowRef r;
+            const float s = plain_sum<GT>(x, a.v, xy, &r, team);
+            lp = row_logp(xy, r, s);
+            term = __fmul_rn(w, __fsub_rn(lp, a.ref[i]));
+            if (threadIdx.x == 0) save_row(p, i, r, s);
         }
-        const char* x = row_of<GT>(a.x, i, a.x_stride);
-        const int64_t y = token_id(a, i);
-        const float xy = y >= 0 ? load1<GT>(x, y) : NAN;
-        const Soft s = row_soft<GT>(x, a.v);
         if (threadIdx.x == 0) {
-            const float lp = __fsub_rn(__fsub_rn(xy, s.m), logf(s.s));
             a.logps[i] = lp;
-            p.term[i] = __fmul_rn(w, __fsub_rn(lp, a.ref[i]));
-            p.row_max[i] = soft_ref(s.m);
-            p.row_inv[i] = __fdiv_rn(1.0f, s.s);
+            p.term[i] = term;
+            p.seq[i] = seq;
         }
+        if (threadIdx.x < 32) rows_done(a, p, t, seq >> 1, 1);
     }
-    // The last block: a warp per pair adds up its two sequences in a fixed
-    // order and forms the pair's loss and slope.
-    const double none[4] = {0.0, 0.0, 0.0, 0.0};
-    if (!join_blocks(a.ws, none, p.first != 0)) return;
-    const int lane = threadIdx.x & 31;
-    const float norm = a.norm;
-    double sums[3] = {0.0, 0.0, 0.0};
-    for (int q = threadIdx.x >> 5; q < t.pairs; q += kRowWarps) {
-        float r[2];
-        for (int h = 0; h < 2; ++h) {
-            double s = 0.0;
-            for (int i = t.start[2 * q + h] + lane; i < t.start[2 * q + h + 1]; i += 32)
-                s += static_cast<double>(__ldcg(p.term + i));
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
-            r[h] = __double2float_rn(s);
-        }
-        const float h = __fmul_rn(p.beta, __fsub_rn(r[0], r[1]));
-        const float ls = p.smoothing, us = __fsub_rn(1.0f, ls);
-        if (lane == 0) {
-            p.log_ratios[2 * q] = r[0];
-            p.log_ratios[2 * q + 1] = r[1];
-            const float dh = __fsub_rn(__fmul_rn(ls, sigmoid(h)), __fmul_rn(us, sigmoid(-h)));
-            const float c = __fmul_rn(dh, __fdiv_rn(p.beta, norm));
-            p.coef[2 * q] = c;
-            p.coef[2 * q + 1] = -c;
-            sums[0] += __fadd_rn(__fmul_rn(us, softplus(-h)), __fmul_rn(ls, softplus(h)));
-            sums[1] += h;
-            sums[2] += h > 0.0f ? 1.0 : 0.0;
-        }
-    }
-    for (int k = 0; k < 3; ++k) {
-        const double s = block_sum(lane == 0 ? sums[k] : 0.0);
-        if (threadIdx.x == 0) {
-            a.ws->total[k] += s;
-            if (p.last)
-                a.stats[k] = __double2float_rn(__ddiv_rn(a.ws->total[k], static_cast<double>(norm)));
-        }
-    }
+    preference_stats(a, p, t);
 }
 
 template <int GT>
 __global__ void __launch_bounds__(kRowThreads)
-    preference_backward(const TokenArgs a, const PreferenceArgs p,
-                        const __grid_constant__ PairTable t) {
+    preference_backward(const TokenArgs a, const PreferenceArgs p, int64_t begin, int64_t end) {
     pdl_enter();
-    const float out_scale =
-        a.loss_scale != nullptr ? __fmul_rn(a.grad_scale, __ldg(a.loss_scale)) : a.grad_scale;
-    const int row0 = t.start[0], rows = t.start[2 * t.pairs] - row0;
-    for (int r = blockIdx.x; r < rows; r += gridDim.x) {
-        const int64_t i = row0 + r;
+    const float scale = out_scale(a);
+    for (int64_t i = begin + blockIdx.x; i < end; i += gridDim.x) {
         char* g = const_cast<char*>(row_of<GT>(a.grad, i, a.g_stride));
-        const float w = a.w != nullptr ? a.w[i] : 1.0f;
+        const float w = token_weight(a, i);
         if (w == 0.0f) {
-            row_zero<GT>(g, a.v);
+            plain_zero<GT>(g, a.v);
             continue;
         }
-        const float c = __fmul_rn(__fmul_rn(p.coef[find_sequence(t, static_cast<int>(i))], w),
-                                  out_scale);
-        row_grad<GT>(row_of<GT>(a.x, i, a.x_stride), g, a.v, token_id(a, i), p.row_max[i],
-                     p.row_inv[i], c);
+        const float c = __fmul_rn(__fmul_rn(p.coef[p.seq[i]], w), scale);
+        const float s = p.row_sum[i];
+        plain_grad<GT>(row_of<GT>(a.x, i, a.x_stride), g, a.v, token_id(a, i),
+                       RowRef{p.row_ref[i], !(s < 0.0f)}, fabsf(s), c);
     }
 }
 
-int row_blocks(int64_t rows) {
-    const int64_t most = 2 * static_cast<int64_t>(device_sms());
+// ------------------------------------------------------ the staged kernels
+
+constexpr int kChunk = 16384;                 // bytes of a chunk, of a slot
+constexpr int kSlots = 13;                    // slots of the ring: 208 KB
+constexpr int kZeroBytes = 4096;
+constexpr size_t kStagedSmem = static_cast<size_t>(kSlots) * kChunk + kZeroBytes;
+
+enum class Pass { kPolicy, kPolicyForward, kPreferenceForward, kPreferenceBackward };
+constexpr __host__ __device__ bool has_sum(Pass m) { return m != Pass::kPreferenceBackward; }
+constexpr __host__ __device__ bool has_grad(Pass m) {
+    return m == Pass::kPolicy || m == Pass::kPreferenceBackward;
+}
+
+// A row's bytes: `head` elements up to the first 16-byte boundary, `body` bytes
+// in whole 16-byte vectors from there, `tail` elements after them (a row
+// without a whole vector is all head).
+struct RowBytes {
+    const char* body_at;
+    uint32_t body;
+    int head, tail;
+};
+template <int GT>
+__device__ __forceinline__ RowBytes row_bytes(const char* row, int64_t v) {
+    constexpr int es = elem_bytes<GT>();
+    const uintptr_t a = reinterpret_cast<uintptr_t>(row), b = a + v * es;
+    const uintptr_t a16 = (a + 15) & ~uintptr_t{15}, b16 = b & ~uintptr_t{15};
+    if (b16 <= a16) return RowBytes{row, 0, static_cast<int>(v), 0};
+    return RowBytes{row + (a16 - a), static_cast<uint32_t>(b16 - a16),
+                    static_cast<int>((a16 - a) / es), static_cast<int>((b - b16) / es)};
+}
+
+// Pairs of fp32 values in one instruction, held in a 64-bit register pair.
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair make_pair(float lo, float hi) {
+    Pair p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
+    return p;
+}
+__device__ __forceinline__ float2 floats(Pair p) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p));
+    return f;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+    Pair d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+    Pair d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ Pair exp2_pair(Pair t) {
+    const float2 f = floats(t);
+    return make_pair(exp2_approx(f.x), exp2_approx(f.y));
+}
+
+// The k-th pair of a 16-byte vector as floats, and back.
+template <int GT>
+constexpr __host__ __device__ int vec_pairs() {
+    return 16 / elem_bytes<GT>() / 2;
+}
+template <int GT>
+__device__ __forceinline__ Pair pair_of(const uint4& u, int k) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    if constexpr (GT == kGradF32) {
+        return make_pair(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
+    } else if constexpr (GT == kGradF16) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+        return make_pair(f.x, f.y);
+    } else {
+        return make_pair(bf16_lo(w[k]), bf16_hi(w[k]));
+    }
+}
+template <int GT>
+__device__ __forceinline__ uint32_t pack_pair(Pair p) {
+    const float2 x = floats(p);
+    if constexpr (GT == kGradF16) {
+        const __half2 h = __floats2half2_rn(x.x, x.y);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return pack_bf16x2(x.x, x.y);
+}
+
+// The constants of a row's fast exponentials, both halves alike.
+struct FastRow {
+    Pair hi, lo, neg_ref;
+};
+__device__ __forceinline__ FastRow fast_row(RowRef r) {
+    return FastRow{make_pair(kLog2e, kLog2e), make_pair(kLog2eLo, kLog2eLo),
+                   make_pair(-r.ref, -r.ref)};
+}
+// acc += the fast exponentials of a vector.
+template <int GT>
+__device__ __forceinline__ void sum_vector(const uint4& u, const FastRow& r, Pair* acc) {
+#pragma unroll
+    for (int k = 0; k < vec_pairs<GT>(); ++k) {
+        const Pair x = pair_of<GT>(u, k);
+        acc[k & 1] = add2(acc[k & 1], exp2_pair(fma2(x, r.hi, fma2(x, r.lo, r.neg_ref))));
+    }
+}
+// A vector's gradient without the id's own term, e f.  For 16-bit logits the
+// low part of log2 e is left out (below 2e-8 |x| of a value that is rounded to
+// 2^-9 or 2^-12).
+template <int GT>
+__device__ __forceinline__ uint4 pack_vector(const Pair* o) {
+    if constexpr (GT == kGradF32) {
+        const float2 a = floats(o[0]), b = floats(o[1]);
+        return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x),
+                          __float_as_uint(b.y));
+    } else {
+        return make_uint4(pack_pair<GT>(o[0]), pack_pair<GT>(o[1]), pack_pair<GT>(o[2]),
+                          pack_pair<GT>(o[3]));
+    }
+}
+template <int GT>
+__device__ __forceinline__ uint4 grad_vector(const uint4& u, const FastRow& r, Pair f) {
+    Pair o[vec_pairs<GT>()];
+#pragma unroll
+    for (int k = 0; k < vec_pairs<GT>(); ++k) {
+        const Pair x = pair_of<GT>(u, k);
+        const Pair t = fma2(x, r.hi, GT == kGradF32 ? fma2(x, r.lo, r.neg_ref) : r.neg_ref);
+        o[k] = mul2(exp2_pair(t), f);
+    }
+    return pack_vector<GT>(o);
+}
+template <int GT>
+__device__ __forceinline__ uint4 grad_vector_slow(const uint4& u, RowRef r, Pair f) {
+    Pair o[vec_pairs<GT>()];
+#pragma unroll
+    for (int k = 0; k < vec_pairs<GT>(); ++k) {
+        const float2 x = floats(pair_of<GT>(u, k));
+        o[k] = mul2(make_pair(row_exp(x.x, r), row_exp(x.y, r)), f);
+    }
+    return pack_vector<GT>(o);
+}
+
+// The ring's position: the slot of the next chunk and its barriers' parity.
+struct Ring {
+    int slot;
+    uint32_t parity;
+    __device__ __forceinline__ void next() {
+        if (++slot == kSlots) {
+            slot = 0;
+            parity ^= 1u;
+        }
+    }
+    __device__ __forceinline__ void skip(uint32_t chunks) {   // at most kSlots
+        slot += static_cast<int>(chunks);
+        if (slot >= kSlots) {
+            slot -= kSlots;
+            parity ^= 1u;
+        }
+    }
+};
+
+// What the computing warps need of a row besides its logits.
+struct RowParam {
+    float w;        // 0: the row takes no part
+    int32_t y;      // the id, -1 outside the vocabulary
+    float xy;       // its logit (forward passes)
+    float f[3];     // policy: old, advantage, ref; preference forward: ref;
+                    // backward: c, the reference and the sum of the exponentials
+};
+// A finished row of the preference loss's forward pass.
+struct RowResult {
+    float logp, term, ref, sum;
+};
+constexpr int kBatch = 32;            // rows whose parameters are fetched at once
+constexpr int kResults = 4;
+
+// One block per SM takes rows blockIdx.x, + gridDim.x, ... of the launch.
+//   2 teams of 8 computing warps, live rows in turn: sum a row's chunks as they
+//     land, join, form the row's terms, then overwrite the chunks with the
+//     gradient; the up to 15 + 7 elements outside whole vectors stay in the
+//     registers of the team's first warp.  While one team joins its sum and
+//     forms its terms the other has the arithmetic units;
+//   loading warp: per live row, its body's chunks into free slots;
+//   storing warp: stores each finished chunk and frees its slot; rows of weight
+//     0 are stored from a zeroed piece of shared memory.  In the preference
+//     loss's forward pass, which stores no rows, it writes the rows' words,
+//     counts their pairs' rows and finishes pairs, off the computing warps' path;
+//   parameter warp: the rows' weights, ids, logits of the ids and so on, 32
+//     rows ahead at a time: fetched row by row, these dependent loads took 3 of
+//     the 6.5 us that a row of 32000 bf16 logits used to take.
+// Without a gradient the computing warps free the slots themselves.  Every wait
+// is bounded: one that runs out sets a status bit, the block leaves at the end
+// of the row, and its copies in flight are waited for first.
+constexpr int kTeams = 2;
+constexpr int kTeamThreads = 256, kTeamWarps = kTeamThreads / 32;
+constexpr int kWorkWarps = kTeams * kTeamWarps;
+constexpr int kLoadWarp = kWorkWarps, kStoreWarp = kWorkWarps + 1, kParamWarp = kWorkWarps + 2;
+constexpr int kStagedThreads = 32 * (kWorkWarps + 3);
+static_assert(kResults % kTeams == 0, "a team's rows keep to their result slots");
+
+template <int GT, Pass M>
+__global__ void __launch_bounds__(kStagedThreads, 1)
+    staged_rows(const TokenArgs a, const PolicyArgs pol, const PreferenceArgs p,
+                const __grid_constant__ PairTable t, int64_t begin, int64_t end,
+                unsigned long long wait_ns) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ TeamShared<kTeamThreads> sh[kTeams];
+    __shared__ double team_sums[kTeams][4];
+    __shared__ uint64_t full[kSlots], done[kSlots], empty[kSlots];
+    __shared__ uint64_t param_full[2], param_empty[2], result_full[kResults],
+        result_empty[kResults];
+    __shared__ RowParam params[2][kBatch];
+    __shared__ RowResult results[kResults];
+    uint8_t* zeros = smem + static_cast<size_t>(kSlots) * kChunk;
+    constexpr int es = elem_bytes<GT>();
+    constexpr bool kPref = M == Pass::kPreferenceForward;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int s = 0; s < kSlots; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&done[s], kTeamWarps);
+            mbar_init(&empty[s], has_grad(M) ? 1 : kTeamWarps);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&param_full[s], 1);
+            mbar_init(&param_empty[s], kWorkWarps);
+        }
+        for (int s = 0; s < kResults; ++s) {
+            mbar_init(&result_full[s], 1);
+            mbar_init(&result_empty[s], 1);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (has_grad(M))
+        for (int k = tid; k < kZeroBytes / 4; k += kStagedThreads)
+            reinterpret_cast<uint32_t*>(zeros)[k] = 0;
+    fence_async();
+    __syncthreads();
+    pdl_enter();
+    double sums[4] = {0.0, 0.0, 0.0, 0.0};
+    const int64_t first = begin + blockIdx.x;
+    const int64_t rows = first < end ? (end - first + gridDim.x - 1) / gridDim.x : 0;
+    const auto row_at = [&](int64_t j) { return first + j * gridDim.x; };
+    // which of the 32 rows from j on are live, one weight per lane
+    const auto live_mask = [&](int64_t j) {
+        const bool live = j + lane < rows && token_weight(a, row_at(j + lane)) != 0.0f;
+        return __ballot_sync(kFull, live);
+    };
+
+    if (warp == kLoadWarp) {
+        Ring r{0, 0};
+        int64_t issued = 0;
+        bool ok = true;
+        unsigned next = live_mask(0);
+        for (int64_t j = 0; j < rows && ok; j += 32) {
+            unsigned live = next;
+            next = live_mask(j + 32);
+            if (lane == 0) {
+                for (; live != 0 && ok; live &= live - 1) {
+                    const int64_t i = row_at(j + __ffs(live) - 1);
+                    const RowBytes b = row_bytes<GT>(row_of<GT>(a.x, i, a.x_stride), a.v);
+                    for (uint32_t o = 0; o < b.body; o += kChunk) {
+                        if (issued >= kSlots &&
+                            !mbar_wait(&empty[r.slot], r.parity ^ 1u, wait_ns)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t n = b.body - o < kChunk ? b.body - o : kChunk;
+                        mbar_expect_tx(&full[r.slot], n);
+                        bulk_load(smem + static_cast<size_t>(r.slot) * kChunk, b.body_at + o, n,
+                                  &full[r.slot]);
+                        r.next();
+                        ++issued;
+                    }
+                }
+            }
+            ok = __shfl_sync(kFull, static_cast<int>(ok), 0) != 0;
+        }
+        if (lane == 0) {
+            if (!ok) atomicOr(&g_loss_status, kStatusProducerTimeout);
+            // the last (at most kSlots) chunks land before the block may exit
+            const int64_t skip = issued > kSlots ? issued - kSlots : 0;
+            Ring d{static_cast<int>(skip % kSlots), static_cast<uint32_t>(skip / kSlots) & 1u};
+            bool drained = true;
+            for (int64_t k = skip; k < issued; ++k) {
+                drained = mbar_wait(&full[d.slot], d.parity, kDrainNs) && drained;
+                d.next();
+            }
+            if (!drained) atomicOr(&g_loss_status, kStatusDrainTimeout);
+        }
+    } else if (warp == kStoreWarp && has_grad(M)) {
+        Ring r{0, 0};
+        int held = -1;                // the slot of the newest store group, or none
+        bool ok = true;
+        unsigned next = live_mask(0);
+        for (int64_t j0 = 0; j0 < rows && ok; j0 += 32) {
+            const unsigned live = next;
+            next = live_mask(j0 + 32);
+            for (int64_t j = j0; j < rows && j < j0 + 32 && ok; ++j) {
+                char* g = const_cast<char*>(row_of<GT>(a.grad, row_at(j), a.g_stride));
+                const RowBytes b = row_bytes<GT>(g, a.v);
+                char* dst = const_cast<char*>(b.body_at);
+                if (!((live >> (j - j0)) & 1u)) {
+                    if (lane < b.head) store1<GT>(g, lane, 0.0f);
+                    if (lane < b.tail) store1<GT>(dst + b.body, lane, 0.0f);
+                    if (lane == 0) {
+                        for (uint32_t o = 0; o < b.body; o += kZeroBytes)
+                            bulk_store(dst + o, zeros,
+                                       b.body - o < kZeroBytes ? b.body - o : kZeroBytes);
+                        bulk_commit();
+                    }
+                    continue;
+                }
+                for (uint32_t o = 0; o < b.body; o += kChunk) {
+                    ok = __all_sync(kFull, mbar_wait(&done[r.slot], r.parity, wait_ns));
+                    if (!ok) break;
+                    if (lane == 0) {
+                        bulk_store(dst + o, smem + static_cast<size_t>(r.slot) * kChunk,
+                                   b.body - o < kChunk ? b.body - o : kChunk);
+                        bulk_commit();
+                        if (held >= 0) {      // the store before this one has been read
+                            bulk_wait_read<1>();
+                            mbar_arrive(&empty[held]);
+                        }
+                        held = r.slot;
+                    }
+                    r.next();
+                }
+                // the loading warp may want the row's last slot at once
+                if (lane == 0 && held >= 0) {
+                    bulk_wait_read<0>();
+                    mbar_arrive(&empty[held]);
+                }
+                held = -1;
+            }
+        }
+        if (!ok && lane == 0) atomicOr(&g_loss_status, kStatusProducerTimeout);
+        if (lane == 0) bulk_wait_all();
+    } else if (warp == kStoreWarp && kPref) {
+        // words of the rows, and the pairs that they complete
+        empty_pairs(a, p, t);
+        int64_t k = 0;                // live rows so far
+        int pair = -1;
+        unsigned count = 0;
+        bool ok = true;
+        unsigned next = live_mask(0);
+        for (int64_t j0 = 0; j0 < rows && ok; j0 += 32) {
+            const unsigned live = next;
+            next = live_mask(j0 + 32);
+            // lane l looks row j0 + l up
+            const int mine = j0 + lane < rows ? find_sequence(t, row_at(j0 + lane)) : 0;
+            for (int64_t j = j0; j < rows && j < j0 + 32; ++j) {
+                const int64_t i = row_at(j);
+                const int seq = __shfl_sync(kFull, mine, static_cast<int>(j - j0));
+                if (seq >> 1 != pair && count != 0) {
+                    rows_done(a, p, t, pair, count);
+                    count = 0;
+                }
+                pair = seq >> 1;
+                RowResult res{0.0f, 0.0f, 0.0f, 0.0f};
+                if ((live >> (j - j0)) & 1u) {
+                    const int s = static_cast<int>(k % kResults);
+                    ok = __all_sync(kFull, mbar_wait(&result_full[s],
+                                                     static_cast<uint32_t>(k / kResults) & 1u,
+                                                     wait_ns));
+                    if (!ok) break;
+                    res = results[s];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&result_empty[s]);
+                    ++k;
+                }
+                if (lane == 0) {
+                    a.logps[i] = res.logp;
+                    p.term[i] = res.term;
+                    p.row_ref[i] = res.ref;
+                    p.row_sum[i] = res.sum;
+                    p.seq[i] = seq;
+                }
+                ++count;
+            }
+        }
+        if (ok && count != 0) rows_done(a, p, t, pair, count);
+        if (!ok && lane == 0) atomicOr(&g_loss_status, kStatusConsumerTimeout);
+    } else if (warp == kParamWarp) {
+        const float scale = M == Pass::kPreferenceBackward ? out_scale(a) : 0.0f;
+        bool ok = true;
+        for (int64_t j = 0, n = 0; j < rows && ok; j += kBatch, ++n) {
+            const int buf = static_cast<int>(n & 1);
+            RowParam q{0.0f, -1, 0.0f, {0.0f, 0.0f, 0.0f}};
+            if (j + lane < rows) {
+                const int64_t i = row_at(j + lane);
+                q.w = token_weight(a, i);
+                if (M == Pass::kPolicy || M == Pass::kPolicyForward) {
+                    q.f[0] = pol.old[i];
+                    q.f[1] = pol.adv[i];
+                    if (pol.kl != 0.0f) q.f[2] = a.ref[i];
+                } else if (kPref) {
+                    q.f[0] = a.ref[i];
+                }
+                if (q.w != 0.0f) {
+                    const int64_t y = token_id(a, i);
+                    q.y = static_cast<int32_t>(y);
+                    if (has_sum(M)) {
+                        q.xy = y >= 0 ? load1<GT>(row_of<GT>(a.x, i, a.x_stride), y) : NAN;
+                    } else {
+                        q.f[0] = __fmul_rn(__fmul_rn(p.coef[p.seq[i]], q.w), scale);
+                        q.f[1] = p.row_ref[i];
+                        q.f[2] = p.row_sum[i];
+                    }
+                } else if (has_sum(M) && !kPref) {
+                    a.logps[i] = 0.0f;
+                }
+            }
+            if (n >= 2)
+                ok = __all_sync(kFull, mbar_wait(&param_empty[buf],
+                                                 static_cast<uint32_t>((n >> 1) - 1) & 1u,
+                                                 wait_ns));
+            if (!ok) break;
+            params[buf][lane] = q;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&param_full[buf]);
+        }
+        if (!ok && lane == 0) atomicOr(&g_loss_status, kStatusProducerTimeout);
+    } else if (warp < kWorkWarps) {
+        const int which = warp / kTeamWarps;
+        const Team<kTeamThreads> team{1 + which, tid - which * kTeamThreads, &sh[which]};
+        float norm = 0.0f;
+        if (M == Pass::kPolicy || M == Pass::kPolicyForward) norm = weight_sum(a, team);
+        const float scale = M == Pass::kPolicy ? out_scale(a) : 0.0f;
+        Ring ring{0, 0};
+        // a wait that ran out: `bad` is made the same for the whole team at a
+        // barrier before any of it leaves; `late` is its first thread's until then
+        bool bad = false, late = false;
+        int turn = 0;
+        int64_t live = 0;
+        for (int64_t j = 0; j < rows && !bad; ++j) {
+            const int buf = static_cast<int>((j / kBatch) & 1);
+            if (j % kBatch == 0)
+                bad = !mbar_wait(&param_full[buf], static_cast<uint32_t>(j / (2 * kBatch)) & 1u,
+                                 wait_ns);
+            const RowParam q = params[buf][j % kBatch];
+            if (j % kBatch == kBatch - 1) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&param_empty[buf]);
+            }
+            if (j % kBatch == 0) bad = team.sync_or(bad);
+            if (bad) break;
+            if (q.w == 0.0f) continue;
+            const int64_t i = row_at(j);
+            const char* x = row_of<GT>(a.x, i, a.x_stride);
+            const RowBytes b = row_bytes<GT>(x, a.v);
+            const int64_t row = live++;
+            if (row % kTeams != which) {      // the other team's
+                ring.skip((b.body + kChunk - 1) / kChunk);
+                continue;
+            }
+            // this lane's element outside the whole vectors, if any
+            int64_t edge = -1;
+            if (team.tid < 32) {
+                if (lane < 16 && lane < b.head) edge = lane;
+                if (lane >= 16 && lane - 16 < b.tail) edge = a.v - b.tail + lane - 16;
+            }
+            const float xe = edge >= 0 ? load1<GT>(x, edge) : 0.0f;
+            RowRef r;
+            float s, c;
+            if (has_sum(M)) {
+                r = fast_ref(q.xy);
+                const FastRow fr = fast_row(r);
+                Pair acc[2] = {0, 0};
+                Ring at_ring = ring;
+                for (uint32_t o = 0; o < b.body; o += kChunk) {
+                    bad = bad || !mbar_wait(&full[at_ring.slot], at_ring.parity, wait_ns);
+                    const uint32_t n = b.body - o < kChunk ? b.body - o : kChunk;
+                    const uint8_t* in = smem + static_cast<size_t>(at_ring.slot) * kChunk;
+                    if (r.fast && !bad) {
+#pragma unroll
+                        for (int k = 0; k < kChunk / (16 * kTeamThreads); ++k) {
+                            const uint32_t at = 16 * (k * kTeamThreads + team.tid);
+                            if (at < n)
+                                sum_vector<GT>(*reinterpret_cast<const uint4*>(in + at), fr, acc);
+                        }
+                    }
+                    if (!has_grad(M)) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&empty[at_ring.slot]);
+                    }
+                    at_ring.next();
+                }
+                if (!has_grad(M)) ring = at_ring;
+                const float2 total = floats(add2(acc[0], acc[1]));
+                s = __fadd_rn(total.x, total.y);
+                if (edge >= 0 && r.fast) s = __fadd_rn(s, row_exp(xe, r));
+                bad = bad || late;
+                s = team.sum(s, &bad, turn);
+                turn ^= 1;
+                if (bad) break;
+                if (!r.fast || !(s < kFastSum)) {
+                    const SlowRow sr = slow_row<GT>(x, a.v, team);
+                    r = sr.r;
+                    s = sr.sum;
+                }
+                if (kPref) {
+                    if (team.tid == 0) {
+                        const int slot = static_cast<int>(row % kResults);
+                        late = row >= kResults &&
+                               !mbar_wait(&result_empty[slot],
+                                          (static_cast<uint32_t>(row / kResults) & 1u) ^ 1u,
+                                          wait_ns);
+                        const float lp = row_logp(q.xy, r, s);
+                        results[slot] = RowResult{lp, __fmul_rn(q.w, __fsub_rn(lp, q.f[0])),
+                                                  r.ref, r.fast ? s : -s};
+                        mbar_arrive(&result_full[slot]);
+                    }
+                } else {
+                    const float lp = row_logp(q.xy, r, s);
+                    const PolicyTerms pt = policy_terms(lp, q.f[0], q.f[1], q.f[2], pol);
+                    const float k = __fdiv_rn(q.w, norm);
+                    c = __fmul_rn(__fmul_rn(pt.slope, k), scale);
+                    if (team.tid == 0) {
+                        a.logps[i] = lp;
+                        add_policy(sums, pt, pol, k);
+                    }
+                }
+            } else {
+                c = q.f[0];
+                s = fabsf(q.f[2]);
+                r = RowRef{q.f[1], !(q.f[2] < 0.0f)};
+            }
+            if (has_grad(M)) {
+                const float cs = __fdiv_rn(c, s);
+                char* g = const_cast<char*>(row_of<GT>(a.grad, i, a.g_stride));
+                // the id's place among the vectors of the body, in bytes
+                const int64_t yb = q.y < b.head ? -1 : static_cast<int64_t>(q.y - b.head) * es;
+                const FastRow fr = fast_row(r);
+                const Pair f = make_pair(-cs, -cs);
+                for (uint32_t o = 0; o < b.body; o += kChunk) {
+                    if (!has_sum(M))
+                        bad = bad || !mbar_wait(&full[ring.slot], ring.parity, wait_ns);
+                    const uint32_t n = b.body - o < kChunk ? b.body - o : kChunk;
+                    uint8_t* io = smem + static_cast<size_t>(ring.slot) * kChunk;
+                    // the id's element, if it is in this chunk: its vector's thread
+                    // takes the logit before and writes the gradient after the vector
+                    const int64_t in = yb - o;
+                    const bool own = in >= 0 && in < n && in / 16 % kTeamThreads == team.tid;
+                    const float xv = own && !bad ? load1<GT>(io, in / es) : 0.0f;
+                    if (r.fast && !bad) {
+#pragma unroll
+                        for (int k = 0; k < kChunk / (16 * kTeamThreads); ++k) {
+                            const uint32_t at = 16 * (k * kTeamThreads + team.tid);
+                            uint4* v4 = reinterpret_cast<uint4*>(io + at);
+                            if (at < n) *v4 = grad_vector<GT>(*v4, fr, f);
+                        }
+                    } else if (!bad) {
+                        for (uint32_t at = 16 * team.tid; at < n; at += 16 * kTeamThreads) {
+                            uint4* v4 = reinterpret_cast<uint4*>(io + at);
+                            *v4 = grad_vector_slow<GT>(*v4, r, f);
+                        }
+                    }
+                    if (own && !bad) store1<GT>(io, in / es, own_grad(row_exp(xv, r), s, cs));
+                    fence_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&done[ring.slot]);
+                    ring.next();
+                }
+                if (edge >= 0) {
+                    const float e = row_exp(xe, r);
+                    store1<GT>(g, edge, edge == q.y ? own_grad(e, s, cs) : -__fmul_rn(e, cs));
+                }
+                if (!has_sum(M)) bad = team.sync_or(bad);
+            }
+        }
+        if ((bad || late) && team.tid == 0) atomicOr(&g_loss_status, kStatusConsumerTimeout);
+        if (team.tid == 0)
+            for (int k = 0; k < 4; ++k) team_sums[which][k] = sums[k];
+    }
+    if (kPref) preference_stats(a, p, t);
+    if (M == Pass::kPolicy || M == Pass::kPolicyForward) {
+        __syncthreads();
+        if (tid == 0)
+            for (int w = 1; w < kTeams; ++w)
+                for (int k = 0; k < 4; ++k) sums[k] += team_sums[w][k];
+        if (join_blocks(a.ws, sums) && tid < 4) a.stats[tid] = __double2float_rn(a.ws->total[tid]);
+    }
+}
+
+int row_blocks(int64_t rows, int per_sm) {
+    const int64_t most = per_sm * static_cast<int64_t>(device_sms());
     const int64_t cap = most < kLossMaxBlocks ? most : kLossMaxBlocks;
     return static_cast<int>(rows < 1 ? 1 : rows < cap ? rows : cap);
 }
 
+template <int GT, Pass M>
+cudaError_t go_staged(const TokenArgs& a, const PolicyArgs& pol, const PreferenceArgs& p,
+                      const PairTable& t, int64_t begin, int64_t end, cudaStream_t s) {
+    static int attr_set[256];   // dynamic shared memory opt-in applied
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 256 || !attr_set[dev]) {
+        e = cudaFuncSetAttribute(staged_rows<GT, M>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(kStagedSmem));
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 256) attr_set[dev] = 1;
+    }
+    return launch_after(staged_rows<GT, M>, dim3(row_blocks(end - begin, 1)),
+                        dim3(kStagedThreads), kStagedSmem, s, a, pol, p, t, begin, end,
+                        tma_wait_limit());
+}
+
 template <int GT>
-cudaError_t go_policy(const TokenArgs& a, const PolicyArgs& p, cudaStream_t s) {
-    return launch_after(policy_rows<GT>, dim3(row_blocks(a.n)), dim3(kRowThreads), 0, s, a, p);
+cudaError_t go_policy(const TokenArgs& a, const PolicyArgs& p, bool staged, cudaStream_t s) {
+    if (!staged)
+        return launch_after(policy_rows<GT>, dim3(row_blocks(a.n, 2)), dim3(kRowThreads), 0, s, a,
+                            p);
+    const PreferenceArgs none{};
+    const PairTable t{};
+    return a.grad != nullptr ? go_staged<GT, Pass::kPolicy>(a, p, none, t, 0, a.n, s)
+                             : go_staged<GT, Pass::kPolicyForward>(a, p, none, t, 0, a.n, s);
 }
 template <int GT>
-cudaError_t go_pref(const TokenArgs& a, const PreferenceArgs& p, const PairTable& t, bool back,
-                    cudaStream_t s) {
-    const dim3 grid(row_blocks(t.start[2 * t.pairs] - t.start[0]));
-    return back ? launch_after(preference_backward<GT>, grid, dim3(kRowThreads), 0, s, a, p, t)
-                : launch_after(preference_forward<GT>, grid, dim3(kRowThreads), 0, s, a, p, t);
+cudaError_t go_forward(const TokenArgs& a, const PreferenceArgs& p, const PairTable& t,
+                       bool staged, cudaStream_t s) {
+    const int64_t begin = t.start[0], end = t.start[2 * t.pairs];
+    if (staged)
+        return go_staged<GT, Pass::kPreferenceForward>(a, PolicyArgs{}, p, t, begin, end, s);
+    return launch_after(preference_forward<GT>, dim3(row_blocks(end - begin, 2)),
+                        dim3(kRowThreads), 0, s, a, p, t);
 }
-cudaError_t pref(const TokenArgs& a, const PreferenceArgs& p, const PairTable& t, int dtype,
-                 bool back, cudaStream_t s) {
-    const cudaError_t e = dtype == kGradF32   ? go_pref<kGradF32>(a, p, t, back, s)
-                          : dtype == kGradF16 ? go_pref<kGradF16>(a, p, t, back, s)
-                                              : go_pref<kGradBF16>(a, p, t, back, s);
-    note_launch();
-    return e;
+template <int GT>
+cudaError_t go_backward(const TokenArgs& a, const PreferenceArgs& p, const PairTable& t,
+                        bool staged, cudaStream_t s) {
+    const int64_t begin = t.start[0], end = t.start[2 * t.pairs];
+    if (staged)
+        return go_staged<GT, Pass::kPreferenceBackward>(a, PolicyArgs{}, p, PairTable{}, begin,
+                                                        end, s);
+    return launch_after(preference_backward<GT>, dim3(row_blocks(end - begin, 2)),
+                        dim3(kRowThreads), 0, s, a, p, begin, end);
 }
 
 }  // namespace
 
-cudaError_t launch_policy_loss(const TokenArgs& a, const PolicyArgs& p, int dtype,
+bool loss_row_fits(int64_t v, int dtype) {
+    return v * (dtype == kGradF32 ? 4 : 2) <= static_cast<int64_t>(kSlots) * kChunk;
+}
+
+cudaError_t read_loss_status(unsigned int* status, bool clear) {
+    cudaError_t e = cudaMemcpyFromSymbol(status, g_loss_status, sizeof(unsigned int));
+    if (e != cudaSuccess || !clear) return e;
+    const unsigned int zero = 0;
+    return cudaMemcpyToSymbol(g_loss_status, &zero, sizeof(unsigned int));
+}
+
+cudaError_t launch_policy_loss(const TokenArgs& a, const PolicyArgs& p, int dtype, bool staged,
                                cudaStream_t stream) {
-    const cudaError_t e = dtype == kGradF32   ? go_policy<kGradF32>(a, p, stream)
-                          : dtype == kGradF16 ? go_policy<kGradF16>(a, p, stream)
-                                              : go_policy<kGradBF16>(a, p, stream);
+    const cudaError_t e = dtype == kGradF32   ? go_policy<kGradF32>(a, p, staged, stream)
+                          : dtype == kGradF16 ? go_policy<kGradF16>(a, p, staged, stream)
+                                              : go_policy<kGradBF16>(a, p, staged, stream);
     note_launch();
     return e;
 }
 cudaError_t launch_preference_forward(const TokenArgs& a, const PreferenceArgs& p,
-                                      const PairTable& t, int dtype, cudaStream_t stream) {
-    return pref(a, p, t, dtype, false, stream);
+                                      const PairTable& t, int dtype, bool staged,
+                                      cudaStream_t stream) {
+    const cudaError_t e = dtype == kGradF32   ? go_forward<kGradF32>(a, p, t, staged, stream)
+                          : dtype == kGradF16 ? go_forward<kGradF16>(a, p, t, staged, stream)
+                                              : go_forward<kGradBF16>(a, p, t, staged, stream);
+    note_launch();
+    return e;
 }
 cudaError_t launch_preference_backward(const TokenArgs& a, const PreferenceArgs& p,
-                                       const PairTable& t, int dtype, cudaStream_t stream) {
-    return pref(a, p, t, dtype, true, stream);
+                                       const PairTable& t, int dtype, bool staged,
+                                       cudaStream_t stream) {
+    const cudaError_t e = dtype == kGradF32   ? go_backward<kGradF32>(a, p, t, staged, stream)
+                          : dtype == kGradF16 ? go_backward<kGradF16>(a, p, t, staged, stream)
+                                              : go_backward<kGradBF16>(a, p, t, staged, stream);
+    note_launch();
+    return e;
 }
 
 }  // namespace shardstep

@@ -285,7 +285,19 @@ int norm_some(const void* const* grads, const int64_t* numels, int32_t n, int32_
 
 // ---------------------------------------------------- losses over tokens
 
-int64_t loss_words(int64_t n_tokens, int64_t n_pairs) { return 3 * n_tokens + 2 * n_pairs; }
+int64_t loss_words(int64_t n_tokens, int64_t n_pairs) { return 4 * n_tokens + 2 * n_pairs; }
+
+// Whether the rows of logits and gradient take the staged kernels: they fit
+// shared memory, and every gradient row lies as far past a 16-byte boundary as
+// its logits row, so that a row's staged bytes can be stored back in bulk.
+bool staged_rows(const shardstep_token_loss_t* a, bool backward) {
+    if (!loss_row_fits(a->vocab, a->dtype)) return false;
+    if (!backward) return true;
+    const uintptr_t off = reinterpret_cast<uintptr_t>(a->grad) -
+                          reinterpret_cast<uintptr_t>(a->logits);
+    const int64_t step = (a->grad_stride - a->row_stride) * elem_size(a->dtype);
+    return off % 16 == 0 && step % 16 == 0;
+}
 
 // The checks both losses share; fills the kernel arguments.
 int take_tokens(const shardstep_token_loss_t* a, int64_t need, TokenArgs* k,
@@ -461,10 +473,13 @@ int token_policy_loss(const shardstep_token_loss_t* args, const float* old_logps
     add_range(reads, advantages, args->n_tokens * 4);
     if (int rc = check_ranges(&reads, &writes); rc != SHARDSTEP_OK) return rc;
     const PolicyArgs p{old_logps, advantages, 1.0f - clip_low, 1.0f + clip_high, kl_coef};
-    const cudaError_t e = launch_policy_loss(k, p, args->dtype, static_cast<cudaStream_t>(stream));
+    const bool staged = staged_rows(args, k.grad != nullptr);
+    const cudaError_t e =
+        launch_policy_loss(k, p, args->dtype, staged, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess)
         return ready_fail(SHARDSTEP_ERR_CUDA, "policy loss launch: %s", cudaGetErrorString(e));
-    record_kernel("policy_rows<%s>", dtype_name(args->dtype));
+    record_kernel(staged ? "policy_staged<%s> (TMA-staged)" : "policy_rows<%s>",
+                  dtype_name(args->dtype));
     return ready_ok();
 } catch (const std::bad_alloc&) {
     return ready_fail(SHARDSTEP_ERR_CAPACITY, "out of host memory");
@@ -503,8 +518,18 @@ int token_preference_loss(const shardstep_token_loss_t* args, const int64_t* seq
     if (int rc = check_ranges(&reads, &writes); rc != SHARDSTEP_OK) return rc;
     if (k.norm == 0.0f) k.norm = static_cast<float>(n_pairs);
     float* words = reinterpret_cast<float*>(k.ws + 1);
-    PreferenceArgs p{beta,  label_smoothing,    log_ratios,         words,
-                     words + tokens, words + 2 * tokens, words + 3 * tokens, 1, 0};
+    PreferenceArgs p{beta,
+                     label_smoothing,
+                     log_ratios,
+                     words,
+                     words + tokens,
+                     words + 2 * tokens,
+                     reinterpret_cast<int32_t*>(words + 3 * tokens),
+                     words + 4 * tokens,
+                     1,
+                     0};
+    const bool staged = staged_rows(args, false);
+    const bool staged_back = staged_rows(args, true);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     std::unique_ptr<PairTable> t(new PairTable);
     int32_t row = 0;
@@ -516,9 +541,9 @@ int token_preference_loss(const shardstep_token_loss_t* args, const int64_t* seq
         }
         t->start[2 * t->pairs] = row;
         p.last = q + t->pairs >= n_pairs;
-        cudaError_t e = launch_preference_forward(k, p, *t, args->dtype, s);
+        cudaError_t e = launch_preference_forward(k, p, *t, args->dtype, staged, s);
         if (e == cudaSuccess && k.grad != nullptr)
-            e = launch_preference_backward(k, p, *t, args->dtype, s);
+            e = launch_preference_backward(k, p, *t, args->dtype, staged_back, s);
         if (e != cudaSuccess)
             return ready_fail(SHARDSTEP_ERR_CUDA, "preference loss launch: %s",
                               cudaGetErrorString(e));
@@ -526,7 +551,10 @@ int token_preference_loss(const shardstep_token_loss_t* args, const int64_t* seq
         p.log_ratios += 2 * static_cast<int64_t>(t->pairs);
         p.coef += 2 * static_cast<int64_t>(t->pairs);
     }
-    record_kernel(k.grad ? "preference_backward<%s>" : "preference_forward<%s>",
+    record_kernel(k.grad ? (staged_back ? "preference_staged_backward<%s> (TMA-staged)"
+                                        : "preference_backward<%s>")
+                         : (staged ? "preference_staged_forward<%s> (TMA-staged)"
+                                   : "preference_forward<%s>"),
                   dtype_name(args->dtype));
     return ready_ok();
 } catch (const std::bad_alloc&) {
