@@ -386,11 +386,9 @@ bool loss_row_fits(int64_t v, int dtype);
 cudaError_t launch_policy_loss(const TokenArgs& a, const PolicyArgs& p, int dtype, bool staged,
                                cudaStream_t stream);
 cudaError_t launch_preference_forward(const TokenArgs& a, const PreferenceArgs& p,
-                                      const PairTable& t, int dtype, bool staged,
-                                      cudaStream_t stream);
-cudaError_t launch_preference_backward(const TokenArgs& a, const PreferenceArgs& p,
-                                       const PairTable& t, int dtype, bool staged,
-                                      cudaStream_t stream);
+                                      const PairTable& t, int dtype, cudaStream_t stream);
+cudaError_t launch_preference_backward(const TokenArgs& a, const PreferenceArgs& p, int64_t begin,
+                                       int64_t end, int dtype, bool staged, cudaStream_t stream);
 
 // Host helpers of api.cpp for the other translation units: the last error of
 // the calling thread, the name shardstep_last_kernel reports, the per-step

@@ -20,6 +20,8 @@
 // least there is, and the kernel is bound by that traffic.  A row that does
 // not fit (or whose gradient lies at another offset from a 16-byte boundary)
 // takes the plain kernels, which read it again for the gradient (from L2).
+#include <atomic>
+
 #include "common.cuh"
 #include "tma.cuh"
 
@@ -80,10 +82,14 @@ struct Team {
     TeamShared<T>* sh;
 
     __device__ __forceinline__ void sync() const {
-        asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(T) : "memory");
+        if (T == 32)
+            __syncwarp();
+        else
+            asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(T) : "memory");
     }
     // The same, true for all where any thread passes true.
     __device__ __forceinline__ bool sync_or(bool any) const {
+        if (T == 32) return __any_sync(kFull, any);
         int r;
         asm volatile(
             "{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n bar.red.or.pred q, %2, %3, p;\n"
@@ -99,6 +105,10 @@ struct Team {
     __device__ __forceinline__ float sum(float x, bool* any, int turn) const {
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) x = __fadd_rn(x, __shfl_xor_sync(kFull, x, d));
+        if (T == 32) {
+            *any = __any_sync(kFull, *any);
+            return x;
+        }
         if ((tid & 31) == 0) sh->part[turn][tid >> 5] = x;
         *any = sync_or(*any);
         x = sh->part[turn][tid & (T / 32 - 1)];
@@ -314,21 +324,30 @@ __device__ __forceinline__ void finish_pair(const TokenArgs& a, const Preference
     a.ws->pair_loss[q][2] = h > 0.0f ? 1.0 : 0.0;
 }
 
-// `rows` more rows of pair q are done, their terms written by this warp's lane
-// 0: the warp that brings the pair's count to its rows finishes the pair.
+// Each lane has written the words of one more row of its pair q (-1: none): the
+// warp that brings a pair's count to its rows finishes the pair.
 __device__ __forceinline__ void rows_done(const TokenArgs& a, const PreferenceArgs& p,
-                                          const PairTable& t, int q, unsigned rows) {
-    unsigned before = 0;
-    if ((threadIdx.x & 31) == 0)
+                                          const PairTable& t, int q) {
+    // lanes of one pair count as one, by the pair's lowest lane
+    const unsigned same = __match_any_sync(kFull, q);
+    const bool leads = q >= 0 && __ffs(same) - 1 == static_cast<int>(threadIdx.x & 31);
+    bool last = false;
+    __syncwarp();
+    if (leads) {
+        unsigned before;
+        const unsigned rows = __popc(same);
+        __threadfence();
         asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;"
                      : "=r"(before)
                      : "l"(&a.ws->rows_done[q]), "r"(rows)
                      : "memory");
-    before = __shfl_sync(kFull, before, 0);
-    __syncwarp();
-    if (before + rows != static_cast<unsigned>(t.start[2 * q + 2] - t.start[2 * q])) return;
-    if ((threadIdx.x & 31) == 0) a.ws->rows_done[q] = 0;
-    finish_pair(a, p, t, q);
+        last = before + rows == static_cast<unsigned>(t.start[2 * q + 2] - t.start[2 * q]);
+        if (last) a.ws->rows_done[q] = 0;
+    }
+    for (unsigned done = __ballot_sync(kFull, last); done != 0; done &= done - 1) {
+        __syncwarp();
+        finish_pair(a, p, t, __shfl_sync(kFull, q, __ffs(done) - 1));
+    }
 }
 
 // Pairs without a token, which no row finishes.
@@ -425,7 +444,7 @@ __global__ void __launch_bounds__(kRowThreads)
         const float w = token_weight(a, i);
         if (w == 0.0f) {   // not read at all: whatever it holds takes no part
             if (threadIdx.x == 0) a.logps[i] = 0.0f;
-            if (a.grad != nullptr) plain_zero<GT>(g, a.v);
+            plain_zero<GT>(g, a.v);
             continue;
         }
         const int64_t y = token_id(a, i);
@@ -440,44 +459,10 @@ __global__ void __launch_bounds__(kRowThreads)
             a.logps[i] = lp;
             add_policy(sums, t, p, k);
         }
-        if (a.grad != nullptr)
-            plain_grad<GT>(x, g, a.v, y, r, s, __fmul_rn(__fmul_rn(t.slope, k), scale));
+        plain_grad<GT>(x, g, a.v, y, r, s, __fmul_rn(__fmul_rn(t.slope, k), scale));
     }
     if (join_blocks(a.ws, sums) && threadIdx.x < 4)
         a.stats[threadIdx.x] = __double2float_rn(a.ws->total[threadIdx.x]);
-}
-
-template <int GT>
-__global__ void __launch_bounds__(kRowThreads)
-    preference_forward(const TokenArgs a, const PreferenceArgs p,
-                       const __grid_constant__ PairTable t) {
-    __shared__ TeamShared<kRowThreads> sh;
-    const Team<kRowThreads> team{1, static_cast<int>(threadIdx.x), &sh};
-    pdl_enter();
-    if (threadIdx.x < 32) empty_pairs(a, p, t);
-    const int64_t end = t.start[2 * t.pairs];
-    for (int64_t i = t.start[0] + static_cast<int64_t>(blockIdx.x); i < end; i += gridDim.x) {
-        const float w = token_weight(a, i);
-        const int seq = find_sequence(t, i);
-        float lp = 0.0f, term = 0.0f;
-        if (w != 0.0f) {
-            const char* x = row_of<GT>(a.x, i, a.x_stride);
-            const int64_t y = token_id(a, i);
-            const float xy = y >= 0 ? load1<GT>(x, y) : NAN;
-            RowRef r;
-            const float s = plain_sum<GT>(x, a.v, xy, &r, team);
-            lp = row_logp(xy, r, s);
-            term = __fmul_rn(w, __fsub_rn(lp, a.ref[i]));
-            if (threadIdx.x == 0) save_row(p, i, r, s);
-        }
-        if (threadIdx.x == 0) {
-            a.logps[i] = lp;
-            p.term[i] = term;
-            p.seq[i] = seq;
-        }
-        if (threadIdx.x < 32) rows_done(a, p, t, seq >> 1, 1);
-    }
-    preference_stats(a, p, t);
 }
 
 template <int GT>
@@ -506,11 +491,7 @@ constexpr int kSlots = 13;                    // slots of the ring: 208 KB
 constexpr int kZeroBytes = 4096;
 constexpr size_t kStagedSmem = static_cast<size_t>(kSlots) * kChunk + kZeroBytes;
 
-enum class Pass { kPolicy, kPolicyForward, kPreferenceForward, kPreferenceBackward };
-constexpr __host__ __device__ bool has_sum(Pass m) { return m != Pass::kPreferenceBackward; }
-constexpr __host__ __device__ bool has_grad(Pass m) {
-    return m == Pass::kPolicy || m == Pass::kPreferenceBackward;
-}
+enum class Pass { kPolicy, kPreferenceBackward };
 
 // A row's bytes: `head` elements up to the first 16-byte boundary, `body` bytes
 // in whole 16-byte vectors from there, `tail` elements after them (a row
@@ -642,17 +623,30 @@ __device__ __forceinline__ uint4 grad_vector_slow(const uint4& u, RowRef r, Pair
     return pack_vector<GT>(o);
 }
 
-// The ring's position: the slot of the next chunk and its barriers' parity.
+__device__ __forceinline__ void st_release(unsigned* p, unsigned x) {
+    asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(smem_addr(p)), "r"(x) : "memory");
+}
+__device__ __forceinline__ unsigned ld_acquire(const unsigned* p) {
+    unsigned x;
+    asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(x) : "r"(smem_addr(p)) : "memory");
+    return x;
+}
+
+// The ring's position: the slot of the next chunk, its barriers' parity and the
+// chunk's number since the start.
 struct Ring {
     int slot;
     uint32_t parity;
+    unsigned chunk;
     __device__ __forceinline__ void next() {
+        ++chunk;
         if (++slot == kSlots) {
             slot = 0;
             parity ^= 1u;
         }
     }
     __device__ __forceinline__ void skip(uint32_t chunks) {   // at most kSlots
+        chunk += chunks;
         slot += static_cast<int>(chunks);
         if (slot >= kSlots) {
             slot -= kSlots;
@@ -665,16 +659,46 @@ struct Ring {
 struct RowParam {
     float w;        // 0: the row takes no part
     int32_t y;      // the id, -1 outside the vocabulary
-    float xy;       // its logit (forward passes)
-    float f[3];     // policy: old, advantage, ref; preference forward: ref;
+    float xy;       // its logit (policy)
+    float f[3];     // policy: old, advantage, ref;
                     // backward: c, the reference and the sum of the exponentials
 };
-// A finished row of the preference loss's forward pass.
-struct RowResult {
-    float logp, term, ref, sum;
-};
 constexpr int kBatch = 32;            // rows whose parameters are fetched at once
-constexpr int kResults = 4;
+
+// The parameters of row i, whose id's logit is wanted where `logit` is set; the
+// caller's lanes take a row each, so the dependent loads of 32 rows overlap.
+template <int GT>
+__device__ __forceinline__ RowParam policy_param(const TokenArgs& a, const PolicyArgs& pol,
+                                                 int64_t i) {
+    RowParam q{token_weight(a, i), -1, 0.0f, {pol.old[i], pol.adv[i], 0.0f}};
+    if (pol.kl != 0.0f) q.f[2] = a.ref[i];
+    if (q.w != 0.0f) {
+        const int64_t y = token_id(a, i);
+        q.y = static_cast<int32_t>(y);
+        q.xy = y >= 0 ? load1<GT>(row_of<GT>(a.x, i, a.x_stride), y) : NAN;
+    }
+    return q;
+}
+
+// Until chunk r.chunk has landed.  A team skips the other team's rows, so it may
+// ask for a slot whose earlier copy is still on its way: a parity alone would
+// then say yes to the copy before that.  It first waits for its own chunk to be
+// issued, which the slot's earlier use has to be over for; from there on the
+// parity is that of its chunk.  `seen`: the issued count this thread last read.
+__device__ __forceinline__ bool wait_chunk(uint64_t* full, const unsigned* issued, unsigned* seen,
+                                           const Ring& r, unsigned long long limit_ns) {
+    if (static_cast<int>(*seen - r.chunk) <= 0) {
+        *seen = ld_acquire(issued);
+        if (static_cast<int>(*seen - r.chunk) <= 0) {
+            const unsigned long long t0 = now_ns();
+            do {
+                if (now_ns() - t0 > limit_ns) return false;
+                *seen = ld_acquire(issued);
+            } while (static_cast<int>(*seen - r.chunk) <= 0);
+        }
+    }
+    return mbar_wait(&full[r.slot], r.parity, limit_ns);
+}
 
 // One block per SM takes rows blockIdx.x, + gridDim.x, ... of the launch.
 //   2 teams of 8 computing warps, live rows in turn: sum a row's chunks as they
@@ -684,13 +708,10 @@ constexpr int kResults = 4;
 //     forms its terms the other has the arithmetic units;
 //   loading warp: per live row, its body's chunks into free slots;
 //   storing warp: stores each finished chunk and frees its slot; rows of weight
-//     0 are stored from a zeroed piece of shared memory.  In the preference
-//     loss's forward pass, which stores no rows, it writes the rows' words,
-//     counts their pairs' rows and finishes pairs, off the computing warps' path;
+//     0 are stored from a zeroed piece of shared memory;
 //   parameter warp: the rows' weights, ids, logits of the ids and so on, 32
-//     rows ahead at a time: fetched row by row, these dependent loads took 3 of
-//     the 6.5 us that a row of 32000 bf16 logits used to take.
-// Without a gradient the computing warps free the slots themselves.  Every wait
+//     rows ahead at a time.
+// Every wait
 // is bounded: one that runs out sets a status bit, the block leaves at the end
 // of the row, and its copies in flight are waited for first.
 constexpr int kTeams = 2;
@@ -698,44 +719,37 @@ constexpr int kTeamThreads = 256, kTeamWarps = kTeamThreads / 32;
 constexpr int kWorkWarps = kTeams * kTeamWarps;
 constexpr int kLoadWarp = kWorkWarps, kStoreWarp = kWorkWarps + 1, kParamWarp = kWorkWarps + 2;
 constexpr int kStagedThreads = 32 * (kWorkWarps + 3);
-static_assert(kResults % kTeams == 0, "a team's rows keep to their result slots");
 
 template <int GT, Pass M>
 __global__ void __launch_bounds__(kStagedThreads, 1)
     staged_rows(const TokenArgs a, const PolicyArgs pol, const PreferenceArgs p,
-                const __grid_constant__ PairTable t, int64_t begin, int64_t end,
-                unsigned long long wait_ns) {
+                int64_t begin, int64_t end, unsigned long long wait_ns) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ TeamShared<kTeamThreads> sh[kTeams];
     __shared__ double team_sums[kTeams][4];
     __shared__ uint64_t full[kSlots], done[kSlots], empty[kSlots];
-    __shared__ uint64_t param_full[2], param_empty[2], result_full[kResults],
-        result_empty[kResults];
+    __shared__ unsigned issued_chunks;    // by the loading warp so far
+    __shared__ uint64_t param_full[2], param_empty[2];
     __shared__ RowParam params[2][kBatch];
-    __shared__ RowResult results[kResults];
     uint8_t* zeros = smem + static_cast<size_t>(kSlots) * kChunk;
     constexpr int es = elem_bytes<GT>();
-    constexpr bool kPref = M == Pass::kPreferenceForward;
+    constexpr bool kPolicy = M == Pass::kPolicy;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
+        issued_chunks = 0;
         for (int s = 0; s < kSlots; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&done[s], kTeamWarps);
-            mbar_init(&empty[s], has_grad(M) ? 1 : kTeamWarps);
+            mbar_init(&empty[s], 1);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&param_full[s], 1);
             mbar_init(&param_empty[s], kWorkWarps);
         }
-        for (int s = 0; s < kResults; ++s) {
-            mbar_init(&result_full[s], 1);
-            mbar_init(&result_empty[s], 1);
-        }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (has_grad(M))
-        for (int k = tid; k < kZeroBytes / 4; k += kStagedThreads)
-            reinterpret_cast<uint32_t*>(zeros)[k] = 0;
+    for (int k = tid; k < kZeroBytes / 4; k += kStagedThreads)
+        reinterpret_cast<uint32_t*>(zeros)[k] = 0;
     fence_async();
     __syncthreads();
     pdl_enter();
@@ -750,7 +764,7 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
     };
 
     if (warp == kLoadWarp) {
-        Ring r{0, 0};
+        Ring r{0, 0, 0};
         int64_t issued = 0;
         bool ok = true;
         unsigned next = live_mask(0);
@@ -773,6 +787,7 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
                                   &full[r.slot]);
                         r.next();
                         ++issued;
+                        st_release(&issued_chunks, static_cast<unsigned>(issued));
                     }
                 }
             }
@@ -782,7 +797,7 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
             if (!ok) atomicOr(&g_loss_status, kStatusProducerTimeout);
             // the last (at most kSlots) chunks land before the block may exit
             const int64_t skip = issued > kSlots ? issued - kSlots : 0;
-            Ring d{static_cast<int>(skip % kSlots), static_cast<uint32_t>(skip / kSlots) & 1u};
+            Ring d{static_cast<int>(skip % kSlots), static_cast<uint32_t>(skip / kSlots) & 1u, 0};
             bool drained = true;
             for (int64_t k = skip; k < issued; ++k) {
                 drained = mbar_wait(&full[d.slot], d.parity, kDrainNs) && drained;
@@ -790,8 +805,8 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
             }
             if (!drained) atomicOr(&g_loss_status, kStatusDrainTimeout);
         }
-    } else if (warp == kStoreWarp && has_grad(M)) {
-        Ring r{0, 0};
+    } else if (warp == kStoreWarp) {
+        Ring r{0, 0, 0};
         int held = -1;                // the slot of the newest store group, or none
         bool ok = true;
         unsigned next = live_mask(0);
@@ -838,79 +853,22 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
         }
         if (!ok && lane == 0) atomicOr(&g_loss_status, kStatusProducerTimeout);
         if (lane == 0) bulk_wait_all();
-    } else if (warp == kStoreWarp && kPref) {
-        // words of the rows, and the pairs that they complete
-        empty_pairs(a, p, t);
-        int64_t k = 0;                // live rows so far
-        int pair = -1;
-        unsigned count = 0;
-        bool ok = true;
-        unsigned next = live_mask(0);
-        for (int64_t j0 = 0; j0 < rows && ok; j0 += 32) {
-            const unsigned live = next;
-            next = live_mask(j0 + 32);
-            // lane l looks row j0 + l up
-            const int mine = j0 + lane < rows ? find_sequence(t, row_at(j0 + lane)) : 0;
-            for (int64_t j = j0; j < rows && j < j0 + 32; ++j) {
-                const int64_t i = row_at(j);
-                const int seq = __shfl_sync(kFull, mine, static_cast<int>(j - j0));
-                if (seq >> 1 != pair && count != 0) {
-                    rows_done(a, p, t, pair, count);
-                    count = 0;
-                }
-                pair = seq >> 1;
-                RowResult res{0.0f, 0.0f, 0.0f, 0.0f};
-                if ((live >> (j - j0)) & 1u) {
-                    const int s = static_cast<int>(k % kResults);
-                    ok = __all_sync(kFull, mbar_wait(&result_full[s],
-                                                     static_cast<uint32_t>(k / kResults) & 1u,
-                                                     wait_ns));
-                    if (!ok) break;
-                    res = results[s];
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&result_empty[s]);
-                    ++k;
-                }
-                if (lane == 0) {
-                    a.logps[i] = res.logp;
-                    p.term[i] = res.term;
-                    p.row_ref[i] = res.ref;
-                    p.row_sum[i] = res.sum;
-                    p.seq[i] = seq;
-                }
-                ++count;
-            }
-        }
-        if (ok && count != 0) rows_done(a, p, t, pair, count);
-        if (!ok && lane == 0) atomicOr(&g_loss_status, kStatusConsumerTimeout);
     } else if (warp == kParamWarp) {
-        const float scale = M == Pass::kPreferenceBackward ? out_scale(a) : 0.0f;
+        const float scale = kPolicy ? 0.0f : out_scale(a);
         bool ok = true;
         for (int64_t j = 0, n = 0; j < rows && ok; j += kBatch, ++n) {
             const int buf = static_cast<int>(n & 1);
             RowParam q{0.0f, -1, 0.0f, {0.0f, 0.0f, 0.0f}};
             if (j + lane < rows) {
                 const int64_t i = row_at(j + lane);
-                q.w = token_weight(a, i);
-                if (M == Pass::kPolicy || M == Pass::kPolicyForward) {
-                    q.f[0] = pol.old[i];
-                    q.f[1] = pol.adv[i];
-                    if (pol.kl != 0.0f) q.f[2] = a.ref[i];
-                } else if (kPref) {
-                    q.f[0] = a.ref[i];
-                }
-                if (q.w != 0.0f) {
-                    const int64_t y = token_id(a, i);
-                    q.y = static_cast<int32_t>(y);
-                    if (has_sum(M)) {
-                        q.xy = y >= 0 ? load1<GT>(row_of<GT>(a.x, i, a.x_stride), y) : NAN;
-                    } else {
-                        q.f[0] = __fmul_rn(__fmul_rn(p.coef[p.seq[i]], q.w), scale);
-                        q.f[1] = p.row_ref[i];
-                        q.f[2] = p.row_sum[i];
-                    }
-                } else if (has_sum(M) && !kPref) {
-                    a.logps[i] = 0.0f;
+                if (kPolicy) {
+                    q = policy_param<GT>(a, pol, i);
+                    if (q.w == 0.0f) a.logps[i] = 0.0f;
+                } else if ((q.w = token_weight(a, i)) != 0.0f) {
+                    q.y = static_cast<int32_t>(token_id(a, i));
+                    q.f[0] = __fmul_rn(__fmul_rn(p.coef[p.seq[i]], q.w), scale);
+                    q.f[1] = p.row_ref[i];
+                    q.f[2] = p.row_sum[i];
                 }
             }
             if (n >= 2)
@@ -926,13 +884,13 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
     } else if (warp < kWorkWarps) {
         const int which = warp / kTeamWarps;
         const Team<kTeamThreads> team{1 + which, tid - which * kTeamThreads, &sh[which]};
-        float norm = 0.0f;
-        if (M == Pass::kPolicy || M == Pass::kPolicyForward) norm = weight_sum(a, team);
-        const float scale = M == Pass::kPolicy ? out_scale(a) : 0.0f;
-        Ring ring{0, 0};
-        // a wait that ran out: `bad` is made the same for the whole team at a
-        // barrier before any of it leaves; `late` is its first thread's until then
-        bool bad = false, late = false;
+        const float norm = kPolicy ? weight_sum(a, team) : 1.0f;
+        const float scale = kPolicy ? out_scale(a) : 0.0f;
+        Ring ring{0, 0, 0};
+        unsigned seen = 0;
+        // a wait that ran out, made the same for the whole team at a barrier before
+        // any of it leaves
+        bool bad = false;
         int turn = 0;
         int64_t live = 0;
         for (int64_t j = 0; j < rows && !bad; ++j) {
@@ -965,13 +923,13 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
             const float xe = edge >= 0 ? load1<GT>(x, edge) : 0.0f;
             RowRef r;
             float s, c;
-            if (has_sum(M)) {
+            if (kPolicy) {
                 r = fast_ref(q.xy);
                 const FastRow fr = fast_row(r);
                 Pair acc[2] = {0, 0};
                 Ring at_ring = ring;
                 for (uint32_t o = 0; o < b.body; o += kChunk) {
-                    bad = bad || !mbar_wait(&full[at_ring.slot], at_ring.parity, wait_ns);
+                    bad = bad || !wait_chunk(full, &issued_chunks, &seen, at_ring, wait_ns);
                     const uint32_t n = b.body - o < kChunk ? b.body - o : kChunk;
                     const uint8_t* in = smem + static_cast<size_t>(at_ring.slot) * kChunk;
                     if (r.fast && !bad) {
@@ -982,17 +940,11 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
                                 sum_vector<GT>(*reinterpret_cast<const uint4*>(in + at), fr, acc);
                         }
                     }
-                    if (!has_grad(M)) {
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&empty[at_ring.slot]);
-                    }
                     at_ring.next();
                 }
-                if (!has_grad(M)) ring = at_ring;
                 const float2 total = floats(add2(acc[0], acc[1]));
                 s = __fadd_rn(total.x, total.y);
                 if (edge >= 0 && r.fast) s = __fadd_rn(s, row_exp(xe, r));
-                bad = bad || late;
                 s = team.sum(s, &bad, turn);
                 turn ^= 1;
                 if (bad) break;
@@ -1001,82 +953,65 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
                     r = sr.r;
                     s = sr.sum;
                 }
-                if (kPref) {
-                    if (team.tid == 0) {
-                        const int slot = static_cast<int>(row % kResults);
-                        late = row >= kResults &&
-                               !mbar_wait(&result_empty[slot],
-                                          (static_cast<uint32_t>(row / kResults) & 1u) ^ 1u,
-                                          wait_ns);
-                        const float lp = row_logp(q.xy, r, s);
-                        results[slot] = RowResult{lp, __fmul_rn(q.w, __fsub_rn(lp, q.f[0])),
-                                                  r.ref, r.fast ? s : -s};
-                        mbar_arrive(&result_full[slot]);
-                    }
-                } else {
-                    const float lp = row_logp(q.xy, r, s);
-                    const PolicyTerms pt = policy_terms(lp, q.f[0], q.f[1], q.f[2], pol);
-                    const float k = __fdiv_rn(q.w, norm);
-                    c = __fmul_rn(__fmul_rn(pt.slope, k), scale);
-                    if (team.tid == 0) {
-                        a.logps[i] = lp;
-                        add_policy(sums, pt, pol, k);
-                    }
+                const float lp = row_logp(q.xy, r, s);
+                const PolicyTerms pt = policy_terms(lp, q.f[0], q.f[1], q.f[2], pol);
+                const float k = __fdiv_rn(q.w, norm);
+                c = __fmul_rn(__fmul_rn(pt.slope, k), scale);
+                if (team.tid == 0) {
+                    a.logps[i] = lp;
+                    add_policy(sums, pt, pol, k);
                 }
             } else {
                 c = q.f[0];
                 s = fabsf(q.f[2]);
                 r = RowRef{q.f[1], !(q.f[2] < 0.0f)};
             }
-            if (has_grad(M)) {
-                const float cs = __fdiv_rn(c, s);
-                char* g = const_cast<char*>(row_of<GT>(a.grad, i, a.g_stride));
-                // the id's place among the vectors of the body, in bytes
-                const int64_t yb = q.y < b.head ? -1 : static_cast<int64_t>(q.y - b.head) * es;
-                const FastRow fr = fast_row(r);
-                const Pair f = make_pair(-cs, -cs);
-                for (uint32_t o = 0; o < b.body; o += kChunk) {
-                    if (!has_sum(M))
-                        bad = bad || !mbar_wait(&full[ring.slot], ring.parity, wait_ns);
-                    const uint32_t n = b.body - o < kChunk ? b.body - o : kChunk;
-                    uint8_t* io = smem + static_cast<size_t>(ring.slot) * kChunk;
-                    // the id's element, if it is in this chunk: its vector's thread
-                    // takes the logit before and writes the gradient after the vector
-                    const int64_t in = yb - o;
-                    const bool own = in >= 0 && in < n && in / 16 % kTeamThreads == team.tid;
-                    const float xv = own && !bad ? load1<GT>(io, in / es) : 0.0f;
-                    if (r.fast && !bad) {
+            const float cs = __fdiv_rn(c, s);
+            char* g = const_cast<char*>(row_of<GT>(a.grad, i, a.g_stride));
+            // the id's place among the vectors of the body, in bytes
+            const int64_t yb = q.y < b.head ? -1 : static_cast<int64_t>(q.y - b.head) * es;
+            const FastRow fr = fast_row(r);
+            const Pair f = make_pair(-cs, -cs);
+            for (uint32_t o = 0; o < b.body; o += kChunk) {
+                if (!kPolicy)
+                    bad = bad || !wait_chunk(full, &issued_chunks, &seen, ring, wait_ns);
+                const uint32_t n = b.body - o < kChunk ? b.body - o : kChunk;
+                uint8_t* io = smem + static_cast<size_t>(ring.slot) * kChunk;
+                // the id's element, if it is in this chunk: its vector's thread
+                // takes the logit before and writes the gradient after the vector
+                const int64_t in = yb - o;
+                const bool own = in >= 0 && in < n && in / 16 % kTeamThreads == team.tid;
+                const float xv = own && !bad ? load1<GT>(io, in / es) : 0.0f;
+                if (r.fast && !bad) {
 #pragma unroll
-                        for (int k = 0; k < kChunk / (16 * kTeamThreads); ++k) {
-                            const uint32_t at = 16 * (k * kTeamThreads + team.tid);
-                            uint4* v4 = reinterpret_cast<uint4*>(io + at);
-                            if (at < n) *v4 = grad_vector<GT>(*v4, fr, f);
-                        }
-                    } else if (!bad) {
-                        for (uint32_t at = 16 * team.tid; at < n; at += 16 * kTeamThreads) {
-                            uint4* v4 = reinterpret_cast<uint4*>(io + at);
-                            *v4 = grad_vector_slow<GT>(*v4, r, f);
-                        }
+                    for (int k = 0; k < kChunk / (16 * kTeamThreads); ++k) {
+                        const uint32_t at = 16 * (k * kTeamThreads + team.tid);
+                        uint4* v4 = reinterpret_cast<uint4*>(io + at);
+                        if (at < n) *v4 = grad_vector<GT>(*v4, fr, f);
                     }
-                    if (own && !bad) store1<GT>(io, in / es, own_grad(row_exp(xv, r), s, cs));
-                    fence_async();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&done[ring.slot]);
-                    ring.next();
+                } else if (!bad) {
+                    for (uint32_t at = 16 * team.tid; at < n; at += 16 * kTeamThreads) {
+                        uint4* v4 = reinterpret_cast<uint4*>(io + at);
+                        *v4 = grad_vector_slow<GT>(*v4, r, f);
+                    }
                 }
-                if (edge >= 0) {
-                    const float e = row_exp(xe, r);
-                    store1<GT>(g, edge, edge == q.y ? own_grad(e, s, cs) : -__fmul_rn(e, cs));
-                }
-                if (!has_sum(M)) bad = team.sync_or(bad);
+                if (own && !bad) store1<GT>(io, in / es, own_grad(row_exp(xv, r), s, cs));
+                fence_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&done[ring.slot]);
+                ring.next();
             }
+            if (edge >= 0) {
+                const float e = row_exp(xe, r);
+                store1<GT>(g, edge, edge == q.y ? own_grad(e, s, cs) : -__fmul_rn(e, cs));
+            }
+            if (!kPolicy) bad = team.sync_or(bad);
         }
-        if ((bad || late) && team.tid == 0) atomicOr(&g_loss_status, kStatusConsumerTimeout);
+        if (bad && team.tid == 0) atomicOr(&g_loss_status, kStatusConsumerTimeout);
         if (team.tid == 0)
             for (int k = 0; k < 4; ++k) team_sums[which][k] = sums[k];
     }
-    if (kPref) preference_stats(a, p, t);
-    if (M == Pass::kPolicy || M == Pass::kPolicyForward) {
+    if (kPolicy) {
         __syncthreads();
         if (tid == 0)
             for (int w = 1; w < kTeams; ++w)
@@ -1085,56 +1020,301 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
     }
 }
 
+// ------------------------------------------------ the streaming forward pass
+
+// A forward pass needs a row's sum alone, so no row has to stay: each of a
+// block's 16 warps streams its own part of its team's row through three 4 KB
+// slots of its own, lane 0 starting the next copy as soon as a slot has been
+// summed.  Nothing is shared on the way; a team of W warps joins its sums once a
+// row, and what follows from a row's sum is formed for 32 rows at once, a row
+// per lane.  W = 16 where rows are few, so that a row's copies spread over the
+// SM's warps, else 4.  Bound by the one read of the logits.
+constexpr int kStreamWarps = 16, kStreamThreads = 32 * kStreamWarps;
+constexpr int kStreamSlots = 3, kStreamChunk = 4096;
+constexpr size_t kStreamSmem = static_cast<size_t>(kStreamWarps) * kStreamSlots * kStreamChunk;
+
+// The chunks of a warp's parts of its team's live rows, in order.
+struct Parts {
+    const char* at;      // the current row's part
+    uint32_t len, off;   // its bytes; those already taken
+    int64_t batch;       // first row of the batch that `mask` speaks of
+    unsigned mask, next; // live rows of the batch not yet taken; of the next batch
+};
+
+template <int GT, int W, bool PREF>
+__global__ void __launch_bounds__(kStreamThreads, 1)
+    stream_forward(const TokenArgs a, const PolicyArgs pol, const PreferenceArgs p,
+                   const __grid_constant__ PairTable t, int64_t begin, int64_t end,
+                   unsigned long long wait_ns) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    constexpr int kRowTeams = kStreamWarps / W;
+    __shared__ TeamShared<32 * W> sh[kRowTeams];
+    __shared__ TeamShared<kStreamThreads> block_sh;
+    __shared__ double team_sums[kRowTeams][4];
+    __shared__ uint64_t full[kStreamWarps][kStreamSlots];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int which = warp / W, part = warp % W;
+    const Team<32 * W> team{1 + which, tid - which * 32 * W, &sh[which]};
+    uint8_t* slots = smem + static_cast<size_t>(warp) * kStreamSlots * kStreamChunk;
+    if (lane == 0) {
+        for (int s = 0; s < kStreamSlots; ++s) mbar_init(&full[warp][s], 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    pdl_enter();
+    const int64_t teams = static_cast<int64_t>(gridDim.x) * kRowTeams;
+    const int64_t first = begin + static_cast<int64_t>(blockIdx.x) * kRowTeams + which;
+    const int64_t rows = first < end ? (end - first + teams - 1) / teams : 0;
+    const auto row_at = [&](int64_t j) { return first + j * teams; };
+    const auto live_mask = [&](int64_t j) {
+        const bool live = j + lane < rows && token_weight(a, row_at(j + lane)) != 0.0f;
+        return __ballot_sync(kFull, live);
+    };
+    // this warp's part of a row's body: whole vectors, contiguous
+    const auto part_of = [&](const RowBytes& b, const char** at) {
+        const uint32_t each = (b.body / 16 + W - 1) / W * 16;
+        const uint32_t lo = part * each < b.body ? part * each : b.body;
+        *at = b.body_at + lo;
+        return b.body - lo < each ? b.body - lo : each;
+    };
+
+    Parts c{nullptr, 0, 0, 0, live_mask(0), live_mask(32)};
+    int issued = 0;
+    // Starts the copy of the next chunk, if there is one, into slot s.
+    const auto start_next = [&](int s) {
+        while (c.off >= c.len) {
+            while (c.mask == 0) {
+                c.batch += 32;
+                if (c.batch >= rows) return;
+                c.mask = c.next;
+                c.next = live_mask(c.batch + 32);
+            }
+            const int64_t i = row_at(c.batch + __ffs(c.mask) - 1);
+            c.mask &= c.mask - 1;
+            c.len = part_of(row_bytes<GT>(row_of<GT>(a.x, i, a.x_stride), a.v), &c.at);
+            c.off = 0;
+        }
+        const uint32_t n = c.len - c.off < kStreamChunk ? c.len - c.off : kStreamChunk;
+        if (lane == 0) {
+            mbar_expect_tx(&full[warp][s], n);
+            bulk_load(slots + s * kStreamChunk, c.at + c.off, n, &full[warp][s]);
+        }
+        c.off += n;
+        ++issued;
+    };
+    for (int s = 0; s < kStreamSlots; ++s) start_next(s);
+
+    float norm = 1.0f;
+    if (!PREF) norm = weight_sum(a, Team<kStreamThreads>{0, tid, &block_sh});
+    if (PREF && warp == 0) empty_pairs(a, p, t);
+    double sums[4] = {0.0, 0.0, 0.0, 0.0};
+    int slot = 0, taken = 0, turn = 0;
+    uint32_t parity = 0;
+    bool bad = false;
+    const auto param = [&](int64_t j) {
+        RowParam q{0.0f, -1, 0.0f, {0.0f, 0.0f, 0.0f}};
+        if (j + lane >= rows) return q;
+        const int64_t i = row_at(j + lane);
+        if (!PREF) return policy_param<GT>(a, pol, i);
+        q.w = token_weight(a, i);
+        if (q.w != 0.0f) {
+            const int64_t y = token_id(a, i);
+            q.xy = y >= 0 ? load1<GT>(row_of<GT>(a.x, i, a.x_stride), y) : NAN;
+            q.f[0] = a.ref[i];
+        }
+        return q;
+    };
+    RowParam mine = param(0), after = param(32);
+    for (int64_t j0 = 0; j0 < rows && !bad; j0 += 32) {
+        RowRef my_ref{0.0f, true};
+        float my_sum = 1.0f;
+        for (unsigned live = __ballot_sync(kFull, mine.w != 0.0f); live != 0 && !bad;
+             live &= live - 1) {
+            const int l = __ffs(live) - 1;
+            const float xy = __shfl_sync(kFull, mine.xy, l);
+            const char* x = row_of<GT>(a.x, row_at(j0 + l), a.x_stride);
+            const RowBytes b = row_bytes<GT>(x, a.v);
+            const char* unused;
+            const uint32_t len = part_of(b, &unused);
+            // this lane's element outside the whole vectors, if any
+            int64_t edge = -1;
+            if (part == 0) {
+                if (lane < 16 && lane < b.head) edge = lane;
+                if (lane >= 16 && lane - 16 < b.tail) edge = a.v - b.tail + lane - 16;
+            }
+            const float xe = edge >= 0 ? load1<GT>(x, edge) : 0.0f;
+            RowRef r = fast_ref(xy);
+            const FastRow fr = fast_row(r);
+            Pair acc[2] = {0, 0};
+            for (uint32_t o = 0; o < len && !bad; o += kStreamChunk) {
+                bad = !__all_sync(kFull, mbar_wait(&full[warp][slot], parity, wait_ns));
+                if (bad) break;
+                const uint32_t n = len - o < kStreamChunk ? len - o : kStreamChunk;
+                const uint8_t* in = slots + slot * kStreamChunk;
+                if (r.fast) {
+                    if (n == kStreamChunk) {
+#pragma unroll
+                        for (int k = 0; k < kStreamChunk / 512; ++k)
+                            sum_vector<GT>(*reinterpret_cast<const uint4*>(in + 16 * (32 * k + lane)),
+                                           fr, acc);
+                    } else {
+                        for (uint32_t at = 16 * lane; at < n; at += 512)
+                            sum_vector<GT>(*reinterpret_cast<const uint4*>(in + at), fr, acc);
+                    }
+                }
+                __syncwarp();                     // every lane has read the slot
+                ++taken;
+                start_next(slot);
+                if (++slot == kStreamSlots) {
+                    slot = 0;
+                    parity ^= 1u;
+                }
+            }
+            const float2 total = floats(add2(acc[0], acc[1]));
+            float s = __fadd_rn(total.x, total.y);
+            if (edge >= 0 && r.fast) s = __fadd_rn(s, row_exp(xe, r));
+            s = team.sum(s, &bad, turn);
+            turn ^= 1;
+            if (bad) break;
+            if (!r.fast || !(s < kFastSum)) {
+                const SlowRow sr = slow_row<GT>(x, a.v, team);
+                r = sr.r;
+                s = sr.sum;
+            }
+            if (lane == l) {
+                my_ref = r;
+                my_sum = s;
+            }
+        }
+        if (bad) break;
+        // the batch's terms, a row per lane
+        const bool held = j0 + lane < rows;
+        if (part == 0) {
+            const int64_t i = held ? row_at(j0 + lane) : begin;
+            const bool live = mine.w != 0.0f;
+            const float lp = live ? row_logp(mine.xy, my_ref, my_sum) : 0.0f;
+            if (held) a.logps[i] = lp;
+            if (!PREF && live) {
+                const PolicyTerms pt = policy_terms(lp, mine.f[0], mine.f[1], mine.f[2], pol);
+                add_policy(sums, pt, pol, __fdiv_rn(mine.w, norm));
+            }
+            if (PREF) {
+                int q = -1;
+                if (held) {
+                    const int seq = find_sequence(t, i);
+                    q = seq >> 1;
+                    p.term[i] = live ? __fmul_rn(mine.w, __fsub_rn(lp, mine.f[0])) : 0.0f;
+                    p.seq[i] = seq;
+                    if (live) save_row(p, i, my_ref, my_sum);
+                }
+                rows_done(a, p, t, q);
+            }
+        }
+        mine = after;
+        after = param(j0 + 64);
+    }
+    if (bad) {
+        // copies in flight land before the block may exit
+        bool drained = true;
+        for (; taken < issued; ++taken) {
+            drained = mbar_wait(&full[warp][slot], parity, kDrainNs) && drained;
+            if (++slot == kStreamSlots) {
+                slot = 0;
+                parity ^= 1u;
+            }
+        }
+        if (lane == 0)
+            atomicOr(&g_loss_status,
+                     kStatusConsumerTimeout | (drained ? 0u : kStatusDrainTimeout));
+    }
+    if (PREF) {
+        preference_stats(a, p, t);
+        return;
+    }
+    if (part == 0) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            double s = sums[k];
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
+            if (lane == 0) team_sums[which][k] = s;
+        }
+    }
+    __syncthreads();
+    if (tid == 0)
+        for (int k = 0; k < 4; ++k) {
+            sums[k] = 0.0;
+            for (int w = 0; w < kRowTeams; ++w) sums[k] += team_sums[w][k];
+        }
+    if (join_blocks(a.ws, sums) && tid < 4) a.stats[tid] = __double2float_rn(a.ws->total[tid]);
+}
+
 int row_blocks(int64_t rows, int per_sm) {
     const int64_t most = per_sm * static_cast<int64_t>(device_sms());
     const int64_t cap = most < kLossMaxBlocks ? most : kLossMaxBlocks;
     return static_cast<int>(rows < 1 ? 1 : rows < cap ? rows : cap);
 }
 
-template <int GT, Pass M>
-cudaError_t go_staged(const TokenArgs& a, const PolicyArgs& pol, const PreferenceArgs& p,
-                      const PairTable& t, int64_t begin, int64_t end, cudaStream_t s) {
-    static int attr_set[256];   // dynamic shared memory opt-in applied
+// Raises a kernel's dynamic shared memory limit, once per device.
+template <class K>
+cudaError_t opt_in(K kernel, size_t bytes, std::atomic<int>* applied) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 256 || !attr_set[dev]) {
-        e = cudaFuncSetAttribute(staged_rows<GT, M>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(kStagedSmem));
-        if (e != cudaSuccess) return e;
-        if (dev >= 0 && dev < 256) attr_set[dev] = 1;
-    }
+    const bool known = dev >= 0 && dev < 256;
+    if (known && applied[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(bytes));
+    if (e == cudaSuccess && known) applied[dev].store(1, std::memory_order_relaxed);
+    return e;
+}
+
+template <int GT, Pass M>
+cudaError_t go_staged(const TokenArgs& a, const PolicyArgs& pol, const PreferenceArgs& p,
+                      int64_t begin, int64_t end, cudaStream_t s) {
+    static std::atomic<int> applied[256];
+    const cudaError_t e = opt_in(staged_rows<GT, M>, kStagedSmem, applied);
+    if (e != cudaSuccess) return e;
     return launch_after(staged_rows<GT, M>, dim3(row_blocks(end - begin, 1)),
-                        dim3(kStagedThreads), kStagedSmem, s, a, pol, p, t, begin, end,
+                        dim3(kStagedThreads), kStagedSmem, s, a, pol, p, begin, end,
                         tma_wait_limit());
+}
+template <int GT, int W, bool PREF>
+cudaError_t go_stream_w(const TokenArgs& a, const PolicyArgs& pol, const PreferenceArgs& p,
+                        const PairTable& t, int64_t begin, int64_t end, cudaStream_t s) {
+    static std::atomic<int> applied[256];
+    const cudaError_t e = opt_in(stream_forward<GT, W, PREF>, kStreamSmem, applied);
+    if (e != cudaSuccess) return e;
+    constexpr int teams = kStreamWarps / W;
+    return launch_after(stream_forward<GT, W, PREF>,
+                        dim3(row_blocks((end - begin + teams - 1) / teams, 1)),
+                        dim3(kStreamThreads), kStreamSmem, s, a, pol, p, t, begin, end,
+                        tma_wait_limit());
+}
+// Warps per row: 4 from 8 rows per SM on (2000 rows of 32000 bf16 logits: 35.2 us
+// against 39.0 with 16), 16 below (152 rows: 13.3 us against 15.6; 760 rows: 23.3
+// against 23.6).  One warp per row was no faster anywhere (3800 rows: 56.3 us
+// against 52.9).
+template <int GT, bool PREF>
+cudaError_t go_stream(const TokenArgs& a, const PolicyArgs& pol, const PreferenceArgs& p,
+                      const PairTable& t, int64_t begin, int64_t end, cudaStream_t s) {
+    if (end - begin >= 8 * static_cast<int64_t>(device_sms()))
+        return go_stream_w<GT, 4, PREF>(a, pol, p, t, begin, end, s);
+    return go_stream_w<GT, 16, PREF>(a, pol, p, t, begin, end, s);
 }
 
 template <int GT>
 cudaError_t go_policy(const TokenArgs& a, const PolicyArgs& p, bool staged, cudaStream_t s) {
-    if (!staged)
-        return launch_after(policy_rows<GT>, dim3(row_blocks(a.n, 2)), dim3(kRowThreads), 0, s, a,
-                            p);
-    const PreferenceArgs none{};
-    const PairTable t{};
-    return a.grad != nullptr ? go_staged<GT, Pass::kPolicy>(a, p, none, t, 0, a.n, s)
-                             : go_staged<GT, Pass::kPolicyForward>(a, p, none, t, 0, a.n, s);
+    if (a.grad == nullptr)
+        return go_stream<GT, false>(a, p, PreferenceArgs{}, PairTable{}, 0, a.n, s);
+    if (staged) return go_staged<GT, Pass::kPolicy>(a, p, PreferenceArgs{}, 0, a.n, s);
+    return launch_after(policy_rows<GT>, dim3(row_blocks(a.n, 2)), dim3(kRowThreads), 0, s, a, p);
 }
 template <int GT>
-cudaError_t go_forward(const TokenArgs& a, const PreferenceArgs& p, const PairTable& t,
-                       bool staged, cudaStream_t s) {
-    const int64_t begin = t.start[0], end = t.start[2 * t.pairs];
-    if (staged)
-        return go_staged<GT, Pass::kPreferenceForward>(a, PolicyArgs{}, p, t, begin, end, s);
-    return launch_after(preference_forward<GT>, dim3(row_blocks(end - begin, 2)),
-                        dim3(kRowThreads), 0, s, a, p, t);
-}
-template <int GT>
-cudaError_t go_backward(const TokenArgs& a, const PreferenceArgs& p, const PairTable& t,
+cudaError_t go_backward(const TokenArgs& a, const PreferenceArgs& p, int64_t begin, int64_t end,
                         bool staged, cudaStream_t s) {
-    const int64_t begin = t.start[0], end = t.start[2 * t.pairs];
     if (staged)
-        return go_staged<GT, Pass::kPreferenceBackward>(a, PolicyArgs{}, p, PairTable{}, begin,
-                                                        end, s);
+        return go_staged<GT, Pass::kPreferenceBackward>(a, PolicyArgs{}, p, begin, end, s);
     return launch_after(preference_backward<GT>, dim3(row_blocks(end - begin, 2)),
                         dim3(kRowThreads), 0, s, a, p, begin, end);
 }
@@ -1161,20 +1341,23 @@ cudaError_t launch_policy_loss(const TokenArgs& a, const PolicyArgs& p, int dtyp
     return e;
 }
 cudaError_t launch_preference_forward(const TokenArgs& a, const PreferenceArgs& p,
-                                      const PairTable& t, int dtype, bool staged,
-                                      cudaStream_t stream) {
-    const cudaError_t e = dtype == kGradF32   ? go_forward<kGradF32>(a, p, t, staged, stream)
-                          : dtype == kGradF16 ? go_forward<kGradF16>(a, p, t, staged, stream)
-                                              : go_forward<kGradBF16>(a, p, t, staged, stream);
+                                      const PairTable& t, int dtype, cudaStream_t stream) {
+    const int64_t begin = t.start[0], end = t.start[2 * t.pairs];
+    const PolicyArgs none{};
+    const cudaError_t e =
+        dtype == kGradF32   ? go_stream<kGradF32, true>(a, none, p, t, begin, end, stream)
+        : dtype == kGradF16 ? go_stream<kGradF16, true>(a, none, p, t, begin, end, stream)
+                            : go_stream<kGradBF16, true>(a, none, p, t, begin, end, stream);
     note_launch();
     return e;
 }
-cudaError_t launch_preference_backward(const TokenArgs& a, const PreferenceArgs& p,
-                                       const PairTable& t, int dtype, bool staged,
+cudaError_t launch_preference_backward(const TokenArgs& a, const PreferenceArgs& p, int64_t begin,
+                                       int64_t end, int dtype, bool staged,
                                        cudaStream_t stream) {
-    const cudaError_t e = dtype == kGradF32   ? go_backward<kGradF32>(a, p, t, staged, stream)
-                          : dtype == kGradF16 ? go_backward<kGradF16>(a, p, t, staged, stream)
-                                              : go_backward<kGradBF16>(a, p, t, staged, stream);
+    const cudaError_t e =
+        dtype == kGradF32   ? go_backward<kGradF32>(a, p, begin, end, staged, stream)
+        : dtype == kGradF16 ? go_backward<kGradF16>(a, p, begin, end, staged, stream)
+                            : go_backward<kGradBF16>(a, p, begin, end, staged, stream);
     note_launch();
     return e;
 }

@@ -290,9 +290,8 @@ int64_t loss_words(int64_t n_tokens, int64_t n_pairs) { return 4 * n_tokens + 2 
 // Whether the rows of logits and gradient take the staged kernels: they fit
 // shared memory, and every gradient row lies as far past a 16-byte boundary as
 // its logits row, so that a row's staged bytes can be stored back in bulk.
-bool staged_rows(const shardstep_token_loss_t* a, bool backward) {
+bool staged_rows(const shardstep_token_loss_t* a) {
     if (!loss_row_fits(a->vocab, a->dtype)) return false;
-    if (!backward) return true;
     const uintptr_t off = reinterpret_cast<uintptr_t>(a->grad) -
                           reinterpret_cast<uintptr_t>(a->logits);
     const int64_t step = (a->grad_stride - a->row_stride) * elem_size(a->dtype);
@@ -473,12 +472,14 @@ int token_policy_loss(const shardstep_token_loss_t* args, const float* old_logps
     add_range(reads, advantages, args->n_tokens * 4);
     if (int rc = check_ranges(&reads, &writes); rc != SHARDSTEP_OK) return rc;
     const PolicyArgs p{old_logps, advantages, 1.0f - clip_low, 1.0f + clip_high, kl_coef};
-    const bool staged = staged_rows(args, k.grad != nullptr);
+    const bool staged = k.grad != nullptr && staged_rows(args);
     const cudaError_t e =
         launch_policy_loss(k, p, args->dtype, staged, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess)
         return ready_fail(SHARDSTEP_ERR_CUDA, "policy loss launch: %s", cudaGetErrorString(e));
-    record_kernel(staged ? "policy_staged<%s> (TMA-staged)" : "policy_rows<%s>",
+    record_kernel(k.grad == nullptr ? "stream_forward<%s> (TMA-staged)"
+                  : staged          ? "staged_rows<%s, policy> (TMA-staged)"
+                                    : "policy_rows<%s>",
                   dtype_name(args->dtype));
     return ready_ok();
 } catch (const std::bad_alloc&) {
@@ -528,8 +529,7 @@ int token_preference_loss(const shardstep_token_loss_t* args, const int64_t* seq
                      words + 4 * tokens,
                      1,
                      0};
-    const bool staged = staged_rows(args, false);
-    const bool staged_back = staged_rows(args, true);
+    const bool staged = k.grad != nullptr && staged_rows(args);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     std::unique_ptr<PairTable> t(new PairTable);
     int32_t row = 0;
@@ -541,9 +541,9 @@ int token_preference_loss(const shardstep_token_loss_t* args, const int64_t* seq
         }
         t->start[2 * t->pairs] = row;
         p.last = q + t->pairs >= n_pairs;
-        cudaError_t e = launch_preference_forward(k, p, *t, args->dtype, staged, s);
+        cudaError_t e = launch_preference_forward(k, p, *t, args->dtype, s);
         if (e == cudaSuccess && k.grad != nullptr)
-            e = launch_preference_backward(k, p, *t, args->dtype, staged_back, s);
+            e = launch_preference_backward(k, p, t->start[0], row, args->dtype, staged, s);
         if (e != cudaSuccess)
             return ready_fail(SHARDSTEP_ERR_CUDA, "preference loss launch: %s",
                               cudaGetErrorString(e));
@@ -551,10 +551,9 @@ int token_preference_loss(const shardstep_token_loss_t* args, const int64_t* seq
         p.log_ratios += 2 * static_cast<int64_t>(t->pairs);
         p.coef += 2 * static_cast<int64_t>(t->pairs);
     }
-    record_kernel(k.grad ? (staged_back ? "preference_staged_backward<%s> (TMA-staged)"
-                                        : "preference_backward<%s>")
-                         : (staged ? "preference_staged_forward<%s> (TMA-staged)"
-                                   : "preference_forward<%s>"),
+    record_kernel(k.grad == nullptr ? "stream_forward<%s> (TMA-staged)"
+                  : staged          ? "staged_rows<%s, preference> (TMA-staged)"
+                                    : "preference_backward<%s>",
                   dtype_name(args->dtype));
     return ready_ok();
 } catch (const std::bad_alloc&) {
