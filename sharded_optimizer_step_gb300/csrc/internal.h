@@ -280,6 +280,8 @@ struct TensorTable {
 };
 struct GroupScalars {
     AdamScalars c[kMaxGroups];
+    float inv_sqrt_bc2[kMaxGroups];   // RN(1 / c[g].sqrt_bc2), host scalars only
+    float neg_zero;                   // -0.0f, unknown to the compiler
 };
 // Elements one block of the list kernels covers.
 constexpr int kListChunk32 = 2048;

@@ -155,21 +155,23 @@ constexpr float kRootMax = 1.9375f;
 constexpr float kTinyBlock = 0x1p-100f;
 
 // Two e4m3 codes (low byte first) as floats.
-__device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t w) {
+__device__ __forceinline__ Pair e4m3x2_to_f32(uint32_t w) {
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w), __NV_E4M3);
-    return __half22float2(__half2(h));
+    const float2 f = __half22float2(__half2(h));
+    return make_pair(f.x, f.y);
 }
-__device__ __forceinline__ uint32_t f32_to_e4m3x2(float a, float b) {
-    return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+__device__ __forceinline__ uint32_t f32_to_e4m3x2(Pair p) {
+    return __nv_cvt_float2_to_fp8x2(floats(p), __NV_SATFINITE, __NV_E4M3);
 }
 // The root's code: 1792 = (127 - 15) * 16 moves the exponent's bias.
 __device__ __forceinline__ float root_to_f32(uint32_t c) {
-    return c != 0 ? __uint_as_float((c + 1792u) << 19) : 0.0f;
+    return c != 0 ? __uint_as_float((c << 19) + (1792u << 19)) : 0.0f;
 }
+// y in [0, 1.9375 (1 + 2^-22)]: the codes' end needs no clamp from above, the
+// unsigned minimum of the bits and 1 is 0 for y = 0 alone.
 __device__ __forceinline__ uint32_t f32_to_root(float y) {
-    int c = static_cast<int>((__float_as_uint(y) + 0x40000u) >> 19) - 1792;
-    c = c < 1 ? 1 : c > 255 ? 255 : c;
-    return y > 0.0f ? static_cast<uint32_t>(c) : 0u;
+    const int c = static_cast<int>(__float_as_uint(y) + 0x40000u - (1792u << 19)) >> 19;
+    return static_cast<uint32_t>(max(c, static_cast<int>(min(__float_as_uint(y), 1u))));
 }
 
 // The scales of a block from the largest magnitudes' bit patterns (as
@@ -195,64 +197,65 @@ __device__ __forceinline__ BlockScales block_scales(uint32_t m_big, uint32_t r_b
     return b;
 }
 
-// 8 consecutive elements of a lane: codes <-> values.
-__device__ __forceinline__ void decode8(uint2 mc, uint2 vc, float ms, float vs, float* m,
-                                        float* r) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const uint32_t w = k < 2 ? mc.x : mc.y;
-        const float2 f = e4m3x2_to_f32((w >> (16 * (k & 1))) & 0xFFFFu);
-        m[2 * k] = __fmul_rn(f.x, ms);
-        m[2 * k + 1] = __fmul_rn(f.y, ms);
-    }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const uint32_t w = k < 4 ? vc.x : vc.y;
-        r[k] = __fmul_rn(root_to_f32((w >> (8 * (k & 3))) & 0xFFu), vs);
-    }
+// 4 consecutive elements of a lane, as two pairs: codes <-> values.
+__device__ __forceinline__ void decode4(uint32_t mc, uint32_t vc, float ms, float vs, Pair* m,
+                                        Pair* r) {
+    const Pair ms2 = make_pair(ms, ms), vs2 = make_pair(vs, vs);
+    m[0] = mul2(e4m3x2_to_f32(mc & 0xFFFFu), ms2);
+    m[1] = mul2(e4m3x2_to_f32(mc >> 16), ms2);
+    r[0] = mul2(make_pair(root_to_f32(vc & 0xFFu), root_to_f32((vc >> 8) & 0xFFu)), vs2);
+    r[1] = mul2(make_pair(root_to_f32((vc >> 16) & 0xFFu), root_to_f32(vc >> 24)), vs2);
 }
-__device__ __forceinline__ void encode8(const float* m, const float* r, const BlockScales& b,
-                                        uint2* mc, uint2* vc) {
-    uint32_t h[4], q[8];
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-        h[k] = f32_to_e4m3x2(__fmul_rn(m[2 * k], b.m_up), __fmul_rn(m[2 * k + 1], b.m_up));
-#pragma unroll
-    for (int k = 0; k < 8; ++k) q[k] = f32_to_root(__fmul_rn(r[k], b.r_up));
-    *mc = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
-    *vc = make_uint2(q[0] | (q[1] << 8) | (q[2] << 16) | (q[3] << 24),
-                     q[4] | (q[5] << 8) | (q[6] << 16) | (q[7] << 24));
+__device__ __forceinline__ void encode4(const Pair* m, const Pair* r, const BlockScales& b,
+                                        uint32_t* mc, uint32_t* vc) {
+    const Pair mu = make_pair(b.m_up, b.m_up), ru = make_pair(b.r_up, b.r_up);
+    *mc = f32_to_e4m3x2(mul2(m[0], mu)) | (f32_to_e4m3x2(mul2(m[1], mu)) << 16);
+    const float2 y0 = floats(mul2(r[0], ru)), y1 = floats(mul2(r[1], ru));
+    *vc = f32_to_root(y0.x) + (f32_to_root(y0.y) << 8) + (f32_to_root(y1.x) << 16) +
+          (f32_to_root(y1.y) << 24);
 }
-__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
-__device__ __forceinline__ BlockScales scales_of(const float* m, const float* r) {
-    uint32_t mb = 0, rb = 0;
+// max(|a|, |b|, |c|), NaN where one is.
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// The scales of a warp's block from each lane's 2 x 4 elements.
+__device__ __forceinline__ uint32_t lane_max(const Pair (*x)[2]) {
+    float big = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        mb = max(mb, abs_bits(m[k]));
-        rb = max(rb, abs_bits(r[k]));
-    }
-    return block_scales(__reduce_max_sync(0xFFFFFFFFu, mb), __reduce_max_sync(0xFFFFFFFFu, rb));
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float2 f = floats(x[h][k]);
+            big = max3_abs(big, f.x, f.y);
+        }
+    return __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(big));
 }
 
-// One element with the root of v in and out:
+// r / b for b = sqrt(bc2), correctly rounded, from y = RN(1 / b): Markstein's
+// correction (named at div_nd), twice, so that the quotient is within an ulp
+// before the step that rounds it whatever the operands' fractions are.  r is 0
+// or between 2^-75 and 2^64 (the root of a positive fp32 value), so no
+// residual leaves the normal range; for an infinite r or an unusable y the
+// caller takes the division itself.
+__device__ __forceinline__ Pair div_root(Pair r, Pair b_neg, Pair y) {
+    Pair q = mul2(r, y);
+    q = fma2(fma2(q, b_neg, r), y, q);
+    return fma2(fma2(q, b_neg, r), y, q);
+}
+
+// The 8-bit step: a warp per block of 256 elements, 4 + 4 per lane (128 apart,
+// so that every access of a warp is one contiguous run), so a block's maxima
+// are two warp reductions and nothing leaves the registers between the load and
+// the store of a code.  Per element, one IEEE rounding per operation as in
+// adamw_elem, with the root of v in and out:
 //   p -= lr wd p;  m = b1 m + (1 - b1) g;  r = sqrt(b2 r^2 + (1 - b2) g g);
 //   p -= (lr / bc1) m / (r / sqrt(bc2) + eps), with m and r before rounding
-// to their codes.  One IEEE rounding per operation, as in adamw_elem.
-__device__ __forceinline__ void adamw_root_elem(float g, float& p, float& m, float& r,
-                                                const AdamScalars& c) {
-    p = __fsub_rn(p, __fmul_rn(c.lr_wd, p));
-    m = __fadd_rn(__fmul_rn(c.beta1, m), __fmul_rn(c.omb1, g));
-    r = __fsqrt_rn(__fadd_rn(__fmul_rn(c.beta2, __fmul_rn(r, r)),
-                             __fmul_rn(__fmul_rn(c.omb2, g), g)));
-    const float den = __fadd_rn(__fdiv_rn(r, c.sqrt_bc2), c.eps);
-    p = __fsub_rn(p, __fdiv_rn(__fmul_rn(c.step_size, m), den));
-}
-
-// The 8-bit step: a warp per block of 256 elements, 8 consecutive ones per
-// lane, so a block's maxima are two warp reductions and nothing leaves the
-// registers between the load and the store of a code.  Bound by memory in the
-// limit, (gradient + 8 + 4 + 2) bytes per element; about 70 instructions per
-// element keep the issue slots close behind.
+// to their codes.  Bound by memory in the limit, (gradient + 8 + 4 + 2) bytes
+// per element, if the issue slots keep up: products and sums go two elements to
+// an instruction.  (A warp that took 4 blocks in turn was slower, 379 us against
+// 359 for 124M elements: its loads no longer overlap other blocks' arithmetic.)
 template <int CAP, int GT, int PT>
 __global__ void __launch_bounds__(kListThreads)
     tensors_adamw8(const __grid_constant__ TensorTable<CAP> t,
@@ -262,113 +265,196 @@ __global__ void __launch_bounds__(kListThreads)
     if (skip_step(skip)) return;
     const int s = find_tensor(t, blockIdx.x);
     const AdamScalars c = resolve_adam(gs.c[t.group[s]]);
+    const float inv_root =
+        c.dev != nullptr ? __fdiv_rn(1.0f, c.sqrt_bc2) : gs.inv_sqrt_bc2[t.group[s]];
     const float k = coef != nullptr ? __ldg(coef) : 1.0f;
     const int64_t n = t.n[s];
-    const int64_t blk = static_cast<int64_t>(blockIdx.x - t.b0[s]) * (kListChunk8 / kMomentBlock) +
-                        (threadIdx.x >> 5);
-    const int64_t base = blk * kMomentBlock;
-    if (base >= n) return;
-    const int64_t i = base + 8 * (threadIdx.x & 31);
     const void* G = t.grad[s];
     float* P = t.master[s];
     uint8_t* M = static_cast<uint8_t*>(t.m[s]);
     uint8_t* V = static_cast<uint8_t*>(t.v[s]);
     uint16_t* O = static_cast<uint16_t*>(t.param[s]);
+    const bool vec = t.vec[s] != 0;
+    const Pair lr_wd = make_pair(-c.lr_wd, -c.lr_wd), b1 = make_pair(c.beta1, c.beta1),
+               o1 = make_pair(c.omb1, c.omb1), b2 = make_pair(c.beta2, c.beta2),
+               o2 = make_pair(c.omb2, c.omb2), kk = make_pair(k, k);
+    // Products that are added to are formed as a b + (-0), the same value: of a
+    // plain product and a sum of pairs the assembler makes one fma (one rounding
+    // instead of two) whatever their rounding modifiers, which it cannot do here
+    // as long as it does not know the -0.
+    const Pair nz = make_pair(gs.neg_zero, gs.neg_zero);
+    const Pair root_neg = make_pair(-c.sqrt_bc2, -c.sqrt_bc2), inv = make_pair(inv_root, inv_root),
+               eps = make_pair(c.eps, c.eps), size = make_pair(c.step_size, c.step_size);
+    const int64_t blk = static_cast<int64_t>(blockIdx.x - t.b0[s]) * (kListChunk8 / kMomentBlock) +
+                        (threadIdx.x >> 5);
+    const int64_t base = blk * kMomentBlock;
+    if (base >= n) return;
+    const int64_t i = base + 4 * (threadIdx.x & 31);
     float* MS = t.m_scale[s] + blk;
     float* VS = t.v_scale[s] + blk;
-    const bool whole = t.vec[s] && base + kMomentBlock <= n;
-    float g[8], p[8], m[8], r[8];
-    uint2 mc = make_uint2(0, 0), vc = make_uint2(0, 0);
+    const bool whole = vec && base + kMomentBlock <= n;
+    float g[2][4];
+    Pair p[2][2], m[2][2], r[2][2];
+    uint32_t mc[2], vc[2];
     const float ms = *MS, vs = *VS;
     if (whole) {
-        loadw<GT, 8>(G, i, g);
-        mc = ldcs8(M + i);
-        vc = ldcs8(V + i);
-        unpack4f(ldcs16(P + i), p);
-        unpack4f(ldcs16(P + i + 4), p + 4);
+        uint4 p4[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            loadw<GT, 4>(G, i + 128 * h, g[h]);
+            mc[h] = __ldcs(reinterpret_cast<const uint32_t*>(M + i + 128 * h));
+            vc[h] = __ldcs(reinterpret_cast<const uint32_t*>(V + i + 128 * h));
+            p4[h] = ldcs16(P + i + 128 * h);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float f[4];
+            unpack4f(p4[h], f);
+            p[h][0] = make_pair(f[0], f[1]);
+            p[h][1] = make_pair(f[2], f[3]);
+        }
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            g[e] = p[e] = 0.0f;
-            if (i + e < n) {
-                g[e] = load1<GT>(G, i + e);
-                p[e] = P[i + e];
-                const uint32_t a = M[i + e], b = V[i + e];
-                if (e < 4) {
-                    mc.x |= a << (8 * e);
-                    vc.x |= b << (8 * e);
-                } else {
-                    mc.y |= a << (8 * (e - 4));
-                    vc.y |= b << (8 * (e - 4));
+        for (int h = 0; h < 2; ++h) {
+            float f[4];
+            mc[h] = vc[h] = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int64_t j = i + 128 * h + e;
+                g[h][e] = f[e] = 0.0f;
+                if (j < n) {
+                    g[h][e] = load1<GT>(G, j);
+                    f[e] = P[j];
+                    mc[h] |= static_cast<uint32_t>(M[j]) << (8 * e);
+                    vc[h] |= static_cast<uint32_t>(V[j]) << (8 * e);
                 }
             }
+            p[h][0] = make_pair(f[0], f[1]);
+            p[h][1] = make_pair(f[2], f[3]);
         }
     }
-    decode8(mc, vc, ms, vs, m, r);
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        adamw_root_elem(coef != nullptr ? __fmul_rn(g[e], k) : g[e], p[e], m[e], r[e], c);
+    for (int h = 0; h < 2; ++h) {
+        decode4(mc[h], vc[h], ms, vs, m[h], r[h]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            Pair gg = make_pair(g[h][2 * e], g[h][2 * e + 1]);
+            if (coef != nullptr) gg = mul2(gg, kk);
+            p[h][e] = add2(p[h][e], fma2(lr_wd, p[h][e], nz));
+            m[h][e] = add2(fma2(b1, m[h][e], nz), fma2(o1, gg, nz));
+            const float2 v = floats(
+                add2(fma2(b2, mul2(r[h][e], r[h][e]), nz), fma2(mul2(o2, gg), gg, nz)));
+            r[h][e] = make_pair(__fsqrt_rn(v.x), __fsqrt_rn(v.y));
+        }
+    }
     if (!whole) {   // places past the tensor's end take no part in the maxima
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (i + e >= n) m[e] = r[e] = 0.0f;
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int64_t j = i + 128 * h + 2 * e;
+                const float2 a = floats(m[h][e]), b = floats(r[h][e]);
+                m[h][e] = make_pair(j < n ? a.x : 0.0f, j + 1 < n ? a.y : 0.0f);
+                r[h][e] = make_pair(j < n ? b.x : 0.0f, j + 1 < n ? b.y : 0.0f);
+            }
     }
-    const BlockScales b = scales_of(m, r);
-    encode8(m, r, b, &mc, &vc);
+    const uint32_t m_big = lane_max(m), r_big = lane_max(r);
+    const BlockScales b = block_scales(m_big, r_big);
     if ((threadIdx.x & 31) == 0) {
         *MS = b.m_scale;
         *VS = b.r_scale;
     }
-    if (whole) {
-        stcs16(P + i, pack4f(p));
-        stcs16(P + i + 4, pack4f(p + 4));
-        stcs8(M + i, mc);
-        stcs8(V + i, vc);
-        if (O != nullptr)
-            stcs16(O + i, make_uint4(pack2<PT>(p[0], p[1]), pack2<PT>(p[2], p[3]),
-                                     pack2<PT>(p[4], p[5]), pack2<PT>(p[6], p[7])));
+    const bool exact = r_big >= 0x7F800000u || !(c.sqrt_bc2 > 0x1p-40f && c.sqrt_bc2 < 0x1p40f);
+    Pair root[2][2];
+    if (exact) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float2 f = floats(r[h][e]);
+                root[h][e] = make_pair(__fdiv_rn(f.x, c.sqrt_bc2), __fdiv_rn(f.y, c.sqrt_bc2));
+            }
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if (i + e < n) {
-                P[i + e] = p[e];
-                M[i + e] = static_cast<uint8_t>((e < 4 ? mc.x : mc.y) >> (8 * (e & 3)));
-                V[i + e] = static_cast<uint8_t>((e < 4 ? vc.x : vc.y) >> (8 * (e & 3)));
-                if (O != nullptr) O[i + e] = pack1<PT>(p[e]);
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) root[h][e] = div_root(r[h][e], root_neg, inv);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        encode4(m[h], r[h], b, &mc[h], &vc[h]);
+        float f[4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float2 den = floats(add2(root[h][e], eps));
+            const float2 num = floats(mul2(size, m[h][e]));
+            const float2 x = floats(p[h][e]);
+            f[2 * e] = __fsub_rn(x.x, __fdiv_rn(num.x, den.x));
+            f[2 * e + 1] = __fsub_rn(x.y, __fdiv_rn(num.y, den.y));
+        }
+        if (whole) {
+            stcs16(P + i + 128 * h, pack4f(f));
+            __stcs(reinterpret_cast<uint32_t*>(M + i + 128 * h), mc[h]);
+            __stcs(reinterpret_cast<uint32_t*>(V + i + 128 * h), vc[h]);
+            if (O != nullptr)
+                stcs8(O + i + 128 * h, make_uint2(pack2<PT>(f[0], f[1]), pack2<PT>(f[2], f[3])));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int64_t j = i + 128 * h + e;
+                if (j < n) {
+                    P[j] = f[e];
+                    M[j] = static_cast<uint8_t>(mc[h] >> (8 * e));
+                    V[j] = static_cast<uint8_t>(vc[h] >> (8 * e));
+                    if (O != nullptr) O[j] = pack1<PT>(f[e]);
+                }
             }
         }
     }
 }
 
-// Codes -> fp32 moments: m = code * scale, v = (code * scale)^2.
+// Codes -> fp32 moments: m = code * scale, v = (code * scale)^2.  A thread takes
+// 4 consecutive elements at 2 places 1024 apart.
+constexpr int kDecodeChunk = 2 * 4 * kListThreads;
 __global__ void __launch_bounds__(kListThreads)
     moments_decode(const uint8_t* __restrict__ M, const float* __restrict__ MS,
                    const uint8_t* __restrict__ V, const float* __restrict__ VS, int64_t n,
                    float* __restrict__ Mo, float* __restrict__ Vo, bool vec) {
     pdl_enter();
-    const int64_t i = 8 * (static_cast<int64_t>(blockIdx.x) * kListThreads + threadIdx.x);
-    if (i >= n) return;
-    const int64_t blk = i / kMomentBlock;
-    const float ms = __ldg(MS + blk), vs = __ldg(VS + blk);
-    float m[8], r[8];
-    if (vec && i + 8 <= n) {
-        decode8(ldcs8(M + i), ldcs8(V + i), ms, vs, m, r);
+    const int64_t base = static_cast<int64_t>(blockIdx.x) * kDecodeChunk;
+    if (vec && base + kDecodeChunk <= n) {
+        uint32_t mc[2], vc[2];
+        float ms[2], vs[2];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) r[e] = __fmul_rn(r[e], r[e]);
-        stcs16(Mo + i, pack4f(m));
-        stcs16(Mo + i + 4, pack4f(m + 4));
-        stcs16(Vo + i, pack4f(r));
-        stcs16(Vo + i + 4, pack4f(r + 4));
+        for (int h = 0; h < 2; ++h) {
+            const int64_t i = base + 4 * (h * kListThreads + threadIdx.x);
+            mc[h] = __ldcs(reinterpret_cast<const uint32_t*>(M + i));
+            vc[h] = __ldcs(reinterpret_cast<const uint32_t*>(V + i));
+            ms[h] = __ldg(MS + i / kMomentBlock);
+            vs[h] = __ldg(VS + i / kMomentBlock);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t i = base + 4 * (h * kListThreads + threadIdx.x);
+            Pair m[2], r[2];
+            decode4(mc[h], vc[h], ms[h], vs[h], m, r);
+            const float2 a = floats(m[0]), b = floats(m[1]);
+            const float2 x = floats(mul2(r[0], r[0])), y = floats(mul2(r[1], r[1]));
+            const float f[4] = {a.x, a.y, b.x, b.y}, g[4] = {x.x, x.y, y.x, y.y};
+            stcs16(Mo + i, pack4f(f));
+            stcs16(Vo + i, pack4f(g));
+        }
         return;
     }
-    for (int e = 0; e < 8 && i + e < n; ++e) {
-        Mo[i + e] = __fmul_rn(e4m3x2_to_f32(M[i + e]).x, ms);
-        const float x = __fmul_rn(root_to_f32(V[i + e]), vs);
-        Vo[i + e] = __fmul_rn(x, x);
+    const int64_t end = base + kDecodeChunk < n ? base + kDecodeChunk : n;
+    for (int64_t i = base + threadIdx.x; i < end; i += kListThreads) {
+        Mo[i] = __fmul_rn(floats(e4m3x2_to_f32(M[i])).x, MS[i / kMomentBlock]);
+        const float x = __fmul_rn(root_to_f32(V[i]), VS[i / kMomentBlock]);
+        Vo[i] = __fmul_rn(x, x);
     }
 }
 
-// fp32 moments -> codes and scales, a warp per block.
+// fp32 moments -> codes and scales, a warp per block, laid out as in the step.
 __global__ void __launch_bounds__(kListThreads)
     moments_encode(const float* __restrict__ Mi, const float* __restrict__ Vi, int64_t n,
                    uint8_t* __restrict__ M, float* __restrict__ MS, uint8_t* __restrict__ V,
@@ -378,37 +464,44 @@ __global__ void __launch_bounds__(kListThreads)
         static_cast<int64_t>(blockIdx.x) * (kListThreads / 32) + (threadIdx.x >> 5);
     const int64_t base = blk * kMomentBlock;
     if (base >= n) return;
-    const int64_t i = base + 8 * (threadIdx.x & 31);
-    float m[8], r[8];
+    const int64_t i = base + 4 * (threadIdx.x & 31);
     const bool whole = vec && base + kMomentBlock <= n;
-    if (whole) {
-        loadw<kGradF32, 8>(Mi, i, m);
-        loadw<kGradF32, 8>(Vi, i, r);
-    } else {
+    Pair m[2][2], r[2][2];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            m[e] = i + e < n ? Mi[i + e] : 0.0f;
-            r[e] = i + e < n ? Vi[i + e] : 0.0f;
+    for (int h = 0; h < 2; ++h) {
+        float a[4], b[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int64_t j = i + 128 * h + e;
+            a[e] = j < n ? Mi[j] : 0.0f;
+            b[e] = j < n ? Vi[j] : 0.0f;
         }
+        m[h][0] = make_pair(a[0], a[1]);
+        m[h][1] = make_pair(a[2], a[3]);
+        r[h][0] = make_pair(__fsqrt_rn(b[0]), __fsqrt_rn(b[1]));
+        r[h][1] = make_pair(__fsqrt_rn(b[2]), __fsqrt_rn(b[3]));
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) r[e] = __fsqrt_rn(r[e]);
-    const BlockScales b = scales_of(m, r);
-    uint2 mc, vc;
-    encode8(m, r, b, &mc, &vc);
+    const uint32_t m_big = lane_max(m), r_big = lane_max(r);
+    const BlockScales b = block_scales(m_big, r_big);
     if ((threadIdx.x & 31) == 0) {
         MS[blk] = b.m_scale;
         VS[blk] = b.r_scale;
     }
-    if (whole) {
-        stcs8(M + i, mc);
-        stcs8(V + i, vc);
-    } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if (i + e < n) {
-                M[i + e] = static_cast<uint8_t>((e < 4 ? mc.x : mc.y) >> (8 * (e & 3)));
-                V[i + e] = static_cast<uint8_t>((e < 4 ? vc.x : vc.y) >> (8 * (e & 3)));
+    for (int h = 0; h < 2; ++h) {
+        uint32_t mc, vc;
+        encode4(m[h], r[h], b, &mc, &vc);
+        if (whole) {
+            __stcs(reinterpret_cast<uint32_t*>(M + i + 128 * h), mc);
+            __stcs(reinterpret_cast<uint32_t*>(V + i + 128 * h), vc);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int64_t j = i + 128 * h + e;
+                if (j < n) {
+                    M[j] = static_cast<uint8_t>(mc >> (8 * e));
+                    V[j] = static_cast<uint8_t>(vc >> (8 * e));
+                }
             }
         }
     }
@@ -430,16 +523,35 @@ __device__ __forceinline__ double block_sum(double x) {
     return s;
 }
 
+// acc += the squares of the elements of 16 bytes.
+template <int GT>
+__device__ __forceinline__ void add_squares(const uint4& raw, Pair* acc) {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    if constexpr (GT == kGradF32) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const Pair x = make_pair(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
+            acc[k] = fma2(x, x, acc[k]);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const Pair x = make_pair(cvt16<GT>(w[k] & 0xFFFFu), cvt16<GT>(w[k] >> 16));
+            acc[k] = fma2(x, x, acc[k]);
+        }
+    }
+}
+
 // Squares are formed and summed in fp32, in 8 sums per thread over the chunks
 // a block takes in turn (b, b + gridDim, ...); the threads' sums are joined in
 // double in a fixed order, the blocks' likewise by the block that arrives
 // last, so the result does not depend on the order in which blocks run.
 // Bound by the one read of the gradients.
 template <int CAP, int GT>
-__global__ void __launch_bounds__(kListThreads)
+__global__ void __launch_bounds__(kListThreads, 4)
     tensors_norm(const __grid_constant__ NormTable<CAP> t, const NormArgs a) {
     pdl_enter();
-    float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    Pair acc[4] = {0, 0, 0, 0};
     const uint32_t chunks = t.b0[t.count];
     int s = blockIdx.x < chunks ? find_tensor(t, blockIdx.x) : 0;
     for (uint32_t b = blockIdx.x; b < chunks; b += gridDim.x) {
@@ -448,26 +560,31 @@ __global__ void __launch_bounds__(kListThreads)
         const int64_t base = static_cast<int64_t>(b - t.b0[s]) * kNormChunk;
         const void* G = t.p[s];
         if (t.vec[s] && base + kNormChunk <= n) {
-            constexpr int U = kNormChunk / (8 * kListThreads);
-            float f[U][8];
+            // all of the chunk's loads in flight before any arithmetic
+            constexpr int es = GT == kGradF32 ? 4 : 2;
+            constexpr int U = kNormChunk * es / (16 * kListThreads);
+            const char* at = static_cast<const char*>(G) + base * es + 16 * threadIdx.x;
+            uint4 raw[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                loadw<GT, 8>(G, base + 8 * (u * kListThreads + threadIdx.x), f[u]);
+            for (int u = 0; u < U; ++u) raw[u] = ld_once(at + 16 * kListThreads * u);
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) acc[e] = __fmaf_rn(f[u][e], f[u][e], acc[e]);
+            for (int u = 0; u < U; ++u) add_squares<GT>(raw[u], acc);
         } else {
             const int64_t end = base + kNormChunk < n ? base + kNormChunk : n;
             for (int64_t i = base + threadIdx.x; i < end; i += kListThreads) {
                 const float x = load1<GT>(G, i);
-                acc[0] = __fmaf_rn(x, x, acc[0]);
+                const Pair x2 = make_pair(x, 0.0f);
+                acc[0] = fma2(x2, x2, acc[0]);
             }
         }
     }
     double sum = 0.0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sum += static_cast<double>(acc[e]);
+    for (int e = 0; e < 4; ++e) {
+        const float2 f = floats(acc[e]);
+        sum += static_cast<double>(f.x);
+        sum += static_cast<double>(f.y);
+    }
     sum = block_sum(sum);
     __shared__ bool last;
     if (threadIdx.x == 0) {
@@ -539,7 +656,7 @@ template cudaError_t launch_tensors_adamw<kTensorsLarge>(const TensorTable<kTens
 cudaError_t launch_moments_decode(const uint8_t* m, const float* m_scale, const uint8_t* v,
                                   const float* v_scale, int64_t n, float* m_out, float* v_out,
                                   bool vec, cudaStream_t stream) {
-    const int64_t blocks = (n + 8 * kListThreads - 1) / (8 * kListThreads);
+    const int64_t blocks = (n + kDecodeChunk - 1) / kDecodeChunk;
     const cudaError_t e = launch_after(moments_decode, dim3(static_cast<unsigned>(blocks)),
                                        dim3(kListThreads), 0, stream, m, m_scale, v, v_scale, n,
                                        m_out, v_out, vec);

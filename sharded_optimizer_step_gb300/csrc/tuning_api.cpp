@@ -77,6 +77,7 @@ int take_groups(const shardstep_adamw_t* hp, const shardstep_adamw_state_t* cons
             // groups that differ only in lr and decay are the rule: the beta
             // powers' running products are the same ones then
             c = host_adam_scalars(hp[g]);
+            gs->inv_sqrt_bc2[g] = 1.0f / c.sqrt_bc2;
         }
     }
     return SHARDSTEP_OK;
@@ -189,6 +190,7 @@ int adamw_step(const void* const* grads, const shardstep_tensor_t* ts, int32_t n
         return ready_fail(SHARDSTEP_ERR_INVALID, "grad_coef misaligned");
     if (skip && !aligned(skip, 4)) return ready_fail(SHARDSTEP_ERR_INVALID, "skip misaligned");
     GroupScalars gs{};
+    gs.neg_zero = -0.0f;
     if (int rc = take_groups(hp, states, on_device, n_groups, &gs); rc != SHARDSTEP_OK) return rc;
     if (n == 0) return ready_ok();
     if (ts == nullptr || grads == nullptr)
@@ -429,8 +431,8 @@ int tensors_grad_norm(const void* const* grads, const int64_t* numels, int32_t n
     if (self_overlap(writes) || cross_overlap(reads, writes))
         return ready_fail(SHARDSTEP_ERR_INVALID, "an output overlaps an input or another output");
     NormArgs a{static_cast<NormWork*>(workspace), loss_scale, max_norm, out, found_inf, 1, 0};
-    // two resident blocks per SM keep 64 KB of loads in flight on each
-    const uint64_t most = std::min<uint64_t>(2 * static_cast<uint64_t>(device_sms()),
+    // four resident blocks per SM keep 64 KB or more of loads in flight on each
+    const uint64_t most = std::min<uint64_t>(4 * static_cast<uint64_t>(device_sms()),
                                              kNormMaxBlocks);
     const int blocks = static_cast<int>(std::max<uint64_t>(1, std::min(chunks, most)));
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
