@@ -12,6 +12,7 @@ N_d data-parallel ranks are emulated as N_d buffers in one GPU's memory.
 from __future__ import annotations
 
 import ctypes
+import struct
 from dataclasses import dataclass
 from typing import NamedTuple
 
@@ -65,6 +66,10 @@ class Layout:
 def _stream(stream, device=None):
     import torch
     if stream is None:
+        # the raw handle alone, where this torch gives it (a tenth of the time)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None and device is not None and device.index is not None:
+            return raw(device.index)
         stream = torch.cuda.current_stream(device)
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
@@ -777,12 +782,27 @@ class LossWorkspace:
     def __init__(self, device="cuda"):
         self.device = device
         self.buf = None
+        self.addr = self.nbytes = 0
 
-    def at_least(self, nbytes: int):
-        import torch
-        if self.buf is None or self.buf.numel() * 8 < nbytes:
-            self.buf = torch.zeros((nbytes + 7) // 8, dtype=torch.int64, device=self.device)
-        return self.buf
+    def at_least(self, n_tokens: int, pairs: int):
+        """(address, bytes, buffer) of a workspace for that many tokens in
+        that many pairs (0: the policy loss)."""
+        need = _loss_head() + (16 * n_tokens + 8 * pairs if pairs else 0)
+        if self.nbytes < need:
+            import torch
+            self.buf = torch.zeros((need + 7) // 8, dtype=torch.int64, device=self.device)
+            self.addr, self.nbytes = self.buf.data_ptr(), self.buf.numel() * 8
+        return self.addr, self.nbytes, self.buf
+
+
+_LOSS_HEAD = []
+
+
+def _loss_head() -> int:
+    """Bytes of a loss workspace before its per-token words."""
+    if not _LOSS_HEAD:
+        _LOSS_HEAD.append(int(_capi.lib().token_loss_workspace_bytes(0, 0)))
+    return _LOSS_HEAD[0]
 
 
 class PolicyLoss(NamedTuple):
@@ -801,60 +821,77 @@ class PreferenceLoss(NamedTuple):
 def _f32_word(t, what):
     import torch
     if t is None:
-        return None
+        return 0
     if t.dtype != torch.float32 or not t.is_cuda or t.numel() < 1:
         raise ValueError(f"{what} must be a CUDA fp32 word")
     return t.data_ptr()
 
 
-def _per_token(t, n, what, optional=False):
+def _per_token(t, n, what, f32):
     """Device address of an fp32 array of n tokens."""
-    import torch
-    if t is None and optional:
-        return None
-    if t is None or t.dtype != torch.float32 or t.numel() != n or not t.is_cuda \
-            or not t.is_contiguous():
+    if t.dtype is not f32 or t.numel() != n or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous CUDA fp32 tensor of {n} elements")
     return t.data_ptr()
+
+
+# shardstep_token_loss_t, packed in one go: this is the losses' host time
+_TOKEN_LOSS = struct.Struct("@QqiiQqqQQQQqffQQQq")
+assert _TOKEN_LOSS.size == ctypes.sizeof(_capi.TokenLoss)
 
 
 def _token_args(logits, ids, weights, ref_logps, grad, grad_scale, loss_scale, norm, workspace,
                 pairs):
     """The checks both losses share; allocates their outputs.  Returns the C
-    arguments, the statistics, the log probabilities and the workspace buffer
-    (which the caller holds until the launch)."""
+    arguments, the statistics and the log probabilities, and the workspace
+    buffer (which the caller holds until the launch)."""
     import torch
-    if logits.dim() != 2 or not logits.is_cuda:
+    f32 = torch.float32
+    shape = logits.shape
+    if len(shape) != 2 or not logits.is_cuda:
         raise ValueError("logits must be a CUDA matrix [tokens, vocabulary]")
-    n, v = logits.shape
-    if n > 0 and logits.stride(1) != 1 and v > 1:
-        raise ValueError("a row of the logits must be contiguous")
-    if ids.dtype not in (torch.int64, torch.int32) or ids.numel() != n or not ids.is_cuda \
-            or not ids.is_contiguous():
+    n, v = shape
+    row, col = logits.stride()
+    if n > 0 and v > 1 and (col != 1 or (n > 1 and row < v)):
+        raise ValueError("the rows of the logits must be contiguous and apart")
+    if row < v:
+        row = v
+    if ids.dtype is torch.int64:
+        id_bytes = 8
+    elif ids.dtype is torch.int32:
+        id_bytes = 4
+    else:
+        id_bytes = 0
+    if not id_bytes or ids.numel() != n or not ids.is_cuda or not ids.is_contiguous():
         raise ValueError(f"ids must be contiguous CUDA int64 or int32 with {n} elements")
-    if grad is not None and (grad.shape != logits.shape or grad.dtype != logits.dtype
-                             or not grad.is_cuda or (n > 0 and v > 1 and grad.stride(1) != 1)):
-        raise ValueError("grad must have the logits' shape and dtype, rows contiguous")
-    if grad is not None and n > 1 and grad.stride(0) < v or n > 1 and logits.stride(0) < v:
-        raise ValueError("the rows of logits or grad overlap")
-    out = torch.empty(n + 4, dtype=torch.float32, device=logits.device)
-    stats, logps = out[:4], out[4:]
-    if n == 0:
-        stats.zero_()
-    ws = workspace if workspace is not None else LossWorkspace(logits.device)
-    need = _capi.lib().token_loss_workspace_bytes(n, pairs)
-    buf = ws.at_least(need)
-    args = _capi.TokenLoss(
-        logits.data_ptr(), max(logits.stride(0), v), _dtype_code(logits), ids.element_size(),
-        ids.data_ptr(), n, v, _per_token(weights, n, "weights", True),
-        _per_token(ref_logps, n, "ref_logps", True), logps.data_ptr(),
-        grad.data_ptr() if grad is not None else None,
-        max(grad.stride(0), v) if grad is not None else v, float(grad_scale),
-        0.0 if norm is None else float(norm), _f32_word(loss_scale, "loss_scale"),
-        stats.data_ptr(), buf.data_ptr(), buf.numel() * 8)
-    if norm is not None and not norm > 0:
+    grad_at, grad_row = 0, v
+    if grad is not None:
+        grad_row, col = grad.stride() if grad.dim() == 2 else (0, 0)
+        if grad.shape != shape or grad.dtype is not logits.dtype or not grad.is_cuda or (
+                n > 0 and v > 1 and (col != 1 or (n > 1 and grad_row < v))):
+            raise ValueError("grad must have the logits' shape and dtype, its rows contiguous "
+                             "and apart")
+        grad_at = grad.data_ptr()
+        if grad_row < v:
+            grad_row = v
+    if norm is None:
+        norm = 0.0
+    elif not norm > 0:
         raise ValueError("norm must be > 0 (None: the sum of the weights, or the pairs)")
-    return args, stats, logps, buf
+    device = logits.device
+    out = torch.empty(n + 4 + 2 * pairs, dtype=f32, device=device)
+    if n == 0:
+        out.zero_()
+    at = out.data_ptr()
+    if workspace is None:
+        workspace = LossWorkspace(device)
+    ws, ws_bytes, held = workspace.at_least(n, pairs)
+    args = _TOKEN_LOSS.pack(
+        logits.data_ptr(), row, _dtype_code(logits), id_bytes, ids.data_ptr(), n, v,
+        _per_token(weights, n, "weights", f32) if weights is not None else 0,
+        _per_token(ref_logps, n, "ref_logps", f32) if ref_logps is not None else 0,
+        at + 16, grad_at, grad_row, grad_scale, norm,
+        _f32_word(loss_scale, "loss_scale") if loss_scale is not None else 0, at, ws, ws_bytes)
+    return args, out, held
 
 
 def policy_loss(logits, ids, old_logps, advantages, *, ref_logps=None, weights=None,
@@ -875,14 +912,17 @@ def policy_loss(logits, ids, old_logps, advantages, *, ref_logps=None, weights=N
     ``grad`` (None: forward only; may be ``logits``) receives d loss / d logits
     times ``grad_scale`` times the device word ``loss_scale`` (a
     ``GradScaler.scale``)."""
-    args, stats, logps, held = _token_args(logits, ids, weights, ref_logps, grad, grad_scale,
-                                           loss_scale, norm, workspace, 0)
-    n = args.n_tokens
-    _capi.check("token_policy_loss", _capi.lib().token_policy_loss(
-        ctypes.byref(args), _per_token(old_logps, n, "old_logps"),
-        _per_token(advantages, n, "advantages"), clip_low, clip_high, kl_coef,
-        _stream(stream, logits.device)))
-    return PolicyLoss(stats, logps, grad)
+    import torch
+    args, out, held = _token_args(logits, ids, weights, ref_logps, grad, grad_scale, loss_scale,
+                                  norm, workspace, 0)
+    n = logits.shape[0]
+    rc = _capi.lib().token_policy_loss(
+        args, _per_token(old_logps, n, "old_logps", torch.float32),
+        _per_token(advantages, n, "advantages", torch.float32), clip_low, clip_high, kl_coef,
+        _stream(stream, logits.device))
+    if rc:
+        _capi.check("token_policy_loss", rc)
+    return PolicyLoss(out[:4], out[4:], grad)
 
 
 def preference_loss(logits, ids, seq_lens, ref_logps, *, beta: float = 0.1,
@@ -900,20 +940,20 @@ def preference_loss(logits, ids, seq_lens, ref_logps, *, beta: float = 0.1,
     ``weights`` [N] fp32 (0: not read, e.g. a prompt; 1 / length for averaged
     log ratios); ``norm`` None: the number of pairs.  ``grad``, ``grad_scale``
     and ``loss_scale`` as in ``policy_loss``."""
-    import torch
-    lens = _capi.i64_array(seq_lens)
-    if len(seq_lens) % 2:
+    count = len(seq_lens)
+    if count % 2:
         raise ValueError("seq_lens must hold chosen and rejected lengths in turn")
-    pairs = len(seq_lens) // 2
-    args, stats, logps, held = _token_args(logits, ids, weights, ref_logps, grad, grad_scale,
-                                           loss_scale, norm, workspace, pairs)
-    ratios = torch.empty(2 * pairs, dtype=torch.float32, device=logits.device)
-    if args.n_tokens == 0:
-        ratios.zero_()
-    _capi.check("token_preference_loss", _capi.lib().token_preference_loss(
-        ctypes.byref(args), lens, pairs, beta, label_smoothing, ratios.data_ptr(),
-        _stream(stream, logits.device)))
-    return PreferenceLoss(stats[:3], ratios, logps, grad)
+    pairs = count // 2
+    lens = struct.pack("@%dq" % count, *seq_lens)
+    args, out, held = _token_args(logits, ids, weights, ref_logps, grad, grad_scale, loss_scale,
+                                  norm, workspace, pairs)
+    n = logits.shape[0]
+    rc = _capi.lib().token_preference_loss(
+        args, lens, pairs, beta, label_smoothing, out.data_ptr() + 4 * (n + 4),
+        _stream(stream, logits.device))
+    if rc:
+        _capi.check("token_preference_loss", rc)
+    return PreferenceLoss(out[:3], out[n + 4:], out[4:n + 4], grad)
 
 
 # ------------------------------------------------------ lists of tensors

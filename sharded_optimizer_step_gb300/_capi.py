@@ -137,9 +137,9 @@ SIGNATURES = {
     "fsdp_state_scaled_rs_avg_adamw_cast": (c_i32, [c_vp, c_i32, c_i32, c_i32, c_i64, c_vp, c_vp,
                                                     c_vp, c_vp, c_vp, c_vp, c_vp, c_vp]),
     "token_loss_workspace_bytes": (c_i64, [c_i64, c_i32]),
-    "token_policy_loss": (c_i32, [ctypes.POINTER(TokenLoss), c_vp, c_vp, c_f32, c_f32, c_f32,
+    "token_policy_loss": (c_i32, [c_vp, c_vp, c_vp, c_f32, c_f32, c_f32,
                                   c_vp]),
-    "token_preference_loss": (c_i32, [ctypes.POINTER(TokenLoss), c_vp, c_i32, c_f32, c_f32,
+    "token_preference_loss": (c_i32, [c_vp, c_vp, c_i32, c_f32, c_f32,
                                       c_vp, c_vp]),
     "tensors_adamw_step": (c_i32, [c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, c_vp, c_i32, c_vp,
                                    c_vp, c_vp]),

@@ -17,7 +17,7 @@ LIB = os.path.join(PKG, "libshardstep.so")
 SOURCES = ["step.cu", "step_tma.cu", "copy.cu", "accum_step.cu", "fsdp2_step.cu", "state.cu",
            "tensors.cu", "token_loss.cu",
            "api.cpp", "tuning_api.cpp", "ckpt.cpp", "ready.cpp"]
-HEADERS = ["common.cuh", "internal.h", "tma.cuh"]
+HEADERS = ["common.cuh", "internal.h", "pairs.cuh", "tma.cuh"]
 ARCH = "103a"
 
 

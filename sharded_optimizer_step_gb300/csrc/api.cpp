@@ -67,6 +67,7 @@ double allreduce_comm_bytes(int32_t nd, double bytes) { return 2.0 * (nd - 1) / 
 
 std::atomic<int> g_fused_path{SHARDSTEP_PATH_AUTO};
 std::atomic<int> g_dependent_launch{1};
+std::atomic<uint64_t> g_wait_limit{2000000000ull};  // of the staged loss kernels' waits, ns
 
 // Whether a launch of n elements goes to a TMA-staged kernel (the caller
 // still checks alignment and the stage size).  PATH_REGISTER: never;
@@ -271,6 +272,8 @@ int ready_fail(int code, const char* fmt, ...) {
 
 int ready_ok() { return ok(); }
 
+unsigned long long tma_wait_limit() { return g_wait_limit.load(std::memory_order_relaxed); }
+
 void record_kernel(const char* fmt, ...) {
     va_list ap;
     va_start(ap, fmt);
@@ -364,6 +367,8 @@ int32_t shardstep_set_tma_stages(int32_t stages) {
 int64_t shardstep_set_tma_wait_ns(int64_t ns) {
     if (ns < 0) return fail(SHARDSTEP_ERR_INVALID, "the wait limit must be >= 0 (got %lld)",
                             static_cast<long long>(ns));
+    g_wait_limit.store(ns == 0 ? 2000000000ull : static_cast<uint64_t>(ns),
+                       std::memory_order_relaxed);
     return set_tma_wait_ns(ns);
 }
 
@@ -385,9 +390,11 @@ int shardstep_check_mean_division(int32_t nd, uint64_t* mismatches, uint32_t* fi
 int shardstep_device_status(uint32_t* status, int32_t clear) {
     if (status == nullptr) return fail(SHARDSTEP_ERR_INVALID, "status is NULL");
     unsigned int s = 0;
+    unsigned int loss = 0;
     cudaError_t e = read_device_status(&s, clear != 0);
+    if (e == cudaSuccess) e = read_loss_status(&loss, clear != 0);
     if (e != cudaSuccess) return cuda_fail(e, "reading the device status word");
-    *status = s;
+    *status = s | loss;
     return ok();
 }
 

@@ -367,10 +367,13 @@ struct PolicyArgs {
 };
 // The sequences of one launch of the preference loss: pairs 2 p, 2 p + 1 are
 // its rows [start[2 p], start[2 p + 1]) and [start[2 p + 1], start[2 p + 2]).
+template <int CAP>
 struct PairTable {
-    int32_t start[2 * kPairsPerLaunch + 1];
+    int32_t start[2 * CAP + 1];
     int32_t pairs;
 };
+constexpr int kPairsSmall = 64;   // 520 bytes of kernel parameter; the other 8 KB
+using PairTableLarge = PairTable<kPairsPerLaunch>;
 struct PreferenceArgs {
     float beta, smoothing;
     float* log_ratios;      // 2 per pair
@@ -388,7 +391,7 @@ bool loss_row_fits(int64_t v, int dtype);
 cudaError_t launch_policy_loss(const TokenArgs& a, const PolicyArgs& p, int dtype, bool staged,
                                cudaStream_t stream);
 cudaError_t launch_preference_forward(const TokenArgs& a, const PreferenceArgs& p,
-                                      const PairTable& t, int dtype, cudaStream_t stream);
+                                      const PairTableLarge& t, int dtype, cudaStream_t stream);
 cudaError_t launch_preference_backward(const TokenArgs& a, const PreferenceArgs& p, int64_t begin,
                                        int64_t end, int dtype, bool staged, cudaStream_t stream);
 

@@ -35,7 +35,6 @@
 #include <atomic>
 
 #include "common.cuh"
-#include "tma.cuh"
 
 namespace shardstep {
 
@@ -57,9 +56,84 @@ constexpr int kConsumerWarps = 16;
 constexpr int kConsumers = kConsumerWarps * 32;   // 512: 4 elements each per tile
 constexpr int kTmaThreads = kConsumers + 32;      // + the producer warp
 constexpr unsigned long long kDefaultWaitNs = 2000000000ull;
+constexpr unsigned long long kDrainNs = 2000000000ull;
 constexpr size_t kBarrierBytes = 2 * kMaxStages * sizeof(uint64_t);
 // Left for the kernels' static shared memory (the step scalars' broadcast).
 constexpr size_t kStaticSmemReserve = 1024;
+
+constexpr unsigned kStatusConsumerTimeout = 1u;
+constexpr unsigned kStatusProducerTimeout = 2u;
+constexpr unsigned kStatusDrainTimeout = 4u;
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ void mbar_init(uint64_t* b, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(b)), "r"(count)
+                 : "memory");
+}
+__device__ __forceinline__ void mbar_expect_tx(uint64_t* b, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(b)),
+                 "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* b) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(b)) : "memory");
+}
+__device__ __forceinline__ bool mbar_test(uint64_t* b, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(smem_addr(b)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+__device__ __forceinline__ unsigned long long now_ns() {
+    unsigned long long t;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+    return t;
+}
+// Non-blocking test of the phase of `parity`.
+__device__ __forceinline__ bool mbar_test_now(uint64_t* b, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(smem_addr(b)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+// Limits below this are a test control: their waits poll without blocking
+// and read the clock after every poll, so that they run out even when each
+// blocking poll would have lasted until the copy landed.
+constexpr unsigned long long kShortWaitNs = 1000000ull;
+// Waits for the phase of `parity` to complete; false after limit_ns.  The
+// usual limit polls with try_wait, which suspends the thread until the
+// phase completes or a hardware time slice ends, and reads the clock every
+// 256 polls.
+__device__ __forceinline__ bool mbar_wait(uint64_t* b, uint32_t parity,
+                                          unsigned long long limit_ns) {
+    const unsigned long long t0 = now_ns();
+    if (limit_ns < kShortWaitNs) {
+        while (!mbar_test_now(b, parity))
+            if (now_ns() - t0 > limit_ns) return false;
+        return true;
+    }
+    for (uint32_t k = 1;; ++k) {
+        if (mbar_test(b, parity)) return true;
+        if ((k & 255u) == 0 && now_ns() - t0 > limit_ns) return false;
+    }
+}
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+            smem_addr(dst)),
+        "l"(src), "r"(bytes), "r"(smem_addr(bar))
+        : "memory");
+}
 
 // 4 consecutive gradient elements of type GT from shared memory, as fp32.
 template <int GT>
@@ -535,8 +609,6 @@ int64_t set_tma_wait_ns(int64_t ns) {
     return static_cast<int64_t>(g_wait_ns.exchange(v));
 }
 
-unsigned long long tma_wait_limit() { return g_wait_ns.load(std::memory_order_relaxed); }
-
 cudaError_t launch_rs_adamw_cast_tma(const PtrTable& tab, int nd, int grad_type, int64_t S,
                                      float* master, float* m, float* v, uint16_t* out,
                                      const AdamScalars& c, const MeanOp& mo,
@@ -577,9 +649,6 @@ cudaError_t launch_nonfinite_check_tma(const PtrTable& tab, int nd, int grad_typ
 
 cudaError_t read_device_status(unsigned int* status, bool clear) {
     cudaError_t e = cudaMemcpyFromSymbol(status, g_device_status, sizeof(unsigned int));
-    unsigned int loss = 0;
-    if (e == cudaSuccess) e = read_loss_status(&loss, clear);
-    *status |= loss;
     if (e != cudaSuccess || !clear) return e;
     const unsigned int zero = 0;
     return cudaMemcpyToSymbol(g_device_status, &zero, sizeof(unsigned int));

@@ -18,6 +18,7 @@
 #include <cuda_fp8.h>
 
 #include "common.cuh"
+#include "pairs.cuh"
 
 namespace shardstep {
 namespace {

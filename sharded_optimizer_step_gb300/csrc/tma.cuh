@@ -1,5 +1,6 @@
-// Device helpers of the TMA-staged kernels: mbarriers with bounded waits and
-// 1-D bulk copies between global and shared memory.
+// Device helpers of the staged loss kernels: mbarriers with bounded waits and
+// 1-D bulk copies between global and shared memory.  (step_tma.cu has its own,
+// which its recorded DRAM counters go with.)
 #pragma once
 
 #include <cuda_runtime.h>

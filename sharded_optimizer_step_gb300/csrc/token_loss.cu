@@ -20,9 +20,12 @@
 // least there is, and the kernel is bound by that traffic.  A row that does
 // not fit (or whose gradient lies at another offset from a 16-byte boundary)
 // takes the plain kernels, which read it again for the gradient (from L2).
+#include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "common.cuh"
+#include "pairs.cuh"
 #include "tma.cuh"
 
 namespace shardstep {
@@ -274,7 +277,8 @@ __device__ __forceinline__ void add_policy(double* sums, const PolicyTerms& t,
 }
 
 // The sequence of the launch that row i belongs to.
-__device__ __forceinline__ int find_sequence(const PairTable& t, int64_t i) {
+template <class Table>
+__device__ __forceinline__ int find_sequence(const Table& t, int64_t i) {
     int lo = 0, hi = 2 * t.pairs - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -292,8 +296,9 @@ __device__ __forceinline__ float sigmoid(float x) {
 
 // A pair's loss and slope from its tokens' terms, added up in a fixed order by
 // one warp.
+template <class Table>
 __device__ __forceinline__ void finish_pair(const TokenArgs& a, const PreferenceArgs& p,
-                                            const PairTable& t, int q) {
+                                            const Table& t, int q) {
     const int lane = threadIdx.x & 31;
     float r[2];
     for (int h = 0; h < 2; ++h) {
@@ -326,8 +331,9 @@ __device__ __forceinline__ void finish_pair(const TokenArgs& a, const Preference
 
 // Each lane has written the words of one more row of its pair q (-1: none): the
 // warp that brings a pair's count to its rows finishes the pair.
+template <class Table>
 __device__ __forceinline__ void rows_done(const TokenArgs& a, const PreferenceArgs& p,
-                                          const PairTable& t, int q) {
+                                          const Table& t, int q) {
     // lanes of one pair count as one, by the pair's lowest lane
     const unsigned same = __match_any_sync(kFull, q);
     const bool leads = q >= 0 && __ffs(same) - 1 == static_cast<int>(threadIdx.x & 31);
@@ -351,16 +357,18 @@ __device__ __forceinline__ void rows_done(const TokenArgs& a, const PreferenceAr
 }
 
 // Pairs without a token, which no row finishes.
+template <class Table>
 __device__ __forceinline__ void empty_pairs(const TokenArgs& a, const PreferenceArgs& p,
-                                            const PairTable& t) {
+                                            const Table& t) {
     for (int q = blockIdx.x; q < t.pairs; q += gridDim.x)
         if (t.start[2 * q + 2] == t.start[2 * q]) finish_pair(a, p, t, q);
 }
 
 // The pairs' losses, added up by the last block in pair order per lane.
 // Every thread of the block calls it.
+template <class Table>
 __device__ __forceinline__ void preference_stats(const TokenArgs& a, const PreferenceArgs& p,
-                                                 const PairTable& t) {
+                                                 const Table& t) {
     __shared__ bool last;
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -1014,11 +1022,16 @@ struct Parts {
     unsigned mask, next; // live rows of the batch not yet taken; of the next batch
 };
 
-template <int GT, int W, bool PREF>
+// The policy loss's stand-in for a table of pairs.
+struct NoTable {
+    int32_t pairs;
+};
+template <int GT, int W, class Table>
 __global__ void __launch_bounds__(kStreamThreads, 1)
     stream_forward(const TokenArgs a, const PolicyArgs pol, const PreferenceArgs p,
-                   const __grid_constant__ PairTable t, int64_t begin, int64_t end,
+                   const __grid_constant__ Table t, int64_t begin, int64_t end,
                    unsigned long long wait_ns) {
+    constexpr bool PREF = !std::is_same<Table, NoTable>::value;
     extern __shared__ __align__(128) uint8_t smem[];
     constexpr int kRowTeams = kStreamWarps / W;
     __shared__ TeamShared<32 * W> sh[kRowTeams];
@@ -1079,7 +1092,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
 
     float norm = 1.0f;
     if (!PREF) norm = weight_sum(a, Team<kStreamThreads>{0, tid, &block_sh});
-    if (PREF && warp == 0) empty_pairs(a, p, t);
+    if constexpr (PREF) {
+        if (warp == 0) empty_pairs(a, p, t);
+    }
     double sums[4] = {0.0, 0.0, 0.0, 0.0};
     int slot = 0, taken = 0, turn = 0;
     uint32_t parity = 0;
@@ -1171,7 +1186,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
                 const PolicyTerms pt = policy_terms(lp, mine.f[0], mine.f[1], mine.f[2], pol);
                 add_policy(sums, pt, pol, __fdiv_rn(mine.w, norm));
             }
-            if (PREF) {
+            if constexpr (PREF) {
                 int q = -1;
                 if (held) {
                     const int seq = find_sequence(t, i);
@@ -1200,7 +1215,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
             atomicOr(&g_loss_status,
                      kStatusConsumerTimeout | (drained ? 0u : kStatusDrainTimeout));
     }
-    if (PREF) {
+    if constexpr (PREF) {
         preference_stats(a, p, t);
         return;
     }
@@ -1252,14 +1267,14 @@ cudaError_t go_staged(const TokenArgs& a, const PolicyArgs& pol, const Preferenc
                         dim3(kStagedThreads), kStagedSmem, s, a, pol, p, begin, end,
                         tma_wait_limit());
 }
-template <int GT, int W, bool PREF>
+template <int GT, int W, class Table>
 cudaError_t go_stream_w(const TokenArgs& a, const PolicyArgs& pol, const PreferenceArgs& p,
-                        const PairTable& t, int64_t begin, int64_t end, cudaStream_t s) {
+                        const Table& t, int64_t begin, int64_t end, cudaStream_t s) {
     static std::atomic<int> applied[256];
-    const cudaError_t e = opt_in(stream_forward<GT, W, PREF>, kStreamSmem, applied);
+    const cudaError_t e = opt_in(stream_forward<GT, W, Table>, kStreamSmem, applied);
     if (e != cudaSuccess) return e;
     constexpr int teams = kStreamWarps / W;
-    return launch_after(stream_forward<GT, W, PREF>,
+    return launch_after(stream_forward<GT, W, Table>,
                         dim3(row_blocks((end - begin + teams - 1) / teams, 1)),
                         dim3(kStreamThreads), kStreamSmem, s, a, pol, p, t, begin, end,
                         tma_wait_limit());
@@ -1268,18 +1283,28 @@ cudaError_t go_stream_w(const TokenArgs& a, const PolicyArgs& pol, const Prefere
 // against 39.0 with 16), 16 below (152 rows: 13.3 us against 15.6; 760 rows: 23.3
 // against 23.6).  One warp per row was no faster anywhere (3800 rows: 56.3 us
 // against 52.9).
-template <int GT, bool PREF>
+template <int GT, class Table>
 cudaError_t go_stream(const TokenArgs& a, const PolicyArgs& pol, const PreferenceArgs& p,
-                      const PairTable& t, int64_t begin, int64_t end, cudaStream_t s) {
+                      const Table& t, int64_t begin, int64_t end, cudaStream_t s) {
     if (end - begin >= 8 * static_cast<int64_t>(device_sms()))
-        return go_stream_w<GT, 4, PREF>(a, pol, p, t, begin, end, s);
-    return go_stream_w<GT, 16, PREF>(a, pol, p, t, begin, end, s);
+        return go_stream_w<GT, 4>(a, pol, p, t, begin, end, s);
+    return go_stream_w<GT, 16>(a, pol, p, t, begin, end, s);
+}
+template <int GT>
+cudaError_t go_forward(const TokenArgs& a, const PreferenceArgs& p, const PairTableLarge& t,
+                       cudaStream_t s) {
+    const int64_t begin = t.start[0], end = t.start[2 * t.pairs];
+    if (t.pairs > kPairsSmall) return go_stream<GT>(a, PolicyArgs{}, p, t, begin, end, s);
+    PairTable<kPairsSmall> small;
+    std::copy(t.start, t.start + 2 * t.pairs + 1, small.start);
+    small.pairs = t.pairs;
+    return go_stream<GT>(a, PolicyArgs{}, p, small, begin, end, s);
 }
 
 template <int GT>
 cudaError_t go_policy(const TokenArgs& a, const PolicyArgs& p, bool staged, cudaStream_t s) {
     if (a.grad == nullptr)
-        return go_stream<GT, false>(a, p, PreferenceArgs{}, PairTable{}, 0, a.n, s);
+        return go_stream<GT>(a, p, PreferenceArgs{}, NoTable{0}, 0, a.n, s);
     if (staged) return go_staged<GT, Pass::kPolicy>(a, p, PreferenceArgs{}, 0, a.n, s);
     return launch_after(policy_rows<GT>, dim3(row_blocks(a.n, 2)), dim3(kRowThreads), 0, s, a, p);
 }
@@ -1314,13 +1339,10 @@ cudaError_t launch_policy_loss(const TokenArgs& a, const PolicyArgs& p, int dtyp
     return e;
 }
 cudaError_t launch_preference_forward(const TokenArgs& a, const PreferenceArgs& p,
-                                      const PairTable& t, int dtype, cudaStream_t stream) {
-    const int64_t begin = t.start[0], end = t.start[2 * t.pairs];
-    const PolicyArgs none{};
-    const cudaError_t e =
-        dtype == kGradF32   ? go_stream<kGradF32, true>(a, none, p, t, begin, end, stream)
-        : dtype == kGradF16 ? go_stream<kGradF16, true>(a, none, p, t, begin, end, stream)
-                            : go_stream<kGradBF16, true>(a, none, p, t, begin, end, stream);
+                                      const PairTableLarge& t, int dtype, cudaStream_t stream) {
+    const cudaError_t e = dtype == kGradF32   ? go_forward<kGradF32>(a, p, t, stream)
+                          : dtype == kGradF16 ? go_forward<kGradF16>(a, p, t, stream)
+                                              : go_forward<kGradBF16>(a, p, t, stream);
     note_launch();
     return e;
 }

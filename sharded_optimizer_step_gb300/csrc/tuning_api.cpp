@@ -533,7 +533,7 @@ int token_preference_loss(const shardstep_token_loss_t* args, const int64_t* seq
                      0};
     const bool staged = k.grad != nullptr && staged_rows(args);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    std::unique_ptr<PairTable> t(new PairTable);
+    std::unique_ptr<PairTableLarge> t(new PairTableLarge);
     int32_t row = 0;
     for (int32_t q = 0; q < n_pairs; q += kPairsPerLaunch) {
         t->pairs = std::min(kPairsPerLaunch, n_pairs - q);
