@@ -388,10 +388,15 @@ struct PreferenceArgs {
 bool loss_row_fits(int64_t v, int dtype);
 // staged: rows go through shared memory (they fit, and the gradient's rows,
 // if any, start at the logits' rows' offsets from 16-byte boundaries).
+// A call's rows go in launches of at most this many (loss_rows_per_launch), so
+// that a block's share of them fits its shared memory.
+constexpr int kShareRows = 1024;   // per SM
+int64_t loss_rows_per_launch();
 cudaError_t launch_policy_loss(const TokenArgs& a, const PolicyArgs& p, int dtype, bool staged,
-                               cudaStream_t stream);
+                               int64_t begin, int64_t end, cudaStream_t stream);
 cudaError_t launch_preference_forward(const TokenArgs& a, const PreferenceArgs& p,
-                                      const PairTableLarge& t, int dtype, cudaStream_t stream);
+                                      const PairTableLarge& t, int64_t begin, int64_t end,
+                                      int dtype, cudaStream_t stream);
 cudaError_t launch_preference_backward(const TokenArgs& a, const PreferenceArgs& p, int64_t begin,
                                        int64_t end, int dtype, bool staged, cudaStream_t stream);
 

@@ -510,11 +510,10 @@ __global__ void __launch_bounds__(kListThreads)
 
 // ------------------------------------------------------------- the norm
 
-// Sum of a block's doubles in a fixed tree order; the result in thread 0.
+// Sum of the first lanes' doubles of a block's warps in a fixed order; the
+// result in thread 0.
 __device__ __forceinline__ double block_sum(double x) {
     __shared__ double part[kListThreads / 32];
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) x += __shfl_down_sync(0xFFFFFFFFu, x, d);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = x;
     __syncthreads();
     double s = 0.0;
@@ -579,14 +578,13 @@ __global__ void __launch_bounds__(kListThreads, 4)
             }
         }
     }
-    double sum = 0.0;
+    // the 8 sums and the warp's in fp32, pairwise; double from there on (an SM has
+    // few units for it)
+    const float2 f = floats(add2(add2(acc[0], acc[1]), add2(acc[2], acc[3])));
+    float own = __fadd_rn(f.x, f.y);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const float2 f = floats(acc[e]);
-        sum += static_cast<double>(f.x);
-        sum += static_cast<double>(f.y);
-    }
-    sum = block_sum(sum);
+    for (int d = 16; d > 0; d >>= 1) own = __fadd_rn(own, __shfl_xor_sync(0xFFFFFFFFu, own, d));
+    double sum = block_sum((threadIdx.x & 31) == 0 ? static_cast<double>(own) : 0.0);
     __shared__ bool last;
     if (threadIdx.x == 0) {
         double* slot = a.ws->partial + blockIdx.x;
@@ -601,6 +599,8 @@ __global__ void __launch_bounds__(kListThreads, 4)
     double total = 0.0;
     for (uint32_t b = threadIdx.x; b < gridDim.x; b += kListThreads)
         total += __ldcg(a.ws->partial + b);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, d);
     total = block_sum(total);
     if (threadIdx.x == 0) {
         const float scale = a.scale != nullptr ? __ldg(a.scale) : 1.0f;

@@ -100,10 +100,6 @@ template <int N>
 __device__ __forceinline__ void bulk_wait_read() {
     asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
-// Until all of this thread's bulk stores are complete.
-__device__ __forceinline__ void bulk_wait_all() {
-    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-}
 // Orders this thread's writes to shared memory before later bulk copies that
 // read it (issued after a barrier by another thread).
 __device__ __forceinline__ void fence_async() {

@@ -73,11 +73,46 @@ __device__ __forceinline__ const char* row_of(const void* x, int64_t i, int64_t 
     return static_cast<const char*>(x) + i * stride * elem_bytes<GT>();
 }
 
+// A sum held as two floats, each addition exact up to the low one's rounding
+// (Knuth's two-sum): as good as a double here, without the double-precision
+// units, of which an SM has so few that a block's worth of additions took a
+// microsecond or two.
+struct Sum2 {
+    float hi, lo;
+    __device__ __forceinline__ void add(float x) {
+        const float s = __fadd_rn(hi, x);
+        const float b = __fsub_rn(s, hi);
+        const float e = __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(x, b));
+        hi = s;
+        lo = __fadd_rn(lo, e);
+    }
+    __device__ __forceinline__ void add(Sum2 x) {
+        add(x.hi);
+        lo = __fadd_rn(lo, x.lo);
+    }
+    // inf and NaN are the high part's
+    __device__ __forceinline__ float value() const {
+        return fabsf(hi) <= 0x1.fffffep127f ? __fadd_rn(hi, lo) : hi;
+    }
+    __device__ __forceinline__ double wide() const {
+        return fabsf(hi) <= 0x1.fffffep127f
+                   ? __dadd_rn(static_cast<double>(hi), static_cast<double>(lo))
+                   : static_cast<double>(hi);
+    }
+};
+// All lanes get the warp's sum, in a fixed order.
+__device__ __forceinline__ Sum2 warp_sum(Sum2 x) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        x.add(Sum2{__shfl_xor_sync(kFull, x.hi, d), __shfl_xor_sync(kFull, x.lo, d)});
+    return x;
+}
+
 // The T threads that work on one row, with a named barrier of their own.
 template <int T>
 struct TeamShared {
     float part[2][T / 32];
-    double dpart[T / 32];
+    Sum2 wide[T / 32];
 };
 template <int T>
 struct Team {
@@ -129,16 +164,15 @@ struct Team {
         sync();
         return x;
     }
-    __device__ __forceinline__ double sum(double x) const {
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(kFull, x, d);
+    __device__ __forceinline__ float sum(Sum2 x) const {
+        x = warp_sum(x);
         sync();
-        if ((tid & 31) == 0) sh->dpart[tid >> 5] = x;
+        if ((tid & 31) == 0) sh->wide[tid >> 5] = x;
         sync();
-        x = 0.0;
-        for (int w = 0; w < T / 32; ++w) x += sh->dpart[w];
+        x = Sum2{0.0f, 0.0f};
+        for (int w = 0; w < T / 32; ++w) x.add(sh->wide[w]);
         sync();
-        return x;
+        return x.value();
     }
 };
 
@@ -234,46 +268,58 @@ template <int T>
 __device__ __forceinline__ float weight_sum(const TokenArgs& a, const Team<T>& team) {
     if (a.norm != 0.0f) return a.norm;
     if (a.w == nullptr) return static_cast<float>(a.n);
-    double s = 0.0;
+    Sum2 s{0.0f, 0.0f};
 #pragma unroll 8
-    for (int64_t i = team.tid; i < a.n; i += T) s += static_cast<double>(a.w[i]);
-    return __double2float_rn(team.sum(s));
+    for (int64_t i = team.tid; i < a.n; i += T) s.add(a.w[i]);
+    return team.sum(s);
+}
+// The same where the block has gone over the launch's weights already: over all
+// of them unless the call takes several launches.
+template <int T>
+__device__ __forceinline__ float weight_sum(const TokenArgs& a, const Team<T>& team, int64_t rows,
+                                            float weight) {
+    if (a.norm == 0.0f && a.w != nullptr && rows == a.n) return weight;
+    return weight_sum(a, team);
 }
 
-// The blocks' sums (thread 0's t) added up by the block that arrives last, in a
-// fixed order; true there, with the sums in the workspace's total.  Every
-// thread of the block calls it.
-__device__ __forceinline__ bool join_blocks(LossWork* ws, const double* t) {
-    __shared__ bool last;
-    if (threadIdx.x == 0) {
-        for (int k = 0; k < 4; ++k) ws->partial[blockIdx.x][k] = t[k];
+// The blocks' sums (lane k's s is the block's k-th) added up by the block that
+// arrives last, in a fixed order, and carried to the call's next launch or
+// written as its statistics; by one warp.
+__device__ __forceinline__ void join_sums(const TokenArgs& a, double s, bool first, bool last) {
+    const int lane = threadIdx.x & 31;
+    LossWork* ws = a.ws;
+    if (lane < 4) ws->partial[blockIdx.x][lane] = s;
+    __syncwarp();
+    unsigned mine = 0;
+    if (lane == 0) {
         __threadfence();
-        last = atomicInc(&ws->arrived, gridDim.x - 1) == gridDim.x - 1;
+        mine = atomicInc(&ws->arrived, gridDim.x - 1) == gridDim.x - 1;
+        __threadfence();
     }
-    __syncthreads();
-    if (!last) return false;
-    __threadfence();
-    const unsigned k = threadIdx.x >> 5;      // a warp per sum
-    if (k < 4) {
-        double s = 0.0;
-#pragma unroll 8
-        for (unsigned b = threadIdx.x & 31; b < gridDim.x; b += 32)
-            s += __ldcg(&ws->partial[b][k]);
+    if (!__shfl_sync(kFull, mine, 0)) return;
+    __syncwarp();
+    double t[4] = {0.0, 0.0, 0.0, 0.0};
+    for (unsigned b = lane; b < gridDim.x; b += 32)
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
-        if ((threadIdx.x & 31) == 0) ws->total[k] = s;
+        for (int k = 0; k < 4; ++k) t[k] += __ldcg(&ws->partial[b][k]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) t[k] += __shfl_xor_sync(kFull, t[k], d);
+        if (lane == 0) {
+            if (!first) t[k] += ws->total[k];
+            ws->total[k] = t[k];
+            if (last) a.stats[k] = __double2float_rn(t[k]);
+        }
     }
-    __syncthreads();
-    return true;
 }
 
-__device__ __forceinline__ void add_policy(double* sums, const PolicyTerms& t,
-                                           const PolicyArgs& p, float k) {
-    const double kd = k;
-    sums[0] += kd * __fadd_rn(t.policy, __fmul_rn(p.kl, t.kl));
-    sums[1] += kd * t.policy;
-    sums[2] += kd * t.kl;
-    sums[3] += kd * t.clipped;
+__device__ __forceinline__ void add_policy(Sum2* sums, const PolicyTerms& t, const PolicyArgs& p,
+                                           float k) {
+    sums[0].add(__fmul_rn(k, __fadd_rn(t.policy, __fmul_rn(p.kl, t.kl))));
+    sums[1].add(__fmul_rn(k, t.policy));
+    sums[2].add(__fmul_rn(k, t.kl));
+    sums[3].add(__fmul_rn(k, t.clipped));
 }
 
 // The sequence of the launch that row i belongs to.
@@ -302,18 +348,16 @@ __device__ __forceinline__ void finish_pair(const TokenArgs& a, const Preference
     const int lane = threadIdx.x & 31;
     float r[2];
     for (int h = 0; h < 2; ++h) {
-        double s = 0.0;
+        Sum2 s{0.0f, 0.0f};
         const int end = t.start[2 * q + h + 1];
         for (int i = t.start[2 * q + h] + lane; i < end; i += 8 * 32) {
             float x[8];          // in flight together
 #pragma unroll
             for (int k = 0; k < 8; ++k) x[k] = i + 32 * k < end ? __ldcg(p.term + i + 32 * k) : 0.0f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) s += static_cast<double>(x[k]);
+            for (int k = 0; k < 8; ++k) s.add(x[k]);
         }
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
-        r[h] = __double2float_rn(s);
+        r[h] = warp_sum(s).value();
     }
     if (lane != 0) return;
     const float h = __fmul_rn(p.beta, __fsub_rn(r[0], r[1]));
@@ -329,30 +373,33 @@ __device__ __forceinline__ void finish_pair(const TokenArgs& a, const Preference
     a.ws->pair_loss[q][2] = h > 0.0f ? 1.0 : 0.0;
 }
 
+// The pairs that a block's rows completed, to be finished at its end by all of
+// its warps: the last rows of a launch complete most pairs at once, and one warp
+// would take them one after the other (16 pairs of 500 tokens: 40 us).
+struct ReadyPairs {
+    int n;
+    int pair[kPairsPerLaunch];
+};
 // Each lane has written the words of one more row of its pair q (-1: none): the
-// warp that brings a pair's count to its rows finishes the pair.
+// lane that brings a pair's count to its rows notes the pair.
 template <class Table>
-__device__ __forceinline__ void rows_done(const TokenArgs& a, const PreferenceArgs& p,
-                                          const Table& t, int q) {
+__device__ __forceinline__ void rows_done(const TokenArgs& a, const Table& t, int q,
+                                          ReadyPairs* ready) {
     // lanes of one pair count as one, by the pair's lowest lane
     const unsigned same = __match_any_sync(kFull, q);
     const bool leads = q >= 0 && __ffs(same) - 1 == static_cast<int>(threadIdx.x & 31);
-    bool last = false;
     __syncwarp();
-    if (leads) {
-        unsigned before;
-        const unsigned rows = __popc(same);
-        __threadfence();
-        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;"
-                     : "=r"(before)
-                     : "l"(&a.ws->rows_done[q]), "r"(rows)
-                     : "memory");
-        last = before + rows == static_cast<unsigned>(t.start[2 * q + 2] - t.start[2 * q]);
-        if (last) a.ws->rows_done[q] = 0;
-    }
-    for (unsigned done = __ballot_sync(kFull, last); done != 0; done &= done - 1) {
-        __syncwarp();
-        finish_pair(a, p, t, __shfl_sync(kFull, q, __ffs(done) - 1));
+    if (!leads) return;
+    unsigned before;
+    const unsigned rows = __popc(same);
+    __threadfence();
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;"
+                 : "=r"(before)
+                 : "l"(&a.ws->rows_done[q]), "r"(rows)
+                 : "memory");
+    if (before + rows == static_cast<unsigned>(t.start[2 * q + 2] - t.start[2 * q])) {
+        a.ws->rows_done[q] = 0;
+        ready->pair[atomicAdd(&ready->n, 1)] = q;
     }
 }
 
@@ -440,13 +487,15 @@ __device__ __forceinline__ void plain_zero(char* g, int64_t v) {
 
 template <int GT>
 __global__ void __launch_bounds__(kRowThreads)
-    policy_rows(const TokenArgs a, const PolicyArgs p) {
+    policy_rows(const TokenArgs a, const PolicyArgs p, int64_t begin, int64_t end,
+                bool first_launch, bool last_launch) {
     __shared__ TeamShared<kRowThreads> sh;
     const Team<kRowThreads> team{1, static_cast<int>(threadIdx.x), &sh};
     pdl_enter();
     const float norm = weight_sum(a, team), scale = out_scale(a);
-    double sums[4] = {0.0, 0.0, 0.0, 0.0};
-    for (int64_t i = blockIdx.x; i < a.n; i += gridDim.x) {
+    Sum2 sums[4] = {};
+    __shared__ double block_sums[4];
+    for (int64_t i = begin + blockIdx.x; i < end; i += gridDim.x) {
         const char* x = row_of<GT>(a.x, i, a.x_stride);
         char* g = const_cast<char*>(row_of<GT>(a.grad, i, a.g_stride));
         const float w = token_weight(a, i);
@@ -469,8 +518,11 @@ __global__ void __launch_bounds__(kRowThreads)
         }
         plain_grad<GT>(x, g, a.v, y, r, s, __fmul_rn(__fmul_rn(t.slope, k), scale));
     }
-    if (join_blocks(a.ws, sums) && threadIdx.x < 4)
-        a.stats[threadIdx.x] = __double2float_rn(a.ws->total[threadIdx.x]);
+    if (threadIdx.x == 0)
+        for (int k = 0; k < 4; ++k) block_sums[k] = sums[k].wide();
+    __syncwarp();
+    if (threadIdx.x < 32)
+        join_sums(a, threadIdx.x < 4 ? block_sums[threadIdx.x] : 0.0, first_launch, last_launch);
 }
 
 template <int GT>
@@ -492,12 +544,125 @@ __global__ void __launch_bounds__(kRowThreads)
     }
 }
 
+// ------------------------------------------------------- shares of the rows
+
+// The rows of a launch are dealt out to `units` (blocks, or teams of warps): the
+// live rows in turn, and the rows of weight 0, which cost less or nothing, in
+// turn after them.  Dealt out by their index alone, the 30% masked rows of 4096
+// left some blocks with a quarter more live rows than others.  Every block finds
+// its own share by going over all weights in the same order; the host keeps a
+// launch below kShareRows rows per SM so that the shares fit shared memory.
+struct Share {
+    const uint32_t* live;     // row - begin; null (no weights): first + j * units
+    const uint32_t* dead;
+    int n_live, n_dead;
+    int64_t begin, first, units;
+
+    __device__ __forceinline__ int64_t row(int j) const {
+        return live != nullptr ? begin + live[j] : first + j * units;
+    }
+    __device__ __forceinline__ int64_t dead_row(int j) const { return begin + dead[j]; }
+};
+// How many of n things dealt out in turn unit u gets.
+__device__ __forceinline__ int dealt(int64_t n, int64_t u, int64_t units) {
+    return static_cast<int>(n > u ? (n - u + units - 1) / units : 0);
+}
+// What a block finds on its way over the weights.
+struct Dealt {
+    int n_live, n_dead;       // of the launch
+    float weight;             // the sum of the launch's weights
+};
+// Fills the lists of the block's `mine` units (the first of them: u0), each of
+// up to kShareRows / mine rows; every thread of the block calls it.  A thread
+// takes 8 consecutive rows at a time.
+template <int THREADS>
+__device__ __forceinline__ Dealt deal_rows(const TokenArgs& a, int64_t begin, int64_t end,
+                                           unsigned u0, unsigned mine, unsigned units,
+                                           uint32_t* live, uint32_t* dead) {
+    constexpr int kWarps = THREADS / 32, kRows = 8;
+    __shared__ int counts[2][kWarps];
+    __shared__ Sum2 sums[kWarps];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const unsigned each = kShareRows / mine;
+    unsigned live_before = 0;
+    Sum2 weight{0.0f, 0.0f};
+    int turn = 0;
+    for (int64_t base = begin; base < end; base += THREADS * kRows, turn ^= 1) {
+        const int64_t i0 = base + kRows * tid;
+        float w[kRows];
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) w[k] = i0 + k < end ? a.w[i0 + k] : 0.0f;
+        unsigned own = 0;
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+            own += w[k] != 0.0f;
+            weight.add(w[k]);
+        }
+        unsigned upto = own;                 // live rows up to this thread's last
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const unsigned x = __shfl_up_sync(kFull, upto, d);
+            if (lane >= d) upto += x;
+        }
+        if (lane == 31) counts[turn][warp] = upto;
+        __syncthreads();
+        unsigned below = 0, total = 0;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) {
+            const unsigned c = counts[turn][k];
+            below += k < warp ? c : 0;
+            total += c;
+        }
+        const unsigned row0 = static_cast<unsigned>(i0 - begin);
+        const unsigned rank = live_before + below + upto - own, other = row0 - rank;
+        unsigned lu = rank % units, lq = rank / units, du = other % units, dq = other / units;
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+            if (i0 + k >= end) break;
+            if (w[k] != 0.0f) {
+                if (lu - u0 < mine) live[(lu - u0) * each + lq] = row0 + k;
+                if (++lu == units) {
+                    lu = 0;
+                    ++lq;
+                }
+            } else {
+                const unsigned u = units - 1 - du - u0;
+                if (u < mine) dead[u * each + dq] = row0 + k;
+                if (++du == units) {
+                    du = 0;
+                    ++dq;
+                }
+            }
+        }
+        live_before += total;
+    }
+    weight = warp_sum(weight);
+    if (lane == 0) sums[warp] = weight;
+    __syncthreads();
+    weight = lane < kWarps ? sums[lane] : Sum2{0.0f, 0.0f};
+    return Dealt{static_cast<int>(live_before),
+                 static_cast<int>(end - begin) - static_cast<int>(live_before),
+                 warp_sum(weight).value()};
+}
+// Unit u's share.  The rows of weight 0 are dealt out from the last unit down,
+// so that the units with a live row more get one of them less.
+__device__ __forceinline__ Share share_of(const TokenArgs& a, int64_t begin, int64_t end,
+                                          int64_t u, int64_t units, const Dealt& found,
+                                          const uint32_t* live, const uint32_t* dead) {
+    if (a.w == nullptr)
+        return Share{nullptr, nullptr, dealt(end - begin, u, units), 0, begin, begin + u,
+                     units};
+    return Share{live,  dead,  dealt(found.n_live, u, units),
+                 dealt(found.n_dead, units - 1 - u, units), begin, begin, units};
+}
+
 // ------------------------------------------------------ the staged kernels
 
 constexpr int kChunk = 16384;                 // bytes of a chunk, of a slot
 constexpr int kSlots = 13;                    // slots of the ring: 208 KB
 constexpr int kZeroBytes = 4096;
-constexpr size_t kStagedSmem = static_cast<size_t>(kSlots) * kChunk + kZeroBytes;
+constexpr size_t kStagedSmem =
+    static_cast<size_t>(kSlots) * kChunk + kZeroBytes + 8 * kShareRows;
 
 enum class Pass { kPolicy, kPreferenceBackward };
 
@@ -646,18 +811,15 @@ struct RowParam {
 };
 constexpr int kBatch = 32;            // rows whose parameters are fetched at once
 
-// The parameters of row i, whose id's logit is wanted where `logit` is set; the
-// caller's lanes take a row each, so the dependent loads of 32 rows overlap.
+// The parameters of live row i; the caller's lanes take a row each, so the
+// dependent loads of 32 rows overlap.
 template <int GT>
 __device__ __forceinline__ RowParam policy_param(const TokenArgs& a, const PolicyArgs& pol,
                                                  int64_t i) {
-    RowParam q{token_weight(a, i), -1, 0.0f, {pol.old[i], pol.adv[i], 0.0f}};
+    const int64_t y = token_id(a, i);
+    RowParam q{token_weight(a, i), static_cast<int32_t>(y), NAN, {pol.old[i], pol.adv[i], 0.0f}};
     if (pol.kl != 0.0f) q.f[2] = a.ref[i];
-    if (q.w != 0.0f) {
-        const int64_t y = token_id(a, i);
-        q.y = static_cast<int32_t>(y);
-        q.xy = y >= 0 ? load1<GT>(row_of<GT>(a.x, i, a.x_stride), y) : NAN;
-    }
+    if (y >= 0) q.xy = load1<GT>(row_of<GT>(a.x, i, a.x_stride), y);
     return q;
 }
 
@@ -681,43 +843,67 @@ __device__ __forceinline__ bool wait_chunk(uint64_t* full, const unsigned* issue
     return mbar_wait(&full[r.slot], r.parity, limit_ns);
 }
 
-// One block per SM takes rows blockIdx.x, + gridDim.x, ... of the launch.
+// A row of weight 0 of the gradient, by one warp, from `zeros`.
+template <int GT>
+__device__ __forceinline__ void zero_row(const TokenArgs& a, int64_t i, const uint8_t* zeros) {
+    const int lane = threadIdx.x & 31;
+    char* g = const_cast<char*>(row_of<GT>(a.grad, i, a.g_stride));
+    const RowBytes b = row_bytes<GT>(g, a.v);
+    char* dst = const_cast<char*>(b.body_at);
+    if (lane < b.head) store1<GT>(g, lane, 0.0f);
+    if (lane < b.tail) store1<GT>(dst + b.body, lane, 0.0f);
+    if (lane == 0) {
+        for (uint32_t o = 0; o < b.body; o += kZeroBytes)
+            bulk_store(dst + o, zeros, b.body - o < kZeroBytes ? b.body - o : kZeroBytes);
+        bulk_commit();
+        bulk_wait_read<1>();
+    }
+}
+
+// One block per SM takes its share of the launch's rows.
 //   2 teams of 8 computing warps, live rows in turn: sum a row's chunks as they
 //     land, join, form the row's terms, then overwrite the chunks with the
 //     gradient; the up to 15 + 7 elements outside whole vectors stay in the
 //     registers of the team's first warp.  While one team joins its sum and
 //     forms its terms the other has the arithmetic units;
 //   loading warp: per live row, its body's chunks into free slots;
-//   storing warp: stores each finished chunk and frees its slot; rows of weight
-//     0 are stored from a zeroed piece of shared memory;
+//   storing warp: stores each finished chunk and frees its slot;
+//   zero warp: the rows of weight 0, from a zeroed piece of shared memory;
 //   parameter warp: the rows' weights, ids, logits of the ids and so on, 32
-//     rows ahead at a time.
+//     rows ahead at a time; at the end it joins the blocks' sums, while the last
+//     rows are still being stored.
 // Every wait
 // is bounded: one that runs out sets a status bit, the block leaves at the end
 // of the row, and its copies in flight are waited for first.
 constexpr int kTeams = 2;
 constexpr int kTeamThreads = 256, kTeamWarps = kTeamThreads / 32;
 constexpr int kWorkWarps = kTeams * kTeamWarps;
-constexpr int kLoadWarp = kWorkWarps, kStoreWarp = kWorkWarps + 1, kParamWarp = kWorkWarps + 2;
-constexpr int kStagedThreads = 32 * (kWorkWarps + 3);
+constexpr int kLoadWarp = kWorkWarps, kStoreWarp = kWorkWarps + 1, kParamWarp = kWorkWarps + 2,
+              kZeroWarp = kWorkWarps + 3;
+constexpr int kStagedThreads = 32 * (kWorkWarps + 4);
 
 template <int GT, Pass M>
 __global__ void __launch_bounds__(kStagedThreads, 1)
     staged_rows(const TokenArgs a, const PolicyArgs pol, const PreferenceArgs p,
-                int64_t begin, int64_t end, unsigned long long wait_ns) {
+                int64_t begin, int64_t end, bool first_launch, bool last_launch,
+                unsigned long long wait_ns) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ TeamShared<kTeamThreads> sh[kTeams];
     __shared__ double team_sums[kTeams][4];
     __shared__ uint64_t full[kSlots], done[kSlots], empty[kSlots];
     __shared__ unsigned issued_chunks;    // by the loading warp so far
-    __shared__ uint64_t param_full[2], param_empty[2];
+    __shared__ unsigned stored_rows;      // by the storing warp so far
+    __shared__ uint64_t param_full[2], param_empty[2], sums_full;
     __shared__ RowParam params[2][kBatch];
     uint8_t* zeros = smem + static_cast<size_t>(kSlots) * kChunk;
+    uint32_t* live_list = reinterpret_cast<uint32_t*>(zeros + kZeroBytes);
+    uint32_t* dead_list = live_list + kShareRows;
     constexpr int es = elem_bytes<GT>();
     constexpr bool kPolicy = M == Pass::kPolicy;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         issued_chunks = 0;
+        stored_rows = 0;
         for (int s = 0; s < kSlots; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&done[s], kTeamWarps);
@@ -727,6 +913,7 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
             mbar_init(&param_full[s], 1);
             mbar_init(&param_empty[s], kWorkWarps);
         }
+        mbar_init(&sums_full, kTeams);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     for (int k = tid; k < kZeroBytes / 4; k += kStagedThreads)
@@ -734,47 +921,35 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
     fence_async();
     __syncthreads();
     pdl_enter();
-    double sums[4] = {0.0, 0.0, 0.0, 0.0};
-    const int64_t first = begin + blockIdx.x;
-    const int64_t rows = first < end ? (end - first + gridDim.x - 1) / gridDim.x : 0;
-    const auto row_at = [&](int64_t j) { return first + j * gridDim.x; };
-    // which of the 32 rows from j on are live, one weight per lane
-    const auto live_mask = [&](int64_t j) {
-        const bool live = j + lane < rows && token_weight(a, row_at(j + lane)) != 0.0f;
-        return __ballot_sync(kFull, live);
-    };
+    Dealt found{0, 0, 0.0f};
+    if (a.w != nullptr)
+        found = deal_rows<kStagedThreads>(a, begin, end, blockIdx.x, 1, gridDim.x, live_list,
+                                          dead_list);
+    const Share share =
+        share_of(a, begin, end, blockIdx.x, gridDim.x, found, live_list, dead_list);
+    const int rows = share.n_live;
 
     if (warp == kLoadWarp) {
-        Ring r{0, 0, 0};
-        int64_t issued = 0;
-        bool ok = true;
-        unsigned next = live_mask(0);
-        for (int64_t j = 0; j < rows && ok; j += 32) {
-            unsigned live = next;
-            next = live_mask(j + 32);
-            if (lane == 0) {
-                for (; live != 0 && ok; live &= live - 1) {
-                    const int64_t i = row_at(j + __ffs(live) - 1);
-                    const RowBytes b = row_bytes<GT>(row_of<GT>(a.x, i, a.x_stride), a.v);
-                    for (uint32_t o = 0; o < b.body; o += kChunk) {
-                        if (issued >= kSlots &&
-                            !mbar_wait(&empty[r.slot], r.parity ^ 1u, wait_ns)) {
-                            ok = false;
-                            break;
-                        }
-                        const uint32_t n = b.body - o < kChunk ? b.body - o : kChunk;
-                        mbar_expect_tx(&full[r.slot], n);
-                        bulk_load(smem + static_cast<size_t>(r.slot) * kChunk, b.body_at + o, n,
-                                  &full[r.slot]);
-                        r.next();
-                        ++issued;
-                        st_release(&issued_chunks, static_cast<unsigned>(issued));
+        if (lane == 0) {
+            Ring r{0, 0, 0};
+            int64_t issued = 0;
+            bool ok = true;
+            for (int j = 0; j < rows && ok; ++j) {
+                const RowBytes b = row_bytes<GT>(row_of<GT>(a.x, share.row(j), a.x_stride), a.v);
+                for (uint32_t o = 0; o < b.body; o += kChunk) {
+                    if (issued >= kSlots && !mbar_wait(&empty[r.slot], r.parity ^ 1u, wait_ns)) {
+                        ok = false;
+                        break;
                     }
+                    const uint32_t n = b.body - o < kChunk ? b.body - o : kChunk;
+                    mbar_expect_tx(&full[r.slot], n);
+                    bulk_load(smem + static_cast<size_t>(r.slot) * kChunk, b.body_at + o, n,
+                              &full[r.slot]);
+                    r.next();
+                    ++issued;
+                    st_release(&issued_chunks, static_cast<unsigned>(issued));
                 }
             }
-            ok = __shfl_sync(kFull, static_cast<int>(ok), 0) != 0;
-        }
-        if (lane == 0) {
             if (!ok) atomicOr(&g_loss_status, kStatusProducerTimeout);
             // the last (at most kSlots) chunks land before the block may exit
             const int64_t skip = issued > kSlots ? issued - kSlots : 0;
@@ -788,64 +963,60 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
         }
     } else if (warp == kStoreWarp) {
         Ring r{0, 0, 0};
-        int held = -1;                // the slot of the newest store group, or none
         bool ok = true;
-        unsigned next = live_mask(0);
-        for (int64_t j0 = 0; j0 < rows && ok; j0 += 32) {
-            const unsigned live = next;
-            next = live_mask(j0 + 32);
-            for (int64_t j = j0; j < rows && j < j0 + 32 && ok; ++j) {
-                char* g = const_cast<char*>(row_of<GT>(a.grad, row_at(j), a.g_stride));
-                const RowBytes b = row_bytes<GT>(g, a.v);
-                char* dst = const_cast<char*>(b.body_at);
-                if (!((live >> (j - j0)) & 1u)) {
-                    if (lane < b.head) store1<GT>(g, lane, 0.0f);
-                    if (lane < b.tail) store1<GT>(dst + b.body, lane, 0.0f);
-                    if (lane == 0) {
-                        for (uint32_t o = 0; o < b.body; o += kZeroBytes)
-                            bulk_store(dst + o, zeros,
-                                       b.body - o < kZeroBytes ? b.body - o : kZeroBytes);
-                        bulk_commit();
+        for (int j = 0; j < rows && ok; ++j) {
+            char* g = const_cast<char*>(row_of<GT>(a.grad, share.row(j), a.g_stride));
+            const RowBytes b = row_bytes<GT>(g, a.v);
+            char* dst = const_cast<char*>(b.body_at);
+            int held = -1;            // the slot of the newest store group, or none
+            for (uint32_t o = 0; o < b.body; o += kChunk) {
+                ok = __all_sync(kFull, mbar_wait(&done[r.slot], r.parity, wait_ns));
+                if (!ok) break;
+                if (lane == 0) {
+                    bulk_store(dst + o, smem + static_cast<size_t>(r.slot) * kChunk,
+                               b.body - o < kChunk ? b.body - o : kChunk);
+                    bulk_commit();
+                    if (held >= 0) {          // the store before this one has been read
+                        bulk_wait_read<1>();
+                        mbar_arrive(&empty[held]);
                     }
-                    continue;
                 }
-                for (uint32_t o = 0; o < b.body; o += kChunk) {
-                    ok = __all_sync(kFull, mbar_wait(&done[r.slot], r.parity, wait_ns));
-                    if (!ok) break;
-                    if (lane == 0) {
-                        bulk_store(dst + o, smem + static_cast<size_t>(r.slot) * kChunk,
-                                   b.body - o < kChunk ? b.body - o : kChunk);
-                        bulk_commit();
-                        if (held >= 0) {      // the store before this one has been read
-                            bulk_wait_read<1>();
-                            mbar_arrive(&empty[held]);
-                        }
-                        held = r.slot;
-                    }
-                    r.next();
-                }
-                // the loading warp may want the row's last slot at once
-                if (lane == 0 && held >= 0) {
-                    bulk_wait_read<0>();
-                    mbar_arrive(&empty[held]);
-                }
-                held = -1;
+                held = r.slot;
+                r.next();
             }
+            // the loading warp may want the row's last slot at once
+            if (lane == 0 && held >= 0) {
+                bulk_wait_read<0>();
+                mbar_arrive(&empty[held]);
+            }
+            if (lane == 0) st_release(&stored_rows, static_cast<unsigned>(j + 1));
         }
         if (!ok && lane == 0) atomicOr(&g_loss_status, kStatusProducerTimeout);
-        if (lane == 0) bulk_wait_all();
+        if (lane == 0) bulk_wait_read<0>();
+    } else if (warp == kZeroWarp) {
+        // spread over the live rows: written all at once at the start, they took the
+        // memory from the live rows' loads, which could not catch up later (4096
+        // rows of 32000, 30% masked: 92.6 us)
+        const unsigned long long t0 = now_ns();
+        for (int j = 0; j < share.n_dead; ++j) {
+            const unsigned after =
+                static_cast<unsigned>(static_cast<int64_t>(j) * rows / share.n_dead);
+            while (ld_acquire(&stored_rows) < after && now_ns() - t0 < wait_ns) __nanosleep(200);
+            zero_row<GT>(a, share.dead_row(j), zeros);
+        }
+        if (lane == 0) bulk_wait_read<0>();
     } else if (warp == kParamWarp) {
         const float scale = kPolicy ? 0.0f : out_scale(a);
         bool ok = true;
-        for (int64_t j = 0, n = 0; j < rows && ok; j += kBatch, ++n) {
-            const int buf = static_cast<int>(n & 1);
+        for (int j = 0, n = 0; j < rows && ok; j += kBatch, ++n) {
+            const int buf = n & 1;
             RowParam q{0.0f, -1, 0.0f, {0.0f, 0.0f, 0.0f}};
             if (j + lane < rows) {
-                const int64_t i = row_at(j + lane);
+                const int64_t i = share.row(j + lane);
                 if (kPolicy) {
                     q = policy_param<GT>(a, pol, i);
-                    if (q.w == 0.0f) a.logps[i] = 0.0f;
-                } else if ((q.w = token_weight(a, i)) != 0.0f) {
+                } else {
+                    q.w = token_weight(a, i);
                     q.y = static_cast<int32_t>(token_id(a, i));
                     q.f[0] = __fmul_rn(__fmul_rn(p.coef[p.seq[i]], q.w), scale);
                     q.f[1] = p.row_ref[i];
@@ -862,36 +1033,47 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
             if (lane == 0) mbar_arrive(&param_full[buf]);
         }
         if (!ok && lane == 0) atomicOr(&g_loss_status, kStatusProducerTimeout);
+        if (kPolicy) {
+            // the block's sums, while the last rows are still being stored
+            for (int j = lane; j < share.n_dead; j += 32) a.logps[share.dead_row(j)] = 0.0f;
+            const bool in = __all_sync(kFull, mbar_wait(&sums_full, 0, 4 * wait_ns));
+            double s = 0.0;
+            if (lane < 4)
+                for (int w = 0; w < kTeams; ++w) s += team_sums[w][lane];
+            if (in)
+                join_sums(a, s, first_launch, last_launch);
+            else if (lane == 0)
+                atomicOr(&g_loss_status, kStatusConsumerTimeout);
+        }
     } else if (warp < kWorkWarps) {
         const int which = warp / kTeamWarps;
         const Team<kTeamThreads> team{1 + which, tid - which * kTeamThreads, &sh[which]};
-        const float norm = kPolicy ? weight_sum(a, team) : 1.0f;
+        const float norm = kPolicy ? weight_sum(a, team, end - begin, found.weight) : 1.0f;
         const float scale = kPolicy ? out_scale(a) : 0.0f;
+        Sum2 sums[4] = {};
         Ring ring{0, 0, 0};
         unsigned seen = 0;
         // a wait that ran out, made the same for the whole team at a barrier before
         // any of it leaves
         bool bad = false;
         int turn = 0;
-        int64_t live = 0;
-        for (int64_t j = 0; j < rows && !bad; ++j) {
-            const int buf = static_cast<int>((j / kBatch) & 1);
-            if (j % kBatch == 0)
+        for (int j = 0; j < rows && !bad; ++j) {
+            const int buf = (j / kBatch) & 1;
+            if (j % kBatch == 0) {
                 bad = !mbar_wait(&param_full[buf], static_cast<uint32_t>(j / (2 * kBatch)) & 1u,
                                  wait_ns);
+                bad = team.sync_or(bad);
+                if (bad) break;
+            }
             const RowParam q = params[buf][j % kBatch];
             if (j % kBatch == kBatch - 1) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&param_empty[buf]);
             }
-            if (j % kBatch == 0) bad = team.sync_or(bad);
-            if (bad) break;
-            if (q.w == 0.0f) continue;
-            const int64_t i = row_at(j);
+            const int64_t i = share.row(j);
             const char* x = row_of<GT>(a.x, i, a.x_stride);
             const RowBytes b = row_bytes<GT>(x, a.v);
-            const int64_t row = live++;
-            if (row % kTeams != which) {      // the other team's
+            if (j % kTeams != which) {        // the other team's
                 ring.skip((b.body + kChunk - 1) / kChunk);
                 continue;
             }
@@ -989,15 +1171,10 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
             if (!kPolicy) bad = team.sync_or(bad);
         }
         if (bad && team.tid == 0) atomicOr(&g_loss_status, kStatusConsumerTimeout);
-        if (team.tid == 0)
-            for (int k = 0; k < 4; ++k) team_sums[which][k] = sums[k];
-    }
-    if (kPolicy) {
-        __syncthreads();
-        if (tid == 0)
-            for (int w = 1; w < kTeams; ++w)
-                for (int k = 0; k < 4; ++k) sums[k] += team_sums[w][k];
-        if (join_blocks(a.ws, sums) && tid < 4) a.stats[tid] = __double2float_rn(a.ws->total[tid]);
+        if (kPolicy && team.tid == 0) {
+            for (int k = 0; k < 4; ++k) team_sums[which][k] = sums[k].wide();
+            mbar_arrive(&sums_full);
+        }
     }
 }
 
@@ -1012,14 +1189,14 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
 // SM's warps, else 4.  Bound by the one read of the logits.
 constexpr int kStreamWarps = 16, kStreamThreads = 32 * kStreamWarps;
 constexpr int kStreamSlots = 3, kStreamChunk = 4096;
-constexpr size_t kStreamSmem = static_cast<size_t>(kStreamWarps) * kStreamSlots * kStreamChunk;
+constexpr size_t kStreamSmem =
+    static_cast<size_t>(kStreamWarps) * kStreamSlots * kStreamChunk + 8 * kShareRows;
 
 // The chunks of a warp's parts of its team's live rows, in order.
 struct Parts {
     const char* at;      // the current row's part
     uint32_t len, off;   // its bytes; those already taken
-    int64_t batch;       // first row of the batch that `mask` speaks of
-    unsigned mask, next; // live rows of the batch not yet taken; of the next batch
+    int row;             // the next row of the share
 };
 
 // The policy loss's stand-in for a table of pairs.
@@ -1029,8 +1206,8 @@ struct NoTable {
 template <int GT, int W, class Table>
 __global__ void __launch_bounds__(kStreamThreads, 1)
     stream_forward(const TokenArgs a, const PolicyArgs pol, const PreferenceArgs p,
-                   const __grid_constant__ Table t, int64_t begin, int64_t end,
-                   unsigned long long wait_ns) {
+                   const __grid_constant__ Table t, int64_t begin, int64_t end, bool first_launch,
+                   bool last_launch, unsigned long long wait_ns) {
     constexpr bool PREF = !std::is_same<Table, NoTable>::value;
     extern __shared__ __align__(128) uint8_t smem[];
     constexpr int kRowTeams = kStreamWarps / W;
@@ -1038,24 +1215,31 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     __shared__ TeamShared<kStreamThreads> block_sh;
     __shared__ double team_sums[kRowTeams][4];
     __shared__ uint64_t full[kStreamWarps][kStreamSlots];
+    __shared__ ReadyPairs ready;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int which = warp / W, part = warp % W;
     const Team<32 * W> team{1 + which, tid - which * 32 * W, &sh[which]};
     uint8_t* slots = smem + static_cast<size_t>(warp) * kStreamSlots * kStreamChunk;
+    uint32_t* live_list = reinterpret_cast<uint32_t*>(
+        smem + static_cast<size_t>(kStreamWarps) * kStreamSlots * kStreamChunk);
+    uint32_t* dead_list = live_list + kShareRows;
+    if (tid == 0) ready.n = 0;
     if (lane == 0) {
         for (int s = 0; s < kStreamSlots; ++s) mbar_init(&full[warp][s], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
     pdl_enter();
-    const int64_t teams = static_cast<int64_t>(gridDim.x) * kRowTeams;
-    const int64_t first = begin + static_cast<int64_t>(blockIdx.x) * kRowTeams + which;
-    const int64_t rows = first < end ? (end - first + teams - 1) / teams : 0;
-    const auto row_at = [&](int64_t j) { return first + j * teams; };
-    const auto live_mask = [&](int64_t j) {
-        const bool live = j + lane < rows && token_weight(a, row_at(j + lane)) != 0.0f;
-        return __ballot_sync(kFull, live);
-    };
+    Dealt found{0, 0, 0.0f};
+    if (a.w != nullptr)
+        found = deal_rows<kStreamThreads>(a, begin, end, blockIdx.x * kRowTeams, kRowTeams,
+                                          gridDim.x * kRowTeams, live_list, dead_list);
+    const Share share =
+        share_of(a, begin, end, blockIdx.x * kRowTeams + which,
+                 static_cast<int64_t>(gridDim.x) * kRowTeams, found,
+                 live_list + which * (kShareRows / kRowTeams),
+                 dead_list + which * (kShareRows / kRowTeams));
+    const int rows = share.n_live;
     // this warp's part of a row's body: whole vectors, contiguous
     const auto part_of = [&](const RowBytes& b, const char** at) {
         const uint32_t each = (b.body / 16 + W - 1) / W * 16;
@@ -1064,20 +1248,14 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         return b.body - lo < each ? b.body - lo : each;
     };
 
-    Parts c{nullptr, 0, 0, 0, live_mask(0), live_mask(32)};
+    Parts c{nullptr, 0, 0, 0};
     int issued = 0;
     // Starts the copy of the next chunk, if there is one, into slot s.
     const auto start_next = [&](int s) {
         while (c.off >= c.len) {
-            while (c.mask == 0) {
-                c.batch += 32;
-                if (c.batch >= rows) return;
-                c.mask = c.next;
-                c.next = live_mask(c.batch + 32);
-            }
-            const int64_t i = row_at(c.batch + __ffs(c.mask) - 1);
-            c.mask &= c.mask - 1;
-            c.len = part_of(row_bytes<GT>(row_of<GT>(a.x, i, a.x_stride), a.v), &c.at);
+            if (c.row >= rows) return;
+            const char* x = row_of<GT>(a.x, share.row(c.row++), a.x_stride);
+            c.len = part_of(row_bytes<GT>(x, a.v), &c.at);
             c.off = 0;
         }
         const uint32_t n = c.len - c.off < kStreamChunk ? c.len - c.off : kStreamChunk;
@@ -1091,36 +1269,32 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     for (int s = 0; s < kStreamSlots; ++s) start_next(s);
 
     float norm = 1.0f;
-    if (!PREF) norm = weight_sum(a, Team<kStreamThreads>{0, tid, &block_sh});
+    if (!PREF) norm = weight_sum(a, Team<kStreamThreads>{0, tid, &block_sh}, end - begin, found.weight);
     if constexpr (PREF) {
-        if (warp == 0) empty_pairs(a, p, t);
+        if (warp == 0 && begin == t.start[0]) empty_pairs(a, p, t);
     }
-    double sums[4] = {0.0, 0.0, 0.0, 0.0};
+    Sum2 sums[4] = {};
     int slot = 0, taken = 0, turn = 0;
     uint32_t parity = 0;
     bool bad = false;
-    const auto param = [&](int64_t j) {
+    const auto param = [&](int j) {
         RowParam q{0.0f, -1, 0.0f, {0.0f, 0.0f, 0.0f}};
         if (j + lane >= rows) return q;
-        const int64_t i = row_at(j + lane);
+        const int64_t i = share.row(j + lane);
         if (!PREF) return policy_param<GT>(a, pol, i);
         q.w = token_weight(a, i);
-        if (q.w != 0.0f) {
-            const int64_t y = token_id(a, i);
-            q.xy = y >= 0 ? load1<GT>(row_of<GT>(a.x, i, a.x_stride), y) : NAN;
-            q.f[0] = a.ref[i];
-        }
+        q.f[0] = a.ref[i];
+        const int64_t y = token_id(a, i);
+        q.xy = y >= 0 ? load1<GT>(row_of<GT>(a.x, i, a.x_stride), y) : NAN;
         return q;
     };
     RowParam mine = param(0), after = param(32);
-    for (int64_t j0 = 0; j0 < rows && !bad; j0 += 32) {
+    for (int j0 = 0; j0 < rows && !bad; j0 += 32) {
         RowRef my_ref{0.0f, true};
         float my_sum = 1.0f;
-        for (unsigned live = __ballot_sync(kFull, mine.w != 0.0f); live != 0 && !bad;
-             live &= live - 1) {
-            const int l = __ffs(live) - 1;
+        for (int l = 0; l < 32 && j0 + l < rows && !bad; ++l) {
             const float xy = __shfl_sync(kFull, mine.xy, l);
-            const char* x = row_of<GT>(a.x, row_at(j0 + l), a.x_stride);
+            const char* x = row_of<GT>(a.x, share.row(j0 + l), a.x_stride);
             const RowBytes b = row_bytes<GT>(x, a.v);
             const char* unused;
             const uint32_t len = part_of(b, &unused);
@@ -1176,27 +1350,24 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         }
         if (bad) break;
         // the batch's terms, a row per lane
-        const bool held = j0 + lane < rows;
         if (part == 0) {
-            const int64_t i = held ? row_at(j0 + lane) : begin;
-            const bool live = mine.w != 0.0f;
-            const float lp = live ? row_logp(mine.xy, my_ref, my_sum) : 0.0f;
-            if (held) a.logps[i] = lp;
-            if (!PREF && live) {
-                const PolicyTerms pt = policy_terms(lp, mine.f[0], mine.f[1], mine.f[2], pol);
-                add_policy(sums, pt, pol, __fdiv_rn(mine.w, norm));
-            }
-            if constexpr (PREF) {
-                int q = -1;
-                if (held) {
+            int q = -1;
+            if (j0 + lane < rows) {
+                const int64_t i = share.row(j0 + lane);
+                const float lp = row_logp(mine.xy, my_ref, my_sum);
+                a.logps[i] = lp;
+                if constexpr (PREF) {
                     const int seq = find_sequence(t, i);
                     q = seq >> 1;
-                    p.term[i] = live ? __fmul_rn(mine.w, __fsub_rn(lp, mine.f[0])) : 0.0f;
+                    p.term[i] = __fmul_rn(mine.w, __fsub_rn(lp, mine.f[0]));
                     p.seq[i] = seq;
-                    if (live) save_row(p, i, my_ref, my_sum);
+                    save_row(p, i, my_ref, my_sum);
+                } else {
+                    const PolicyTerms pt = policy_terms(lp, mine.f[0], mine.f[1], mine.f[2], pol);
+                    add_policy(sums, pt, pol, __fdiv_rn(mine.w, norm));
                 }
-                rows_done(a, p, t, q);
             }
+            if constexpr (PREF) rows_done(a, t, q, &ready);
         }
         mine = after;
         after = param(j0 + 64);
@@ -1215,26 +1386,44 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
             atomicOr(&g_loss_status,
                      kStatusConsumerTimeout | (drained ? 0u : kStatusDrainTimeout));
     }
+    // the rows of weight 0
+    if (part == 0 && !bad) {
+        for (int j0 = 0; j0 < share.n_dead; j0 += 32) {
+            int q = -1;
+            if (j0 + lane < share.n_dead) {
+                const int64_t i = share.dead_row(j0 + lane);
+                a.logps[i] = 0.0f;
+                if constexpr (PREF) {
+                    const int seq = find_sequence(t, i);
+                    q = seq >> 1;
+                    p.term[i] = 0.0f;
+                    p.seq[i] = seq;
+                }
+            }
+            if constexpr (PREF) rows_done(a, t, q, &ready);
+        }
+    }
     if constexpr (PREF) {
-        preference_stats(a, p, t);
-        return;
-    }
-    if (part == 0) {
+        // the pairs that this block's rows completed, a warp each
+        __syncthreads();
+        for (int k = warp; k < ready.n; k += kStreamWarps) finish_pair(a, p, t, ready.pair[k]);
+        if (end == t.start[2 * t.pairs]) preference_stats(a, p, t);
+    } else {
+        if (part == 0) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            double s = sums[k];
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
-            if (lane == 0) team_sums[which][k] = s;
+            for (int k = 0; k < 4; ++k) {
+                const Sum2 s = warp_sum(sums[k]);
+                if (lane == 0) team_sums[which][k] = s.wide();
+            }
+        }
+        __syncthreads();
+        if (warp == 0) {
+            double s = 0.0;
+            if (lane < 4)
+                for (int w = 0; w < kRowTeams; ++w) s += team_sums[w][lane];
+            join_sums(a, s, first_launch, last_launch);
         }
     }
-    __syncthreads();
-    if (tid == 0)
-        for (int k = 0; k < 4; ++k) {
-            sums[k] = 0.0;
-            for (int w = 0; w < kRowTeams; ++w) sums[k] += team_sums[w][k];
-        }
-    if (join_blocks(a.ws, sums) && tid < 4) a.stats[tid] = __double2float_rn(a.ws->total[tid]);
 }
 
 int row_blocks(int64_t rows, int per_sm) {
@@ -1264,8 +1453,8 @@ cudaError_t go_staged(const TokenArgs& a, const PolicyArgs& pol, const Preferenc
     const cudaError_t e = opt_in(staged_rows<GT, M>, kStagedSmem, applied);
     if (e != cudaSuccess) return e;
     return launch_after(staged_rows<GT, M>, dim3(row_blocks(end - begin, 1)),
-                        dim3(kStagedThreads), kStagedSmem, s, a, pol, p, begin, end,
-                        tma_wait_limit());
+                        dim3(kStagedThreads), kStagedSmem, s, a, pol, p, begin, end, begin == 0,
+                        end == a.n, tma_wait_limit());
 }
 template <int GT, int W, class Table>
 cudaError_t go_stream_w(const TokenArgs& a, const PolicyArgs& pol, const PreferenceArgs& p,
@@ -1277,7 +1466,7 @@ cudaError_t go_stream_w(const TokenArgs& a, const PolicyArgs& pol, const Prefere
     return launch_after(stream_forward<GT, W, Table>,
                         dim3(row_blocks((end - begin + teams - 1) / teams, 1)),
                         dim3(kStreamThreads), kStreamSmem, s, a, pol, p, t, begin, end,
-                        tma_wait_limit());
+                        begin == 0, end == a.n, tma_wait_limit());
 }
 // Warps per row: 4 from 8 rows per SM on (2000 rows of 32000 bf16 logits: 35.2 us
 // against 39.0 with 16), 16 below (152 rows: 13.3 us against 15.6; 760 rows: 23.3
@@ -1292,8 +1481,7 @@ cudaError_t go_stream(const TokenArgs& a, const PolicyArgs& pol, const Preferenc
 }
 template <int GT>
 cudaError_t go_forward(const TokenArgs& a, const PreferenceArgs& p, const PairTableLarge& t,
-                       cudaStream_t s) {
-    const int64_t begin = t.start[0], end = t.start[2 * t.pairs];
+                       int64_t begin, int64_t end, cudaStream_t s) {
     if (t.pairs > kPairsSmall) return go_stream<GT>(a, PolicyArgs{}, p, t, begin, end, s);
     PairTable<kPairsSmall> small;
     std::copy(t.start, t.start + 2 * t.pairs + 1, small.start);
@@ -1302,11 +1490,13 @@ cudaError_t go_forward(const TokenArgs& a, const PreferenceArgs& p, const PairTa
 }
 
 template <int GT>
-cudaError_t go_policy(const TokenArgs& a, const PolicyArgs& p, bool staged, cudaStream_t s) {
+cudaError_t go_policy(const TokenArgs& a, const PolicyArgs& p, bool staged, int64_t begin,
+                      int64_t end, cudaStream_t s) {
     if (a.grad == nullptr)
-        return go_stream<GT>(a, p, PreferenceArgs{}, NoTable{0}, 0, a.n, s);
-    if (staged) return go_staged<GT, Pass::kPolicy>(a, p, PreferenceArgs{}, 0, a.n, s);
-    return launch_after(policy_rows<GT>, dim3(row_blocks(a.n, 2)), dim3(kRowThreads), 0, s, a, p);
+        return go_stream<GT>(a, p, PreferenceArgs{}, NoTable{0}, begin, end, s);
+    if (staged) return go_staged<GT, Pass::kPolicy>(a, p, PreferenceArgs{}, begin, end, s);
+    return launch_after(policy_rows<GT>, dim3(row_blocks(end - begin, 2)), dim3(kRowThreads), 0,
+                        s, a, p, begin, end, begin == 0, end == a.n);
 }
 template <int GT>
 cudaError_t go_backward(const TokenArgs& a, const PreferenceArgs& p, int64_t begin, int64_t end,
@@ -1330,19 +1520,22 @@ cudaError_t read_loss_status(unsigned int* status, bool clear) {
     return cudaMemcpyToSymbol(g_loss_status, &zero, sizeof(unsigned int));
 }
 
+int64_t loss_rows_per_launch() { return static_cast<int64_t>(kShareRows) * device_sms(); }
+
 cudaError_t launch_policy_loss(const TokenArgs& a, const PolicyArgs& p, int dtype, bool staged,
-                               cudaStream_t stream) {
-    const cudaError_t e = dtype == kGradF32   ? go_policy<kGradF32>(a, p, staged, stream)
-                          : dtype == kGradF16 ? go_policy<kGradF16>(a, p, staged, stream)
-                                              : go_policy<kGradBF16>(a, p, staged, stream);
+                               int64_t begin, int64_t end, cudaStream_t s) {
+    const cudaError_t e = dtype == kGradF32   ? go_policy<kGradF32>(a, p, staged, begin, end, s)
+                          : dtype == kGradF16 ? go_policy<kGradF16>(a, p, staged, begin, end, s)
+                                              : go_policy<kGradBF16>(a, p, staged, begin, end, s);
     note_launch();
     return e;
 }
 cudaError_t launch_preference_forward(const TokenArgs& a, const PreferenceArgs& p,
-                                      const PairTableLarge& t, int dtype, cudaStream_t stream) {
-    const cudaError_t e = dtype == kGradF32   ? go_forward<kGradF32>(a, p, t, stream)
-                          : dtype == kGradF16 ? go_forward<kGradF16>(a, p, t, stream)
-                                              : go_forward<kGradBF16>(a, p, t, stream);
+                                      const PairTableLarge& t, int64_t begin, int64_t end,
+                                      int dtype, cudaStream_t s) {
+    const cudaError_t e = dtype == kGradF32   ? go_forward<kGradF32>(a, p, t, begin, end, s)
+                          : dtype == kGradF16 ? go_forward<kGradF16>(a, p, t, begin, end, s)
+                                              : go_forward<kGradBF16>(a, p, t, begin, end, s);
     note_launch();
     return e;
 }

@@ -475,10 +475,15 @@ int token_policy_loss(const shardstep_token_loss_t* args, const float* old_logps
     if (int rc = check_ranges(&reads, &writes); rc != SHARDSTEP_OK) return rc;
     const PolicyArgs p{old_logps, advantages, 1.0f - clip_low, 1.0f + clip_high, kl_coef};
     const bool staged = k.grad != nullptr && staged_rows(args);
-    const cudaError_t e =
-        launch_policy_loss(k, p, args->dtype, staged, static_cast<cudaStream_t>(stream));
-    if (e != cudaSuccess)
-        return ready_fail(SHARDSTEP_ERR_CUDA, "policy loss launch: %s", cudaGetErrorString(e));
+    const int64_t most = loss_rows_per_launch();
+    for (int64_t row = 0; row < k.n; row += most) {
+        const cudaError_t e =
+            launch_policy_loss(k, p, args->dtype, staged, row, std::min(k.n, row + most),
+                               static_cast<cudaStream_t>(stream));
+        if (e != cudaSuccess)
+            return ready_fail(SHARDSTEP_ERR_CUDA, "policy loss launch: %s",
+                              cudaGetErrorString(e));
+    }
     record_kernel(k.grad == nullptr ? "stream_forward<%s> (TMA-staged)"
                   : staged          ? "staged_rows<%s, policy> (TMA-staged)"
                                     : "policy_rows<%s>",
@@ -534,6 +539,7 @@ int token_preference_loss(const shardstep_token_loss_t* args, const int64_t* seq
     const bool staged = k.grad != nullptr && staged_rows(args);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     std::unique_ptr<PairTableLarge> t(new PairTableLarge);
+    const int64_t most = loss_rows_per_launch();
     int32_t row = 0;
     for (int32_t q = 0; q < n_pairs; q += kPairsPerLaunch) {
         t->pairs = std::min(kPairsPerLaunch, n_pairs - q);
@@ -543,9 +549,16 @@ int token_preference_loss(const shardstep_token_loss_t* args, const int64_t* seq
         }
         t->start[2 * t->pairs] = row;
         p.last = q + t->pairs >= n_pairs;
-        cudaError_t e = launch_preference_forward(k, p, *t, args->dtype, s);
-        if (e == cudaSuccess && k.grad != nullptr)
-            e = launch_preference_backward(k, p, t->start[0], row, args->dtype, staged, s);
+        // the table's rows in as few launches as they fit; all of its forward
+        // passes before the first backward pass, which needs its pairs' slopes
+        const int64_t begin = t->start[0], end = row;
+        cudaError_t e = cudaSuccess;
+        for (int64_t r = begin; e == cudaSuccess && (r < end || r == begin); r += most)
+            e = launch_preference_forward(k, p, *t, r, std::min(end, r + most), args->dtype, s);
+        if (k.grad != nullptr)
+            for (int64_t r = begin; e == cudaSuccess && r < end; r += most)
+                e = launch_preference_backward(k, p, r, std::min(end, r + most), args->dtype,
+                                               staged, s);
         if (e != cudaSuccess)
             return ready_fail(SHARDSTEP_ERR_CUDA, "preference loss launch: %s",
                               cudaGetErrorString(e));
