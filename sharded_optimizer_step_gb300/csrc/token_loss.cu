@@ -557,8 +557,10 @@ struct Share {
     const uint32_t* dead;
     int n_live, n_dead;
     int64_t begin, first, units;
+    bool backwards;           // the live rows from the last to the first
 
     __device__ __forceinline__ int64_t row(int j) const {
+        if (backwards) j = n_live - 1 - j;
         return live != nullptr ? begin + live[j] : first + j * units;
     }
     __device__ __forceinline__ int64_t dead_row(int j) const { return begin + dead[j]; }
@@ -572,18 +574,33 @@ struct Dealt {
     int n_live, n_dead;       // of the launch
     float weight;             // the sum of the launch's weights
 };
-// Fills the lists of the block's `mine` units (the first of them: u0), each of
-// up to kShareRows / mine rows; every thread of the block calls it.  A thread
-// takes 8 consecutive rows at a time.
+// Where the rank-th of the things dealt out goes: to the blocks in turn, then to
+// each block's teams in turn, so that a row's block is the same whatever the
+// number of teams.
+struct Deal {
+    unsigned rank, block, team, place;
+    __device__ __forceinline__ Deal(unsigned r, unsigned teams)
+        : rank(r), block(r % gridDim.x), team(r / gridDim.x % teams),
+          place(r / gridDim.x / teams) {}
+    __device__ __forceinline__ void next(unsigned teams) {
+        if (++block < gridDim.x) return;
+        block = 0;
+        if (++team < teams) return;
+        team = 0;
+        ++place;
+    }
+};
+// Fills the lists of the block's teams, each of up to kShareRows / teams rows;
+// every thread of the block calls it.  A thread takes 8 consecutive rows at a
+// time.
 template <int THREADS>
 __device__ __forceinline__ Dealt deal_rows(const TokenArgs& a, int64_t begin, int64_t end,
-                                           unsigned u0, unsigned mine, unsigned units,
-                                           uint32_t* live, uint32_t* dead) {
+                                           unsigned teams, uint32_t* live, uint32_t* dead) {
     constexpr int kWarps = THREADS / 32, kRows = 8;
     __shared__ int counts[2][kWarps];
     __shared__ Sum2 sums[kWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const unsigned each = kShareRows / mine;
+    const unsigned each = kShareRows / teams;
     unsigned live_before = 0;
     Sum2 weight{0.0f, 0.0f};
     int turn = 0;
@@ -614,24 +631,16 @@ __device__ __forceinline__ Dealt deal_rows(const TokenArgs& a, int64_t begin, in
             total += c;
         }
         const unsigned row0 = static_cast<unsigned>(i0 - begin);
-        const unsigned rank = live_before + below + upto - own, other = row0 - rank;
-        unsigned lu = rank % units, lq = rank / units, du = other % units, dq = other / units;
+        Deal l(live_before + below + upto - own, teams), d(row0 - l.rank, teams);
 #pragma unroll
         for (int k = 0; k < kRows; ++k) {
             if (i0 + k >= end) break;
             if (w[k] != 0.0f) {
-                if (lu - u0 < mine) live[(lu - u0) * each + lq] = row0 + k;
-                if (++lu == units) {
-                    lu = 0;
-                    ++lq;
-                }
+                if (l.block == blockIdx.x) live[l.team * each + l.place] = row0 + k;
+                l.next(teams);
             } else {
-                const unsigned u = units - 1 - du - u0;
-                if (u < mine) dead[u * each + dq] = row0 + k;
-                if (++du == units) {
-                    du = 0;
-                    ++dq;
-                }
+                if (d.block == gridDim.x - 1 - blockIdx.x) dead[d.team * each + d.place] = row0 + k;
+                d.next(teams);
             }
         }
         live_before += total;
@@ -644,16 +653,19 @@ __device__ __forceinline__ Dealt deal_rows(const TokenArgs& a, int64_t begin, in
                  static_cast<int>(end - begin) - static_cast<int>(live_before),
                  warp_sum(weight).value()};
 }
-// Unit u's share.  The rows of weight 0 are dealt out from the last unit down,
-// so that the units with a live row more get one of them less.
-__device__ __forceinline__ Share share_of(const TokenArgs& a, int64_t begin, int64_t end,
-                                          int64_t u, int64_t units, const Dealt& found,
-                                          const uint32_t* live, const uint32_t* dead) {
+// The share of the block's team `team` of `teams`.  The rows of weight 0 are
+// dealt out from the last block down, so that the blocks with a live row more get
+// one of them less.
+__device__ __forceinline__ Share share_of(const TokenArgs& a, int64_t begin, int64_t end, int team,
+                                          int teams, const Dealt& found, const uint32_t* live,
+                                          const uint32_t* dead) {
+    const int64_t blocks = gridDim.x, units = blocks * teams;
+    const int64_t u = team * blocks + blockIdx.x, down = team * blocks + blocks - 1 - blockIdx.x;
     if (a.w == nullptr)
-        return Share{nullptr, nullptr, dealt(end - begin, u, units), 0, begin, begin + u,
-                     units};
-    return Share{live,  dead,  dealt(found.n_live, u, units),
-                 dealt(found.n_dead, units - 1 - u, units), begin, begin, units};
+        return Share{nullptr, nullptr, dealt(end - begin, u, units), 0, begin, begin + u, units,
+                     false};
+    return Share{live,  dead,  dealt(found.n_live, u, units), dealt(found.n_dead, down, units),
+                 begin, begin, units, false};
 }
 
 // ------------------------------------------------------ the staged kernels
@@ -923,10 +935,11 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
     pdl_enter();
     Dealt found{0, 0, 0.0f};
     if (a.w != nullptr)
-        found = deal_rows<kStagedThreads>(a, begin, end, blockIdx.x, 1, gridDim.x, live_list,
-                                          dead_list);
-    const Share share =
-        share_of(a, begin, end, blockIdx.x, gridDim.x, found, live_list, dead_list);
+        found = deal_rows<kStagedThreads>(a, begin, end, 1, live_list, dead_list);
+    Share share = share_of(a, begin, end, 0, 1, found, live_list, dead_list);
+    // the backward pass after a forward pass over the same rows: those read last
+    // are the ones that L2 still holds
+    share.backwards = !kPolicy;
     const int rows = share.n_live;
 
     if (warp == kLoadWarp) {
@@ -1232,13 +1245,10 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     pdl_enter();
     Dealt found{0, 0, 0.0f};
     if (a.w != nullptr)
-        found = deal_rows<kStreamThreads>(a, begin, end, blockIdx.x * kRowTeams, kRowTeams,
-                                          gridDim.x * kRowTeams, live_list, dead_list);
-    const Share share =
-        share_of(a, begin, end, blockIdx.x * kRowTeams + which,
-                 static_cast<int64_t>(gridDim.x) * kRowTeams, found,
-                 live_list + which * (kShareRows / kRowTeams),
-                 dead_list + which * (kShareRows / kRowTeams));
+        found = deal_rows<kStreamThreads>(a, begin, end, kRowTeams, live_list, dead_list);
+    const Share share = share_of(a, begin, end, which, kRowTeams, found,
+                                 live_list + which * (kShareRows / kRowTeams),
+                                 dead_list + which * (kShareRows / kRowTeams));
     const int rows = share.n_live;
     // this warp's part of a row's body: whole vectors, contiguous
     const auto part_of = [&](const RowBytes& b, const char** at) {
