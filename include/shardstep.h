@@ -773,8 +773,9 @@ typedef struct {
 
 /* Bytes of the workspace for up to n_tokens tokens in n_pairs pairs (0, 0 for
  * the policy loss, which needs its head alone); -1 for negative arguments.
- * The caller zeroes the workspace once; calls that may run at the same time
- * need workspaces of their own. */
+ * The caller zeroes the workspace once (and again after a call whose waits ran
+ * out, see shardstep_device_status); calls that may run at the same time need
+ * workspaces of their own. */
 int64_t token_loss_workspace_bytes(int64_t n_tokens, int32_t n_pairs);
 
 /* token_policy_loss -- device, one launch.  Per token, W = norm or sum w:

@@ -865,8 +865,9 @@ __device__ __forceinline__ void zero_row(const TokenArgs& a, int64_t i, const ui
     if (lane < b.head) store1<GT>(g, lane, 0.0f);
     if (lane < b.tail) store1<GT>(dst + b.body, lane, 0.0f);
     if (lane == 0) {
+        const uint64_t once = evict_first();
         for (uint32_t o = 0; o < b.body; o += kZeroBytes)
-            bulk_store(dst + o, zeros, b.body - o < kZeroBytes ? b.body - o : kZeroBytes);
+            bulk_store(dst + o, zeros, b.body - o < kZeroBytes ? b.body - o : kZeroBytes, once);
         bulk_commit();
         bulk_wait_read<1>();
     }
@@ -944,6 +945,7 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
 
     if (warp == kLoadWarp) {
         if (lane == 0) {
+            const uint64_t once = evict_first();
             Ring r{0, 0, 0};
             int64_t issued = 0;
             bool ok = true;
@@ -956,8 +958,8 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
                     }
                     const uint32_t n = b.body - o < kChunk ? b.body - o : kChunk;
                     mbar_expect_tx(&full[r.slot], n);
-                    bulk_load(smem + static_cast<size_t>(r.slot) * kChunk, b.body_at + o, n,
-                              &full[r.slot]);
+                    bulk_load_once(smem + static_cast<size_t>(r.slot) * kChunk, b.body_at + o, n,
+                                   &full[r.slot], once);
                     r.next();
                     ++issued;
                     st_release(&issued_chunks, static_cast<unsigned>(issued));
@@ -975,6 +977,7 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
             if (!drained) atomicOr(&g_loss_status, kStatusDrainTimeout);
         }
     } else if (warp == kStoreWarp) {
+        const uint64_t once = evict_first();
         Ring r{0, 0, 0};
         bool ok = true;
         for (int j = 0; j < rows && ok; ++j) {
@@ -987,7 +990,7 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
                 if (!ok) break;
                 if (lane == 0) {
                     bulk_store(dst + o, smem + static_cast<size_t>(r.slot) * kChunk,
-                               b.body - o < kChunk ? b.body - o : kChunk);
+                               b.body - o < kChunk ? b.body - o : kChunk, once);
                     bulk_commit();
                     if (held >= 0) {          // the store before this one has been read
                         bulk_wait_read<1>();
@@ -1053,10 +1056,8 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
             double s = 0.0;
             if (lane < 4)
                 for (int w = 0; w < kTeams; ++w) s += team_sums[w][lane];
-            if (in)
-                join_sums(a, s, first_launch, last_launch);
-            else if (lane == 0)
-                atomicOr(&g_loss_status, kStatusConsumerTimeout);
+            if (!in && lane == 0) atomicOr(&g_loss_status, kStatusConsumerTimeout);
+            join_sums(a, s, first_launch, last_launch);   // in any case: it counts the blocks
         }
     } else if (warp < kWorkWarps) {
         const int which = warp / kTeamWarps;
