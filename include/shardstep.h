@@ -755,7 +755,7 @@ typedef struct {
     int32_t id_bytes;         /* 4 or 8: int32 or int64 ids                      */
     const void* ids;          /* device, n_tokens                                */
     int64_t n_tokens;         /* 0 .. 2^31 - 1                                   */
-    int64_t vocab;            /* 1 .. 2^31 - 1                                   */
+    int64_t vocab;            /* 1 .. 2^28                                       */
     const float* weights;     /* device, n_tokens, or NULL: ones                 */
     const float* ref_logps;   /* device, n_tokens: the reference model's         */
     float* logps;             /* device, n_tokens, written                       */

@@ -309,7 +309,7 @@ int take_tokens(const shardstep_token_loss_t* a, int64_t need, TokenArgs* k,
         return ready_fail(SHARDSTEP_ERR_INVALID, "id_bytes must be 4 or 8");
     if (a->n_tokens < 0 || a->n_tokens > INT32_MAX)
         return ready_fail(SHARDSTEP_ERR_INVALID, "n_tokens out of range");
-    if (a->vocab < 1 || a->vocab > INT32_MAX)
+    if (a->vocab < 1 || a->vocab > (int64_t{1} << 28))   // a row's bytes fit 31 bits
         return ready_fail(SHARDSTEP_ERR_INVALID, "vocab out of range");
     if (!std::isfinite(a->grad_scale))
         return ready_fail(SHARDSTEP_ERR_INVALID, "grad_scale is not finite");

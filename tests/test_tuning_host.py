@@ -59,6 +59,15 @@ def test_both_losses_refuse(bad):
     assert _pref(_tokens(**bad)) == _capi.ERR_INVALID
 
 
+def test_widest_vocabulary():
+    """A row's byte offsets are 32-bit in the kernels; the check comes first."""
+    wide = dict(vocab=(1 << 28) + 1, row_stride=(1 << 28) + 1, grad=None, n_tokens=1)
+    assert _policy(_tokens(**wide)) == _capi.ERR_INVALID
+    assert b"vocab" in _capi.lib().shardstep_last_error()
+    assert _pref(_tokens(**wide), lens=(1, 0)) == _capi.ERR_INVALID
+    assert b"vocab" in _capi.lib().shardstep_last_error()
+
+
 def test_policy_refuses():
     t = _tokens()
     assert _capi.lib().token_policy_loss(None, A, A, 0.2, 0.2, 0.0, None) == _capi.ERR_INVALID
