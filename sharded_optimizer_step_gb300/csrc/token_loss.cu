@@ -37,7 +37,8 @@ constexpr unsigned kFull = 0xFFFFFFFFu;
 // the same side, which a sum over a sequence's tokens would gather up.
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLog2eLo = 1.9259629911e-8f;
-constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLn2 = 0.6931471805599453f, kLn2Hi = 2839.0f / 4096.0f,
+                kLn2Lo = static_cast<float>(0.6931471805599453 - 2839.0 / 4096.0);
 constexpr float kFastLogit = 32768.0f;        // |x_y| below this: R and its products are fine
 constexpr float kFastSum = 0x1p120f;
 
@@ -192,11 +193,37 @@ __device__ __forceinline__ float row_exp(float x, RowRef r) {
 __device__ __forceinline__ RowRef fast_ref(float xy) {
     return RowRef{rintf(__fmul_rn(xy, kLog2e)), fabsf(xy) < kFastLogit};
 }
-// The id's log probability.
-__device__ __forceinline__ float row_logp(float xy, RowRef r, float sum) {
-    if (!r.fast) return __fsub_rn(__fsub_rn(xy, r.ref), logf(sum));
+// The id's log probability as the sum of two floats.  It is some 10 in size and
+// what is wanted of it is mostly its small distance from another model's: rounded
+// to one float (up to 5e-7 off), that distance summed over a short sequence was
+// further from the exact one than a 32-bit log-softmax's.  log S = k log 2 + log m
+// with S = 2^k m and m in [0.75, 1.5), so that the logarithm's own rounding is
+// that of a number below 0.41; k times the upper 12 bits of log 2 is exact.
+struct Logp {
+    float hi, lo;
+};
+__device__ __forceinline__ Logp two_sum(float a, float b) {
+    const float s = __fadd_rn(a, b), bb = __fsub_rn(s, a);
+    const float e = __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb));
+    return Logp{s, fabsf(s) < INFINITY ? e : 0.0f};
+}
+__device__ __forceinline__ Logp row_logp(float xy, RowRef r, float sum) {
+    // sum is normal, or NaN, which the product keeps
+    const int k = (__float_as_int(sum) - __float_as_int(0.75f)) >> 23;
+    const float m = __fmul_rn(sum, __int_as_float((127 - k) << 23));
+    const float minus_k = static_cast<float>(-k);
+    const float big = __fmul_rn(minus_k, kLn2Hi);
+    const float small = __fmaf_rn(minus_k, kLn2Lo, -logf(m));
+    if (!r.fast) {
+        const Logp d = two_sum(xy, -r.ref), e = two_sum(d.hi, big);
+        return two_sum(e.hi, __fadd_rn(__fadd_rn(d.lo, e.lo), small));
+    }
     const float t = __fmaf_rn(xy, kLog2e, __fmaf_rn(xy, kLog2eLo, -r.ref));
-    return __fmaf_rn(t, kLn2, -logf(sum));
+    return two_sum(big, __fmaf_rn(t, kLn2, small));
+}
+// lp - x.
+__device__ __forceinline__ float logp_less(Logp lp, float x) {
+    return __fadd_rn(__fsub_rn(lp.hi, x), lp.lo);
 }
 
 // The sum against the true maximum, from global memory: rows that the fast
@@ -243,9 +270,9 @@ __device__ __forceinline__ float out_scale(const TokenArgs& a) {
 struct PolicyTerms {
     float policy, kl, clipped, slope;
 };
-__device__ __forceinline__ PolicyTerms policy_terms(float lp, float old, float adv, float ref,
+__device__ __forceinline__ PolicyTerms policy_terms(Logp lp, float old, float adv, float ref,
                                                     const PolicyArgs& p) {
-    const float u = expf(__fsub_rn(lp, old));
+    const float u = expf(logp_less(lp, old));
     const float cu = u < p.lo ? p.lo : u > p.hi ? p.hi : u;
     const float one = __fmul_rn(u, adv), two = __fmul_rn(cu, adv);
     PolicyTerms t;
@@ -254,7 +281,7 @@ __device__ __forceinline__ PolicyTerms policy_terms(float lp, float old, float a
     t.slope = one > two ? 0.0f : -one;
     t.kl = 0.0f;
     if (p.kl != 0.0f) {
-        const float d = __fsub_rn(ref, lp);
+        const float d = -logp_less(lp, ref);
         const float e = expm1f(d);
         t.kl = __fsub_rn(e, d);
         t.slope = __fsub_rn(t.slope, __fmul_rn(p.kl, e));
@@ -346,7 +373,7 @@ template <class Table>
 __device__ __forceinline__ void finish_pair(const TokenArgs& a, const PreferenceArgs& p,
                                             const Table& t, int q) {
     const int lane = threadIdx.x & 31;
-    float r[2];
+    Sum2 r[2];
     for (int h = 0; h < 2; ++h) {
         Sum2 s{0.0f, 0.0f};
         const int end = t.start[2 * q + h + 1];
@@ -357,13 +384,14 @@ __device__ __forceinline__ void finish_pair(const TokenArgs& a, const Preference
 #pragma unroll
             for (int k = 0; k < 8; ++k) s.add(x[k]);
         }
-        r[h] = warp_sum(s).value();
+        r[h] = warp_sum(s);
     }
     if (lane != 0) return;
-    const float h = __fmul_rn(p.beta, __fsub_rn(r[0], r[1]));
+    p.log_ratios[2 * q] = r[0].value();
+    p.log_ratios[2 * q + 1] = r[1].value();
+    r[0].add(Sum2{-r[1].hi, -r[1].lo});          // rounded after the difference
+    const float h = __fmul_rn(p.beta, r[0].value());
     const float ls = p.smoothing, us = __fsub_rn(1.0f, ls);
-    p.log_ratios[2 * q] = r[0];
-    p.log_ratios[2 * q + 1] = r[1];
     const float dh = __fsub_rn(__fmul_rn(ls, sigmoid(h)), __fmul_rn(us, sigmoid(-h)));
     const float c = __fmul_rn(dh, __fdiv_rn(p.beta, a.norm));
     p.coef[2 * q] = c;
@@ -508,12 +536,12 @@ __global__ void __launch_bounds__(kRowThreads)
         const float xy = y >= 0 ? load1<GT>(x, y) : NAN;
         RowRef r;
         const float s = plain_sum<GT>(x, a.v, xy, &r, team);
-        const float lp = row_logp(xy, r, s);
+        const Logp lp = row_logp(xy, r, s);
         const PolicyTerms t =
             policy_terms(lp, p.old[i], p.adv[i], p.kl != 0.0f ? a.ref[i] : 0.0f, p);
         const float k = __fdiv_rn(w, norm);
         if (threadIdx.x == 0) {
-            a.logps[i] = lp;
+            a.logps[i] = lp.hi;
             add_policy(sums, t, p, k);
         }
         plain_grad<GT>(x, g, a.v, y, r, s, __fmul_rn(__fmul_rn(t.slope, k), scale));
@@ -1130,12 +1158,12 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
                     r = sr.r;
                     s = sr.sum;
                 }
-                const float lp = row_logp(q.xy, r, s);
+                const Logp lp = row_logp(q.xy, r, s);
                 const PolicyTerms pt = policy_terms(lp, q.f[0], q.f[1], q.f[2], pol);
                 const float k = __fdiv_rn(q.w, norm);
                 c = __fmul_rn(__fmul_rn(pt.slope, k), scale);
                 if (team.tid == 0) {
-                    a.logps[i] = lp;
+                    a.logps[i] = lp.hi;
                     add_policy(sums, pt, pol, k);
                 }
             } else {
@@ -1365,12 +1393,12 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
             int q = -1;
             if (j0 + lane < rows) {
                 const int64_t i = share.row(j0 + lane);
-                const float lp = row_logp(mine.xy, my_ref, my_sum);
-                a.logps[i] = lp;
+                const Logp lp = row_logp(mine.xy, my_ref, my_sum);
+                a.logps[i] = lp.hi;
                 if constexpr (PREF) {
                     const int seq = find_sequence(t, i);
                     q = seq >> 1;
-                    p.term[i] = __fmul_rn(mine.w, __fsub_rn(lp, mine.f[0]));
+                    p.term[i] = __fmul_rn(mine.w, logp_less(lp, mine.f[0]));
                     p.seq[i] = seq;
                     save_row(p, i, my_ref, my_sum);
                 } else {
