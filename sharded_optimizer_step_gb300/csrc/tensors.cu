@@ -207,11 +207,12 @@ __device__ __forceinline__ void decode4(uint32_t mc, uint32_t vc, float ms, floa
     r[0] = mul2(make_pair(root_to_f32(vc & 0xFFu), root_to_f32((vc >> 8) & 0xFFu)), vs2);
     r[1] = mul2(make_pair(root_to_f32((vc >> 16) & 0xFFu), root_to_f32(vc >> 24)), vs2);
 }
-__device__ __forceinline__ void encode4(const Pair* m, const Pair* r, const BlockScales& b,
+// The roots come negated, as the step has them.
+__device__ __forceinline__ void encode4(const Pair* m, const Pair* r_neg, const BlockScales& b,
                                         uint32_t* mc, uint32_t* vc) {
-    const Pair mu = make_pair(b.m_up, b.m_up), ru = make_pair(b.r_up, b.r_up);
+    const Pair mu = make_pair(b.m_up, b.m_up), ru = make_pair(-b.r_up, -b.r_up);
     *mc = f32_to_e4m3x2(mul2(m[0], mu)) | (f32_to_e4m3x2(mul2(m[1], mu)) << 16);
-    const float2 y0 = floats(mul2(r[0], ru)), y1 = floats(mul2(r[1], ru));
+    const float2 y0 = floats(mul2(r_neg[0], ru)), y1 = floats(mul2(r_neg[1], ru));
     *vc = f32_to_root(y0.x) + (f32_to_root(y0.y) << 8) + (f32_to_root(y1.x) << 16) +
           (f32_to_root(y1.y) << 24);
 }
@@ -234,16 +235,49 @@ __device__ __forceinline__ uint32_t lane_max(const Pair (*x)[2]) {
     return __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(big));
 }
 
-// r / b for b = sqrt(bc2), correctly rounded, from y = RN(1 / b): Markstein's
-// correction (named at div_nd), twice, so that the quotient is within an ulp
-// before the step that rounds it whatever the operands' fractions are.  r is 0
-// or between 2^-75 and 2^64 (the root of a positive fp32 value), so no
-// residual leaves the normal range; for an infinite r or an unusable y the
-// caller takes the division itself.
-__device__ __forceinline__ Pair div_root(Pair r, Pair b_neg, Pair y) {
-    Pair q = mul2(r, y);
-    q = fma2(fma2(q, b_neg, r), y, q);
-    return fma2(fma2(q, b_neg, r), y, q);
+// min(|a|, |b|, |c|), NaN where one is.
+__device__ __forceinline__ float min3_abs(float a, float b, float c) {
+    float d;
+    asm("min.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// Roots and quotients two elements to an instruction, correctly rounded, by
+// Markstein's corrections ("Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990): an approximation, one Newton step, and the
+// residual, which fma gives exactly, times the reciprocal.  They hold where no
+// residual leaves the normal range: see kFastLeast.  Signs are chosen so that no
+// operand has to be negated on the way.
+constexpr float kFastLeast = 0x1p-80f;
+
+// -sqrt(v) from -v.  Equal to the IEEE root for all 2^24 fractions of [1, 4).
+__device__ __forceinline__ Pair neg_sqrt2(Pair v_neg) {
+    const float2 v = floats(v_neg);
+    float a, b;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(-v.x));
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(b) : "f"(-v.y));
+    const Pair y = make_pair(a, b), half = make_pair(0.5f, 0.5f);
+    Pair s = mul2(v_neg, y), h = mul2(y, half);      // s: the negative root
+    const Pair e = fma2(s, h, half);
+    s = fma2(s, e, s);
+    h = fma2(h, e, h);
+    return fma2(fma2(s, s, v_neg), h, s);
+}
+// 1 / d from -d.  Equal to the IEEE quotient for all 2^23 fractions of d.
+__device__ __forceinline__ Pair reciprocal2(Pair d_neg) {
+    const float2 d = floats(d_neg);
+    float a, b;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(-d.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(b) : "f"(-d.y));
+    const Pair y = make_pair(a, b);
+    return fma2(y, fma2(d_neg, y, make_pair(1.0f, 1.0f)), y);
+}
+// n / d from -d and y = RN(1 / d): twice the correction, so that the quotient is
+// within an ulp before the step that rounds it whatever the fractions are.
+__device__ __forceinline__ Pair divide2(Pair n, Pair d_neg, Pair y) {
+    Pair q = mul2(n, y);
+    q = fma2(fma2(q, d_neg, n), y, q);
+    return fma2(fma2(q, d_neg, n), y, q);
 }
 
 // The 8-bit step: a warp per block of 256 elements, 4 + 4 per lane (128 apart,
@@ -254,8 +288,8 @@ __device__ __forceinline__ Pair div_root(Pair r, Pair b_neg, Pair y) {
 //   p -= lr wd p;  m = b1 m + (1 - b1) g;  r = sqrt(b2 r^2 + (1 - b2) g g);
 //   p -= (lr / bc1) m / (r / sqrt(bc2) + eps), with m and r before rounding
 // to their codes.  Bound by memory in the limit, (gradient + 8 + 4 + 2) bytes
-// per element, if the issue slots keep up: products and sums go two elements to
-// an instruction.  (A warp that took 4 blocks in turn was slower, 379 us against
+// per element, if the issue slots keep up: all arithmetic goes two elements to
+// an instruction, roots and quotients too where the block's values allow it.  (A warp that took 4 blocks in turn was slower, 379 us against
 // 359 for 124M elements: its loads no longer overlap other blocks' arithmetic.)
 template <int CAP, int GT, int PT>
 __global__ void __launch_bounds__(kListThreads)
@@ -277,15 +311,15 @@ __global__ void __launch_bounds__(kListThreads)
     uint16_t* O = static_cast<uint16_t*>(t.param[s]);
     const bool vec = t.vec[s] != 0;
     const Pair lr_wd = make_pair(-c.lr_wd, -c.lr_wd), b1 = make_pair(c.beta1, c.beta1),
-               o1 = make_pair(c.omb1, c.omb1), b2 = make_pair(c.beta2, c.beta2),
-               o2 = make_pair(c.omb2, c.omb2), kk = make_pair(k, k);
+               o1 = make_pair(c.omb1, c.omb1), b2_neg = make_pair(-c.beta2, -c.beta2),
+               o2_neg = make_pair(-c.omb2, -c.omb2), kk = make_pair(k, k);
     // Products that are added to are formed as a b + (-0), the same value: of a
     // plain product and a sum of pairs the assembler makes one fma (one rounding
     // instead of two) whatever their rounding modifiers, which it cannot do here
     // as long as it does not know the -0.
     const Pair nz = make_pair(gs.neg_zero, gs.neg_zero);
     const Pair root_neg = make_pair(-c.sqrt_bc2, -c.sqrt_bc2), inv = make_pair(inv_root, inv_root),
-               eps = make_pair(c.eps, c.eps), size = make_pair(c.step_size, c.step_size);
+               eps_neg = make_pair(-c.eps, -c.eps), size = make_pair(c.step_size, c.step_size);
     const int64_t blk = static_cast<int64_t>(blockIdx.x - t.b0[s]) * (kListChunk8 / kMomentBlock) +
                         (threadIdx.x >> 5);
     const int64_t base = blk * kMomentBlock;
@@ -295,7 +329,7 @@ __global__ void __launch_bounds__(kListThreads)
     float* VS = t.v_scale[s] + blk;
     const bool whole = vec && base + kMomentBlock <= n;
     float g[2][4];
-    Pair p[2][2], m[2][2], r[2][2];
+    Pair p[2][2], m[2][2], r[2][2];     // r: the old root, -v, then the new root negated
     uint32_t mc[2], vc[2];
     const float ms = *MS, vs = *VS;
     if (whole) {
@@ -343,9 +377,8 @@ __global__ void __launch_bounds__(kListThreads)
             if (coef != nullptr) gg = mul2(gg, kk);
             p[h][e] = add2(p[h][e], fma2(lr_wd, p[h][e], nz));
             m[h][e] = add2(fma2(b1, m[h][e], nz), fma2(o1, gg, nz));
-            const float2 v = floats(
-                add2(fma2(b2, mul2(r[h][e], r[h][e]), nz), fma2(mul2(o2, gg), gg, nz)));
-            r[h][e] = make_pair(__fsqrt_rn(v.x), __fsqrt_rn(v.y));
+            r[h][e] = add2(fma2(b2_neg, mul2(r[h][e], r[h][e]), nz),
+                           fma2(mul2(o2_neg, gg), gg, nz));
         }
     }
     if (!whole) {   // places past the tensor's end take no part in the maxima
@@ -359,27 +392,55 @@ __global__ void __launch_bounds__(kListThreads)
                 r[h][e] = make_pair(j < n ? b.x : 0.0f, j + 1 < n ? b.y : 0.0f);
             }
     }
-    const uint32_t m_big = lane_max(m), r_big = lane_max(r);
+    // the root of the largest v is the largest root
+    const uint32_t m_big = lane_max(m), v_big = lane_max(r);
+    const uint32_t r_big = __float_as_uint(__fsqrt_rn(__uint_as_float(v_big)));
     const BlockScales b = block_scales(m_big, r_big);
     if ((threadIdx.x & 31) == 0) {
         *MS = b.m_scale;
         *VS = b.r_scale;
     }
-    const bool exact = r_big >= 0x7F800000u || !(c.sqrt_bc2 > 0x1p-40f && c.sqrt_bc2 < 0x1p40f);
-    Pair root[2][2];
-    if (exact) {
+    Pair num[2][2];
+    float least = INFINITY;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            num[h][e] = mul2(size, m[h][e]);
+            const float2 a = floats(num[h][e]), v = floats(r[h][e]);
+            least = min3_abs(least, a.x, a.y);
+            least = min3_abs(least, v.x, v.y);
+        }
+    // Every v and every numerator at least 2^-80 (a zero is not: its sign would be
+    // lost), v below 2^30, sqrt(bc2) from 2^-8 to 1, eps below 1: denominators lie
+    // between 2^-40 and 2^23 + 1, quotients between 2^-104 and 2^100, residuals
+    // above 2^-130.
+    const bool fast = __all_sync(0xFFFFFFFFu, least >= kFastLeast) &&
+                      __uint_as_float(v_big) < 0x1p30f &&
+                      fabsf(__fmul_rn(c.step_size, __uint_as_float(m_big))) < 0x1p60f &&
+                      c.sqrt_bc2 > 0x1p-8f && c.sqrt_bc2 <= 1.0f && c.eps >= 0.0f &&
+                      c.eps < 1.0f;
+    if (fast) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float2 f = floats(r[h][e]);
-                root[h][e] = make_pair(__fdiv_rn(f.x, c.sqrt_bc2), __fdiv_rn(f.y, c.sqrt_bc2));
+                r[h][e] = neg_sqrt2(r[h][e]);
+                const Pair den_neg = add2(divide2(r[h][e], root_neg, inv), eps_neg);
+                num[h][e] = divide2(num[h][e], den_neg, reciprocal2(den_neg));
             }
     } else {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) root[h][e] = div_root(r[h][e], root_neg, inv);
+            for (int e = 0; e < 2; ++e) {
+                const float2 v = floats(r[h][e]), a = floats(num[h][e]);
+                const float x = __fsqrt_rn(-v.x), y = __fsqrt_rn(-v.y);
+                r[h][e] = make_pair(-x, -y);
+                num[h][e] = make_pair(
+                    __fdiv_rn(a.x, __fadd_rn(__fdiv_rn(x, c.sqrt_bc2), c.eps)),
+                    __fdiv_rn(a.y, __fadd_rn(__fdiv_rn(y, c.sqrt_bc2), c.eps)));
+            }
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -387,11 +448,9 @@ __global__ void __launch_bounds__(kListThreads)
         float f[4];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const float2 den = floats(add2(root[h][e], eps));
-            const float2 num = floats(mul2(size, m[h][e]));
-            const float2 x = floats(p[h][e]);
-            f[2 * e] = __fsub_rn(x.x, __fdiv_rn(num.x, den.x));
-            f[2 * e + 1] = __fsub_rn(x.y, __fdiv_rn(num.y, den.y));
+            const float2 x = floats(p[h][e]), q = floats(num[h][e]);
+            f[2 * e] = __fsub_rn(x.x, q.x);
+            f[2 * e + 1] = __fsub_rn(x.y, q.y);
         }
         if (whole) {
             stcs16(P + i + 128 * h, pack4f(f));
@@ -479,8 +538,8 @@ __global__ void __launch_bounds__(kListThreads)
         }
         m[h][0] = make_pair(a[0], a[1]);
         m[h][1] = make_pair(a[2], a[3]);
-        r[h][0] = make_pair(__fsqrt_rn(b[0]), __fsqrt_rn(b[1]));
-        r[h][1] = make_pair(__fsqrt_rn(b[2]), __fsqrt_rn(b[3]));
+        r[h][0] = make_pair(-__fsqrt_rn(b[0]), -__fsqrt_rn(b[1]));
+        r[h][1] = make_pair(-__fsqrt_rn(b[2]), -__fsqrt_rn(b[3]));
     }
     const uint32_t m_big = lane_max(m), r_big = lane_max(r);
     const BlockScales b = block_scales(m_big, r_big);

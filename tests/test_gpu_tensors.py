@@ -238,6 +238,49 @@ def test_eight_bit_state_special_values():
     assert not m[:256].any() and not v[:256].any() and (v[512:768] > 0).all()
 
 
+@pytest.mark.parametrize("hp", [dict(), dict(lr=0.0), dict(eps=0.0), dict(eps=2.0),
+                                dict(beta1=0.0, beta2=0.0), dict(beta2=0.99999), dict(lr=1e12)],
+                         ids=lambda h: "-".join(h) or "default")
+def test_eight_bit_step_over_all_magnitudes(hp):
+    """Blocks whose gradients have magnitudes from 2^-75 to 2^60, most of one size
+    and some of many, with zeros of both signs among gradients and parameters: the
+    step's roots and quotients are the IEEE ones on either side of every bound of
+    the paired arithmetic."""
+    r = np.random.default_rng(13)
+    e = np.arange(-75, 61)
+    n = 256 * len(e)
+    x = np.exp2(np.repeat(e, 256) + r.uniform(-1, 1, n)) * r.choice([-1.0, 1.0], n)
+    spread = np.repeat(np.arange(len(e)) % 4 == 3, 256)
+    x = np.where(spread, x * np.exp2(r.integers(-30, 31, n)), x).astype(np.float32)
+    x[r.integers(0, n, 20)] = 0.0
+    x[r.integers(0, n, 20)] = -0.0
+    params, _ = _make([n], "f32", 14)
+    params[0][::97] = 0.0
+    params[0][::89] = -0.0
+    cfg = dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.1)
+    cfg.update(hp)
+    opt = _opt(params, 8, ss.AdamW(**cfg))
+    o = _Oracle(params, 8, [AdamWConfig(**cfg)], [0])
+    sound = np.ones(n, bool)
+    for t in range(1, 4):
+        g = torch.from_numpy(x * np.float32(0.9 ** t)).to(DEV)
+        opt.step([g])
+        o.step([g], t)
+        scales = opt.m_scale.cpu().numpy(), opt.v_scale.cpu().numpy()
+        for got, want in zip(scales, o.s[0][1::2]):
+            _same(np.isfinite(got), np.isfinite(want))
+        # a block whose squares overflow keeps a non-finite scale and nothing else
+        # that is fixed
+        sound &= np.repeat(np.isfinite(scales[0]) & np.isfinite(scales[1]), 256)
+        _same(opt.master[:n].cpu().numpy()[sound], o.p[0][sound], "master")
+        _same(np.signbit(opt.master[:n].cpu().numpy()[sound]), np.signbit(o.p[0][sound]))
+        for got, want, what in ((opt.m, o.s[0][0], "m"), (opt.v, o.s[0][2], "v")):
+            _same(got[:n].cpu().numpy()[sound], want[sound], what)
+        for got, want, what in zip(scales, o.s[0][1::2], ("m_scale", "v_scale")):
+            _same(got[sound[::256]], want[sound[::256]], what)
+    assert sound.mean() > 0.9
+
+
 @pytest.mark.parametrize("n", [1, 7, 256, 1000, 256 * 300 + 9])
 def test_moment_codes_both_ways(n):
     r = np.random.default_rng(n)
