@@ -771,14 +771,18 @@ typedef struct {
     int64_t workspace_bytes;  /* >= token_loss_workspace_bytes(...)              */
 } shardstep_token_loss_t;
 
-/* Bytes of the workspace for up to n_tokens tokens in n_pairs pairs (0, 0 for
- * the policy loss, which needs its head alone); -1 for negative arguments.
+/* Bytes of the workspace for up to n_tokens tokens in n_pairs pairs (0 pairs: the
+ * policy loss; 0 tokens do for it without a gradient, and where a row of logits
+ * has at most 212992 bytes and the gradient's rows lie as far past 16-byte
+ * boundaries as the logits'); -1 for negative arguments.
  * The caller zeroes the workspace once (and again after a call whose waits ran
  * out, see shardstep_device_status); calls that may run at the same time need
  * workspaces of their own. */
 int64_t token_loss_workspace_bytes(int64_t n_tokens, int32_t n_pairs);
 
-/* token_policy_loss -- device, one launch.  Per token, W = norm or sum w:
+/* token_policy_loss -- device, one launch (with a gradient two, forward and
+ * backward, where the workspace needs words per token) per 1024 tokens of every
+ * SM.  Per token, W = norm or sum w:
  *     u = exp(a - old), policy = -min(u A, clip(u, 1 - clip_low, 1 + clip_high) A)
  *     d = ref - a, kl = expm1(d) - d                (kl_coef 0: not formed, ref unused)
  *     stats = sum over tokens of w / W * {policy + kl_coef kl, policy, kl,

@@ -787,7 +787,7 @@ class LossWorkspace:
     def at_least(self, n_tokens: int, pairs: int):
         """(address, bytes, buffer) of a workspace for that many tokens in
         that many pairs (0: the policy loss)."""
-        need = _loss_head() + (16 * n_tokens + 8 * pairs if pairs else 0)
+        need = _loss_head() + 16 * n_tokens + 8 * pairs
         if self.nbytes < need:
             import torch
             self.buf = torch.zeros((need + 7) // 8, dtype=torch.int64, device=self.device)

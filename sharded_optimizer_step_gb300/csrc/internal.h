@@ -379,26 +379,31 @@ struct PreferenceArgs {
     float* log_ratios;      // 2 per pair
     float* row_ref;         // per token: what its exponents refer to
     float* row_sum;         // per token: the sum of its exponentials
-    float* term;            // per token: w (a - ref)
+    float* term;            // per token: w (a - ref); of the policy loss c, or null
     int32_t* seq;           // per token: its sequence within the launch
-    float* coef;            // per sequence: d loss / d a at weight 1
+    float* coef;            // per sequence: d loss / d a at weight 1; null: policy
     int first, last;        // this launch starts / ends the call
 };
-// Whether a row of v elements fits the staged kernels' shared memory.
+// Whether a row of v elements fits the staged policy kernel's shared memory.
 bool loss_row_fits(int64_t v, int dtype);
-// staged: rows go through shared memory (they fit, and the gradient's rows,
-// if any, start at the logits' rows' offsets from 16-byte boundaries).
 // A call's rows go in launches of at most this many (loss_rows_per_launch), so
 // that a block's share of them fits its shared memory.
 constexpr int kShareRows = 1024;   // per SM
 int64_t loss_rows_per_launch();
-cudaError_t launch_policy_loss(const TokenArgs& a, const PolicyArgs& p, int dtype, bool staged,
-                               int64_t begin, int64_t end, cudaStream_t stream);
+// The policy loss forward and backward; the rows fit and can be staged.
+cudaError_t launch_policy_staged(const TokenArgs& a, const PolicyArgs& pol, int64_t begin,
+                                 int64_t end, int dtype, cudaStream_t stream);
+// Forward; with p.term also p.term, p.row_ref and p.row_sum for the backward pass.
+cudaError_t launch_policy_forward(const TokenArgs& a, const PolicyArgs& pol,
+                                  const PreferenceArgs& p, int64_t begin, int64_t end, int dtype,
+                                  cudaStream_t stream);
 cudaError_t launch_preference_forward(const TokenArgs& a, const PreferenceArgs& p,
                                       const PairTableLarge& t, int64_t begin, int64_t end,
                                       int dtype, cudaStream_t stream);
-cudaError_t launch_preference_backward(const TokenArgs& a, const PreferenceArgs& p, int64_t begin,
-                                       int64_t end, int dtype, bool staged, cudaStream_t stream);
+// The gradient from what a forward pass has left.  staged: the gradient's rows
+// start at the logits' rows' offsets from 16-byte boundaries.
+cudaError_t launch_loss_backward(const TokenArgs& a, const PreferenceArgs& p, int64_t begin,
+                                 int64_t end, int dtype, bool staged, cudaStream_t stream);
 
 // Host helpers of api.cpp for the other translation units: the last error of
 // the calling thread, the name shardstep_last_kernel reports, the per-step

@@ -13,13 +13,23 @@
 // Statistics, terms and coefficients are fp32, sums over tokens double; the
 // gradient is rounded once, to the logits' type.
 //
-// The staged kernels move a row through shared memory once: bulk copies bring
-// it in 16 KB chunks, 512 threads sum it, form the row's terms, overwrite it in
-// place with the gradient, and bulk copies store it, while the next rows are on
-// their way.  Each logit is read once and each gradient written once, the
-// least there is, and the kernel is bound by that traffic.  A row that does
-// not fit (or whose gradient lies at another offset from a 16-byte boundary)
-// takes the plain kernels, which read it again for the gradient (from L2).
+// Three kernels, all bound by the logits' and the gradient's traffic:
+//   stream_forward  a forward pass: each logit is read once, nothing is kept.
+//   staged_rows     policy: a row is brought into shared memory in 16 KB chunks by
+//                   bulk copies, summed there, overwritten in place with the
+//                   gradient and stored by bulk copies, while the next rows are on
+//                   their way: each logit read once, each gradient written once.
+//                   backward: the same ring without the sum, after a forward pass.
+//   plain_backward  a backward pass where the gradient's rows lie at other offsets
+//                   from 16-byte boundaries than the logits', so that a row's
+//                   staged bytes cannot be stored back in bulk.
+// Which of them: the policy loss takes one pass of staged_rows where a row fits its
+// 13 slots of shared memory (4096 rows of 32000 bf16 logits: 90 us against 137 in
+// two passes), else stream_forward and a backward pass (2048 rows of 128256 bf16
+// logits: 262 us; the same in one kernel that read a row again from L2 through
+// registers: 1056).  The preference loss always takes two passes: a row's slope
+// needs the sums of its whole pair.  A gradient at other offsets costs
+// (4096 x 32000): 257 us against 90.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -466,10 +476,18 @@ __device__ __forceinline__ void preference_stats(const TokenArgs& a, const Prefe
     }
 }
 
-// What the backward pass needs of a row; a negative sum marks the slow form.
+// What a backward pass of its own needs of a row; a negative sum marks the slow
+// form.
 __device__ __forceinline__ void save_row(const PreferenceArgs& p, int64_t i, RowRef r, float sum) {
     p.row_ref[i] = r.ref;
     p.row_sum[i] = r.fast ? sum : -sum;
+}
+// c: the slope of the row's sequence times its weight, or what the policy loss's
+// forward pass has left.
+__device__ __forceinline__ float row_coef(const PreferenceArgs& p, int64_t i, float w,
+                                          float scale) {
+    const float c = p.coef != nullptr ? __fmul_rn(p.coef[p.seq[i]], w) : p.term[i];
+    return __fmul_rn(c, scale);
 }
 
 // The id's own gradient, c (1 - e_y / S), as (c / S) (S - e_y): the difference
@@ -478,84 +496,39 @@ __device__ __forceinline__ float own_grad(float e, float sum, float cs) {
     return __fmul_rn(__fsub_rn(sum, e), cs);
 }
 
-// ------------------------------------------------------- the plain kernels
+// -------------------------------------------------- the plain backward pass
 
-template <int GT>
-__device__ __forceinline__ float plain_sum(const char* x, int64_t v, float xy, RowRef* r,
-                                           const Team<kRowThreads>& team) {
-    *r = fast_ref(xy);
-    float s = 0.0f;
-    if (r->fast)
-        for (int64_t j = threadIdx.x; j < v; j += kRowThreads)
-            s = __fadd_rn(s, row_exp(load1<GT>(x, j), *r));
-    bool none = false;
-    team.sync();
-    s = team.sum(s, &none, 0);
-    if (!r->fast || !(s < kFastSum)) {
-        const SlowRow q = slow_row<GT>(x, v, team);
-        *r = q.r;
-        s = q.sum;
-    }
-    return s;
-}
 // grad = c (1[y] - e / S), rounded once.
 template <int GT>
 __device__ __forceinline__ void plain_grad(const char* x, char* g, int64_t v, int64_t y, RowRef r,
                                            float sum, float c) {
     const float cs = __fdiv_rn(c, sum);
-    for (int64_t j = threadIdx.x; j < v; j += kRowThreads) {
-        const float e = row_exp(load1<GT>(x, j), r);
+    const auto put = [&](int64_t j, float xj) {
+        const float e = row_exp(xj, r);
         store1<GT>(g, j, j == y ? own_grad(e, sum, cs) : -__fmul_rn(e, cs));
+    };
+    constexpr int U = 16;                 // loads in flight together
+    int64_t j = threadIdx.x;
+    for (; j + (U - 1) * kRowThreads < v; j += U * kRowThreads) {
+        float f[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) f[u] = load1<GT>(x, j + u * kRowThreads);
+#pragma unroll
+        for (int u = 0; u < U; ++u) put(j + u * kRowThreads, f[u]);
     }
+    for (; j < v; j += kRowThreads) put(j, load1<GT>(x, j));
 }
 template <int GT>
 __device__ __forceinline__ void plain_zero(char* g, int64_t v) {
     for (int64_t j = threadIdx.x; j < v; j += kRowThreads) store1<GT>(g, j, 0.0f);
 }
 
+// The gradient of a row whose forward pass has left its sum, where gradient and
+// logits lie at different offsets from 16-byte boundaries and so cannot share a
+// vector: element by element.
 template <int GT>
 __global__ void __launch_bounds__(kRowThreads)
-    policy_rows(const TokenArgs a, const PolicyArgs p, int64_t begin, int64_t end,
-                bool first_launch, bool last_launch) {
-    __shared__ TeamShared<kRowThreads> sh;
-    const Team<kRowThreads> team{1, static_cast<int>(threadIdx.x), &sh};
-    pdl_enter();
-    const float norm = weight_sum(a, team), scale = out_scale(a);
-    Sum2 sums[4] = {};
-    __shared__ double block_sums[4];
-    for (int64_t i = begin + blockIdx.x; i < end; i += gridDim.x) {
-        const char* x = row_of<GT>(a.x, i, a.x_stride);
-        char* g = const_cast<char*>(row_of<GT>(a.grad, i, a.g_stride));
-        const float w = token_weight(a, i);
-        if (w == 0.0f) {   // not read at all: whatever it holds takes no part
-            if (threadIdx.x == 0) a.logps[i] = 0.0f;
-            plain_zero<GT>(g, a.v);
-            continue;
-        }
-        const int64_t y = token_id(a, i);
-        const float xy = y >= 0 ? load1<GT>(x, y) : NAN;
-        RowRef r;
-        const float s = plain_sum<GT>(x, a.v, xy, &r, team);
-        const Logp lp = row_logp(xy, r, s);
-        const PolicyTerms t =
-            policy_terms(lp, p.old[i], p.adv[i], p.kl != 0.0f ? a.ref[i] : 0.0f, p);
-        const float k = __fdiv_rn(w, norm);
-        if (threadIdx.x == 0) {
-            a.logps[i] = lp.hi;
-            add_policy(sums, t, p, k);
-        }
-        plain_grad<GT>(x, g, a.v, y, r, s, __fmul_rn(__fmul_rn(t.slope, k), scale));
-    }
-    if (threadIdx.x == 0)
-        for (int k = 0; k < 4; ++k) block_sums[k] = sums[k].wide();
-    __syncwarp();
-    if (threadIdx.x < 32)
-        join_sums(a, threadIdx.x < 4 ? block_sums[threadIdx.x] : 0.0, first_launch, last_launch);
-}
-
-template <int GT>
-__global__ void __launch_bounds__(kRowThreads)
-    preference_backward(const TokenArgs a, const PreferenceArgs p, int64_t begin, int64_t end) {
+    plain_backward(const TokenArgs a, const PreferenceArgs p, int64_t begin, int64_t end) {
     pdl_enter();
     const float scale = out_scale(a);
     for (int64_t i = begin + blockIdx.x; i < end; i += gridDim.x) {
@@ -565,7 +538,7 @@ __global__ void __launch_bounds__(kRowThreads)
             plain_zero<GT>(g, a.v);
             continue;
         }
-        const float c = __fmul_rn(__fmul_rn(p.coef[p.seq[i]], w), scale);
+        const float c = row_coef(p, i, w, scale);
         const float s = p.row_sum[i];
         plain_grad<GT>(row_of<GT>(a.x, i, a.x_stride), g, a.v, token_id(a, i),
                        RowRef{p.row_ref[i], !(s < 0.0f)}, fabsf(s), c);
@@ -704,7 +677,7 @@ constexpr int kZeroBytes = 4096;
 constexpr size_t kStagedSmem =
     static_cast<size_t>(kSlots) * kChunk + kZeroBytes + 8 * kShareRows;
 
-enum class Pass { kPolicy, kPreferenceBackward };
+enum class Pass { kPolicy, kBackward };
 
 // A row's bytes: `head` elements up to the first 16-byte boundary, `body` bytes
 // in whole 16-byte vectors from there, `tail` elements after them (a row
@@ -831,13 +804,11 @@ struct Ring {
             parity ^= 1u;
         }
     }
-    __device__ __forceinline__ void skip(uint32_t chunks) {   // at most kSlots
+    // any number: a row of the backward pass may be longer than the ring
+    __device__ __forceinline__ void skip(uint32_t chunks) {
         chunk += chunks;
-        slot += static_cast<int>(chunks);
-        if (slot >= kSlots) {
-            slot -= kSlots;
-            parity ^= 1u;
-        }
+        slot = static_cast<int>(chunk % kSlots);
+        parity = chunk / kSlots & 1u;
     }
 };
 
@@ -1062,7 +1033,7 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
                 } else {
                     q.w = token_weight(a, i);
                     q.y = static_cast<int32_t>(token_id(a, i));
-                    q.f[0] = __fmul_rn(__fmul_rn(p.coef[p.seq[i]], q.w), scale);
+                    q.f[0] = row_coef(p, i, q.w, scale);
                     q.f[1] = p.row_ref[i];
                     q.f[2] = p.row_sum[i];
                 }
@@ -1403,7 +1374,12 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
                     save_row(p, i, my_ref, my_sum);
                 } else {
                     const PolicyTerms pt = policy_terms(lp, mine.f[0], mine.f[1], mine.f[2], pol);
-                    add_policy(sums, pt, pol, __fdiv_rn(mine.w, norm));
+                    const float k = __fdiv_rn(mine.w, norm);
+                    add_policy(sums, pt, pol, k);
+                    if (p.term != nullptr) {      // for a backward pass of its own
+                        p.term[i] = __fmul_rn(pt.slope, k);
+                        save_row(p, i, my_ref, my_sum);
+                    }
                 }
             }
             if constexpr (PREF) rows_done(a, t, q, &ready);
@@ -1529,21 +1505,11 @@ cudaError_t go_forward(const TokenArgs& a, const PreferenceArgs& p, const PairTa
 }
 
 template <int GT>
-cudaError_t go_policy(const TokenArgs& a, const PolicyArgs& p, bool staged, int64_t begin,
-                      int64_t end, cudaStream_t s) {
-    if (a.grad == nullptr)
-        return go_stream<GT>(a, p, PreferenceArgs{}, NoTable{0}, begin, end, s);
-    if (staged) return go_staged<GT, Pass::kPolicy>(a, p, PreferenceArgs{}, begin, end, s);
-    return launch_after(policy_rows<GT>, dim3(row_blocks(end - begin, 2)), dim3(kRowThreads), 0,
-                        s, a, p, begin, end, begin == 0, end == a.n);
-}
-template <int GT>
 cudaError_t go_backward(const TokenArgs& a, const PreferenceArgs& p, int64_t begin, int64_t end,
                         bool staged, cudaStream_t s) {
-    if (staged)
-        return go_staged<GT, Pass::kPreferenceBackward>(a, PolicyArgs{}, p, begin, end, s);
-    return launch_after(preference_backward<GT>, dim3(row_blocks(end - begin, 2)),
-                        dim3(kRowThreads), 0, s, a, p, begin, end);
+    if (staged) return go_staged<GT, Pass::kBackward>(a, PolicyArgs{}, p, begin, end, s);
+    return launch_after(plain_backward<GT>, dim3(row_blocks(end - begin, 2)), dim3(kRowThreads),
+                        0, s, a, p, begin, end);
 }
 
 }  // namespace
@@ -1561,11 +1527,23 @@ cudaError_t read_loss_status(unsigned int* status, bool clear) {
 
 int64_t loss_rows_per_launch() { return static_cast<int64_t>(kShareRows) * device_sms(); }
 
-cudaError_t launch_policy_loss(const TokenArgs& a, const PolicyArgs& p, int dtype, bool staged,
-                               int64_t begin, int64_t end, cudaStream_t s) {
-    const cudaError_t e = dtype == kGradF32   ? go_policy<kGradF32>(a, p, staged, begin, end, s)
-                          : dtype == kGradF16 ? go_policy<kGradF16>(a, p, staged, begin, end, s)
-                                              : go_policy<kGradBF16>(a, p, staged, begin, end, s);
+cudaError_t launch_policy_staged(const TokenArgs& a, const PolicyArgs& pol, int64_t begin,
+                                 int64_t end, int dtype, cudaStream_t s) {
+    const PreferenceArgs none{};
+    const cudaError_t e =
+        dtype == kGradF32   ? go_staged<kGradF32, Pass::kPolicy>(a, pol, none, begin, end, s)
+        : dtype == kGradF16 ? go_staged<kGradF16, Pass::kPolicy>(a, pol, none, begin, end, s)
+                            : go_staged<kGradBF16, Pass::kPolicy>(a, pol, none, begin, end, s);
+    note_launch();
+    return e;
+}
+cudaError_t launch_policy_forward(const TokenArgs& a, const PolicyArgs& pol,
+                                  const PreferenceArgs& p, int64_t begin, int64_t end, int dtype,
+                                  cudaStream_t s) {
+    const NoTable t{0};
+    const cudaError_t e = dtype == kGradF32   ? go_stream<kGradF32>(a, pol, p, t, begin, end, s)
+                          : dtype == kGradF16 ? go_stream<kGradF16>(a, pol, p, t, begin, end, s)
+                                              : go_stream<kGradBF16>(a, pol, p, t, begin, end, s);
     note_launch();
     return e;
 }
@@ -1578,9 +1556,8 @@ cudaError_t launch_preference_forward(const TokenArgs& a, const PreferenceArgs& 
     note_launch();
     return e;
 }
-cudaError_t launch_preference_backward(const TokenArgs& a, const PreferenceArgs& p, int64_t begin,
-                                       int64_t end, int dtype, bool staged,
-                                       cudaStream_t stream) {
+cudaError_t launch_loss_backward(const TokenArgs& a, const PreferenceArgs& p, int64_t begin,
+                                 int64_t end, int dtype, bool staged, cudaStream_t stream) {
     const cudaError_t e =
         dtype == kGradF32   ? go_backward<kGradF32>(a, p, begin, end, staged, stream)
         : dtype == kGradF16 ? go_backward<kGradF16>(a, p, begin, end, staged, stream)

@@ -289,15 +289,24 @@ int norm_some(const void* const* grads, const int64_t* numels, int32_t n, int32_
 
 int64_t loss_words(int64_t n_tokens, int64_t n_pairs) { return 4 * n_tokens + 2 * n_pairs; }
 
-// Whether the rows of logits and gradient take the staged kernels: they fit
-// shared memory, and every gradient row lies as far past a 16-byte boundary as
-// its logits row, so that a row's staged bytes can be stored back in bulk.
-bool staged_rows(const shardstep_token_loss_t* a) {
-    if (!loss_row_fits(a->vocab, a->dtype)) return false;
-    const uintptr_t off = reinterpret_cast<uintptr_t>(a->grad) -
-                          reinterpret_cast<uintptr_t>(a->logits);
-    const int64_t step = (a->grad_stride - a->row_stride) * elem_size(a->dtype);
+// Whether every gradient row lies as far past a 16-byte boundary as its logits
+// row, so that a row's staged bytes can be stored back in bulk.
+bool same_offsets(const shardstep_token_loss_t* a) {
+    const uint64_t off = reinterpret_cast<uintptr_t>(a->grad) -
+                         reinterpret_cast<uintptr_t>(a->logits);
+    const uint64_t step = (static_cast<uint64_t>(a->grad_stride) -
+                           static_cast<uint64_t>(a->row_stride)) * elem_size(a->dtype);
     return off % 16 == 0 && step % 16 == 0;
+}
+
+// The per-token words of a workspace.
+PreferenceArgs loss_words_at(void* workspace, int64_t tokens) {
+    float* words = reinterpret_cast<float*>(static_cast<LossWork*>(workspace) + 1);
+    PreferenceArgs p{};
+    p.row_ref = words;
+    p.row_sum = words + tokens;
+    p.term = words + 2 * tokens;
+    return p;
 }
 
 // The checks both losses share; fills the kernel arguments.
@@ -451,7 +460,7 @@ int tensors_grad_norm(const void* const* grads, const int64_t* numels, int32_t n
 
 int64_t token_loss_workspace_bytes(int64_t n_tokens, int32_t n_pairs) {
     if (n_tokens < 0 || n_tokens > INT32_MAX || n_pairs < 0) return -1;
-    return static_cast<int64_t>(sizeof(LossWork)) + 4 * loss_words(n_pairs ? n_tokens : 0, n_pairs);
+    return static_cast<int64_t>(sizeof(LossWork)) + 4 * loss_words(n_tokens, n_pairs);
 }
 
 int token_policy_loss(const shardstep_token_loss_t* args, const float* old_logps,
@@ -461,10 +470,15 @@ int token_policy_loss(const shardstep_token_loss_t* args, const float* old_logps
     if (!(clip_low >= 0.0f && clip_low <= 1.0f) || !(clip_high >= 0.0f) ||
         !std::isfinite(clip_high) || !(kl_coef >= 0.0f) || !std::isfinite(kl_coef))
         return ready_fail(SHARDSTEP_ERR_INVALID, "clip_low, clip_high or kl_coef out of range");
+    // in one pass where a row fits an SM's shared memory; else forward, then backward
+    const bool one_pass = args->vocab >= 1 && args->vocab <= (int64_t{1} << 28) &&
+                          loss_row_fits(args->vocab, args->dtype) && same_offsets(args);
+    const bool two_passes = args->grad != nullptr && !one_pass;
+    const int64_t need = two_passes ? token_loss_workspace_bytes(args->n_tokens, 0)
+                                    : static_cast<int64_t>(sizeof(LossWork));
     TokenArgs k{};
     std::vector<Range> reads, writes;
-    if (int rc = take_tokens(args, sizeof(LossWork), &k, &reads, &writes); rc != SHARDSTEP_OK)
-        return rc;
+    if (int rc = take_tokens(args, need, &k, &reads, &writes); rc != SHARDSTEP_OK) return rc;
     if (args->n_tokens == 0) return ready_ok();
     if (!old_logps || !advantages || (kl_coef != 0.0f && !args->ref_logps))
         return ready_fail(SHARDSTEP_ERR_INVALID, "old_logps / advantages / ref_logps is NULL");
@@ -474,19 +488,27 @@ int token_policy_loss(const shardstep_token_loss_t* args, const float* old_logps
     add_range(reads, advantages, args->n_tokens * 4);
     if (int rc = check_ranges(&reads, &writes); rc != SHARDSTEP_OK) return rc;
     const PolicyArgs p{old_logps, advantages, 1.0f - clip_low, 1.0f + clip_high, kl_coef};
-    const bool staged = k.grad != nullptr && staged_rows(args);
+    const PreferenceArgs words =
+        two_passes ? loss_words_at(args->workspace, k.n) : PreferenceArgs{};
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int64_t most = loss_rows_per_launch();
-    for (int64_t row = 0; row < k.n; row += most) {
-        const cudaError_t e =
-            launch_policy_loss(k, p, args->dtype, staged, row, std::min(k.n, row + most),
-                               static_cast<cudaStream_t>(stream));
-        if (e != cudaSuccess)
-            return ready_fail(SHARDSTEP_ERR_CUDA, "policy loss launch: %s",
-                              cudaGetErrorString(e));
+    cudaError_t e = cudaSuccess;
+    for (int64_t row = 0; e == cudaSuccess && row < k.n; row += most) {
+        const int64_t end = std::min(k.n, row + most);
+        if (k.grad != nullptr && one_pass) {
+            e = launch_policy_staged(k, p, row, end, args->dtype, s);
+            continue;
+        }
+        e = launch_policy_forward(k, p, words, row, end, args->dtype, s);
+        if (e == cudaSuccess && two_passes)
+            e = launch_loss_backward(k, words, row, end, args->dtype, same_offsets(args), s);
     }
-    record_kernel(k.grad == nullptr ? "stream_forward<%s> (TMA-staged)"
-                  : staged          ? "staged_rows<%s, policy> (TMA-staged)"
-                                    : "policy_rows<%s>",
+    if (e != cudaSuccess)
+        return ready_fail(SHARDSTEP_ERR_CUDA, "policy loss launch: %s", cudaGetErrorString(e));
+    record_kernel(k.grad == nullptr    ? "stream_forward<%s> (TMA-staged)"
+                  : one_pass           ? "staged_rows<%s, policy> (TMA-staged)"
+                  : same_offsets(args) ? "staged_rows<%s, backward> (TMA-staged)"
+                                       : "plain_backward<%s>",
                   dtype_name(args->dtype));
     return ready_ok();
 } catch (const std::bad_alloc&) {
@@ -525,18 +547,14 @@ int token_preference_loss(const shardstep_token_loss_t* args, const int64_t* seq
     add_range(writes, log_ratios, 8 * static_cast<int64_t>(n_pairs));
     if (int rc = check_ranges(&reads, &writes); rc != SHARDSTEP_OK) return rc;
     if (k.norm == 0.0f) k.norm = static_cast<float>(n_pairs);
-    float* words = reinterpret_cast<float*>(k.ws + 1);
-    PreferenceArgs p{beta,
-                     label_smoothing,
-                     log_ratios,
-                     words,
-                     words + tokens,
-                     words + 2 * tokens,
-                     reinterpret_cast<int32_t*>(words + 3 * tokens),
-                     words + 4 * tokens,
-                     1,
-                     0};
-    const bool staged = k.grad != nullptr && staged_rows(args);
+    PreferenceArgs p = loss_words_at(k.ws, tokens);
+    p.beta = beta;
+    p.smoothing = label_smoothing;
+    p.log_ratios = log_ratios;
+    p.seq = reinterpret_cast<int32_t*>(p.term + tokens);
+    p.coef = p.term + 2 * tokens;
+    p.first = 1;
+    const bool staged = k.grad != nullptr && same_offsets(args);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     std::unique_ptr<PairTableLarge> t(new PairTableLarge);
     const int64_t most = loss_rows_per_launch();
@@ -557,8 +575,7 @@ int token_preference_loss(const shardstep_token_loss_t* args, const int64_t* seq
             e = launch_preference_forward(k, p, *t, r, std::min(end, r + most), args->dtype, s);
         if (k.grad != nullptr)
             for (int64_t r = begin; e == cudaSuccess && r < end; r += most)
-                e = launch_preference_backward(k, p, r, std::min(end, r + most), args->dtype,
-                                               staged, s);
+                e = launch_loss_backward(k, p, r, std::min(end, r + most), args->dtype, staged, s);
         if (e != cudaSuccess)
             return ready_fail(SHARDSTEP_ERR_CUDA, "preference loss launch: %s",
                               cudaGetErrorString(e));
@@ -567,8 +584,8 @@ int token_preference_loss(const shardstep_token_loss_t* args, const int64_t* seq
         p.coef += 2 * static_cast<int64_t>(t->pairs);
     }
     record_kernel(k.grad == nullptr ? "stream_forward<%s> (TMA-staged)"
-                  : staged          ? "staged_rows<%s, preference> (TMA-staged)"
-                                    : "preference_backward<%s>",
+                  : staged          ? "staged_rows<%s, backward> (TMA-staged)"
+                                    : "plain_backward<%s>",
                   dtype_name(args->dtype));
     return ready_ok();
 } catch (const std::bad_alloc&) {

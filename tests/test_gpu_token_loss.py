@@ -156,6 +156,20 @@ def test_many_wide_rows_per_block(v, dt):
     _check_pref(c, lens, _run_pref(c, lens, g), dt)
 
 
+@pytest.mark.parametrize("v,dt,shift", [(128256, "bf16", 0), (60001, "f32", 0),
+                                        (128256, "f16", 1), (230001, "bf16", 0)])
+def test_many_rows_longer_than_shared_memory(v, dt, shift):
+    """Rows that do not fit an SM's shared memory, several per block: the losses
+    take a forward and a backward pass, whose teams skip rows of more chunks than
+    there are slots.  Also with the gradient at another offset than the logits."""
+    n = 400
+    c = _inputs(n, v, dt, seed=v, masked=0.15)
+    _, g = _grad_buffer(n, v, dt, v, shift)
+    _check_policy(c, _run_policy(c, dt, grad=g), dt, 0.05)
+    lens = [100, 50, 60, 190]
+    _check_pref(c, lens, _run_pref(c, lens, g), dt)
+
+
 def test_policy_forms():
     """int32 ids, no weights, a given norm, scales, forward only, in place."""
     n, v, dt = 12, 777, "bf16"
