@@ -575,22 +575,21 @@ struct Dealt {
     int n_live, n_dead;       // of the launch
     float weight;             // the sum of the launch's weights
 };
-// Where the rank-th of the things dealt out goes: to the blocks in turn, then to
-// each block's teams in turn, so that a row's block is the same whatever the
-// number of teams.
-struct Deal {
-    unsigned rank, block, team, place;
-    __device__ __forceinline__ Deal(unsigned r, unsigned teams)
-        : rank(r), block(r % gridDim.x), team(r / gridDim.x % teams),
-          place(r / gridDim.x / teams) {}
-    __device__ __forceinline__ void next(unsigned teams) {
-        if (++block < gridDim.x) return;
-        block = 0;
-        if (++team < teams) return;
-        team = 0;
-        ++place;
+// Of the things of one kind that a thread has found, the set bits of `rows` with
+// ranks from `rank` on, those dealt to block b go to its list: a rank goes to the
+// blocks in turn, then to each block's teams in turn, so that a row's block is the
+// same whatever the number of teams.  The block's rank is looked for, not each
+// row's block: one division per thread.
+__device__ __forceinline__ void take_share(unsigned rows, unsigned rank, unsigned row0, unsigned b,
+                                           unsigned teams, uint32_t* list) {
+    const unsigned end = rank + __popc(rows);
+    unsigned q = rank > b ? (rank - b + gridDim.x - 1) / gridDim.x : 0;
+    for (unsigned mine = b + q * gridDim.x; mine < end; mine += gridDim.x, ++q) {
+        unsigned left = rows;
+        for (unsigned k = rank; k < mine; ++k) left &= left - 1;
+        list[q % teams * (kShareRows / teams) + q / teams] = row0 + __ffs(left) - 1;
     }
-};
+}
 // Fills the lists of the block's teams, each of up to kShareRows / teams rows;
 // every thread of the block calls it.  A thread takes 8 consecutive rows at a
 // time.
@@ -601,21 +600,22 @@ __device__ __forceinline__ Dealt deal_rows(const TokenArgs& a, int64_t begin, in
     __shared__ int counts[2][kWarps];
     __shared__ Sum2 sums[kWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const unsigned each = kShareRows / teams;
     unsigned live_before = 0;
     Sum2 weight{0.0f, 0.0f};
     int turn = 0;
     for (int64_t base = begin; base < end; base += THREADS * kRows, turn ^= 1) {
         const int64_t i0 = base + kRows * tid;
+        const int here = i0 >= end ? 0 : end - i0 < kRows ? static_cast<int>(end - i0) : kRows;
         float w[kRows];
 #pragma unroll
-        for (int k = 0; k < kRows; ++k) w[k] = i0 + k < end ? a.w[i0 + k] : 0.0f;
-        unsigned own = 0;
+        for (int k = 0; k < kRows; ++k) w[k] = k < here ? a.w[i0 + k] : 0.0f;
+        unsigned alive = 0;
 #pragma unroll
         for (int k = 0; k < kRows; ++k) {
-            own += w[k] != 0.0f;
+            alive |= w[k] != 0.0f ? 1u << k : 0u;
             weight.add(w[k]);
         }
+        const unsigned own = __popc(alive);
         unsigned upto = own;                 // live rows up to this thread's last
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -632,18 +632,10 @@ __device__ __forceinline__ Dealt deal_rows(const TokenArgs& a, int64_t begin, in
             total += c;
         }
         const unsigned row0 = static_cast<unsigned>(i0 - begin);
-        Deal l(live_before + below + upto - own, teams), d(row0 - l.rank, teams);
-#pragma unroll
-        for (int k = 0; k < kRows; ++k) {
-            if (i0 + k >= end) break;
-            if (w[k] != 0.0f) {
-                if (l.block == blockIdx.x) live[l.team * each + l.place] = row0 + k;
-                l.next(teams);
-            } else {
-                if (d.block == gridDim.x - 1 - blockIdx.x) dead[d.team * each + d.place] = row0 + k;
-                d.next(teams);
-            }
-        }
+        const unsigned rank = live_before + below + upto - own;
+        take_share(alive, rank, row0, blockIdx.x, teams, live);
+        take_share(~alive & ((1u << here) - 1), row0 - rank, row0, gridDim.x - 1 - blockIdx.x,
+                   teams, dead);
         live_before += total;
     }
     weight = warp_sum(weight);
