@@ -591,51 +591,55 @@ __device__ __forceinline__ void take_share(unsigned rows, unsigned rank, unsigne
     }
 }
 // Fills the lists of the block's teams, each of up to kShareRows / teams rows;
-// every thread of the block calls it.  A thread takes 8 consecutive rows at a
-// time.
+// every thread of the block calls it.  A warp takes 8 times 32 consecutive rows
+// at a time, and its lanes 0-7 and 8-15 look among these for the block's live and
+// masked ones; the next weights are on their way meanwhile.
 template <int THREADS>
 __device__ __forceinline__ Dealt deal_rows(const TokenArgs& a, int64_t begin, int64_t end,
                                            unsigned teams, uint32_t* live, uint32_t* dead) {
-    constexpr int kWarps = THREADS / 32, kRows = 8;
-    __shared__ int counts[2][kWarps];
+    constexpr int kWarps = THREADS / 32, kGroups = 8, kStep = THREADS * kGroups;
+    __shared__ unsigned counts[2][kWarps];
     __shared__ Sum2 sums[kWarps];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = lane % kGroups;
+    const unsigned n = static_cast<unsigned>(end - begin);
     unsigned live_before = 0;
     Sum2 weight{0.0f, 0.0f};
+    float w[kGroups];
+    const auto fetch = [&](unsigned base) {
+#pragma unroll
+        for (int k = 0; k < kGroups; ++k) {
+            const unsigned r = base + 32 * (kGroups * warp + k) + lane;
+            w[k] = r < n ? a.w[begin + r] : 0.0f;
+        }
+    };
+    fetch(0);
     int turn = 0;
-    for (int64_t base = begin; base < end; base += THREADS * kRows, turn ^= 1) {
-        const int64_t i0 = base + kRows * tid;
-        const int here = i0 >= end ? 0 : end - i0 < kRows ? static_cast<int>(end - i0) : kRows;
-        float w[kRows];
+    for (unsigned base = 0; base < n; base += kStep, turn ^= 1) {
+        unsigned alive = 0, before = 0, own = 0;   // this lane's group; live rows of the warp
 #pragma unroll
-        for (int k = 0; k < kRows; ++k) w[k] = k < here ? a.w[i0 + k] : 0.0f;
-        unsigned alive = 0;
-#pragma unroll
-        for (int k = 0; k < kRows; ++k) {
-            alive |= w[k] != 0.0f ? 1u << k : 0u;
+        for (int k = 0; k < kGroups; ++k) {
+            const unsigned m = __ballot_sync(kFull, w[k] != 0.0f);
+            if (k == group) {
+                alive = m;
+                before = own;
+            }
+            own += __popc(m);
             weight.add(w[k]);
         }
-        const unsigned own = __popc(alive);
-        unsigned upto = own;                 // live rows up to this thread's last
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const unsigned x = __shfl_up_sync(kFull, upto, d);
-            if (lane >= d) upto += x;
-        }
-        if (lane == 31) counts[turn][warp] = upto;
+        fetch(base + kStep);
+        if (lane == 0) counts[turn][warp] = own;
         __syncthreads();
-        unsigned below = 0, total = 0;
-#pragma unroll
-        for (int k = 0; k < kWarps; ++k) {
-            const unsigned c = counts[turn][k];
-            below += k < warp ? c : 0;
-            total += c;
-        }
-        const unsigned row0 = static_cast<unsigned>(i0 - begin);
-        const unsigned rank = live_before + below + upto - own;
-        take_share(alive, rank, row0, blockIdx.x, teams, live);
-        take_share(~alive & ((1u << here) - 1), row0 - rank, row0, gridDim.x - 1 - blockIdx.x,
-                   teams, dead);
+        const unsigned c = lane < kWarps ? counts[turn][lane] : 0;
+        const unsigned below = __reduce_add_sync(kFull, lane < warp ? c : 0);
+        const unsigned total = __reduce_add_sync(kFull, c);
+        const unsigned row0 = base + 32 * (kGroups * warp + group);
+        const unsigned here = row0 < n ? n - row0 : 0;
+        const unsigned rank = live_before + below + before;
+        if (lane < kGroups)
+            take_share(alive, rank, row0, blockIdx.x, teams, live);
+        else if (lane < 2 * kGroups)
+            take_share(~alive & (here < 32 ? (1u << here) - 1 : kFull), row0 - rank, row0,
+                       gridDim.x - 1 - blockIdx.x, teams, dead);
         live_before += total;
     }
     weight = warp_sum(weight);
