@@ -87,7 +87,9 @@ __device__ __forceinline__ int find_tensor(const Table& t, uint32_t b) {
 
 // The 32-bit step: the fused step's update (adamw_elem, so the bits are those
 // of the flat step at N_d = 1) over one block's chunk of a tensor.  Bound by
-// memory: (gradient + 24 + 2) bytes per element.
+// memory: (gradient + 24 + 2) bytes per element.  A chunk's loads are all issued
+// before its arithmetic.  124M elements in 148 tensors, bf16 gradients: 492 us,
+// 7.08 TB/s; 400M: 1563 us, 7.16 TB/s.
 template <int CAP, int GT, int PT>
 __global__ void __launch_bounds__(kListThreads)
     tensors_adamw32(const __grid_constant__ TensorTable<CAP> t,
@@ -289,8 +291,11 @@ __device__ __forceinline__ Pair divide2(Pair n, Pair d_neg, Pair y) {
 //   p -= (lr / bc1) m / (r / sqrt(bc2) + eps), with m and r before rounding
 // to their codes.  Bound by memory in the limit, (gradient + 8 + 4 + 2) bytes
 // per element, if the issue slots keep up: all arithmetic goes two elements to
-// an instruction, roots and quotients too where the block's values allow it.  (A warp that took 4 blocks in turn was slower, 379 us against
-// 359 for 124M elements: its loads no longer overlap other blocks' arithmetic.)
+// an instruction, roots and quotients too where the block's values allow it (344
+// us for 124M elements, 5.8 TB/s, with issue slots 67% busy; 360 with the IEEE
+// operations alone).  One block per warp: a warp that took 4 in turn needed 450 us
+// with the next block's loads in flight, for want of warps to hide a block's chain
+// of dependent operations behind.
 template <int CAP, int GT, int PT>
 __global__ void __launch_bounds__(kListThreads)
     tensors_adamw8(const __grid_constant__ TensorTable<CAP> t,
@@ -474,7 +479,8 @@ __global__ void __launch_bounds__(kListThreads)
 }
 
 // Codes -> fp32 moments: m = code * scale, v = (code * scale)^2.  A thread takes
-// 4 consecutive elements at 2 places 1024 apart.
+// 4 consecutive elements at 2 places 1024 apart.  Bound by memory: 124M elements
+// in 182 us, 6.85 TB/s.
 constexpr int kDecodeChunk = 2 * 4 * kListThreads;
 __global__ void __launch_bounds__(kListThreads)
     moments_decode(const uint8_t* __restrict__ M, const float* __restrict__ MS,
@@ -515,6 +521,7 @@ __global__ void __launch_bounds__(kListThreads)
 }
 
 // fp32 moments -> codes and scales, a warp per block, laid out as in the step.
+// For setting a state once; its loads are single elements.
 __global__ void __launch_bounds__(kListThreads)
     moments_encode(const float* __restrict__ Mi, const float* __restrict__ Vi, int64_t n,
                    uint8_t* __restrict__ M, float* __restrict__ MS, uint8_t* __restrict__ V,
@@ -605,7 +612,8 @@ __device__ __forceinline__ void add_squares(const uint4& raw, Pair* acc) {
 // a block takes in turn (b, b + gridDim, ...); the threads' sums are joined in
 // double in a fixed order, the blocks' likewise by the block that arrives
 // last, so the result does not depend on the order in which blocks run.
-// Bound by the one read of the gradients.
+// Bound by the one read of the gradients: 124M bf16 elements in 148 tensors take
+// 41.6 us, 6.0 TB/s; 400M 119 us, 6.7 TB/s.
 template <int CAP, int GT>
 __global__ void __launch_bounds__(kListThreads, 4)
     tensors_norm(const __grid_constant__ NormTable<CAP> t, const NormArgs a) {

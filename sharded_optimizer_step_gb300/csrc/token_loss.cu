@@ -525,7 +525,8 @@ __device__ __forceinline__ void plain_zero(char* g, int64_t v) {
 
 // The gradient of a row whose forward pass has left its sum, where gradient and
 // logits lie at different offsets from 16-byte boundaries and so cannot share a
-// vector: element by element.
+// vector: element by element, 16 loads of a thread in flight.  Bound by their
+// latency: 4096 rows of 32000 bf16 logits in some 205 us, 2.6 TB/s.
 template <int GT>
 __global__ void __launch_bounds__(kRowThreads)
     plain_backward(const TokenArgs a, const PreferenceArgs p, int64_t begin, int64_t end) {
@@ -880,9 +881,12 @@ __device__ __forceinline__ void zero_row(const TokenArgs& a, int64_t i, const ui
 //   parameter warp: the rows' weights, ids, logits of the ids and so on, 32
 //     rows ahead at a time; at the end it joins the blocks' sums, while the last
 //     rows are still being stored.
-// Every wait
-// is bounded: one that runs out sets a status bit, the block leaves at the end
-// of the row, and its copies in flight are waited for first.
+// Every wait is bounded: one that runs out sets a status bit, the block leaves at
+// the end of the row, and its copies in flight are waited for first.
+// Bound by the logits' read and the gradient's write.  Policy, with gradient: 4096
+// rows of 32000 bf16 logits, 30% masked, 81.5 us, 5.5 TB/s; 8192 rows of 50257, 25%
+// masked, 239 us, 6.0 TB/s.  Backward: 8111 rows of 32000, 30% masked, 148 us, 5.9
+// TB/s.
 constexpr int kTeams = 2;
 constexpr int kTeamThreads = 256, kTeamWarps = kTeamThreads / 32;
 constexpr int kWorkWarps = kTeams * kTeamWarps;
@@ -1195,7 +1199,9 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
 // summed.  Nothing is shared on the way; a team of W warps joins its sums once a
 // row, and what follows from a row's sum is formed for 32 rows at once, a row
 // per lane.  W = 16 where rows are few, so that a row's copies spread over the
-// SM's warps, else 4.  Bound by the one read of the logits.
+// SM's warps, else 4.  Bound by the one read of the logits: 8192 rows of 50257 bf16
+// logits, 25% masked, 103 us, 6.0 TB/s; 2048 rows of 32000 fp16, 10% masked, 29.9
+// us, 4.0 TB/s, of which 20 us stream and the rest starts and joins.
 constexpr int kStreamWarps = 16, kStreamThreads = 32 * kStreamWarps;
 constexpr int kStreamSlots = 3, kStreamChunk = 4096;
 constexpr size_t kStreamSmem =
