@@ -386,8 +386,9 @@ __device__ __forceinline__ void finish_pair(const TokenArgs& a, const Preference
     Sum2 r[2];
     for (int h = 0; h < 2; ++h) {
         Sum2 s{0.0f, 0.0f};
-        const int end = t.start[2 * q + h + 1];
-        for (int i = t.start[2 * q + h] + lane; i < end; i += 8 * 32) {
+        const unsigned end = t.start[2 * q + h + 1];
+        // unsigned: i may pass 2^31
+        for (unsigned i = t.start[2 * q + h] + lane; i < end; i += 8 * 32) {
             float x[8];          // in flight together
 #pragma unroll
             for (int k = 0; k < 8; ++k) x[k] = i + 32 * k < end ? __ldcg(p.term + i + 32 * k) : 0.0f;
