@@ -7,6 +7,7 @@
 #include <cstddef>
 #include <memory>
 #include <new>
+#include <utility>
 #include <vector>
 
 #include "internal.h"
@@ -83,11 +84,11 @@ int take_groups(const shardstep_adamw_t* hp, const shardstep_adamw_state_t* cons
     return SHARDSTEP_OK;
 }
 
-int check_tensors(const void* const* grads, const shardstep_tensor_t* ts, int32_t n, int gs, int bits, int32_t n_groups,
-                  int64_t* total) {
-    *total = 0;
-    std::vector<Range> reads, writes;
-    reads.reserve(n);
+// `reads`: the words and states that the step reads besides the gradients.
+int check_tensors(const void* const* grads, const shardstep_tensor_t* ts, int32_t n, int gs,
+                  int bits, int32_t n_groups, std::vector<Range> reads) {
+    std::vector<Range> writes;
+    reads.reserve(reads.size() + n);
     writes.reserve(static_cast<size_t>(n) * (bits == 8 ? 6 : 4));
     const int ms = bits == 8 ? 1 : 4;
     for (int32_t i = 0; i < n; ++i) {
@@ -105,7 +106,6 @@ int check_tensors(const void* const* grads, const shardstep_tensor_t* ts, int32_
             !aligned(t.v, ms) || (t.param && !aligned(t.param, 2)) ||
             (bits == 8 && (!aligned(t.m_scale, 4) || !aligned(t.v_scale, 4))))
             return ready_fail(SHARDSTEP_ERR_INVALID, "tensor %d: an array misaligned", i);
-        *total += t.numel;
         add_range(reads, grads[i], t.numel * gs);
         add_range(writes, t.master, t.numel * 4);
         add_range(writes, t.m, t.numel * ms);
@@ -122,7 +122,7 @@ int check_tensors(const void* const* grads, const shardstep_tensor_t* ts, int32_
     if (self_overlap(writes))
         return ready_fail(SHARDSTEP_ERR_INVALID, "two of the tensors' outputs overlap");
     if (cross_overlap(reads, writes))
-        return ready_fail(SHARDSTEP_ERR_INVALID, "a gradient overlaps an output");
+        return ready_fail(SHARDSTEP_ERR_INVALID, "an input overlaps an output");
     return SHARDSTEP_OK;
 }
 
@@ -195,8 +195,14 @@ int adamw_step(const void* const* grads, const shardstep_tensor_t* ts, int32_t n
     if (n == 0) return ready_ok();
     if (ts == nullptr || grads == nullptr)
         return ready_fail(SHARDSTEP_ERR_INVALID, "tensors / grads is NULL");
-    int64_t total = 0;
-    if (int rc = check_tensors(grads, ts, n, es, bits, n_groups, &total); rc != SHARDSTEP_OK) return rc;
+    std::vector<Range> reads;
+    add_range(reads, coef, coef ? 4 : 0);
+    add_range(reads, skip, skip ? 4 : 0);
+    for (int32_t g = 0; on_device && g < n_groups; ++g)
+        add_range(reads, states[g], sizeof(shardstep_adamw_state_t));
+    if (int rc = check_tensors(grads, ts, n, es, bits, n_groups, std::move(reads));
+        rc != SHARDSTEP_OK)
+        return rc;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     for (int32_t at = 0; at < n;) {
         const int rc = n - at <= kTensorsSmall

@@ -140,6 +140,20 @@ def test_tensors_adamw_step_refuses():
                                           None, None) == _capi.ERR_INVALID
 
 
+def test_step_words_may_not_lie_in_its_outputs():
+    """The factor, the skip word and the step states are read by every block while
+    others write."""
+    g, ts = _list()
+    inside = ts[0].master + 8
+    for kw in (dict(coef=inside), dict(skip=inside)):
+        assert _step(g, ts, **kw) == _capi.ERR_INVALID, kw
+        assert "overlap" in _capi.lib().shardstep_last_error().decode()
+    assert _capi.lib().tensors_state_adamw_step(
+        _capi.ptr_array(g), ts, 2, 0, 0, 8, _capi.ptr_array([inside]), 1, None, None,
+        None) == _capi.ERR_INVALID
+    assert "overlap" in _capi.lib().shardstep_last_error().decode()
+
+
 def test_empty_lists_are_nothing_to_do():
     assert _step([], (_capi.Tensor * 0)()) == _capi.OK
     ts = (_capi.Tensor * 3)()                                   # numel 0, NULL arrays
