@@ -11,6 +11,7 @@ N_d data-parallel ranks are emulated as N_d buffers in one GPU's memory.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import struct
 from dataclasses import dataclass
@@ -72,6 +73,18 @@ def _stream(stream, device=None):
             return raw(device.index)
         stream = torch.cuda.current_stream(device)
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+
+
+def _on(stream, device):
+    """For what a call given a stream of its own allocates and fills: on that
+    stream, so that neither the fill nor a later use of the memory can run
+    beside the call's kernels."""
+    import torch
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = (torch.cuda.ExternalStream(handle, device=device) if handle
+                  else torch.cuda.default_stream(device))
+    return torch.cuda.stream(stream)
 
 
 def _dtype_code(t):
@@ -777,7 +790,8 @@ class LossWorkspace:
     """Device workspace of the token losses, kept from call to call so that a
     call allocates nothing once it is large enough.  It carries no results;
     calls that may run at the same time (on different streams) need
-    workspaces of their own."""
+    workspaces of their own, and calls on different streams that share one
+    must be ordered by the caller, as for any tensor."""
 
     def __init__(self, device="cuda"):
         self.device = device
@@ -790,6 +804,8 @@ class LossWorkspace:
         need = _loss_head() + 16 * n_tokens + 8 * pairs
         if self.nbytes < need:
             import torch
+            if self.buf is not None:      # a kernel on this stream may still use it
+                self.buf.record_stream(torch.cuda.current_stream(self.buf.device))
             self.buf = torch.zeros((need + 7) // 8, dtype=torch.int64, device=self.device)
             self.addr, self.nbytes = self.buf.data_ptr(), self.buf.numel() * 8
         return self.addr, self.nbytes, self.buf
@@ -839,8 +855,19 @@ _TOKEN_LOSS = struct.Struct("@QqiiQqqQQQQqffQQQq")
 assert _TOKEN_LOSS.size == ctypes.sizeof(_capi.TokenLoss)
 
 
+def _loss_buffers(workspace, n, pairs, device):
+    """A call's outputs, and the workspace's address, size and buffer."""
+    import torch
+    out = torch.empty(n + 4 + 2 * pairs, dtype=torch.float32, device=device)
+    if n == 0:
+        out.zero_()
+    if workspace is None:
+        workspace = LossWorkspace(device)
+    return out, workspace.at_least(n, pairs)
+
+
 def _token_args(logits, ids, weights, ref_logps, grad, grad_scale, loss_scale, norm, workspace,
-                pairs):
+                pairs, stream):
     """The checks both losses share; allocates their outputs.  Returns the C
     arguments, the statistics and the log probabilities, and the workspace
     buffer (which the caller holds until the launch)."""
@@ -878,13 +905,12 @@ def _token_args(logits, ids, weights, ref_logps, grad, grad_scale, loss_scale, n
     elif not norm > 0:
         raise ValueError("norm must be > 0 (None: the sum of the weights, or the pairs)")
     device = logits.device
-    out = torch.empty(n + 4 + 2 * pairs, dtype=f32, device=device)
-    if n == 0:
-        out.zero_()
+    if stream is None:
+        out, (ws, ws_bytes, held) = _loss_buffers(workspace, n, pairs, device)
+    else:
+        with _on(stream, device):
+            out, (ws, ws_bytes, held) = _loss_buffers(workspace, n, pairs, device)
     at = out.data_ptr()
-    if workspace is None:
-        workspace = LossWorkspace(device)
-    ws, ws_bytes, held = workspace.at_least(n, pairs)
     args = _TOKEN_LOSS.pack(
         logits.data_ptr(), row, _dtype_code(logits), id_bytes, ids.data_ptr(), n, v,
         _per_token(weights, n, "weights", f32) if weights is not None else 0,
@@ -917,7 +943,7 @@ def policy_loss(logits, ids, old_logps, advantages, *, ref_logps=None, weights=N
     ``GradScaler.scale``)."""
     import torch
     args, out, held = _token_args(logits, ids, weights, ref_logps, grad, grad_scale, loss_scale,
-                                  norm, workspace, 0)
+                                  norm, workspace, 0, stream)
     n = logits.shape[0]
     rc = _capi.lib().token_policy_loss(
         args, _per_token(old_logps, n, "old_logps", torch.float32),
@@ -949,7 +975,7 @@ def preference_loss(logits, ids, seq_lens, ref_logps, *, beta: float = 0.1,
     pairs = count // 2
     lens = struct.pack("@%dq" % count, *seq_lens)
     args, out, held = _token_args(logits, ids, weights, ref_logps, grad, grad_scale, loss_scale,
-                                  norm, workspace, pairs)
+                                  norm, workspace, pairs, stream)
     n = logits.shape[0]
     rc = _capi.lib().token_preference_loss(
         args, lens, pairs, beta, label_smoothing, out.data_ptr() + 4 * (n + 4),
@@ -1018,6 +1044,10 @@ def grad_norm_clip(grads, max_norm: float, *, loss_scale=None, found_inf=None, o
     if not len(grads) and out is None:
         raise ValueError("an empty list needs out")
     dev = grads.device if len(grads) else out.device
+    if stream is not None and (out is None or workspace is None):
+        with _on(stream, dev):
+            out = torch.empty(2, dtype=torch.float32, device=dev) if out is None else out
+            workspace = NormWorkspace(dev) if workspace is None else workspace
     if out is None:
         out = torch.empty(2, dtype=torch.float32, device=dev)
     elif out.dtype != torch.float32 or out.numel() != 2 or not out.is_cuda \
@@ -1052,8 +1082,9 @@ def moments_decode(m, m_scale, v, v_scale, out=None, stream=None):
     """8-bit moments (codes and scales in blocks of 256) -> fp32 (m, v)."""
     import torch
     if out is None:
-        out = (torch.empty(m.numel(), dtype=torch.float32, device=m.device),
-               torch.empty(m.numel(), dtype=torch.float32, device=m.device))
+        with _on(stream, m.device) if stream is not None else contextlib.nullcontext():
+            out = (torch.empty(m.numel(), dtype=torch.float32, device=m.device),
+                   torch.empty(m.numel(), dtype=torch.float32, device=m.device))
     n = _moment_args(m, m_scale, v, v_scale, *out)
     _capi.check("tensors_moments_decode", _capi.lib().tensors_moments_decode(
         m.data_ptr(), m_scale.data_ptr(), v.data_ptr(), v_scale.data_ptr(), n,
@@ -1081,7 +1112,8 @@ class TensorAdamW:
     elements).  ``hp`` is one ``AdamW`` or a list of up to 8, ``groups[t]``
     each tensor's index into it (e.g. no weight decay for norm vectors).
     ``t`` counts the steps; ``device_step_state`` moves the count to the
-    device for ``step_on_device``, which a CUDA graph can capture."""
+    device for ``step_on_device``, which a CUDA graph can capture.  ``stream``
+    is where the state is made and filled (None: the current one)."""
 
     def __init__(self, params, hp, groups=None, state_bits: int = 32, stream=None):
         import torch
@@ -1110,16 +1142,17 @@ class TensorAdamW:
             self.offsets.append(pos)
             pos += -(-n // blk) * blk
         self.flat = pos
-        self.master = torch.zeros(pos, dtype=torch.float32, device=dev)
-        for p, o, n in zip(self.params, self.offsets, self.numels):
-            self.master[o:o + n].copy_(p.reshape(-1))
-        code = torch.float32 if state_bits == 32 else torch.uint8
-        self.m = torch.zeros(pos, dtype=code, device=dev)
-        self.v = torch.zeros(pos, dtype=code, device=dev)
         self.m_scale = self.v_scale = None
-        if state_bits == 8:
-            self.m_scale = torch.zeros(pos // blk, dtype=torch.float32, device=dev)
-            self.v_scale = torch.zeros(pos // blk, dtype=torch.float32, device=dev)
+        with _on(stream, dev) if stream is not None else contextlib.nullcontext():
+            self.master = torch.zeros(pos, dtype=torch.float32, device=dev)
+            for p, o, n in zip(self.params, self.offsets, self.numels):
+                self.master[o:o + n].copy_(p.reshape(-1))
+            code = torch.float32 if state_bits == 32 else torch.uint8
+            self.m = torch.zeros(pos, dtype=code, device=dev)
+            self.v = torch.zeros(pos, dtype=code, device=dev)
+            if state_bits == 8:
+                self.m_scale = torch.zeros(pos // blk, dtype=torch.float32, device=dev)
+                self.v_scale = torch.zeros(pos // blk, dtype=torch.float32, device=dev)
         self._param_code = _dtype_code(self.params[0])
         self._table = (_capi.Tensor * len(self.params))()
         self._addrs = None
@@ -1137,7 +1170,10 @@ class TensorAdamW:
             [self.m_scale, self.v_scale] if self.state_bits == 8 else [])
         addrs = [b.data_ptr() for b in state] + [p.data_ptr() for p in self.params]
         if addrs != self._addrs:
-            _need_cuda(*state)
+            _need_cuda(*state, *self.params)
+            if any(p.numel() != n or _dtype_code(p) != self._param_code
+                   for p, n in zip(self.params, self.numels)):
+                raise ValueError("a parameter changed its size or dtype")
             es = 4 if self.state_bits == 32 else 1
             for t, row in enumerate(self._table):
                 o = self.offsets[t]
@@ -1203,8 +1239,10 @@ class TensorAdamW:
     def load_moments(self, m32, v32, stream=None):
         """Sets the moments from flat fp32 buffers laid out like ``master``."""
         if self.state_bits == 32:
-            self.m.copy_(m32)
-            self.v.copy_(v32)
+            with (_on(stream, self.m.device) if stream is not None
+                  else contextlib.nullcontext()):
+                self.m.copy_(m32)
+                self.v.copy_(v32)
         else:
             moments_encode(m32, v32, self.m, self.m_scale, self.v, self.v_scale, stream=stream)
 

@@ -68,3 +68,45 @@ def test_a_wait_that_runs_out_is_reported():
     assert torch.equal(ss.policy_loss(x, ids, z, z, grad=g).logps, want)
     torch.cuda.synchronize()
     assert ss.device_status() == 0
+
+
+@pytest.mark.parametrize("form", ["stream", "handle"])
+def test_a_stream_of_its_own_while_the_current_one_is_busy(form):
+    """Calls given `stream` allocate, fill and zero on it: nothing that they need is
+    left to the current stream, which is busy."""
+    n, v = 300, 1000
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(n, v, device="cuda", generator=g).bfloat16()
+    ids = torch.randint(0, v, (n,), device="cuda", generator=g)
+    z = torch.full((n,), -7.0, device="cuda")
+    adv = torch.randn(n, device="cuda", generator=g)
+    w = (torch.rand(n, device="cuda", generator=g) < 0.7).float()
+    params = [torch.randn(k, device="cuda", generator=g).bfloat16() for k in (5000, 300)]
+    grads = [torch.randn(k, device="cuda", generator=g).bfloat16() for k in (5000, 300)]
+
+    def run(stream, side):
+        d1, d2 = torch.empty_like(x), torch.empty_like(x)
+        p = [q.clone() for q in params]
+        torch.cuda.synchronize()
+        if stream is not None:
+            torch.cuda._sleep(int(2e8))          # about 0.1 s of the current stream
+        a = ss.policy_loss(x, ids, z, adv, weights=w, grad=d1, stream=stream)
+        b = ss.preference_loss(x, ids, [100, 50, 70, 80], z, weights=w, grad=d2, stream=stream)
+        c = ss.grad_norm_clip(grads, 1.0, stream=stream)
+        opt = ss.TensorAdamW(p, ss.AdamW(), state_bits=8, stream=stream)
+        opt.step(grads, grad_coef=c[1:], stream=stream)
+        m = opt.moments(stream=stream)
+        with torch.cuda.stream(side):
+            out = [t.cpu() for t in (a.stats, a.logps, d1, b.stats, b.log_ratios, d2, c, *m, *p)]
+        torch.cuda.synchronize()
+        return out
+
+    want = run(None, torch.cuda.current_stream())
+    side = torch.cuda.Stream()
+    # memory that is not zero where a workspace may land
+    junk = [torch.full((k,), -1, dtype=torch.int64, device="cuda") for k in (1 << 12, 1 << 14, 1 << 16)]
+    torch.cuda.synchronize()
+    del junk
+    got = run(side if form == "stream" else side.cuda_stream, side)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
