@@ -170,6 +170,22 @@ def test_many_rows_longer_than_shared_memory(v, dt, shift):
     _check_pref(c, lens, _run_pref(c, lens, g), dt)
 
 
+@pytest.mark.parametrize("shift", [0, 1])
+def test_more_rows_than_one_launch_takes(shift):
+    """Above 1024 rows per SM a call goes in several launches, which carry the sums
+    on; a sequence may begin in one launch and end in another."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    n, v, dt = 1024 * sms + 4321, 37, "bf16"
+    c = _inputs(n, v, dt, seed=21, masked=0.3)
+    buf, g = _grad_buffer(n, v, dt, v, shift)
+    _check_policy(c, _run_policy(c, dt, grad=g), dt, 0.05)
+    _check_untouched(buf, n, v, v, shift)
+    _check_policy(c, _run_policy(c, dt), dt, 0.05)
+    lens = [70_000, 20_000, 50_001, n - 140_001]
+    _check_pref(c, lens, _run_pref(c, lens, g), dt)
+    _check_untouched(buf, n, v, v, shift)
+
+
 def test_policy_forms():
     """int32 ids, no weights, a given norm, scales, forward only, in place."""
     n, v, dt = 12, 777, "bf16"
