@@ -928,8 +928,8 @@ def policy_loss(logits, ids, old_logps, advantages, *, ref_logps=None, weights=N
     of any stride) on the tokens ``ids`` [N], with a KL term against
     ``ref_logps`` when ``kl_coef`` > 0, in one launch (forward and backward in
     two where a row of logits exceeds 212992 bytes, or where the rows of
-    ``grad`` lie at other offsets from 16-byte boundaries than the logits',
-    which is slow: give it the logits' row stride):
+    ``grad`` lie at other offsets from 16-byte boundaries than the logits':
+    the logits' own row stride is the faster one):
 
         u = exp(logp - old_logps)
         loss = sum w (-min(u A, clip(u, 1 - clip_low, 1 + clip_high) A)

@@ -20,16 +20,15 @@
 //                   gradient and stored by bulk copies, while the next rows are on
 //                   their way: each logit read once, each gradient written once.
 //                   backward: the same ring without the sum, after a forward pass.
-//   plain_backward  a backward pass where the gradient's rows lie at other offsets
-//                   from 16-byte boundaries than the logits', so that a row's
-//                   staged bytes cannot be stored back in bulk.
+//   offset_backward  a backward pass where the gradient's rows lie at other offsets
+//                   from 16-byte boundaries than the logits'.
 // Which of them: the policy loss takes one pass of staged_rows where a row fits its
 // 13 slots of shared memory (4096 rows of 32000 bf16 logits: 90 us against 137 in
 // two passes), else stream_forward and a backward pass (2048 rows of 128256 bf16
 // logits: 262 us; the same in one kernel that read a row again from L2 through
 // registers: 1056).  The preference loss always takes two passes: a row's slope
-// needs the sums of its whole pair.  A gradient at other offsets costs
-// (4096 x 32000): 257 us against 90.
+// needs the sums of its whole pair.  A gradient at other offsets: 172 us for the
+// policy loss of 4096 x 32000, against 90.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -497,56 +496,6 @@ __device__ __forceinline__ float own_grad(float e, float sum, float cs) {
     return __fmul_rn(__fsub_rn(sum, e), cs);
 }
 
-// -------------------------------------------------- the plain backward pass
-
-// grad = c (1[y] - e / S), rounded once.
-template <int GT>
-__device__ __forceinline__ void plain_grad(const char* x, char* g, int64_t v, int64_t y, RowRef r,
-                                           float sum, float c) {
-    const float cs = __fdiv_rn(c, sum);
-    const auto put = [&](int64_t j, float xj) {
-        const float e = row_exp(xj, r);
-        store1<GT>(g, j, j == y ? own_grad(e, sum, cs) : -__fmul_rn(e, cs));
-    };
-    constexpr int U = 16;                 // loads in flight together
-    int64_t j = threadIdx.x;
-    for (; j + (U - 1) * kRowThreads < v; j += U * kRowThreads) {
-        float f[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) f[u] = load1<GT>(x, j + u * kRowThreads);
-#pragma unroll
-        for (int u = 0; u < U; ++u) put(j + u * kRowThreads, f[u]);
-    }
-    for (; j < v; j += kRowThreads) put(j, load1<GT>(x, j));
-}
-template <int GT>
-__device__ __forceinline__ void plain_zero(char* g, int64_t v) {
-    for (int64_t j = threadIdx.x; j < v; j += kRowThreads) store1<GT>(g, j, 0.0f);
-}
-
-// The gradient of a row whose forward pass has left its sum, where gradient and
-// logits lie at different offsets from 16-byte boundaries and so cannot share a
-// vector: element by element, 16 loads of a thread in flight.  Bound by their
-// latency: 4096 rows of 32000 bf16 logits in some 205 us, 2.6 TB/s.
-template <int GT>
-__global__ void __launch_bounds__(kRowThreads)
-    plain_backward(const TokenArgs a, const PreferenceArgs p, int64_t begin, int64_t end) {
-    pdl_enter();
-    const float scale = out_scale(a);
-    for (int64_t i = begin + blockIdx.x; i < end; i += gridDim.x) {
-        char* g = const_cast<char*>(row_of<GT>(a.grad, i, a.g_stride));
-        const float w = token_weight(a, i);
-        if (w == 0.0f) {
-            plain_zero<GT>(g, a.v);
-            continue;
-        }
-        const float c = row_coef(p, i, w, scale);
-        const float s = p.row_sum[i];
-        plain_grad<GT>(row_of<GT>(a.x, i, a.x_stride), g, a.v, token_id(a, i),
-                       RowRef{p.row_ref[i], !(s < 0.0f)}, fabsf(s), c);
-    }
-}
-
 // ------------------------------------------------------- shares of the rows
 
 // The rows of a launch are dealt out to `units` (blocks, or teams of warps): the
@@ -778,6 +727,133 @@ __device__ __forceinline__ uint4 grad_vector_slow(const uint4& u, RowRef r, Pair
         o[k] = mul2(make_pair(row_exp(x.x, r), row_exp(x.y, r)), f);
     }
     return pack_vector<GT>(o);
+}
+
+// ------------------------------------- the backward pass at other offsets
+
+// The 16 bytes that begin `shift` elements into lo, of lo and hi in turn.
+template <int GT>
+__device__ __forceinline__ uint4 join_vectors(const uint4& lo, const uint4& hi, int shift) {
+    uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    const int words = GT == kGradF32 ? shift : shift >> 1;
+    if (words & 2)
+#pragma unroll
+        for (int k = 0; k < 6; ++k) w[k] = w[k + 2];
+    if (words & 1)
+#pragma unroll
+        for (int k = 0; k < 5; ++k) w[k] = w[k + 1];
+    if (GT != kGradF32 && (shift & 1))
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(w[k], w[k + 1], 16);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// Elements [from, to) of a vector, one by one.
+template <int GT>
+__device__ __forceinline__ void store_some(char* at, const uint4& o, int from, int to) {
+    const uint32_t w[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+    for (int e = 0; e < 16 / elem_bytes<GT>(); ++e) {
+        if (e < from || e >= to) continue;
+        if constexpr (GT == kGradF32)
+            reinterpret_cast<uint32_t*>(at)[e] = w[e];
+        else
+            reinterpret_cast<uint16_t*>(at)[e] = static_cast<uint16_t>(w[e / 2] >> (16 * (e % 2)));
+    }
+}
+// Element e of a vector replaced by x.
+template <int GT>
+__device__ __forceinline__ uint4 with_element(const uint4& o, int e, float x) {
+    uint32_t w[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if constexpr (GT == kGradF32) {
+            if (e == k) w[k] = __float_as_uint(x);
+        } else {
+            const uint32_t bits = pack_pair<GT>(make_pair(x, 0.0f)) & 0xFFFFu;
+            if (e == 2 * k) w[k] = (w[k] & 0xFFFF0000u) | bits;
+            if (e == 2 * k + 1) w[k] = (w[k] & 0xFFFFu) | bits << 16;
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The gradient, c (1[y] - e / S), of rows whose forward pass has left S, where
+// gradient and logits lie at different offsets from 16-byte boundaries, so that a
+// staged row's bytes cannot be stored back in bulk.  A lane forms the gradient of
+// a whole vector of logits; with the next lane's it holds the 16 bytes between two
+// boundaries of the gradient's row.  What a warp's 32 vectors do not fill goes out
+// one element at a time.  Bound by memory and the loads' latency: 4096 rows of 32000
+// bf16 logits in 121 us, 4.3 TB/s (206 us with every element loaded and stored by
+// itself).
+template <int GT>
+__global__ void __launch_bounds__(kRowThreads, 2)
+    offset_backward(const TokenArgs a, const PreferenceArgs p, int64_t begin, int64_t end) {
+    constexpr int es = elem_bytes<GT>(), kElems = 16 / es, kStep = kRowThreads, U = 4;
+    pdl_enter();
+    const float scale = out_scale(a);
+    const int lane = threadIdx.x & 31;
+    for (int64_t i = begin + blockIdx.x; i < end; i += gridDim.x) {
+        char* g = const_cast<char*>(row_of<GT>(a.grad, i, a.g_stride));
+        const float w = token_weight(a, i);
+        if (w == 0.0f) {
+            const RowBytes b = row_bytes<GT>(g, a.v);
+            char* body = const_cast<char*>(b.body_at);
+            if (threadIdx.x < b.head) store1<GT>(g, threadIdx.x, 0.0f);
+            if (threadIdx.x < b.tail) store1<GT>(body + b.body, threadIdx.x, 0.0f);
+            for (uint32_t at = 16 * threadIdx.x; at < b.body; at += 16 * kStep)
+                __stcs(reinterpret_cast<uint4*>(body + at), make_uint4(0, 0, 0, 0));
+            continue;
+        }
+        const char* x = row_of<GT>(a.x, i, a.x_stride);
+        const RowBytes b = row_bytes<GT>(x, a.v);
+        const int64_t y = token_id(a, i);
+        const float sum = p.row_sum[i], s = fabsf(sum);
+        const RowRef r{p.row_ref[i], !(sum < 0.0f)};
+        const float cs = __fdiv_rn(row_coef(p, i, w, scale), s);
+        const FastRow fr = fast_row(r);
+        const Pair f = make_pair(-cs, -cs);
+        if (threadIdx.x < 32) {           // the elements outside whole vectors
+            int64_t edge = -1;
+            if (lane < 16 && lane < b.head) edge = lane;
+            if (lane >= 16 && lane - 16 < b.tail) edge = a.v - b.tail + lane - 16;
+            if (edge >= 0) {
+                const float e = row_exp(load1<GT>(x, edge), r);
+                store1<GT>(g, edge, edge == y ? own_grad(e, s, cs) : -__fmul_rn(e, cs));
+            }
+        }
+        char* to = g + b.head * es;       // the first whole vector's gradient
+        const int shift =
+            static_cast<int>((16 - (reinterpret_cast<uintptr_t>(to) & 15)) & 15) / es;
+        const int n = static_cast<int>(b.body / 16);
+        const int64_t yv = y >= b.head ? (y - b.head) / kElems : -1;
+        for (int v0 = threadIdx.x - lane; v0 < n; v0 += U * kStep) {
+            uint4 u[U];
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                const int at = v0 + k * kStep + lane;
+                u[k] = at < n ? ldcs16(reinterpret_cast<const uint4*>(b.body_at) + at)
+                              : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                const int at = v0 + k * kStep + lane;
+                if (at - lane >= n) break;
+                uint4 o = r.fast ? grad_vector<GT>(u[k], fr, f) : grad_vector_slow<GT>(u[k], r, f);
+                if (at == yv)
+                    o = with_element<GT>(o, static_cast<int>((y - b.head) % kElems),
+                                         own_grad(row_exp(load1<GT>(x, y), r), s, cs));
+                const uint4 next{__shfl_down_sync(kFull, o.x, 1), __shfl_down_sync(kFull, o.y, 1),
+                                 __shfl_down_sync(kFull, o.z, 1), __shfl_down_sync(kFull, o.w, 1)};
+                char* dst = to + static_cast<int64_t>(at) * 16;
+                if (shift == 0 ? at < n : lane < 31 && at + 1 < n)
+                    __stcs(reinterpret_cast<uint4*>(dst + shift * es),
+                           join_vectors<GT>(o, next, shift));
+                else if (at < n)
+                    store_some<GT>(dst, o, shift, kElems);
+                if (lane == 0) store_some<GT>(dst, o, 0, shift);
+            }
+        }
+    }
 }
 
 __device__ __forceinline__ void st_release(unsigned* p, unsigned x) {
@@ -1511,7 +1587,7 @@ template <int GT>
 cudaError_t go_backward(const TokenArgs& a, const PreferenceArgs& p, int64_t begin, int64_t end,
                         bool staged, cudaStream_t s) {
     if (staged) return go_staged<GT, Pass::kBackward>(a, PolicyArgs{}, p, begin, end, s);
-    return launch_after(plain_backward<GT>, dim3(row_blocks(end - begin, 2)), dim3(kRowThreads),
+    return launch_after(offset_backward<GT>, dim3(row_blocks(end - begin, 2)), dim3(kRowThreads),
                         0, s, a, p, begin, end);
 }
 

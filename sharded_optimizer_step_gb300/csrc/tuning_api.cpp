@@ -514,7 +514,7 @@ int token_policy_loss(const shardstep_token_loss_t* args, const float* old_logps
     record_kernel(k.grad == nullptr    ? "stream_forward<%s> (TMA-staged)"
                   : one_pass           ? "staged_rows<%s, policy> (TMA-staged)"
                   : same_offsets(args) ? "staged_rows<%s, backward> (TMA-staged)"
-                                       : "plain_backward<%s>",
+                                       : "offset_backward<%s>",
                   dtype_name(args->dtype));
     return ready_ok();
 } catch (const std::bad_alloc&) {
@@ -591,7 +591,7 @@ int token_preference_loss(const shardstep_token_loss_t* args, const int64_t* seq
     }
     record_kernel(k.grad == nullptr ? "stream_forward<%s> (TMA-staged)"
                   : staged          ? "staged_rows<%s, backward> (TMA-staged)"
-                                    : "plain_backward<%s>",
+                                    : "offset_backward<%s>",
                   dtype_name(args->dtype));
     return ready_ok();
 } catch (const std::bad_alloc&) {
