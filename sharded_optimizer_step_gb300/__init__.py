@@ -951,7 +951,8 @@ def policy_loss(logits, ids, old_logps, advantages, *, ref_logps=None, weights=N
         _stream(stream, logits.device))
     if rc:
         _capi.check("token_policy_loss", rc)
-    return PolicyLoss(out[:4], out[4:], grad)
+    stats, logps = out.split_with_sizes((4, n))     # one call for both views
+    return PolicyLoss(stats, logps, grad)
 
 
 def preference_loss(logits, ids, seq_lens, ref_logps, *, beta: float = 0.1,
@@ -982,7 +983,8 @@ def preference_loss(logits, ids, seq_lens, ref_logps, *, beta: float = 0.1,
         _stream(stream, logits.device))
     if rc:
         _capi.check("token_preference_loss", rc)
-    return PreferenceLoss(out[:3], out[n + 4:], out[4:n + 4], grad)
+    stats, _, logps, ratios = out.split_with_sizes((3, 1, n, count))
+    return PreferenceLoss(stats, ratios, logps, grad)
 
 
 # ------------------------------------------------------ lists of tensors
