@@ -263,6 +263,9 @@ constexpr int kTensorsLarge = 400;
 // Elements that share one scale of the 8-bit moments.
 constexpr int kMomentBlock = SHARDSTEP_MOMENT_BLOCK;
 
+// A launch's blocks in up to kNear runs of 2^near_shift, so that a block looks for
+// its tensor among those of its run, mostly one.
+constexpr int kNear = 128;
 template <int CAP>
 struct TensorTable {
     const void* grad[CAP];
@@ -276,6 +279,8 @@ struct TensorTable {
     uint32_t b0[CAP + 1];   // first block of each tensor; b0[count] = the launch's blocks
     uint16_t group[CAP];
     uint8_t vec[CAP];       // every array of the tensor takes 16-byte accesses
+    uint16_t near[kNear + 1];   // the tensor of block k << near_shift (the last one: of the end)
+    int32_t near_shift;
     int32_t count;
 };
 struct GroupScalars {

@@ -2,7 +2,7 @@
 // moments in 32 or in 8 bits, and the global gradient norm with its clipping
 // factor.  The list travels as a kernel parameter (a table of pointers and
 // block ranges), so a call keeps nothing on the device and copies nothing to
-// it; a block finds its tensor by a binary search of the table.
+// it; a block finds its tensor by a search of the table.
 //
 // 8-bit moments.  A tensor's elements are taken in blocks of 256; each block
 // keeps max|m| / 448 and max sqrt(v) / 1.9375 in fp32.  m is an e4m3 float of
@@ -73,16 +73,22 @@ __device__ __forceinline__ uint16_t pack1(float a) {
     return static_cast<uint16_t>(pack2<PT>(a, 0.0f) & 0xFFFFu);
 }
 
-// The tensor that block b of the launch belongs to.
+// The tensor among lo .. hi that block b of the launch belongs to.
 template <class Table>
-__device__ __forceinline__ int find_tensor(const Table& t, uint32_t b) {
-    int lo = 0, hi = t.count - 1;
+__device__ __forceinline__ int find_tensor(const Table& t, uint32_t b, int lo, int hi) {
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (t.b0[mid] <= b) lo = mid;
         else hi = mid - 1;
     }
     return lo;
+}
+
+// (A search of all of 148 tensors took a tenth of the 8-bit step's instructions.)
+template <int CAP>
+__device__ __forceinline__ int find_tensor(const TensorTable<CAP>& t, uint32_t b) {
+    const uint32_t k = b >> t.near_shift;
+    return find_tensor(t, b, t.near[k], t.near[k + 1]);
 }
 
 // The 32-bit step: the fused step's update (adamw_elem, so the bits are those
@@ -620,7 +626,7 @@ __global__ void __launch_bounds__(kListThreads, 4)
     pdl_enter();
     Pair acc[4] = {0, 0, 0, 0};
     const uint32_t chunks = t.b0[t.count];
-    int s = blockIdx.x < chunks ? find_tensor(t, blockIdx.x) : 0;
+    int s = blockIdx.x < chunks ? find_tensor(t, blockIdx.x, 0, t.count - 1) : 0;
     for (uint32_t b = blockIdx.x; b < chunks; b += gridDim.x) {
         while (b >= t.b0[s + 1]) ++s;
         const int64_t n = t.n[s];

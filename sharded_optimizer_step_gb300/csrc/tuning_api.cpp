@@ -166,6 +166,13 @@ int launch_some(const void* const* grads, const shardstep_tensor_t* ts, int32_t 
     if (k == 0) return SHARDSTEP_OK;
     tab->b0[k] = static_cast<uint32_t>(blocks);
     tab->count = k;
+    tab->near_shift = 0;
+    while ((blocks - 1) >> tab->near_shift >= kNear) ++tab->near_shift;
+    for (int r = 0, at_tensor = 0; r <= kNear; ++r) {
+        const uint64_t b = static_cast<uint64_t>(r) << tab->near_shift;
+        while (at_tensor < k - 1 && b >= tab->b0[at_tensor + 1]) ++at_tensor;
+        tab->near[r] = static_cast<uint16_t>(at_tensor);
+    }
     const cudaError_t e =
         launch_tensors_adamw<CAP>(*tab, grad_type, param_type, bits, gs, coef, skip, stream);
     if (e != cudaSuccess)
