@@ -297,8 +297,8 @@ __device__ __forceinline__ Pair divide2(Pair n, Pair d_neg, Pair y) {
 //   p -= (lr / bc1) m / (r / sqrt(bc2) + eps), with m and r before rounding
 // to their codes.  Bound by memory in the limit, (gradient + 8 + 4 + 2) bytes
 // per element, if the issue slots keep up: all arithmetic goes two elements to
-// an instruction, roots and quotients too where the block's values allow it (344
-// us for 124M elements, 5.8 TB/s, with issue slots 67% busy; 360 with the IEEE
+// an instruction, roots and quotients too where the block's values allow it (124M
+// elements in 326 us, 6.1 TB/s, with issue slots 64% busy; 16 us more with the IEEE
 // operations alone).  One block per warp: a warp that took 4 in turn needed 450 us
 // with the next block's loads in flight, for want of warps to hide a block's chain
 // of dependent operations behind.
