@@ -42,8 +42,7 @@ namespace {
 
 constexpr int kRowThreads = 512;              // threads of a plain kernel's block
 constexpr unsigned kFull = 0xFFFFFFFFu;
-// log2 e as the sum of two floats: the first alone is 1.3e-8 off, always to
-// the same side, which a sum over a sequence's tokens would gather up.
+// log2 e, and what the float lacks.
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLog2eLo = 1.9259629911e-8f;
 constexpr float kLn2 = 0.6931471805599453f, kLn2Hi = 2839.0f / 4096.0f,
@@ -122,6 +121,7 @@ __device__ __forceinline__ Sum2 warp_sum(Sum2 x) {
 template <int T>
 struct TeamShared {
     float part[2][T / 32];
+    float3 sums[2][T / 32];
     Sum2 wide[T / 32];
 };
 template <int T>
@@ -164,6 +164,22 @@ struct Team {
         for (int d = T / 64; d > 0; d >>= 1) x = __fadd_rn(x, __shfl_xor_sync(kFull, x, d));
         return x;
     }
+    // The same of three values at once.
+    __device__ __forceinline__ float3 sum(float3 x, bool* any, int turn) const {
+        const auto add = [&x](int d) {
+            x.x = __fadd_rn(x.x, __shfl_xor_sync(kFull, x.x, d));
+            x.y = __fadd_rn(x.y, __shfl_xor_sync(kFull, x.y, d));
+            x.z = __fadd_rn(x.z, __shfl_xor_sync(kFull, x.z, d));
+        };
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) add(d);
+        if ((tid & 31) == 0) sh->sums[turn][tid >> 5] = x;
+        *any = sync_or(*any);
+        x = sh->sums[turn][tid & (T / 32 - 1)];
+#pragma unroll
+        for (int d = T / 64; d > 0; d >>= 1) add(d);
+        return x;
+    }
     __device__ __forceinline__ float max(float x) const {
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, d));
@@ -195,7 +211,7 @@ struct RowRef {
     bool fast;
 };
 __device__ __forceinline__ float row_exp(float x, RowRef r) {
-    if (r.fast) return exp2_approx(__fmaf_rn(x, kLog2e, __fmaf_rn(x, kLog2eLo, -r.ref)));
+    if (r.fast) return exp2_approx(__fmaf_rn(x, kLog2e, -r.ref));
     const float d = __fsub_rn(x, r.ref);
     return exp2_approx(__fmaf_rn(d, kLog2e, __fmul_rn(d, kLog2eLo)));
 }
@@ -227,7 +243,7 @@ __device__ __forceinline__ Logp row_logp(float xy, RowRef r, float sum) {
         const Logp d = two_sum(xy, -r.ref), e = two_sum(d.hi, big);
         return two_sum(e.hi, __fadd_rn(__fadd_rn(d.lo, e.lo), small));
     }
-    const float t = __fmaf_rn(xy, kLog2e, __fmaf_rn(xy, kLog2eLo, -r.ref));
+    const float t = __fmaf_rn(xy, kLog2e, -r.ref);
     return two_sum(big, __fmaf_rn(t, kLn2, small));
 }
 // lp - x.
@@ -678,24 +694,61 @@ __device__ __forceinline__ uint32_t pack_pair(Pair p) {
 
 // The constants of a row's fast exponentials, both halves alike.
 struct FastRow {
-    Pair hi, lo, neg_ref;
+    Pair log2e, neg_ref;
 };
 __device__ __forceinline__ FastRow fast_row(RowRef r) {
-    return FastRow{make_pair(kLog2e, kLog2e), make_pair(kLog2eLo, kLog2eLo),
-                   make_pair(-r.ref, -r.ref)};
+    return FastRow{make_pair(kLog2e, kLog2e), make_pair(-r.ref, -r.ref)};
 }
-// acc += the fast exponentials of a vector.
+// A row's fast sum, and of one pair in each vector (a sample: a quarter of 16-bit
+// logits, half of fp32 ones) the exponentials of arguments from 0 on and the
+// exponentials times their arguments, for small_bias.
+struct RowSum {
+    Pair acc[2], above, moment;
+};
 template <int GT>
-__device__ __forceinline__ void sum_vector(const uint4& u, const FastRow& r, Pair* acc) {
+__device__ __forceinline__ void sum_vector(const uint4& u, const FastRow& r, RowSum* s) {
 #pragma unroll
     for (int k = 0; k < vec_pairs<GT>(); ++k) {
-        const Pair x = pair_of<GT>(u, k);
-        acc[k & 1] = add2(acc[k & 1], exp2_pair(fma2(x, r.hi, fma2(x, r.lo, r.neg_ref))));
+        const Pair t = fma2(pair_of<GT>(u, k), r.log2e, r.neg_ref), e = exp2_pair(t);
+        s->acc[k & 1] = add2(s->acc[k & 1], e);
+        if (k == 0) {
+            const float2 f = floats(t);
+            float a, b;
+            asm("set.ge.f32.f32 %0, %1, 0f00000000;" : "=f"(a) : "f"(f.x));
+            asm("set.ge.f32.f32 %0, %1, 0f00000000;" : "=f"(b) : "f"(f.y));
+            s->above = fma2(e, make_pair(a, b), s->above);
+            // of -inf, e = 0: no product with an infinity
+            s->moment = fma2(e, make_pair(fmaxf(f.x, -256.0f), fmaxf(f.y, -256.0f)), s->moment);
+        }
     }
 }
-// A vector's gradient without the id's own term, e f.  For 16-bit logits the
-// low part of log2 e is left out (below 2e-8 |x| of a value that is rounded to
-// 2^-9 or 2^-12).
+__device__ __forceinline__ float3 row_totals(const RowSum& s) {
+    const float2 a = floats(add2(s.acc[0], s.acc[1])), b = floats(s.above), c = floats(s.moment);
+    return float3{__fadd_rn(a.x, a.y), __fadd_rn(b.x, b.y), __fadd_rn(c.x, c.y)};
+}
+// What is to be taken off a fast row's log probability.  Two errors of some 5e-8
+// have one sign for most tokens, so that a sequence's summed log ratio would gather
+// them up (100 tokens: 2e-6, as much as a 32-bit log-softmax's random errors):
+//   ex2.approx's mean relative error, measured over all fractions, is -5.06e-8
+//     for arguments below 0 and +3.43e-8 from 0 on, whatever their integer part;
+//   the float log2 e is 1 - d of the number, d = 1.33e-8: every logit counts as
+//     x (1 - d), and the result is d (x_y - mean of x under the softmax) too small.
+//     (The low part's product cannot be added to an argument beyond 2: it is
+//     below half of its last place.)
+template <int GT>
+__device__ __forceinline__ float small_bias(float3 total, float xy, RowRef r) {
+    if (!r.fast) return 0.0f;
+    const float scale = __fdiv_rn(static_cast<float>(vec_pairs<GT>()), total.x);
+    const float share = fminf(__fmul_rn(total.y, scale), 1.0f);
+    const float mean = __fmul_rn(total.z, scale);
+    const float t = __fmaf_rn(xy, kLog2e, -r.ref);
+    return __fmaf_rn(share, -8.49e-8f, 5.06e-8f) -
+           __fmul_rn(kLog2eLo * kLn2 * kLn2, __fsub_rn(t, mean));
+}
+__device__ __forceinline__ Logp without(Logp lp, float bias) {
+    return Logp{lp.hi, __fsub_rn(lp.lo, bias)};
+}
+// A vector's gradient without the id's own term, e f.
 template <int GT>
 __device__ __forceinline__ uint4 pack_vector(const Pair* o) {
     if constexpr (GT == kGradF32) {
@@ -712,9 +765,7 @@ __device__ __forceinline__ uint4 grad_vector(const uint4& u, const FastRow& r, P
     Pair o[vec_pairs<GT>()];
 #pragma unroll
     for (int k = 0; k < vec_pairs<GT>(); ++k) {
-        const Pair x = pair_of<GT>(u, k);
-        const Pair t = fma2(x, r.hi, GT == kGradF32 ? fma2(x, r.lo, r.neg_ref) : r.neg_ref);
-        o[k] = mul2(exp2_pair(t), f);
+        o[k] = mul2(exp2_pair(fma2(pair_of<GT>(u, k), r.log2e, r.neg_ref)), f);
     }
     return pack_vector<GT>(o);
 }
@@ -961,8 +1012,8 @@ __device__ __forceinline__ void zero_row(const TokenArgs& a, int64_t i, const ui
 // Every wait is bounded: one that runs out sets a status bit, the block leaves at
 // the end of the row, and its copies in flight are waited for first.
 // Bound by the logits' read and the gradient's write.  Policy, with gradient: 4096
-// rows of 32000 bf16 logits, 30% masked, 81.5 us, 5.5 TB/s; 8192 rows of 50257, 25%
-// masked, 239 us, 6.0 TB/s.  Backward: 8111 rows of 32000, 30% masked, 148 us, 5.9
+// rows of 32000 bf16 logits, 30% masked, 81.3 us, 5.5 TB/s; 8192 rows of 50257, 25%
+// masked, 234 us, 6.2 TB/s.  Backward: 8111 rows of 32000, 30% masked, 148 us, 5.9
 // TB/s.
 constexpr int kTeams = 2;
 constexpr int kTeamThreads = 256, kTeamWarps = kTeamThreads / 32;
@@ -1179,7 +1230,7 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
             if (kPolicy) {
                 r = fast_ref(q.xy);
                 const FastRow fr = fast_row(r);
-                Pair acc[2] = {0, 0};
+                RowSum acc{};
                 Ring at_ring = ring;
                 for (uint32_t o = 0; o < b.body; o += kChunk) {
                     bad = bad || !wait_chunk(full, &issued_chunks, &seen, at_ring, wait_ns);
@@ -1190,15 +1241,15 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
                         for (int k = 0; k < kChunk / (16 * kTeamThreads); ++k) {
                             const uint32_t at = 16 * (k * kTeamThreads + team.tid);
                             if (at < n)
-                                sum_vector<GT>(*reinterpret_cast<const uint4*>(in + at), fr, acc);
+                                sum_vector<GT>(*reinterpret_cast<const uint4*>(in + at), fr, &acc);
                         }
                     }
                     at_ring.next();
                 }
-                const float2 total = floats(add2(acc[0], acc[1]));
-                s = __fadd_rn(total.x, total.y);
-                if (edge >= 0 && r.fast) s = __fadd_rn(s, row_exp(xe, r));
-                s = team.sum(s, &bad, turn);
+                float3 total = row_totals(acc);
+                if (edge >= 0 && r.fast) total.x = __fadd_rn(total.x, row_exp(xe, r));
+                total = team.sum(total, &bad, turn);
+                s = total.x;
                 turn ^= 1;
                 if (bad) break;
                 if (!r.fast || !(s < kFastSum)) {
@@ -1206,7 +1257,7 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
                     r = sr.r;
                     s = sr.sum;
                 }
-                const Logp lp = row_logp(q.xy, r, s);
+                const Logp lp = without(row_logp(q.xy, r, s), small_bias<GT>(total, q.xy, r));
                 const PolicyTerms pt = policy_terms(lp, q.f[0], q.f[1], q.f[2], pol);
                 const float k = __fdiv_rn(q.w, norm);
                 c = __fmul_rn(__fmul_rn(pt.slope, k), scale);
@@ -1380,7 +1431,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     RowParam mine = param(0), after = param(32);
     for (int j0 = 0; j0 < rows && !bad; j0 += 32) {
         RowRef my_ref{0.0f, true};
-        float my_sum = 1.0f;
+        float my_sum = 1.0f, my_bias = 0.0f;
         for (int l = 0; l < 32 && j0 + l < rows && !bad; ++l) {
             const float xy = __shfl_sync(kFull, mine.xy, l);
             const char* x = row_of<GT>(a.x, share.row(j0 + l), a.x_stride);
@@ -1396,7 +1447,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
             const float xe = edge >= 0 ? load1<GT>(x, edge) : 0.0f;
             RowRef r = fast_ref(xy);
             const FastRow fr = fast_row(r);
-            Pair acc[2] = {0, 0};
+            RowSum acc{};
             for (uint32_t o = 0; o < len && !bad; o += kStreamChunk) {
                 bad = !__all_sync(kFull, mbar_wait(&full[warp][slot], parity, wait_ns));
                 if (bad) break;
@@ -1407,10 +1458,10 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
 #pragma unroll
                         for (int k = 0; k < kStreamChunk / 512; ++k)
                             sum_vector<GT>(*reinterpret_cast<const uint4*>(in + 16 * (32 * k + lane)),
-                                           fr, acc);
+                                           fr, &acc);
                     } else {
                         for (uint32_t at = 16 * lane; at < n; at += 512)
-                            sum_vector<GT>(*reinterpret_cast<const uint4*>(in + at), fr, acc);
+                            sum_vector<GT>(*reinterpret_cast<const uint4*>(in + at), fr, &acc);
                     }
                 }
                 __syncwarp();                     // every lane has read the slot
@@ -1421,10 +1472,10 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
                     parity ^= 1u;
                 }
             }
-            const float2 total = floats(add2(acc[0], acc[1]));
-            float s = __fadd_rn(total.x, total.y);
-            if (edge >= 0 && r.fast) s = __fadd_rn(s, row_exp(xe, r));
-            s = team.sum(s, &bad, turn);
+            float3 total = row_totals(acc);
+            if (edge >= 0 && r.fast) total.x = __fadd_rn(total.x, row_exp(xe, r));
+            total = team.sum(total, &bad, turn);
+            float s = total.x;
             turn ^= 1;
             if (bad) break;
             if (!r.fast || !(s < kFastSum)) {
@@ -1435,6 +1486,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
             if (lane == l) {
                 my_ref = r;
                 my_sum = s;
+                my_bias = small_bias<GT>(total, xy, r);
             }
         }
         if (bad) break;
@@ -1443,7 +1495,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
             int q = -1;
             if (j0 + lane < rows) {
                 const int64_t i = share.row(j0 + lane);
-                const Logp lp = row_logp(mine.xy, my_ref, my_sum);
+                const Logp lp = without(row_logp(mine.xy, my_ref, my_sum), my_bias);
                 a.logps[i] = lp.hi;
                 if constexpr (PREF) {
                     const int seq = find_sequence(t, i);

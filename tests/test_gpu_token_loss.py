@@ -358,6 +358,26 @@ def test_preference_forms():
     assert torch.equal(again.grad, keep) and torch.equal(again.log_ratios, both.log_ratios)
 
 
+@pytest.mark.parametrize("spread,boost", [(1.5, 0.0), (1.5, 5.0), (3.0, 0.0)])
+@pytest.mark.parametrize("v,dt", [(32000, "bf16"), (4099, "f32")])
+def test_log_ratios_gather_no_common_error(v, dt, spread, boost):
+    """Sequences of one token against the exact log probabilities as references:
+    each log ratio is the token's own error, at most a few 1e-7 with either sign,
+    and their mean stays below 1.5e-8 (a one-sided relative error of 2^-24, 6e-8,
+    of the exponentials or of log2 e would show as 2e-8 to 1.2e-7)."""
+    n = 4096
+    g = torch.Generator(device=DEV).manual_seed(v + int(10 * spread + boost))
+    x = (torch.randn(n, v, device=DEV, generator=g) * spread).to(DT[dt])
+    ids = torch.randint(0, v, (n,), device=DEV, generator=g)
+    rows = torch.arange(n, device=DEV)
+    x[rows, ids] = (x[rows, ids].float() + boost).to(DT[dt])
+    exact = torch.cat([x[i:i + 512].double().gather(1, ids[i:i + 512, None])[:, 0] -
+                       torch.logsumexp(x[i:i + 512].double(), 1) for i in range(0, n, 512)])
+    out = ss.preference_loss(x, ids, [1] * n, exact.float())
+    error = out.log_ratios.double() + exact.float().double() - exact
+    assert error.abs().max() < 2e-6 and abs(float(error.mean())) < 1.5e-8
+
+
 def test_preference_many_pairs_and_all_masked():
     """More pairs than one launch's table holds; then every token masked."""
     r = np.random.default_rng(8)
