@@ -49,6 +49,7 @@ constexpr float kLn2 = 0.6931471805599453f, kLn2Hi = 2839.0f / 4096.0f,
                 kLn2Lo = static_cast<float>(0.6931471805599453 - 2839.0 / 4096.0);
 constexpr float kFastLogit = 32768.0f;        // |x_y| below this: R and its products are fine
 constexpr float kFastSum = 0x1p120f;
+constexpr float kLargeSum = 0x1p16f;          // settle()
 
 // Status of this device's staged loss launches (0 = no wait ran out).
 __device__ unsigned int g_loss_status = 0;
@@ -251,14 +252,27 @@ __device__ __forceinline__ float logp_less(Logp lp, float x) {
     return __fadd_rn(__fsub_rn(lp.hi, x), lp.lo);
 }
 
-// The sum against the true maximum, from global memory: rows that the fast
-// form does not cover.  The products of x - max stay in range whatever x is.
-struct SlowRow {
+// A row's sum and what its exponentials refer to, for its gradient: a fast row's
+// sum may be close to 2^120, and c / S would then lose its last bits or vanish for
+// slopes that the gradient's type still holds (an id 80 below the largest logit,
+// c = 1e-9: 5% off).  The exponent of a large sum moves into the reference; of a
+// small one it stays, so that the id's own exponential has the bits that went into
+// the sum, which own_grad takes it off.
+struct RowScale {
     RowRef r;
     float sum;
 };
+__device__ __forceinline__ RowScale settle(RowRef r, float sum) {
+    if (!r.fast || sum < kLargeSum) return RowScale{r, sum};
+    const int k = (__float_as_int(sum) >> 23) - 127;
+    return RowScale{RowRef{__fadd_rn(r.ref, static_cast<float>(k)), true},
+                    __fmul_rn(sum, __int_as_float((127 - k) << 23))};
+}
+
+// The sum against the true maximum, from global memory: rows that the fast
+// form does not cover.  The products of x - max stay in range whatever x is.
 template <int GT, int T>
-__device__ __forceinline__ SlowRow slow_row(const char* x, int64_t v, const Team<T>& team) {
+__device__ __forceinline__ RowScale slow_row(const char* x, int64_t v, const Team<T>& team) {
     float m = -INFINITY;
     for (int64_t j = team.tid; j < v; j += T) m = fmaxf(m, load1<GT>(x, j));
     m = team.max(m);
@@ -270,7 +284,7 @@ __device__ __forceinline__ SlowRow slow_row(const char* x, int64_t v, const Team
     s = team.sum(s, &none, 0);
     team.sync();
     if (m == -INFINITY) s = NAN;   // nothing but -inf (or NaN): no distribution
-    return SlowRow{r, s};
+    return RowScale{r, s};
 }
 
 // -------------------------------------------------------- terms of a token
@@ -495,8 +509,9 @@ __device__ __forceinline__ void preference_stats(const TokenArgs& a, const Prefe
 // What a backward pass of its own needs of a row; a negative sum marks the slow
 // form.
 __device__ __forceinline__ void save_row(const PreferenceArgs& p, int64_t i, RowRef r, float sum) {
-    p.row_ref[i] = r.ref;
-    p.row_sum[i] = r.fast ? sum : -sum;
+    const RowScale s = settle(r, sum);
+    p.row_ref[i] = s.r.ref;
+    p.row_sum[i] = r.fast ? s.sum : -s.sum;
 }
 // c: the slope of the row's sequence times its weight, or what the policy loss's
 // forward pass has left.
@@ -1253,7 +1268,7 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
                 turn ^= 1;
                 if (bad) break;
                 if (!r.fast || !(s < kFastSum)) {
-                    const SlowRow sr = slow_row<GT>(x, a.v, team);
+                    const RowScale sr = slow_row<GT>(x, a.v, team);
                     r = sr.r;
                     s = sr.sum;
                 }
@@ -1265,6 +1280,9 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
                     a.logps[i] = lp.hi;
                     add_policy(sums, pt, pol, k);
                 }
+                const RowScale settled = settle(r, s);
+                r = settled.r;
+                s = settled.sum;
             } else {
                 c = q.f[0];
                 s = fabsf(q.f[2]);
@@ -1479,7 +1497,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
             turn ^= 1;
             if (bad) break;
             if (!r.fast || !(s < kFastSum)) {
-                const SlowRow sr = slow_row<GT>(x, a.v, team);
+                const RowScale sr = slow_row<GT>(x, a.v, team);
                 r = sr.r;
                 s = sr.sum;
             }
