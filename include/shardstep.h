@@ -747,7 +747,9 @@ int fsdp_reshard_plan(int64_t total, int32_t old_nd, int32_t new_nd, int32_t new
  * rounded once to the logits' type.  A token of weight 0 takes no part: its
  * logits and id are not read, its logps entry and gradient row are 0.  An id
  * outside [0, vocab) makes its token's log probability NaN, and the loss with
- * it. */
+ * it.  A call with n_tokens 0 launches nothing and writes nothing, stats and
+ * log_ratios included: the policy loss is then 0, the preference loss of pairs
+ * without tokens n_pairs * log 2 / W. */
 typedef struct {
     const void* logits;       /* device, row i at logits + i * row_stride       */
     int64_t row_stride;       /* elements, >= vocab                              */
@@ -767,6 +769,7 @@ typedef struct {
                               /* (policy), the number of pairs (preference)      */
     const float* loss_scale;  /* device fp32 word or NULL                        */
     float* stats;             /* device, 4 fp32, written (preference: 3 of them) */
+                              /* unless n_tokens is 0                            */
     void* workspace;          /* device, 8-byte aligned, its head zeroed once    */
     int64_t workspace_bytes;  /* >= token_loss_workspace_bytes(...)              */
 } shardstep_token_loss_t;

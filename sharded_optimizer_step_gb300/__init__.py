@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 import struct
 from dataclasses import dataclass
 from typing import NamedTuple
@@ -855,12 +856,16 @@ _TOKEN_LOSS = struct.Struct("@QqiiQqqQQQQqffQQQq")
 assert _TOKEN_LOSS.size == ctypes.sizeof(_capi.TokenLoss)
 
 
-def _loss_buffers(workspace, n, pairs, device):
-    """A call's outputs, and the workspace's address, size and buffer."""
+def _loss_buffers(workspace, n, pairs, norm, device):
+    """A call's outputs, and the workspace's address, size and buffer.  Without a
+    token nothing is launched, and the outputs are filled here: a pair's margin
+    is then 0 and its loss log 2 whatever the smoothing."""
     import torch
     out = torch.empty(n + 4 + 2 * pairs, dtype=torch.float32, device=device)
     if n == 0:
         out.zero_()
+        if pairs:
+            out[:1].fill_(math.log(2.0) * pairs / (norm or pairs))
     if workspace is None:
         workspace = LossWorkspace(device)
     return out, workspace.at_least(n, pairs)
@@ -906,10 +911,10 @@ def _token_args(logits, ids, weights, ref_logps, grad, grad_scale, loss_scale, n
         raise ValueError("norm must be > 0 (None: the sum of the weights, or the pairs)")
     device = logits.device
     if stream is None:
-        out, (ws, ws_bytes, held) = _loss_buffers(workspace, n, pairs, device)
+        out, (ws, ws_bytes, held) = _loss_buffers(workspace, n, pairs, norm, device)
     else:
         with _on(stream, device):
-            out, (ws, ws_bytes, held) = _loss_buffers(workspace, n, pairs, device)
+            out, (ws, ws_bytes, held) = _loss_buffers(workspace, n, pairs, norm, device)
     at = out.data_ptr()
     args = _TOKEN_LOSS.pack(
         logits.data_ptr(), row, _dtype_code(logits), id_bytes, ids.data_ptr(), n, v,

@@ -1,5 +1,6 @@
 """The token losses on rows that are not one heap of noise: ids far below the
-row's largest logit with small slopes.  Against 64 bits."""
+row's largest logit with small slopes; and calls without a token.  Against 64
+bits."""
 import numpy as np
 import pytest
 import torch
@@ -76,3 +77,25 @@ def test_gradients_of_unlikely_ids(v, dt, shift):
     ss.preference_loss(x, _dev(ids), lens, _dev(lp), beta=0.5, weights=_dev(w), norm=1.0, grad=g)
     want = OL.preference(host, ids, lens, lp, 0.5, 0.0, w, 1.0)[3]
     _check_relative(g, want, host, ids, lp, dt)
+
+
+# ----------------------------------------------------- calls without a token
+
+@pytest.mark.parametrize("weights", [False, True])
+def test_pairs_without_a_token_have_the_loss_of_a_zero_margin(weights):
+    x = torch.empty(0, 100, dtype=torch.bfloat16, device=DEV)
+    e, i = torch.empty(0, device=DEV), torch.empty(0, dtype=torch.int64, device=DEV)
+    kw = dict(weights=e) if weights else {}
+    for lens in ([0, 0], [0, 0, 0, 0, 0, 0]):
+        for ls, norm in ((0.0, None), (0.2, None), (0.1, 7.0)):
+            want = OL.preference(np.zeros((0, 100)), np.zeros(0, int), lens, np.zeros(0), 0.3, ls,
+                                 None, norm)[0]
+            for grad in (None, x):
+                out = ss.preference_loss(x, i, lens, e, beta=0.3, label_smoothing=ls, norm=norm,
+                                         grad=grad, **kw)
+                assert np.abs(out.stats.cpu().numpy() - want).max() <= 2.0 ** -23 * want.max()
+                assert out.log_ratios.shape == (len(lens),) and not out.log_ratios.any()
+    out = ss.preference_loss(x, i, [], e, **kw)
+    assert not out.stats.any() and out.log_ratios.numel() == 0
+    out = ss.policy_loss(x, i, e, e, grad=x, **kw)
+    assert not out.stats.any() and out.logps.numel() == 0
