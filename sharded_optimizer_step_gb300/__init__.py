@@ -883,7 +883,7 @@ def _token_args(logits, ids, weights, ref_logps, grad, grad_scale, loss_scale, n
         raise ValueError("logits must be a CUDA matrix [tokens, vocabulary]")
     n, v = shape
     row, col = logits.stride()
-    if n > 0 and v > 1 and (col != 1 or (n > 1 and row < v)):
+    if n > 0 and ((v > 1 and col != 1) or (n > 1 and row < v)):
         raise ValueError("the rows of the logits must be contiguous and apart")
     if row < v:
         row = v
@@ -899,7 +899,7 @@ def _token_args(logits, ids, weights, ref_logps, grad, grad_scale, loss_scale, n
     if grad is not None:
         grad_row, col = grad.stride() if grad.dim() == 2 else (0, 0)
         if grad.shape != shape or grad.dtype is not logits.dtype or not grad.is_cuda or (
-                n > 0 and v > 1 and (col != 1 or (n > 1 and grad_row < v))):
+                n > 0 and ((v > 1 and col != 1) or (n > 1 and grad_row < v))):
             raise ValueError("grad must have the logits' shape and dtype, its rows contiguous "
                              "and apart")
         grad_at = grad.data_ptr()
