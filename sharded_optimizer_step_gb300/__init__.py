@@ -14,6 +14,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import math
+import operator
 import struct
 from dataclasses import dataclass
 from typing import NamedTuple
@@ -994,11 +995,28 @@ def preference_loss(logits, ids, seq_lens, ref_logps, *, beta: float = 0.1,
 
 # ------------------------------------------------------ lists of tensors
 
+def _places(tensors):
+    """Addresses and bytes, to be compared from call to call: a tensor can be
+    given another size or type at the same address (``t.data = ...``).  One pass
+    per property, through C: each costs 148 tensors 7 us."""
+    import torch
+    return ([*map(torch.Tensor.data_ptr, tensors)],
+            [*map(operator.attrgetter("nbytes"), tensors)])
+
+
+def _forms(tensors):
+    """The same of what else a step over their elements goes by."""
+    import torch
+    return ([*map(operator.attrgetter("dtype"), tensors)],
+            [*map(torch.Tensor.is_contiguous, tensors)])
+
+
 class TensorList:
     """Gradient tensors checked once: contiguous CUDA tensors of one dtype on
     one device.  It keeps them alive and takes their addresses when made;
-    each call checks only that none has moved, so that a step over many small
-    tensors costs little host time."""
+    each call checks only that none has got another address or size in bytes
+    (the step also that their dtypes and layouts are still those), so that a
+    call over many small tensors costs little host time."""
 
     def __init__(self, tensors):
         self.tensors = list(tensors)
@@ -1007,9 +1025,11 @@ class TensorList:
             if t.dtype != self.tensors[0].dtype or t.device != self.tensors[0].device:
                 raise ValueError("one dtype and one device per list")
         self.dtype = _dtype_code(self.tensors[0]) if self.tensors else _capi.DTYPE_BF16
+        self._dtype = self.tensors[0].dtype if self.tensors else None
         self.device = self.tensors[0].device if self.tensors else None
         self.numels = [t.numel() for t in self.tensors]
-        self.addrs = [t.data_ptr() for t in self.tensors]
+        self._known = _places(self.tensors)
+        self.addrs = self._known[0]
         self._numels = _capi.i64_array(self.numels)
         self._ptrs = _capi.ptr_array(self.addrs)
 
@@ -1017,9 +1037,14 @@ class TensorList:
         return len(self.tensors)
 
     def check(self):
-        if [t.data_ptr() for t in self.tensors] != self.addrs:
-            raise ValueError("a tensor moved since this TensorList was made")
+        if _places(self.tensors) != self._known:
+            raise ValueError("a tensor moved or changed its size since this TensorList was made")
         return self
+
+    def check_forms(self):
+        dtypes, contiguous = _forms(self.tensors)
+        if not all(contiguous) or any(d != self._dtype for d in {*dtypes}):
+            raise ValueError("a tensor changed its dtype or layout since this TensorList was made")
 
 
 def _tensor_list(x):
@@ -1138,9 +1163,7 @@ class TensorAdamW:
         if not 1 <= len(self.hps) <= _capi.MAX_GROUPS:
             raise ValueError(f"1 to {_capi.MAX_GROUPS} hyper-parameter groups")
         self.groups = [0] * len(self.params) if groups is None else [int(g) for g in groups]
-        if len(self.groups) != len(self.params) or any(
-                not 0 <= g < len(self.hps) for g in self.groups):
-            raise ValueError("groups must give each parameter an index into hp")
+        self._check_groups()
         self.state_bits, self.t, self.states = state_bits, 0, None
         self.numels = [p.numel() for p in self.params]
         blk = _capi.MOMENT_BLOCK
@@ -1162,7 +1185,7 @@ class TensorAdamW:
                 self.v_scale = torch.zeros(pos // blk, dtype=torch.float32, device=dev)
         self._param_code = _dtype_code(self.params[0])
         self._table = (_capi.Tensor * len(self.params))()
-        self._addrs = None
+        self._known = None
 
     def view(self, buf, t):
         """Tensor t's piece of a flat buffer of the state, in its shape."""
@@ -1172,16 +1195,16 @@ class TensorAdamW:
     def _call(self, grads):
         """The list of this call's gradients, checked against the parameters,
         with the table of the state's addresses brought up to date where a
-        buffer or a parameter has moved."""
+        buffer, a parameter or a group has changed."""
         state = [self.master, self.m, self.v] + (
             [self.m_scale, self.v_scale] if self.state_bits == 8 else [])
-        addrs = [b.data_ptr() for b in state] + [p.data_ptr() for p in self.params]
-        if addrs != self._addrs:
-            _need_cuda(*state, *self.params)
-            if any(p.numel() != n or _dtype_code(p) != self._param_code
-                   for p, n in zip(self.params, self.numels)):
-                raise ValueError("a parameter changed its size or dtype")
+        held = state + self.params
+        now = (*_places(held), *_forms(held), list(self.groups))
+        if now != self._known:
+            _need_cuda(*held)
+            self._check_state(state)
             es = 4 if self.state_bits == 32 else 1
+            addrs = now[0]
             for t, row in enumerate(self._table):
                 o = self.offsets[t]
                 row.master = addrs[0] + 4 * o
@@ -1191,13 +1214,34 @@ class TensorAdamW:
                     row.v_scale = addrs[4] + 4 * (o // _capi.MOMENT_BLOCK)
                 row.param = addrs[len(state) + t]
                 row.numel, row.group = self.numels[t], self.groups[t]
-            self._addrs = addrs
-        grads = _tensor_list(grads)
+            self._known = now
+        given, grads = grads, _tensor_list(grads)
         if grads.numels != self.numels:
             raise ValueError("gradients must match the parameters one by one")
         if grads.device != self.master.device:
             raise ValueError("gradients on another device than the parameters")
+        if grads is given:
+            grads.check_forms()
         return grads
+
+    def _check_state(self, state):
+        """That the parameters, the state's buffers and the groups are still of
+        the sizes and types the table is made for."""
+        import torch
+        if [p.numel() for p in self.params] != self.numels or any(
+                _dtype_code(p) != self._param_code for p in self.params):
+            raise ValueError("a parameter changed its size or dtype")
+        code = torch.float32 if self.state_bits == 32 else torch.uint8
+        types = [torch.float32, code, code, torch.float32, torch.float32]
+        sizes = [self.flat] * 3 + [self.flat // _capi.MOMENT_BLOCK] * 2
+        if any(b.dtype != d or b.numel() < n for b, d, n in zip(state, types, sizes)):
+            raise ValueError("a buffer of the state changed its size or dtype")
+        self._check_groups()
+
+    def _check_groups(self):
+        if len(self.groups) != len(self.params) or any(
+                not 0 <= g < len(self.hps) for g in self.groups):
+            raise ValueError("groups must give each parameter an index into hp")
 
     def _words(self, grad_coef, skip):
         if skip is not None and (skip.element_size() != 4 or not skip.is_cuda):
