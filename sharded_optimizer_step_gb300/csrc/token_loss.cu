@@ -42,14 +42,20 @@ namespace {
 
 constexpr int kRowThreads = 512;              // threads of a plain kernel's block
 constexpr unsigned kFull = 0xFFFFFFFFu;
-// log2 e, and what the float lacks.
+// log2 e, and what the float lacks; log2 e as a number of 12 bits and the rest.
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLog2eLo = 1.9259629911e-8f;
+constexpr float kLog2eHead = 1.4423828125f;
+constexpr float kLog2eTail = static_cast<float>(1.4426950408889634 - 1.4423828125);
 constexpr float kLn2 = 0.6931471805599453f, kLn2Hi = 2839.0f / 4096.0f,
                 kLn2Lo = static_cast<float>(0.6931471805599453 - 2839.0 / 4096.0);
 constexpr float kFastLogit = 32768.0f;        // |x_y| below this: R and its products are fine
 constexpr float kFastSum = 0x1p120f;
 constexpr float kLargeSum = 0x1p16f;          // settle()
+// Sums are weighted: see weight().
+constexpr uint32_t kWeightBits = 0x3FB48362u; // 1.41025949
+constexpr float kWeight = 1.410259485244751f;
+constexpr float kUnweighted = 0x1.6b0dc2p-1f; // 1 / (kWeight (1 + 3.41e-8))
 
 // Status of this device's staged loss launches (0 = no wait ran out).
 __device__ unsigned int g_loss_status = 0;
@@ -122,7 +128,6 @@ __device__ __forceinline__ Sum2 warp_sum(Sum2 x) {
 template <int T>
 struct TeamShared {
     float part[2][T / 32];
-    float3 sums[2][T / 32];
     Sum2 wide[T / 32];
 };
 template <int T>
@@ -165,22 +170,6 @@ struct Team {
         for (int d = T / 64; d > 0; d >>= 1) x = __fadd_rn(x, __shfl_xor_sync(kFull, x, d));
         return x;
     }
-    // The same of three values at once.
-    __device__ __forceinline__ float3 sum(float3 x, bool* any, int turn) const {
-        const auto add = [&x](int d) {
-            x.x = __fadd_rn(x.x, __shfl_xor_sync(kFull, x.x, d));
-            x.y = __fadd_rn(x.y, __shfl_xor_sync(kFull, x.y, d));
-            x.z = __fadd_rn(x.z, __shfl_xor_sync(kFull, x.z, d));
-        };
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) add(d);
-        if ((tid & 31) == 0) sh->sums[turn][tid >> 5] = x;
-        *any = sync_or(*any);
-        x = sh->sums[turn][tid & (T / 32 - 1)];
-#pragma unroll
-        for (int d = T / 64; d > 0; d >>= 1) add(d);
-        return x;
-    }
     __device__ __forceinline__ float max(float x) const {
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, d));
@@ -207,14 +196,38 @@ struct Team {
 
 // How a row's exponentials are formed: fast, 2^(x log2 e - ref); else
 // 2^((x - ref) log2 e) with ref the row's maximum (0 for a row of -inf).
+//
+// Two errors of some 1e-8 would have one sign for all of a row's terms, so that a
+// sequence's summed log ratio would gather them up (100 tokens: 2e-6, as much as a
+// 32-bit log-softmax's random errors).  Neither is left, whatever the row looks like:
+//   The float log2 e lacks 1.3e-8 of itself, and x (log2 e - float) is below half the
+//     last place of most arguments, so it cannot be added to one.  A fast argument
+//     takes log2 e as 12 bits and a tail: x times the 12 bits, less the reference,
+//     is exact for 16-bit logits of a size that counts, and the tail's product is
+//     added with one rounding.  (The tail is positive: -inf stays -inf.)
+//   ex2.approx's mean relative error, measured over every float of each binade, is
+//     +3.4e-8 from 1 on and -5.0e-8 below -1 (inside +0.8e-8 and -2.5e-8 at most): see
+//     weight().
 struct RowRef {
     float ref;
     bool fast;
 };
-__device__ __forceinline__ float row_exp(float x, RowRef r) {
-    if (r.fast) return exp2_approx(__fmaf_rn(x, kLog2e, -r.ref));
+__device__ __forceinline__ float row_arg(float x, RowRef r) {
+    if (r.fast) return __fmaf_rn(x, kLog2eTail, __fmaf_rn(x, kLog2eHead, -r.ref));
     const float d = __fsub_rn(x, r.ref);
-    return exp2_approx(__fmaf_rn(d, kLog2e, __fmul_rn(d, kLog2eLo)));
+    return __fmaf_rn(d, kLog2e, __fmul_rn(d, kLog2eLo));
+}
+__device__ __forceinline__ float row_exp(float x, RowRef r) { return exp2_approx(row_arg(x, r)); }
+// What the exponential of argument t counts in a row's sum: 1.41026, and one last
+// place (8.45e-8 of it) more for t < 0, which levels the two mean errors.  The sum
+// is 1.41026 (1 + 3.41e-8) times too large, which kUnweighted takes off the log
+// probability's; the gradient's quotients carry kWeight instead.
+__device__ __forceinline__ float weight(float t) {
+    return __uint_as_float(kWeightBits + (__float_as_uint(t) >> 31));
+}
+__device__ __forceinline__ float row_term(float x, RowRef r) {
+    const float t = row_arg(x, r);
+    return __fmul_rn(exp2_approx(t), weight(t));
 }
 __device__ __forceinline__ RowRef fast_ref(float xy) {
     return RowRef{rintf(__fmul_rn(xy, kLog2e)), fabsf(xy) < kFastLogit};
@@ -234,6 +247,7 @@ __device__ __forceinline__ Logp two_sum(float a, float b) {
     return Logp{s, fabsf(s) < INFINITY ? e : 0.0f};
 }
 __device__ __forceinline__ Logp row_logp(float xy, RowRef r, float sum) {
+    sum = __fmul_rn(sum, kUnweighted);
     // sum is normal, or NaN, which the product keeps
     const int k = (__float_as_int(sum) - __float_as_int(0.75f)) >> 23;
     const float m = __fmul_rn(sum, __int_as_float((127 - k) << 23));
@@ -244,8 +258,7 @@ __device__ __forceinline__ Logp row_logp(float xy, RowRef r, float sum) {
         const Logp d = two_sum(xy, -r.ref), e = two_sum(d.hi, big);
         return two_sum(e.hi, __fadd_rn(__fadd_rn(d.lo, e.lo), small));
     }
-    const float t = __fmaf_rn(xy, kLog2e, -r.ref);
-    return two_sum(big, __fmaf_rn(t, kLn2, small));
+    return two_sum(big, __fmaf_rn(row_arg(xy, r), kLn2, small));
 }
 // lp - x.
 __device__ __forceinline__ float logp_less(Logp lp, float x) {
@@ -278,7 +291,7 @@ __device__ __forceinline__ RowScale slow_row(const char* x, int64_t v, const Tea
     m = team.max(m);
     const RowRef r{m == -INFINITY ? 0.0f : m, false};
     float s = 0.0f;
-    for (int64_t j = team.tid; j < v; j += T) s = __fadd_rn(s, row_exp(load1<GT>(x, j), r));
+    for (int64_t j = team.tid; j < v; j += T) s = __fadd_rn(s, row_term(load1<GT>(x, j), r));
     bool none = false;
     team.sync();
     s = team.sum(s, &none, 0);
@@ -521,10 +534,11 @@ __device__ __forceinline__ float row_coef(const PreferenceArgs& p, int64_t i, fl
     return __fmul_rn(c, scale);
 }
 
-// The id's own gradient, c (1 - e_y / S), as (c / S) (S - e_y): the difference
-// is that of the other tokens' terms, and exactly 0 where there are none.
-__device__ __forceinline__ float own_grad(float e, float sum, float cs) {
-    return __fmul_rn(__fsub_rn(sum, e), cs);
+// The id's own gradient, c (1 - e_y / S), as (c / S) (S - e_y) with its weighted
+// term of the sum: the difference is that of the other tokens' terms, and exactly 0
+// where there are none.  Of another token with exponential e: -(e kWeight) c / S.
+__device__ __forceinline__ float own_grad(float x, RowRef r, float sum, float cs) {
+    return __fmul_rn(__fsub_rn(sum, row_term(x, r)), cs);
 }
 
 // ------------------------------------------------------- shares of the rows
@@ -709,59 +723,31 @@ __device__ __forceinline__ uint32_t pack_pair(Pair p) {
 
 // The constants of a row's fast exponentials, both halves alike.
 struct FastRow {
-    Pair log2e, neg_ref;
+    Pair head, tail, neg_ref;
 };
 __device__ __forceinline__ FastRow fast_row(RowRef r) {
-    return FastRow{make_pair(kLog2e, kLog2e), make_pair(-r.ref, -r.ref)};
+    return FastRow{make_pair(kLog2eHead, kLog2eHead), make_pair(kLog2eTail, kLog2eTail),
+                   make_pair(-r.ref, -r.ref)};
 }
-// A row's fast sum, and of one pair in each vector (a sample: a quarter of 16-bit
-// logits, half of fp32 ones) the exponentials of arguments from 0 on and the
-// exponentials times their arguments, for small_bias.
+__device__ __forceinline__ Pair fast_args(Pair x, const FastRow& r) {
+    return fma2(x, r.tail, fma2(x, r.head, r.neg_ref));
+}
+// A row's fast sum, in two chains.
 struct RowSum {
-    Pair acc[2], above, moment;
+    Pair acc[2];
 };
 template <int GT>
 __device__ __forceinline__ void sum_vector(const uint4& u, const FastRow& r, RowSum* s) {
 #pragma unroll
     for (int k = 0; k < vec_pairs<GT>(); ++k) {
-        const Pair t = fma2(pair_of<GT>(u, k), r.log2e, r.neg_ref), e = exp2_pair(t);
-        s->acc[k & 1] = add2(s->acc[k & 1], e);
-        if (k == 0) {
-            const float2 f = floats(t);
-            float a, b;
-            asm("set.ge.f32.f32 %0, %1, 0f00000000;" : "=f"(a) : "f"(f.x));
-            asm("set.ge.f32.f32 %0, %1, 0f00000000;" : "=f"(b) : "f"(f.y));
-            s->above = fma2(e, make_pair(a, b), s->above);
-            // of -inf, e = 0: no product with an infinity
-            s->moment = fma2(e, make_pair(fmaxf(f.x, -256.0f), fmaxf(f.y, -256.0f)), s->moment);
-        }
+        const Pair t = fast_args(pair_of<GT>(u, k), r);
+        const float2 f = floats(t);
+        s->acc[k & 1] = fma2(exp2_pair(t), make_pair(weight(f.x), weight(f.y)), s->acc[k & 1]);
     }
 }
-__device__ __forceinline__ float3 row_totals(const RowSum& s) {
-    const float2 a = floats(add2(s.acc[0], s.acc[1])), b = floats(s.above), c = floats(s.moment);
-    return float3{__fadd_rn(a.x, a.y), __fadd_rn(b.x, b.y), __fadd_rn(c.x, c.y)};
-}
-// What is to be taken off a fast row's log probability.  Two errors of some 5e-8
-// have one sign for most tokens, so that a sequence's summed log ratio would gather
-// them up (100 tokens: 2e-6, as much as a 32-bit log-softmax's random errors):
-//   ex2.approx's mean relative error, measured over all fractions, is -5.06e-8
-//     for arguments below 0 and +3.43e-8 from 0 on, whatever their integer part;
-//   the float log2 e is 1 - d of the number, d = 1.33e-8: every logit counts as
-//     x (1 - d), and the result is d (x_y - mean of x under the softmax) too small.
-//     (The low part's product cannot be added to an argument beyond 2: it is
-//     below half of its last place.)
-template <int GT>
-__device__ __forceinline__ float small_bias(float3 total, float xy, RowRef r) {
-    if (!r.fast) return 0.0f;
-    const float scale = __fdiv_rn(static_cast<float>(vec_pairs<GT>()), total.x);
-    const float share = fminf(__fmul_rn(total.y, scale), 1.0f);
-    const float mean = __fmul_rn(total.z, scale);
-    const float t = __fmaf_rn(xy, kLog2e, -r.ref);
-    return __fmaf_rn(share, -8.49e-8f, 5.06e-8f) -
-           __fmul_rn(kLog2eLo * kLn2 * kLn2, __fsub_rn(t, mean));
-}
-__device__ __forceinline__ Logp without(Logp lp, float bias) {
-    return Logp{lp.hi, __fsub_rn(lp.lo, bias)};
+__device__ __forceinline__ float row_total(const RowSum& s) {
+    const float2 a = floats(add2(s.acc[0], s.acc[1]));
+    return __fadd_rn(a.x, a.y);
 }
 // A vector's gradient without the id's own term, e f.
 template <int GT>
@@ -780,7 +766,7 @@ __device__ __forceinline__ uint4 grad_vector(const uint4& u, const FastRow& r, P
     Pair o[vec_pairs<GT>()];
 #pragma unroll
     for (int k = 0; k < vec_pairs<GT>(); ++k) {
-        o[k] = mul2(exp2_pair(fma2(pair_of<GT>(u, k), r.log2e, r.neg_ref)), f);
+        o[k] = mul2(exp2_pair(fast_args(pair_of<GT>(u, k), r)), f);
     }
     return pack_vector<GT>(o);
 }
@@ -875,16 +861,17 @@ __global__ void __launch_bounds__(kRowThreads, 2)
         const int64_t y = token_id(a, i);
         const float sum = p.row_sum[i], s = fabsf(sum);
         const RowRef r{p.row_ref[i], !(sum < 0.0f)};
-        const float cs = __fdiv_rn(row_coef(p, i, w, scale), s);
+        const float cs = __fdiv_rn(row_coef(p, i, w, scale), s), other = -__fmul_rn(cs, kWeight);
         const FastRow fr = fast_row(r);
-        const Pair f = make_pair(-cs, -cs);
+        const Pair f = make_pair(other, other);
         if (threadIdx.x < 32) {           // the elements outside whole vectors
             int64_t edge = -1;
             if (lane < 16 && lane < b.head) edge = lane;
             if (lane >= 16 && lane - 16 < b.tail) edge = a.v - b.tail + lane - 16;
             if (edge >= 0) {
-                const float e = row_exp(load1<GT>(x, edge), r);
-                store1<GT>(g, edge, edge == y ? own_grad(e, s, cs) : -__fmul_rn(e, cs));
+                const float xe = load1<GT>(x, edge);
+                store1<GT>(g, edge, edge == y ? own_grad(xe, r, s, cs)
+                                              : __fmul_rn(row_exp(xe, r), other));
             }
         }
         char* to = g + b.head * es;       // the first whole vector's gradient
@@ -907,7 +894,7 @@ __global__ void __launch_bounds__(kRowThreads, 2)
                 uint4 o = r.fast ? grad_vector<GT>(u[k], fr, f) : grad_vector_slow<GT>(u[k], r, f);
                 if (at == yv)
                     o = with_element<GT>(o, static_cast<int>((y - b.head) % kElems),
-                                         own_grad(row_exp(load1<GT>(x, y), r), s, cs));
+                                         own_grad(load1<GT>(x, y), r, s, cs));
                 const uint4 next{__shfl_down_sync(kFull, o.x, 1), __shfl_down_sync(kFull, o.y, 1),
                                  __shfl_down_sync(kFull, o.z, 1), __shfl_down_sync(kFull, o.w, 1)};
                 char* dst = to + static_cast<int64_t>(at) * 16;
@@ -1261,10 +1248,9 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
                     }
                     at_ring.next();
                 }
-                float3 total = row_totals(acc);
-                if (edge >= 0 && r.fast) total.x = __fadd_rn(total.x, row_exp(xe, r));
-                total = team.sum(total, &bad, turn);
-                s = total.x;
+                s = row_total(acc);
+                if (edge >= 0 && r.fast) s = __fadd_rn(s, row_term(xe, r));
+                s = team.sum(s, &bad, turn);
                 turn ^= 1;
                 if (bad) break;
                 if (!r.fast || !(s < kFastSum)) {
@@ -1272,7 +1258,7 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
                     r = sr.r;
                     s = sr.sum;
                 }
-                const Logp lp = without(row_logp(q.xy, r, s), small_bias<GT>(total, q.xy, r));
+                const Logp lp = row_logp(q.xy, r, s);
                 const PolicyTerms pt = policy_terms(lp, q.f[0], q.f[1], q.f[2], pol);
                 const float k = __fdiv_rn(q.w, norm);
                 c = __fmul_rn(__fmul_rn(pt.slope, k), scale);
@@ -1288,12 +1274,12 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
                 s = fabsf(q.f[2]);
                 r = RowRef{q.f[1], !(q.f[2] < 0.0f)};
             }
-            const float cs = __fdiv_rn(c, s);
+            const float cs = __fdiv_rn(c, s), other = -__fmul_rn(cs, kWeight);
             char* g = const_cast<char*>(row_of<GT>(a.grad, i, a.g_stride));
             // the id's place among the vectors of the body, in bytes
             const int64_t yb = q.y < b.head ? -1 : static_cast<int64_t>(q.y - b.head) * es;
             const FastRow fr = fast_row(r);
-            const Pair f = make_pair(-cs, -cs);
+            const Pair f = make_pair(other, other);
             for (uint32_t o = 0; o < b.body; o += kChunk) {
                 if (!kPolicy)
                     bad = bad || !wait_chunk(full, &issued_chunks, &seen, ring, wait_ns);
@@ -1317,16 +1303,15 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
                         *v4 = grad_vector_slow<GT>(*v4, r, f);
                     }
                 }
-                if (own && !bad) store1<GT>(io, in / es, own_grad(row_exp(xv, r), s, cs));
+                if (own && !bad) store1<GT>(io, in / es, own_grad(xv, r, s, cs));
                 fence_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&done[ring.slot]);
                 ring.next();
             }
-            if (edge >= 0) {
-                const float e = row_exp(xe, r);
-                store1<GT>(g, edge, edge == q.y ? own_grad(e, s, cs) : -__fmul_rn(e, cs));
-            }
+            if (edge >= 0)
+                store1<GT>(g, edge, edge == q.y ? own_grad(xe, r, s, cs)
+                                                : __fmul_rn(row_exp(xe, r), other));
             if (!kPolicy) bad = team.sync_or(bad);
         }
         if (bad && team.tid == 0) atomicOr(&g_loss_status, kStatusConsumerTimeout);
@@ -1449,7 +1434,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     RowParam mine = param(0), after = param(32);
     for (int j0 = 0; j0 < rows && !bad; j0 += 32) {
         RowRef my_ref{0.0f, true};
-        float my_sum = 1.0f, my_bias = 0.0f;
+        float my_sum = 1.0f;
         for (int l = 0; l < 32 && j0 + l < rows && !bad; ++l) {
             const float xy = __shfl_sync(kFull, mine.xy, l);
             const char* x = row_of<GT>(a.x, share.row(j0 + l), a.x_stride);
@@ -1490,10 +1475,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
                     parity ^= 1u;
                 }
             }
-            float3 total = row_totals(acc);
-            if (edge >= 0 && r.fast) total.x = __fadd_rn(total.x, row_exp(xe, r));
-            total = team.sum(total, &bad, turn);
-            float s = total.x;
+            float s = row_total(acc);
+            if (edge >= 0 && r.fast) s = __fadd_rn(s, row_term(xe, r));
+            s = team.sum(s, &bad, turn);
             turn ^= 1;
             if (bad) break;
             if (!r.fast || !(s < kFastSum)) {
@@ -1504,7 +1488,6 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
             if (lane == l) {
                 my_ref = r;
                 my_sum = s;
-                my_bias = small_bias<GT>(total, xy, r);
             }
         }
         if (bad) break;
@@ -1513,7 +1496,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
             int q = -1;
             if (j0 + lane < rows) {
                 const int64_t i = share.row(j0 + lane);
-                const Logp lp = without(row_logp(mine.xy, my_ref, my_sum), my_bias);
+                const Logp lp = row_logp(mine.xy, my_ref, my_sum);
                 a.logps[i] = lp.hi;
                 if constexpr (PREF) {
                     const int seq = find_sequence(t, i);

@@ -1,6 +1,8 @@
 """The token losses on rows that are not one heap of noise: ids far below the
-row's largest logit with small slopes; and calls without a token.  Against 64
-bits."""
+row's largest logit with small slopes, confident rows, rows whose mass is one
+other token; and calls without a token.  Against 64 bits."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -77,6 +79,57 @@ def test_gradients_of_unlikely_ids(v, dt, shift):
     ss.preference_loss(x, _dev(ids), lens, _dev(lp), beta=0.5, weights=_dev(w), norm=1.0, grad=g)
     want = OL.preference(host, ids, lens, lp, 0.5, 0.0, w, 1.0)[3]
     _check_relative(g, want, host, ids, lp, dt)
+
+
+# ------------------------------------------------------ log probabilities
+
+def _token_errors(x, ids):
+    """Each token's log ratio against its exact log probability, 64 bits."""
+    n = x.shape[0]
+    exact = torch.cat([x[i:i + 512].double().gather(1, ids[i:i + 512, None])[:, 0] -
+                       torch.logsumexp(x[i:i + 512].double(), 1) for i in range(0, n, 512)])
+    out = ss.preference_loss(x, ids, [1] * n, exact.float())
+    return out.log_ratios.double() + exact.float().double() - exact
+
+
+@pytest.mark.parametrize("v,dt", [(4099, "bf16"), (4099, "f32"), (4096, "f16")])
+@pytest.mark.parametrize("kind", ["confident", "other_5", "other_12", "other_20", "other_50"])
+def test_log_ratios_of_peaked_rows_gather_no_common_error(kind, v, dt):
+    """Rows whose mass is the id's (probability 0.9 to 1) or one other token's, 5
+    to 50 above: the mean error over the rows whose dominant token lies at one
+    place of a 16-byte vector stays at the level of rounding.  The argument t of
+    the dominant exponential, |t| in [2^k, 2^(k+1)), rounds by up to 2^(k-24) either
+    way, which moves the result by log 2 / sqrt(3) of that (rms); what else rounds
+    is below 2^-25.  Equal arguments round alike, so a class counts as many draws
+    as it has different ones; allowed are four standard deviations of its mean, and
+    1.5e-8 for what is one-sided."""
+    n, vec = 16384, 16 // (4 if dt == "f32" else 2)
+    g = torch.Generator(device=DEV).manual_seed(v + len(kind))
+    draw = lambda: torch.rand(n, device=DEV, generator=g)  # noqa: E731
+    x = torch.randn(n, v, device=DEV, generator=g)
+    rows = torch.arange(n, device=DEV)
+    top = torch.randint(0, v, (n,), device=DEV, generator=g)
+    if kind == "confident":
+        ids = top
+        x[rows, top] = math.log(v) + 0.5 + 2.2 + 4 * draw()      # p from 0.9 to 0.998
+    else:
+        gap = float(kind.split("_")[1])
+        ids = (top + 1 + torch.randint(0, v - 1, (n,), device=DEV, generator=g)) % v
+        x -= 24.0 + gap / 2
+        x[rows, top] = gap / 2 + 4 + 4 * draw()
+        x[rows, ids] = -gap / 2 + 4 - 3 * draw()
+    x = x.to(DT[dt])
+    error = _token_errors(x, ids)
+    xt, ref = x[rows, top].double(), torch.round(x[rows, ids].double() / math.log(2))
+    t = (xt / math.log(2) - ref).abs().clamp(min=0.5)
+    var = torch.exp2(2 * (torch.floor(torch.log2(t)) - 24)) * math.log(2) ** 2 / 3 + 2.0 ** -50
+    place = (rows * v + top) % vec
+    for k in range(vec):
+        e = error[place == k]
+        draws = len(torch.unique(t[place == k]))
+        assert len(e) > n / vec / 2
+        limit = 1.5e-8 + 4 * math.sqrt(float(var[place == k].mean()) / draws)
+        assert abs(float(e.mean())) < limit, (k, float(e.mean()), limit)
 
 
 # ----------------------------------------------------- calls without a token
