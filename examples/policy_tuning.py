@@ -39,7 +39,7 @@ def tune(steps=20, nd=4, micro=2, tokens=192, hidden=256, vocab=2000, state_bits
     params = [(rand(hidden, hidden) * hidden ** -0.5).bfloat16(),
               (rand(vocab, hidden) * 0.02).bfloat16(),
               torch.ones(hidden, device=device).bfloat16()]
-    hps = [ss.AdamW(lr=2e-3), ss.AdamW(lr=2e-3, weight_decay=0.0)]
+    hps = [ss.AdamW(lr=2e-3, beta2=0.95), ss.AdamW(lr=2e-3, beta2=0.95, weight_decay=0.0)]
     opt = ss.TensorAdamW(params, hps, groups=[0, 0, 1], state_bits=state_bits)
     scaler = ss.GradScaler(init_scale=256.0, device=device)
     numels = [p.numel() for p in params]

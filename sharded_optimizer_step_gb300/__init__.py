@@ -1141,7 +1141,11 @@ class TensorAdamW:
     [offsets[t], offsets[t] + numel) with every tensor starting on a multiple
     of 256: ``master`` (fp32, from the parameters' values), ``m`` and ``v``
     (fp32, or uint8 codes with ``m_scale`` / ``v_scale``, one fp32 per 256
-    elements).  ``hp`` is one ``AdamW`` or a list of up to 8, ``groups[t]``
+    elements).  8 bits hold the second moment's root with 4 mantissa bits, rounded
+    to nearest: with beta2 = 0.999 its codes stop changing after some 500 steps and
+    an element keeps its share of its block's largest (roots of steady gradients
+    0.85 to 1.31 of the 32-bit ones), with beta2 <= 0.95 they follow (0.93 to
+    1.07).  ``hp`` is one ``AdamW`` or a list of up to 8, ``groups[t]``
     each tensor's index into it (e.g. no weight decay for norm vectors).
     ``t`` counts the steps; ``device_step_state`` moves the count to the
     device for ``step_on_device``, which a CUDA graph can capture.  ``stream``
