@@ -743,7 +743,8 @@ int fsdp_reshard_plan(int64_t total, int32_t old_nd, int32_t new_nd, int32_t new
  * 3.5), which stays on the device.  Per token i with logits x, id y:
  *     a = (x_y - max x) - log(sum exp(x - max x)),   logps[i] = a
  *     d loss / d x = c (1[y] - softmax x),           c = d loss / d a
- * Statistics, terms and c are fp32, sums over tokens double; the gradient is
+ * Statistics, terms and c are fp32, sums over tokens two floats within a block
+ * and double from block to block; the gradient is
  * rounded once to the logits' type.  A token of weight 0 takes no part: its
  * logits and id are not read, its logps entry and gradient row are 0.  An id
  * outside [0, vocab) makes its token's log probability NaN, and the loss with
@@ -911,7 +912,8 @@ int tensors_moments_encode(const float* m_in, const float* v_in, int64_t n, uint
  *     out[1] = factor = min(1, max_norm / (norm + 1e-6)) / s
  * so that tensors_adamw_step with grad_coef = out + 1 clips and unscales in
  * its own pass.  Squares are summed in fp32 per thread and in double beyond
- * that, in an order that depends on the sizes alone.  When norm is inf or NaN
+ * that, in an order that depends on the sizes alone; squares below 2^-126 keep
+ * fewer bits and below 2^-150 none (|g| < 1e-19, 2.6e-23).  When norm is inf or NaN
  * (also when a square passes fp32's range, |g| > 1.8e19) *found_inf becomes 1;
  * it is never cleared here (fsdp_grad_scaler_update does).
  *   grads[n], numels[n]  host arrays; NULL allowed where numel is 0.

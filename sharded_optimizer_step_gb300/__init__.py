@@ -793,7 +793,8 @@ class LossWorkspace:
     call allocates nothing once it is large enough.  It carries no results;
     calls that may run at the same time (on different streams) need
     workspaces of their own, and calls on different streams that share one
-    must be ordered by the caller, as for any tensor."""
+    must be ordered by the caller, as for any tensor.  After a call whose waits
+    ran out (``device_status``) its counters are not ready: take a new one."""
 
     def __init__(self, device="cuda"):
         self.device = device

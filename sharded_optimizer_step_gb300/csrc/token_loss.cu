@@ -10,8 +10,9 @@
 // summed again against its true maximum, which is subtracted before anything
 // is scaled, so rows of the type's lowest value and rows with -inf are right.
 // Both losses have d loss / d x = c (1[y] - softmax x) with one c per row.
-// Statistics, terms and coefficients are fp32, sums over tokens double; the
-// gradient is rounded once, to the logits' type.
+// Statistics, terms and coefficients are fp32, sums over tokens two floats within a
+// block and double from block to block; the gradient is rounded once, to the
+// logits' type.
 //
 // Three kernels, all bound by the logits' and the gradient's traffic:
 //   stream_forward  a forward pass: each logit is read once, nothing is kept.
@@ -23,12 +24,12 @@
 //   offset_backward  a backward pass where the gradient's rows lie at other offsets
 //                   from 16-byte boundaries than the logits'.
 // Which of them: the policy loss takes one pass of staged_rows where a row fits its
-// 13 slots of shared memory (4096 rows of 32000 bf16 logits: 90 us against 137 in
+// 13 slots of shared memory (4096 rows of 32000 bf16 logits: 96 us against 137 in
 // two passes), else stream_forward and a backward pass (2048 rows of 128256 bf16
-// logits: 262 us; the same in one kernel that read a row again from L2 through
+// logits: 267 us; the same in one kernel that read a row again from L2 through
 // registers: 1056).  The preference loss always takes two passes: a row's slope
-// needs the sums of its whole pair.  A gradient at other offsets: 172 us for the
-// policy loss of 4096 x 32000, against 90.
+// needs the sums of its whole pair.  A gradient at other offsets: 177 us for the
+// policy loss of 4096 x 32000, against 96.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -835,7 +836,7 @@ __device__ __forceinline__ uint4 with_element(const uint4& o, int e, float x) {
 // a whole vector of logits; with the next lane's it holds the 16 bytes between two
 // boundaries of the gradient's row.  What a warp's 32 vectors do not fill goes out
 // one element at a time.  Bound by memory and the loads' latency: 4096 rows of 32000
-// bf16 logits in 121 us, 4.3 TB/s (206 us with every element loaded and stored by
+// bf16 logits in 127 us, 4.1 TB/s (206 us with every element loaded and stored by
 // itself).
 template <int GT>
 __global__ void __launch_bounds__(kRowThreads, 2)
@@ -1014,9 +1015,14 @@ __device__ __forceinline__ void zero_row(const TokenArgs& a, int64_t i, const ui
 // Every wait is bounded: one that runs out sets a status bit, the block leaves at
 // the end of the row, and its copies in flight are waited for first.
 // Bound by the logits' read and the gradient's write.  Policy, with gradient: 4096
-// rows of 32000 bf16 logits, 30% masked, 81.3 us, 5.5 TB/s; 8192 rows of 50257, 25%
-// masked, 234 us, 6.2 TB/s.  Backward: 8111 rows of 32000, 30% masked, 148 us, 5.9
+// rows of 32000 bf16 logits, 30% masked, 81.4 us, 5.5 TB/s; 8192 rows of 50257, 25%
+// masked, 233 us, 6.2 TB/s.  Backward: 8111 rows of 32000, 30% masked, 149 us, 5.9
 // TB/s.
+// Loads and stores are evict-first, chosen on the kernel's own time (4096 x 32000: 83
+// us against 86).  The gradient's next reader loses little by it if it is a matrix
+// product (with 1024 columns after 152 to 2048 rows of 32000: the two take 26.9 to
+// 135.1 us, with plain stores 26.8 to 134.8), more if it is bound by memory (a sum
+// after 1024 rows: 57.6 against 49.5).
 constexpr int kTeams = 2;
 constexpr int kTeamThreads = 256, kTeamWarps = kTeamThreads / 32;
 constexpr int kWorkWarps = kTeams * kTeamWarps;
@@ -1331,8 +1337,8 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
 // row, and what follows from a row's sum is formed for 32 rows at once, a row
 // per lane.  W = 16 where rows are few, so that a row's copies spread over the
 // SM's warps, else 4.  Bound by the one read of the logits: 8192 rows of 50257 bf16
-// logits, 25% masked, 103 us, 6.0 TB/s; 2048 rows of 32000 fp16, 10% masked, 29.9
-// us, 4.0 TB/s, of which 20 us stream and the rest starts and joins.
+// logits, 25% masked, 102 us, 6.1 TB/s; 2048 rows of 32000 fp16, 10% masked, 31 us,
+// 3.8 TB/s, of which some 21 us stream and the rest starts and joins.
 constexpr int kStreamWarps = 16, kStreamThreads = 32 * kStreamWarps;
 constexpr int kStreamSlots = 3, kStreamChunk = 4096;
 constexpr size_t kStreamSmem =
@@ -1615,10 +1621,10 @@ cudaError_t go_stream_w(const TokenArgs& a, const PolicyArgs& pol, const Prefere
                         dim3(kStreamThreads), kStreamSmem, s, a, pol, p, t, begin, end,
                         begin == 0, end == a.n, tma_wait_limit());
 }
-// Warps per row: 4 from 8 rows per SM on (2000 rows of 32000 bf16 logits: 35.2 us
-// against 39.0 with 16), 16 below (152 rows: 13.3 us against 15.6; 760 rows: 23.3
-// against 23.6).  One warp per row was no faster anywhere (3800 rows: 56.3 us
-// against 52.9).
+// Warps per row: 4 from 8 rows per SM on (1216 rows of 32000 bf16 logits: 22.3 us
+// against 26.9 with 16; 2000 rows: 30.2 against 37.5), 16 below (152 rows: 10.7 us
+// against 13.6; at 760 rows 4 are ahead already, 19.8 against 21.4: the two meet
+// between 1 and 5 rows per SM).  One warp per row was 6% slower at 3800 rows.
 template <int GT, class Table>
 cudaError_t go_stream(const TokenArgs& a, const PolicyArgs& pol, const PreferenceArgs& p,
                       const Table& t, int64_t begin, int64_t end, cudaStream_t s) {
