@@ -43,9 +43,8 @@ namespace {
 
 constexpr int kRowThreads = 512;              // threads of a plain kernel's block
 constexpr unsigned kFull = 0xFFFFFFFFu;
-// log2 e, and what the float lacks; log2 e as a number of 12 bits and the rest.
+// log2 e; the same as a number of 12 bits and the rest.
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLog2eLo = 1.9259629911e-8f;
 constexpr float kLog2eHead = 1.4423828125f;
 constexpr float kLog2eTail = static_cast<float>(1.4426950408889634 - 1.4423828125);
 constexpr float kLn2 = 0.6931471805599453f, kLn2Hi = 2839.0f / 4096.0f,
@@ -202,10 +201,10 @@ struct Team {
 // sequence's summed log ratio would gather them up (100 tokens: 2e-6, as much as a
 // 32-bit log-softmax's random errors).  Neither is left, whatever the row looks like:
 //   The float log2 e lacks 1.3e-8 of itself, and x (log2 e - float) is below half the
-//     last place of most arguments, so it cannot be added to one.  A fast argument
-//     takes log2 e as 12 bits and a tail: x times the 12 bits, less the reference,
-//     is exact for 16-bit logits of a size that counts, and the tail's product is
-//     added with one rounding.  (The tail is positive: -inf stays -inf.)
+//     last place of most arguments, so it cannot be added to one.  An argument takes
+//     log2 e as 12 bits and a tail: x times the 12 bits, less the reference, is
+//     exact for 16-bit logits of a size that counts, and the tail's product is added
+//     with one rounding.  (The tail is positive: -inf stays -inf.)
 //   ex2.approx's mean relative error, measured over every float of each binade, is
 //     +3.4e-8 from 1 on and -5.0e-8 below -1 (inside +0.8e-8 and -2.5e-8 at most): see
 //     weight().
@@ -216,7 +215,7 @@ struct RowRef {
 __device__ __forceinline__ float row_arg(float x, RowRef r) {
     if (r.fast) return __fmaf_rn(x, kLog2eTail, __fmaf_rn(x, kLog2eHead, -r.ref));
     const float d = __fsub_rn(x, r.ref);
-    return __fmaf_rn(d, kLog2e, __fmul_rn(d, kLog2eLo));
+    return __fmaf_rn(d, kLog2eTail, __fmul_rn(d, kLog2eHead));
 }
 __device__ __forceinline__ float row_exp(float x, RowRef r) { return exp2_approx(row_arg(x, r)); }
 // What the exponential of argument t counts in a row's sum: 1.41026, and one last
