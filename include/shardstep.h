@@ -930,6 +930,141 @@ int tensors_grad_norm(const void* const* grads, const int64_t* numels, int32_t n
                       float max_norm, const float* loss_scale, float* out, uint32_t* found_inf,
                       void* workspace, void* stream);
 
+/* -------------------------------- embedding, layer norm, matrices */
+
+/* The operators at both ends of the tensors' step: the gradients of a model's
+ * vocabulary table and norm vectors, and the update of its matrices as matrices.
+ * Elements are SHARDSTEP_DTYPE_BF16, _F16 or _F32; arithmetic and sums are fp32,
+ * each result rounded once, to nearest even.  Rows of any stride >= their length
+ * (in elements); rows whose addresses are 16-byte aligned take vector accesses.
+ * No output may overlap an input or another output. */
+
+/* token_embedding -- device, one launch.  out[i] = scale * table[ids[i]]; an id
+ * outside [0, vocab) (padding) gives a row of zeros.
+ *   table   device, vocab rows of dim elements.    out  device, n rows, as table.
+ *   ids     device, n of id_bytes 4 or 8.
+ *   0 <= n < 2^31, 1 <= vocab < 2^31, 1 <= dim <= 2^23, scale finite.
+ * Errors: INVALID, CUDA. */
+int token_embedding(const void* table, int64_t table_stride, int32_t dtype, int64_t vocab,
+                    int64_t dim, const void* ids, int32_t id_bytes, int64_t n, float scale,
+                    void* out, int64_t out_stride, void* stream);
+
+/* token_embedding_grad -- device, two launches (three where a workspace chunk of
+ * sorted tokens does not hold them all).
+ *     grad[v] = scale * sum over i with ids[i] = v of d_out[i]
+ * added to grad's rows with accumulate != 0 (rows that do not occur are not
+ * touched), else written to all of them.  Tokens are sorted by id and summed in
+ * fp32 in their order, in chunks whose length goes by n and dim alone: equal
+ * calls give equal bits.  Tokens with an id outside [0, vocab) are not read.
+ *   workspace  device, 16-byte aligned, token_embedding_grad_workspace_bytes(n,
+ *              vocab, dim) bytes (-1 for arguments out of range); any contents,
+ *              but calls that may run at the same time need workspaces of their own.
+ * Errors: INVALID, CUDA. */
+int64_t token_embedding_grad_workspace_bytes(int64_t n, int64_t vocab, int64_t dim);
+int token_embedding_grad(const void* d_out, int64_t d_out_stride, int32_t dtype, const void* ids,
+                         int32_t id_bytes, int64_t n, float scale, void* grad,
+                         int64_t grad_stride, int32_t grad_dtype, int64_t vocab, int64_t dim,
+                         int32_t accumulate, void* workspace, int64_t workspace_bytes,
+                         void* stream);
+
+/* rows_layer_norm -- device, one launch.  Per row of x, with population variance:
+ *     mean, rstd = 1 / sqrt(var + eps),   out = (x - mean) rstd weight + bias
+ *   x, out        device, rows of cols elements of dtype.
+ *   weight, bias  device, cols of weight_dtype (dtype or F32), or NULL (1, 0).
+ *   mean, rstd    device, rows fp32, written.
+ *   rows >= 0, 1 <= cols <= 2^24, eps >= 0 and finite.
+ * Errors: INVALID, CUDA. */
+int rows_layer_norm(const void* x, int64_t x_stride, int32_t dtype, int64_t rows, int64_t cols,
+                    const void* weight, const void* bias, int32_t weight_dtype, float eps,
+                    void* out, int64_t out_stride, float* mean, float* rstd, void* stream);
+
+/* rows_layer_norm_grad -- device, two launches (one without d_weight and d_bias;
+ * three for rows wider than registers hold).  With xh = (x - mean) rstd and
+ * g = d_out weight:
+ *     d_x = rstd (g - mean(g) - xh mean(g xh))
+ *     d_weight = sum over rows of d_out xh,   d_bias = sum over rows of d_out
+ * each left out where NULL; with accumulate != 0 d_weight and d_bias are added to.
+ * Sums over rows run in an order that depends on the sizes and the GPU alone.
+ *   mean, rstd  as rows_layer_norm left them.
+ *   d_weight, d_bias  device, cols of weight_dtype.
+ *   workspace   device, 16-byte aligned, rows_layer_norm_workspace_bytes(cols)
+ *               bytes, for d_weight or d_bias; any contents, but calls that may
+ *               run at the same time need workspaces of their own.
+ * Errors: INVALID, CUDA. */
+int64_t rows_layer_norm_workspace_bytes(int64_t cols);
+int rows_layer_norm_grad(const void* d_out, int64_t d_out_stride, const void* x,
+                         int64_t x_stride, int32_t dtype, int64_t rows, int64_t cols,
+                         const float* mean, const float* rstd, const void* weight,
+                         int32_t weight_dtype, void* d_x, int64_t d_x_stride, void* d_weight,
+                         void* d_bias, int32_t accumulate, void* workspace,
+                         int64_t workspace_bytes, void* stream);
+
+/* The orthogonalisation of a matrix u by Newton-Schulz products:
+ *     X = u / (|u| + eps), the 2-norm of its elements; transposed if rows > cols
+ *     rounds times: A = X X^T, X = a X + (b A + c A A) X; transposed back
+ * The singular values of the result are those of X under s -> a s + b s^3 + c s^5,
+ * `rounds` times; the usual (3.4445, -4.7750, 2.0315), 5 times, brings all but the
+ * smallest to between 0.7 and 1.2.  Products are formed on the tensor cores from
+ * values held as two halves each (22 bits): single precision.  A gradient that
+ * holds an inf or NaN (or whose square passes fp32's range) gives NaNs.
+ *   rounds        1..64.
+ *   a, b, c       such that no singular value in [0, 1] passes 1.39 and no value of
+ *                 b s^2 + c s^4 passes 3.9 in magnitude in any round. */
+typedef struct {
+    double a, b, c, eps;
+    int32_t rounds;
+    int32_t pad_;
+} shardstep_quintic_t;
+
+/* matrices_orthogonalize -- device, two launches and three a round for each group
+ * of up to 64 matrices (up to 2 GB of workspace, or one matrix).
+ *   in[n], out[n]      host arrays of device pointers: contiguous matrices of
+ *                      rows[i] x cols[i] elements of in_dtype and out_dtype.
+ *   rows, cols         0..2^20; a matrix without elements is left out.
+ *   workspace          device, 16-byte aligned, matrices_workspace_bytes(rows, cols,
+ *                      n) bytes (-1 for sizes out of range); any contents, but calls
+ *                      that may run at the same time need workspaces of their own.
+ * Errors: INVALID, CAPACITY, CUDA. */
+int64_t matrices_workspace_bytes(const int64_t* rows, const int64_t* cols, int32_t n);
+int matrices_orthogonalize(const void* const* in, void* const* out, const int64_t* rows,
+                           const int64_t* cols, int32_t n, int32_t in_dtype, int32_t out_dtype,
+                           const shardstep_quintic_t* quintic, void* workspace,
+                           int64_t workspace_bytes, void* stream);
+
+typedef struct {
+    double lr, momentum, weight_decay;
+    double match_rms;      /* > 0: s = match_rms sqrt(max(rows, cols)), the update's rms
+                              near match_rms lr; 0: s = sqrt(max(1, rows / cols)) */
+    int32_t nesterov;
+    int32_t pad_;
+} shardstep_muon_t;
+
+typedef struct {
+    const void* grad;      /* device, rows x cols of grad_dtype             */
+    float* master;         /* device, rows x cols fp32, updated in place    */
+    float* m;              /* device, likewise: the momentum                */
+    void* param;           /* device, rows x cols of param_dtype, or NULL   */
+    int64_t rows, cols;    /* 0..2^20                                       */
+    int32_t group;         /* index of its hyper-parameters                 */
+    int32_t pad_;
+} shardstep_matrix_t;
+
+/* tensors_muon_step -- device, launches as matrices_orthogonalize.  Per matrix:
+ *     g = grad * *grad_coef                     (grad itself where NULL)
+ *     m = momentum m + (1 - momentum) g
+ *     u = nesterov ? momentum m + (1 - momentum) g : m
+ *     p = p - lr weight_decay p;  p = p - lr s orthogonal(u);  param = param_dtype(p)
+ *   matrices[n]  host array.   param_dtype  SHARDSTEP_DTYPE_BF16 or _F16.
+ *   hp[n_groups] host, 1 <= n_groups <= SHARDSTEP_MAX_GROUPS; momentum in [0, 1).
+ *   skip         device word or NULL: non-zero at launch, nothing changes.
+ * The step holds no count, so a CUDA graph can capture it as it is.
+ * Errors: INVALID, CAPACITY, CUDA. */
+int tensors_muon_step(const shardstep_matrix_t* matrices, int32_t n, int32_t grad_dtype,
+                      int32_t param_dtype, const shardstep_muon_t* hp, int32_t n_groups,
+                      const shardstep_quintic_t* quintic, const float* grad_coef,
+                      const uint32_t* skip, void* workspace, int64_t workspace_bytes,
+                      void* stream);
+
 /* ------------------------------------------------------------ misc */
 
 /* Selects the kernels the streaming calls may use, process-wide: the fused

@@ -38,6 +38,9 @@ __all__ = [
     "LossWorkspace", "PolicyLoss", "policy_loss", "PreferenceLoss", "preference_loss",
     "TensorList", "NormWorkspace", "grad_norm_clip", "TensorAdamW", "moments_decode",
     "moments_encode",
+    "embedding", "embedding_grad", "EmbeddingWorkspace", "LayerNorm", "LayerNormGrad",
+    "layer_norm", "layer_norm_grad", "LayerNormWorkspace", "Muon", "TensorMuon",
+    "orthogonalize", "MatrixWorkspace",
 ]
 
 
@@ -1301,6 +1304,474 @@ class TensorAdamW:
                 self.v.copy_(v32)
         else:
             moments_encode(m32, v32, self.m, self.m_scale, self.v, self.v_scale, stream=stream)
+
+
+# ------------------------------------- embedding, layer norm, matrices
+
+class _Scratch:
+    """Device workspace kept from call to call, so that a call allocates nothing
+    once it is large enough.  It carries no results and may hold anything; calls
+    that may run at the same time (on different streams, or in graphs replayed
+    beside each other) need workspaces of their own.  A buffer that a CUDA graph
+    has captured stays alive with the workspace when a later call needs a larger
+    one, so the workspace must live as long as the graph."""
+
+    def __init__(self, device="cuda"):
+        self.device = device
+        self.buf = None
+        self._captured, self._kept = False, []
+
+    def at_least(self, nbytes: int):
+        """(address, bytes) of a workspace of that size."""
+        import torch
+        capturing = torch.cuda.is_current_stream_capturing()
+        if self.buf is None or self.buf.numel() < nbytes:
+            if self._captured:
+                self._kept.append(self.buf)
+            elif self.buf is not None:      # a kernel on this stream may still use it
+                self.buf.record_stream(torch.cuda.current_stream(self.buf.device))
+            self.buf = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=self.device)
+            self._captured = False
+        self._captured |= capturing
+        return self.buf.data_ptr(), self.buf.numel()
+
+
+class EmbeddingWorkspace(_Scratch):
+    __doc__ = _Scratch.__doc__
+
+
+class LayerNormWorkspace(_Scratch):
+    __doc__ = _Scratch.__doc__
+
+
+class MatrixWorkspace(_Scratch):
+    __doc__ = _Scratch.__doc__
+
+
+def _scratch(workspace, kind, device, nbytes):
+    """(address, bytes, holder) of a call's workspace: the caller's, or one of its own."""
+    if workspace is None:
+        workspace = kind(device)
+    elif workspace.buf is not None and workspace.buf.device != device:
+        raise ValueError("the workspace is on another device")
+    return (*workspace.at_least(nbytes), workspace)
+
+
+@contextlib.contextmanager
+def _at(device, stream):
+    """Where a call allocates and launches: its tensors' device, its stream."""
+    import torch
+    with torch.cuda.device(device):
+        with _on(stream, device) if stream is not None else contextlib.nullcontext():
+            yield
+
+
+def _here(device, stream):
+    """``_at``, at no cost where device and stream are the current ones already."""
+    import torch
+    if stream is None and device.index == torch.cuda.current_device():
+        return _NOWHERE
+    return _at(device, stream)
+
+
+_NOWHERE = contextlib.nullcontext()
+
+
+def _rows(t, cols, what):
+    """(address, rows, row stride) of a matrix with contiguous rows, or of a
+    contiguous tensor taken as rows of ``cols``."""
+    shape = t.shape
+    if not t.is_cuda or not shape or shape[-1] != cols:
+        raise ValueError(f"{what} must be a CUDA tensor with rows of {cols} elements")
+    if len(shape) == 2:
+        rows, (stride, one) = shape[0], t.stride()
+        if rows and ((cols > 1 and one != 1) or (rows > 1 and stride < cols)):
+            raise ValueError(f"the rows of {what} must be contiguous and apart")
+        return t.data_ptr(), rows, stride if rows > 1 else cols
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous, or a matrix with contiguous rows")
+    return t.data_ptr(), t.numel() // cols, cols
+
+
+def _one_device(device, *tensors):
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError("tensors on different devices")
+
+
+def _id_bytes(ids):
+    import torch
+    size = {torch.int64: 8, torch.int32: 4}.get(ids.dtype)
+    if size is None or not ids.is_cuda or not ids.is_contiguous():
+        raise ValueError("ids must be contiguous CUDA int64 or int32")
+    return size
+
+
+def embedding(table, ids, *, scale: float = 1.0, out=None, stream=None):
+    """Rows ``ids`` of ``table`` [V, D] (bf16, fp16 or fp32, rows of any stride)
+    times ``scale``, in one launch: ``out`` (table's dtype; [*ids.shape, D], or
+    [ids.numel(), D] with rows of any stride; allocated if None).  An id outside
+    [0, V), such as a padding of -1, gives a row of zeros."""
+    import torch
+    if table.dim() != 2 or not table.shape[0] or not table.shape[1]:
+        raise ValueError("table must be a matrix [vocabulary, features]")
+    vocab, dim = table.shape
+    at, _, stride = _rows(table, dim, "table")
+    id_bytes, n, dev = _id_bytes(ids), ids.numel(), table.device
+    with _here(dev, stream):
+        if out is None:
+            out = torch.empty(*ids.shape, dim, dtype=table.dtype, device=dev)
+        elif out.dtype is not table.dtype:
+            raise ValueError("out must have the table's dtype")
+        to, rows, out_stride = _rows(out, dim, "out")
+        if rows != n:
+            raise ValueError(f"out must have {n} rows")
+        _one_device(dev, ids, out)
+        rc = _capi.lib().token_embedding(at, stride, _dtype_code(table), vocab, dim,
+                                         ids.data_ptr(), id_bytes, n, scale, to, out_stride,
+                                         _stream(stream, dev))
+    if rc:
+        _capi.check("token_embedding", rc)
+    return out
+
+
+def embedding_grad(d_out, ids, grad, *, scale: float = 1.0, accumulate: bool = False,
+                   workspace=None, stream=None):
+    """The gradient of ``embedding`` in its table, into ``grad`` [V, D] (bf16, fp16
+    or fp32, rows of any stride): row v becomes ``scale`` times the sum of the rows
+    of ``d_out`` ([*ids.shape, D], or [ids.numel(), D] with rows of any stride) whose
+    id is v, summed in fp32 in the tokens' order.  ``accumulate`` adds to the rows
+    that occur and leaves the others alone (a table tied to the head, whose gradient
+    is there already; micro-batches), else every row is written.  Rows of ``d_out``
+    whose id is outside [0, V) are not read.  Returns ``grad``."""
+    if grad.dim() != 2 or not grad.shape[0] or not grad.shape[1]:
+        raise ValueError("grad must be a matrix [vocabulary, features]")
+    vocab, dim = grad.shape
+    to, _, grad_stride = _rows(grad, dim, "grad")
+    at, rows, stride = _rows(d_out, dim, "d_out")
+    id_bytes, n, dev = _id_bytes(ids), ids.numel(), grad.device
+    if rows != n:
+        raise ValueError(f"d_out must have {n} rows")
+    _one_device(dev, ids, d_out)
+    lib = _capi.lib()
+    with _here(dev, stream):
+        ws, ws_bytes, held = _scratch(workspace, EmbeddingWorkspace, dev,
+                                      lib.token_embedding_grad_workspace_bytes(n, vocab, dim))
+        rc = lib.token_embedding_grad(at, stride, _dtype_code(d_out), ids.data_ptr(), id_bytes, n,
+                                      scale, to, grad_stride, _dtype_code(grad), vocab, dim,
+                                      int(bool(accumulate)), ws, ws_bytes, _stream(stream, dev))
+    if rc:
+        _capi.check("token_embedding_grad", rc)
+    return grad
+
+
+class LayerNorm(NamedTuple):
+    out: object    # like x
+    mean: object   # fp32, one per row
+    rstd: object   # fp32, 1 / sqrt(variance + eps)
+
+
+class LayerNormGrad(NamedTuple):
+    d_x: object       # or None
+    d_weight: object  # or None
+    d_bias: object    # or None
+
+
+def _norm_vector(t, cols, dtype, what):
+    """Device address of a weight, bias or gradient of theirs."""
+    import torch
+    if t is None:
+        return None
+    if t.numel() != cols or not t.is_cuda or not t.is_contiguous() or (
+            t.dtype is not dtype and t.dtype is not torch.float32):
+        raise ValueError(f"{what} must be a contiguous CUDA tensor of {cols} elements, of x's "
+                         "dtype or fp32")
+    return t.data_ptr()
+
+
+def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, out=None,
+               stream=None) -> LayerNorm:
+    """Layer norm over the last dimension of ``x`` (bf16, fp16 or fp32; a matrix
+    with rows of any stride, or contiguous), in one launch:
+
+        out = (x - mean) rstd weight + bias,  rstd = 1 / sqrt(var + eps)
+
+    ``weight`` and ``bias`` [cols] are of x's dtype or fp32, both the same (None: 1
+    and 0).  ``out`` (x's dtype and shape; allocated if None) may not be ``x``.
+    ``mean`` and ``rstd`` (fp32, one per row) are what ``layer_norm_grad`` takes."""
+    import torch
+    if not x.dim() or not x.shape[-1]:
+        raise ValueError("x must have rows")
+    cols, dev = x.shape[-1], x.device
+    at, rows, stride = _rows(x, cols, "x")
+    w = _norm_vector(weight, cols, x.dtype, "weight")
+    b = _norm_vector(bias, cols, x.dtype, "bias")
+    if weight is not None and bias is not None and weight.dtype is not bias.dtype:
+        raise ValueError("weight and bias must have one dtype")
+    given = weight if weight is not None else bias if bias is not None else x
+    with _here(dev, stream):
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        elif out.dtype is not x.dtype or out.shape != x.shape:
+            raise ValueError("out must have x's dtype and shape")
+        to, _, out_stride = _rows(out, cols, "out")
+        _one_device(dev, weight, bias, out)
+        stats = torch.empty(2, rows, dtype=torch.float32, device=dev)
+        mean = stats.data_ptr()
+        rc = _capi.lib().rows_layer_norm(at, stride, _dtype_code(x), rows, cols, w, b,
+                                         _dtype_code(given), eps, to, out_stride, mean,
+                                         mean + 4 * rows, _stream(stream, dev))
+    if rc:
+        _capi.check("rows_layer_norm", rc)
+    return LayerNorm(out, *stats.unbind())
+
+
+def layer_norm_grad(d_out, x, mean, rstd, weight=None, *, d_x=None, d_weight=None, d_bias=None,
+                    accumulate: bool = False, workspace=None, stream=None) -> LayerNormGrad:
+    """The gradients of ``layer_norm`` from ``d_out`` (x's dtype and shape) and what
+    it returned, in two launches (one without ``d_weight`` and ``d_bias``):
+
+        g = d_out weight,  xh = (x - mean) rstd
+        d_x = rstd (g - mean(g) - xh mean(g xh))
+        d_weight = sum over rows of d_out xh,  d_bias = sum over rows of d_out
+
+    ``d_x`` (x's dtype and shape), ``d_weight`` and ``d_bias`` ([cols], the weight's
+    dtype, or x's or fp32 without a weight) receive them; None leaves one out, and
+    ``d_x`` None with neither of the others allocates it.  ``accumulate`` adds to
+    ``d_weight`` and ``d_bias`` instead (micro-batches)."""
+    import torch
+    if not x.dim() or not x.shape[-1]:
+        raise ValueError("x must have rows")
+    cols, dev = x.shape[-1], x.device
+    at, rows, stride = _rows(x, cols, "x")
+    if d_out.dtype is not x.dtype or d_out.shape != x.shape:
+        raise ValueError("d_out must have x's dtype and shape")
+    d_at, _, d_stride = _rows(d_out, cols, "d_out")
+    for t, what in ((mean, "mean"), (rstd, "rstd")):
+        if t.dtype is not torch.float32 or t.numel() != rows or not t.is_cuda or (
+                not t.is_contiguous()):
+            raise ValueError(f"{what} must be a contiguous CUDA fp32 tensor of {rows} elements")
+    w = _norm_vector(weight, cols, x.dtype, "weight")
+    dw = _norm_vector(d_weight, cols, x.dtype, "d_weight")
+    db = _norm_vector(d_bias, cols, x.dtype, "d_bias")
+    given = [t for t in (weight, d_weight, d_bias) if t is not None]
+    if any(t.dtype is not given[0].dtype for t in given):
+        raise ValueError("weight, d_weight and d_bias must have one dtype")
+    lib = _capi.lib()
+    with _here(dev, stream):
+        if d_x is None and dw is None and db is None:
+            d_x = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        if d_x is not None and (d_x.dtype is not x.dtype or d_x.shape != x.shape):
+            raise ValueError("d_x must have x's dtype and shape")
+        to, _, to_stride = _rows(d_x, cols, "d_x") if d_x is not None else (None, rows, cols)
+        _one_device(dev, d_out, mean, rstd, weight, d_x, d_weight, d_bias)
+        ws, ws_bytes, held = None, 0, None
+        if dw is not None or db is not None:
+            ws, ws_bytes, held = _scratch(workspace, LayerNormWorkspace, dev,
+                                          lib.rows_layer_norm_workspace_bytes(cols))
+        rc = lib.rows_layer_norm_grad(d_at, d_stride, at, stride, _dtype_code(x), rows, cols,
+                                      mean.data_ptr(), rstd.data_ptr(), w,
+                                      _dtype_code(given[0] if given else x), to, to_stride, dw,
+                                      db, int(bool(accumulate)), ws, ws_bytes,
+                                      _stream(stream, dev))
+    if rc:
+        _capi.check("rows_layer_norm_grad", rc)
+    return LayerNormGrad(d_x, d_weight, d_bias)
+
+
+QUINTIC = (3.4445, -4.7750, 2.0315)
+
+
+def _quintic(rounds, coefficients, eps):
+    a, b, c = coefficients
+    return _capi.Quintic(a, b, c, eps, int(rounds), 0)
+
+
+def orthogonalize(matrices, out=None, *, rounds: int = 5, coefficients=QUINTIC,
+                  eps: float = 1e-7, workspace=None, stream=None):
+    """The Newton-Schulz orthogonalisation of each of ``matrices`` (a tensor, a list
+    or a ``TensorList`` of contiguous matrices of one dtype: bf16, fp16 or fp32), all
+    of them together in two launches and three a round (per 64 matrices or 2 GB of
+    workspace):
+
+        X = u / (|u| + eps), transposed if taller than wide
+        A = X X^T,  X = a X + (b A + c A A) X      ``rounds`` times
+
+    Products run on the tensor cores in single precision.  ``out``: matrices of the
+    same shapes, contiguous, of one dtype (None: allocated, of the input's dtype).
+    Returns ``out``, a tensor if a tensor was given."""
+    import torch
+    single = isinstance(matrices, torch.Tensor)
+    given = [matrices] if single else matrices
+    known = isinstance(given, TensorList)
+    ins = _tensor_list(given)
+    if known:
+        ins.check_forms()
+    if not len(ins):
+        return [] if out is None else out
+    shapes = [t.shape for t in ins.tensors]
+    if any(len(s) != 2 for s in shapes):
+        raise ValueError("expected matrices")
+    dev, n = ins.device, len(shapes)
+    lib = _capi.lib()
+    with _here(dev, stream):
+        if out is None:
+            outs = [torch.empty(s, dtype=t.dtype, device=dev) for s, t in zip(shapes, ins.tensors)]
+            out = outs[0] if single else outs
+        outs = [out] if single else list(out)
+        if [t.shape for t in outs] != shapes:
+            raise ValueError("out must match the matrices one by one")
+        _need_cuda(*outs)
+        if any(t.dtype != outs[0].dtype or t.device != dev for t in outs):
+            raise ValueError("out must have one dtype, on the matrices' device")
+        rows, cols = (_capi.i64_array([s[k] for s in shapes]) for k in (0, 1))
+        ws, ws_bytes, held = _scratch(workspace, MatrixWorkspace, dev,
+                                      lib.matrices_workspace_bytes(rows, cols, n))
+        rc = lib.matrices_orthogonalize(
+            ins._ptrs, _capi.ptr_array([t.data_ptr() for t in outs]), rows, cols, n, ins.dtype,
+            _dtype_code(outs[0]), _quintic(rounds, coefficients, eps), ws, ws_bytes,
+            _stream(stream, dev))
+    if rc:
+        _capi.check("matrices_orthogonalize", rc)
+    return out
+
+
+@dataclass
+class Muon:
+    """Hyper-parameters of the orthogonalised step.  ``match_rms`` > 0 scales the
+    update by match_rms sqrt(max(rows, columns)), so that its elements' rms is near
+    match_rms lr (0.2: AdamW's learning rates carry over); 0 by sqrt(max(1, rows /
+    columns))."""
+    lr: float = 1e-3
+    momentum: float = 0.95
+    weight_decay: float = 0.01
+    match_rms: float = 0.2
+    nesterov: bool = True
+
+
+class TensorMuon:
+    """The orthogonalised momentum step over a list of parameter matrices (bf16 or
+    fp16, one dtype) with an fp32 master copy and fp32 momentum, beside
+    ``TensorAdamW`` for the vectors and tables:
+
+        m = momentum m + (1 - momentum) g,  u = momentum m + (1 - momentum) g  (nesterov)
+        p = p - lr weight_decay p - lr s orthogonalize(u)
+
+    The state sits in flat buffers laid out like ``TensorAdamW``'s: ``master`` and
+    ``m``.  ``hp`` is one ``Muon`` or a list of up to 8, ``groups[t]`` each matrix's
+    index into it; ``rounds``, ``coefficients`` and ``eps`` are those of
+    ``orthogonalize``.  The step depends on no count, so a CUDA graph can capture
+    ``step`` as it is, after one call outside.  ``stream`` is where the state is
+    made and filled (None: the current one)."""
+
+    def __init__(self, params, hp, groups=None, rounds: int = 5, coefficients=QUINTIC,
+                 eps: float = 1e-7, stream=None):
+        import torch
+        self.params = list(params)
+        if not self.params:
+            raise ValueError("need at least one parameter matrix")
+        _need_cuda(*self.params)
+        dt, dev = self.params[0].dtype, self.params[0].device
+        if dt not in (torch.bfloat16, torch.float16) or any(
+                p.dtype != dt or p.device != dev for p in self.params):
+            raise ValueError("parameters must be all bf16 or all fp16, on one device")
+        if any(p.dim() != 2 for p in self.params):
+            raise ValueError("parameters must be matrices")
+        self.hps = list(hp) if isinstance(hp, (list, tuple)) else [hp]
+        if not 1 <= len(self.hps) <= _capi.MAX_GROUPS:
+            raise ValueError(f"1 to {_capi.MAX_GROUPS} hyper-parameter groups")
+        self.groups = [0] * len(self.params) if groups is None else [int(g) for g in groups]
+        self._check_groups()
+        self.rounds, self.coefficients, self.eps = int(rounds), tuple(coefficients), float(eps)
+        self.shapes = [p.shape for p in self.params]
+        self.numels = [p.numel() for p in self.params]
+        blk = _capi.MOMENT_BLOCK
+        self.offsets, pos = [], 0
+        for n in self.numels:
+            self.offsets.append(pos)
+            pos += -(-n // blk) * blk
+        self.flat = pos
+        with _here(dev, stream):
+            self.master = torch.zeros(pos, dtype=torch.float32, device=dev)
+            for p, o, n in zip(self.params, self.offsets, self.numels):
+                self.master[o:o + n].copy_(p.reshape(-1))
+            self.m = torch.zeros(pos, dtype=torch.float32, device=dev)
+        self._param_code = _dtype_code(self.params[0])
+        self._table = (_capi.Matrix * len(self.params))()
+        self._known = self._grads = None
+        self.workspace = MatrixWorkspace(dev)
+        sides = [_capi.i64_array([s[k] for s in self.shapes]) for k in (0, 1)]
+        self._need = _capi.lib().matrices_workspace_bytes(*sides, len(self.params))
+        if self._need < 0:
+            raise ValueError("a matrix is too large")
+
+    def view(self, buf, t):
+        """Matrix t's piece of a flat buffer of the state, in its shape."""
+        o, n = self.offsets[t], self.numels[t]
+        return buf[o:o + n].view(self.shapes[t])
+
+    def _check_groups(self):
+        if len(self.groups) != len(self.params) or any(
+                not 0 <= g < len(self.hps) for g in self.groups):
+            raise ValueError("groups must give each parameter an index into hp")
+
+    def _call(self, grads):
+        """This call's gradients, checked against the parameters, with the table
+        brought up to date where an address or a group has changed."""
+        import torch
+        state = [self.master, self.m]
+        held = state + self.params
+        now = (*_places(held), *_forms(held), list(self.groups))
+        fresh = now != self._known
+        if fresh:
+            _need_cuda(*held)
+            if [p.shape for p in self.params] != self.shapes or any(
+                    _dtype_code(p) != self._param_code for p in self.params):
+                raise ValueError("a parameter changed its shape or dtype")
+            if any(b.dtype != torch.float32 or b.numel() < self.flat for b in state):
+                raise ValueError("a buffer of the state changed its size or dtype")
+            self._check_groups()
+        given, grads = grads, _tensor_list(grads)
+        if grads.numels != self.numels:
+            raise ValueError("gradients must match the parameters one by one")
+        if grads.device != self.master.device:
+            raise ValueError("gradients on another device than the parameters")
+        if grads is given:
+            grads.check_forms()
+        if fresh or grads.addrs != self._grads:
+            addrs = now[0]
+            for t, row in enumerate(self._table):
+                o = 4 * self.offsets[t]
+                row.grad = grads.addrs[t]
+                row.master, row.m = addrs[0] + o, addrs[1] + o
+                row.param = addrs[2 + t]
+                row.rows, row.cols = self.shapes[t]
+                row.group = self.groups[t]
+            self._known, self._grads = now, list(grads.addrs)
+        return grads
+
+    def step(self, grads, grad_coef=None, skip=None, stream=None):
+        """One step on ``grads`` (a list or a ``TensorList``, one tensor per
+        parameter): g = grad * ``grad_coef`` (a device fp32 word, e.g. the factor of
+        ``grad_norm_clip``); a non-zero device word ``skip`` leaves everything
+        unchanged on the device."""
+        if skip is not None and (skip.element_size() != 4 or not skip.is_cuda):
+            raise ValueError("skip must be a 4-byte CUDA word")
+        coef = _f32_word(grad_coef, "grad_coef") or None
+        grads = self._call(grads)
+        dev = self.master.device
+        hp = (_capi.MuonHP * len(self.hps))(*[
+            (h.lr, h.momentum, h.weight_decay, h.match_rms, int(bool(h.nesterov)), 0)
+            for h in self.hps])
+        with _here(dev, stream):
+            ws, ws_bytes = self.workspace.at_least(self._need)
+            rc = _capi.lib().tensors_muon_step(
+                self._table, len(self.params), grads.dtype, self._param_code, hp, len(self.hps),
+                _quintic(self.rounds, self.coefficients, self.eps),
+                coef, skip.data_ptr() if skip is not None else None, ws, ws_bytes,
+                _stream(stream, dev))
+        if rc:
+            _capi.check("tensors_muon_step", rc)
 
 
 # ---------------------------------------------------------------- ledger

@@ -72,6 +72,21 @@ class TokenLoss(ctypes.Structure):
                 ("workspace", c_vp), ("workspace_bytes", c_i64)]
 
 
+class Quintic(ctypes.Structure):
+    _fields_ = [("a", c_f64), ("b", c_f64), ("c", c_f64), ("eps", c_f64), ("rounds", c_i32),
+                ("pad_", c_i32)]
+
+
+class MuonHP(ctypes.Structure):
+    _fields_ = [("lr", c_f64), ("momentum", c_f64), ("weight_decay", c_f64),
+                ("match_rms", c_f64), ("nesterov", c_i32), ("pad_", c_i32)]
+
+
+class Matrix(ctypes.Structure):
+    _fields_ = [("grad", c_vp), ("master", c_vp), ("m", c_vp), ("param", c_vp), ("rows", c_i64),
+                ("cols", c_i64), ("group", c_i32), ("pad_", c_i32)]
+
+
 # name -> (restype, argtypes), exactly the declarations of include/shardstep.h
 SIGNATURES = {
     "fsdp_layout": (c_i32, [P_i64, c_i32, c_i32, ctypes.POINTER(LayoutInfo), P_i64, P_i64, P_i64]),
@@ -152,6 +167,22 @@ SIGNATURES = {
                                   c_vp]),
     "fsdp_state_rs_avg_adamw_cast": (c_i32, [c_vp, c_i32, c_i32, c_i32, c_i64, c_vp, c_vp, c_vp,
                                              c_vp, c_vp, c_vp]),
+    "token_embedding": (c_i32, [c_vp, c_i64, c_i32, c_i64, c_i64, c_vp, c_i32, c_i64, c_f32, c_vp,
+                                c_i64, c_vp]),
+    "token_embedding_grad_workspace_bytes": (c_i64, [c_i64, c_i64, c_i64]),
+    "token_embedding_grad": (c_i32, [c_vp, c_i64, c_i32, c_vp, c_i32, c_i64, c_f32, c_vp, c_i64,
+                                     c_i32, c_i64, c_i64, c_i32, c_vp, c_i64, c_vp]),
+    "rows_layer_norm": (c_i32, [c_vp, c_i64, c_i32, c_i64, c_i64, c_vp, c_vp, c_i32, c_f32, c_vp,
+                                c_i64, c_vp, c_vp, c_vp]),
+    "rows_layer_norm_workspace_bytes": (c_i64, [c_i64]),
+    "rows_layer_norm_grad": (c_i32, [c_vp, c_i64, c_vp, c_i64, c_i32, c_i64, c_i64, c_vp, c_vp,
+                                     c_vp, c_i32, c_vp, c_i64, c_vp, c_vp, c_i32, c_vp, c_i64,
+                                     c_vp]),
+    "matrices_workspace_bytes": (c_i64, [P_i64, P_i64, c_i32]),
+    "matrices_orthogonalize": (c_i32, [c_vp, c_vp, P_i64, P_i64, c_i32, c_i32, c_i32,
+                                       ctypes.POINTER(Quintic), c_vp, c_i64, c_vp]),
+    "tensors_muon_step": (c_i32, [c_vp, c_i32, c_i32, c_i32, ctypes.POINTER(MuonHP), c_i32,
+                                  ctypes.POINTER(Quintic), c_vp, c_vp, c_vp, c_i64, c_vp]),
 }
 
 # Size in bytes of shardstep_adamw_state_t (int64 step, two doubles, 8 floats).

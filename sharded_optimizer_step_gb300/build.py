@@ -15,9 +15,9 @@ OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libshardstep.so")
 
 SOURCES = ["step.cu", "step_tma.cu", "copy.cu", "accum_step.cu", "fsdp2_step.cu", "state.cu",
-           "tensors.cu", "token_loss.cu",
-           "api.cpp", "tuning_api.cpp", "ckpt.cpp", "ready.cpp"]
-HEADERS = ["common.cuh", "internal.h", "pairs.cuh", "tma.cuh"]
+           "tensors.cu", "token_loss.cu", "embedding.cu", "layer_norm.cu", "matrix.cu",
+           "api.cpp", "tuning_api.cpp", "model_api.cpp", "ckpt.cpp", "ready.cpp"]
+HEADERS = ["checks.h", "common.cuh", "elem.cuh", "internal.h", "pairs.cuh", "tcgen05.cuh", "tma.cuh"]
 ARCH = "103a"
 
 

@@ -393,8 +393,10 @@ int shardstep_device_status(uint32_t* status, int32_t clear) {
     unsigned int loss = 0;
     cudaError_t e = read_device_status(&s, clear != 0);
     if (e == cudaSuccess) e = read_loss_status(&loss, clear != 0);
+    unsigned int matrix = 0;
+    if (e == cudaSuccess) e = read_matrix_status(&matrix, clear != 0);
     if (e != cudaSuccess) return cuda_fail(e, "reading the device status word");
-    *status = s | loss;
+    *status = s | loss | matrix;
     return ok();
 }
 

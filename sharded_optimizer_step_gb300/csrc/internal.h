@@ -410,6 +410,115 @@ cudaError_t launch_preference_forward(const TokenArgs& a, const PreferenceArgs& 
 cudaError_t launch_loss_backward(const TokenArgs& a, const PreferenceArgs& p, int64_t begin,
                                  int64_t end, int dtype, bool staged, cudaStream_t stream);
 
+// ------------------------------------------- embedding and layer norm
+// (embedding.cu, layer_norm.cu; host side in model_api.cpp)
+
+// Token i's row at rows + i * row_stride (the lookup's output, the gradient's
+// d_out), id v's at table + v * table_stride (the table, or its gradient).
+struct EmbedArgs {
+    void* table;
+    int64_t table_stride;   // elements, as row_stride
+    void* rows;
+    int64_t row_stride;
+    const void* ids;
+    int ids64;
+    int accumulate;
+    int64_t n, vocab, dim;
+    float scale;
+};
+constexpr int kEmbedChunkMax = 512;    // sorted tokens of a chunk
+constexpr int kEmbedSortRange = 2048;  // ids of a sorting block
+constexpr int kEmbedZeroRows = 16;     // rows that a block looks through for absent ids
+struct EmbedPlan {
+    int chunk;              // sorted tokens per block
+    int64_t chunks;
+};
+EmbedPlan embed_plan(int64_t n, int64_t dim);
+// The gradient's workspace.
+struct EmbedSort {
+    int32_t* token;         // sorted by id; n each
+    int32_t* id;
+    uint32_t* row_start;    // vocab + 1: each id's first place in the list
+    float* piece;           // 2 * dim per chunk: of a run from before, of one that goes on
+    int range, chunk;
+    int64_t chunks, slices;
+};
+cudaError_t launch_embedding(const EmbedArgs& a, int type, bool vec, cudaStream_t stream);
+cudaError_t launch_embedding_grad(const EmbedArgs& a, EmbedSort s, int in_type, int out_type,
+                                  bool vec, cudaStream_t stream);
+
+struct NormRows {
+    const void* x;
+    int64_t x_stride;       // elements, as all strides
+    void* out;
+    int64_t out_stride;
+    const void *w, *b;      // or null
+    float *mean, *rstd;
+    int64_t rows, cols;
+    float eps;
+};
+struct NormGradRows {
+    const void* x;
+    int64_t x_stride;
+    const void* d;
+    int64_t d_stride;
+    void* d_x;              // or null
+    int64_t d_x_stride;
+    const void* w;          // or null
+    const float *mean, *rstd;
+    float* piece;           // 2 * cols per block, or null: no d_w, d_b
+    int64_t rows, cols;
+};
+// Blocks of the backward pass, each of which leaves one row of column sums; at
+// most kNormPieces.
+constexpr int kNormPieces = 160;
+int norm_pieces(int64_t rows, int64_t cols, bool vec);
+cudaError_t launch_layer_norm(const NormRows& a, int type, int w_type, bool vec,
+                              cudaStream_t stream);
+cudaError_t launch_layer_norm_grad(const NormGradRows& a, int type, int w_type, void* d_w,
+                                   void* d_b, int accumulate, bool vec, cudaStream_t stream);
+
+// ------------------------------------------------ matrices' updates
+// (matrix.cu; host side in model_api.cpp)
+
+constexpr int kMatrices = 64;        // of one group: a launch's table
+constexpr int kMatrixParts = 256;    // sums of squares of one matrix
+struct MatrixItem {
+    const void* grad;                // m x n, or n x m where tall
+    float* master;                   // null: `out` takes the orthogonal matrix
+    float* m_buf;                    // momentum, or null
+    void* out;                       // the parameter (may be null), or the result
+    void* x[2];                      // images in the workspace
+    void* gram;
+    void* poly;
+    double* part;
+    float step;                      // learning rate times the matrix's factor
+    int32_t m, n, mp, np;            // m <= n, and padded to 128
+    int16_t tall, group;
+};
+struct MatrixTable {
+    MatrixItem item[kMatrices];
+    uint32_t sym0[kMatrices + 1];    // first tile of the symmetric products
+    uint32_t full0[kMatrices + 1];   // of the others
+    uint32_t part0[kMatrices + 1];   // first sum of squares
+    uint32_t image0[kMatrices + 1];  // first image block of x
+    int32_t count;
+};
+struct MatrixGroup {
+    float lr_wd, mu, one_mu;
+    int nesterov;
+};
+struct MatrixCall {
+    MatrixGroup group[kMaxGroups];
+    const float* coef;
+    const unsigned int* skip;
+    float a, b, c, eps;
+    int rounds, out_type;
+};
+cudaError_t launch_matrices(const MatrixTable& t, const MatrixCall& c, int grad_type,
+                            cudaStream_t stream);
+cudaError_t read_matrix_status(unsigned int* status, bool clear);
+
 // Host helpers of api.cpp for the other translation units: the last error of
 // the calling thread, the name shardstep_last_kernel reports, the per-step
 // scalars.

@@ -1,0 +1,572 @@
+// Host side of the embedding (token_embedding*), layer norm (rows_layer_norm*)
+// and the matrices' updates (matrices_*, tensors_muon_step): argument checks, the
+// tables that travel with each launch, and dispatch.  Nothing here allocates
+// device memory or keeps a pointer.
+#include <algorithm>
+#include <cmath>
+#include <memory>
+#include <new>
+#include <numeric>
+#include <vector>
+
+#include "checks.h"
+#include "internal.h"
+#include "shardstep.h"
+
+namespace shardstep {
+namespace {
+
+int64_t span(int64_t rows, int64_t cols, int64_t stride, int es) {
+    return rows > 0 ? ((rows - 1) * stride + cols) * es : 0;
+}
+// Whether every row starts on a 16-byte boundary.
+bool rows_aligned(const void* p, int64_t stride, int64_t rows, int es) {
+    return aligned(p, 16) && (rows <= 1 || stride * es % 16 == 0);
+}
+bool stride_ok(int64_t stride, int64_t rows, int64_t cols) {
+    return stride >= cols && (rows == 0 || stride <= (int64_t{1} << 60) / rows);
+}
+int cuda_fail(const char* what, cudaError_t e) {
+    return ready_fail(SHARDSTEP_ERR_CUDA, "%s launch: %s", what, cudaGetErrorString(e));
+}
+
+// -------------------------------------------------------------- embedding
+
+bool embed_sizes(int64_t n, int64_t vocab, int64_t dim) {
+    return n >= 0 && n <= INT32_MAX && vocab >= 1 && vocab < INT32_MAX && dim >= 1 &&
+           dim <= (int64_t{1} << 23);
+}
+
+// The checks that both directions share.
+int check_embedding(const void* table, int64_t table_stride, int64_t vocab, int64_t dim,
+                    const void* ids, int32_t id_bytes, int64_t n, float scale, const void* rows,
+                    int64_t row_stride, int es_table, int es_rows) {
+    if (es_table == 0 || es_rows == 0) return ready_fail(SHARDSTEP_ERR_INVALID, "unknown dtype");
+    if (id_bytes != 4 && id_bytes != 8)
+        return ready_fail(SHARDSTEP_ERR_INVALID, "id_bytes must be 4 or 8");
+    if (!embed_sizes(n, vocab, dim))
+        return ready_fail(SHARDSTEP_ERR_INVALID, "n, vocab or dim out of range");
+    if (!std::isfinite(scale)) return ready_fail(SHARDSTEP_ERR_INVALID, "scale is not finite");
+    if (!stride_ok(table_stride, vocab, dim) || !stride_ok(row_stride, n, dim))
+        return ready_fail(SHARDSTEP_ERR_INVALID, "a row stride is out of range");
+    if (!table || (n > 0 && (!ids || !rows)))
+        return ready_fail(SHARDSTEP_ERR_INVALID, "a NULL array");
+    if (!aligned(table, es_table) || !aligned(rows, es_rows) || !aligned(ids, id_bytes))
+        return ready_fail(SHARDSTEP_ERR_INVALID, "an array is misaligned");
+    return SHARDSTEP_OK;
+}
+
+int64_t round16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
+
+// --------------------------------------------------------------- matrices
+
+constexpr int64_t kSideMax = int64_t{1} << 20;
+constexpr int64_t kGroupBytes = int64_t{2} << 30;
+
+int64_t padded(int64_t n) { return (n + 127) / 128 * 128; }
+// A matrix's part of the workspace: two images of X, those of A and B, the sums.
+int64_t matrix_bytes(int64_t rows, int64_t cols) {
+    const int64_t m = padded(std::min(rows, cols)), n = padded(std::max(rows, cols));
+    return 8 * m * n + 8 * m * m + kMatrixParts * static_cast<int64_t>(sizeof(double));
+}
+bool side_ok(int64_t n) { return n >= 0 && n <= kSideMax; }
+
+struct Sides {
+    int64_t rows, cols;
+};
+// The end of the group that starts at `at`, and its workspace.
+template <typename F>
+int32_t group_end(const F& sides, int32_t n, int32_t at, int64_t* bytes) {
+    int count = 0;
+    *bytes = 0;
+    for (; at < n; ++at) {
+        const Sides s = sides(at);
+        if (s.rows == 0 || s.cols == 0) continue;
+        const int64_t b = matrix_bytes(s.rows, s.cols);
+        if (count == kMatrices || (count > 0 && *bytes + b > kGroupBytes)) break;
+        *bytes += b;
+        ++count;
+    }
+    return at;
+}
+template <typename F>
+int64_t workspace_for(const F& sides, int32_t n) {
+    int64_t most = 0;
+    for (int32_t at = 0; at < n;) {
+        int64_t bytes;
+        at = group_end(sides, n, at, &bytes);
+        most = std::max(most, bytes);
+    }
+    return most;
+}
+
+// The largest magnitude of a x + b x^3 + c x^5 over [0, hi].
+double quintic_most(double a, double b, double c, double hi) {
+    const auto f = [&](double x) { return std::fabs(x * (a + x * x * (b + x * x * c))); };
+    double most = f(hi);
+    // where a + 3 b t + 5 c t^2 = 0, t = x^2
+    const double q = 9 * b * b - 20 * a * c;
+    const auto at = [&](double t) {
+        if (t > 0 && t < hi * hi) most = std::max(most, f(std::sqrt(t)));
+    };
+    if (c != 0 && q >= 0) {
+        at((-3 * b + std::sqrt(q)) / (10 * c));
+        at((-3 * b - std::sqrt(q)) / (10 * c));
+    } else if (c == 0 && b != 0) {
+        at(-a / (3 * b));
+    }
+    return most;
+}
+// The largest magnitude of b t + c t^2 over [0, hi].
+double square_most(double b, double c, double hi) {
+    const auto f = [&](double t) { return std::fabs(t * (b + t * c)); };
+    double most = f(hi);
+    if (c != 0 && -b / (2 * c) > 0 && -b / (2 * c) < hi) most = std::max(most, f(-b / (2 * c)));
+    return most;
+}
+
+int take_quintic(const shardstep_quintic_t* q, MatrixCall* call) {
+    if (q == nullptr) return ready_fail(SHARDSTEP_ERR_INVALID, "quintic is NULL");
+    if (q->rounds < 1 || q->rounds > 64)
+        return ready_fail(SHARDSTEP_ERR_INVALID, "rounds must be 1..64 (got %d)", q->rounds);
+    if (!std::isfinite(q->a) || !std::isfinite(q->b) || !std::isfinite(q->c) ||
+        !(q->eps >= 0) || !std::isfinite(q->eps))
+        return ready_fail(SHARDSTEP_ERR_INVALID, "a coefficient or eps is out of range");
+    double hi = 1.0;
+    for (int32_t k = 0; k < q->rounds; ++k) {
+        // X and A are held times 2^15 and B times 2^14 in halves, which end at 65504
+        if (!(hi <= 1.39) || !(square_most(q->b, q->c, hi * hi) <= 3.9))
+            return ready_fail(SHARDSTEP_ERR_INVALID,
+                              "the coefficients let values grow past what round %d holds", k + 1);
+        hi = std::max(hi, quintic_most(q->a, q->b, q->c, hi));
+    }
+    call->a = static_cast<float>(q->a);
+    call->b = static_cast<float>(q->b);
+    call->c = static_cast<float>(q->c);
+    call->eps = static_cast<float>(q->eps);
+    call->rounds = q->rounds;
+    return SHARDSTEP_OK;
+}
+
+// The matrices [at, end) of the list as one group's table; false: all empty.
+template <typename F>
+bool fill_table(const F& item, int32_t at, int32_t end, char* ws, MatrixTable* t) {
+    int k = 0;
+    for (; at < end; ++at) {
+        MatrixItem x{};
+        int64_t rows, cols;
+        item(at, &x, &rows, &cols);
+        if (rows == 0 || cols == 0) continue;
+        x.tall = rows > cols;
+        x.m = static_cast<int32_t>(std::min(rows, cols));
+        x.n = static_cast<int32_t>(std::max(rows, cols));
+        x.mp = static_cast<int32_t>(padded(x.m));
+        x.np = static_cast<int32_t>(padded(x.n));
+        const int64_t wide = 4 * static_cast<int64_t>(x.mp) * x.np;
+        const int64_t square = 4 * static_cast<int64_t>(x.mp) * x.mp;
+        x.x[0] = ws;
+        x.x[1] = ws + wide;
+        x.gram = ws + 2 * wide;
+        x.poly = ws + 2 * wide + square;
+        x.part = reinterpret_cast<double*>(ws + 2 * wide + 2 * square);
+        ws += matrix_bytes(rows, cols);
+        t->item[k++] = x;
+    }
+    t->count = k;
+    if (k == 0) return false;
+    // the longest tiles first, so that the last ones to end are short
+    std::sort(t->item, t->item + k, [](const MatrixItem& a, const MatrixItem& b) {
+        return a.mp != b.mp ? a.mp > b.mp : a.np > b.np;
+    });
+    uint32_t sym = 0, full = 0, part = 0, image = 0;
+    for (int j = 0; j < k; ++j) {
+        const MatrixItem& x = t->item[j];
+        t->sym0[j] = sym;
+        t->full0[j] = full;
+        t->part0[j] = part;
+        t->image0[j] = image;
+        const uint32_t side = x.mp / 128;
+        sym += side * (side + 1) / 2;
+        full += side * (x.np / 128);
+        part += static_cast<uint32_t>(std::min<int64_t>(
+            kMatrixParts, (static_cast<int64_t>(x.m) * x.n + 4095) / 4096));
+        image += side * (x.np / 64);
+    }
+    t->sym0[k] = sym;
+    t->full0[k] = full;
+    t->part0[k] = part;
+    t->image0[k] = image;
+    return true;
+}
+
+template <typename S, typename F>
+int run_groups(const S& sides, const F& item, int32_t n, const MatrixCall& call, int grad_dtype,
+               void* workspace, const char* what, cudaStream_t stream) {
+    std::unique_ptr<MatrixTable> t(new MatrixTable);
+    for (int32_t at = 0; at < n;) {
+        int64_t bytes;
+        const int32_t end = group_end(sides, n, at, &bytes);
+        if (fill_table(item, at, end, static_cast<char*>(workspace), t.get())) {
+            const cudaError_t e = launch_matrices(*t, call, grad_dtype, stream);
+            if (e != cudaSuccess) return cuda_fail(what, e);
+        }
+        at = end;
+    }
+    return SHARDSTEP_OK;
+}
+
+int check_workspace(const void* workspace, int64_t bytes, int64_t need) {
+    if (need > 0 && workspace == nullptr)
+        return ready_fail(SHARDSTEP_ERR_INVALID, "workspace is NULL");
+    if (!aligned(workspace, 16)) return ready_fail(SHARDSTEP_ERR_INVALID, "workspace misaligned");
+    if (bytes < need)
+        return ready_fail(SHARDSTEP_ERR_INVALID, "the workspace needs %lld bytes, got %lld",
+                          static_cast<long long>(need), static_cast<long long>(bytes));
+    return SHARDSTEP_OK;
+}
+
+}  // namespace
+}  // namespace shardstep
+
+using namespace shardstep;
+
+extern "C" {
+
+int token_embedding(const void* table, int64_t table_stride, int32_t dtype, int64_t vocab,
+                    int64_t dim, const void* ids, int32_t id_bytes, int64_t n, float scale,
+                    void* out, int64_t out_stride, void* stream) try {
+    const int es = elem_size(dtype);
+    if (int rc = check_embedding(table, table_stride, vocab, dim, ids, id_bytes, n, scale, out,
+                                 out_stride, es, es);
+        rc != SHARDSTEP_OK)
+        return rc;
+    if (n == 0) return ready_ok();
+    std::vector<Range> reads, writes;
+    add_range(reads, table, span(vocab, dim, table_stride, es));
+    add_range(reads, ids, n * id_bytes);
+    add_range(writes, out, span(n, dim, out_stride, es));
+    if (int rc = check_ranges(&reads, &writes); rc != SHARDSTEP_OK) return rc;
+    EmbedArgs a{};
+    a.table = const_cast<void*>(table);
+    a.table_stride = table_stride;
+    a.rows = out;
+    a.row_stride = out_stride;
+    a.ids = ids;
+    a.ids64 = id_bytes == 8;
+    a.n = n;
+    a.vocab = vocab;
+    a.dim = dim;
+    a.scale = scale;
+    const bool vec = rows_aligned(table, table_stride, vocab, es) &&
+                     rows_aligned(out, out_stride, n, es) && dim * es % 16 == 0;
+    const cudaError_t e = launch_embedding(a, dtype, vec, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail("embedding", e);
+    record_kernel("embedding_lookup<%s>", dtype_name(dtype));
+    return ready_ok();
+} catch (const std::bad_alloc&) {
+    return ready_fail(SHARDSTEP_ERR_CAPACITY, "out of host memory");
+}
+
+int64_t token_embedding_grad_workspace_bytes(int64_t n, int64_t vocab, int64_t dim) {
+    if (!embed_sizes(n, vocab, dim)) return -1;
+    return 2 * round16(4 * n) + round16(4 * (vocab + 1)) +
+           8 * dim * embed_plan(n, dim).chunks;
+}
+
+int token_embedding_grad(const void* d_out, int64_t d_out_stride, int32_t dtype, const void* ids,
+                         int32_t id_bytes, int64_t n, float scale, void* grad,
+                         int64_t grad_stride, int32_t grad_dtype, int64_t vocab, int64_t dim,
+                         int32_t accumulate, void* workspace, int64_t workspace_bytes,
+                         void* stream) try {
+    const int es = elem_size(dtype), gs = elem_size(grad_dtype);
+    if (int rc = check_embedding(grad, grad_stride, vocab, dim, ids, id_bytes, n, scale, d_out,
+                                 d_out_stride, gs, es);
+        rc != SHARDSTEP_OK)
+        return rc;
+    const int64_t need = token_embedding_grad_workspace_bytes(n, vocab, dim);
+    if (int rc = check_workspace(workspace, workspace_bytes, need); rc != SHARDSTEP_OK) return rc;
+    if (n == 0 && accumulate) return ready_ok();
+    std::vector<Range> reads, writes;
+    add_range(reads, d_out, span(n, dim, d_out_stride, es));
+    add_range(reads, ids, n * id_bytes);
+    add_range(writes, grad, span(vocab, dim, grad_stride, gs));
+    add_range(writes, workspace, need);
+    if (int rc = check_ranges(&reads, &writes); rc != SHARDSTEP_OK) return rc;
+    EmbedArgs a{};
+    a.table = grad;
+    a.table_stride = grad_stride;
+    a.rows = const_cast<void*>(d_out);
+    a.row_stride = d_out_stride;
+    a.ids = ids;
+    a.ids64 = id_bytes == 8;
+    a.accumulate = accumulate != 0;
+    a.n = n;
+    a.vocab = vocab;
+    a.dim = dim;
+    a.scale = scale;
+    const EmbedPlan plan = embed_plan(n, dim);
+    char* ws = static_cast<char*>(workspace);
+    EmbedSort s{};
+    s.token = reinterpret_cast<int32_t*>(ws);
+    s.id = reinterpret_cast<int32_t*>(ws += round16(4 * n));
+    s.row_start = reinterpret_cast<uint32_t*>(ws += round16(4 * n));
+    s.piece = reinterpret_cast<float*>(ws + round16(4 * (vocab + 1)));
+    s.chunk = plan.chunk;
+    s.chunks = plan.chunks;
+    // a vector of d_out stands over as many elements of grad
+    const int per = 16 / es;
+    const int at_grad = std::min(16, per * gs);
+    const bool vec = rows_aligned(d_out, d_out_stride, n, es) && dim % per == 0 &&
+                     aligned(grad, at_grad) && (vocab == 1 || grad_stride * gs % at_grad == 0);
+    const cudaError_t e = launch_embedding_grad(a, s, dtype, grad_dtype, vec,
+                                                static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail("embedding gradient", e);
+    record_kernel("embedding_sum<%s, %s>", dtype_name(dtype), dtype_name(grad_dtype));
+    return ready_ok();
+} catch (const std::bad_alloc&) {
+    return ready_fail(SHARDSTEP_ERR_CAPACITY, "out of host memory");
+}
+
+// ------------------------------------------------------------- layer norm
+
+int rows_layer_norm(const void* x, int64_t x_stride, int32_t dtype, int64_t rows, int64_t cols,
+                    const void* weight, const void* bias, int32_t weight_dtype, float eps,
+                    void* out, int64_t out_stride, float* mean, float* rstd, void* stream) try {
+    const int es = elem_size(dtype), ws = elem_size(weight_dtype);
+    if (es == 0) return ready_fail(SHARDSTEP_ERR_INVALID, "unknown dtype %d", dtype);
+    if (weight_dtype != dtype && weight_dtype != SHARDSTEP_DTYPE_F32)
+        return ready_fail(SHARDSTEP_ERR_INVALID, "weight_dtype must be dtype or fp32");
+    if (rows < 0 || rows > (int64_t{1} << 40) || cols < 1 || cols > (int64_t{1} << 24))
+        return ready_fail(SHARDSTEP_ERR_INVALID, "rows or cols out of range");
+    if (!(eps >= 0.0f) || !std::isfinite(eps))
+        return ready_fail(SHARDSTEP_ERR_INVALID, "eps must be finite and >= 0");
+    if (!stride_ok(x_stride, rows, cols) || !stride_ok(out_stride, rows, cols))
+        return ready_fail(SHARDSTEP_ERR_INVALID, "a row stride is out of range");
+    if (rows == 0) return ready_ok();
+    if (!x || !out || !mean || !rstd) return ready_fail(SHARDSTEP_ERR_INVALID, "a NULL array");
+    if (!aligned(x, es) || !aligned(out, es) || !aligned(weight, ws) || !aligned(bias, ws) ||
+        !aligned(mean, 4) || !aligned(rstd, 4))
+        return ready_fail(SHARDSTEP_ERR_INVALID, "an array is misaligned");
+    std::vector<Range> reads, writes;
+    add_range(reads, x, span(rows, cols, x_stride, es));
+    add_range(reads, weight, weight ? cols * ws : 0);
+    add_range(reads, bias, bias ? cols * ws : 0);
+    add_range(writes, out, span(rows, cols, out_stride, es));
+    add_range(writes, mean, rows * 4);
+    add_range(writes, rstd, rows * 4);
+    if (int rc = check_ranges(&reads, &writes); rc != SHARDSTEP_OK) return rc;
+    const NormRows a{x, x_stride, out, out_stride, weight, bias, mean, rstd, rows, cols, eps};
+    const bool vec = rows_aligned(x, x_stride, rows, es) &&
+                     rows_aligned(out, out_stride, rows, es) && aligned(weight, 16) &&
+                     aligned(bias, 16);
+    const cudaError_t e =
+        launch_layer_norm(a, dtype, weight_dtype, vec, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail("layer norm", e);
+    record_kernel("layer_norm_rows<%s>", dtype_name(dtype));
+    return ready_ok();
+} catch (const std::bad_alloc&) {
+    return ready_fail(SHARDSTEP_ERR_CAPACITY, "out of host memory");
+}
+
+int64_t rows_layer_norm_workspace_bytes(int64_t cols) {
+    if (cols < 1 || cols > (int64_t{1} << 24)) return -1;
+    return 8 * cols * kNormPieces;
+}
+
+int rows_layer_norm_grad(const void* d_out, int64_t d_out_stride, const void* x,
+                         int64_t x_stride, int32_t dtype, int64_t rows, int64_t cols,
+                         const float* mean, const float* rstd, const void* weight,
+                         int32_t weight_dtype, void* d_x, int64_t d_x_stride, void* d_weight,
+                         void* d_bias, int32_t accumulate, void* workspace,
+                         int64_t workspace_bytes, void* stream) try {
+    const int es = elem_size(dtype), ws = elem_size(weight_dtype);
+    if (es == 0) return ready_fail(SHARDSTEP_ERR_INVALID, "unknown dtype %d", dtype);
+    if (weight_dtype != dtype && weight_dtype != SHARDSTEP_DTYPE_F32)
+        return ready_fail(SHARDSTEP_ERR_INVALID, "weight_dtype must be dtype or fp32");
+    if (rows < 0 || rows > (int64_t{1} << 40) || cols < 1 || cols > (int64_t{1} << 24))
+        return ready_fail(SHARDSTEP_ERR_INVALID, "rows or cols out of range");
+    if (!stride_ok(x_stride, rows, cols) || !stride_ok(d_out_stride, rows, cols) ||
+        (d_x && !stride_ok(d_x_stride, rows, cols)))
+        return ready_fail(SHARDSTEP_ERR_INVALID, "a row stride is out of range");
+    const bool columns = d_weight != nullptr || d_bias != nullptr;
+    const int64_t need = columns ? rows_layer_norm_workspace_bytes(cols) : 0;
+    if (rows > 0 && (!x || !d_out || !mean || !rstd))
+        return ready_fail(SHARDSTEP_ERR_INVALID, "a NULL array");
+    if (!aligned(x, es) || !aligned(d_out, es) || !aligned(d_x, es) || !aligned(weight, ws) ||
+        !aligned(d_weight, ws) || !aligned(d_bias, ws) || !aligned(mean, 4) || !aligned(rstd, 4))
+        return ready_fail(SHARDSTEP_ERR_INVALID, "an array is misaligned");
+    if (int rc = check_workspace(workspace, workspace_bytes, need); rc != SHARDSTEP_OK) return rc;
+    if (!columns && (rows == 0 || d_x == nullptr)) return ready_ok();
+    if (rows == 0 && accumulate) return ready_ok();
+    std::vector<Range> reads, writes;
+    add_range(reads, x, span(rows, cols, x_stride, es));
+    add_range(reads, d_out, span(rows, cols, d_out_stride, es));
+    add_range(reads, weight, weight ? cols * ws : 0);
+    add_range(reads, mean, rows * 4);
+    add_range(reads, rstd, rows * 4);
+    add_range(writes, d_x, d_x ? span(rows, cols, d_x_stride, es) : 0);
+    add_range(writes, d_weight, d_weight ? cols * ws : 0);
+    add_range(writes, d_bias, d_bias ? cols * ws : 0);
+    add_range(writes, workspace, need);
+    if (int rc = check_ranges(&reads, &writes); rc != SHARDSTEP_OK) return rc;
+    const NormGradRows a{x,    x_stride, d_out, d_out_stride,
+                         d_x,  d_x_stride, weight, mean, rstd,
+                         columns ? static_cast<float*>(workspace) : nullptr, rows, cols};
+    const bool vec = rows_aligned(x, x_stride, rows, es) &&
+                     rows_aligned(d_out, d_out_stride, rows, es) && aligned(weight, 16) &&
+                     (d_x == nullptr || rows_aligned(d_x, d_x_stride, rows, es));
+    const cudaError_t e =
+        launch_layer_norm_grad(a, dtype, weight_dtype, d_weight, d_bias, accumulate != 0, vec,
+                               static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail("layer norm gradient", e);
+    record_kernel("layer_norm_rows_grad<%s>", dtype_name(dtype));
+    return ready_ok();
+} catch (const std::bad_alloc&) {
+    return ready_fail(SHARDSTEP_ERR_CAPACITY, "out of host memory");
+}
+
+// --------------------------------------------------------------- matrices
+
+int64_t matrices_workspace_bytes(const int64_t* rows, const int64_t* cols, int32_t n) {
+    if (n < 0 || (n > 0 && (!rows || !cols))) return -1;
+    for (int32_t i = 0; i < n; ++i)
+        if (!side_ok(rows[i]) || !side_ok(cols[i])) return -1;
+    return workspace_for([&](int32_t i) { return Sides{rows[i], cols[i]}; }, n);
+}
+
+int matrices_orthogonalize(const void* const* in, void* const* out, const int64_t* rows,
+                           const int64_t* cols, int32_t n, int32_t in_dtype, int32_t out_dtype,
+                           const shardstep_quintic_t* quintic, void* workspace,
+                           int64_t workspace_bytes, void* stream) try {
+    const int es = elem_size(in_dtype), os = elem_size(out_dtype);
+    if (es == 0 || os == 0) return ready_fail(SHARDSTEP_ERR_INVALID, "unknown dtype");
+    if (n < 0) return ready_fail(SHARDSTEP_ERR_INVALID, "n must be >= 0");
+    MatrixCall call{};
+    if (int rc = take_quintic(quintic, &call); rc != SHARDSTEP_OK) return rc;
+    call.out_type = out_dtype;
+    if (n == 0) return ready_ok();
+    if (!in || !out || !rows || !cols) return ready_fail(SHARDSTEP_ERR_INVALID, "a NULL array");
+    std::vector<Range> reads, writes;
+    reads.reserve(n);
+    writes.reserve(n + 1);
+    for (int32_t i = 0; i < n; ++i) {
+        if (!side_ok(rows[i]) || !side_ok(cols[i]))
+            return ready_fail(SHARDSTEP_ERR_INVALID, "matrix %d: a side is out of range", i);
+        const int64_t numel = rows[i] * cols[i];
+        if (numel == 0) continue;
+        if (!in[i] || !out[i] || !aligned(in[i], es) || !aligned(out[i], os))
+            return ready_fail(SHARDSTEP_ERR_INVALID, "matrix %d: NULL or misaligned", i);
+        add_range(reads, in[i], numel * es);
+        add_range(writes, out[i], numel * os);
+    }
+    const auto sides = [&](int32_t i) { return Sides{rows[i], cols[i]}; };
+    const int64_t need = workspace_for(sides, n);
+    if (int rc = check_workspace(workspace, workspace_bytes, need); rc != SHARDSTEP_OK) return rc;
+    add_range(writes, workspace, need);
+    if (int rc = check_ranges(&reads, &writes); rc != SHARDSTEP_OK) return rc;
+    const auto item = [&](int32_t i, MatrixItem* x, int64_t* r, int64_t* c) {
+        x->grad = in[i];
+        x->out = out[i];
+        *r = rows[i];
+        *c = cols[i];
+    };
+    if (int rc = run_groups(sides, item, n, call, in_dtype, workspace, "orthogonalize",
+                            static_cast<cudaStream_t>(stream));
+        rc != SHARDSTEP_OK)
+        return rc;
+    record_kernel("matrix_product<last> (tcgen05)");
+    return ready_ok();
+} catch (const std::bad_alloc&) {
+    return ready_fail(SHARDSTEP_ERR_CAPACITY, "out of host memory");
+}
+
+int tensors_muon_step(const shardstep_matrix_t* ms, int32_t n, int32_t grad_dtype,
+                      int32_t param_dtype, const shardstep_muon_t* hp, int32_t n_groups,
+                      const shardstep_quintic_t* quintic, const float* grad_coef,
+                      const uint32_t* skip, void* workspace, int64_t workspace_bytes,
+                      void* stream) try {
+    const int es = elem_size(grad_dtype);
+    if (es == 0) return ready_fail(SHARDSTEP_ERR_INVALID, "unknown grad dtype %d", grad_dtype);
+    if (param_dtype != SHARDSTEP_DTYPE_BF16 && param_dtype != SHARDSTEP_DTYPE_F16)
+        return ready_fail(SHARDSTEP_ERR_INVALID, "param dtype %d is not bf16 or fp16",
+                          param_dtype);
+    if (n < 0) return ready_fail(SHARDSTEP_ERR_INVALID, "n must be >= 0");
+    if (n_groups < 1) return ready_fail(SHARDSTEP_ERR_INVALID, "n_groups must be >= 1");
+    if (n_groups > kMaxGroups)
+        return ready_fail(SHARDSTEP_ERR_CAPACITY, "n_groups %d > %d", n_groups, kMaxGroups);
+    if (hp == nullptr) return ready_fail(SHARDSTEP_ERR_INVALID, "hp is NULL");
+    if (grad_coef && !aligned(grad_coef, 4))
+        return ready_fail(SHARDSTEP_ERR_INVALID, "grad_coef misaligned");
+    if (skip && !aligned(skip, 4)) return ready_fail(SHARDSTEP_ERR_INVALID, "skip misaligned");
+    MatrixCall call{};
+    if (int rc = take_quintic(quintic, &call); rc != SHARDSTEP_OK) return rc;
+    call.out_type = param_dtype;
+    call.coef = grad_coef;
+    call.skip = skip;
+    for (int32_t g = 0; g < n_groups; ++g) {
+        const shardstep_muon_t& h = hp[g];
+        if (!std::isfinite(h.lr) || !std::isfinite(h.weight_decay) ||
+            !(h.momentum >= 0 && h.momentum < 1) || !(h.match_rms >= 0) ||
+            !std::isfinite(h.match_rms))
+            return ready_fail(SHARDSTEP_ERR_INVALID, "hp[%d]: a value is out of range", g);
+        call.group[g] = MatrixGroup{static_cast<float>(h.lr * h.weight_decay),
+                                    static_cast<float>(h.momentum),
+                                    static_cast<float>(1 - h.momentum), h.nesterov != 0};
+    }
+    if (n == 0) return ready_ok();
+    if (ms == nullptr) return ready_fail(SHARDSTEP_ERR_INVALID, "matrices is NULL");
+    std::vector<Range> reads, writes;
+    reads.reserve(n + 2);
+    writes.reserve(3 * static_cast<size_t>(n) + 1);
+    add_range(reads, grad_coef, grad_coef ? 4 : 0);
+    add_range(reads, skip, skip ? 4 : 0);
+    for (int32_t i = 0; i < n; ++i) {
+        const shardstep_matrix_t& t = ms[i];
+        if (!side_ok(t.rows) || !side_ok(t.cols))
+            return ready_fail(SHARDSTEP_ERR_INVALID, "matrix %d: a side is out of range", i);
+        if (t.group < 0 || t.group >= n_groups)
+            return ready_fail(SHARDSTEP_ERR_INVALID, "matrix %d: group %d out of range", i,
+                              t.group);
+        const int64_t numel = t.rows * t.cols;
+        if (numel == 0) continue;
+        if (!t.grad || !t.master || !t.m)
+            return ready_fail(SHARDSTEP_ERR_INVALID, "matrix %d: a NULL array", i);
+        if (!aligned(t.grad, es) || !aligned(t.master, 4) || !aligned(t.m, 4) ||
+            !aligned(t.param, 2))
+            return ready_fail(SHARDSTEP_ERR_INVALID, "matrix %d: an array misaligned", i);
+        add_range(reads, t.grad, numel * es);
+        add_range(writes, t.master, numel * 4);
+        add_range(writes, t.m, numel * 4);
+        add_range(writes, t.param, t.param ? numel * 2 : 0);
+    }
+    const auto sides = [&](int32_t i) { return Sides{ms[i].rows, ms[i].cols}; };
+    const int64_t need = workspace_for(sides, n);
+    if (int rc = check_workspace(workspace, workspace_bytes, need); rc != SHARDSTEP_OK) return rc;
+    add_range(writes, workspace, need);
+    if (int rc = check_ranges(&reads, &writes); rc != SHARDSTEP_OK) return rc;
+    const auto item = [&](int32_t i, MatrixItem* x, int64_t* r, int64_t* c) {
+        const shardstep_matrix_t& t = ms[i];
+        const shardstep_muon_t& h = hp[t.group];
+        x->grad = t.grad;
+        x->master = t.master;
+        x->m_buf = t.m;
+        x->out = t.param;
+        x->group = static_cast<int16_t>(t.group);
+        const double rows = static_cast<double>(t.rows), cols = static_cast<double>(t.cols);
+        x->step = static_cast<float>(
+            h.lr * (h.match_rms > 0 ? h.match_rms * std::sqrt(std::max(rows, cols))
+                                    : std::sqrt(std::max(1.0, rows / std::max(cols, 1.0)))));
+        *r = t.rows;
+        *c = t.cols;
+    };
+    if (int rc = run_groups(sides, item, n, call, grad_dtype, workspace, "muon step",
+                            static_cast<cudaStream_t>(stream));
+        rc != SHARDSTEP_OK)
+        return rc;
+    record_kernel("matrix_product<last> (tcgen05)");
+    return ready_ok();
+} catch (const std::bad_alloc&) {
+    return ready_fail(SHARDSTEP_ERR_CAPACITY, "out of host memory");
+}
+
+}  // extern "C"

@@ -10,50 +10,12 @@
 #include <utility>
 #include <vector>
 
+#include "checks.h"
 #include "internal.h"
 #include "shardstep.h"
 
 namespace shardstep {
 namespace {
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-int elem_size(int32_t dtype) {
-    return dtype == SHARDSTEP_DTYPE_F32                                        ? 4
-           : dtype == SHARDSTEP_DTYPE_BF16 || dtype == SHARDSTEP_DTYPE_F16 ? 2
-                                                                               : 0;
-}
-const char* dtype_name(int dtype) {
-    return dtype == SHARDSTEP_DTYPE_F32 ? "f32" : dtype == SHARDSTEP_DTYPE_F16 ? "f16" : "bf16";
-}
-
-struct Range {
-    uintptr_t lo, hi;
-};
-void add_range(std::vector<Range>& v, const void* p, int64_t bytes) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    if (bytes > 0) v.push_back(Range{a, a + static_cast<uintptr_t>(bytes)});
-}
-void sort_ranges(std::vector<Range>& v) {
-    const auto less = [](const Range& a, const Range& b) { return a.lo < b.lo; };
-    if (!std::is_sorted(v.begin(), v.end(), less)) std::sort(v.begin(), v.end(), less);
-}
-// Whether any two of the sorted ranges share a byte.
-bool self_overlap(const std::vector<Range>& v) {
-    for (size_t k = 1; k < v.size(); ++k)
-        if (v[k].lo < v[k - 1].hi) return true;
-    return false;
-}
-// Whether a range of `reads` shares a byte with one of `writes` (both sorted;
-// the writes disjoint).
-bool cross_overlap(const std::vector<Range>& reads, const std::vector<Range>& writes) {
-    size_t w = 0;
-    for (const Range& r : reads) {
-        while (w < writes.size() && writes[w].hi <= r.lo) ++w;
-        if (w < writes.size() && writes[w].lo < r.hi) return true;
-    }
-    return false;
-}
 
 // The scalars of every group, from the host's hyper-parameters or from the
 // device-resident step states.
@@ -371,14 +333,6 @@ int take_tokens(const shardstep_token_loss_t* a, int64_t need, TokenArgs* k,
                    a->ids,     a->id_bytes == 8, a->weights, a->ref_logps,
                    a->logps,   n,             a->vocab,      a->grad_scale,
                    a->loss_scale, a->norm,    a->stats,      static_cast<LossWork*>(a->workspace)};
-    return SHARDSTEP_OK;
-}
-
-int check_ranges(std::vector<Range>* reads, std::vector<Range>* writes) {
-    sort_ranges(*reads);
-    sort_ranges(*writes);
-    if (self_overlap(*writes) || cross_overlap(*reads, *writes))
-        return ready_fail(SHARDSTEP_ERR_INVALID, "an output overlaps an input or another output");
     return SHARDSTEP_OK;
 }
 
