@@ -1008,8 +1008,9 @@ int rows_layer_norm_grad(const void* d_out, int64_t d_out_stride, const void* x,
  * values held as two halves each (22 bits): single precision.  A gradient that
  * holds an inf or NaN (or whose square passes fp32's range) gives NaNs.
  *   rounds        1..64.
- *   a, b, c       such that no singular value in [0, 1] passes 1.39 and no value of
- *                 b s^2 + c s^4 passes 3.9 in magnitude in any round. */
+ *   a, b, c       such that, of the singular values s that [0, 1] leads to, none
+ *                 passes 1.39 in any round, |b + c s^2| stays below 7.9 and
+ *                 |a + b s^2 + c s^4| below 3.9. */
 typedef struct {
     double a, b, c, eps;
     int32_t rounds;

@@ -489,12 +489,15 @@ struct MatrixItem {
     float* m_buf;                    // momentum, or null
     void* out;                       // the parameter (may be null), or the result
     void* x[2];                      // images in the workspace
-    void* gram;
-    void* poly;
+    void* gram;                      // X X^T
+    void* comb;                      // b + c X X^T
+    void* poly;                      // a + gram comb
     double* part;
+    unsigned int* tiles_done;        // result warps of all steps so far
     float step;                      // learning rate times the matrix's factor
-    int32_t m, n, mp, np;            // m <= n, and padded to 128
+    int32_t m, n, mp, np;            // m <= n, and padded to the tile
     int16_t tall, group;
+    int32_t whole;                   // master and out take whole vectors of 8 along rows
 };
 struct MatrixTable {
     MatrixItem item[kMatrices];
@@ -503,6 +506,7 @@ struct MatrixTable {
     uint32_t part0[kMatrices + 1];   // first sum of squares
     uint32_t image0[kMatrices + 1];  // first image block of x
     int32_t count;
+    int32_t pair;                    // tiles of 256 by pairs of blocks
 };
 struct MatrixGroup {
     float lr_wd, mu, one_mu;

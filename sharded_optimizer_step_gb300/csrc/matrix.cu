@@ -3,18 +3,17 @@
 //   X = u / (|u| + eps)            (transposed where u is taller than wide)
 //   A = X X^T,  B = b A + c A A,   X = a X + B X     `rounds` times
 //
-// over a list of matrices, as such or as an optimizer's step.  Three grouped
-// products a round, one launch each for all matrices of a group; A and B are
-// symmetric, so the first two compute the tiles on and above the diagonal and
-// write each off-diagonal one to both places.
+// over a list of matrices, as such or as an optimizer's step.  A and B are
+// symmetric, so the first two products of a round compute the tiles on and above
+// the diagonal and write each off-diagonal one to both places.
 //
 // The tensor cores multiply halves; to keep single precision each value v is
 // held as two, hi = half(s v) and lo = half(s v - hi) with s a power of two: 22
 // bits, of which three products hi hi + hi lo + lo hi make a product good to
 // about 2^-21 (one product of single halves loses 2e-3 to 2e-2 of the result
 // over five rounds, these three 1e-6).  s is 2^15 for X and A, whose elements
-// stay below sqrt(2) and 2, and 2^14 for B, below 4 (the host checks the
-// coefficients for it): nothing overflows, and an element of rms 1 / sqrt(m n),
+// stay below sqrt(2) and 2, 2^13 for C, below 8, and 2^14 for P, below 4 (the host
+// checks the coefficients for it): nothing overflows, and an element of rms 1 / sqrt(m n),
 // the smallest that occurs throughout, still has its 22 bits at m n = 2^30.
 //
 // Layout.  All operands live in the workspace as the images of what shared
@@ -24,6 +23,8 @@
 // and one block serves both as rows of k (X and A times their transposes) and
 // as k rows (X behind B).  Both sides are padded to 128 with zeros, which the
 // products keep zero.
+#include <atomic>
+
 #include "elem.cuh"
 #include "tcgen05.cuh"
 
@@ -32,26 +33,58 @@ namespace {
 
 __device__ unsigned int g_matrix_status;
 
-constexpr int kTile = 128;                    // of the results, both ways
 constexpr int kBlockBytes = 32768;            // 128 x 64 halves, hi and lo
 constexpr int kStages = 3;
 constexpr int kStageBytes = 2 * kBlockBytes;
-constexpr int kMatrixThreads = 192;           // producer, products, four warps of results
-constexpr int kTmemColumns = 256;             // two accumulators of 128
+// Results on their way out: each result warp's 32 rows x 32 columns of hi or lo.
+constexpr int kOutPiece = 2048;
 // The tensor cores cut sums off at fp32's last bit instead of rounding them, so a
 // long sum of positive terms (a row's square) falls behind by K / 16 times half a
 // bit.  A sum over k therefore goes in pieces of this many, which the result warps
 // add up in their registers (rounding to nearest).
-constexpr int kPiece = 512;
-constexpr float kScaleX = 32768.0f, kScaleB = 16384.0f;
+constexpr int kPiece = 256;
+constexpr float kScaleX = 32768.0f, kScaleC = 8192.0f, kScaleP = 16384.0f;
 
-enum class Step { kGram, kPoly, kApply, kLast };
+// A tile of results: 128 x 128 by one block, or 256 x 256 by a pair.  Each block
+// has 128 rows of it, and eight result warps, two for each quarter of the rows.
+template <bool PAIR>
+struct Shape {
+    static constexpr int kTile = PAIR ? 256 : 128;
+    static constexpr int kResultWarps = 8;
+    static constexpr int kColumns = kTile / 2;           // of a result warp
+    static constexpr int kThreads = 64 + 32 * kResultWarps;
+    static constexpr int kTmemColumns = 2 * kTile;       // two accumulators
+    static constexpr int kBlocks = PAIR ? 2 : 1;
+    static constexpr int kArrivals = kBlocks * kResultWarps;   // per tile
+    // stages from a multiple of 1024 on, then the pieces on their way out
+    static constexpr int kDynamicBytes =
+        kStages * kStageBytes + kResultWarps * kOutPiece + 1024;
+};
+
+enum Step { kGram, kPoly, kApply };
+
+struct Tile {
+    int matrix, round;
+    Step step;
+    int row, col;            // of the result, in elements
+    int k;                   // length of the sum
+    uint32_t before;         // tiles of the matrix that have to be done
+};
+// What a result warp goes by, in shared memory: its registers hold sums.
+struct Work {
+    Tile tile;
+    uint32_t index, step, end;   // of the tile, to the next one, of all
+    uint32_t lanes, out;     // its tensor memory, and its piece of shared memory
+    int down, across;        // its part of the tile
+};
 
 struct Shared {
     uint64_t full[kStages], empty[kStages];
+    uint64_t peer[kStages];                   // the other block's stage is full
     uint64_t done[2], taken[2];               // an accumulator is complete / has been read
     uint64_t drain;
     uint32_t tmem;
+    Work work[8];                             // of each result warp
 };
 
 // Byte offset of element (row, col) within an image block's hi half.
@@ -67,13 +100,6 @@ __device__ __forceinline__ const char* block_at(const void* image, int row, int 
     return block_at(const_cast<void*>(image), row, col, width);
 }
 
-struct Halves {
-    uint16_t hi, lo;
-};
-__device__ __forceinline__ Halves split(float v) {
-    const __half h = __float2half_rn(v);
-    return Halves{__half_as_ushort(h), __half_as_ushort(__float2half_rn(v - __half2float(h)))};
-}
 __device__ __forceinline__ void split_pair(float a, float b, uint32_t* hi, uint32_t* lo) {
     const __half2 h = __floats2half2_rn(a, b);
     const float2 f = __half22float2(h);
@@ -93,20 +119,22 @@ __device__ __forceinline__ int find(const uint32_t* first, int count, uint32_t t
     return lo;
 }
 
-struct Tile {
-    int matrix, row, col;    // of the result, in elements
-    int k;                   // length of the sum
-};
-template <Step STEP>
+// Tile `index` of the call: round by round, step by step, matrix by matrix.
+template <bool PAIR>
 __device__ __forceinline__ Tile tile_at(const MatrixTable& t, uint32_t index) {
-    constexpr bool sym = STEP == Step::kGram || STEP == Step::kPoly;
-    const uint32_t* first = sym ? t.sym0 : t.full0;
+    constexpr int kTile = Shape<PAIR>::kTile;
+    const uint32_t sym = t.sym0[t.count], full = t.full0[t.count];
     Tile out;
+    out.round = static_cast<int>(index / (2 * sym + full));
+    index -= out.round * (2 * sym + full);
+    out.step = index < sym ? kGram : index < 2 * sym ? kPoly : kApply;
+    index -= out.step * sym;
+    const uint32_t* first = out.step == kApply ? t.full0 : t.sym0;
     out.matrix = find(first, t.count, index);
     const MatrixItem& x = t.item[out.matrix];
     int i = static_cast<int>(index - first[out.matrix]);
-    const int side = x.mp / kTile;
-    if constexpr (sym) {
+    const int side = x.mp / kTile, all = x.np / kTile, half = side * (side + 1) / 2;
+    if (out.step != kApply) {
         int r = 0;
         while (i >= side - r) i -= side - r++;
         out.row = r * kTile;
@@ -115,131 +143,230 @@ __device__ __forceinline__ Tile tile_at(const MatrixTable& t, uint32_t index) {
         out.row = i % side * kTile;
         out.col = i / side * kTile;
     }
-    out.k = STEP == Step::kGram ? x.np : x.mp;
+    out.k = out.step == kGram ? x.np : x.mp;
+    out.before = out.round * (2 * half + side * all) + out.step * half;
     return out;
+}
+
+// Which operands' 64 k from k on come from blocks that hold k along their rows: X
+// behind P, and of a symmetric matrix what lies below the diagonal.
+struct Turned {
+    bool left, right;
+};
+template <bool PAIR>
+__device__ __forceinline__ Turned turned_at(const Tile& at, int k) {
+    const int tile = k / Shape<PAIR>::kTile * Shape<PAIR>::kTile;
+    return Turned{at.step != kGram && tile < at.row,
+                  at.step == kApply || (at.step == kPoly && tile < at.col)};
+}
+// 128 rows' 64 k, hi and lo: one block, or, turned, 64 rows of k of two blocks (hi of
+// both, then lo of both).
+__device__ __forceinline__ void copy_rows(char* to, const void* image, int row, int k, int width,
+                                          bool turned, uint64_t* bar) {
+    if (!turned) {
+        bulk_load(to, block_at(image, row, k, width), kBlockBytes, bar);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        bulk_load(to + j * 8192,
+                  block_at(image, k, row + j % 2 * 64, width) + j / 2 * (kBlockBytes / 2) +
+                      k % 128 * 128,
+                  8192, bar);
+}
+
+// Waits until `count` warps' parts of a matrix's tiles are written.
+__device__ __forceinline__ bool tiles_wait(const unsigned int* counter, uint32_t count,
+                                           unsigned long long limit_ns) {
+    unsigned long long t0 = 0;
+    for (uint32_t k = 0;; ++k) {
+        unsigned int v;
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(counter) : "memory");
+        if (v >= count) return true;
+        if (k == 0) t0 = now_ns();
+        else if (now_ns() - t0 > limit_ns) return false;
+    }
 }
 
 // ------------------------------------------------------------------ results
 
-// 32 columns of a thread's row, as halves of s v, to an image.
-__device__ __forceinline__ void store_row(void* image, int row, int col, int width,
-                                          const float* v) {
-    char* block = block_at(image, row, col, width);
+// 32 columns of this lane's row, in place: each eight sums become, times scale and
+// with `diagonal` added to column `on`, four words of halves hi and four of lo; and
+// those become the same of what they stand for.
+__device__ __forceinline__ void split_sums(uint32_t* w, float scale, float diagonal, int on) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        uint4 hi, lo;
-        split_pair(v[8 * k], v[8 * k + 1], &hi.x, &lo.x);
-        split_pair(v[8 * k + 2], v[8 * k + 3], &hi.y, &lo.y);
-        split_pair(v[8 * k + 4], v[8 * k + 5], &hi.z, &lo.z);
-        split_pair(v[8 * k + 6], v[8 * k + 7], &hi.w, &lo.w);
-        char* p = block + swizzled(row % 128, col % 64 + 8 * k);
-        *reinterpret_cast<uint4*>(p) = hi;
-        *reinterpret_cast<uint4*>(p + kBlockBytes / 2) = lo;
+    for (int k = 0; k < 32; k += 8) {
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            f[j] = __uint_as_float(w[k + j]) * scale;
+            if (on == k + j) f[j] += diagonal;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) split_pair(f[2 * j], f[2 * j + 1], &w[k + j], &w[k + 4 + j]);
     }
 }
-// The same values to the mirrored place: lanes are consecutive columns there.
-__device__ __forceinline__ void store_mirrored(void* image, int row, int col, int width,
-                                               const float* v) {
-    char* block = block_at(image, col, row, width);
+__device__ __forceinline__ void split_again(uint32_t* w, float scale, float diagonal, int on) {
 #pragma unroll
-    for (int k = 0; k < 32; ++k) {
-        const Halves h = split(v[k]);
-        char* p = block + swizzled(col % 128 + k, row % 64);
-        *reinterpret_cast<uint16_t*>(p) = h.hi;
-        *reinterpret_cast<uint16_t*>(p + kBlockBytes / 2) = h.lo;
-    }
-}
-// s v of 32 columns of a row.
-__device__ __forceinline__ void load_row(const void* image, int row, int col, int width,
-                                         float* v) {
-    const char* block = block_at(image, row, col, width);
+    for (int k = 0; k < 32; k += 8) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const char* p = block + swizzled(row % 128, col % 64 + 8 * k);
-        float hi[8], lo[8];
-        unpack16<kGradF16>(*reinterpret_cast<const uint4*>(p), hi);
-        unpack16<kGradF16>(*reinterpret_cast<const uint4*>(p + kBlockBytes / 2), lo);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[8 * k + j] = hi[j] + lo[j];
+        for (int j = 0; j < 4; ++j) {
+            const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&w[k + j]));
+            const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&w[k + 4 + j]));
+            float a = (hi.x + lo.x) * scale, b = (hi.y + lo.y) * scale;
+            if (on == k + 2 * j) a += diagonal;
+            if (on == k + 2 * j + 1) b += diagonal;
+            split_pair(a, b, &w[k + j], &w[k + 4 + j]);
+        }
     }
 }
 
-// The last round's results: an output, or the step of the weights.
-__device__ __forceinline__ void finish(const MatrixItem& x, const MatrixCall& c, int row, int col,
-                                       const float* v) {
-    const MatrixGroup& g = c.group[x.group];
-    if (row >= x.m) return;
+// Those words to an image's block, `first` 16-byte pieces into its rows.  Through
+// shared memory, so that four lanes write 64 bytes of one row (each lane its own row
+// would be 32 lines an instruction, 4 us a step).
+__device__ __forceinline__ void store_words(char* block, int first, const uint32_t* w,
+                                            uint32_t piece) {
+    const int lane = threadIdx.x % 32;
 #pragma unroll
-    for (int k = 0; k < 32; ++k) {
+    for (int q = 0; q < 2; ++q) {                        // hi, lo
+        __syncwarp();                                    // what was there has left
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             piece + lane * 64 + (c ^ lane / 2 % 4) * 16),
+                         "r"(w[8 * c + 4 * q]), "r"(w[8 * c + 4 * q + 1]),
+                         "r"(w[8 * c + 4 * q + 2]), "r"(w[8 * c + 4 * q + 3])
+                         : "memory");
+        __syncwarp();
+        char* to = block + q * (kBlockBytes / 2) + lane / 4 * 128 +
+                   ((first + lane % 4) ^ lane / 4) * 16;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {                    // rows 8 i + lane / 4
+            uint4 v;
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                         : "r"(piece + (i * 8 + lane / 4) * 64 +
+                               (lane % 4 ^ lane / 8 % 4) * 16)
+                         : "memory");
+            *reinterpret_cast<uint4*>(to + i * 1024) = v;
+        }
+    }
+}
+
+// Eight columns of the last round's results: an output, or the step of the weights.
+__device__ __forceinline__ void finish(const MatrixItem& x, const MatrixCall& c, int row, int col,
+                                       const uint32_t* sum, float scale) {
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(sum[k]) * scale;
+    if (row >= x.m || col >= x.n) return;
+    const float decay = c.group[x.group].lr_wd;
+    if (!x.tall && x.whole) {        // rows of whole vectors
+        const int64_t at = static_cast<int64_t>(row) * x.n + col;
+        if (x.master != nullptr) {
+            float p[8];
+            load_elems<kGradF32, 8>(x.master + at, p);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                p[k] -= decay * p[k];
+                v[k] = p[k] - x.step * v[k];
+            }
+            store_elems<kGradF32, 8>(x.master + at, v);
+            if (x.out == nullptr) return;
+        }
+        if (c.out_type == kGradF32)
+            store_elems<kGradF32, 8>(static_cast<float*>(x.out) + at, v);
+        else if (c.out_type == kGradF16)
+            store_elems<kGradF16, 8>(static_cast<uint16_t*>(x.out) + at, v);
+        else
+            store_elems<kGradBF16, 8>(static_cast<uint16_t*>(x.out) + at, v);
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
         if (col + k >= x.n) continue;
         const int64_t at = x.tall ? static_cast<int64_t>(col + k) * x.m + row
                                   : static_cast<int64_t>(row) * x.n + col + k;
+        float r = v[k];
         if (x.master != nullptr) {
             float p = x.master[at];
-            p -= g.lr_wd * p;
-            p -= x.step * v[k];
-            x.master[at] = p;
+            p -= decay * p;
+            r = p - x.step * r;
+            x.master[at] = r;
             if (x.out == nullptr) continue;
-            if (c.out_type == kGradF16) static_cast<uint16_t*>(x.out)[at] = elem_from_f32<kGradF16>(p);
-            else static_cast<uint16_t*>(x.out)[at] = f32_to_bf16(p);
-        } else if (c.out_type == kGradF32) {
-            static_cast<float*>(x.out)[at] = v[k];
-        } else {
-            static_cast<uint16_t*>(x.out)[at] =
-                c.out_type == kGradF16 ? elem_from_f32<kGradF16>(v[k]) : f32_to_bf16(v[k]);
         }
+        if (c.out_type == kGradF32) static_cast<float*>(x.out)[at] = r;
+        else if (c.out_type == kGradF16)
+            static_cast<uint16_t*>(x.out)[at] = elem_from_f32<kGradF16>(r);
+        else static_cast<uint16_t*>(x.out)[at] = f32_to_bf16(r);
     }
 }
 
 // ----------------------------------------------------------------- products
 
-// One block per SM walks the tiles.  Warp 0 copies operands into a ring of
-// stages, warp 1 issues the products into one of two accumulators, warps 2 to 5
-// turn the other into results.  Every wait has a limit: past it the block sets
-// the status word, lets its copies and products in flight end, frees its tensor
-// memory and returns.
-template <Step STEP>
-__global__ void __launch_bounds__(kMatrixThreads, 1)
-    matrix_product(const __grid_constant__ MatrixTable t,
-                   const __grid_constant__ MatrixCall call, int from,
-                   unsigned long long limit_ns) {
+// All rounds in one launch: every SM's block (or pair of blocks) walks the tiles of
+// all steps in one fixed order.  A tile waits until its matrix has all tiles of the
+// step before, so matrices follow each other through the steps without a barrier
+// between them, and no step's last wave leaves SMs idle while another matrix has
+// work.  (The launch is cooperative: all blocks are resident, and a tile waits for
+// earlier ones only.)
+//
+// Warp 0 copies operands into a ring of stages, warp 1 issues the products into one
+// of two accumulators, the others turn the other into results.  In a pair, each
+// block copies its half of both operands; the first block's warp 1 issues the
+// products of both, and the second's passes on that its stages are full.  Every
+// wait has a limit: past it the block sets the status word, lets its copies and
+// products in flight end, frees its tensor memory and returns.
+template <bool PAIR>
+__global__ void __launch_bounds__(Shape<PAIR>::kThreads, 1)
+    matrix_rounds(const __grid_constant__ MatrixTable t, const __grid_constant__ MatrixCall call,
+                  unsigned long long limit_ns) {
+    using F = Shape<PAIR>;
+    constexpr int kTile = F::kTile;
     extern __shared__ char raw[];
     __shared__ Shared sh;
-    char* ring = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t{1023});
-    constexpr bool sym = STEP == Step::kGram || STEP == Step::kPoly;
+    char* ring =
+        reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t{1023});
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const uint32_t tiles = sym ? t.sym0[t.count] : t.full0[t.count];
+    const uint32_t rank = PAIR ? pair_rank() : 0;
+    const uint32_t unit = blockIdx.x / F::kBlocks, units = gridDim.x / F::kBlocks;
+    const uint32_t tiles = call.rounds * (2 * t.sym0[t.count] + t.full0[t.count]);
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&sh.full[s], 1);
             mbar_init(&sh.empty[s], 1);
+            mbar_init(&sh.peer[s], 1);
         }
         for (int k = 0; k < 2; ++k) {
             mbar_init(&sh.done[k], 1);
-            mbar_init(&sh.taken[k], 4);
+            mbar_init(&sh.taken[k], F::kResultWarps * F::kBlocks);
         }
         mbar_init(&sh.drain, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 1) tmem_alloc<kTmemColumns>(&sh.tmem);
+    if (warp == 1) tmem_alloc<PAIR, F::kTmemColumns>(&sh.tmem);
     tmem_fence_before();
-    __syncthreads();
+    if constexpr (PAIR) pair_sync();
+    else __syncthreads();
     tmem_fence_after();
     const uint32_t tmem = sh.tmem;
-    pdl_enter();
     const bool skip = skip_step(call.skip);
 
     if (!skip && warp == 0) {
         if (lane == 0) {
-            asm volatile("fence.proxy.async.global;" ::: "memory");
             uint32_t issued = 0;
             bool ok = true;
-            for (uint32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
-                const Tile at = tile_at<STEP>(t, i);
+            for (uint32_t i = unit; ok && i < tiles; i += units) {
+                const Tile at = tile_at<PAIR>(t, i);
                 const MatrixItem& x = t.item[at.matrix];
-                const void* left = STEP == Step::kGram   ? x.x[from]
-                                   : STEP == Step::kPoly ? x.gram
-                                                         : x.poly;
+                if (at.before > 0)
+                    ok = tiles_wait(x.tiles_done, at.before * F::kArrivals, limit_ns);
+                if (!ok) break;
+                asm volatile("fence.proxy.async.global;" ::: "memory");
+                const void* from = x.x[at.round & 1];
+                const void* left = at.step == kGram ? from : at.step == kPoly ? x.gram : x.poly;
+                const void* right = at.step == kPoly ? x.comb : from;
+                const int row = at.row + 128 * rank, col = at.col + 128 * rank;
                 for (int k = 0; k < at.k; k += 64, ++issued) {
                     const uint32_t s = issued % kStages;
                     if (issued >= kStages &&
@@ -249,19 +376,10 @@ __global__ void __launch_bounds__(kMatrixThreads, 1)
                     }
                     char* to = ring + s * kStageBytes;
                     mbar_expect_tx(&sh.full[s], kStageBytes);
-                    bulk_load(to, block_at(left, at.row, k, at.k), kBlockBytes, &sh.full[s]);
-                    to += kBlockBytes;
-                    if constexpr (sym) {
-                        bulk_load(to, block_at(left, at.col, k, at.k), kBlockBytes, &sh.full[s]);
-                    } else {
-                        // 64 rows of each of two blocks: hi of both, then lo of both
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            bulk_load(to + j * 8192,
-                                      block_at(x.x[from], k, at.col + j % 2 * 64, x.np) +
-                                          j / 2 * (kBlockBytes / 2) + k % 128 * 128,
-                                      8192, &sh.full[s]);
-                    }
+                    const Turned turned = turned_at<PAIR>(at, k);
+                    copy_rows(to, left, row, k, at.k, turned.left, &sh.full[s]);
+                    copy_rows(to + kBlockBytes, right, col, k, at.step == kApply ? x.np : at.k,
+                              turned.right, &sh.full[s]);
                 }
             }
             if (!ok) atomicOr(&g_matrix_status, kStatusProducerTimeout);
@@ -270,121 +388,190 @@ __global__ void __launch_bounds__(kMatrixThreads, 1)
                 if (!mbar_wait(&sh.full[j % kStages], (j / kStages) & 1, kDrainNs))
                     atomicOr(&g_matrix_status, kStatusDrainTimeout);
         }
-    } else if (!skip && warp == 1) {
+    } else if (!skip && warp == 1 && rank == 0) {
         if (lane == 0) {
-            constexpr uint32_t form = half_product(kTile, kTile, !sym);
             uint32_t used = 0, n = 0;                     // stages, pieces
             bool ok = true;
-            for (uint32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
-                const Tile at = tile_at<STEP>(t, i);
+            for (uint32_t i = unit; ok && i < tiles; i += units) {
+                const Tile at = tile_at<PAIR>(t, i);
                 for (int k0 = 0; ok && k0 < at.k; k0 += kPiece, ++n) {
                     const uint32_t d = tmem + n % 2 * kTile;
-                    if (n >= 2 && !mbar_wait(&sh.taken[n % 2], (n / 2 - 1) & 1, limit_ns)) {
-                        ok = false;
-                        break;
+                    if (n >= 2) {
+                        ok = PAIR ? mbar_wait_pair(&sh.taken[n % 2], (n / 2 - 1) & 1, limit_ns)
+                                  : mbar_wait(&sh.taken[n % 2], (n / 2 - 1) & 1, limit_ns);
+                        if (!ok) break;
                     }
                     tmem_fence_after();
                     const int end = at.k - k0 < kPiece ? at.k : k0 + kPiece;
                     for (int k = k0; k < end; k += 64, ++used) {
                         const uint32_t s = used % kStages;
-                        if (!mbar_wait(&sh.full[s], (used / kStages) & 1, limit_ns)) {
-                            ok = false;
-                            break;
-                        }
+                        ok = mbar_wait(&sh.full[s], (used / kStages) & 1, limit_ns);
+                        if (PAIR && ok)
+                            ok = mbar_wait_pair(&sh.peer[s], (used / kStages) & 1, limit_ns);
+                        if (!ok) break;
                         tmem_fence_after();
                         const uint32_t a = smem_addr(ring + s * kStageBytes);
                         const uint32_t b = a + kBlockBytes;
+                        const Turned turned = turned_at<PAIR>(at, k);
+                        const uint32_t form =
+                            half_product(kTile, kTile, turned.left, turned.right);
+                        // 16 k are 32 bytes along the rows, or 16 rows of 128 bytes
+                        uint64_t ah = turned.left ? mn_major(a, 8192) : k_major(a);
+                        uint64_t bh = turned.right ? mn_major(b, 8192) : k_major(b);
+                        const uint64_t next_a = turned.left ? 2048 / 16 : 32 / 16;
+                        const uint64_t next_b = turned.right ? 2048 / 16 : 32 / 16;
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {      // 16 of k each
-                            const uint64_t ah = k_major(a + q * 32);
-                            const uint64_t al = k_major(a + kBlockBytes / 2 + q * 32);
-                            const uint64_t bh =
-                                sym ? k_major(b + q * 32) : mn_major(b + q * 2048, 8192);
-                            const uint64_t bl =
-                                sym ? k_major(b + kBlockBytes / 2 + q * 32)
-                                    : mn_major(b + kBlockBytes / 2 + q * 2048, 8192);
-                            mma_half(d, ah, bh, form, k > k0 || q > 0);
-                            mma_half(d, ah, bl, form, true);
-                            mma_half(d, al, bh, form, true);
+                        for (int q = 0; q < 4; ++q, ah += next_a, bh += next_b) {
+                            const uint64_t al = ah + kBlockBytes / 2 / 16;
+                            const uint64_t bl = bh + kBlockBytes / 2 / 16;
+                            mma_half<PAIR>(d, ah, bh, form, k > k0 || q > 0);
+                            mma_half<PAIR>(d, ah, bl, form, true);
+                            mma_half<PAIR>(d, al, bh, form, true);
                         }
-                        mma_commit(&sh.empty[s]);
+                        mma_commit<PAIR>(&sh.empty[s]);
                     }
-                    if (ok) mma_commit(&sh.done[n % 2]);
+                    if (ok) mma_commit<PAIR>(&sh.done[n % 2]);
                 }
             }
             if (!ok) atomicOr(&g_matrix_status, kStatusConsumerTimeout);
-            mma_commit(&sh.drain);          // the products in flight end before their memory goes
+            mma_commit<PAIR>(&sh.drain);    // the products in flight end before their memory goes
             if (!mbar_wait(&sh.drain, 0, kDrainNs))
                 atomicOr(&g_matrix_status, kStatusDrainTimeout);
         }
+    } else if (!skip && warp == 1) {
+        if (lane == 0) {
+            uint32_t used = 0;
+            bool ok = true;
+            for (uint32_t i = unit; ok && i < tiles; i += units) {
+                const Tile at = tile_at<PAIR>(t, i);
+                for (int k = 0; k < at.k; k += 64, ++used) {
+                    const uint32_t s = used % kStages;
+                    ok = mbar_wait(&sh.full[s], (used / kStages) & 1, limit_ns);
+                    if (!ok) break;
+                    arrive_at_first(&sh.peer[s]);
+                }
+            }
+            if (!ok) atomicOr(&g_matrix_status, kStatusConsumerTimeout);
+            // the products that the first block has in flight read this block's stages
+            if (!mbar_wait(&sh.drain, 0, 2 * kDrainNs + 2 * limit_ns))
+                atomicOr(&g_matrix_status, kStatusDrainTimeout);
+        }
     } else if (!skip) {
-        const int quarter = warp % 4;                    // the lanes this warp may read
+        volatile Work& my = sh.work[warp - 2];
+        if (lane == 0) {
+            // the quarter of the lanes that this warp may read, and its columns
+            my.lanes = tmem + (static_cast<uint32_t>(warp % 4 * 32) << 16) +
+                       (warp - 2) / 4 * F::kColumns;
+            my.out = smem_addr(ring) + kStages * kStageBytes + (warp - 2) * kOutPiece;
+            my.down = 128 * rank + warp % 4 * 32;
+            my.across = (warp - 2) / 4 * F::kColumns;
+            my.index = unit;
+            my.step = units;
+            my.end = tiles;
+        }
+        __syncwarp();
         uint32_t n = 0;
-        bool ok = true;
-        for (uint32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
-            const Tile at = tile_at<STEP>(t, i);
-            const MatrixItem& x = t.item[at.matrix];
-            float sum[kTile / 32][32] = {};
+        for (;;) {
+            const bool more = my.index < my.end;
+            __syncwarp();                                // all have read what lane 0 moves on
+            if (!more) break;
+            if (lane == 0) {
+                const Tile next = tile_at<PAIR>(t, my.index);
+                my.tile.matrix = next.matrix;
+                my.tile.round = next.round;
+                my.tile.step = next.step;
+                my.tile.row = next.row + my.down;        // this warp's
+                my.tile.col = next.col + my.across;
+                my.tile.k = next.k;
+                my.index += my.step;
+            }
+            __syncwarp();
+            volatile Tile& at = my.tile;
+            bool ok = true;
+            uint32_t sum[F::kColumns];                   // fp32, then halves
+#pragma unroll
+            for (int k = 0; k < F::kColumns; ++k) sum[k] = 0u;
             for (int k0 = 0; k0 < at.k; k0 += kPiece, ++n) {
                 // every lane waits, so that all of them see the products
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sh.done[n % 2], (n / 2) & 1, limit_ns));
                 if (!ok) break;
                 tmem_fence_after();
 #pragma unroll
-                for (int c = 0; c < kTile / 32; ++c) {
-                    uint32_t acc[32];
-                    tmem_load32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
-                                    n % 2 * kTile + c * 32,
-                                acc);
+                for (int c = 0; c < F::kColumns; c += 8) {
+                    uint32_t acc[8];
+                    tmem_load8(my.lanes + n % 2 * kTile + c, acc);
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) sum[c][k] += __uint_as_float(acc[k]);
+                    for (int k = 0; k < 8; ++k)
+                        sum[c + k] = __float_as_uint(__uint_as_float(sum[c + k]) +
+                                                     __uint_as_float(acc[k]));
                 }
                 tmem_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.taken[n % 2]);   // the next products may come
+                if (lane == 0) {                         // the next products may come
+                    if constexpr (PAIR) arrive_at_first(&sh.taken[n % 2]);
+                    else mbar_arrive(&sh.taken[n % 2]);
+                }
             }
+            const MatrixItem& x = t.item[at.matrix];
             if (!ok) {
                 atomicOr(&g_matrix_status, kStatusConsumerTimeout);
                 break;
             }
-            const int row = at.row + quarter * 32 + lane;
+            // result = scale product, and `diagonal` on it
+            float scale = 1.0f / kScaleX, diagonal = 0.0f;
+            if (at.step == kPoly) {
+                scale = kScaleP / kScaleX / kScaleC;
+                diagonal = call.a * kScaleP;
+            } else if (at.step == kApply) {
+                scale = 1.0f / kScaleP;
+                if (at.round + 1 == call.rounds) {
+                    scale *= 1.0f / kScaleX;
 #pragma unroll
-            for (int c = 0; c < kTile / 32; ++c) {
-                float* v = sum[c];
-                const int col = at.col + c * 32;
-                if constexpr (STEP == Step::kGram) {
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) v[k] *= 1.0f / kScaleX;
-                    store_row(x.gram, row, col, x.mp, v);
-                    if (at.row != at.col) store_mirrored(x.gram, row, col, x.mp, v);
-                } else if constexpr (STEP == Step::kPoly) {
-                    float g[32];
-                    load_row(x.gram, row, col, x.mp, g);
-                    const float b = call.b * (kScaleB / kScaleX);
-                    const float c2 = call.c * (kScaleB / kScaleX / kScaleX);
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) v[k] = fmaf(c2, v[k], b * g[k]);
-                    store_row(x.poly, row, col, x.mp, v);
-                    if (at.row != at.col) store_mirrored(x.poly, row, col, x.mp, v);
-                } else {
-                    float y[32];
-                    load_row(x.x[from], row, col, x.np, y);
-                    constexpr float out = STEP == Step::kLast ? 1.0f / kScaleX : 1.0f;
-                    const float a = call.a * out, p = out / kScaleB;
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) v[k] = fmaf(p, v[k], a * y[k]);
-                    if constexpr (STEP == Step::kLast) finish(x, call, row, col, v);
-                    else store_row(x.x[from ^ 1], row, col, x.np, v);
+                    for (int c = 0; c < F::kColumns; c += 8)
+                        finish(x, call, at.row + lane, at.col + c, sum + c, scale);
+                    __syncwarp();
+                    continue;
                 }
             }
+            // 32 columns at a time: of X X^T, then of b + c X X^T
+            const int images = at.step == kGram ? 2 : 1;
+#pragma unroll
+            for (int c = 0; c < F::kColumns; c += 32) {
+#pragma unroll 1                                             // twice its code takes more registers
+                for (int image = 0; image < images; ++image) {
+                    int row = threadIdx.x % 32;
+                    asm volatile("" : "+r"(row));            // formed here, not kept
+                    const int on = at.row + row - at.col - c;   // the column on the diagonal
+                    if (image == 0)
+                        split_sums(sum + c, scale, diagonal, on);
+                    else
+                        split_again(sum + c, call.c * (kScaleC / kScaleX), call.b * kScaleC, on);
+                    void* to = at.step == kApply  ? x.x[(at.round & 1) ^ 1]
+                               : at.step == kPoly ? x.poly
+                               : image == 0       ? x.gram
+                                                  : x.comb;
+                    store_words(block_at(to, at.row, at.col + c,
+                                         at.step == kApply ? x.np : x.mp) +
+                                    at.row % 128 * 128,
+                                c % 64 / 8, sum + c, my.out);
+                }
+            }
+            // written, for copies as for loads; then another warp of the matrix is done
+            asm volatile("fence.proxy.async.global;" ::: "memory");
+            __threadfence();
+            __syncwarp();
+            if (lane == 0)
+                asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(x.tiles_done)
+                             : "memory");
         }
     }
     tmem_fence_before();
-    __syncthreads();
+    __syncwarp();
+    if constexpr (PAIR) pair_sync();
+    else __syncthreads();
     if (warp == 1) {
-        __syncwarp();
         tmem_fence_after();
-        tmem_free<kTmemColumns>(tmem);
+        tmem_free<PAIR, F::kTmemColumns>(tmem);
     }
 }
 
@@ -410,6 +597,7 @@ __global__ void __launch_bounds__(256) matrix_moments(const __grid_constant__ Ma
     const MatrixItem& x = t.item[k];
     const MatrixGroup& g = call.group[x.group];
     const int part = blockIdx.x - t.part0[k], parts = t.part0[k + 1] - t.part0[k];
+    if (part == 0 && threadIdx.x == 0) *x.tiles_done = 0;
     const float coef = call.coef != nullptr ? __ldg(call.coef) : 1.0f;
     const int64_t n = static_cast<int64_t>(x.m) * x.n;
     const S* grad = static_cast<const S*>(x.grad);
@@ -489,17 +677,57 @@ __global__ void __launch_bounds__(256) matrix_image(const __grid_constant__ Matr
     }
 }
 
-template <Step STEP>
-cudaError_t go_product(const MatrixTable& t, const MatrixCall& c, int from, cudaStream_t stream) {
-    constexpr bool sym = STEP == Step::kGram || STEP == Step::kPoly;
-    const uint32_t tiles = sym ? t.sym0[t.count] : t.full0[t.count];
-    const uint32_t sms = static_cast<uint32_t>(device_sms());
-    constexpr int smem = kStages * kStageBytes + 1024;
-    cudaError_t e = cudaFuncSetAttribute(matrix_product<STEP>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    e = launch_after(matrix_product<STEP>, dim3(tiles < sms ? tiles : sms), dim3(kMatrixThreads),
-                     smem, stream, t, c, from, tma_wait_limit());
+// Blocks of the rounds' kernel that can be resident at once, by device.
+template <bool PAIR>
+int resident_units() {
+    static std::atomic<int> cache[256];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 256) return 0;
+    int v = cache[dev].load(std::memory_order_relaxed);
+    if (v > 0) return v;
+    if (cudaFuncSetAttribute(matrix_rounds<PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Shape<PAIR>::kDynamicBytes) != cudaSuccess)
+        return 0;
+    v = device_sms();
+    if constexpr (PAIR) {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim = {2, 1, 1};
+        cfg.gridDim = dim3(static_cast<unsigned>(v / 2 * 2));
+        cfg.blockDim = dim3(Shape<PAIR>::kThreads);
+        cfg.dynamicSmemBytes = Shape<PAIR>::kDynamicBytes;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int clusters = 0;
+        if (cudaOccupancyMaxActiveClusters(&clusters, matrix_rounds<PAIR>, &cfg) != cudaSuccess)
+            return 0;
+        v = clusters < v / 2 ? clusters : v / 2;
+    }
+    if (v > 0) cache[dev].store(v, std::memory_order_relaxed);
+    return v;
+}
+
+template <bool PAIR>
+cudaError_t go_rounds(const MatrixTable& t, const MatrixCall& c, cudaStream_t stream) {
+    const uint32_t sym = t.sym0[t.count], full = t.full0[t.count];
+    const uint32_t most = sym > full ? sym : full;
+    const int fit = resident_units<PAIR>();
+    if (fit < 1) return cudaErrorLaunchOutOfResources;
+    const uint32_t units = most < static_cast<uint32_t>(fit) ? most : static_cast<uint32_t>(fit);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {2, 1, 1};
+    cfg.gridDim = dim3(units * Shape<PAIR>::kBlocks);
+    cfg.blockDim = dim3(Shape<PAIR>::kThreads);
+    cfg.dynamicSmemBytes = Shape<PAIR>::kDynamicBytes;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = PAIR ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, matrix_rounds<PAIR>, t, c, tma_wait_limit());
     note_launch();
     return e;
 }
@@ -526,14 +754,8 @@ cudaError_t launch_matrices(const MatrixTable& t, const MatrixCall& c, int grad_
         note_launch();
         return second;
     });
-    for (int k = 0; e == cudaSuccess && k < c.rounds; ++k) {
-        e = go_product<Step::kGram>(t, c, k & 1, stream);
-        if (e == cudaSuccess) e = go_product<Step::kPoly>(t, c, k & 1, stream);
-        if (e != cudaSuccess) return e;
-        e = k + 1 < c.rounds ? go_product<Step::kApply>(t, c, k & 1, stream)
-                             : go_product<Step::kLast>(t, c, k & 1, stream);
-    }
-    return e;
+    if (e != cudaSuccess) return e;
+    return t.pair ? go_rounds<true>(t, c, stream) : go_rounds<false>(t, c, stream);
 }
 
 }  // namespace shardstep

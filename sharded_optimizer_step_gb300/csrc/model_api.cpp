@@ -63,11 +63,13 @@ int64_t round16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
 constexpr int64_t kSideMax = int64_t{1} << 20;
 constexpr int64_t kGroupBytes = int64_t{2} << 30;
 
-int64_t padded(int64_t n) { return (n + 127) / 128 * 128; }
-// A matrix's part of the workspace: two images of X, those of A and B, the sums.
+int64_t padded(int64_t n, int64_t tile) { return (n + tile - 1) / tile * tile; }
+constexpr int64_t kMatrixWords = kMatrixParts * sizeof(double) + 128;   // sums and a counter
+// A matrix's part of the workspace: two images of X, three of its products, the words
+// (with either tile).
 int64_t matrix_bytes(int64_t rows, int64_t cols) {
-    const int64_t m = padded(std::min(rows, cols)), n = padded(std::max(rows, cols));
-    return 8 * m * n + 8 * m * m + kMatrixParts * static_cast<int64_t>(sizeof(double));
+    const int64_t m = padded(std::min(rows, cols), 256), n = padded(std::max(rows, cols), 256);
+    return 8 * m * n + 12 * m * m + kMatrixWords;
 }
 bool side_ok(int64_t n) { return n >= 0 && n <= kSideMax; }
 
@@ -117,10 +119,10 @@ double quintic_most(double a, double b, double c, double hi) {
     }
     return most;
 }
-// The largest magnitude of b t + c t^2 over [0, hi].
-double square_most(double b, double c, double hi) {
-    const auto f = [&](double t) { return std::fabs(t * (b + t * c)); };
-    double most = f(hi);
+// The largest magnitude of a + b t + c t^2 over [0, hi].
+double square_most(double a, double b, double c, double hi) {
+    const auto f = [&](double t) { return std::fabs(a + t * (b + t * c)); };
+    double most = std::max(f(0.0), f(hi));
     if (c != 0 && -b / (2 * c) > 0 && -b / (2 * c) < hi) most = std::max(most, f(-b / (2 * c)));
     return most;
 }
@@ -134,8 +136,10 @@ int take_quintic(const shardstep_quintic_t* q, MatrixCall* call) {
         return ready_fail(SHARDSTEP_ERR_INVALID, "a coefficient or eps is out of range");
     double hi = 1.0;
     for (int32_t k = 0; k < q->rounds; ++k) {
-        // X and A are held times 2^15 and B times 2^14 in halves, which end at 65504
-        if (!(hi <= 1.39) || !(square_most(q->b, q->c, hi * hi) <= 3.9))
+        // X and A are held times 2^15 in halves, which end at 65504, b + c A times 2^13
+        // and a + b A + c A A times 2^14
+        if (!(hi <= 1.39) || !(square_most(q->b, q->c, 0.0, hi * hi) <= 7.9) ||
+            !(square_most(q->a, q->b, q->c, hi * hi) <= 3.9))
             return ready_fail(SHARDSTEP_ERR_INVALID,
                               "the coefficients let values grow past what round %d holds", k + 1);
         hi = std::max(hi, quintic_most(q->a, q->b, q->c, hi));
@@ -148,55 +152,85 @@ int take_quintic(const shardstep_quintic_t* q, MatrixCall* call) {
     return SHARDSTEP_OK;
 }
 
-// The matrices [at, end) of the list as one group's table; false: all empty.
+// The matrices [at, end) of the list; false: all are empty.
 template <typename F>
-bool fill_table(const F& item, int32_t at, int32_t end, char* ws, MatrixTable* t) {
-    int k = 0;
+bool take_group(const F& item, int32_t at, int32_t end, MatrixTable* t) {
+    t->count = 0;
     for (; at < end; ++at) {
         MatrixItem x{};
         int64_t rows, cols;
         item(at, &x, &rows, &cols);
         if (rows == 0 || cols == 0) continue;
         x.tall = rows > cols;
+        x.whole = std::max(rows, cols) % 8 == 0 && aligned(x.master, 16) && aligned(x.out, 16);
         x.m = static_cast<int32_t>(std::min(rows, cols));
         x.n = static_cast<int32_t>(std::max(rows, cols));
-        x.mp = static_cast<int32_t>(padded(x.m));
-        x.np = static_cast<int32_t>(padded(x.n));
+        t->item[t->count++] = x;
+    }
+    return t->count > 0;
+}
+
+// About how long a round takes with either tile, in units of 64 k of a 128 x 128 tile
+// (0.49 us; a 256 x 256 tile takes a pair 0.79 us: it copies half as much per product).
+// The larger tile is the faster one where there are enough of them for all pairs: 12
+// matrices of 1024 x 1024 take 671 us with it and 770 with the smaller one, one of
+// them 376 and 264.
+double round_cost(const MatrixTable& t, int64_t tile, int units) {
+    double total = 0.0;
+    for (int step = 0; step < 3; ++step) {
+        double work = 0.0, longest = 0.0;
+        for (int j = 0; j < t.count; ++j) {
+            const double side = static_cast<double>(padded(t.item[j].m, tile) / tile);
+            const double wide = static_cast<double>(padded(t.item[j].n, tile) / tile);
+            const double k = (step == 0 ? wide : side) * static_cast<double>(tile / 64);
+            work += k * (step == 2 ? side * wide : side * (side + 1) / 2);
+            longest = std::max(longest, k);
+        }
+        work /= units;
+        total += work < longest ? longest : work + longest / 3;
+    }
+    return tile == 256 ? total * 1.6 : total;
+}
+
+// Tiles, workspace and the launches' bounds.
+void lay_out(MatrixTable* t, char* ws) {
+    const int sms = device_sms();
+    t->pair = round_cost(*t, 256, sms / 2) < round_cost(*t, 128, sms);
+    const int64_t tile = t->pair ? 256 : 128;
+    // the longest tiles first, so that the last ones to end are short
+    std::sort(t->item, t->item + t->count, [](const MatrixItem& a, const MatrixItem& b) {
+        return a.m != b.m ? a.m > b.m : a.n > b.n;
+    });
+    uint32_t sym = 0, full = 0, part = 0, image = 0;
+    for (int j = 0; j < t->count; ++j) {
+        MatrixItem& x = t->item[j];
+        x.mp = static_cast<int32_t>(padded(x.m, tile));
+        x.np = static_cast<int32_t>(padded(x.n, tile));
         const int64_t wide = 4 * static_cast<int64_t>(x.mp) * x.np;
         const int64_t square = 4 * static_cast<int64_t>(x.mp) * x.mp;
         x.x[0] = ws;
         x.x[1] = ws + wide;
         x.gram = ws + 2 * wide;
-        x.poly = ws + 2 * wide + square;
-        x.part = reinterpret_cast<double*>(ws + 2 * wide + 2 * square);
-        ws += matrix_bytes(rows, cols);
-        t->item[k++] = x;
-    }
-    t->count = k;
-    if (k == 0) return false;
-    // the longest tiles first, so that the last ones to end are short
-    std::sort(t->item, t->item + k, [](const MatrixItem& a, const MatrixItem& b) {
-        return a.mp != b.mp ? a.mp > b.mp : a.np > b.np;
-    });
-    uint32_t sym = 0, full = 0, part = 0, image = 0;
-    for (int j = 0; j < k; ++j) {
-        const MatrixItem& x = t->item[j];
+        x.comb = ws + 2 * wide + square;
+        x.poly = ws + 2 * wide + 2 * square;
+        x.part = reinterpret_cast<double*>(ws + 2 * wide + 3 * square);
+        x.tiles_done = reinterpret_cast<unsigned int*>(x.part + kMatrixParts);
+        ws += matrix_bytes(x.m, x.n);
         t->sym0[j] = sym;
         t->full0[j] = full;
         t->part0[j] = part;
         t->image0[j] = image;
-        const uint32_t side = x.mp / 128;
+        const uint32_t side = static_cast<uint32_t>(x.mp / tile);
         sym += side * (side + 1) / 2;
-        full += side * (x.np / 128);
+        full += side * static_cast<uint32_t>(x.np / tile);
         part += static_cast<uint32_t>(std::min<int64_t>(
             kMatrixParts, (static_cast<int64_t>(x.m) * x.n + 4095) / 4096));
-        image += side * (x.np / 64);
+        image += static_cast<uint32_t>(x.mp / 128) * (x.np / 64);
     }
-    t->sym0[k] = sym;
-    t->full0[k] = full;
-    t->part0[k] = part;
-    t->image0[k] = image;
-    return true;
+    t->sym0[t->count] = sym;
+    t->full0[t->count] = full;
+    t->part0[t->count] = part;
+    t->image0[t->count] = image;
 }
 
 template <typename S, typename F>
@@ -206,7 +240,8 @@ int run_groups(const S& sides, const F& item, int32_t n, const MatrixCall& call,
     for (int32_t at = 0; at < n;) {
         int64_t bytes;
         const int32_t end = group_end(sides, n, at, &bytes);
-        if (fill_table(item, at, end, static_cast<char*>(workspace), t.get())) {
+        if (take_group(item, at, end, t.get())) {
+            lay_out(t.get(), static_cast<char*>(workspace));
             const cudaError_t e = launch_matrices(*t, call, grad_dtype, stream);
             if (e != cudaSuccess) return cuda_fail(what, e);
         }

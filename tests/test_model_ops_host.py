@@ -133,7 +133,8 @@ OUT_OF_RANGE = [
     _capi.Quintic(*ss.QUINTIC, -1.0, 5, 0), _capi.Quintic(*ss.QUINTIC, NAN, 5, 0),
     _capi.Quintic(NAN, -1.0, 1.0, 1e-7, 5, 0), _capi.Quintic(1.5, INF, 0.0, 1e-7, 5, 0),
     _capi.Quintic(4.0, -1.0, 0.0, 1e-7, 5, 0),       # grows past what halves hold
-    _capi.Quintic(1.0, -5.0, 0.0, 1e-7, 1, 0),       # b s^2 does
+    _capi.Quintic(1.0, -8.0, 7.0, 1e-7, 1, 0),       # b does
+    _capi.Quintic(1.0, 1.0, 2.0, 1e-7, 1, 0),        # a + b + c does
     _capi.Quintic(1.39, 0.0, 0.0, 1e-7, 3, 0),       # in its second round
 ]
 
@@ -165,7 +166,8 @@ def test_matrices_workspace():
     assert need([-1], [3]) == need([3], [(1 << 20) + 1]) == -1 and need([], []) == 0
     assert need([0, 7], [9, 0]) == 0
     one = need([1], [1])
-    assert one == 16 * 128 * 128 + 2048 and need([128], [100]) == need([100], [128]) == one
+    assert one == 20 * 256 * 256 + 2176 and need([128], [100]) == need([100], [128]) == one
+    assert need([600], [700]) == 20 * 768 * 768 + 2176
     assert need([200] * 3, [300] * 3) == 3 * need([200], [300])
     assert need([5] * 200, [5] * 200) == 64 * one          # a group at a time
     assert need([8192] * 9, [8192] * 9) == need([8192], [8192])
