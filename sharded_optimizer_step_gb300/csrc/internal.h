@@ -483,21 +483,22 @@ cudaError_t launch_layer_norm_grad(const NormGradRows& a, int type, int w_type, 
 
 constexpr int kMatrices = 64;        // of one group: a launch's table
 constexpr int kMatrixParts = 256;    // sums of squares of one matrix
+// The images of a matrix in the workspace: X twice, then symmetric ones of its short
+// side: A = X X^T, C = b + c A, P = a + A C twice, A P, and the product of the P.
+enum MatrixImage { kX0, kX1, kA, kC, kP0, kP1, kZ, kQ, kImages };
 struct MatrixItem {
     const void* grad;                // m x n, or n x m where tall
     float* master;                   // null: `out` takes the orthogonal matrix
     float* m_buf;                    // momentum, or null
     void* out;                       // the parameter (may be null), or the result
-    void* x[2];                      // images in the workspace
-    void* gram;                      // X X^T
-    void* comb;                      // b + c X X^T
-    void* poly;                      // a + gram comb
+    void* image[kImages];
     double* part;
     unsigned int* tiles_done;        // result warps of all steps so far
     float step;                      // learning rate times the matrix's factor
     int32_t m, n, mp, np;            // m <= n, and padded to the tile
     int16_t tall, group;
     int32_t whole;                   // master and out take whole vectors of 8 along rows
+    int32_t flat;                    // grad and m_buf take whole vectors of 8
 };
 struct MatrixTable {
     MatrixItem item[kMatrices];
@@ -512,12 +513,32 @@ struct MatrixGroup {
     float lr_wd, mu, one_mu;
     int nesterov;
 };
+// One product of the rounds, of all matrices: out = scale left right + diagonal.
+enum MatrixStepFlags {
+    kSymmetric = 1,       // its tiles on and above the diagonal only
+    kLeftX = 2,           // rows of X on the left
+    kRightX = 4,          // X behind a symmetric matrix
+    kWithC = 8,           // write C beside A
+    kLastStep = 16,       // the result itself
+};
+struct MatrixStep {
+    uint32_t first;                  // tile of the call
+    float scale, diagonal;           // of the values as the images hold them
+    uint16_t sym_before, full_before;   // steps that have to be done, of either kind
+    uint8_t left, right, out, flags;
+};
+constexpr int kMatrixSteps = 256;
+constexpr float kImageScaleX = 32768.0f;   // what X's images hold X times
 struct MatrixCall {
     MatrixGroup group[kMaxGroups];
     const float* coef;
     const unsigned int* skip;
     float a, b, c, eps;
     int rounds, out_type;
+    float c_scale, c_diagonal;       // C from A, as the images hold them
+    uint32_t tiles, most;            // of all steps, of one level of them
+    int steps;
+    MatrixStep step[kMatrixSteps];
 };
 cudaError_t launch_matrices(const MatrixTable& t, const MatrixCall& c, int grad_type,
                             cudaStream_t stream);

@@ -43,8 +43,6 @@ constexpr int kOutPiece = 2048;
 // bit.  A sum over k therefore goes in pieces of this many, which the result warps
 // add up in their registers (rounding to nearest).
 constexpr int kPiece = 256;
-constexpr float kScaleX = 32768.0f, kScaleC = 8192.0f, kScaleP = 16384.0f;
-
 // A tile of results: 128 x 128 by one block, or 256 x 256 by a pair.  Each block
 // has 128 rows of it, and eight result warps, two for each quarter of the rows.
 template <bool PAIR>
@@ -61,11 +59,8 @@ struct Shape {
         kStages * kStageBytes + kResultWarps * kOutPiece + 1024;
 };
 
-enum Step { kGram, kPoly, kApply };
-
 struct Tile {
-    int matrix, round;
-    Step step;
+    int matrix, step;
     int row, col;            // of the result, in elements
     int k;                   // length of the sum
     uint32_t before;         // tiles of the matrix that have to be done
@@ -119,22 +114,28 @@ __device__ __forceinline__ int find(const uint32_t* first, int count, uint32_t t
     return lo;
 }
 
-// Tile `index` of the call: round by round, step by step, matrix by matrix.
+// Tile `index` of the call: step by step, matrix by matrix.
 template <bool PAIR>
-__device__ __forceinline__ Tile tile_at(const MatrixTable& t, uint32_t index) {
+__device__ __forceinline__ Tile tile_at(const MatrixTable& t, const MatrixCall& call,
+                                        uint32_t index) {
     constexpr int kTile = Shape<PAIR>::kTile;
-    const uint32_t sym = t.sym0[t.count], full = t.full0[t.count];
     Tile out;
-    out.round = static_cast<int>(index / (2 * sym + full));
-    index -= out.round * (2 * sym + full);
-    out.step = index < sym ? kGram : index < 2 * sym ? kPoly : kApply;
-    index -= out.step * sym;
-    const uint32_t* first = out.step == kApply ? t.full0 : t.sym0;
+    int lo = 0, hi = call.steps - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (call.step[mid].first <= index) lo = mid;
+        else hi = mid - 1;
+    }
+    out.step = lo;
+    const MatrixStep& step = call.step[lo];
+    index -= step.first;
+    const bool sym = step.flags & kSymmetric;
+    const uint32_t* first = sym ? t.sym0 : t.full0;
     out.matrix = find(first, t.count, index);
     const MatrixItem& x = t.item[out.matrix];
     int i = static_cast<int>(index - first[out.matrix]);
-    const int side = x.mp / kTile, all = x.np / kTile, half = side * (side + 1) / 2;
-    if (out.step != kApply) {
+    const int side = x.mp / kTile, all = x.np / kTile;
+    if (sym) {
         int r = 0;
         while (i >= side - r) i -= side - r++;
         out.row = r * kTile;
@@ -143,21 +144,21 @@ __device__ __forceinline__ Tile tile_at(const MatrixTable& t, uint32_t index) {
         out.row = i % side * kTile;
         out.col = i / side * kTile;
     }
-    out.k = out.step == kGram ? x.np : x.mp;
-    out.before = out.round * (2 * half + side * all) + out.step * half;
+    out.k = step.flags & kLeftX ? x.np : x.mp;
+    out.before = step.sym_before * (side * (side + 1) / 2) + step.full_before * (side * all);
     return out;
 }
 
 // Which operands' 64 k from k on come from blocks that hold k along their rows: X
-// behind P, and of a symmetric matrix what lies below the diagonal.
+// behind a symmetric matrix, and of a symmetric matrix what lies below the diagonal.
 struct Turned {
     bool left, right;
 };
 template <bool PAIR>
-__device__ __forceinline__ Turned turned_at(const Tile& at, int k) {
+__device__ __forceinline__ Turned turned_at(const Tile& at, int flags, int k) {
     const int tile = k / Shape<PAIR>::kTile * Shape<PAIR>::kTile;
-    return Turned{at.step != kGram && tile < at.row,
-                  at.step == kApply || (at.step == kPoly && tile < at.col)};
+    return Turned{!(flags & kLeftX) && tile < at.row,
+                  (flags & kRightX) || (!(flags & kLeftX) && tile < at.col)};
 }
 // 128 rows' 64 k, hi and lo: one block, or, turned, 64 rows of k of two blocks (hi of
 // both, then lo of both).
@@ -330,7 +331,7 @@ __global__ void __launch_bounds__(Shape<PAIR>::kThreads, 1)
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = PAIR ? pair_rank() : 0;
     const uint32_t unit = blockIdx.x / F::kBlocks, units = gridDim.x / F::kBlocks;
-    const uint32_t tiles = call.rounds * (2 * t.sym0[t.count] + t.full0[t.count]);
+    const uint32_t tiles = call.tiles;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&sh.full[s], 1);
@@ -357,15 +358,15 @@ __global__ void __launch_bounds__(Shape<PAIR>::kThreads, 1)
             uint32_t issued = 0;
             bool ok = true;
             for (uint32_t i = unit; ok && i < tiles; i += units) {
-                const Tile at = tile_at<PAIR>(t, i);
+                const Tile at = tile_at<PAIR>(t, call, i);
                 const MatrixItem& x = t.item[at.matrix];
                 if (at.before > 0)
                     ok = tiles_wait(x.tiles_done, at.before * F::kArrivals, limit_ns);
                 if (!ok) break;
                 asm volatile("fence.proxy.async.global;" ::: "memory");
-                const void* from = x.x[at.round & 1];
-                const void* left = at.step == kGram ? from : at.step == kPoly ? x.gram : x.poly;
-                const void* right = at.step == kPoly ? x.comb : from;
+                const MatrixStep& step = call.step[at.step];
+                const void* left = x.image[step.left];
+                const void* right = x.image[step.right];
                 const int row = at.row + 128 * rank, col = at.col + 128 * rank;
                 for (int k = 0; k < at.k; k += 64, ++issued) {
                     const uint32_t s = issued % kStages;
@@ -376,10 +377,10 @@ __global__ void __launch_bounds__(Shape<PAIR>::kThreads, 1)
                     }
                     char* to = ring + s * kStageBytes;
                     mbar_expect_tx(&sh.full[s], kStageBytes);
-                    const Turned turned = turned_at<PAIR>(at, k);
+                    const Turned turned = turned_at<PAIR>(at, step.flags, k);
                     copy_rows(to, left, row, k, at.k, turned.left, &sh.full[s]);
-                    copy_rows(to + kBlockBytes, right, col, k, at.step == kApply ? x.np : at.k,
-                              turned.right, &sh.full[s]);
+                    copy_rows(to + kBlockBytes, right, col, k,
+                              step.flags & kRightX ? x.np : at.k, turned.right, &sh.full[s]);
                 }
             }
             if (!ok) atomicOr(&g_matrix_status, kStatusProducerTimeout);
@@ -393,7 +394,8 @@ __global__ void __launch_bounds__(Shape<PAIR>::kThreads, 1)
             uint32_t used = 0, n = 0;                     // stages, pieces
             bool ok = true;
             for (uint32_t i = unit; ok && i < tiles; i += units) {
-                const Tile at = tile_at<PAIR>(t, i);
+                const Tile at = tile_at<PAIR>(t, call, i);
+                const int flags = call.step[at.step].flags;
                 for (int k0 = 0; ok && k0 < at.k; k0 += kPiece, ++n) {
                     const uint32_t d = tmem + n % 2 * kTile;
                     if (n >= 2) {
@@ -412,7 +414,7 @@ __global__ void __launch_bounds__(Shape<PAIR>::kThreads, 1)
                         tmem_fence_after();
                         const uint32_t a = smem_addr(ring + s * kStageBytes);
                         const uint32_t b = a + kBlockBytes;
-                        const Turned turned = turned_at<PAIR>(at, k);
+                        const Turned turned = turned_at<PAIR>(at, flags, k);
                         const uint32_t form =
                             half_product(kTile, kTile, turned.left, turned.right);
                         // 16 k are 32 bytes along the rows, or 16 rows of 128 bytes
@@ -443,7 +445,7 @@ __global__ void __launch_bounds__(Shape<PAIR>::kThreads, 1)
             uint32_t used = 0;
             bool ok = true;
             for (uint32_t i = unit; ok && i < tiles; i += units) {
-                const Tile at = tile_at<PAIR>(t, i);
+                const Tile at = tile_at<PAIR>(t, call, i);
                 for (int k = 0; k < at.k; k += 64, ++used) {
                     const uint32_t s = used % kStages;
                     ok = mbar_wait(&sh.full[s], (used / kStages) & 1, limit_ns);
@@ -476,9 +478,8 @@ __global__ void __launch_bounds__(Shape<PAIR>::kThreads, 1)
             __syncwarp();                                // all have read what lane 0 moves on
             if (!more) break;
             if (lane == 0) {
-                const Tile next = tile_at<PAIR>(t, my.index);
+                const Tile next = tile_at<PAIR>(t, call, my.index);
                 my.tile.matrix = next.matrix;
-                my.tile.round = next.round;
                 my.tile.step = next.step;
                 my.tile.row = next.row + my.down;        // this warp's
                 my.tile.col = next.col + my.across;
@@ -517,24 +518,16 @@ __global__ void __launch_bounds__(Shape<PAIR>::kThreads, 1)
                 atomicOr(&g_matrix_status, kStatusConsumerTimeout);
                 break;
             }
-            // result = scale product, and `diagonal` on it
-            float scale = 1.0f / kScaleX, diagonal = 0.0f;
-            if (at.step == kPoly) {
-                scale = kScaleP / kScaleX / kScaleC;
-                diagonal = call.a * kScaleP;
-            } else if (at.step == kApply) {
-                scale = 1.0f / kScaleP;
-                if (at.round + 1 == call.rounds) {
-                    scale *= 1.0f / kScaleX;
+            const MatrixStep& step = call.step[at.step];
+            if (step.flags & kLastStep) {
 #pragma unroll
-                    for (int c = 0; c < F::kColumns; c += 8)
-                        finish(x, call, at.row + lane, at.col + c, sum + c, scale);
-                    __syncwarp();
-                    continue;
-                }
+                for (int c = 0; c < F::kColumns; c += 8)
+                    finish(x, call, at.row + lane, at.col + c, sum + c, step.scale);
+                __syncwarp();
+                continue;
             }
-            // 32 columns at a time: of X X^T, then of b + c X X^T
-            const int images = at.step == kGram ? 2 : 1;
+            // 32 columns at a time: of the result, then of C where it is A
+            const int images = step.flags & kWithC ? 2 : 1;
 #pragma unroll
             for (int c = 0; c < F::kColumns; c += 32) {
 #pragma unroll 1                                             // twice its code takes more registers
@@ -543,15 +536,11 @@ __global__ void __launch_bounds__(Shape<PAIR>::kThreads, 1)
                     asm volatile("" : "+r"(row));            // formed here, not kept
                     const int on = at.row + row - at.col - c;   // the column on the diagonal
                     if (image == 0)
-                        split_sums(sum + c, scale, diagonal, on);
+                        split_sums(sum + c, step.scale, step.diagonal, on);
                     else
-                        split_again(sum + c, call.c * (kScaleC / kScaleX), call.b * kScaleC, on);
-                    void* to = at.step == kApply  ? x.x[(at.round & 1) ^ 1]
-                               : at.step == kPoly ? x.poly
-                               : image == 0       ? x.gram
-                                                  : x.comb;
-                    store_words(block_at(to, at.row, at.col + c,
-                                         at.step == kApply ? x.np : x.mp) +
+                        split_again(sum + c, call.c_scale, call.c_diagonal, on);
+                    store_words(block_at(x.image[image == 0 ? step.out : kC], at.row, at.col + c,
+                                         step.out <= kX1 ? x.np : x.mp) +
                                     at.row % 128 * 128,
                                 c % 64 / 8, sum + c, my.out);
                 }
@@ -577,19 +566,36 @@ __global__ void __launch_bounds__(Shape<PAIR>::kThreads, 1)
 
 // --------------------------------------------------- moments, norms, images
 
-// u of element i from the gradient and the new momentum.
-template <int T>
+// The update from the gradient and the new momentum.
 __device__ __forceinline__ float update_of(const MatrixItem& x, const MatrixGroup& g, float coef,
                                            float grad, float m) {
     if (x.m_buf == nullptr) return grad;
     return g.nesterov ? fmaf(g.mu, m, g.one_mu * (grad * coef)) : m;
 }
 
+// N elements from i on: the momentum, and the sum of the update's squares.
+template <int T, int N>
+__device__ __forceinline__ void moments_of(const MatrixItem& x, const MatrixGroup& g, float coef,
+                                           int64_t i, float* sum) {
+    float d[N], m[N] = {};
+    load_elems<T, N>(static_cast<const typename Elem<T>::Store*>(x.grad) + i, d);
+    if (x.m_buf != nullptr) {
+        load_elems<kGradF32, N>(x.m_buf + i, m);
+#pragma unroll
+        for (int k = 0; k < N; ++k) m[k] = fmaf(g.mu, m[k], g.one_mu * (d[k] * coef));
+        store_elems<kGradF32, N>(x.m_buf + i, m);
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const float u = update_of(x, g, coef, d[k], m[k]);
+        *sum = fmaf(u, u, *sum);
+    }
+}
+
 // The momentum, and each part's sum of the update's squares.
 template <int T>
 __global__ void __launch_bounds__(256) matrix_moments(const __grid_constant__ MatrixTable t,
-                                                      const MatrixCall call) {
-    using S = typename Elem<T>::Store;
+                                                      const __grid_constant__ MatrixCall call) {
     __shared__ double warp_sum[8];
     pdl_enter();
     if (skip_step(call.skip)) return;
@@ -600,19 +606,15 @@ __global__ void __launch_bounds__(256) matrix_moments(const __grid_constant__ Ma
     if (part == 0 && threadIdx.x == 0) *x.tiles_done = 0;
     const float coef = call.coef != nullptr ? __ldg(call.coef) : 1.0f;
     const int64_t n = static_cast<int64_t>(x.m) * x.n;
-    const S* grad = static_cast<const S*>(x.grad);
+    const int64_t first = static_cast<int64_t>(part) * 256 + threadIdx.x;
+    const int64_t next = static_cast<int64_t>(parts) * 256;
     float sum = 0.0f;
-    for (int64_t i = static_cast<int64_t>(part) * 256 + threadIdx.x; i < n;
-         i += static_cast<int64_t>(parts) * 256) {
-        const float d = elem_to_f32<T>(grad[i]);
-        float m = 0.0f;
-        if (x.m_buf != nullptr) {
-            m = fmaf(g.mu, x.m_buf[i], g.one_mu * (d * coef));
-            x.m_buf[i] = m;
-        }
-        const float u = update_of<T>(x, g, coef, d, m);
-        sum = fmaf(u, u, sum);
+    int64_t at = 0;                              // elements done in vectors
+    if (x.flat) {
+        at = n / 8 * 8;
+        for (int64_t i = first; i < n / 8; i += next) moments_of<T, 8>(x, g, coef, 8 * i, &sum);
     }
+    for (int64_t i = at + first; i < n; i += next) moments_of<T, 1>(x, g, coef, i, &sum);
     double s = sum;
 #pragma unroll
     for (int d = 16; d > 0; d /= 2) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
@@ -626,7 +628,7 @@ __global__ void __launch_bounds__(256) matrix_moments(const __grid_constant__ Ma
 // X's image: a block of it per thread block.
 template <int T>
 __global__ void __launch_bounds__(256) matrix_image(const __grid_constant__ MatrixTable t,
-                                                    const MatrixCall call) {
+                                                    const __grid_constant__ MatrixCall call) {
     using S = typename Elem<T>::Store;
     __shared__ double warp_sum[8];
     pdl_enter();
@@ -644,27 +646,40 @@ __global__ void __launch_bounds__(256) matrix_image(const __grid_constant__ Matr
     for (int w = 0; w < 8; ++w) s += warp_sum[w];
     // a sum that is not finite leaves nothing finite
     const float scale = s <= 1.7976931348623157e308
-                            ? static_cast<float>(kScaleX / (sqrt(s) + call.eps))
+                            ? static_cast<float>(kImageScaleX / (sqrt(s) + call.eps))
                             : __int_as_float(0x7FFFFFFF);
     const float coef = call.coef != nullptr ? __ldg(call.coef) : 1.0f;
     const S* grad = static_cast<const S*>(x.grad);
     const int block = blockIdx.x - t.image0[k], wide = x.np / 64;
     const int row0 = block / wide * 128, col0 = block % wide * 64;
-    char* to = static_cast<char*>(x.x[0]) + static_cast<int64_t>(block) * kBlockBytes;
+    char* to = static_cast<char*>(x.image[kX0]) + static_cast<int64_t>(block) * kBlockBytes;
+    const bool whole = x.flat && !x.tall && x.n % 8 == 0;   // eight columns are one vector
+#pragma unroll
     for (int q = threadIdx.x; q < 1024; q += 256) {
         // eight columns of a row; consecutive threads along what memory has in a row
         const int r = x.tall ? q % 128 : q / 8, c = x.tall ? q / 128 * 8 : q % 8 * 8;
-        float v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int row = row0 + r, col = col0 + c + j;
-            v[j] = 0.0f;
+        const int row = row0 + r, col = col0 + c;
+        float v[8] = {}, m[8] = {};
+        if (whole) {
             if (row < x.m && col < x.n) {
-                const int64_t i = x.tall ? static_cast<int64_t>(col) * x.m + row
-                                         : static_cast<int64_t>(row) * x.n + col;
-                v[j] = scale * update_of<T>(x, g, coef, elem_to_f32<T>(grad[i]),
-                                            x.m_buf != nullptr ? x.m_buf[i] : 0.0f);
+                const int64_t i = static_cast<int64_t>(row) * x.n + col;
+                load_elems<T, 8>(grad + i, v);
+                if (x.m_buf != nullptr) load_elems<kGradF32, 8>(x.m_buf + i, m);
             }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (row >= x.m || col + j >= x.n) continue;
+                const int64_t i = x.tall ? static_cast<int64_t>(col + j) * x.m + row
+                                         : static_cast<int64_t>(row) * x.n + col + j;
+                v[j] = elem_to_f32<T>(grad[i]);
+                if (x.m_buf != nullptr) m[j] = x.m_buf[i];
+            }
+        }
+        if (row < x.m) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] = col + j < x.n ? scale * update_of(x, g, coef, v[j], m[j]) : 0.0f;
         }
         uint4 hi, lo;
         split_pair(v[0], v[1], &hi.x, &lo.x);
@@ -710,8 +725,7 @@ int resident_units() {
 
 template <bool PAIR>
 cudaError_t go_rounds(const MatrixTable& t, const MatrixCall& c, cudaStream_t stream) {
-    const uint32_t sym = t.sym0[t.count], full = t.full0[t.count];
-    const uint32_t most = sym > full ? sym : full;
+    const uint32_t most = c.most;
     const int fit = resident_units<PAIR>();
     if (fit < 1) return cudaErrorLaunchOutOfResources;
     const uint32_t units = most < static_cast<uint32_t>(fit) ? most : static_cast<uint32_t>(fit);

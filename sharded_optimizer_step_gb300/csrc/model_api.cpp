@@ -65,11 +65,11 @@ constexpr int64_t kGroupBytes = int64_t{2} << 30;
 
 int64_t padded(int64_t n, int64_t tile) { return (n + tile - 1) / tile * tile; }
 constexpr int64_t kMatrixWords = kMatrixParts * sizeof(double) + 128;   // sums and a counter
-// A matrix's part of the workspace: two images of X, three of its products, the words
-// (with either tile).
+// A matrix's part of the workspace: two images of X, six of symmetric matrices, the
+// words (with either tile).
 int64_t matrix_bytes(int64_t rows, int64_t cols) {
     const int64_t m = padded(std::min(rows, cols), 256), n = padded(std::max(rows, cols), 256);
-    return 8 * m * n + 12 * m * m + kMatrixWords;
+    return 8 * m * n + 24 * m * m + kMatrixWords;
 }
 bool side_ok(int64_t n) { return n >= 0 && n <= kSideMax; }
 
@@ -163,6 +163,7 @@ bool take_group(const F& item, int32_t at, int32_t end, MatrixTable* t) {
         if (rows == 0 || cols == 0) continue;
         x.tall = rows > cols;
         x.whole = std::max(rows, cols) % 8 == 0 && aligned(x.master, 16) && aligned(x.out, 16);
+        x.flat = aligned(x.grad, 16) && aligned(x.m_buf, 16);
         x.m = static_cast<int32_t>(std::min(rows, cols));
         x.n = static_cast<int32_t>(std::max(rows, cols));
         t->item[t->count++] = x;
@@ -170,32 +171,114 @@ bool take_group(const F& item, int32_t at, int32_t end, MatrixTable* t) {
     return t->count > 0;
 }
 
-// About how long a round takes with either tile, in units of 64 k of a 128 x 128 tile
-// (0.49 us; a 256 x 256 tile takes a pair 0.79 us: it copies half as much per product).
-// The larger tile is the faster one where there are enough of them for all pairs: 12
-// matrices of 1024 x 1024 take 671 us with it and 770 with the smaller one, one of
-// them 376 and 264.
-double round_cost(const MatrixTable& t, int64_t tile, int units) {
-    double total = 0.0;
-    for (int step = 0; step < 3; ++step) {
-        double work = 0.0, longest = 0.0;
-        for (int j = 0; j < t.count; ++j) {
-            const double side = static_cast<double>(padded(t.item[j].m, tile) / tile);
-            const double wide = static_cast<double>(padded(t.item[j].n, tile) / tile);
-            const double k = (step == 0 ? wide : side) * static_cast<double>(tile / 64);
-            work += k * (step == 2 ? side * wide : side * (side + 1) / 2);
-            longest = std::max(longest, k);
+// The products of all rounds.  One round at a time these are A = X X^T, P = a + A C and
+// X = P X.  Rounds can also be taken two or three at a time without forming X in
+// between, since everything is a polynomial in A: A' = (P X)(P X)^T = (A P) P, the next
+// P from it, and X = P'' P' P X.  That is 2 products with X a segment and 5 to 9 without
+// instead of 2 and 1 a round: for 5 rounds of an m x n matrix 14 m^3 + 6 m^2 n
+// (products of symmetric matrices half) instead of 5 m^3 + 15 m^2 n.  What a round
+// leaves of small singular values grows with their square, so three rounds are the
+// most, and only at the start: errors are then those of round by round (1e-5 of the
+// norm; 3 then 2 rounds 1.3e-5 to 1.7e-5 on decaying spectra, round by round 1.4e-5 to
+// 4.5e-5, 2 then 3 rounds 1e-4).
+void plan_steps(MatrixCall* call, bool segments) {
+    double scale[kImages];
+    scale[kX0] = scale[kX1] = scale[kA] = scale[kZ] = kImageScaleX;
+    scale[kC] = kImageScaleX / 4;
+    scale[kP0] = scale[kP1] = scale[kQ] = kImageScaleX / 2;
+    call->c_scale = static_cast<float>(call->c * scale[kC] / scale[kA]);
+    call->c_diagonal = static_cast<float>(call->b * scale[kC]);
+    int sym = 0, full = 0, sym_level = 0, full_level = 0;
+    call->steps = 0;
+    const auto add = [&](int left, int right, int out, int flags, bool same_level = false) {
+        if (!same_level) {
+            sym_level = sym;
+            full_level = full;
         }
-        work /= units;
-        total += work < longest ? longest : work + longest / 3;
+        MatrixStep& s = call->step[call->steps++];
+        s = MatrixStep{};
+        s.left = static_cast<uint8_t>(left);
+        s.right = static_cast<uint8_t>(right);
+        s.out = static_cast<uint8_t>(out);
+        s.flags = static_cast<uint8_t>(flags);
+        s.scale = static_cast<float>((flags & kLastStep ? 1.0 : scale[out]) /
+                                     (scale[left] * scale[right]));
+        s.diagonal = right == kC ? static_cast<float>(call->a * scale[out]) : 0.0f;
+        s.sym_before = static_cast<uint16_t>(sym_level);
+        s.full_before = static_cast<uint16_t>(full_level);
+        ++(flags & kSymmetric ? sym : full);
+    };
+    int x = kX0;
+    for (int done = 0; done < call->rounds;) {
+        const int left = call->rounds - done;
+        const int take = !segments ? 1 : done == 0 ? std::min(left, 3) : std::min(left, 2);
+        add(x, x, kA, kSymmetric | kLeftX | kWithC);
+        int p = kP0, q = kP0;
+        scale[kP0] = scale[kP1] = kImageScaleX / 2;
+        add(kA, kC, p, kSymmetric);
+        for (int k = 1; k < take; ++k) {
+            add(kA, p, kZ, kSymmetric, k > 1);       // beside the last product of the P
+            add(kZ, p, kA, kSymmetric | kWithC);
+            const int next = p ^ kP0 ^ kP1;
+            scale[next] = kImageScaleX / 2;
+            add(kA, kC, next, kSymmetric);
+            // its elements are below 3.9 to the power of the rounds so far
+            const int to = q == kQ ? p : kQ;         // (p is done with by then)
+            scale[to] = kImageScaleX / (k == 1 ? 8 : 32);
+            add(next, q, to, kSymmetric);
+            q = to;
+            p = next;
+        }
+        done += take;
+        add(q, x, x ^ 1, kRightX | (done == call->rounds ? kLastStep : 0));
+        x ^= 1;
     }
-    return tile == 256 ? total * 1.6 : total;
+}
+
+// About how long the steps take, in units of 64 k of a 128 x 128 tile (0.49 us; a
+// 256 x 256 tile takes a pair 0.79 us: it copies half as much per product).  A level of
+// steps takes its longest tile and 7 us from the last results to the next products, or
+// the tiles' share per SM.  So the larger tile is taken where there are enough of them
+// for all pairs (12 matrices of 1024 x 1024 take 671 us with it and 770 with the
+// smaller one, one of them 376 and 264), and segments for long matrices.
+double steps_cost(const MatrixTable& t, const MatrixCall& call, int64_t tile, int units) {
+    const double each = tile == 256 ? 1.6 : 1.0;
+    double total = 0.0;
+    for (int s = 0; s < call.steps;) {
+        double work = 0.0, longest = 0.0;
+        const int level = call.step[s].sym_before + call.step[s].full_before;
+        for (; s < call.steps && call.step[s].sym_before + call.step[s].full_before == level; ++s) {
+            const int flags = call.step[s].flags;
+            for (int j = 0; j < t.count; ++j) {
+                const double side = static_cast<double>(padded(t.item[j].m, tile) / tile);
+                const double wide = static_cast<double>(padded(t.item[j].n, tile) / tile);
+                const double k = each * (flags & kLeftX ? wide : side) *
+                                 static_cast<double>(tile / 64);
+                work += k * (flags & kSymmetric ? side * (side + 1) / 2 : side * wide);
+                longest = std::max(longest, k);
+            }
+        }
+        total += std::max(work / units + longest / 3, longest + (tile == 256 ? 18 : 14));
+    }
+    return total;
 }
 
 // Tiles, workspace and the launches' bounds.
-void lay_out(MatrixTable* t, char* ws) {
+void lay_out(MatrixTable* t, MatrixCall* call, char* ws) {
     const int sms = device_sms();
-    t->pair = round_cost(*t, 256, sms / 2) < round_cost(*t, 128, sms);
+    double best = 0.0;
+    bool segments = false;
+    for (const bool split : {false, true}) {
+        plan_steps(call, split);
+        for (const int pair : {0, 1}) {
+            const double cost = steps_cost(*t, *call, pair ? 256 : 128, pair ? sms / 2 : sms);
+            if ((split || pair) && cost >= best) continue;
+            best = cost;
+            segments = split;
+            t->pair = pair;
+        }
+    }
+    plan_steps(call, segments);
     const int64_t tile = t->pair ? 256 : 128;
     // the longest tiles first, so that the last ones to end are short
     std::sort(t->item, t->item + t->count, [](const MatrixItem& a, const MatrixItem& b) {
@@ -208,12 +291,10 @@ void lay_out(MatrixTable* t, char* ws) {
         x.np = static_cast<int32_t>(padded(x.n, tile));
         const int64_t wide = 4 * static_cast<int64_t>(x.mp) * x.np;
         const int64_t square = 4 * static_cast<int64_t>(x.mp) * x.mp;
-        x.x[0] = ws;
-        x.x[1] = ws + wide;
-        x.gram = ws + 2 * wide;
-        x.comb = ws + 2 * wide + square;
-        x.poly = ws + 2 * wide + 2 * square;
-        x.part = reinterpret_cast<double*>(ws + 2 * wide + 3 * square);
+        x.image[kX0] = ws;
+        x.image[kX1] = ws + wide;
+        for (int i = kA; i < kImages; ++i) x.image[i] = ws + 2 * wide + (i - kA) * square;
+        x.part = reinterpret_cast<double*>(ws + 2 * wide + (kImages - kA) * square);
         x.tiles_done = reinterpret_cast<unsigned int*>(x.part + kMatrixParts);
         ws += matrix_bytes(x.m, x.n);
         t->sym0[j] = sym;
@@ -231,18 +312,30 @@ void lay_out(MatrixTable* t, char* ws) {
     t->full0[t->count] = full;
     t->part0[t->count] = part;
     t->image0[t->count] = image;
+    call->tiles = call->most = 0;
+    uint32_t level = 0;
+    for (int k = 0; k < call->steps; ++k) {
+        MatrixStep& s = call->step[k];
+        s.first = call->tiles;
+        const uint32_t tiles = s.flags & kSymmetric ? sym : full;
+        level = k > 0 && s.sym_before == call->step[k - 1].sym_before &&
+                        s.full_before == call->step[k - 1].full_before
+                    ? level + tiles : tiles;
+        call->tiles += tiles;
+        call->most = std::max(call->most, level);
+    }
 }
 
 template <typename S, typename F>
-int run_groups(const S& sides, const F& item, int32_t n, const MatrixCall& call, int grad_dtype,
+int run_groups(const S& sides, const F& item, int32_t n, MatrixCall* call, int grad_dtype,
                void* workspace, const char* what, cudaStream_t stream) {
     std::unique_ptr<MatrixTable> t(new MatrixTable);
     for (int32_t at = 0; at < n;) {
         int64_t bytes;
         const int32_t end = group_end(sides, n, at, &bytes);
         if (take_group(item, at, end, t.get())) {
-            lay_out(t.get(), static_cast<char*>(workspace));
-            const cudaError_t e = launch_matrices(*t, call, grad_dtype, stream);
+            lay_out(t.get(), call, static_cast<char*>(workspace));
+            const cudaError_t e = launch_matrices(*t, *call, grad_dtype, stream);
             if (e != cudaSuccess) return cuda_fail(what, e);
         }
         at = end;
@@ -505,7 +598,7 @@ int matrices_orthogonalize(const void* const* in, void* const* out, const int64_
         *r = rows[i];
         *c = cols[i];
     };
-    if (int rc = run_groups(sides, item, n, call, in_dtype, workspace, "orthogonalize",
+    if (int rc = run_groups(sides, item, n, &call, in_dtype, workspace, "orthogonalize",
                             static_cast<cudaStream_t>(stream));
         rc != SHARDSTEP_OK)
         return rc;
@@ -594,7 +687,7 @@ int tensors_muon_step(const shardstep_matrix_t* ms, int32_t n, int32_t grad_dtyp
         *r = t.rows;
         *c = t.cols;
     };
-    if (int rc = run_groups(sides, item, n, call, grad_dtype, workspace, "muon step",
+    if (int rc = run_groups(sides, item, n, &call, grad_dtype, workspace, "muon step",
                             static_cast<cudaStream_t>(stream));
         rc != SHARDSTEP_OK)
         return rc;

@@ -166,8 +166,8 @@ def test_matrices_workspace():
     assert need([-1], [3]) == need([3], [(1 << 20) + 1]) == -1 and need([], []) == 0
     assert need([0, 7], [9, 0]) == 0
     one = need([1], [1])
-    assert one == 20 * 256 * 256 + 2176 and need([128], [100]) == need([100], [128]) == one
-    assert need([600], [700]) == 20 * 768 * 768 + 2176
+    assert one == 32 * 256 * 256 + 2176 and need([128], [100]) == need([100], [128]) == one
+    assert need([600], [700]) == 32 * 768 * 768 + 2176
     assert need([200] * 3, [300] * 3) == 3 * need([200], [300])
     assert need([5] * 200, [5] * 200) == 64 * one          # a group at a time
     assert need([8192] * 9, [8192] * 9) == need([8192], [8192])
