@@ -395,8 +395,10 @@ int shardstep_device_status(uint32_t* status, int32_t clear) {
     if (e == cudaSuccess) e = read_loss_status(&loss, clear != 0);
     unsigned int matrix = 0;
     if (e == cudaSuccess) e = read_matrix_status(&matrix, clear != 0);
+    unsigned int norm = 0;
+    if (e == cudaSuccess) e = read_norm_status(&norm, clear != 0);
     if (e != cudaSuccess) return cuda_fail(e, "reading the device status word");
-    *status = s | loss | matrix;
+    *status = s | loss | matrix | norm;
     return ok();
 }
 

@@ -472,7 +472,8 @@ struct NormGradRows {
 // Blocks of the backward pass, each of which leaves one row of column sums; at
 // most kNormPieces.
 constexpr int kNormPieces = 160;
-int norm_pieces(int64_t rows, int64_t cols, bool vec);
+int norm_pieces(int64_t rows, int64_t cols, int type, bool vec);
+cudaError_t read_norm_status(unsigned int* status, bool clear);
 cudaError_t launch_layer_norm(const NormRows& a, int type, int w_type, bool vec,
                               cudaStream_t stream);
 cudaError_t launch_layer_norm_grad(const NormGradRows& a, int type, int w_type, void* d_w,

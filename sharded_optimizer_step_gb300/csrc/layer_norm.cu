@@ -23,6 +23,8 @@
 #include <algorithm>
 
 #include "elem.cuh"
+#include "pairs.cuh"
+#include "tma.cuh"
 
 namespace shardstep {
 namespace {
@@ -30,15 +32,33 @@ namespace {
 constexpr int kNormThreads = 512;   // most threads of a block; whole groups of rows
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 
+__device__ unsigned int g_norm_status;
+
 // Sums of two values over a group of `size` threads (32, 64, .., 512) that take
 // one row: shuffles, then one word per warp.  `words` holds 2 x 2 words per
 // warp of the block: two banks in turn, so that one barrier a sum is enough.
+// ALONE: the group is its block.  (A barrier whose number is not known when the kernel
+// is compiled takes all sixteen of a block, and an SM has 64.)
+template <bool ALONE>
 struct Group {
     int size, warp, first_warp, id;
     float2* words;
     int bank;
     __device__ __forceinline__ void sync() const {
-        asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(size) : "memory");
+        if constexpr (ALONE) __syncthreads();
+        else asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(size) : "memory");
+    }
+    __device__ __forceinline__ float sum(float a) {
+#pragma unroll
+        for (int d = 16; d > 0; d /= 2) a += __shfl_xor_sync(kFull, a, d);
+        if (size == 32) return a;
+        float* w = reinterpret_cast<float*>(words + bank * (kNormThreads / 32));
+        bank ^= 1;
+        if (threadIdx.x % 32 == 0) w[warp] = a;
+        sync();
+        float t = 0.0f;
+        for (int k = 0; k < size / 32; ++k) t += w[first_warp + k];
+        return t;
     }
     __device__ __forceinline__ float2 sum(float a, float b) {
 #pragma unroll
@@ -60,9 +80,10 @@ struct Group {
         return t;
     }
 };
-__device__ __forceinline__ Group group_of(int size, float2* words) {
-    const int g = threadIdx.x / size;
-    return Group{size, static_cast<int>(threadIdx.x / 32), g * size / 32, g, words, 0};
+template <bool ALONE>
+__device__ __forceinline__ Group<ALONE> group_of(int size, float2* words) {
+    const int g = ALONE ? 0 : threadIdx.x / size;
+    return Group<ALONE>{size, static_cast<int>(threadIdx.x / 32), g * size / 32, g, words, 0};
 }
 
 // The N elements of a row from column c on; those past its end are zeros, and
@@ -89,13 +110,117 @@ __device__ __forceinline__ void store_part(typename Elem<T>::Store* p, int c, in
     }
 }
 
+// A row as it is in memory: V vectors of N elements per thread (N 1: elements), and
+// two of its values at a time.
+template <int T, int N>
+struct Raw {
+    uint4 v;
+    __device__ __forceinline__ Pair pair(int j) const {
+        if constexpr (T == kGradF32) {
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            return make_pair(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
+        } else {
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            if constexpr (T == kGradF16) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+                return make_pair(f.x, f.y);
+            } else {
+                return make_pair(bf16_lo(w[j]), bf16_hi(w[j]));
+            }
+        }
+    }
+};
+template <int TW, int N>
+__device__ __forceinline__ void load_weights(const void* p, int c, Pair* w) {
+    float f[N];
+    load_elems<TW, N>(static_cast<const typename Elem<TW>::Store*>(p) + c, f);
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) w[j] = make_pair(f[2 * j], f[2 * j + 1]);
+}
+
+// Rows of whole vectors: kept as they are in memory (16 registers for 32 elements of
+// 16 bits), so that twice as many rows are on their way as with fp32 copies of them.
+template <int T, int TW, bool ALONE>
+__global__ void __launch_bounds__(kNormThreads, T == kGradF32 ? 1 : 2)
+    layer_norm_vectors(const NormRows a, int size) {
+    using S = typename Elem<T>::Store;
+    constexpr int N = Elem<T>::kVec, V = 32 / N;
+    __shared__ float2 words[2 * kNormThreads / 32];
+    Group<ALONE> g = group_of<ALONE>(size, words);
+    const int t = ALONE ? threadIdx.x : threadIdx.x % 32;
+    const int groups = ALONE ? 1 : blockDim.x / 32;
+    const float n = static_cast<float>(a.cols);
+    const int cols = static_cast<int>(a.cols);
+    pdl_enter();
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * groups + g.id;
+    if (row >= a.rows) return;   // a whole warp, or no one of the block
+    const S* x = static_cast<const S*>(a.x) + row * a.x_stride;
+    Raw<T, N> raw[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        const int c = (t + k * size) * N;
+        raw[k].v = c < cols ? *reinterpret_cast<const uint4*>(x + c) : make_uint4(0, 0, 0, 0);
+    }
+    Pair sum = make_pair(0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) sum = add2(sum, raw[k].pair(j));
+    // no rounded 1 / n: rows far from 0
+    const float mean = __fdiv_rn(g.sum(floats(sum).x + floats(sum).y), n);
+    const Pair off = make_pair(-mean, -mean);
+    sum = make_pair(0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        if ((t + k * size) * N >= cols) continue;
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) {
+            const Pair d = add2(raw[k].pair(j), off);
+            sum = fma2(d, d, sum);
+        }
+    }
+    const float var = __fdiv_rn(g.sum(floats(sum).x + floats(sum).y), n);
+    const float r = __fdiv_rn(1.0f, __fsqrt_rn(var + a.eps));
+    if (t == 0) {
+        a.mean[row] = mean;
+        a.rstd[row] = r;
+    }
+    S* out = static_cast<S*>(a.out) + row * a.out_stride;
+    const Pair r2 = make_pair(r, r);
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        const int c = (t + k * size) * N;
+        if (c >= cols) continue;
+        Pair y[N / 2], w[N / 2];
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) y[j] = mul2(add2(raw[k].pair(j), off), r2);
+        if (a.w != nullptr) {
+            load_weights<TW, N>(a.w, c, w);
+#pragma unroll
+            for (int j = 0; j < N / 2; ++j) y[j] = mul2(y[j], w[j]);
+        }
+        if (a.b != nullptr) {
+            load_weights<TW, N>(a.b, c, w);
+#pragma unroll
+            for (int j = 0; j < N / 2; ++j) y[j] = add2(y[j], w[j]);
+        }
+        float f[N];
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) {
+            f[2 * j] = floats(y[j]).x;
+            f[2 * j + 1] = floats(y[j]).y;
+        }
+        store_elems<T, N>(out + c, f);
+    }
+}
+
 // V vectors of N elements per thread.
 template <int T, int TW, int N, int V, bool TAIL>
 __global__ void __launch_bounds__(kNormThreads) layer_norm_rows(const NormRows a, int size) {
     using S = typename Elem<T>::Store;
     using W = typename Elem<TW>::Store;
     __shared__ float2 words[2 * kNormThreads / 32];
-    Group g = group_of(size, words);
+    Group<false> g = group_of<false>(size, words);
     const int t = threadIdx.x % size, groups = blockDim.x / size;
     const int cols = static_cast<int>(a.cols);
     pdl_enter();
@@ -119,7 +244,7 @@ __global__ void __launch_bounds__(kNormThreads) layer_norm_rows(const NormRows a
         for (int k = 0; k < V; ++k)
 #pragma unroll
             for (int j = 0; j < N; ++j) s += f[k][j];
-        const float mean = __fdiv_rn(g.sum(s, 0.0f).x, n);   // no rounded 1 / n: rows far from 0
+        const float mean = __fdiv_rn(g.sum(s), n);   // no rounded 1 / n: rows far from 0
         float q = 0.0f;
 #pragma unroll
         for (int k = 0; k < V; ++k) {
@@ -132,7 +257,7 @@ __global__ void __launch_bounds__(kNormThreads) layer_norm_rows(const NormRows a
                 q = fmaf(f[k][j], f[k][j], q);
             }
         }
-        const float var = __fdiv_rn(g.sum(q, 0.0f).x, n);
+        const float var = __fdiv_rn(g.sum(q), n);
         const float r = __fdiv_rn(1.0f, __fsqrt_rn(var + a.eps));
         if (t == 0) {
             a.mean[row] = mean;
@@ -166,7 +291,7 @@ __global__ void __launch_bounds__(THREADS) layer_norm_rows_grad(const NormGradRo
     using W = typename Elem<TW>::Store;
     __shared__ float2 words[2 * kNormThreads / 32];
     extern __shared__ float sums[];
-    Group g = group_of(size, words);
+    Group<false> g = group_of<false>(size, words);
     const int t = threadIdx.x % size, groups = blockDim.x / size;
     const int cols = static_cast<int>(a.cols);
     pdl_enter();
@@ -242,35 +367,200 @@ __global__ void __launch_bounds__(THREADS) layer_norm_rows_grad(const NormGradRo
     }
 }
 
+// Backward with rows on their way through shared memory: each group of threads has
+// `depth` slots of its own for rows of x and d, which its first thread fills by bulk
+// copies as soon as all have done with a row, so that some 190 KB a SM are in flight
+// whatever the threads do.  The row is read twice from shared memory, once for the
+// sums and once for d_x: in registers it would leave room for half the threads.  After
+// a wait that ran out a block goes on without waiting (its barriers need all threads),
+// with the status word set.
+constexpr int kStagedThreads = 512;
+constexpr int kStagedBytes = 216 * 1024;
+struct StagedShape {
+    int size, groups, depth;
+};
+template <int T, int TW, int N>
+__global__ void __launch_bounds__(kStagedThreads, 1)
+    layer_norm_staged_grad(const NormGradRows a, const StagedShape sh,
+                           unsigned long long limit_ns) {
+    using S = typename Elem<T>::Store;
+    using W = typename Elem<TW>::Store;
+    constexpr int V = 32 / N;
+    extern __shared__ __align__(128) char slots[];
+    __shared__ float2 words[2 * kNormThreads / 32];
+    __shared__ uint64_t full[kStagedThreads / 32 * 4];     // up to four slots a group
+    const int size = sh.size;
+    Group<false> g = group_of<false>(size, words);
+    const int t = threadIdx.x % size;
+    const int cols = static_cast<int>(a.cols);
+    const uint32_t row_bytes = cols * sizeof(S);
+    // the weights in fp32, then the slots
+    float* weights = reinterpret_cast<float*>(slots);
+    char* mine = slots + (a.w != nullptr ? 4 * cols : 0) +
+                 static_cast<size_t>(g.id) * sh.depth * 2 * row_bytes;
+    uint64_t* bar = full + g.id * sh.depth;
+    if (t == 0)
+        for (int k = 0; k < sh.depth; ++k) mbar_init(bar + k, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    pdl_enter();
+    if (a.w != nullptr)
+        for (int c = threadIdx.x; c < cols; c += blockDim.x)
+            weights[c] = elem_to_f32<TW>(static_cast<const W*>(a.w)[c]);
+    __syncthreads();
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * sh.groups + g.id;
+    const int64_t next = static_cast<int64_t>(gridDim.x) * sh.groups;
+    const int64_t rows = first < a.rows ? (a.rows - first + next - 1) / next : 0;   // of this group
+    const auto fetch = [&](int64_t j) {
+        const int64_t row = first + j * next;
+        const int slot = static_cast<int>(j % sh.depth);
+        char* to = mine + slot * 2 * row_bytes;
+        mbar_expect_tx(bar + slot, 2 * row_bytes);
+        bulk_load(to, static_cast<const S*>(a.x) + row * a.x_stride, row_bytes, bar + slot);
+        bulk_load(to + row_bytes, static_cast<const S*>(a.d) + row * a.d_stride, row_bytes,
+                  bar + slot);
+    };
+    int64_t fetched = 0;
+    if (t == 0)
+        for (; fetched < sh.depth && fetched < rows; ++fetched) fetch(fetched);
+    const float inv = 1.0f / static_cast<float>(a.cols);
+    bool late = false;
+    Pair dw[V][N / 2], db[V][N / 2];
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) dw[k][i] = db[k][i] = make_pair(0.0f, 0.0f);
+    int slot = 0, phase = 0;
+    float next_mean = rows > 0 ? __ldg(a.mean + first) : 0.0f;
+    float next_r = rows > 0 ? __ldg(a.rstd + first) : 0.0f;
+    for (int64_t j = 0; j < rows; ++j) {
+        const int64_t row = first + j * next;
+        const float mean = next_mean, r = next_r;
+        if (j + 1 < rows) {
+            next_mean = __ldg(a.mean + row + next);
+            next_r = __ldg(a.rstd + row + next);
+        }
+        const Pair off = make_pair(-mean, -mean), r2 = make_pair(r, r);
+        if (!late && !mbar_wait(bar + slot, phase, limit_ns)) {
+            late = true;
+            atomicOr(&g_norm_status, kStatusConsumerTimeout);
+        }
+        const S* x = reinterpret_cast<const S*>(mine + slot * 2 * row_bytes);
+        const S* d = reinterpret_cast<const S*>(mine + slot * 2 * row_bytes + row_bytes);
+        Pair s1 = make_pair(0.0f, 0.0f), s2 = s1;
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int c = (t + k * size) * N;
+            if (c >= cols) continue;
+            Raw<T, N> rx{*reinterpret_cast<const uint4*>(x + c)};
+            Raw<T, N> rd{*reinterpret_cast<const uint4*>(d + c)};
+            Pair w[N / 2];
+            if (a.w != nullptr) load_weights<kGradF32, N>(weights, c, w);
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) {
+                const Pair xh = mul2(add2(rx.pair(i), off), r2);
+                Pair f = rd.pair(i);
+                dw[k][i] = fma2(f, xh, dw[k][i]);
+                db[k][i] = add2(db[k][i], f);
+                if (a.w != nullptr) f = mul2(f, w[i]);
+                s1 = add2(s1, f);
+                s2 = fma2(f, xh, s2);
+            }
+        }
+        const float2 m = g.sum(floats(s1).x + floats(s1).y, floats(s2).x + floats(s2).y);
+        // all threads are here: none reads the row before any more
+        if (t == 0 && !late && j > 0 && fetched < rows) fetch(fetched++);
+        if (a.d_x != nullptr) {
+            // r (f - c1 - xh c2) = r f + (x - mean) (-r r c2) - r c1
+            const float c1 = -r * (m.x * inv), c2 = -r * (r * (m.y * inv));
+            const Pair k1 = make_pair(c1, c1), k2 = make_pair(c2, c2);
+            S* dx = static_cast<S*>(a.d_x) + row * a.d_x_stride;
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                const int c = (t + k * size) * N;
+                if (c >= cols) continue;
+                Raw<T, N> rx{*reinterpret_cast<const uint4*>(x + c)};
+                Raw<T, N> rd{*reinterpret_cast<const uint4*>(d + c)};
+                Pair w[N / 2];
+                if (a.w != nullptr) load_weights<kGradF32, N>(weights, c, w);
+                float f[N];
+#pragma unroll
+                for (int i = 0; i < N / 2; ++i) {
+                    Pair y = rd.pair(i);
+                    if (a.w != nullptr) y = mul2(y, w[i]);
+                    y = fma2(y, r2, fma2(add2(rx.pair(i), off), k2, k1));
+                    f[2 * i] = floats(y).x;
+                    f[2 * i + 1] = floats(y).y;
+                }
+                store_elems<T, N>(dx + c, f);
+            }
+        }
+        if (++slot == sh.depth) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+    if (late && t == 0)      // copies in flight land before the block's memory goes
+        for (int64_t j = fetched > sh.depth ? fetched - sh.depth : 0; j < fetched; ++j)
+            if (!mbar_wait(bar + j % sh.depth, (j / sh.depth) & 1, kDrainNs))
+                atomicOr(&g_norm_status, kStatusDrainTimeout);
+    if (a.piece == nullptr) return;
+    // the groups' sums, added in the groups' order, where the rows were
+    float* sums = reinterpret_cast<float*>(slots + (a.w != nullptr ? 4 * cols : 0));
+    float* piece = a.piece + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
+    for (int q = 0; q < sh.groups; ++q) {
+        __syncthreads();
+        if (g.id != q) continue;
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int c = (t + k * size) * N;
+            if (c >= cols) continue;
+            float fw[N], fb[N];
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) {
+                fw[2 * i] = floats(dw[k][i]).x;
+                fw[2 * i + 1] = floats(dw[k][i]).y;
+                fb[2 * i] = floats(db[k][i]).x;
+                fb[2 * i + 1] = floats(db[k][i]).y;
+            }
+            if (q > 0) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    fw[i] += sums[c + i];
+                    fb[i] += sums[cols + c + i];
+                }
+            }
+            float* to = (q + 1 < sh.groups ? sums : piece) + c;
+            store_elems<kGradF32, N>(to, fw);
+            store_elems<kGradF32, N>(to + cols, fb);
+        }
+    }
+}
+
 // d_w and d_b from the blocks' sums: 32 columns per block, a warp takes every
-// eighth of the pieces, the warps' sums are added in their order.
+// sixteenth of the pieces, the warps' sums are added in their order.
 template <int TW>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(512)
     layer_norm_columns(const float* piece, int pieces, int64_t cols, void* d_w, void* d_b,
                        int accumulate) {
     using W = typename Elem<TW>::Store;
-    __shared__ float part[8][32];
+    __shared__ float part[16][32];
     pdl_enter();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;   // of 2 * cols
     float s = 0.0f;
     if (c < 2 * cols) {
         const float* p = piece + c;
-        int q = warp;
-        for (; q + 24 < pieces; q += 32) {
-            float f[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) f[k] = p[static_cast<int64_t>(q + 8 * k) * 2 * cols];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) s += f[k];
+        for (int k = 0; k < kNormPieces / 16; ++k) {
+            const int q = warp + 16 * k;
+            if (q < pieces) s += p[static_cast<int64_t>(q) * 2 * cols];
         }
-        for (; q < pieces; q += 8) s += p[static_cast<int64_t>(q) * 2 * cols];
     }
     part[warp][lane] = s;
     __syncthreads();
     if (warp != 0 || c >= 2 * cols) return;
 #pragma unroll
-    for (int k = 1; k < 8; ++k) s += part[k][lane];
+    for (int k = 1; k < 16; ++k) s += part[k][lane];
     W* to = static_cast<W*>(c < cols ? d_w : d_b);
     if (to == nullptr) return;
     to += c < cols ? c : c - cols;
@@ -285,20 +575,20 @@ __global__ void __launch_bounds__(kNormThreads) layer_norm_wide(const NormRows a
     using S = typename Elem<T>::Store;
     using W = typename Elem<TW>::Store;
     __shared__ float2 words[2 * kNormThreads / 32];
-    Group g = group_of(kNormThreads, words);
+    Group<true> g = group_of<true>(kNormThreads, words);
     pdl_enter();
     const float n = static_cast<float>(a.cols);
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const S* x = static_cast<const S*>(a.x) + row * a.x_stride;
         float s = 0.0f;
         for (int64_t c = threadIdx.x; c < a.cols; c += kNormThreads) s += elem_to_f32<T>(x[c]);
-        const float mean = __fdiv_rn(g.sum(s, 0.0f).x, n);   // no rounded 1 / n: rows far from 0
+        const float mean = __fdiv_rn(g.sum(s), n);   // no rounded 1 / n: rows far from 0
         float q = 0.0f;
         for (int64_t c = threadIdx.x; c < a.cols; c += kNormThreads) {
             const float y = elem_to_f32<T>(x[c]) - mean;
             q = fmaf(y, y, q);
         }
-        const float var = __fdiv_rn(g.sum(q, 0.0f).x, n);
+        const float var = __fdiv_rn(g.sum(q), n);
         const float r = __fdiv_rn(1.0f, __fsqrt_rn(var + a.eps));
         if (threadIdx.x == 0) {
             a.mean[row] = mean;
@@ -319,7 +609,7 @@ __global__ void __launch_bounds__(kNormThreads) layer_norm_wide_grad(const NormG
     using S = typename Elem<T>::Store;
     using W = typename Elem<TW>::Store;
     __shared__ float2 words[2 * kNormThreads / 32];
-    Group g = group_of(kNormThreads, words);
+    Group<true> g = group_of<true>(kNormThreads, words);
     pdl_enter();
     const float inv = 1.0f / static_cast<float>(a.cols);
     const W* w = static_cast<const W*>(a.w);
@@ -387,7 +677,9 @@ cudaError_t go_rows(const NormRows& a, bool vec, cudaStream_t stream) {
         return launch_after(layer_norm_wide<T, TW>,
                             dim3(static_cast<unsigned>(a.rows < most ? a.rows : most)),
                             dim3(kNormThreads), 0, stream, a);
-    const int threads = size > 128 ? size : 128;
+    // rows of vectors: four warps with a row each, or a block to a row
+    const bool whole = vec && a.cols % Elem<T>::kVec == 0;
+    const int threads = size > 128 || (whole && size > 32) ? size : 128;
     const int64_t blocks = (a.rows + threads / size - 1) / (threads / size);
     const dim3 grid(static_cast<unsigned>(blocks < 0x7FFFFFFF ? blocks : 0x7FFFFFFF));
     constexpr int N = Elem<T>::kVec;
@@ -395,8 +687,39 @@ cudaError_t go_rows(const NormRows& a, bool vec, cudaStream_t stream) {
         return launch_after(kernel, grid, dim3(threads), 0, stream, a, size);
     };
     return !vec              ? go(layer_norm_rows<T, TW, 1, 16, false>)
-           : a.cols % N == 0 ? go(layer_norm_rows<T, TW, N, 32 / N, false>)
+           : whole && size > 32 ? go(layer_norm_vectors<T, TW, true>)
+           : whole           ? go(layer_norm_vectors<T, TW, false>)
                              : go(layer_norm_rows<T, TW, N, 32 / N, true>);
+}
+
+// The groups of a block and their slots: as many groups as leave three slots each.
+StagedShape staged_shape(int64_t cols, int type) {
+    StagedShape s{fit_group(cols, 256, 32), 0, 0};
+    const int64_t slot = 2 * cols * (type == kGradF32 ? 4 : 2);
+    const int64_t room = kStagedBytes - 4 * cols;    // beside the weights
+    if (s.size == 0) return s;
+    // where few rows fit, more threads to each
+    while (s.size < kStagedThreads && room / (3 * slot) * s.size < kStagedThreads) s.size *= 2;
+    s.groups = static_cast<int>(std::min<int64_t>(kStagedThreads / s.size, room / (3 * slot)));
+    if (s.groups > 0)
+        s.depth = static_cast<int>(std::min<int64_t>(4, room / (s.groups * slot)));
+    return s;
+}
+template <int T, int TW>
+cudaError_t go_staged_grad(const NormGradRows& a, int blocks, cudaStream_t stream) {
+    const StagedShape s = staged_shape(a.cols, T);
+    const auto kernel = layer_norm_staged_grad<T, TW, Elem<T>::kVec>;
+    const cudaError_t e = cudaFuncSetAttribute(
+        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStagedBytes);
+    if (e != cudaSuccess) return e;
+    return launch_after(kernel, dim3(blocks), dim3(s.groups * s.size),
+                        static_cast<size_t>(s.groups) * s.depth * 2 * a.cols *
+                                sizeof(typename Elem<T>::Store) + 4 * a.cols,
+                        stream, a, s, tma_wait_limit());
+}
+// Whether rows go through shared memory: whole vectors, and some for every SM.
+bool staged(int64_t rows, int64_t cols, int type, bool vec) {
+    return vec && cols % (type == kGradF32 ? 4 : 8) == 0 && staged_shape(cols, type).groups > 0;
 }
 
 template <int T, int TW>
@@ -417,10 +740,11 @@ template <int T, int TW>
 cudaError_t go_grad(const NormGradRows& a, void* d_w, void* d_b, int accumulate, bool vec,
                     cudaStream_t stream) {
     const int size = fit_grad(a.cols, vec);
-    const int pieces = norm_pieces(a.rows, a.cols, vec);
+    const int pieces = norm_pieces(a.rows, a.cols, T, vec);
     cudaError_t e = cudaSuccess;
     if (a.rows > 0 && size != 0) {
-        e = go_rows_grad<T, TW>(a, size, pieces, vec, stream);
+        e = staged(a.rows, a.cols, T, vec) ? go_staged_grad<T, TW>(a, pieces, stream)
+                                           : go_rows_grad<T, TW>(a, size, pieces, vec, stream);
         note_launch();
     } else if (a.rows > 0) {
         if (a.d_x != nullptr) {
@@ -439,7 +763,7 @@ cudaError_t go_grad(const NormGradRows& a, void* d_w, void* d_b, int accumulate,
     }
     if (e != cudaSuccess || a.piece == nullptr) return e;
     e = launch_after(layer_norm_columns<TW>, dim3(static_cast<unsigned>((2 * a.cols + 31) / 32)),
-                     dim3(256), 0, stream, static_cast<const float*>(a.piece), pieces, a.cols, d_w,
+                     dim3(512), 0, stream, static_cast<const float*>(a.piece), pieces, a.cols, d_w,
                      d_b, accumulate);
     note_launch();
     return e;
@@ -456,14 +780,22 @@ cudaError_t by_types(int type, int w_type, F&& f) {
 }  // namespace
 
 // Blocks of the backward pass, each of which leaves one row of column sums.
-int norm_pieces(int64_t rows, int64_t cols, bool vec) {
+int norm_pieces(int64_t rows, int64_t cols, int type, bool vec) {
     const int size = fit_grad(cols, vec);
     if (rows == 0) return 0;
     if (size == 0) return static_cast<int>(rows < 64 ? rows : 64);
-    const int groups = grad_threads(vec) / size;
+    const int groups = staged(rows, cols, type, vec) ? staged_shape(cols, type).groups
+                                                     : grad_threads(vec) / size;
     const int64_t most = std::min(device_sms(), kNormPieces);
     const int64_t need = (rows + groups - 1) / groups;
     return static_cast<int>(need < most ? need : most);
+}
+
+cudaError_t read_norm_status(unsigned int* status, bool clear) {
+    cudaError_t e = cudaMemcpyFromSymbol(status, g_norm_status, sizeof(unsigned int));
+    if (e != cudaSuccess || !clear) return e;
+    const unsigned int zero = 0;
+    return cudaMemcpyToSymbol(g_norm_status, &zero, sizeof(unsigned int));
 }
 
 cudaError_t launch_layer_norm(const NormRows& a, int type, int w_type, bool vec,
