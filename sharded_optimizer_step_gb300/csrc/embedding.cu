@@ -15,7 +15,8 @@
 // chunks, whatever the ids are:
 //
 //   embedding_sort   block b owns the ids [b r, (b + 1) r).  It scans all ids
-//                    twice (from L2: 2 x 8 bytes a token and block): once to
+//                    twice (8 bytes a token and block from L2; up to 32768
+//                    tokens the second time from shared memory): once to
 //                    count its own and those below its range, which gives it
 //                    its place in the sorted list without any other block's
 //                    answer, once to place them.
@@ -32,9 +33,12 @@
 namespace shardstep {
 namespace {
 
-constexpr int kSortThreads = 512;
+constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kRowsAhead = 8;   // rows of d_out in flight per thread
+constexpr int kSortHeld = 32768;   // tokens whose ids a block keeps after its first scan
+constexpr int kIdsAhead = 4;       // loads of ids in flight per thread
+constexpr int kRowsAhead = 8;      // rows of d_out in flight per thread
+constexpr int kPiecesAhead = 16;   // of the pieces of a run
 
 __device__ __forceinline__ int64_t load_id(const void* ids, int ids64, int64_t i) {
     return ids64 ? __ldg(static_cast<const long long*>(ids) + i)
@@ -96,16 +100,22 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort(const EmbedArgs a
     const int64_t begin = warp * per < a.n ? warp * per : a.n;
     const int64_t end = begin + per < a.n ? begin + per : a.n;
     uint32_t* mine = counts + warp * s.range;
+    // what a token is to this block: its place in the range, or -1
+    int16_t* held = reinterpret_cast<int16_t*>(counts + kSortWarps * s.range);
+    const bool hold = a.n <= kSortHeld;
     uint32_t below = 0;
-    for (int64_t i = begin + lane; i < end; i += 4 * 32) {
-        int64_t id[4];
+    for (int64_t i = begin + lane; i < end; i += kIdsAhead * 32) {
+        int64_t id[kIdsAhead];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < kIdsAhead; ++k)
             id[k] = i + 32 * k < end ? load_id(a.ids, a.ids64, i + 32 * k) : -1;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < kIdsAhead; ++k) {
+            const bool in = id[k] >= lo && id[k] < lo + own;
             below += id[k] >= 0 && id[k] < lo;
-            if (id[k] >= lo && id[k] < lo + own) atomicAdd(mine + (id[k] - lo), 1u);
+            if (in) atomicAdd(mine + (id[k] - lo), 1u);
+            if (hold && i + 32 * k < end)
+                held[i + 32 * k] = static_cast<int16_t>(in ? id[k] - lo : -1);
         }
     }
     below = __reduce_add_sync(0xFFFFFFFFu, below);
@@ -139,30 +149,34 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort(const EmbedArgs a
     if (lo + own == a.vocab && k0 < own && k0 + each >= own) s.row_start[a.vocab] = at;
     __syncthreads();
 
-    for (int64_t i = begin; i < end; i += 4 * 32) {
-        int64_t id[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int64_t j = i + 32 * k + lane;
-            id[k] = j < end ? load_id(a.ids, a.ids64, j) : -1;
+    const auto place_tokens = [&](int64_t i, int slot) {
+        const uint32_t live = __ballot_sync(0xFFFFFFFFu, slot >= 0);
+        if (live == 0) return;
+        if (slot >= 0) {
+            const uint32_t peers = __match_any_sync(live, slot);
+            const uint32_t rank = __popc(peers & ((1u << lane) - 1));
+            const uint32_t place = mine[slot] + rank;
+            s.token[place] = static_cast<int32_t>(i);
+            s.id[place] = static_cast<int32_t>(lo + slot);
+            __syncwarp(live);
+            if (rank == 0) mine[slot] += __popc(peers);
         }
+        __syncwarp();
+    };
+    if (hold) {
+        for (int64_t i = begin + lane; i - lane < end; i += 32)
+            place_tokens(i, i < end ? held[i] : -1);
+        return;
+    }
+    for (int64_t i = begin + lane; i - lane < end; i += kIdsAhead * 32) {
+        int64_t id[kIdsAhead];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const bool in = id[k] >= lo && id[k] < lo + own;
-            const uint32_t live = __ballot_sync(0xFFFFFFFFu, in);
-            if (live == 0) continue;
-            if (in) {
-                const int slot = static_cast<int>(id[k] - lo);
-                const uint32_t peers = __match_any_sync(live, slot);
-                const uint32_t rank = __popc(peers & ((1u << lane) - 1));
-                const uint32_t place = mine[slot] + rank;
-                s.token[place] = static_cast<int32_t>(i + 32 * k + lane);
-                s.id[place] = static_cast<int32_t>(id[k]);
-                __syncwarp(live);
-                if (rank == 0) mine[slot] += __popc(peers);
-            }
-            __syncwarp();
-        }
+        for (int k = 0; k < kIdsAhead; ++k)
+            id[k] = i + 32 * k < end ? load_id(a.ids, a.ids64, i + 32 * k) : -1;
+#pragma unroll
+        for (int k = 0; k < kIdsAhead; ++k)
+            place_tokens(i + 32 * k, id[k] >= lo && id[k] < lo + own
+                                         ? static_cast<int>(id[k] - lo) : -1);
     }
 }
 
@@ -194,27 +208,47 @@ __device__ __forceinline__ void keep_piece(float* p, const float* sum) {
     }
 }
 
+template <int T, int N>
+struct RawElems {          // as they are in memory: a vector, or one element
+    using Type = uint4;
+};
+template <int T>
+struct RawElems<T, 1> {
+    using Type = typename Elem<T>::Store;
+};
+
 template <int TIN, int TOUT, int N>
 __global__ void __launch_bounds__(256) embedding_sum(const EmbedArgs a, const EmbedSort s) {
     using S = typename Elem<TIN>::Store;
+    using Raw = typename RawElems<TIN, N>::Type;
     __shared__ int32_t token[kEmbedChunkMax], id[kEmbedChunkMax];
+    __shared__ uint32_t start[kEmbedZeroRows + 1];
     __shared__ int32_t before, after;
     pdl_enter();
+    // units of sums and of zeros in turn, so that loads and stores mix
     const int64_t units = static_cast<int64_t>(s.chunks) * s.slices;
-    if (blockIdx.x >= units) {   // rows that do not occur
-        const int64_t v0 = (blockIdx.x - units) * kEmbedZeroRows;
+    const int64_t zeros = gridDim.x - units, both = units < zeros ? units : zeros;
+    const int64_t b = blockIdx.x;
+    const bool zero_rows = b < 2 * both ? b % 2 : units < zeros;
+    const int64_t unit = b < 2 * both ? b / 2 : b - both;
+    if (zero_rows) {   // rows that do not occur
+        const int64_t v0 = unit * kEmbedZeroRows;
+        const int count = static_cast<int>(a.vocab - v0 < kEmbedZeroRows ? a.vocab - v0
+                                                                         : kEmbedZeroRows);
+        if (threadIdx.x <= count) start[threadIdx.x] = s.row_start[v0 + threadIdx.x];
+        __syncthreads();
         const float zero[N] = {};
-        for (int64_t v = v0; v < v0 + kEmbedZeroRows && v < a.vocab; ++v) {
-            if (s.row_start[v] != s.row_start[v + 1]) continue;
+        for (int v = 0; v < count; ++v) {
+            if (start[v] != start[v + 1]) continue;
             typename Elem<TOUT>::Store* row =
-                static_cast<typename Elem<TOUT>::Store*>(a.table) + v * a.table_stride;
+                static_cast<typename Elem<TOUT>::Store*>(a.table) + (v0 + v) * a.table_stride;
             for (int64_t c = static_cast<int64_t>(threadIdx.x) * N; c < a.dim;
                  c += static_cast<int64_t>(blockDim.x) * N)
                 store_elems<TOUT, N>(row + c, zero);
         }
         return;
     }
-    const int64_t chunk = blockIdx.x / s.slices;
+    const int64_t chunk = unit / s.slices;
     const uint32_t live = s.row_start[a.vocab];   // tokens in the list
     const int64_t first = chunk * s.chunk;
     if (first >= live) return;
@@ -228,23 +262,26 @@ __global__ void __launch_bounds__(256) embedding_sum(const EmbedArgs a, const Em
         after = first + count < live ? s.id[first + count] : -1;
     }
     __syncthreads();
-    const int64_t c =
-        (blockIdx.x % s.slices * static_cast<int64_t>(blockDim.x) + threadIdx.x) * N;
+    const int64_t c = (unit % s.slices * static_cast<int64_t>(blockDim.x) + threadIdx.x) * N;
     if (c >= a.dim) return;
     const S* rows = static_cast<const S*>(a.rows) + c;
     float* piece = s.piece + 2 * chunk * a.dim + c;
     float sum[N] = {};
     for (int j0 = 0; j0 < count; j0 += kRowsAhead) {
-        float f[kRowsAhead][N];
+        Raw raw[kRowsAhead];
 #pragma unroll
         for (int j = 0; j < kRowsAhead; ++j)
-            if (j0 + j < count) load_elems<TIN, N>(rows + token[j0 + j] * a.row_stride, f[j]);
+            if (j0 + j < count)
+                raw[j] = __ldcs(reinterpret_cast<const Raw*>(rows + token[j0 + j] * a.row_stride));
 #pragma unroll
         for (int j = 0; j < kRowsAhead; ++j) {
             if (j0 + j >= count) continue;
             const int at = j0 + j, v = id[at];
+            float f[N];
+            if constexpr (N == 1) f[0] = elem_to_f32<TIN>(raw[j]);
+            else unpack16<TIN>(raw[j], f);
 #pragma unroll
-            for (int k = 0; k < N; ++k) sum[k] += f[j][k];
+            for (int k = 0; k < N; ++k) sum[k] += f[k];
             if (at + 1 < count && id[at + 1] == v) continue;
             // the run ends here: with what came before, alone, or to be continued
             if (v == before) keep_piece<N>(piece, sum);
@@ -274,13 +311,13 @@ __global__ void __launch_bounds__(256) embedding_join(const EmbedArgs a, const E
     const float* p = s.piece + c;
     float sum[N];
     load_elems<kGradF32, N>(p + (2 * chunk + 1) * a.dim, sum);
-    for (int64_t q = chunk + 1; q <= last; q += 4) {
-        float f[4][N];
+    for (int64_t q = chunk + 1; q <= last; q += kPiecesAhead) {
+        float f[kPiecesAhead][N];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < kPiecesAhead; ++j)
             if (q + j <= last) load_elems<kGradF32, N>(p + 2 * (q + j) * a.dim, f[j]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kPiecesAhead; ++j) {
             if (q + j > last) continue;
 #pragma unroll
             for (int k = 0; k < N; ++k) sum[k] += f[j][k];
@@ -315,9 +352,13 @@ cudaError_t go_sum(const EmbedArgs& a, EmbedSort s, cudaStream_t stream) {
                                  block, 0, stream, a, s);
     note_launch();
     if (e != cudaSuccess || s.chunks <= 1) return e;   // no run goes on
-    e = launch_after(embedding_join<TOUT, N>,
-                     dim3(static_cast<unsigned>(s.chunks - 1), static_cast<unsigned>(s.slices)),
-                     block, 0, stream, a, s);
+    // pieces are fp32: four columns a thread
+    constexpr int J = N == 1 ? 1 : 4;
+    const dim3 threads(threads_for(a.dim / J));
+    const int64_t slices = (a.dim / J + threads.x - 1) / threads.x;
+    e = launch_after(embedding_join<TOUT, J>,
+                     dim3(static_cast<unsigned>(s.chunks - 1), static_cast<unsigned>(slices)),
+                     threads, 0, stream, a, s);
     note_launch();
     return e;
 }
@@ -349,7 +390,8 @@ cudaError_t launch_embedding_grad(const EmbedArgs& a, EmbedSort s, int in_type, 
     const int sms = device_sms();
     const int64_t fair = (a.vocab + sms - 1) / sms;
     s.range = static_cast<int>(fair < kEmbedSortRange ? fair : kEmbedSortRange);
-    const size_t smem = sizeof(uint32_t) * kSortWarps * s.range;
+    const size_t smem = sizeof(uint32_t) * kSortWarps * s.range +
+                        (a.n <= kSortHeld ? sizeof(int16_t) * a.n : 0);
     cudaError_t e = cudaSuccess;
     if (smem > 48 * 1024)
         e = cudaFuncSetAttribute(embedding_sort, cudaFuncAttributeMaxDynamicSharedMemorySize,

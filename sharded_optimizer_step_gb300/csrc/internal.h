@@ -427,7 +427,7 @@ struct EmbedArgs {
     float scale;
 };
 constexpr int kEmbedChunkMax = 512;    // sorted tokens of a chunk
-constexpr int kEmbedSortRange = 2048;  // ids of a sorting block
+constexpr int kEmbedSortRange = 1024;  // ids of a sorting block
 constexpr int kEmbedZeroRows = 16;     // rows that a block looks through for absent ids
 struct EmbedPlan {
     int chunk;              // sorted tokens per block
