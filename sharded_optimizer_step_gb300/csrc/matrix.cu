@@ -44,12 +44,14 @@ constexpr int kOutPiece = 2048;
 // add up in their registers (rounding to nearest).
 constexpr int kPiece = 256;
 // A tile of results: 128 x 128 by one block, or 256 x 256 by a pair.  Each block
-// has 128 rows of it, and eight result warps, two for each quarter of the rows.
+// has 128 rows of it, and two result warps for each quarter of the rows with 128
+// columns each, or four with 32 (where tiles are few, a step's time is its last
+// tile's).
 template <bool PAIR>
 struct Shape {
     static constexpr int kTile = PAIR ? 256 : 128;
-    static constexpr int kResultWarps = 8;
-    static constexpr int kColumns = kTile / 2;           // of a result warp
+    static constexpr int kColumns = PAIR ? 128 : 32;     // of a result warp
+    static constexpr int kResultWarps = 4 * kTile / kColumns;
     static constexpr int kThreads = 64 + 32 * kResultWarps;
     static constexpr int kTmemColumns = 2 * kTile;       // two accumulators
     static constexpr int kBlocks = PAIR ? 2 : 1;
@@ -79,7 +81,7 @@ struct Shared {
     uint64_t done[2], taken[2];               // an accumulator is complete / has been read
     uint64_t drain;
     uint32_t tmem;
-    Work work[8];                             // of each result warp
+    Work work[16];                            // of each result warp
 };
 
 // Byte offset of element (row, col) within an image block's hi half.
@@ -542,7 +544,7 @@ __global__ void __launch_bounds__(Shape<PAIR>::kThreads, 1)
                     store_words(block_at(x.image[image == 0 ? step.out : kC], at.row, at.col + c,
                                          step.out <= kX1 ? x.np : x.mp) +
                                     at.row % 128 * 128,
-                                c % 64 / 8, sum + c, my.out);
+                                (at.col + c) % 64 / 8, sum + c, my.out);
                 }
             }
             // written, for copies as for loads; then another warp of the matrix is done
