@@ -501,6 +501,7 @@ struct MatrixItem {
     int32_t whole;                   // master and out take whole vectors of 8 along rows
     int32_t flat;                    // grad and m_buf take whole vectors of 8
 };
+constexpr int kMatrixTiles[3][2] = {{128, 64}, {128, 128}, {256, 256}};
 struct MatrixTable {
     MatrixItem item[kMatrices];
     uint32_t sym0[kMatrices + 1];    // first tile of the symmetric products
@@ -508,7 +509,7 @@ struct MatrixTable {
     uint32_t part0[kMatrices + 1];   // first sum of squares
     uint32_t image0[kMatrices + 1];  // first image block of x
     int32_t count;
-    int32_t pair;                    // tiles of 256 by pairs of blocks
+    int32_t shape;                   // of the tiles: kMatrixTiles[shape]
 };
 struct MatrixGroup {
     float lr_wd, mu, one_mu;

@@ -34,8 +34,8 @@ namespace {
 __device__ unsigned int g_matrix_status;
 
 constexpr int kBlockBytes = 32768;            // 128 x 64 halves, hi and lo
-constexpr int kStages = 3;
-constexpr int kStageBytes = 2 * kBlockBytes;
+constexpr int kRingBytes = 196608;            // of the stages
+constexpr int kMostStages = 4;
 // Results on their way out: each result warp's 32 rows x 32 columns of hi or lo.
 constexpr int kOutPiece = 2048;
 // The tensor cores cut sums off at fp32's last bit instead of rounding them, so a
@@ -43,22 +43,30 @@ constexpr int kOutPiece = 2048;
 // bit.  A sum over k therefore goes in pieces of this many, which the result warps
 // add up in their registers (rounding to nearest).
 constexpr int kPiece = 256;
-// A tile of results: 128 x 128 by one block, or 256 x 256 by a pair.  Each block
-// has 128 rows of it, and two result warps for each quarter of the rows with 128
-// columns each, or four with 32 (where tiles are few, a step's time is its last
-// tile's).
-template <bool PAIR>
+// A tile of results: 128 x 128 by one block, 128 x 64 where tiles are few (a step's
+// time is then its last tile's), or 256 x 256 by a pair of blocks, which copies half as
+// much for a product.  Each block has 128 rows of it, and for each quarter of them two
+// or four result warps with 128 or 32 columns each.  (256 x 128 by a pair was slower
+// than 128 x 128 by one block at every size: a stage is too short for the pair's
+// signals.)
+template <int ROWS, int COLS>
 struct Shape {
-    static constexpr int kTile = PAIR ? 256 : 128;
-    static constexpr int kColumns = PAIR ? 128 : 32;     // of a result warp
-    static constexpr int kResultWarps = 4 * kTile / kColumns;
+    static constexpr int kRows = ROWS, kCols = COLS;
+    static constexpr int kBlocks = ROWS / 128;
+    static constexpr bool kPair = kBlocks == 2;
+    static constexpr int kColumns = COLS == 256 ? 128 : 32;     // of a result warp
+    static constexpr int kResultWarps = 4 * COLS / kColumns;
     static constexpr int kThreads = 64 + 32 * kResultWarps;
-    static constexpr int kTmemColumns = 2 * kTile;       // two accumulators
-    static constexpr int kBlocks = PAIR ? 2 : 1;
-    static constexpr int kArrivals = kBlocks * kResultWarps;   // per tile
+    static constexpr int kTmemColumns = 2 * COLS;               // two accumulators
+    static constexpr int kArrivals = kBlocks * kResultWarps;    // per tile
+    // a stage: 128 rows and this block's columns, 64 k of each, hi and lo
+    static constexpr int kRightRows = COLS / kBlocks;
+    static constexpr int kRightHalf = kRightRows * 128;         // bytes of hi, and of lo
+    static constexpr int kStageBytes = kBlockBytes + 2 * kRightHalf;
+    static constexpr int kStages = kRingBytes / kStageBytes;
     // stages from a multiple of 1024 on, then the pieces on their way out
-    static constexpr int kDynamicBytes =
-        kStages * kStageBytes + kResultWarps * kOutPiece + 1024;
+    static constexpr int kDynamicBytes = kRingBytes + kResultWarps * kOutPiece + 1024;
+    static_assert(kStages <= kMostStages && kStageBytes % 1024 == 0, "the ring");
 };
 
 struct Tile {
@@ -76,8 +84,8 @@ struct Work {
 };
 
 struct Shared {
-    uint64_t full[kStages], empty[kStages];
-    uint64_t peer[kStages];                   // the other block's stage is full
+    uint64_t full[kMostStages], empty[kMostStages];
+    uint64_t peer[kMostStages];               // the other block's stage is full
     uint64_t done[2], taken[2];               // an accumulator is complete / has been read
     uint64_t drain;
     uint32_t tmem;
@@ -117,10 +125,9 @@ __device__ __forceinline__ int find(const uint32_t* first, int count, uint32_t t
 }
 
 // Tile `index` of the call: step by step, matrix by matrix.
-template <bool PAIR>
+template <class F>
 __device__ __forceinline__ Tile tile_at(const MatrixTable& t, const MatrixCall& call,
                                         uint32_t index) {
-    constexpr int kTile = Shape<PAIR>::kTile;
     Tile out;
     int lo = 0, hi = call.steps - 1;
     while (lo < hi) {
@@ -136,18 +143,19 @@ __device__ __forceinline__ Tile tile_at(const MatrixTable& t, const MatrixCall& 
     out.matrix = find(first, t.count, index);
     const MatrixItem& x = t.item[out.matrix];
     int i = static_cast<int>(index - first[out.matrix]);
-    const int side = x.mp / kTile, all = x.np / kTile;
+    const int side = x.mp / F::kRows, all = x.np / F::kCols;
+    constexpr int per = F::kRows / F::kCols;     // tiles on the diagonal of each row of them
     if (sym) {
         int r = 0;
-        while (i >= side - r) i -= side - r++;
-        out.row = r * kTile;
-        out.col = (r + i) * kTile;
+        while (i >= (side - r) * per) i -= (side - r++) * per;
+        out.row = r * F::kRows;
+        out.col = r * F::kRows + i * F::kCols;
     } else {          // the rows of a column first: they share X's columns
-        out.row = i % side * kTile;
-        out.col = i / side * kTile;
+        out.row = i % side * F::kRows;
+        out.col = i / side * F::kCols;
     }
     out.k = step.flags & kLeftX ? x.np : x.mp;
-    out.before = step.sym_before * (side * (side + 1) / 2) + step.full_before * (side * all);
+    out.before = step.sym_before * (per * side * (side + 1) / 2) + step.full_before * (side * all);
     return out;
 }
 
@@ -156,25 +164,32 @@ __device__ __forceinline__ Tile tile_at(const MatrixTable& t, const MatrixCall& 
 struct Turned {
     bool left, right;
 };
-template <bool PAIR>
+template <class F>
 __device__ __forceinline__ Turned turned_at(const Tile& at, int flags, int k) {
-    const int tile = k / Shape<PAIR>::kTile * Shape<PAIR>::kTile;
-    return Turned{!(flags & kLeftX) && tile < at.row,
-                  (flags & kRightX) || (!(flags & kLeftX) && tile < at.col)};
+    const bool x = flags & kLeftX;
+    return Turned{!x && k / F::kRows < at.row / F::kRows,
+                  (flags & kRightX) || (!x && k / F::kRows < at.col / F::kRows)};
 }
-// 128 rows' 64 k, hi and lo: one block, or, turned, 64 rows of k of two blocks (hi of
-// both, then lo of both).
+// 64 k of 128 or 64 rows, hi then lo: a block (its half of each part), or, turned, 64
+// rows of k of one block for each 64 rows.
+template <int ROWS>
 __device__ __forceinline__ void copy_rows(char* to, const void* image, int row, int k, int width,
                                           bool turned, uint64_t* bar) {
     if (!turned) {
-        bulk_load(to, block_at(image, row, k, width), kBlockBytes, bar);
+        const char* from = block_at(image, row, k, width) + row % 128 * 128;
+        if constexpr (ROWS == 128) {
+            bulk_load(to, from, kBlockBytes, bar);
+        } else {
+            bulk_load(to, from, 8192, bar);
+            bulk_load(to + 8192, from + kBlockBytes / 2, 8192, bar);
+        }
         return;
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < ROWS / 32; ++j)          // hi of all, then lo of all
         bulk_load(to + j * 8192,
-                  block_at(image, k, row + j % 2 * 64, width) + j / 2 * (kBlockBytes / 2) +
-                      k % 128 * 128,
+                  block_at(image, k, row + j % (ROWS / 64) * 64, width) +
+                      j / (ROWS / 64) * (kBlockBytes / 2) + k % 128 * 128,
                   8192, bar);
 }
 
@@ -320,18 +335,18 @@ __device__ __forceinline__ void finish(const MatrixItem& x, const MatrixCall& c,
 // products of both, and the second's passes on that its stages are full.  Every
 // wait has a limit: past it the block sets the status word, lets its copies and
 // products in flight end, frees its tensor memory and returns.
-template <bool PAIR>
-__global__ void __launch_bounds__(Shape<PAIR>::kThreads, 1)
+template <class F>
+__global__ void __launch_bounds__(F::kThreads, 1)
     matrix_rounds(const __grid_constant__ MatrixTable t, const __grid_constant__ MatrixCall call,
                   unsigned long long limit_ns) {
-    using F = Shape<PAIR>;
-    constexpr int kTile = F::kTile;
+    constexpr bool kPair = F::kPair;
+    constexpr int kStages = F::kStages;
     extern __shared__ char raw[];
     __shared__ Shared sh;
     char* ring =
         reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t{1023});
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const uint32_t rank = PAIR ? pair_rank() : 0;
+    const uint32_t rank = kPair ? pair_rank() : 0;
     const uint32_t unit = blockIdx.x / F::kBlocks, units = gridDim.x / F::kBlocks;
     const uint32_t tiles = call.tiles;
     if (threadIdx.x == 0) {
@@ -347,9 +362,9 @@ __global__ void __launch_bounds__(Shape<PAIR>::kThreads, 1)
         mbar_init(&sh.drain, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 1) tmem_alloc<PAIR, F::kTmemColumns>(&sh.tmem);
+    if (warp == 1) tmem_alloc<kPair, F::kTmemColumns>(&sh.tmem);
     tmem_fence_before();
-    if constexpr (PAIR) pair_sync();
+    if constexpr (kPair) pair_sync();
     else __syncthreads();
     tmem_fence_after();
     const uint32_t tmem = sh.tmem;
@@ -360,7 +375,7 @@ __global__ void __launch_bounds__(Shape<PAIR>::kThreads, 1)
             uint32_t issued = 0;
             bool ok = true;
             for (uint32_t i = unit; ok && i < tiles; i += units) {
-                const Tile at = tile_at<PAIR>(t, call, i);
+                const Tile at = tile_at<F>(t, call, i);
                 const MatrixItem& x = t.item[at.matrix];
                 if (at.before > 0)
                     ok = tiles_wait(x.tiles_done, at.before * F::kArrivals, limit_ns);
@@ -369,7 +384,7 @@ __global__ void __launch_bounds__(Shape<PAIR>::kThreads, 1)
                 const MatrixStep& step = call.step[at.step];
                 const void* left = x.image[step.left];
                 const void* right = x.image[step.right];
-                const int row = at.row + 128 * rank, col = at.col + 128 * rank;
+                const int row = at.row + 128 * rank, col = at.col + F::kRightRows * rank;
                 for (int k = 0; k < at.k; k += 64, ++issued) {
                     const uint32_t s = issued % kStages;
                     if (issued >= kStages &&
@@ -377,12 +392,13 @@ __global__ void __launch_bounds__(Shape<PAIR>::kThreads, 1)
                         ok = false;
                         break;
                     }
-                    char* to = ring + s * kStageBytes;
-                    mbar_expect_tx(&sh.full[s], kStageBytes);
-                    const Turned turned = turned_at<PAIR>(at, step.flags, k);
-                    copy_rows(to, left, row, k, at.k, turned.left, &sh.full[s]);
-                    copy_rows(to + kBlockBytes, right, col, k,
-                              step.flags & kRightX ? x.np : at.k, turned.right, &sh.full[s]);
+                    char* to = ring + s * F::kStageBytes;
+                    mbar_expect_tx(&sh.full[s], F::kStageBytes);
+                    const Turned turned = turned_at<F>(at, step.flags, k);
+                    copy_rows<128>(to, left, row, k, at.k, turned.left, &sh.full[s]);
+                    copy_rows<F::kRightRows>(to + kBlockBytes, right, col, k,
+                                             step.flags & kRightX ? x.np : at.k, turned.right,
+                                             &sh.full[s]);
                 }
             }
             if (!ok) atomicOr(&g_matrix_status, kStatusProducerTimeout);
@@ -396,12 +412,12 @@ __global__ void __launch_bounds__(Shape<PAIR>::kThreads, 1)
             uint32_t used = 0, n = 0;                     // stages, pieces
             bool ok = true;
             for (uint32_t i = unit; ok && i < tiles; i += units) {
-                const Tile at = tile_at<PAIR>(t, call, i);
+                const Tile at = tile_at<F>(t, call, i);
                 const int flags = call.step[at.step].flags;
                 for (int k0 = 0; ok && k0 < at.k; k0 += kPiece, ++n) {
-                    const uint32_t d = tmem + n % 2 * kTile;
+                    const uint32_t d = tmem + n % 2 * F::kCols;
                     if (n >= 2) {
-                        ok = PAIR ? mbar_wait_pair(&sh.taken[n % 2], (n / 2 - 1) & 1, limit_ns)
+                        ok = kPair ? mbar_wait_pair(&sh.taken[n % 2], (n / 2 - 1) & 1, limit_ns)
                                   : mbar_wait(&sh.taken[n % 2], (n / 2 - 1) & 1, limit_ns);
                         if (!ok) break;
                     }
@@ -410,15 +426,15 @@ __global__ void __launch_bounds__(Shape<PAIR>::kThreads, 1)
                     for (int k = k0; k < end; k += 64, ++used) {
                         const uint32_t s = used % kStages;
                         ok = mbar_wait(&sh.full[s], (used / kStages) & 1, limit_ns);
-                        if (PAIR && ok)
+                        if (kPair && ok)
                             ok = mbar_wait_pair(&sh.peer[s], (used / kStages) & 1, limit_ns);
                         if (!ok) break;
                         tmem_fence_after();
-                        const uint32_t a = smem_addr(ring + s * kStageBytes);
+                        const uint32_t a = smem_addr(ring + s * F::kStageBytes);
                         const uint32_t b = a + kBlockBytes;
-                        const Turned turned = turned_at<PAIR>(at, flags, k);
+                        const Turned turned = turned_at<F>(at, flags, k);
                         const uint32_t form =
-                            half_product(kTile, kTile, turned.left, turned.right);
+                            half_product(F::kRows, F::kCols, turned.left, turned.right);
                         // 16 k are 32 bytes along the rows, or 16 rows of 128 bytes
                         uint64_t ah = turned.left ? mn_major(a, 8192) : k_major(a);
                         uint64_t bh = turned.right ? mn_major(b, 8192) : k_major(b);
@@ -427,18 +443,18 @@ __global__ void __launch_bounds__(Shape<PAIR>::kThreads, 1)
 #pragma unroll
                         for (int q = 0; q < 4; ++q, ah += next_a, bh += next_b) {
                             const uint64_t al = ah + kBlockBytes / 2 / 16;
-                            const uint64_t bl = bh + kBlockBytes / 2 / 16;
-                            mma_half<PAIR>(d, ah, bh, form, k > k0 || q > 0);
-                            mma_half<PAIR>(d, ah, bl, form, true);
-                            mma_half<PAIR>(d, al, bh, form, true);
+                            const uint64_t bl = bh + F::kRightHalf / 16;
+                            mma_half<kPair>(d, ah, bh, form, k > k0 || q > 0);
+                            mma_half<kPair>(d, ah, bl, form, true);
+                            mma_half<kPair>(d, al, bh, form, true);
                         }
-                        mma_commit<PAIR>(&sh.empty[s]);
+                        mma_commit<kPair>(&sh.empty[s]);
                     }
-                    if (ok) mma_commit<PAIR>(&sh.done[n % 2]);
+                    if (ok) mma_commit<kPair>(&sh.done[n % 2]);
                 }
             }
             if (!ok) atomicOr(&g_matrix_status, kStatusConsumerTimeout);
-            mma_commit<PAIR>(&sh.drain);    // the products in flight end before their memory goes
+            mma_commit<kPair>(&sh.drain);    // the products in flight end before their memory goes
             if (!mbar_wait(&sh.drain, 0, kDrainNs))
                 atomicOr(&g_matrix_status, kStatusDrainTimeout);
         }
@@ -447,7 +463,7 @@ __global__ void __launch_bounds__(Shape<PAIR>::kThreads, 1)
             uint32_t used = 0;
             bool ok = true;
             for (uint32_t i = unit; ok && i < tiles; i += units) {
-                const Tile at = tile_at<PAIR>(t, call, i);
+                const Tile at = tile_at<F>(t, call, i);
                 for (int k = 0; k < at.k; k += 64, ++used) {
                     const uint32_t s = used % kStages;
                     ok = mbar_wait(&sh.full[s], (used / kStages) & 1, limit_ns);
@@ -466,7 +482,7 @@ __global__ void __launch_bounds__(Shape<PAIR>::kThreads, 1)
             // the quarter of the lanes that this warp may read, and its columns
             my.lanes = tmem + (static_cast<uint32_t>(warp % 4 * 32) << 16) +
                        (warp - 2) / 4 * F::kColumns;
-            my.out = smem_addr(ring) + kStages * kStageBytes + (warp - 2) * kOutPiece;
+            my.out = smem_addr(ring) + kRingBytes + (warp - 2) * kOutPiece;
             my.down = 128 * rank + warp % 4 * 32;
             my.across = (warp - 2) / 4 * F::kColumns;
             my.index = unit;
@@ -480,7 +496,7 @@ __global__ void __launch_bounds__(Shape<PAIR>::kThreads, 1)
             __syncwarp();                                // all have read what lane 0 moves on
             if (!more) break;
             if (lane == 0) {
-                const Tile next = tile_at<PAIR>(t, call, my.index);
+                const Tile next = tile_at<F>(t, call, my.index);
                 my.tile.matrix = next.matrix;
                 my.tile.step = next.step;
                 my.tile.row = next.row + my.down;        // this warp's
@@ -502,7 +518,7 @@ __global__ void __launch_bounds__(Shape<PAIR>::kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < F::kColumns; c += 8) {
                     uint32_t acc[8];
-                    tmem_load8(my.lanes + n % 2 * kTile + c, acc);
+                    tmem_load8(my.lanes + n % 2 * F::kCols + c, acc);
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
                         sum[c + k] = __float_as_uint(__uint_as_float(sum[c + k]) +
@@ -511,7 +527,7 @@ __global__ void __launch_bounds__(Shape<PAIR>::kThreads, 1)
                 tmem_fence_before();
                 __syncwarp();
                 if (lane == 0) {                         // the next products may come
-                    if constexpr (PAIR) arrive_at_first(&sh.taken[n % 2]);
+                    if constexpr (kPair) arrive_at_first(&sh.taken[n % 2]);
                     else mbar_arrive(&sh.taken[n % 2]);
                 }
             }
@@ -558,11 +574,11 @@ __global__ void __launch_bounds__(Shape<PAIR>::kThreads, 1)
     }
     tmem_fence_before();
     __syncwarp();
-    if constexpr (PAIR) pair_sync();
+    if constexpr (kPair) pair_sync();
     else __syncthreads();
     if (warp == 1) {
         tmem_fence_after();
-        tmem_free<PAIR, F::kTmemColumns>(tmem);
+        tmem_free<kPair, F::kTmemColumns>(tmem);
     }
 }
 
@@ -627,17 +643,53 @@ __global__ void __launch_bounds__(256) matrix_moments(const __grid_constant__ Ma
     x.part[part] = s;
 }
 
-// X's image: a block of it per thread block.
+// X's image: a block of it per thread block.  All loads go out before the norm is
+// added up from its parts.
 template <int T>
 __global__ void __launch_bounds__(256) matrix_image(const __grid_constant__ MatrixTable t,
                                                     const __grid_constant__ MatrixCall call) {
     using S = typename Elem<T>::Store;
     __shared__ double warp_sum[8];
+    __shared__ uint4 out[kBlockBytes / 16];
     pdl_enter();
     if (skip_step(call.skip)) return;
     const int k = find(t.image0, t.count, blockIdx.x);
     const MatrixItem& x = t.item[k];
     const MatrixGroup& g = call.group[x.group];
+    const float coef = call.coef != nullptr ? __ldg(call.coef) : 1.0f;
+    const S* grad = static_cast<const S*>(x.grad);
+    const int block = blockIdx.x - t.image0[k], wide = x.np / 64;
+    const int row0 = block / wide * 128, col0 = block % wide * 64;
+    const bool whole = x.flat && !x.tall && x.n % 8 == 0;   // eight columns are one vector
+    float u[4][8];
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        // eight columns of a row; consecutive threads along what memory has in a row
+        const int q = p * 256 + threadIdx.x;
+        const int row = row0 + (x.tall ? q % 128 : q / 8);
+        const int col = col0 + (x.tall ? q / 128 * 8 : q % 8 * 8);
+        float m[8] = {};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[p][j] = 0.0f;
+        if (whole) {
+            if (row < x.m && col < x.n) {
+                const int64_t i = static_cast<int64_t>(row) * x.n + col;
+                load_elems<T, 8>(grad + i, u[p]);
+                if (x.m_buf != nullptr) load_elems<kGradF32, 8>(x.m_buf + i, m);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (row >= x.m || col + j >= x.n) continue;
+                const int64_t i = x.tall ? static_cast<int64_t>(col + j) * x.m + row
+                                         : static_cast<int64_t>(row) * x.n + col + j;
+                u[p][j] = elem_to_f32<T>(grad[i]);
+                if (x.m_buf != nullptr) m[j] = x.m_buf[i];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[p][j] = update_of(x, g, coef, u[p][j], m[j]);
+    }
     const int parts = t.part0[k + 1] - t.part0[k];
     double s = threadIdx.x < parts ? x.part[threadIdx.x] : 0.0;
 #pragma unroll
@@ -647,77 +699,58 @@ __global__ void __launch_bounds__(256) matrix_image(const __grid_constant__ Matr
     s = 0.0;
     for (int w = 0; w < 8; ++w) s += warp_sum[w];
     // a sum that is not finite leaves nothing finite
-    const float scale = s <= 1.7976931348623157e308
-                            ? static_cast<float>(kImageScaleX / (sqrt(s) + call.eps))
-                            : __int_as_float(0x7FFFFFFF);
-    const float coef = call.coef != nullptr ? __ldg(call.coef) : 1.0f;
-    const S* grad = static_cast<const S*>(x.grad);
-    const int block = blockIdx.x - t.image0[k], wide = x.np / 64;
-    const int row0 = block / wide * 128, col0 = block % wide * 64;
-    char* to = static_cast<char*>(x.image[kX0]) + static_cast<int64_t>(block) * kBlockBytes;
-    const bool whole = x.flat && !x.tall && x.n % 8 == 0;   // eight columns are one vector
+    const bool finite = s <= 1.7976931348623157e308;
+    const float scale = finite ? static_cast<float>(kImageScaleX / (sqrt(s) + call.eps))
+                               : __int_as_float(0x7FFFFFFF);
 #pragma unroll
-    for (int q = threadIdx.x; q < 1024; q += 256) {
-        // eight columns of a row; consecutive threads along what memory has in a row
+    for (int p = 0; p < 4; ++p) {
+        const int q = p * 256 + threadIdx.x;
         const int r = x.tall ? q % 128 : q / 8, c = x.tall ? q / 128 * 8 : q % 8 * 8;
-        const int row = row0 + r, col = col0 + c;
-        float v[8] = {}, m[8] = {};
-        if (whole) {
-            if (row < x.m && col < x.n) {
-                const int64_t i = static_cast<int64_t>(row) * x.n + col;
-                load_elems<T, 8>(grad + i, v);
-                if (x.m_buf != nullptr) load_elems<kGradF32, 8>(x.m_buf + i, m);
-            }
-        } else {
+        float v[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (row >= x.m || col + j >= x.n) continue;
-                const int64_t i = x.tall ? static_cast<int64_t>(col + j) * x.m + row
-                                         : static_cast<int64_t>(row) * x.n + col + j;
-                v[j] = elem_to_f32<T>(grad[i]);
-                if (x.m_buf != nullptr) m[j] = x.m_buf[i];
-            }
-        }
-        if (row < x.m) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                v[j] = col + j < x.n ? scale * update_of(x, g, coef, v[j], m[j]) : 0.0f;
-        }
+        for (int j = 0; j < 8; ++j)       // padding stays zero whatever the scale is
+            v[j] = row0 + r < x.m && col0 + c + j < x.n ? scale * u[p][j] : 0.0f;
         uint4 hi, lo;
         split_pair(v[0], v[1], &hi.x, &lo.x);
         split_pair(v[2], v[3], &hi.y, &lo.y);
         split_pair(v[4], v[5], &hi.z, &lo.z);
         split_pair(v[6], v[7], &hi.w, &lo.w);
-        char* p = to + swizzled(r, c);
-        *reinterpret_cast<uint4*>(p) = hi;
-        *reinterpret_cast<uint4*>(p + kBlockBytes / 2) = lo;
+        const int at = swizzled(r, c) / 16;
+        out[at] = hi;
+        out[kBlockBytes / 32 + at] = lo;
     }
+    __syncthreads();
+    // on in the image's order: a tall matrix's threads hold 16 bytes of a row each
+    uint4* to = reinterpret_cast<uint4*>(static_cast<char*>(x.image[kX0]) +
+                                         static_cast<int64_t>(block) * kBlockBytes);
+#pragma unroll
+    for (int q = 0; q < kBlockBytes / 16; q += 256) to[q + threadIdx.x] = out[q + threadIdx.x];
 }
 
 // Blocks of the rounds' kernel that can be resident at once, by device.
-template <bool PAIR>
+template <class F>
 int resident_units() {
     static std::atomic<int> cache[256];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 256) return 0;
     int v = cache[dev].load(std::memory_order_relaxed);
     if (v > 0) return v;
-    if (cudaFuncSetAttribute(matrix_rounds<PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Shape<PAIR>::kDynamicBytes) != cudaSuccess)
+    if (cudaFuncSetAttribute(matrix_rounds<F>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             F::kDynamicBytes) != cudaSuccess)
         return 0;
     v = device_sms();
-    if constexpr (PAIR) {
+    if constexpr (F::kPair) {
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim = {2, 1, 1};
         cfg.gridDim = dim3(static_cast<unsigned>(v / 2 * 2));
-        cfg.blockDim = dim3(Shape<PAIR>::kThreads);
-        cfg.dynamicSmemBytes = Shape<PAIR>::kDynamicBytes;
+        cfg.blockDim = dim3(F::kThreads);
+        cfg.dynamicSmemBytes = F::kDynamicBytes;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         int clusters = 0;
-        if (cudaOccupancyMaxActiveClusters(&clusters, matrix_rounds<PAIR>, &cfg) != cudaSuccess)
+        if (cudaOccupancyMaxActiveClusters(&clusters, matrix_rounds<F>, &cfg) != cudaSuccess)
             return 0;
         v = clusters < v / 2 ? clusters : v / 2;
     }
@@ -725,10 +758,10 @@ int resident_units() {
     return v;
 }
 
-template <bool PAIR>
+template <class F>
 cudaError_t go_rounds(const MatrixTable& t, const MatrixCall& c, cudaStream_t stream) {
     const uint32_t most = c.most;
-    const int fit = resident_units<PAIR>();
+    const int fit = resident_units<F>();
     if (fit < 1) return cudaErrorLaunchOutOfResources;
     const uint32_t units = most < static_cast<uint32_t>(fit) ? most : static_cast<uint32_t>(fit);
     cudaLaunchConfig_t cfg = {};
@@ -737,13 +770,13 @@ cudaError_t go_rounds(const MatrixTable& t, const MatrixCall& c, cudaStream_t st
     attr[0].val.cooperative = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim = {2, 1, 1};
-    cfg.gridDim = dim3(units * Shape<PAIR>::kBlocks);
-    cfg.blockDim = dim3(Shape<PAIR>::kThreads);
-    cfg.dynamicSmemBytes = Shape<PAIR>::kDynamicBytes;
+    cfg.gridDim = dim3(units * F::kBlocks);
+    cfg.blockDim = dim3(F::kThreads);
+    cfg.dynamicSmemBytes = F::kDynamicBytes;
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = PAIR ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, matrix_rounds<PAIR>, t, c, tma_wait_limit());
+    cfg.numAttrs = F::kPair ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, matrix_rounds<F>, t, c, tma_wait_limit());
     note_launch();
     return e;
 }
@@ -771,7 +804,9 @@ cudaError_t launch_matrices(const MatrixTable& t, const MatrixCall& c, int grad_
         return second;
     });
     if (e != cudaSuccess) return e;
-    return t.pair ? go_rounds<true>(t, c, stream) : go_rounds<false>(t, c, stream);
+    return t.shape == 2   ? go_rounds<Shape<256, 256>>(t, c, stream)
+           : t.shape == 1 ? go_rounds<Shape<128, 128>>(t, c, stream)
+                          : go_rounds<Shape<128, 64>>(t, c, stream);
 }
 
 }  // namespace shardstep

@@ -235,14 +235,16 @@ void plan_steps(MatrixCall* call, bool segments) {
     }
 }
 
+constexpr double kTileCost[3] = {0.95, 1.0, 1.6}, kLevelCost[3] = {11.5, 13, 18};
 // About how long the steps take, in units of 64 k of a 128 x 128 tile (0.49 us; a
 // 256 x 256 tile takes a pair 0.79 us: it copies half as much per product).  A level of
 // steps takes its longest tile and 7 us from the last results to the next products, or
 // the tiles' share per SM.  So the larger tile is taken where there are enough of them
 // for all pairs (12 matrices of 1024 x 1024 take 671 us with it and 770 with the
 // smaller one, one of them 376 and 264), and segments for long matrices.
-double steps_cost(const MatrixTable& t, const MatrixCall& call, int64_t tile, int units) {
-    const double each = tile == 256 ? 1.6 : 1.0;
+double steps_cost(const MatrixTable& t, const MatrixCall& call, int shape, int sms) {
+    const int64_t high = kMatrixTiles[shape][0], wide = kMatrixTiles[shape][1];
+    const double each = kTileCost[shape], units = static_cast<double>(sms / (high / 128));
     double total = 0.0;
     for (int s = 0; s < call.steps;) {
         double work = 0.0, longest = 0.0;
@@ -250,15 +252,16 @@ double steps_cost(const MatrixTable& t, const MatrixCall& call, int64_t tile, in
         for (; s < call.steps && call.step[s].sym_before + call.step[s].full_before == level; ++s) {
             const int flags = call.step[s].flags;
             for (int j = 0; j < t.count; ++j) {
-                const double side = static_cast<double>(padded(t.item[j].m, tile) / tile);
-                const double wide = static_cast<double>(padded(t.item[j].n, tile) / tile);
-                const double k = each * (flags & kLeftX ? wide : side) *
-                                 static_cast<double>(tile / 64);
-                work += k * (flags & kSymmetric ? side * (side + 1) / 2 : side * wide);
+                const int64_t mp = padded(t.item[j].m, high), np = padded(t.item[j].n, wide);
+                const double side = static_cast<double>(mp / high);
+                const double k = each * static_cast<double>((flags & kLeftX ? np : mp) / 64);
+                work += k * (flags & kSymmetric
+                                 ? side * (side + 1) / 2 * static_cast<double>(high / wide)
+                                 : side * static_cast<double>(np / wide));
                 longest = std::max(longest, k);
             }
         }
-        total += std::max(work / units + longest / 3, longest + (tile == 256 ? 18 : 14));
+        total += std::max(work / units + longest / 3, longest + kLevelCost[shape]);
     }
     return total;
 }
@@ -270,16 +273,16 @@ void lay_out(MatrixTable* t, MatrixCall* call, char* ws) {
     bool segments = false;
     for (const bool split : {false, true}) {
         plan_steps(call, split);
-        for (const int pair : {0, 1}) {
-            const double cost = steps_cost(*t, *call, pair ? 256 : 128, pair ? sms / 2 : sms);
-            if ((split || pair) && cost >= best) continue;
+        for (int shape = 0; shape < 3; ++shape) {
+            const double cost = steps_cost(*t, *call, shape, sms);
+            if ((split || shape) && cost >= best) continue;
             best = cost;
             segments = split;
-            t->pair = pair;
+            t->shape = shape;
         }
     }
     plan_steps(call, segments);
-    const int64_t tile = t->pair ? 256 : 128;
+    const int64_t high = kMatrixTiles[t->shape][0], across = kMatrixTiles[t->shape][1];
     // the longest tiles first, so that the last ones to end are short
     std::sort(t->item, t->item + t->count, [](const MatrixItem& a, const MatrixItem& b) {
         return a.m != b.m ? a.m > b.m : a.n > b.n;
@@ -287,8 +290,8 @@ void lay_out(MatrixTable* t, MatrixCall* call, char* ws) {
     uint32_t sym = 0, full = 0, part = 0, image = 0;
     for (int j = 0; j < t->count; ++j) {
         MatrixItem& x = t->item[j];
-        x.mp = static_cast<int32_t>(padded(x.m, tile));
-        x.np = static_cast<int32_t>(padded(x.n, tile));
+        x.mp = static_cast<int32_t>(padded(x.m, high));
+        x.np = static_cast<int32_t>(padded(x.n, across));
         const int64_t wide = 4 * static_cast<int64_t>(x.mp) * x.np;
         const int64_t square = 4 * static_cast<int64_t>(x.mp) * x.mp;
         x.image[kX0] = ws;
@@ -301,9 +304,9 @@ void lay_out(MatrixTable* t, MatrixCall* call, char* ws) {
         t->full0[j] = full;
         t->part0[j] = part;
         t->image0[j] = image;
-        const uint32_t side = static_cast<uint32_t>(x.mp / tile);
-        sym += side * (side + 1) / 2;
-        full += side * static_cast<uint32_t>(x.np / tile);
+        const uint32_t side = static_cast<uint32_t>(x.mp / high);
+        sym += side * (side + 1) / 2 * static_cast<uint32_t>(high / across);
+        full += side * static_cast<uint32_t>(x.np / across);
         part += static_cast<uint32_t>(std::min<int64_t>(
             kMatrixParts, (static_cast<int64_t>(x.m) * x.n + 4095) / 4096));
         image += static_cast<uint32_t>(x.mp / 128) * (x.np / 64);
