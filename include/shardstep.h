@@ -949,13 +949,13 @@ int token_embedding(const void* table, int64_t table_stride, int32_t dtype, int6
                     int64_t dim, const void* ids, int32_t id_bytes, int64_t n, float scale,
                     void* out, int64_t out_stride, void* stream);
 
-/* token_embedding_grad -- device, two launches (three where a workspace chunk of
- * sorted tokens does not hold them all).
+/* token_embedding_grad -- device, three launches (two for up to 8 tokens).
  *     grad[v] = scale * sum over i with ids[i] = v of d_out[i]
  * added to grad's rows with accumulate != 0 (rows that do not occur are not
  * touched), else written to all of them.  Tokens are sorted by id and summed in
  * fp32 in their order, in chunks whose length goes by n and dim alone: equal
  * calls give equal bits.  Tokens with an id outside [0, vocab) are not read.
+ *   n, vocab and dim as above; n dim below some 2^40.
  *   workspace  device, 16-byte aligned, token_embedding_grad_workspace_bytes(n,
  *              vocab, dim) bytes (-1 for arguments out of range); any contents,
  *              but calls that may run at the same time need workspaces of their own.
@@ -972,14 +972,14 @@ int token_embedding_grad(const void* d_out, int64_t d_out_stride, int32_t dtype,
  *   x, out        device, rows of cols elements of dtype.
  *   weight, bias  device, cols of weight_dtype (dtype or F32), or NULL (1, 0).
  *   mean, rstd    device, rows fp32, written.
- *   rows >= 0, 1 <= cols <= 2^24, eps >= 0 and finite.
+ *   0 <= rows <= 2^32, 1 <= cols <= 2^24, eps >= 0 and finite.
  * Errors: INVALID, CUDA. */
 int rows_layer_norm(const void* x, int64_t x_stride, int32_t dtype, int64_t rows, int64_t cols,
                     const void* weight, const void* bias, int32_t weight_dtype, float eps,
                     void* out, int64_t out_stride, float* mean, float* rstd, void* stream);
 
 /* rows_layer_norm_grad -- device, two launches (one without d_weight and d_bias;
- * three for rows wider than registers hold).  With xh = (x - mean) rstd and
+ * three for rows of over 8192 columns, or 4096 where rows are not 16-byte aligned).  With xh = (x - mean) rstd and
  * g = d_out weight:
  *     d_x = rstd (g - mean(g) - xh mean(g xh))
  *     d_weight = sum over rows of d_out xh,   d_bias = sum over rows of d_out
@@ -1005,8 +1005,10 @@ int rows_layer_norm_grad(const void* d_out, int64_t d_out_stride, const void* x,
  * The singular values of the result are those of X under s -> a s + b s^3 + c s^5,
  * `rounds` times; the usual (3.4445, -4.7750, 2.0315), 5 times, brings all but the
  * smallest to between 0.7 and 1.2.  Products are formed on the tensor cores from
- * values held as two halves each (22 bits): single precision.  A gradient that
- * holds an inf or NaN (or whose square passes fp32's range) gives NaNs.
+ * values held as two halves each (22 bits): single precision.  For long matrices two
+ * or three rounds are taken together, which forms the same polynomial in fewer
+ * operations.  A matrix that holds an inf or NaN (or an element whose square passes
+ * fp32's range) gives NaNs; eps 0 gives NaNs for a matrix of zeros.
  *   rounds        1..64.
  *   a, b, c       such that, of the singular values s that [0, 1] leads to, none
  *                 passes 1.39 in any round, |b + c s^2| stays below 7.9 and
@@ -1017,8 +1019,9 @@ typedef struct {
     int32_t pad_;
 } shardstep_quintic_t;
 
-/* matrices_orthogonalize -- device, two launches and three a round for each group
- * of up to 64 matrices (up to 2 GB of workspace, or one matrix).
+/* matrices_orthogonalize -- device, three launches for each group of up to 64
+ * matrices (up to 2 GB of workspace, or one matrix); the third is cooperative, one
+ * block per SM.
  *   in[n], out[n]      host arrays of device pointers: contiguous matrices of
  *                      rows[i] x cols[i] elements of in_dtype and out_dtype.
  *   rows, cols         0..2^20; a matrix without elements is left out.

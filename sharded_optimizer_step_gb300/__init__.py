@@ -1591,8 +1591,7 @@ def orthogonalize(matrices, out=None, *, rounds: int = 5, coefficients=QUINTIC,
                   eps: float = 1e-7, workspace=None, stream=None):
     """The Newton-Schulz orthogonalisation of each of ``matrices`` (a tensor, a list
     or a ``TensorList`` of contiguous matrices of one dtype: bf16, fp16 or fp32), all
-    of them together in two launches and three a round (per 64 matrices or 2 GB of
-    workspace):
+    of them together in three launches (per 64 matrices or 2 GB of workspace):
 
         X = u / (|u| + eps), transposed if taller than wide
         A = X X^T,  X = a X + (b A + c A A) X      ``rounds`` times

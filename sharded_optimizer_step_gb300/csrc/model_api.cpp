@@ -1,6 +1,7 @@
 // Host side of the embedding (token_embedding*), layer norm (rows_layer_norm*)
 // and the matrices' updates (matrices_*, tensors_muon_step): argument checks, the
-// tables that travel with each launch, and dispatch.  Nothing here allocates
+// products that make up the rounds, the tables that travel with each launch, and
+// dispatch.  Nothing here allocates
 // device memory or keeps a pointer.
 #include <algorithm>
 #include <cmath>
@@ -444,6 +445,9 @@ int token_embedding_grad(const void* d_out, int64_t d_out_stride, int32_t dtype,
     s.piece = reinterpret_cast<float*>(ws + round16(4 * (vocab + 1)));
     s.chunk = plan.chunk;
     s.chunks = plan.chunks;
+    // blocks of the sums, if every slice is of 256 single columns, and of the zeros
+    if (plan.chunks * ((dim + 255) / 256) + vocab / kEmbedZeroRows + 1 > INT32_MAX)
+        return ready_fail(SHARDSTEP_ERR_INVALID, "n x dim or vocab too large for one launch");
     // a vector of d_out stands over as many elements of grad
     const int per = 16 / es;
     const int at_grad = std::min(16, per * gs);
@@ -467,7 +471,7 @@ int rows_layer_norm(const void* x, int64_t x_stride, int32_t dtype, int64_t rows
     if (es == 0) return ready_fail(SHARDSTEP_ERR_INVALID, "unknown dtype %d", dtype);
     if (weight_dtype != dtype && weight_dtype != SHARDSTEP_DTYPE_F32)
         return ready_fail(SHARDSTEP_ERR_INVALID, "weight_dtype must be dtype or fp32");
-    if (rows < 0 || rows > (int64_t{1} << 40) || cols < 1 || cols > (int64_t{1} << 24))
+    if (rows < 0 || rows > (int64_t{1} << 32) || cols < 1 || cols > (int64_t{1} << 24))
         return ready_fail(SHARDSTEP_ERR_INVALID, "rows or cols out of range");
     if (!(eps >= 0.0f) || !std::isfinite(eps))
         return ready_fail(SHARDSTEP_ERR_INVALID, "eps must be finite and >= 0");
@@ -514,7 +518,7 @@ int rows_layer_norm_grad(const void* d_out, int64_t d_out_stride, const void* x,
     if (es == 0) return ready_fail(SHARDSTEP_ERR_INVALID, "unknown dtype %d", dtype);
     if (weight_dtype != dtype && weight_dtype != SHARDSTEP_DTYPE_F32)
         return ready_fail(SHARDSTEP_ERR_INVALID, "weight_dtype must be dtype or fp32");
-    if (rows < 0 || rows > (int64_t{1} << 40) || cols < 1 || cols > (int64_t{1} << 24))
+    if (rows < 0 || rows > (int64_t{1} << 32) || cols < 1 || cols > (int64_t{1} << 24))
         return ready_fail(SHARDSTEP_ERR_INVALID, "rows or cols out of range");
     if (!stride_ok(x_stride, rows, cols) || !stride_ok(d_out_stride, rows, cols) ||
         (d_x && !stride_ok(d_x_stride, rows, cols)))
