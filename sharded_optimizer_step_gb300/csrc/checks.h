@@ -59,4 +59,31 @@ inline int check_ranges(std::vector<Range>* reads, std::vector<Range>* writes) {
     return SHARDSTEP_OK;
 }
 
+
+// The ranges of a call with a few arrays, without allocations.
+struct FewRanges {
+    Range r[16];
+    int n = 0;
+    void add(const void* p, int64_t bytes) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+        if (bytes > 0) r[n++] = Range{a, a + static_cast<uintptr_t>(bytes)};
+    }
+};
+inline int check_ranges(const FewRanges& reads, const FewRanges& writes) {
+    for (int w = 0; w < writes.n; ++w) {
+        const auto shares = [&](const Range& o) {
+            return o.lo < writes.r[w].hi && writes.r[w].lo < o.hi;
+        };
+        for (int k = 0; k < w; ++k)
+            if (shares(writes.r[k]))
+                return ready_fail(SHARDSTEP_ERR_INVALID,
+                                  "an output overlaps an input or another output");
+        for (int k = 0; k < reads.n; ++k)
+            if (shares(reads.r[k]))
+                return ready_fail(SHARDSTEP_ERR_INVALID,
+                                  "an output overlaps an input or another output");
+    }
+    return SHARDSTEP_OK;
+}
+
 }  // namespace shardstep

@@ -1,28 +1,44 @@
 // Orthogonalised updates of matrices: the Newton-Schulz quintic iteration
 //
 //   X = u / (|u| + eps)            (transposed where u is taller than wide)
-//   A = X X^T,  B = b A + c A A,   X = a X + B X     `rounds` times
+//   A = X X^T,  X = (a + b A + c A A) X             `rounds` times
 //
-// over a list of matrices, as such or as an optimizer's step.  A and B are
-// symmetric, so the first two products of a round compute the tiles on and above
-// the diagonal and write each off-diagonal one to both places.
+// over a list of matrices, as such or as an optimizer's step: the momentum and the
+// norms (matrix_moments), X's image (matrix_image), and all products of all rounds in
+// one launch (matrix_rounds), the last of which steps the weights.
 //
-// The tensor cores multiply halves; to keep single precision each value v is
-// held as two, hi = half(s v) and lo = half(s v - hi) with s a power of two: 22
-// bits, of which three products hi hi + hi lo + lo hi make a product good to
-// about 2^-21 (one product of single halves loses 2e-3 to 2e-2 of the result
-// over five rounds, these three 1e-6).  s is 2^15 for X and A, whose elements
+// Products.  A round forms A, then P = a + A C with C = b + c A written beside A, then
+// P X; no result needs another image than its own operands (a result warp's loads
+// would stand at the end of every step: they took 6 of its 12 us).  Everything but X
+// is symmetric: its products compute the tiles on and above the diagonal, and where an
+// operand lies below it, the tile from above is read the other way round.  Rounds of
+// long matrices go three or two at a time without forming X between them (plan_steps
+// in model_api.cpp).
+//
+// The tensor cores multiply halves; to keep single precision each value v is held as
+// two, hi = half(s v) and lo = half(s v - hi) with s a power of two: 22 bits, of which
+// three products hi hi + hi lo + lo hi make a product good to about 2^-21.  One product
+// of single halves loses 2e-3 to 2e-2 of the result's norm over five rounds, these three
+// 4e-6 to 1e-5, as much as 32-bit products do.  s is 2^15 for X and A, whose elements
 // stay below sqrt(2) and 2, 2^13 for C, below 8, and 2^14 for P, below 4 (the host
-// checks the coefficients for it): nothing overflows, and an element of rms 1 / sqrt(m n),
-// the smallest that occurs throughout, still has its 22 bits at m n = 2^30.
+// checks the coefficients for it): nothing overflows, and an element of rms
+// 1 / sqrt(m n), the smallest that occurs throughout, has its 22 bits up to m n = 2^30.
 //
-// Layout.  All operands live in the workspace as the images of what shared
-// memory holds: blocks of 128 rows x 64 columns, 16 KB of hi then 16 KB of lo,
-// rows of 128 bytes in the tensor cores' 128-byte swizzle.  A tile's operands
-// are then whole contiguous pieces, copied by bulk copies without a tensor map,
-// and one block serves both as rows of k (X and A times their transposes) and
-// as k rows (X behind B).  Both sides are padded to 128 with zeros, which the
-// products keep zero.
+// What bounds it: three products of halves each, 1718 TFLOP/s of them sustained, so 573
+// of the results' own; and the operands, which come from L2 (a 256 x 256 tile's 128 KB
+// in 0.79 us, 12 TB/s over all SMs).  Eight matrices of 2048 x 2048 run at 508 (2.71 ms),
+// 14 of a Llama-1B layer pair at 613 counted round by round (7.7 ms: segments do less).
+// A few small matrices are bound by their chain of 15 to 17 steps, 6 to 8 us each beside
+// the products: 0.75 for the first operands, 0.3 to read the sums, 1 to 2 to turn them
+// into halves, 0.9 for the stores to be seen, 1.5 until another SM knows (256 x 256:
+// 106 us).
+//
+// Layout.  All operands live in the workspace as the images of what shared memory
+// holds: blocks of 128 rows x 64 columns, 16 KB of hi then 16 KB of lo, rows of 128
+// bytes in the tensor cores' 128-byte swizzle.  A tile's operands are then whole
+// contiguous pieces, copied by bulk copies without a tensor map, and one block serves
+// both as rows of k and as k rows.  Both sides are padded to the tile with zeros, which
+// the products keep zero in X.
 #include <atomic>
 
 #include "elem.cuh"
@@ -43,6 +59,7 @@ constexpr int kOutPiece = 2048;
 // bit.  A sum over k therefore goes in pieces of this many, which the result warps
 // add up in their registers (rounding to nearest).
 constexpr int kPiece = 256;
+
 // A tile of results: 128 x 128 by one block, 128 x 64 where tiles are few (a step's
 // time is then its last tile's), or 256 x 256 by a pair of blocks, which copies half as
 // much for a product.  Each block has 128 rows of it, and for each quarter of them two

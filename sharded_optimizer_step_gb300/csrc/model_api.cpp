@@ -366,18 +366,18 @@ extern "C" {
 
 int token_embedding(const void* table, int64_t table_stride, int32_t dtype, int64_t vocab,
                     int64_t dim, const void* ids, int32_t id_bytes, int64_t n, float scale,
-                    void* out, int64_t out_stride, void* stream) try {
+                    void* out, int64_t out_stride, void* stream) {
     const int es = elem_size(dtype);
     if (int rc = check_embedding(table, table_stride, vocab, dim, ids, id_bytes, n, scale, out,
                                  out_stride, es, es);
         rc != SHARDSTEP_OK)
         return rc;
     if (n == 0) return ready_ok();
-    std::vector<Range> reads, writes;
-    add_range(reads, table, span(vocab, dim, table_stride, es));
-    add_range(reads, ids, n * id_bytes);
-    add_range(writes, out, span(n, dim, out_stride, es));
-    if (int rc = check_ranges(&reads, &writes); rc != SHARDSTEP_OK) return rc;
+    FewRanges reads, writes;
+    reads.add(table, span(vocab, dim, table_stride, es));
+    reads.add(ids, n * id_bytes);
+    writes.add(out, span(n, dim, out_stride, es));
+    if (int rc = check_ranges(reads, writes); rc != SHARDSTEP_OK) return rc;
     EmbedArgs a{};
     a.table = const_cast<void*>(table);
     a.table_stride = table_stride;
@@ -395,8 +395,6 @@ int token_embedding(const void* table, int64_t table_stride, int32_t dtype, int6
     if (e != cudaSuccess) return cuda_fail("embedding", e);
     record_kernel("embedding_lookup<%s>", dtype_name(dtype));
     return ready_ok();
-} catch (const std::bad_alloc&) {
-    return ready_fail(SHARDSTEP_ERR_CAPACITY, "out of host memory");
 }
 
 int64_t token_embedding_grad_workspace_bytes(int64_t n, int64_t vocab, int64_t dim) {
@@ -409,7 +407,7 @@ int token_embedding_grad(const void* d_out, int64_t d_out_stride, int32_t dtype,
                          int32_t id_bytes, int64_t n, float scale, void* grad,
                          int64_t grad_stride, int32_t grad_dtype, int64_t vocab, int64_t dim,
                          int32_t accumulate, void* workspace, int64_t workspace_bytes,
-                         void* stream) try {
+                         void* stream) {
     const int es = elem_size(dtype), gs = elem_size(grad_dtype);
     if (int rc = check_embedding(grad, grad_stride, vocab, dim, ids, id_bytes, n, scale, d_out,
                                  d_out_stride, gs, es);
@@ -418,12 +416,12 @@ int token_embedding_grad(const void* d_out, int64_t d_out_stride, int32_t dtype,
     const int64_t need = token_embedding_grad_workspace_bytes(n, vocab, dim);
     if (int rc = check_workspace(workspace, workspace_bytes, need); rc != SHARDSTEP_OK) return rc;
     if (n == 0 && accumulate) return ready_ok();
-    std::vector<Range> reads, writes;
-    add_range(reads, d_out, span(n, dim, d_out_stride, es));
-    add_range(reads, ids, n * id_bytes);
-    add_range(writes, grad, span(vocab, dim, grad_stride, gs));
-    add_range(writes, workspace, need);
-    if (int rc = check_ranges(&reads, &writes); rc != SHARDSTEP_OK) return rc;
+    FewRanges reads, writes;
+    reads.add(d_out, span(n, dim, d_out_stride, es));
+    reads.add(ids, n * id_bytes);
+    writes.add(grad, span(vocab, dim, grad_stride, gs));
+    writes.add(workspace, need);
+    if (int rc = check_ranges(reads, writes); rc != SHARDSTEP_OK) return rc;
     EmbedArgs a{};
     a.table = grad;
     a.table_stride = grad_stride;
@@ -458,15 +456,13 @@ int token_embedding_grad(const void* d_out, int64_t d_out_stride, int32_t dtype,
     if (e != cudaSuccess) return cuda_fail("embedding gradient", e);
     record_kernel("embedding_sum<%s, %s>", dtype_name(dtype), dtype_name(grad_dtype));
     return ready_ok();
-} catch (const std::bad_alloc&) {
-    return ready_fail(SHARDSTEP_ERR_CAPACITY, "out of host memory");
 }
 
 // ------------------------------------------------------------- layer norm
 
 int rows_layer_norm(const void* x, int64_t x_stride, int32_t dtype, int64_t rows, int64_t cols,
                     const void* weight, const void* bias, int32_t weight_dtype, float eps,
-                    void* out, int64_t out_stride, float* mean, float* rstd, void* stream) try {
+                    void* out, int64_t out_stride, float* mean, float* rstd, void* stream) {
     const int es = elem_size(dtype), ws = elem_size(weight_dtype);
     if (es == 0) return ready_fail(SHARDSTEP_ERR_INVALID, "unknown dtype %d", dtype);
     if (weight_dtype != dtype && weight_dtype != SHARDSTEP_DTYPE_F32)
@@ -482,14 +478,14 @@ int rows_layer_norm(const void* x, int64_t x_stride, int32_t dtype, int64_t rows
     if (!aligned(x, es) || !aligned(out, es) || !aligned(weight, ws) || !aligned(bias, ws) ||
         !aligned(mean, 4) || !aligned(rstd, 4))
         return ready_fail(SHARDSTEP_ERR_INVALID, "an array is misaligned");
-    std::vector<Range> reads, writes;
-    add_range(reads, x, span(rows, cols, x_stride, es));
-    add_range(reads, weight, weight ? cols * ws : 0);
-    add_range(reads, bias, bias ? cols * ws : 0);
-    add_range(writes, out, span(rows, cols, out_stride, es));
-    add_range(writes, mean, rows * 4);
-    add_range(writes, rstd, rows * 4);
-    if (int rc = check_ranges(&reads, &writes); rc != SHARDSTEP_OK) return rc;
+    FewRanges reads, writes;
+    reads.add(x, span(rows, cols, x_stride, es));
+    reads.add(weight, weight ? cols * ws : 0);
+    reads.add(bias, bias ? cols * ws : 0);
+    writes.add(out, span(rows, cols, out_stride, es));
+    writes.add(mean, rows * 4);
+    writes.add(rstd, rows * 4);
+    if (int rc = check_ranges(reads, writes); rc != SHARDSTEP_OK) return rc;
     const NormRows a{x, x_stride, out, out_stride, weight, bias, mean, rstd, rows, cols, eps};
     const bool vec = rows_aligned(x, x_stride, rows, es) &&
                      rows_aligned(out, out_stride, rows, es) && aligned(weight, 16) &&
@@ -499,8 +495,6 @@ int rows_layer_norm(const void* x, int64_t x_stride, int32_t dtype, int64_t rows
     if (e != cudaSuccess) return cuda_fail("layer norm", e);
     record_kernel("layer_norm_rows<%s>", dtype_name(dtype));
     return ready_ok();
-} catch (const std::bad_alloc&) {
-    return ready_fail(SHARDSTEP_ERR_CAPACITY, "out of host memory");
 }
 
 int64_t rows_layer_norm_workspace_bytes(int64_t cols) {
@@ -513,7 +507,7 @@ int rows_layer_norm_grad(const void* d_out, int64_t d_out_stride, const void* x,
                          const float* mean, const float* rstd, const void* weight,
                          int32_t weight_dtype, void* d_x, int64_t d_x_stride, void* d_weight,
                          void* d_bias, int32_t accumulate, void* workspace,
-                         int64_t workspace_bytes, void* stream) try {
+                         int64_t workspace_bytes, void* stream) {
     const int es = elem_size(dtype), ws = elem_size(weight_dtype);
     if (es == 0) return ready_fail(SHARDSTEP_ERR_INVALID, "unknown dtype %d", dtype);
     if (weight_dtype != dtype && weight_dtype != SHARDSTEP_DTYPE_F32)
@@ -533,17 +527,17 @@ int rows_layer_norm_grad(const void* d_out, int64_t d_out_stride, const void* x,
     if (int rc = check_workspace(workspace, workspace_bytes, need); rc != SHARDSTEP_OK) return rc;
     if (!columns && (rows == 0 || d_x == nullptr)) return ready_ok();
     if (rows == 0 && accumulate) return ready_ok();
-    std::vector<Range> reads, writes;
-    add_range(reads, x, span(rows, cols, x_stride, es));
-    add_range(reads, d_out, span(rows, cols, d_out_stride, es));
-    add_range(reads, weight, weight ? cols * ws : 0);
-    add_range(reads, mean, rows * 4);
-    add_range(reads, rstd, rows * 4);
-    add_range(writes, d_x, d_x ? span(rows, cols, d_x_stride, es) : 0);
-    add_range(writes, d_weight, d_weight ? cols * ws : 0);
-    add_range(writes, d_bias, d_bias ? cols * ws : 0);
-    add_range(writes, workspace, need);
-    if (int rc = check_ranges(&reads, &writes); rc != SHARDSTEP_OK) return rc;
+    FewRanges reads, writes;
+    reads.add(x, span(rows, cols, x_stride, es));
+    reads.add(d_out, span(rows, cols, d_out_stride, es));
+    reads.add(weight, weight ? cols * ws : 0);
+    reads.add(mean, rows * 4);
+    reads.add(rstd, rows * 4);
+    writes.add(d_x, d_x ? span(rows, cols, d_x_stride, es) : 0);
+    writes.add(d_weight, d_weight ? cols * ws : 0);
+    writes.add(d_bias, d_bias ? cols * ws : 0);
+    writes.add(workspace, need);
+    if (int rc = check_ranges(reads, writes); rc != SHARDSTEP_OK) return rc;
     const NormGradRows a{x,    x_stride, d_out, d_out_stride,
                          d_x,  d_x_stride, weight, mean, rstd,
                          columns ? static_cast<float*>(workspace) : nullptr, rows, cols};
@@ -556,8 +550,6 @@ int rows_layer_norm_grad(const void* d_out, int64_t d_out_stride, const void* x,
     if (e != cudaSuccess) return cuda_fail("layer norm gradient", e);
     record_kernel("layer_norm_rows_grad<%s>", dtype_name(dtype));
     return ready_ok();
-} catch (const std::bad_alloc&) {
-    return ready_fail(SHARDSTEP_ERR_CAPACITY, "out of host memory");
 }
 
 // --------------------------------------------------------------- matrices

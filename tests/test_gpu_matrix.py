@@ -3,15 +3,15 @@ quintic iteration in 64 bits.
 
 A value held as two halves is off by 2^-23 of itself, the product left out
 2^-22, so an element of a product is off by 2^-21 of the sum of its terms'
-magnitudes; the tensor cores' fp32 sums add less than K / 4 steps of 2^-23 of it
-on average signs.  One round multiplies an error by at most the map's steepest
-slope, 3.4445, and X's norm grows by no more, so after five rounds the error is
-at most 5 * 3.4445^5 times a round's own, which is C 2^-21 of |X| <= 1 at the
-start: in norm 2430 * C * 2^-21, C = 8 for the three products' terms: 0.0093.
-That is absolute; the result's norm is about 0.9 sqrt(min side).  What is
-asserted is a tenth of it, 1e-3 (the bound above takes every error to point the same
-way), which one product of single halves misses by far at every size but the
-smallest (2e-3 to 2e-2 of the norm)."""
+magnitudes; the tensor cores cut off their sums of 256 k at the last bit, 48
+times by half a bit of what is there by then, a quarter of the result on average:
+48 / 4 / 2 * 2^-23 = 7e-7 of it, downwards.  A round multiplies the settled
+values' errors by at most 1.7 or so and adds some 6 such products' errors, so
+after five rounds each singular value is off by a few 1e-5 at the worst, the
+result in norm by that times the root of its short side: below 1e-3 for sides up
+to 1024.  That is asserted of the norm of the whole error (1e-3, not of the
+result's norm, which is up to 30); one product of single halves misses it
+by 2e-3 to 2e-2 of the norm.  What is measured is 4e-6 to 1e-5 of the norm."""
 import math
 
 import pytest
