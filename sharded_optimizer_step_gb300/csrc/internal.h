@@ -466,8 +466,8 @@ struct NormGradRows {
     int64_t d_x_stride;
     const void* w;          // or null
     const float *mean, *rstd;
-    float* piece;           // 2 * cols per block, or null: no d_w, d_b
-    int64_t rows, cols;
+    float* piece;           // 2 * pitch per block, or null: no d_w, d_b
+    int64_t rows, cols, pitch;
 };
 // Blocks of the backward pass, each of which leaves one row of column sums; at
 // most kNormPieces.

@@ -86,30 +86,6 @@ __device__ __forceinline__ Group<ALONE> group_of(int size, float2* words) {
     return Group<ALONE>{size, static_cast<int>(threadIdx.x / 32), g * size / 32, g, words, 0};
 }
 
-// The N elements of a row from column c on; those past its end are zeros, and
-// are not read.  TAIL: whether a row may end inside a vector.
-template <int T, int N, bool TAIL>
-__device__ __forceinline__ void load_part(const typename Elem<T>::Store* p, int c, int cols,
-                                          float* f) {
-    if (!TAIL || c + N <= cols) {
-        load_elems<T, N>(p + c, f);
-    } else {
-#pragma unroll
-        for (int j = 0; j < N; ++j) f[j] = c + j < cols ? elem_to_f32<T>(p[c + j]) : 0.0f;
-    }
-}
-template <int T, int N, bool TAIL>
-__device__ __forceinline__ void store_part(typename Elem<T>::Store* p, int c, int cols,
-                                           const float* f) {
-    if (!TAIL || c + N <= cols) {
-        store_elems<T, N>(p + c, f);
-    } else {
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-            if (c + j < cols) p[c + j] = elem_from_f32<T>(f[j]);
-    }
-}
-
 // A row as it is in memory: V vectors of N elements per thread (N 1: elements), and
 // two of its values at a time.
 template <int T, int N>
@@ -138,9 +114,10 @@ __device__ __forceinline__ void load_weights(const void* p, int c, Pair* w) {
     for (int j = 0; j < N / 2; ++j) w[j] = make_pair(f[2 * j], f[2 * j + 1]);
 }
 
-// Rows of whole vectors: kept as they are in memory (16 registers for 32 elements of
-// 16 bits), so that twice as many rows are on their way as with fp32 copies of them.
-template <int T, int TW, bool ALONE>
+// Rows of vectors: kept as they are in memory (16 registers for 32 elements of 16
+// bits), so that twice as many rows are on their way as with fp32 copies of them.
+// TAIL: a row ends inside a vector, whose elements go to the first threads one each.
+template <int T, int TW, bool ALONE, bool TAIL>
 __global__ void __launch_bounds__(kNormThreads, T == kGradF32 ? 1 : 2)
     layer_norm_vectors(const NormRows a, int size) {
     using S = typename Elem<T>::Store;
@@ -150,7 +127,8 @@ __global__ void __launch_bounds__(kNormThreads, T == kGradF32 ? 1 : 2)
     const int t = ALONE ? threadIdx.x : threadIdx.x % 32;
     const int groups = ALONE ? 1 : blockDim.x / 32;
     const float n = static_cast<float>(a.cols);
-    const int cols = static_cast<int>(a.cols);
+    const int cols = static_cast<int>(a.cols) / N * N;           // in whole vectors
+    const bool mine = TAIL && cols + t < static_cast<int>(a.cols);
     pdl_enter();
     const int64_t row = static_cast<int64_t>(blockIdx.x) * groups + g.id;
     if (row >= a.rows) return;   // a whole warp, or no one of the block
@@ -161,7 +139,8 @@ __global__ void __launch_bounds__(kNormThreads, T == kGradF32 ? 1 : 2)
         const int c = (t + k * size) * N;
         raw[k].v = c < cols ? *reinterpret_cast<const uint4*>(x + c) : make_uint4(0, 0, 0, 0);
     }
-    Pair sum = make_pair(0.0f, 0.0f);
+    float end = mine ? elem_to_f32<T>(x[cols + t]) : 0.0f;
+    Pair sum = make_pair(end, 0.0f);
 #pragma unroll
     for (int k = 0; k < V; ++k)
 #pragma unroll
@@ -169,7 +148,8 @@ __global__ void __launch_bounds__(kNormThreads, T == kGradF32 ? 1 : 2)
     // no rounded 1 / n: rows far from 0
     const float mean = __fdiv_rn(g.sum(floats(sum).x + floats(sum).y), n);
     const Pair off = make_pair(-mean, -mean);
-    sum = make_pair(0.0f, 0.0f);
+    if (mine) end -= mean;
+    sum = make_pair(end * end, 0.0f);
 #pragma unroll
     for (int k = 0; k < V; ++k) {
         if ((t + k * size) * N >= cols) continue;
@@ -212,11 +192,17 @@ __global__ void __launch_bounds__(kNormThreads, T == kGradF32 ? 1 : 2)
         }
         store_elems<T, N>(out + c, f);
     }
+    if (!mine) return;
+    using W = typename Elem<TW>::Store;
+    end *= r;
+    if (a.w != nullptr) end *= elem_to_f32<TW>(static_cast<const W*>(a.w)[cols + t]);
+    if (a.b != nullptr) end += elem_to_f32<TW>(static_cast<const W*>(a.b)[cols + t]);
+    out[cols + t] = elem_from_f32<T>(end);
 }
 
-// V vectors of N elements per thread.
-template <int T, int TW, int N, int V, bool TAIL>
-__global__ void __launch_bounds__(kNormThreads) layer_norm_rows(const NormRows a, int size) {
+// Rows that are not aligned: V single elements per thread.
+template <int T, int TW, int V>
+__global__ void __launch_bounds__(kNormThreads) layer_norm_elements(const NormRows a, int size) {
     using S = typename Elem<T>::Store;
     using W = typename Elem<TW>::Store;
     __shared__ float2 words[2 * kNormThreads / 32];
@@ -228,34 +214,21 @@ __global__ void __launch_bounds__(kNormThreads) layer_norm_rows(const NormRows a
     for (int64_t row = static_cast<int64_t>(blockIdx.x) * groups + g.id; row < a.rows;
          row += static_cast<int64_t>(gridDim.x) * groups) {
         const S* x = static_cast<const S*>(a.x) + row * a.x_stride;
-        float f[V][N];
+        float f[V];
         float s = 0.0f;
 #pragma unroll
         for (int k = 0; k < V; ++k) {
-            const int c = (t + k * size) * N;
-            if (c < cols) {
-                load_part<T, N, TAIL>(x, c, cols, f[k]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < N; ++j) f[k][j] = 0.0f;
-            }
+            const int c = t + k * size;
+            f[k] = c < cols ? elem_to_f32<T>(x[c]) : 0.0f;
+            s += f[k];
         }
-#pragma unroll
-        for (int k = 0; k < V; ++k)
-#pragma unroll
-            for (int j = 0; j < N; ++j) s += f[k][j];
         const float mean = __fdiv_rn(g.sum(s), n);   // no rounded 1 / n: rows far from 0
         float q = 0.0f;
 #pragma unroll
         for (int k = 0; k < V; ++k) {
-            const int c = (t + k * size) * N;
-            if (c >= cols) continue;
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                if (TAIL && c + j >= cols) continue;
-                f[k][j] -= mean;
-                q = fmaf(f[k][j], f[k][j], q);
-            }
+            if (t + k * size >= cols) continue;
+            f[k] -= mean;
+            q = fmaf(f[k], f[k], q);
         }
         const float var = __fdiv_rn(g.sum(q), n);
         const float r = __fdiv_rn(1.0f, __fsqrt_rn(var + a.eps));
@@ -266,27 +239,21 @@ __global__ void __launch_bounds__(kNormThreads) layer_norm_rows(const NormRows a
         S* out = static_cast<S*>(a.out) + row * a.out_stride;
 #pragma unroll
         for (int k = 0; k < V; ++k) {
-            const int c = (t + k * size) * N;
+            const int c = t + k * size;
             if (c >= cols) continue;
-            float w[N], b[N];
-            if (a.w != nullptr) load_part<TW, N, TAIL>(static_cast<const W*>(a.w), c, cols, w);
-            if (a.b != nullptr) load_part<TW, N, TAIL>(static_cast<const W*>(a.b), c, cols, b);
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                float y = f[k][j] * r;
-                if (a.w != nullptr) y *= w[j];
-                if (a.b != nullptr) y += b[j];
-                f[k][j] = y;
-            }
-            store_part<T, N, TAIL>(out, c, cols, f[k]);
+            float y = f[k] * r;
+            if (a.w != nullptr) y *= elem_to_f32<TW>(static_cast<const W*>(a.w)[c]);
+            if (a.b != nullptr) y += elem_to_f32<TW>(static_cast<const W*>(a.b)[c]);
+            out[c] = elem_from_f32<T>(y);
         }
     }
 }
 
-// Backward.  Dynamic shared memory: the groups' column sums, where a block has
+// Its backward pass.  Dynamic shared memory: the groups' column sums, where a block has
 // more than one group.
-template <int T, int TW, int N, int V, bool TAIL, int THREADS>
-__global__ void __launch_bounds__(THREADS) layer_norm_rows_grad(const NormGradRows a, int size) {
+template <int T, int TW, int V>
+__global__ void __launch_bounds__(kNormThreads)
+    layer_norm_elements_grad(const NormGradRows a, int size) {
     using S = typename Elem<T>::Store;
     using W = typename Elem<TW>::Store;
     __shared__ float2 words[2 * kNormThreads / 32];
@@ -296,73 +263,52 @@ __global__ void __launch_bounds__(THREADS) layer_norm_rows_grad(const NormGradRo
     const int cols = static_cast<int>(a.cols);
     pdl_enter();
     const float inv = 1.0f / static_cast<float>(a.cols);
-    float dw[V][N] = {}, db[V][N] = {};
+    float dw[V] = {}, db[V] = {};
     for (int64_t row = static_cast<int64_t>(blockIdx.x) * groups + g.id; row < a.rows;
          row += static_cast<int64_t>(gridDim.x) * groups) {
         const S* x = static_cast<const S*>(a.x) + row * a.x_stride;
         const S* d = static_cast<const S*>(a.d) + row * a.d_stride;
-        float xh[V][N], f[V][N];
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-            const int c = (t + k * size) * N;
-            if (c < cols) {
-                load_part<T, N, TAIL>(x, c, cols, xh[k]);
-                load_part<T, N, TAIL>(d, c, cols, f[k]);
-            }
-        }
         const float mean = __ldg(a.mean + row), r = __ldg(a.rstd + row);
+        float xh[V], f[V];
         float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
         for (int k = 0; k < V; ++k) {
-            const int c = (t + k * size) * N;
+            const int c = t + k * size;
             if (c >= cols) continue;
-            float w[N];
-            if (a.w != nullptr) load_part<TW, N, TAIL>(static_cast<const W*>(a.w), c, cols, w);
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                xh[k][j] = (xh[k][j] - mean) * r;
-                dw[k][j] = fmaf(f[k][j], xh[k][j], dw[k][j]);
-                db[k][j] += f[k][j];
-                if (a.w != nullptr) f[k][j] *= w[j];
-                s1 += f[k][j];
-                s2 = fmaf(f[k][j], xh[k][j], s2);
-            }
+            xh[k] = (elem_to_f32<T>(x[c]) - mean) * r;
+            f[k] = elem_to_f32<T>(d[c]);
+            dw[k] = fmaf(f[k], xh[k], dw[k]);
+            db[k] += f[k];
+            if (a.w != nullptr) f[k] *= elem_to_f32<TW>(static_cast<const W*>(a.w)[c]);
+            s1 += f[k];
+            s2 = fmaf(f[k], xh[k], s2);
         }
         if (a.d_x == nullptr) continue;
         const float2 m = g.sum(s1, s2);
         const float c1 = m.x * inv, c2 = m.y * inv;
         S* dx = static_cast<S*>(a.d_x) + row * a.d_x_stride;
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-            const int c = (t + k * size) * N;
-            if (c >= cols) continue;
-#pragma unroll
-            for (int j = 0; j < N; ++j)
-                f[k][j] = r * (f[k][j] - c1 - xh[k][j] * c2);
-            store_part<T, N, TAIL>(dx, c, cols, f[k]);
-        }
+        for (int k = 0; k < V; ++k)
+            if (t + k * size < cols)
+                dx[t + k * size] = elem_from_f32<T>(r * (f[k] - c1 - xh[k] * c2));
     }
     if (a.piece == nullptr) return;
     // the groups' sums, added in the groups' order
-    float* piece = a.piece + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
+    float* piece = a.piece + static_cast<int64_t>(blockIdx.x) * 2 * a.pitch;
     for (int q = 0; q < groups; ++q) {
         if (q > 0) __syncthreads();
         if (g.id != q) continue;
+        const bool last = q + 1 == groups;
 #pragma unroll
         for (int k = 0; k < V; ++k) {
-            const int c = (t + k * size) * N;
+            const int c = t + k * size;
             if (c >= cols) continue;
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                if (TAIL && c + j >= cols) continue;
-                if (q > 0) {
-                    dw[k][j] += sums[c + j];
-                    db[k][j] += sums[a.cols + c + j];
-                }
-                float* to = q + 1 < groups ? sums : piece;
-                to[c + j] = dw[k][j];
-                to[a.cols + c + j] = db[k][j];
+            if (q > 0) {
+                dw[k] += sums[c];
+                db[k] += sums[cols + c];
             }
+            (last ? piece : sums)[c] = dw[k];
+            (last ? piece + a.pitch : sums + cols)[c] = db[k];
         }
     }
 }
@@ -376,11 +322,15 @@ __global__ void __launch_bounds__(THREADS) layer_norm_rows_grad(const NormGradRo
 // with the status word set.
 constexpr int kStagedThreads = 512;
 constexpr int kStagedBytes = 216 * 1024;
+// Rows of 16 bits that end inside a vector take a few registers more.
+constexpr int staged_threads(int type, bool tail) {
+    return tail && type != kGradF32 ? 384 : kStagedThreads;
+}
 struct StagedShape {
     int size, groups, depth;
 };
-template <int T, int TW, int N>
-__global__ void __launch_bounds__(kStagedThreads, 1)
+template <int T, int TW, int N, bool TAIL>
+__global__ void __launch_bounds__(staged_threads(T, TAIL), 1)
     layer_norm_staged_grad(const NormGradRows a, const StagedShape sh,
                            unsigned long long limit_ns) {
     using S = typename Elem<T>::Store;
@@ -389,14 +339,19 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
     extern __shared__ __align__(128) char slots[];
     __shared__ float2 words[2 * kNormThreads / 32];
     __shared__ uint64_t full[kStagedThreads / 32 * 4];     // up to four slots a group
+    __shared__ float tails[TAIL ? 2 * N * kStagedThreads / 32 : 1];   // sums of the row's end
     const int size = sh.size;
     Group<false> g = group_of<false>(size, words);
     const int t = threadIdx.x % size;
-    const int cols = static_cast<int>(a.cols);
-    const uint32_t row_bytes = cols * sizeof(S);
+    const int cols = static_cast<int>(a.cols) / N * N;           // in whole vectors
+    const int wide = TAIL ? cols + N : cols;                     // of a slot
+    // the elements after them: the first threads', one each
+    const int tail = cols + t;
+    const bool has = TAIL && tail < static_cast<int>(a.cols);
+    const uint32_t row_bytes = wide * sizeof(S);
     // the weights in fp32, then the slots
     float* weights = reinterpret_cast<float*>(slots);
-    char* mine = slots + (a.w != nullptr ? 4 * cols : 0) +
+    char* mine = slots + (a.w != nullptr ? 4 * wide : 0) +
                  static_cast<size_t>(g.id) * sh.depth * 2 * row_bytes;
     uint64_t* bar = full + g.id * sh.depth;
     if (t == 0)
@@ -404,20 +359,31 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     pdl_enter();
     if (a.w != nullptr)
-        for (int c = threadIdx.x; c < cols; c += blockDim.x)
-            weights[c] = elem_to_f32<TW>(static_cast<const W*>(a.w)[c]);
+        for (int c = threadIdx.x; c < wide; c += blockDim.x)
+            weights[c] = c < a.cols ? elem_to_f32<TW>(static_cast<const W*>(a.w)[c]) : 0.0f;
     __syncthreads();
     const int64_t first = static_cast<int64_t>(blockIdx.x) * sh.groups + g.id;
     const int64_t next = static_cast<int64_t>(gridDim.x) * sh.groups;
-    const int64_t rows = first < a.rows ? (a.rows - first + next - 1) / next : 0;   // of this group
-    const auto fetch = [&](int64_t j) {
+    const int64_t rows = first < a.rows ? (a.rows - first + next - 1) / next : 0;
+    const auto fetch = [&](int64_t j) {                          // the group's j-th row
         const int64_t row = first + j * next;
         const int slot = static_cast<int>(j % sh.depth);
         char* to = mine + slot * 2 * row_bytes;
-        mbar_expect_tx(bar + slot, 2 * row_bytes);
-        bulk_load(to, static_cast<const S*>(a.x) + row * a.x_stride, row_bytes, bar + slot);
-        bulk_load(to + row_bytes, static_cast<const S*>(a.d) + row * a.d_stride, row_bytes,
-                  bar + slot);
+        const S* x = static_cast<const S*>(a.x) + row * a.x_stride;
+        const S* d = static_cast<const S*>(a.d) + row * a.d_stride;
+        uint32_t bytes = row_bytes;
+        if (TAIL && row + 1 == a.rows) {
+            // what follows the last row may not be read: its end goes by itself
+            bytes = cols * sizeof(S);
+            for (int c = cols; c < a.cols; ++c) {
+                reinterpret_cast<S*>(to)[c] = x[c];
+                reinterpret_cast<S*>(to + row_bytes)[c] = d[c];
+            }
+        }
+        mbar_expect_tx(bar + slot, 2 * bytes);
+        if (TAIL && bytes == 0) return;
+        bulk_load(to, x, bytes, bar + slot);
+        bulk_load(to + row_bytes, d, bytes, bar + slot);
     };
     int64_t fetched = 0;
     if (t == 0)
@@ -429,6 +395,7 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
     for (int k = 0; k < V; ++k)
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) dw[k][i] = db[k][i] = make_pair(0.0f, 0.0f);
+    if (has) tails[2 * (g.id * N + t)] = tails[2 * (g.id * N + t) + 1] = 0.0f;
     int slot = 0, phase = 0;
     float next_mean = rows > 0 ? __ldg(a.mean + first) : 0.0f;
     float next_r = rows > 0 ? __ldg(a.rstd + first) : 0.0f;
@@ -447,6 +414,16 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
         const S* x = reinterpret_cast<const S*>(mine + slot * 2 * row_bytes);
         const S* d = reinterpret_cast<const S*>(mine + slot * 2 * row_bytes + row_bytes);
         Pair s1 = make_pair(0.0f, 0.0f), s2 = s1;
+        if (has) {
+            const float xh = (elem_to_f32<T>(x[tail]) - mean) * r;
+            float f = elem_to_f32<T>(d[tail]);
+            float* own = tails + 2 * (g.id * N + t);
+            own[0] = fmaf(f, xh, own[0]);
+            own[1] += f;
+            if (a.w != nullptr) f *= weights[tail];
+            s1 = make_pair(f, 0.0f);
+            s2 = make_pair(f * xh, 0.0f);
+        }
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             const int c = (t + k * size) * N;
@@ -493,6 +470,11 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
                 }
                 store_elems<T, N>(dx + c, f);
             }
+            if (has) {
+                float y = elem_to_f32<T>(d[tail]);
+                if (a.w != nullptr) y *= weights[tail];
+                dx[tail] = elem_from_f32<T>(fmaf(y, r, fmaf(elem_to_f32<T>(x[tail]) - mean, c2, c1)));
+            }
         }
         if (++slot == sh.depth) {
             slot = 0;
@@ -505,11 +487,18 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
                 atomicOr(&g_norm_status, kStatusDrainTimeout);
     if (a.piece == nullptr) return;
     // the groups' sums, added in the groups' order, where the rows were
-    float* sums = reinterpret_cast<float*>(slots + (a.w != nullptr ? 4 * cols : 0));
-    float* piece = a.piece + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
+    float* sums = reinterpret_cast<float*>(slots + (a.w != nullptr ? 4 * wide : 0));
+    float* piece = a.piece + static_cast<int64_t>(blockIdx.x) * 2 * a.pitch;
     for (int q = 0; q < sh.groups; ++q) {
         __syncthreads();
         if (g.id != q) continue;
+        const bool last = q + 1 == sh.groups;
+        if (has) {
+            float* to = (last ? piece : sums) + tail;
+            to[0] = tails[2 * (g.id * N + t)] + (q > 0 ? sums[tail] : 0.0f);
+            to[last ? a.pitch : wide] =
+                tails[2 * (g.id * N + t) + 1] + (q > 0 ? sums[wide + tail] : 0.0f);
+        }
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             const int c = (t + k * size) * N;
@@ -526,12 +515,12 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
                     fw[i] += sums[c + i];
-                    fb[i] += sums[cols + c + i];
+                    fb[i] += sums[wide + c + i];
                 }
             }
-            float* to = (q + 1 < sh.groups ? sums : piece) + c;
+            float* to = (last ? piece : sums) + c;
             store_elems<kGradF32, N>(to, fw);
-            store_elems<kGradF32, N>(to + cols, fb);
+            store_elems<kGradF32, N>(to + (last ? a.pitch : wide), fb);
         }
     }
 }
@@ -540,30 +529,31 @@ __global__ void __launch_bounds__(kStagedThreads, 1)
 // sixteenth of the pieces, the warps' sums are added in their order.
 template <int TW>
 __global__ void __launch_bounds__(512)
-    layer_norm_columns(const float* piece, int pieces, int64_t cols, void* d_w, void* d_b,
-                       int accumulate) {
+    layer_norm_columns(const float* piece, int pieces, int64_t cols, int64_t pitch, void* d_w,
+                       void* d_b, int accumulate) {
     using W = typename Elem<TW>::Store;
     __shared__ float part[16][32];
     pdl_enter();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;   // of 2 * cols
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * 32 + lane;   // of 2 * pitch
+    const int64_t c = at < pitch ? at : at - pitch;
+    const bool live = at < 2 * pitch && c < cols;
     float s = 0.0f;
-    if (c < 2 * cols) {
-        const float* p = piece + c;
+    if (live) {
 #pragma unroll
         for (int k = 0; k < kNormPieces / 16; ++k) {
             const int q = warp + 16 * k;
-            if (q < pieces) s += p[static_cast<int64_t>(q) * 2 * cols];
+            if (q < pieces) s += piece[static_cast<int64_t>(q) * 2 * pitch + at];
         }
     }
     part[warp][lane] = s;
     __syncthreads();
-    if (warp != 0 || c >= 2 * cols) return;
+    if (warp != 0 || !live) return;
 #pragma unroll
     for (int k = 1; k < 16; ++k) s += part[k][lane];
-    W* to = static_cast<W*>(c < cols ? d_w : d_b);
+    W* to = static_cast<W*>(at < pitch ? d_w : d_b);
     if (to == nullptr) return;
-    to += c < cols ? c : c - cols;
+    to += c;
     if (accumulate) s += elem_to_f32<TW>(*to);
     *to = elem_from_f32<TW>(s);
 }
@@ -648,9 +638,9 @@ __global__ void __launch_bounds__(256) layer_norm_wide_columns(const NormGradRow
         dw = fmaf(d, (x - __ldg(a.mean + row)) * __ldg(a.rstd + row), dw);
         db += d;
     }
-    float* piece = a.piece + static_cast<int64_t>(blockIdx.y) * 2 * a.cols;
+    float* piece = a.piece + static_cast<int64_t>(blockIdx.y) * 2 * a.pitch;
     piece[c] = dw;
-    piece[a.cols + c] = db;
+    piece[a.pitch + c] = db;
 }
 
 // ----------------------------------------------------------------- launches
@@ -661,13 +651,12 @@ int fit_group(int64_t cols, int most, int held) {
         if (static_cast<int64_t>(s) * held >= cols) return s;
     return 0;
 }
-
-// A thread holds up to 32 elements of a row in vectors (4 of 16 bits, 8 of fp32),
-// or 16 single ones where rows are not aligned; backward, with their columns'
-// sums, 32 or 8 (up to 200 and 128 registers), 256 or 512 threads to a block.
+// A thread holds up to 32 elements of a row in vectors (4 of 16 bits, 8 of fp32), or 16
+// single ones where rows are not aligned; backward, with their columns' sums, 32 or 8.
 int fit_rows(int64_t cols, bool vec) { return fit_group(cols, kNormThreads, vec ? 32 : 16); }
-int grad_threads(bool vec) { return vec ? 256 : 512; }
-int fit_grad(int64_t cols, bool vec) { return fit_group(cols, grad_threads(vec), vec ? 32 : 8); }
+int fit_grad(int64_t cols, bool vec) {
+    return vec ? fit_group(cols, 256, 32) : fit_group(cols, kNormThreads, 8);
+}
 
 template <int T, int TW>
 cudaError_t go_rows(const NormRows& a, bool vec, cudaStream_t stream) {
@@ -678,62 +667,55 @@ cudaError_t go_rows(const NormRows& a, bool vec, cudaStream_t stream) {
                             dim3(static_cast<unsigned>(a.rows < most ? a.rows : most)),
                             dim3(kNormThreads), 0, stream, a);
     // rows of vectors: four warps with a row each, or a block to a row
-    const bool whole = vec && a.cols % Elem<T>::kVec == 0;
-    const int threads = size > 128 || (whole && size > 32) ? size : 128;
+    const int threads = size > 128 || (vec && size > 32) ? size : 128;
     const int64_t blocks = (a.rows + threads / size - 1) / (threads / size);
     const dim3 grid(static_cast<unsigned>(blocks < 0x7FFFFFFF ? blocks : 0x7FFFFFFF));
     constexpr int N = Elem<T>::kVec;
     const auto go = [&](auto* kernel) {
         return launch_after(kernel, grid, dim3(threads), 0, stream, a, size);
     };
-    return !vec              ? go(layer_norm_rows<T, TW, 1, 16, false>)
-           : whole && size > 32 ? go(layer_norm_vectors<T, TW, true>)
-           : whole           ? go(layer_norm_vectors<T, TW, false>)
-                             : go(layer_norm_rows<T, TW, N, 32 / N, true>);
+    if (!vec) return go(layer_norm_elements<T, TW, 16>);
+    if (a.cols % N == 0)
+        return size > 32 ? go(layer_norm_vectors<T, TW, true, false>)
+                         : go(layer_norm_vectors<T, TW, false, false>);
+    return size > 32 ? go(layer_norm_vectors<T, TW, true, true>)
+                     : go(layer_norm_vectors<T, TW, false, true>);
 }
 
-// The groups of a block and their slots: as many groups as leave three slots each.
+// The groups of a block and their slots: as many groups as leave three slots each (a row
+// of 64 KB, 8192 of fp32, has two).
 StagedShape staged_shape(int64_t cols, int type) {
     StagedShape s{fit_group(cols, 256, 32), 0, 0};
-    const int64_t slot = 2 * cols * (type == kGradF32 ? 4 : 2);
-    const int64_t room = kStagedBytes - 4 * cols;    // beside the weights
-    if (s.size == 0) return s;
+    const int64_t wide = (cols + 7) / 8 * 8;         // as much as the kernel takes, or more
+    const int64_t slot = 2 * wide * (type == kGradF32 ? 4 : 2);
+    const int64_t room = kStagedBytes - 4 * wide;    // beside the weights
+    const int64_t most = std::max<int64_t>(1, room / (3 * slot));
+    const int threads = staged_threads(type, cols % (type == kGradF32 ? 4 : 8) != 0);
     // where few rows fit, more threads to each
-    while (s.size < kStagedThreads && room / (3 * slot) * s.size < kStagedThreads) s.size *= 2;
-    s.groups = static_cast<int>(std::min<int64_t>(kStagedThreads / s.size, room / (3 * slot)));
-    if (s.groups > 0)
-        s.depth = static_cast<int>(std::min<int64_t>(4, room / (s.groups * slot)));
+    while (2 * s.size <= threads && most * s.size < threads) s.size *= 2;
+    s.groups = static_cast<int>(std::min<int64_t>(threads / s.size, most));
+    s.depth = static_cast<int>(std::min<int64_t>(4, room / (s.groups * slot)));
     return s;
 }
 template <int T, int TW>
 cudaError_t go_staged_grad(const NormGradRows& a, int blocks, cudaStream_t stream) {
-    const StagedShape s = staged_shape(a.cols, T);
-    const auto kernel = layer_norm_staged_grad<T, TW, Elem<T>::kVec>;
-    const cudaError_t e = cudaFuncSetAttribute(
-        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStagedBytes);
-    if (e != cudaSuccess) return e;
-    return launch_after(kernel, dim3(blocks), dim3(s.groups * s.size),
-                        static_cast<size_t>(s.groups) * s.depth * 2 * a.cols *
-                                sizeof(typename Elem<T>::Store) + 4 * a.cols,
-                        stream, a, s, tma_wait_limit());
-}
-// Whether rows go through shared memory: whole vectors, and some for every SM.
-bool staged(int64_t rows, int64_t cols, int type, bool vec) {
-    return vec && cols % (type == kGradF32 ? 4 : 8) == 0 && staged_shape(cols, type).groups > 0;
-}
-
-template <int T, int TW>
-cudaError_t go_rows_grad(const NormGradRows& a, int size, int blocks, bool vec,
-                         cudaStream_t stream) {
     constexpr int N = Elem<T>::kVec;
-    const int threads = grad_threads(vec);
-    const size_t smem = threads > size ? sizeof(float) * 2 * a.cols : 0;   // 32 KB at most
+    const StagedShape s = staged_shape(a.cols, T);
     const auto go = [&](auto* kernel) {
-        return launch_after(kernel, dim3(blocks), dim3(threads), smem, stream, a, size);
+        const cudaError_t e = cudaFuncSetAttribute(
+            kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStagedBytes);
+        if (e != cudaSuccess) return e;
+        return launch_after(kernel, dim3(blocks), dim3(s.groups * s.size), kStagedBytes, stream, a,
+                            s, tma_wait_limit());
     };
-    return !vec              ? go(layer_norm_rows_grad<T, TW, 1, 8, false, 512>)
-           : a.cols % N == 0 ? go(layer_norm_rows_grad<T, TW, N, 32 / N, false, 256>)
-                             : go(layer_norm_rows_grad<T, TW, N, 32 / N, true, 256>);
+    return a.cols % N == 0 ? go(layer_norm_staged_grad<T, TW, N, false>)
+                           : go(layer_norm_staged_grad<T, TW, N, true>);
+}
+template <int T, int TW>
+cudaError_t go_elements_grad(const NormGradRows& a, int size, int blocks, cudaStream_t stream) {
+    const size_t smem = kNormThreads > size ? sizeof(float) * 2 * a.cols : 0;   // 16 KB at most
+    return launch_after(layer_norm_elements_grad<T, TW, 8>, dim3(blocks), dim3(kNormThreads), smem,
+                        stream, a, size);
 }
 
 template <int T, int TW>
@@ -743,8 +725,8 @@ cudaError_t go_grad(const NormGradRows& a, void* d_w, void* d_b, int accumulate,
     const int pieces = norm_pieces(a.rows, a.cols, T, vec);
     cudaError_t e = cudaSuccess;
     if (a.rows > 0 && size != 0) {
-        e = staged(a.rows, a.cols, T, vec) ? go_staged_grad<T, TW>(a, pieces, stream)
-                                           : go_rows_grad<T, TW>(a, size, pieces, vec, stream);
+        e = vec ? go_staged_grad<T, TW>(a, pieces, stream)
+                : go_elements_grad<T, TW>(a, size, pieces, stream);
         note_launch();
     } else if (a.rows > 0) {
         if (a.d_x != nullptr) {
@@ -762,9 +744,9 @@ cudaError_t go_grad(const NormGradRows& a, void* d_w, void* d_b, int accumulate,
         }
     }
     if (e != cudaSuccess || a.piece == nullptr) return e;
-    e = launch_after(layer_norm_columns<TW>, dim3(static_cast<unsigned>((2 * a.cols + 31) / 32)),
-                     dim3(512), 0, stream, static_cast<const float*>(a.piece), pieces, a.cols, d_w,
-                     d_b, accumulate);
+    e = launch_after(layer_norm_columns<TW>, dim3(static_cast<unsigned>((2 * a.pitch + 31) / 32)),
+                     dim3(512), 0, stream, static_cast<const float*>(a.piece), pieces, a.cols,
+                     a.pitch, d_w, d_b, accumulate);
     note_launch();
     return e;
 }
@@ -784,8 +766,7 @@ int norm_pieces(int64_t rows, int64_t cols, int type, bool vec) {
     const int size = fit_grad(cols, vec);
     if (rows == 0) return 0;
     if (size == 0) return static_cast<int>(rows < 64 ? rows : 64);
-    const int groups = staged(rows, cols, type, vec) ? staged_shape(cols, type).groups
-                                                     : grad_threads(vec) / size;
+    const int groups = vec ? staged_shape(cols, type).groups : kNormThreads / size;
     const int64_t most = std::min(device_sms(), kNormPieces);
     const int64_t need = (rows + groups - 1) / groups;
     return static_cast<int>(need < most ? need : most);

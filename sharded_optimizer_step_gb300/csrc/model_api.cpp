@@ -499,7 +499,7 @@ int rows_layer_norm(const void* x, int64_t x_stride, int32_t dtype, int64_t rows
 
 int64_t rows_layer_norm_workspace_bytes(int64_t cols) {
     if (cols < 1 || cols > (int64_t{1} << 24)) return -1;
-    return 8 * cols * kNormPieces;
+    return 8 * ((cols + 7) / 8 * 8) * kNormPieces;
 }
 
 int rows_layer_norm_grad(const void* d_out, int64_t d_out_stride, const void* x,
@@ -540,7 +540,8 @@ int rows_layer_norm_grad(const void* d_out, int64_t d_out_stride, const void* x,
     if (int rc = check_ranges(reads, writes); rc != SHARDSTEP_OK) return rc;
     const NormGradRows a{x,    x_stride, d_out, d_out_stride,
                          d_x,  d_x_stride, weight, mean, rstd,
-                         columns ? static_cast<float*>(workspace) : nullptr, rows, cols};
+                         columns ? static_cast<float*>(workspace) : nullptr, rows, cols,
+                         (cols + 7) / 8 * 8};
     const bool vec = rows_aligned(x, x_stride, rows, es) &&
                      rows_aligned(d_out, d_out_stride, rows, es) && aligned(weight, 16) &&
                      (d_x == nullptr || rows_aligned(d_x, d_x_stride, rows, es));
