@@ -474,10 +474,13 @@ struct NormGradRows {
 constexpr int kNormPieces = 160;
 int norm_pieces(int64_t rows, int64_t cols, int type, bool vec);
 cudaError_t read_norm_status(unsigned int* status, bool clear);
-cudaError_t launch_layer_norm(const NormRows& a, int type, int w_type, bool vec,
+// vec: the rows that are read, the weights and the bias take vectors; whole: the rows
+// that are written do.
+cudaError_t launch_layer_norm(const NormRows& a, int type, int w_type, bool vec, bool whole,
                               cudaStream_t stream);
 cudaError_t launch_layer_norm_grad(const NormGradRows& a, int type, int w_type, void* d_w,
-                                   void* d_b, int accumulate, bool vec, cudaStream_t stream);
+                                   void* d_b, int accumulate, bool vec, bool whole,
+                                   cudaStream_t stream);
 
 // ------------------------------------------------ matrices' updates
 // (matrix.cu; host side in model_api.cpp)

@@ -4,22 +4,26 @@
 //   g = d w,  d_x = r (g - mean(g) - xh mean(g xh))
 //   d_w = sum over rows of d xh,  d_b = sum over rows of d
 //
-// Both passes are bound by memory: forward reads x and writes out, backward
-// reads x and d and writes d_x; a row stays in registers between its sums and
-// its results, so nothing is read twice.  The variance is formed from the
-// differences from the mean, not from a sum of squares, so a row far from zero
-// keeps its bits.  All sums are fp32 (a thread's terms, then a tree over the
-// threads).
+// Both passes move each row once: forward reads x and writes out, backward reads x
+// and d and writes d_x.  The variance is formed from the differences from the mean,
+// not from a sum of squares, so a row far from zero keeps its bits.  All sums are fp32
+// (a thread's terms, then a tree over the threads).
 //
-// Backward, a thread holds the same columns of every row it meets, so their
-// d_w and d_b stay in its registers until the block's last row; the blocks'
-// sums then go to the workspace and layer_norm_columns adds them in the blocks'
-// order.  The grid goes by the sizes and the number of SMs alone, so equal
-// calls give equal bits.
+// Forward, a row stays in registers as it is in memory (layer_norm_vectors: 16384 rows
+// of 4096 bf16 in 58 to 61 us, 4.4 TB/s; 20 instructions an element and 6 blocks a SM,
+// bound by their latency), or in shared memory where the results' rows take no vectors
+// (layer_norm_staged).  Backward, rows come through shared memory some 190 KB ahead
+// (layer_norm_staged_grad: 84 us, 4.8 TB/s; 27 instructions an element, issue slots 46%
+// busy, 16 warps a SM for their registers).  A thread holds the same columns of every row
+// it meets, so their d_w and d_b stay in its registers until the block's last row; the
+// blocks' sums then go to the workspace and layer_norm_columns adds them in the blocks'
+// order (6 us).  The grid goes by the sizes and the number of SMs alone, so equal calls
+// give equal bits.
 //
-// Rows too wide for registers (over 16384 columns forward and 8192 backward, or
-// 8192 and 4096 where rows are not aligned) are read again for each sum (layer_norm_wide, layer_norm_wide_grad,
-// layer_norm_wide_columns).
+// Rows that are not 16-byte aligned take single elements (layer_norm_elements, up to
+// 8192 columns forward and 4096 backward); wider rows (over 16384 forward and 8192
+// backward where they are aligned) are read again for each sum (layer_norm_wide,
+// layer_norm_wide_grad, layer_norm_wide_columns).
 #include <algorithm>
 
 #include "elem.cuh"
@@ -34,8 +38,8 @@ constexpr uint32_t kFull = 0xFFFFFFFFu;
 
 __device__ unsigned int g_norm_status;
 
-// Sums of two values over a group of `size` threads (32, 64, .., 512) that take
-// one row: shuffles, then one word per warp.  `words` holds 2 x 2 words per
+// Sums of one or two values over a group of `size` threads (32, 64, .., 512) that take
+// one row: shuffles, then a word or two per warp.  `words` holds 2 x 2 words per
 // warp of the block: two banks in turn, so that one barrier a sum is enough.
 // ALONE: the group is its block.  (A barrier whose number is not known when the kernel
 // is compiled takes all sixteen of a block, and an SM has 64.)
@@ -52,7 +56,7 @@ struct Group {
 #pragma unroll
         for (int d = 16; d > 0; d /= 2) a += __shfl_xor_sync(kFull, a, d);
         if (size == 32) return a;
-        float* w = reinterpret_cast<float*>(words + bank * (kNormThreads / 32));
+        float* w = reinterpret_cast<float*>(words + bank * (blockDim.x / 32));
         bank ^= 1;
         if (threadIdx.x % 32 == 0) w[warp] = a;
         sync();
@@ -67,7 +71,7 @@ struct Group {
             b += __shfl_xor_sync(kFull, b, d);
         }
         if (size == 32) return make_float2(a, b);
-        float2* w = words + bank * (kNormThreads / 32);
+        float2* w = words + bank * (blockDim.x / 32);
         bank ^= 1;
         if (threadIdx.x % 32 == 0) w[warp] = make_float2(a, b);
         sync();
@@ -329,7 +333,8 @@ constexpr int staged_threads(int type, bool tail) {
 struct StagedShape {
     int size, groups, depth;
 };
-template <int T, int TW, int N, bool TAIL>
+// WHOLE: d_x's rows take vectors; else consecutive threads write consecutive elements.
+template <int T, int TW, int N, bool TAIL, bool WHOLE>
 __global__ void __launch_bounds__(staged_threads(T, TAIL), 1)
     layer_norm_staged_grad(const NormGradRows a, const StagedShape sh,
                            unsigned long long limit_ns) {
@@ -449,31 +454,37 @@ __global__ void __launch_bounds__(staged_threads(T, TAIL), 1)
         if (a.d_x != nullptr) {
             // r (f - c1 - xh c2) = r f + (x - mean) (-r r c2) - r c1
             const float c1 = -r * (m.x * inv), c2 = -r * (r * (m.y * inv));
-            const Pair k1 = make_pair(c1, c1), k2 = make_pair(c2, c2);
             S* dx = static_cast<S*>(a.d_x) + row * a.d_x_stride;
+            const auto element = [&](int c) {
+                float y = elem_to_f32<T>(d[c]);
+                if (a.w != nullptr) y *= weights[c];
+                dx[c] = elem_from_f32<T>(fmaf(y, r, fmaf(elem_to_f32<T>(x[c]) - mean, c2, c1)));
+            };
+            if constexpr (WHOLE) {
+                const Pair k1 = make_pair(c1, c1), k2 = make_pair(c2, c2);
 #pragma unroll
-            for (int k = 0; k < V; ++k) {
-                const int c = (t + k * size) * N;
-                if (c >= cols) continue;
-                Raw<T, N> rx{*reinterpret_cast<const uint4*>(x + c)};
-                Raw<T, N> rd{*reinterpret_cast<const uint4*>(d + c)};
-                Pair w[N / 2];
-                if (a.w != nullptr) load_weights<kGradF32, N>(weights, c, w);
-                float f[N];
+                for (int k = 0; k < V; ++k) {
+                    const int c = (t + k * size) * N;
+                    if (c >= cols) continue;
+                    Raw<T, N> rx{*reinterpret_cast<const uint4*>(x + c)};
+                    Raw<T, N> rd{*reinterpret_cast<const uint4*>(d + c)};
+                    Pair w[N / 2];
+                    if (a.w != nullptr) load_weights<kGradF32, N>(weights, c, w);
+                    float f[N];
 #pragma unroll
-                for (int i = 0; i < N / 2; ++i) {
-                    Pair y = rd.pair(i);
-                    if (a.w != nullptr) y = mul2(y, w[i]);
-                    y = fma2(y, r2, fma2(add2(rx.pair(i), off), k2, k1));
-                    f[2 * i] = floats(y).x;
-                    f[2 * i + 1] = floats(y).y;
+                    for (int i = 0; i < N / 2; ++i) {
+                        Pair y = rd.pair(i);
+                        if (a.w != nullptr) y = mul2(y, w[i]);
+                        y = fma2(y, r2, fma2(add2(rx.pair(i), off), k2, k1));
+                        f[2 * i] = floats(y).x;
+                        f[2 * i + 1] = floats(y).y;
+                    }
+                    store_elems<T, N>(dx + c, f);
                 }
-                store_elems<T, N>(dx + c, f);
-            }
-            if (has) {
-                float y = elem_to_f32<T>(d[tail]);
-                if (a.w != nullptr) y *= weights[tail];
-                dx[tail] = elem_from_f32<T>(fmaf(y, r, fmaf(elem_to_f32<T>(x[tail]) - mean, c2, c1)));
+                if (has) element(tail);
+            } else {
+#pragma unroll 4
+                for (int c = t; c < static_cast<int>(a.cols); c += size) element(c);
             }
         }
         if (++slot == sh.depth) {
@@ -523,6 +534,118 @@ __global__ void __launch_bounds__(staged_threads(T, TAIL), 1)
             store_elems<kGradF32, N>(to + (last ? a.pitch : wide), fb);
         }
     }
+}
+
+// Forward in the same way, where x's rows take vectors and out's do not: consecutive
+// threads read vectors of x for the sums and write consecutive elements of out.  Weight
+// and bias are in shared memory too, in fp32.
+constexpr int kForwardThreads = 1024;
+template <int T, int TW, int N, bool TAIL>
+__global__ void __launch_bounds__(kForwardThreads, 1)
+    layer_norm_staged(const NormRows a, const StagedShape sh, unsigned long long limit_ns) {
+    using S = typename Elem<T>::Store;
+    using W = typename Elem<TW>::Store;
+    constexpr int V = 32 / N;
+    extern __shared__ __align__(128) char slots[];
+    __shared__ float2 words[2 * kForwardThreads / 32];
+    __shared__ uint64_t full[kForwardThreads / 32 * 4];    // up to four slots a group
+    const int size = sh.size;
+    Group<false> g = group_of<false>(size, words);
+    const int t = threadIdx.x % size;
+    const int cols = static_cast<int>(a.cols) / N * N;           // in whole vectors
+    const int wide = TAIL ? cols + N : cols;                     // of a slot
+    const int tail = cols + t;
+    const bool has = TAIL && tail < static_cast<int>(a.cols);
+    const uint32_t row_bytes = wide * sizeof(S);
+    float* weights = reinterpret_cast<float*>(slots);
+    float* biases = weights + wide;
+    char* mine = slots + 8 * wide + static_cast<size_t>(g.id) * sh.depth * row_bytes;
+    uint64_t* bar = full + g.id * sh.depth;
+    if (t == 0)
+        for (int k = 0; k < sh.depth; ++k) mbar_init(bar + k, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    pdl_enter();
+    for (int c = threadIdx.x; c < static_cast<int>(a.cols); c += blockDim.x) {
+        weights[c] = a.w != nullptr ? elem_to_f32<TW>(static_cast<const W*>(a.w)[c]) : 1.0f;
+        biases[c] = a.b != nullptr ? elem_to_f32<TW>(static_cast<const W*>(a.b)[c]) : 0.0f;
+    }
+    __syncthreads();
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * sh.groups + g.id;
+    const int64_t next = static_cast<int64_t>(gridDim.x) * sh.groups;
+    const int64_t rows = first < a.rows ? (a.rows - first + next - 1) / next : 0;
+    const auto fetch = [&](int64_t j) {                          // the group's j-th row
+        const int64_t row = first + j * next;
+        const int slot = static_cast<int>(j % sh.depth);
+        char* to = mine + slot * row_bytes;
+        const S* x = static_cast<const S*>(a.x) + row * a.x_stride;
+        uint32_t bytes = row_bytes;
+        if (TAIL && row + 1 == a.rows) {
+            // what follows the last row may not be read: its end goes by itself
+            bytes = cols * sizeof(S);
+            for (int c = cols; c < a.cols; ++c) reinterpret_cast<S*>(to)[c] = x[c];
+        }
+        mbar_expect_tx(bar + slot, bytes);
+        if (!TAIL || bytes > 0) bulk_load(to, x, bytes, bar + slot);
+    };
+    int64_t fetched = 0;
+    if (t == 0)
+        for (; fetched < sh.depth && fetched < rows; ++fetched) fetch(fetched);
+    const float n = static_cast<float>(a.cols);
+    bool late = false;
+    int slot = 0, phase = 0;
+    for (int64_t j = 0; j < rows; ++j) {
+        const int64_t row = first + j * next;
+        if (!late && !mbar_wait(bar + slot, phase, limit_ns)) {
+            late = true;
+            atomicOr(&g_norm_status, kStatusConsumerTimeout);
+        }
+        const S* x = reinterpret_cast<const S*>(mine + slot * row_bytes);
+        Pair sum = make_pair(has ? elem_to_f32<T>(x[tail]) : 0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int c = (t + k * size) * N;
+            if (c >= cols) continue;
+            const Raw<T, N> raw{*reinterpret_cast<const uint4*>(x + c)};
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) sum = add2(sum, raw.pair(i));
+        }
+        // no rounded 1 / n: rows far from 0
+        const float mean = __fdiv_rn(g.sum(floats(sum).x + floats(sum).y), n);
+        // all threads are here: none reads the row before any more
+        if (t == 0 && !late && j > 0 && fetched < rows) fetch(fetched++);
+        const Pair off = make_pair(-mean, -mean);
+        const float end = has ? elem_to_f32<T>(x[tail]) - mean : 0.0f;
+        sum = make_pair(end * end, 0.0f);
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int c = (t + k * size) * N;
+            if (c >= cols) continue;
+            const Raw<T, N> raw{*reinterpret_cast<const uint4*>(x + c)};
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) {
+                const Pair d = add2(raw.pair(i), off);
+                sum = fma2(d, d, sum);
+            }
+        }
+        const float var = __fdiv_rn(g.sum(floats(sum).x + floats(sum).y), n);
+        const float r = __fdiv_rn(1.0f, __fsqrt_rn(var + a.eps));
+        if (t == 0) {
+            a.mean[row] = mean;
+            a.rstd[row] = r;
+        }
+        S* out = static_cast<S*>(a.out) + row * a.out_stride;
+#pragma unroll 4
+        for (int c = t; c < static_cast<int>(a.cols); c += size)
+            out[c] = elem_from_f32<T>((elem_to_f32<T>(x[c]) - mean) * r * weights[c] + biases[c]);
+        if (++slot == sh.depth) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+    if (late && t == 0)      // copies in flight land before the block's memory goes
+        for (int64_t j = fetched > sh.depth ? fetched - sh.depth : 0; j < fetched; ++j)
+            if (!mbar_wait(bar + j % sh.depth, (j / sh.depth) & 1, kDrainNs))
+                atomicOr(&g_norm_status, kStatusDrainTimeout);
 }
 
 // d_w and d_b from the blocks' sums: 32 columns per block, a warp takes every
@@ -658,8 +781,48 @@ int fit_grad(int64_t cols, bool vec) {
     return vec ? fit_group(cols, 256, 32) : fit_group(cols, kNormThreads, 8);
 }
 
+// The groups of a block and their slots: as many groups as leave three slots each (or
+// two, in rows of 32 KB and more).
+StagedShape staged_shape(int64_t cols, int slot_rows, int beside, int es, int threads) {
+    StagedShape s{fit_group(cols, 256, 32), 0, 0};
+    const int64_t wide = (cols + 7) / 8 * 8;         // as much as the kernels take, or more
+    const int64_t slot = slot_rows * wide * es;
+    const int64_t room = kStagedBytes - beside * wide;
+    const int64_t most = std::max<int64_t>(1, room / (3 * slot));
+    // where few rows fit, more threads to each; a group of several warps has one of 15
+    // barriers
+    while (2 * s.size <= std::min(threads, kStagedThreads) && most * s.size < threads) s.size *= 2;
+    s.groups = static_cast<int>(std::min<int64_t>(threads / s.size, most));
+    if (s.size > 32 && s.groups > 15) s.groups = 15;
+    s.depth = static_cast<int>(std::min<int64_t>(4, room / (s.groups * slot)));
+    return s;
+}
+template <typename Kernel, typename Args>
+cudaError_t go_staged(Kernel* kernel, const Args& a, const StagedShape& s, int blocks,
+                      cudaStream_t stream) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStagedBytes);
+    if (e != cudaSuccess) return e;
+    return launch_after(kernel, dim3(blocks), dim3(s.groups * s.size), kStagedBytes, stream, a, s,
+                        tma_wait_limit());
+}
 template <int T, int TW>
-cudaError_t go_rows(const NormRows& a, bool vec, cudaStream_t stream) {
+cudaError_t go_staged_rows(const NormRows& a, cudaStream_t stream) {
+    constexpr int N = Elem<T>::kVec;
+    const StagedShape s = staged_shape(a.cols, 1, 8, 16 / N, kForwardThreads);
+    const int64_t need = (a.rows + s.groups - 1) / s.groups;
+    const int blocks = static_cast<int>(std::min<int64_t>(need, device_sms()));
+    return a.cols % N == 0 ? go_staged(layer_norm_staged<T, TW, N, false>, a, s, blocks, stream)
+                           : go_staged(layer_norm_staged<T, TW, N, true>, a, s, blocks, stream);
+}
+
+template <int T, int TW>
+cudaError_t go_rows(const NormRows& a, bool vec, bool whole, cudaStream_t stream) {
+    // results that take no vectors go through shared memory (999 rows of 5003 fp32 in 21
+    // us, by single elements 27); others are faster from registers (16384 of 4096 bf16 in
+    // 58 to 61 us, 84)
+    if (vec && !whole && fit_group(a.cols, 256, 32) != 0) return go_staged_rows<T, TW>(a, stream);
+    vec = vec && whole;
     const int size = fit_rows(a.cols, vec);
     const int64_t most = static_cast<int64_t>(device_sms()) * 8;
     if (size == 0)
@@ -682,34 +845,20 @@ cudaError_t go_rows(const NormRows& a, bool vec, cudaStream_t stream) {
                      : go(layer_norm_vectors<T, TW, false, true>);
 }
 
-// The groups of a block and their slots: as many groups as leave three slots each (a row
-// of 64 KB, 8192 of fp32, has two).
-StagedShape staged_shape(int64_t cols, int type) {
-    StagedShape s{fit_group(cols, 256, 32), 0, 0};
-    const int64_t wide = (cols + 7) / 8 * 8;         // as much as the kernel takes, or more
-    const int64_t slot = 2 * wide * (type == kGradF32 ? 4 : 2);
-    const int64_t room = kStagedBytes - 4 * wide;    // beside the weights
-    const int64_t most = std::max<int64_t>(1, room / (3 * slot));
-    const int threads = staged_threads(type, cols % (type == kGradF32 ? 4 : 8) != 0);
-    // where few rows fit, more threads to each
-    while (2 * s.size <= threads && most * s.size < threads) s.size *= 2;
-    s.groups = static_cast<int>(std::min<int64_t>(threads / s.size, most));
-    s.depth = static_cast<int>(std::min<int64_t>(4, room / (s.groups * slot)));
-    return s;
+StagedShape grad_shape(int64_t cols, int type) {
+    const int es = type == kGradF32 ? 4 : 2;
+    return staged_shape(cols, 2, 4, es, staged_threads(type, cols * es % 16 != 0));
 }
 template <int T, int TW>
-cudaError_t go_staged_grad(const NormGradRows& a, int blocks, cudaStream_t stream) {
+cudaError_t go_staged_grad(const NormGradRows& a, int blocks, bool whole, cudaStream_t stream) {
     constexpr int N = Elem<T>::kVec;
-    const StagedShape s = staged_shape(a.cols, T);
-    const auto go = [&](auto* kernel) {
-        const cudaError_t e = cudaFuncSetAttribute(
-            kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStagedBytes);
-        if (e != cudaSuccess) return e;
-        return launch_after(kernel, dim3(blocks), dim3(s.groups * s.size), kStagedBytes, stream, a,
-                            s, tma_wait_limit());
-    };
-    return a.cols % N == 0 ? go(layer_norm_staged_grad<T, TW, N, false>)
-                           : go(layer_norm_staged_grad<T, TW, N, true>);
+    const StagedShape s = grad_shape(a.cols, T);
+    if (a.cols % N == 0)
+        return whole
+                   ? go_staged(layer_norm_staged_grad<T, TW, N, false, true>, a, s, blocks, stream)
+                   : go_staged(layer_norm_staged_grad<T, TW, N, false, false>, a, s, blocks, stream);
+    return whole ? go_staged(layer_norm_staged_grad<T, TW, N, true, true>, a, s, blocks, stream)
+                 : go_staged(layer_norm_staged_grad<T, TW, N, true, false>, a, s, blocks, stream);
 }
 template <int T, int TW>
 cudaError_t go_elements_grad(const NormGradRows& a, int size, int blocks, cudaStream_t stream) {
@@ -720,12 +869,12 @@ cudaError_t go_elements_grad(const NormGradRows& a, int size, int blocks, cudaSt
 
 template <int T, int TW>
 cudaError_t go_grad(const NormGradRows& a, void* d_w, void* d_b, int accumulate, bool vec,
-                    cudaStream_t stream) {
+                    bool whole, cudaStream_t stream) {
     const int size = fit_grad(a.cols, vec);
     const int pieces = norm_pieces(a.rows, a.cols, T, vec);
     cudaError_t e = cudaSuccess;
     if (a.rows > 0 && size != 0) {
-        e = vec ? go_staged_grad<T, TW>(a, pieces, stream)
+        e = vec ? go_staged_grad<T, TW>(a, pieces, whole, stream)
                 : go_elements_grad<T, TW>(a, size, pieces, stream);
         note_launch();
     } else if (a.rows > 0) {
@@ -766,7 +915,7 @@ int norm_pieces(int64_t rows, int64_t cols, int type, bool vec) {
     const int size = fit_grad(cols, vec);
     if (rows == 0) return 0;
     if (size == 0) return static_cast<int>(rows < 64 ? rows : 64);
-    const int groups = vec ? staged_shape(cols, type).groups : kNormThreads / size;
+    const int groups = vec ? grad_shape(cols, type).groups : kNormThreads / size;
     const int64_t most = std::min(device_sms(), kNormPieces);
     const int64_t need = (rows + groups - 1) / groups;
     return static_cast<int>(need < most ? need : most);
@@ -779,20 +928,21 @@ cudaError_t read_norm_status(unsigned int* status, bool clear) {
     return cudaMemcpyToSymbol(g_norm_status, &zero, sizeof(unsigned int));
 }
 
-cudaError_t launch_layer_norm(const NormRows& a, int type, int w_type, bool vec,
+cudaError_t launch_layer_norm(const NormRows& a, int type, int w_type, bool vec, bool whole,
                               cudaStream_t stream) {
     const cudaError_t e = by_types(type, w_type, [&](auto t, auto w) {
-        return go_rows<decltype(t)::value, decltype(w)::value>(a, vec, stream);
+        return go_rows<decltype(t)::value, decltype(w)::value>(a, vec, whole, stream);
     });
     note_launch();
     return e;
 }
 
 cudaError_t launch_layer_norm_grad(const NormGradRows& a, int type, int w_type, void* d_w,
-                                   void* d_b, int accumulate, bool vec, cudaStream_t stream) {
+                                   void* d_b, int accumulate, bool vec, bool whole,
+                                   cudaStream_t stream) {
     return by_types(type, w_type, [&](auto t, auto w) {
         return go_grad<decltype(t)::value, decltype(w)::value>(a, d_w, d_b, accumulate, vec,
-                                                               stream);
+                                                               whole, stream);
     });
 }
 

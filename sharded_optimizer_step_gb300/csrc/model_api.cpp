@@ -487,11 +487,11 @@ int rows_layer_norm(const void* x, int64_t x_stride, int32_t dtype, int64_t rows
     writes.add(rstd, rows * 4);
     if (int rc = check_ranges(reads, writes); rc != SHARDSTEP_OK) return rc;
     const NormRows a{x, x_stride, out, out_stride, weight, bias, mean, rstd, rows, cols, eps};
-    const bool vec = rows_aligned(x, x_stride, rows, es) &&
-                     rows_aligned(out, out_stride, rows, es) && aligned(weight, 16) &&
-                     aligned(bias, 16);
+    const bool vec =
+        rows_aligned(x, x_stride, rows, es) && aligned(weight, 16) && aligned(bias, 16);
     const cudaError_t e =
-        launch_layer_norm(a, dtype, weight_dtype, vec, static_cast<cudaStream_t>(stream));
+        launch_layer_norm(a, dtype, weight_dtype, vec, rows_aligned(out, out_stride, rows, es),
+                          static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail("layer norm", e);
     record_kernel("layer_norm_rows<%s>", dtype_name(dtype));
     return ready_ok();
@@ -543,11 +543,11 @@ int rows_layer_norm_grad(const void* d_out, int64_t d_out_stride, const void* x,
                          columns ? static_cast<float*>(workspace) : nullptr, rows, cols,
                          (cols + 7) / 8 * 8};
     const bool vec = rows_aligned(x, x_stride, rows, es) &&
-                     rows_aligned(d_out, d_out_stride, rows, es) && aligned(weight, 16) &&
-                     (d_x == nullptr || rows_aligned(d_x, d_x_stride, rows, es));
+                     rows_aligned(d_out, d_out_stride, rows, es) && aligned(weight, 16);
+    const bool whole = d_x == nullptr || rows_aligned(d_x, d_x_stride, rows, es);
     const cudaError_t e =
         launch_layer_norm_grad(a, dtype, weight_dtype, d_weight, d_bias, accumulate != 0, vec,
-                               static_cast<cudaStream_t>(stream));
+                               whole, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail("layer norm gradient", e);
     record_kernel("layer_norm_rows_grad<%s>", dtype_name(dtype));
     return ready_ok();

@@ -135,6 +135,38 @@ def test_forward_and_backward(rows, cols, stride, shift, dt, w_dt):
     _backward(d, x, y.mean, y.rstd, w, got, old_w, old_b)
 
 
+@pytest.mark.parametrize("rows,cols,out_stride,out_shift", [
+    (37, 5003, 5003, 0), (19, 768, 769, 1), (1, 4097, 4097, 0), (70, 31, 31, 3), (5, 8191, 8191, 0),
+    (3, 5, 5, 1), (1500, 2056, 2056, 0), (1300, 3001, 3001, 0), (1700, 4099, 4104, 0),
+    (2, 8192, 8200, 0), (1, 3, 8, 0), (6, 8, 9, 0)])
+@pytest.mark.parametrize("dt,w_dt", [("bf16", "f32"), ("f16", "f16"), ("f32", "f32")])
+def test_results_in_other_rows_than_the_inputs(rows, cols, out_stride, out_shift, dt, w_dt):
+    """Aligned inputs, results anywhere; many long rows; nothing past the last row's end."""
+    g = _gen(rows + cols)
+    rand = lambda *s: torch.randn(*s, generator=g, device=DEV)  # noqa: E731
+    wide = (cols + 15) // 8 * 8
+
+    def aligned(v):                             # the last row ends where its buffer does
+        buf = torch.full(((rows - 1) * wide + cols,), float("nan"), dtype=DT[dt], device=DEV)
+        view = torch.as_strided(buf, (rows, cols), (wide, 1))
+        view.copy_(v)
+        return view
+    x, d = aligned(rand(rows, cols) + 2 * rand(rows, 1)), aligned(rand(rows, cols))
+    w, b = (1 + 0.3 * rand(cols)).to(DT[w_dt]), rand(cols).to(DT[w_dt])
+    empty = torch.zeros(rows, cols, device=DEV)
+    out_buf, out = _matrix(empty, DT[dt], out_stride, out_shift, fill=7.0)
+    y = ss.layer_norm(x, w, b, out=out)
+    _forward(x, w, b, 1e-5, y)
+    assert _untouched(out_buf, out, 7.0)
+    dx_buf, d_x = _matrix(empty, DT[dt], out_stride, out_shift, fill=7.0)
+    got = ss.layer_norm_grad(d, x, y.mean, y.rstd, w, d_x=d_x, d_weight=torch.empty_like(w),
+                             d_bias=torch.empty_like(b))
+    _backward(d, x, y.mean, y.rstd, w, got)
+    assert _untouched(dx_buf, d_x, 7.0)
+    _forward(x, None, None, 1e-5, ss.layer_norm(x, out=out))
+    _backward(d, x, y.mean, y.rstd, None, ss.layer_norm_grad(d, x, y.mean, y.rstd, d_x=d_x))
+
+
 @pytest.mark.parametrize("cols", [96, 5003, 20000])
 def test_parts_left_out(cols):
     g = _gen(cols)
