@@ -631,7 +631,7 @@ __device__ __forceinline__ void moments_of(const MatrixItem& x, const MatrixGrou
 template <int T>
 __global__ void __launch_bounds__(256) matrix_moments(const __grid_constant__ MatrixTable t,
                                                       const __grid_constant__ MatrixCall call) {
-    __shared__ double warp_sum[8];
+    __shared__ float warp_sum[8];
     pdl_enter();
     if (skip_step(call.skip)) return;
     const int k = find(t.part0, t.count, blockIdx.x);
@@ -650,13 +650,13 @@ __global__ void __launch_bounds__(256) matrix_moments(const __grid_constant__ Ma
         for (int64_t i = first; i < n / 8; i += next) moments_of<T, 8>(x, g, coef, 8 * i, &sum);
     }
     for (int64_t i = at + first; i < n; i += next) moments_of<T, 1>(x, g, coef, i, &sum);
-    double s = sum;
 #pragma unroll
-    for (int d = 16; d > 0; d /= 2) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-    if (threadIdx.x % 32 == 0) warp_sum[threadIdx.x / 32] = s;
+    for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+    if (threadIdx.x % 32 == 0) warp_sum[threadIdx.x / 32] = sum;
     __syncthreads();
     if (threadIdx.x != 0) return;
-    for (int w = 1; w < 8; ++w) s += warp_sum[w];
+    double s = 0.0;                     // in double from warp to warp
+    for (int w = 0; w < 8; ++w) s += warp_sum[w];
     x.part[part] = s;
 }
 
@@ -666,7 +666,7 @@ template <int T>
 __global__ void __launch_bounds__(256) matrix_image(const __grid_constant__ MatrixTable t,
                                                     const __grid_constant__ MatrixCall call) {
     using S = typename Elem<T>::Store;
-    __shared__ double warp_sum[8];
+    __shared__ float scale;
     __shared__ uint4 out[kBlockBytes / 16];
     pdl_enter();
     if (skip_step(call.skip)) return;
@@ -707,18 +707,23 @@ __global__ void __launch_bounds__(256) matrix_image(const __grid_constant__ Matr
 #pragma unroll
         for (int j = 0; j < 8; ++j) u[p][j] = update_of(x, g, coef, u[p][j], m[j]);
     }
-    const int parts = t.part0[k + 1] - t.part0[k];
-    double s = threadIdx.x < parts ? x.part[threadIdx.x] : 0.0;
+    // by one warp: an SM has few double-precision units (9.4M elements: the pass takes 26 us,
+    // and 37 where every thread forms the scale)
+    if (threadIdx.x < 32) {
+        const int parts = t.part0[k + 1] - t.part0[k];
+        double s = 0.0;
 #pragma unroll
-    for (int d = 16; d > 0; d /= 2) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-    if (threadIdx.x % 32 == 0) warp_sum[threadIdx.x / 32] = s;
+        for (int q = 0; q < kMatrixParts / 32; ++q)
+            if (threadIdx.x + 32 * q < parts) s += x.part[threadIdx.x + 32 * q];
+#pragma unroll
+        for (int d = 16; d > 0; d /= 2) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+        // a sum that is not finite leaves nothing finite
+        if (threadIdx.x == 0)
+            scale = s <= 1.7976931348623157e308
+                        ? static_cast<float>(kImageScaleX / (sqrt(s) + call.eps))
+                        : __int_as_float(0x7FFFFFFF);
+    }
     __syncthreads();
-    s = 0.0;
-    for (int w = 0; w < 8; ++w) s += warp_sum[w];
-    // a sum that is not finite leaves nothing finite
-    const bool finite = s <= 1.7976931348623157e308;
-    const float scale = finite ? static_cast<float>(kImageScaleX / (sqrt(s) + call.eps))
-                               : __int_as_float(0x7FFFFFFF);
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
         const int q = p * 256 + threadIdx.x;
