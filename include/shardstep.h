@@ -1008,7 +1008,8 @@ int rows_layer_norm_grad(const void* d_out, int64_t d_out_stride, const void* x,
  * values held as two halves each (22 bits): single precision.  For long matrices two
  * or three rounds are taken together, which forms the same polynomial in fewer
  * operations.  A matrix that holds an inf or NaN (or an element whose square passes
- * fp32's range) gives NaNs; eps 0 gives NaNs for a matrix of zeros.
+ * fp32's range) gives NaNs.  Squares below fp32's range count as zeros, and |u| of 0
+ * with eps 0 gives NaNs.
  *   rounds        1..64.
  *   a, b, c       such that, of the singular values s that [0, 1] leads to, none
  *                 passes 1.39 in any round, |b + c s^2| stays below 7.9 and

@@ -1312,7 +1312,8 @@ class _Scratch:
     """Device workspace kept from call to call, so that a call allocates nothing
     once it is large enough.  It carries no results and may hold anything; calls
     that may run at the same time (on different streams, or in graphs replayed
-    beside each other) need workspaces of their own.  A buffer that a CUDA graph
+    beside each other) need workspaces of their own, and calls on different streams
+    that share one must be ordered by the caller.  A buffer that a CUDA graph
     has captured stays alive with the workspace when a later call needs a larger
     one, so the workspace must live as long as the graph."""
 
@@ -1618,7 +1619,7 @@ def orthogonalize(matrices, out=None, *, rounds: int = 5, coefficients=QUINTIC,
         if out is None:
             outs = [torch.empty(s, dtype=t.dtype, device=dev) for s, t in zip(shapes, ins.tensors)]
             out = outs[0] if single else outs
-        outs = [out] if single else list(out)
+        outs = [out] if single else list(out.tensors if isinstance(out, TensorList) else out)
         if [t.shape for t in outs] != shapes:
             raise ValueError("out must match the matrices one by one")
         _need_cuda(*outs)
@@ -1732,7 +1733,9 @@ class TensorMuon:
                 raise ValueError("a buffer of the state changed its size or dtype")
             self._check_groups()
         given, grads = grads, _tensor_list(grads)
-        if grads.numels != self.numels:
+        # a flat piece of a bucket is taken, a matrix of another shape is not
+        if grads.numels != self.numels or any(
+                t.shape != s for t, s in zip(grads.tensors, self.shapes) if t.dim() > 1):
             raise ValueError("gradients must match the parameters one by one")
         if grads.device != self.master.device:
             raise ValueError("gradients on another device than the parameters")
@@ -1752,8 +1755,8 @@ class TensorMuon:
 
     def step(self, grads, grad_coef=None, skip=None, stream=None):
         """One step on ``grads`` (a list or a ``TensorList``, one tensor per
-        parameter): g = grad * ``grad_coef`` (a device fp32 word, e.g. the factor of
-        ``grad_norm_clip``); a non-zero device word ``skip`` leaves everything
+        parameter, of its shape or flat): g = grad * ``grad_coef`` (a device fp32
+        word, e.g. the factor of ``grad_norm_clip``); a non-zero device word ``skip`` leaves everything
         unchanged on the device."""
         if skip is not None and (skip.element_size() != 4 or not skip.is_cuda):
             raise ValueError("skip must be a 4-byte CUDA word")

@@ -285,3 +285,13 @@ def test_waits_that_run_out_are_reported():
     assert ss.device_status(clear=True) & 3
     assert ss.device_status() == 0
     assert torch.equal(ss.orthogonalize(u), want)
+
+
+def test_a_list_as_output():
+    g = _gen(5)
+    us = [torch.randn(40, 30, device=DEV, generator=g), torch.randn(9, 70, device=DEV, generator=g)]
+    want = ss.orthogonalize(us)
+    outs = ss.TensorList([torch.empty_like(u) for u in us])
+    assert ss.orthogonalize(us, out=outs) is outs
+    for a, b in zip(outs.tensors, want):
+        assert torch.equal(a, b)

@@ -325,3 +325,16 @@ def test_muon_list_checks(wrappers):
     opt.m = opt.m[:5]
     with pytest.raises(ValueError):
         opt._call(grads)
+
+
+def test_muon_refuses_gradients_of_another_shape(wrappers):
+    """As many elements are not enough: the update sees rows and columns."""
+    opt = ss.TensorMuon([_claim(4, 6, dtype=torch.bfloat16)], ss.Muon())
+    opt.master, opt.m = (t.as_subclass(_Claimed) for t in (opt.master, opt.m))
+    opt._call([_claim(4, 6)])
+    opt._call([_claim(24)])                       # a bucket's piece
+    for shape in ((6, 4), (2, 12), (1, 4, 6)):
+        with pytest.raises(ValueError):
+            opt._call([_claim(*shape)])
+        with pytest.raises(ValueError):
+            opt._call(ss.TensorList([_claim(*shape)]))
