@@ -187,13 +187,18 @@ __device__ __forceinline__ Turned turned_at(const Tile& at, int flags, int k) {
     return Turned{!x && k / F::kRows < at.row / F::kRows,
                   (flags & kRightX) || (!x && k / F::kRows < at.col / F::kRows)};
 }
+// Where 64 k of a row of results lie: in a block's rows, or, turned, in 64 of its rows.
+__device__ __forceinline__ const char* operand_at(const void* image, int row, int k, int width,
+                                                  bool turned) {
+    return turned ? block_at(image, k, row, width) + k % 128 * 128
+                  : block_at(image, row, k, width) + row % 128 * 128;
+}
 // 64 k of 128 or 64 rows, hi then lo: a block (its half of each part), or, turned, 64
 // rows of k of one block for each 64 rows.
 template <int ROWS>
-__device__ __forceinline__ void copy_rows(char* to, const void* image, int row, int k, int width,
-                                          bool turned, uint64_t* bar) {
+__device__ __forceinline__ void copy_rows(char* to, const char* from, bool turned,
+                                          uint64_t* bar) {
     if (!turned) {
-        const char* from = block_at(image, row, k, width) + row % 128 * 128;
         if constexpr (ROWS == 128) {
             bulk_load(to, from, kBlockBytes, bar);
         } else {
@@ -205,9 +210,8 @@ __device__ __forceinline__ void copy_rows(char* to, const void* image, int row, 
 #pragma unroll
     for (int j = 0; j < ROWS / 32; ++j)          // hi of all, then lo of all
         bulk_load(to + j * 8192,
-                  block_at(image, k, row + j % (ROWS / 64) * 64, width) +
-                      j / (ROWS / 64) * (kBlockBytes / 2) + k % 128 * 128,
-                  8192, bar);
+                  from + j % (ROWS / 64) * kBlockBytes + j / (ROWS / 64) * (kBlockBytes / 2), 8192,
+                  bar);
 }
 
 // Waits until `count` warps' parts of a matrix's tiles are written.
@@ -404,6 +408,12 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                 const int row = at.row + 128 * rank, col = at.col + F::kRightRows * rank;
                 for (int k = 0; k < at.k; k += 64, ++issued) {
                     const uint32_t s = issued % kStages;
+                    const Turned turned = turned_at<F>(at, step.flags, k);
+                    const char* from_left = operand_at(left, row, k, at.k, turned.left);
+                    const char* from_right = operand_at(
+                        right, col, k, step.flags & kRightX ? x.np : at.k, turned.right);
+                    // formed before the wait, not after it
+                    asm volatile("" : "+l"(from_left), "+l"(from_right));
                     if (issued >= kStages &&
                         !mbar_wait(&sh.empty[s], (issued / kStages - 1) & 1, limit_ns)) {
                         ok = false;
@@ -411,10 +421,8 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                     }
                     char* to = ring + s * F::kStageBytes;
                     mbar_expect_tx(&sh.full[s], F::kStageBytes);
-                    const Turned turned = turned_at<F>(at, step.flags, k);
-                    copy_rows<128>(to, left, row, k, at.k, turned.left, &sh.full[s]);
-                    copy_rows<F::kRightRows>(to + kBlockBytes, right, col, k,
-                                             step.flags & kRightX ? x.np : at.k, turned.right,
+                    copy_rows<128>(to, from_left, turned.left, &sh.full[s]);
+                    copy_rows<F::kRightRows>(to + kBlockBytes, from_right, turned.right,
                                              &sh.full[s]);
                 }
             }
@@ -442,21 +450,24 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                     const int end = at.k - k0 < kPiece ? at.k : k0 + kPiece;
                     for (int k = k0; k < end; k += 64, ++used) {
                         const uint32_t s = used % kStages;
+                        const uint32_t a = smem_addr(ring + s * F::kStageBytes);
+                        const uint32_t b = a + kBlockBytes;
+                        const Turned turned = turned_at<F>(at, flags, k);
+                        uint32_t form =
+                            half_product(F::kRows, F::kCols, turned.left, turned.right);
+                        // 16 k are 32 bytes along the rows, or 16 rows of 128 bytes
+                        uint64_t ah = turned.left ? mn_major(a, 8192) : k_major(a);
+                        uint64_t bh = turned.right ? mn_major(b, 8192) : k_major(b);
+                        uint64_t next_a = turned.left ? 2048 / 16 : 32 / 16;
+                        uint64_t next_b = turned.right ? 2048 / 16 : 32 / 16;
+                        // formed before the wait, not after it
+                        asm volatile("" : "+r"(form), "+l"(ah), "+l"(bh), "+l"(next_a),
+                                     "+l"(next_b));
                         ok = mbar_wait(&sh.full[s], (used / kStages) & 1, limit_ns);
                         if (kPair && ok)
                             ok = mbar_wait_pair(&sh.peer[s], (used / kStages) & 1, limit_ns);
                         if (!ok) break;
                         tmem_fence_after();
-                        const uint32_t a = smem_addr(ring + s * F::kStageBytes);
-                        const uint32_t b = a + kBlockBytes;
-                        const Turned turned = turned_at<F>(at, flags, k);
-                        const uint32_t form =
-                            half_product(F::kRows, F::kCols, turned.left, turned.right);
-                        // 16 k are 32 bytes along the rows, or 16 rows of 128 bytes
-                        uint64_t ah = turned.left ? mn_major(a, 8192) : k_major(a);
-                        uint64_t bh = turned.right ? mn_major(b, 8192) : k_major(b);
-                        const uint64_t next_a = turned.left ? 2048 / 16 : 32 / 16;
-                        const uint64_t next_b = turned.right ? 2048 / 16 : 32 / 16;
 #pragma unroll
                         for (int q = 0; q < 4; ++q, ah += next_a, bh += next_b) {
                             const uint64_t al = ah + kBlockBytes / 2 / 16;
