@@ -1422,11 +1422,11 @@ def embedding(table, ids, *, scale: float = 1.0, out=None, stream=None):
     with _here(dev, stream):
         if out is None:
             out = torch.empty(*ids.shape, dim, dtype=table.dtype, device=dev)
-        elif out.dtype is not table.dtype:
-            raise ValueError("out must have the table's dtype")
-        to, rows, out_stride = _rows(out, dim, "out")
-        if rows != n:
-            raise ValueError(f"out must have {n} rows")
+            to, out_stride = out.data_ptr(), dim
+        else:
+            to, rows, out_stride = _rows(out, dim, "out")
+            if out.dtype is not table.dtype or rows != n:
+                raise ValueError(f"out must have {n} rows of the table's dtype")
         _one_device(dev, ids, out)
         rc = _capi.lib().token_embedding(at, stride, _dtype_code(table), vocab, dim,
                                          ids.data_ptr(), id_bytes, n, scale, to, out_stride,
@@ -1480,14 +1480,18 @@ class LayerNormGrad(NamedTuple):
 
 def _norm_vector(t, cols, dtype, what):
     """Device address of a weight, bias or gradient of theirs."""
-    import torch
     if t is None:
         return None
     if t.numel() != cols or not t.is_cuda or not t.is_contiguous() or (
-            t.dtype is not dtype and t.dtype is not torch.float32):
+            t.dtype is not dtype and not _is_f32(t)):
         raise ValueError(f"{what} must be a contiguous CUDA tensor of {cols} elements, of x's "
                          "dtype or fp32")
     return t.data_ptr()
+
+
+def _is_f32(t):
+    import torch
+    return t.dtype is torch.float32
 
 
 def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, out=None,
@@ -1510,19 +1514,23 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, out=None,
     if weight is not None and bias is not None and weight.dtype is not bias.dtype:
         raise ValueError("weight and bias must have one dtype")
     given = weight if weight is not None else bias if bias is not None else x
+    code = _dtype_code(x)
     with _here(dev, stream):
         if out is None:
             out = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        elif out.dtype is not x.dtype or out.shape != x.shape:
-            raise ValueError("out must have x's dtype and shape")
-        to, _, out_stride = _rows(out, cols, "out")
+            to, out_stride = out.data_ptr(), cols
+        else:
+            if out.dtype is not x.dtype or out.shape != x.shape:
+                raise ValueError("out must have x's dtype and shape")
+            to, _, out_stride = _rows(out, cols, "out")
         _one_device(dev, weight, bias, out)
         # two tensors, not two views of one: half the host's time
         mean = torch.empty(rows, dtype=torch.float32, device=dev)
         rstd = torch.empty(rows, dtype=torch.float32, device=dev)
-        rc = _capi.lib().rows_layer_norm(at, stride, _dtype_code(x), rows, cols, w, b,
-                                         _dtype_code(given), eps, to, out_stride,
-                                         mean.data_ptr(), rstd.data_ptr(), _stream(stream, dev))
+        rc = _capi.lib().rows_layer_norm(
+            at, stride, code, rows, cols, w, b,
+            code if given.dtype is x.dtype else _capi.DTYPE_F32, eps, to, out_stride,
+            mean.data_ptr(), rstd.data_ptr(), _stream(stream, dev))
     if rc:
         _capi.check("rows_layer_norm", rc)
     return LayerNorm(out, mean, rstd)
@@ -1556,10 +1564,15 @@ def layer_norm_grad(d_out, x, mean, rstd, weight=None, *, d_x=None, d_weight=Non
     w = _norm_vector(weight, cols, x.dtype, "weight")
     dw = _norm_vector(d_weight, cols, x.dtype, "d_weight")
     db = _norm_vector(d_bias, cols, x.dtype, "d_bias")
-    given = [t for t in (weight, d_weight, d_bias) if t is not None]
-    if any(t.dtype is not given[0].dtype for t in given):
-        raise ValueError("weight, d_weight and d_bias must have one dtype")
+    of = x.dtype                          # of weight, d_weight and d_bias
+    for t in (d_bias, d_weight, weight):
+        if t is not None:
+            of = t.dtype
+    for t in (d_bias, d_weight):
+        if t is not None and t.dtype is not of:
+            raise ValueError("weight, d_weight and d_bias must have one dtype")
     lib = _capi.lib()
+    code = _dtype_code(x)
     with _here(dev, stream):
         if d_x is None and dw is None and db is None:
             d_x = torch.empty(x.shape, dtype=x.dtype, device=dev)
@@ -1571,10 +1584,10 @@ def layer_norm_grad(d_out, x, mean, rstd, weight=None, *, d_x=None, d_weight=Non
         if dw is not None or db is not None:
             ws, ws_bytes, held = _scratch(workspace, LayerNormWorkspace, dev,
                                           lib.rows_layer_norm_workspace_bytes(cols))
-        rc = lib.rows_layer_norm_grad(d_at, d_stride, at, stride, _dtype_code(x), rows, cols,
+        rc = lib.rows_layer_norm_grad(d_at, d_stride, at, stride, code, rows, cols,
                                       mean.data_ptr(), rstd.data_ptr(), w,
-                                      _dtype_code(given[0] if given else x), to, to_stride, dw,
-                                      db, int(bool(accumulate)), ws, ws_bytes,
+                                      code if of is x.dtype else _capi.DTYPE_F32, to, to_stride,
+                                      dw, db, int(bool(accumulate)), ws, ws_bytes,
                                       _stream(stream, dev))
     if rc:
         _capi.check("rows_layer_norm_grad", rc)
