@@ -472,7 +472,6 @@ struct NormGradRows {
 // Blocks of the backward pass, each of which leaves one row of column sums; at
 // most kNormPieces.
 constexpr int kNormPieces = 160;
-int norm_pieces(int64_t rows, int64_t cols, int type, bool vec);
 cudaError_t read_norm_status(unsigned int* status, bool clear);
 // vec: the rows that are read, the weights and the bias take vectors; whole: the rows
 // that are written do.

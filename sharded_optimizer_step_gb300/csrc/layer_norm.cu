@@ -11,10 +11,12 @@
 //
 // Forward, a row stays in registers as it is in memory (layer_norm_vectors: 16384 rows
 // of 4096 bf16 in 58 to 61 us, 4.4 TB/s; 20 instructions an element and 6 blocks a SM,
-// bound by their latency), or in shared memory where the results' rows take no vectors
-// (layer_norm_staged).  Backward, rows come through shared memory some 190 KB ahead
-// (layer_norm_staged_grad: 84 us, 4.8 TB/s; 27 instructions an element, issue slots 46%
-// busy, 16 warps a SM for their registers).  A thread holds the same columns of every row
+// bound by their latency).  Backward, rows come through shared memory some 190 KB ahead
+// (layer_norm_staged_grad: 84 us, 4.8 TB/s; 27 instructions an element, issue slots 53%
+// busy, 16 warps a SM for their registers).  Where only the results' rows take no
+// vectors, consecutive threads write consecutive elements: forward by turning each
+// warp's, backward from the shared rows (with turned ones 27.5 us at 999 x 5003 fp32 and
+// 137 at 16384 x 4096 bf16 instead of 23.7 and 112: there are no registers for it).  A thread holds the same columns of every row
 // it meets, so their d_w and d_b stay in its registers until the block's last row; the
 // blocks' sums then go to the workspace and layer_norm_columns adds them in the blocks'
 // order (6 us).  The grid goes by the sizes and the number of SMs alone, so equal calls
@@ -118,15 +120,38 @@ __device__ __forceinline__ void load_weights(const void* p, int c, Pair* w) {
     for (int j = 0; j < N / 2; ++j) w[j] = make_pair(f[2 * j], f[2 * j + 1]);
 }
 
+// A warp's 32 vectors of a row, `c` this lane's column, into elements: consecutive lanes
+// write consecutive ones below `cols`.  All lanes of the warp call it.  (999 rows of 5003
+// fp32 between padded ones and packed ones: forward 13.2 us; 17.9 where whole rows wait in
+// shared memory to be written element by element, 27 where they are read that way too.)
+template <int T, int N>
+__device__ __forceinline__ void store_turned(typename Elem<T>::Store* row, int c, int cols,
+                                             const float* f, uint4* turn) {
+    const int lane = threadIdx.x % 32;
+    uint4* mine = turn + threadIdx.x / 32 * 32;
+    mine[lane] = pack16<T>(f);
+    __syncwarp();
+    const auto* from = reinterpret_cast<const typename Elem<T>::Store*>(mine);
+    const int first = c - lane * N;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (first + 32 * i + lane < cols) row[first + 32 * i + lane] = from[32 * i + lane];
+    __syncwarp();
+}
+
 // Rows of vectors: kept as they are in memory (16 registers for 32 elements of 16
 // bits), so that twice as many rows are on their way as with fp32 copies of them.
 // TAIL: a row ends inside a vector, whose elements go to the first threads one each.
-template <int T, int TW, bool ALONE, bool TAIL>
-__global__ void __launch_bounds__(kNormThreads, T == kGradF32 ? 1 : 2)
+// WHOLE: out's rows take vectors; else a warp turns its 32 vectors into elements through
+// shared memory, so that consecutive lanes write consecutive ones.
+template <int T, int TW, bool ALONE, bool TAIL, bool WHOLE>
+__global__ void __launch_bounds__(ALONE ? kNormThreads : 128,
+                                  T == kGradF32 ? 1 : ALONE ? 2 : WHOLE ? 8 : 6)
     layer_norm_vectors(const NormRows a, int size) {
     using S = typename Elem<T>::Store;
     constexpr int N = Elem<T>::kVec, V = 32 / N;
     __shared__ float2 words[2 * kNormThreads / 32];
+    __shared__ uint4 turn[WHOLE ? 1 : ALONE ? kNormThreads : 128];
     Group<ALONE> g = group_of<ALONE>(size, words);
     const int t = ALONE ? threadIdx.x : threadIdx.x % 32;
     const int groups = ALONE ? 1 : blockDim.x / 32;
@@ -174,16 +199,16 @@ __global__ void __launch_bounds__(kNormThreads, T == kGradF32 ? 1 : 2)
 #pragma unroll
     for (int k = 0; k < V; ++k) {
         const int c = (t + k * size) * N;
-        if (c >= cols) continue;
+        if (WHOLE ? c >= cols : c - threadIdx.x % 32 * N >= cols) continue;   // or the warp's
         Pair y[N / 2], w[N / 2];
 #pragma unroll
         for (int j = 0; j < N / 2; ++j) y[j] = mul2(add2(raw[k].pair(j), off), r2);
-        if (a.w != nullptr) {
+        if (a.w != nullptr && (WHOLE || c < cols)) {
             load_weights<TW, N>(a.w, c, w);
 #pragma unroll
             for (int j = 0; j < N / 2; ++j) y[j] = mul2(y[j], w[j]);
         }
-        if (a.b != nullptr) {
+        if (a.b != nullptr && (WHOLE || c < cols)) {
             load_weights<TW, N>(a.b, c, w);
 #pragma unroll
             for (int j = 0; j < N / 2; ++j) y[j] = add2(y[j], w[j]);
@@ -194,7 +219,11 @@ __global__ void __launch_bounds__(kNormThreads, T == kGradF32 ? 1 : 2)
             f[2 * j] = floats(y[j]).x;
             f[2 * j + 1] = floats(y[j]).y;
         }
-        store_elems<T, N>(out + c, f);
+        if constexpr (WHOLE) {
+            store_elems<T, N>(out + c, f);
+        } else {
+            store_turned<T, N>(out, c, cols, f, turn);
+        }
     }
     if (!mine) return;
     using W = typename Elem<TW>::Store;
@@ -536,118 +565,6 @@ __global__ void __launch_bounds__(staged_threads(T, TAIL), 1)
     }
 }
 
-// Forward in the same way, where x's rows take vectors and out's do not: consecutive
-// threads read vectors of x for the sums and write consecutive elements of out.  Weight
-// and bias are in shared memory too, in fp32.
-constexpr int kForwardThreads = 1024;
-template <int T, int TW, int N, bool TAIL>
-__global__ void __launch_bounds__(kForwardThreads, 1)
-    layer_norm_staged(const NormRows a, const StagedShape sh, unsigned long long limit_ns) {
-    using S = typename Elem<T>::Store;
-    using W = typename Elem<TW>::Store;
-    constexpr int V = 32 / N;
-    extern __shared__ __align__(128) char slots[];
-    __shared__ float2 words[2 * kForwardThreads / 32];
-    __shared__ uint64_t full[kForwardThreads / 32 * 4];    // up to four slots a group
-    const int size = sh.size;
-    Group<false> g = group_of<false>(size, words);
-    const int t = threadIdx.x % size;
-    const int cols = static_cast<int>(a.cols) / N * N;           // in whole vectors
-    const int wide = TAIL ? cols + N : cols;                     // of a slot
-    const int tail = cols + t;
-    const bool has = TAIL && tail < static_cast<int>(a.cols);
-    const uint32_t row_bytes = wide * sizeof(S);
-    float* weights = reinterpret_cast<float*>(slots);
-    float* biases = weights + wide;
-    char* mine = slots + 8 * wide + static_cast<size_t>(g.id) * sh.depth * row_bytes;
-    uint64_t* bar = full + g.id * sh.depth;
-    if (t == 0)
-        for (int k = 0; k < sh.depth; ++k) mbar_init(bar + k, 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    pdl_enter();
-    for (int c = threadIdx.x; c < static_cast<int>(a.cols); c += blockDim.x) {
-        weights[c] = a.w != nullptr ? elem_to_f32<TW>(static_cast<const W*>(a.w)[c]) : 1.0f;
-        biases[c] = a.b != nullptr ? elem_to_f32<TW>(static_cast<const W*>(a.b)[c]) : 0.0f;
-    }
-    __syncthreads();
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * sh.groups + g.id;
-    const int64_t next = static_cast<int64_t>(gridDim.x) * sh.groups;
-    const int64_t rows = first < a.rows ? (a.rows - first + next - 1) / next : 0;
-    const auto fetch = [&](int64_t j) {                          // the group's j-th row
-        const int64_t row = first + j * next;
-        const int slot = static_cast<int>(j % sh.depth);
-        char* to = mine + slot * row_bytes;
-        const S* x = static_cast<const S*>(a.x) + row * a.x_stride;
-        uint32_t bytes = row_bytes;
-        if (TAIL && row + 1 == a.rows) {
-            // what follows the last row may not be read: its end goes by itself
-            bytes = cols * sizeof(S);
-            for (int c = cols; c < a.cols; ++c) reinterpret_cast<S*>(to)[c] = x[c];
-        }
-        mbar_expect_tx(bar + slot, bytes);
-        if (!TAIL || bytes > 0) bulk_load(to, x, bytes, bar + slot);
-    };
-    int64_t fetched = 0;
-    if (t == 0)
-        for (; fetched < sh.depth && fetched < rows; ++fetched) fetch(fetched);
-    const float n = static_cast<float>(a.cols);
-    bool late = false;
-    int slot = 0, phase = 0;
-    for (int64_t j = 0; j < rows; ++j) {
-        const int64_t row = first + j * next;
-        if (!late && !mbar_wait(bar + slot, phase, limit_ns)) {
-            late = true;
-            atomicOr(&g_norm_status, kStatusConsumerTimeout);
-        }
-        const S* x = reinterpret_cast<const S*>(mine + slot * row_bytes);
-        Pair sum = make_pair(has ? elem_to_f32<T>(x[tail]) : 0.0f, 0.0f);
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-            const int c = (t + k * size) * N;
-            if (c >= cols) continue;
-            const Raw<T, N> raw{*reinterpret_cast<const uint4*>(x + c)};
-#pragma unroll
-            for (int i = 0; i < N / 2; ++i) sum = add2(sum, raw.pair(i));
-        }
-        // no rounded 1 / n: rows far from 0
-        const float mean = __fdiv_rn(g.sum(floats(sum).x + floats(sum).y), n);
-        // all threads are here: none reads the row before any more
-        if (t == 0 && !late && j > 0 && fetched < rows) fetch(fetched++);
-        const Pair off = make_pair(-mean, -mean);
-        const float end = has ? elem_to_f32<T>(x[tail]) - mean : 0.0f;
-        sum = make_pair(end * end, 0.0f);
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-            const int c = (t + k * size) * N;
-            if (c >= cols) continue;
-            const Raw<T, N> raw{*reinterpret_cast<const uint4*>(x + c)};
-#pragma unroll
-            for (int i = 0; i < N / 2; ++i) {
-                const Pair d = add2(raw.pair(i), off);
-                sum = fma2(d, d, sum);
-            }
-        }
-        const float var = __fdiv_rn(g.sum(floats(sum).x + floats(sum).y), n);
-        const float r = __fdiv_rn(1.0f, __fsqrt_rn(var + a.eps));
-        if (t == 0) {
-            a.mean[row] = mean;
-            a.rstd[row] = r;
-        }
-        S* out = static_cast<S*>(a.out) + row * a.out_stride;
-#pragma unroll 4
-        for (int c = t; c < static_cast<int>(a.cols); c += size)
-            out[c] = elem_from_f32<T>((elem_to_f32<T>(x[c]) - mean) * r * weights[c] + biases[c]);
-        if (++slot == sh.depth) {
-            slot = 0;
-            phase ^= 1;
-        }
-    }
-    if (late && t == 0)      // copies in flight land before the block's memory goes
-        for (int64_t j = fetched > sh.depth ? fetched - sh.depth : 0; j < fetched; ++j)
-            if (!mbar_wait(bar + j % sh.depth, (j / sh.depth) & 1, kDrainNs))
-                atomicOr(&g_norm_status, kStatusDrainTimeout);
-}
-
 // d_w and d_b from the blocks' sums: 32 columns per block, a warp takes every
 // sixteenth of the pieces, the warps' sums are added in their order.
 template <int TW>
@@ -783,11 +700,11 @@ int fit_grad(int64_t cols, bool vec) {
 
 // The groups of a block and their slots: as many groups as leave three slots each (or
 // two, in rows of 32 KB and more).
-StagedShape staged_shape(int64_t cols, int slot_rows, int beside, int es, int threads) {
+StagedShape staged_shape(int64_t cols, int es, int threads) {
     StagedShape s{fit_group(cols, 256, 32), 0, 0};
     const int64_t wide = (cols + 7) / 8 * 8;         // as much as the kernels take, or more
-    const int64_t slot = slot_rows * wide * es;
-    const int64_t room = kStagedBytes - beside * wide;
+    const int64_t slot = 2 * wide * es;              // a row of x and one of d
+    const int64_t room = kStagedBytes - 4 * wide;    // beside the weights
     const int64_t most = std::max<int64_t>(1, room / (3 * slot));
     // where few rows fit, more threads to each; a group of several warps has one of 15
     // barriers
@@ -807,22 +724,7 @@ cudaError_t go_staged(Kernel* kernel, const Args& a, const StagedShape& s, int b
                         tma_wait_limit());
 }
 template <int T, int TW>
-cudaError_t go_staged_rows(const NormRows& a, cudaStream_t stream) {
-    constexpr int N = Elem<T>::kVec;
-    const StagedShape s = staged_shape(a.cols, 1, 8, 16 / N, kForwardThreads);
-    const int64_t need = (a.rows + s.groups - 1) / s.groups;
-    const int blocks = static_cast<int>(std::min<int64_t>(need, device_sms()));
-    return a.cols % N == 0 ? go_staged(layer_norm_staged<T, TW, N, false>, a, s, blocks, stream)
-                           : go_staged(layer_norm_staged<T, TW, N, true>, a, s, blocks, stream);
-}
-
-template <int T, int TW>
 cudaError_t go_rows(const NormRows& a, bool vec, bool whole, cudaStream_t stream) {
-    // results that take no vectors go through shared memory (999 rows of 5003 fp32 in 21
-    // us, by single elements 27); others are faster from registers (16384 of 4096 bf16 in
-    // 58 to 61 us, 84)
-    if (vec && !whole && fit_group(a.cols, 256, 32) != 0) return go_staged_rows<T, TW>(a, stream);
-    vec = vec && whole;
     const int size = fit_rows(a.cols, vec);
     const int64_t most = static_cast<int64_t>(device_sms()) * 8;
     if (size == 0)
@@ -838,17 +740,33 @@ cudaError_t go_rows(const NormRows& a, bool vec, bool whole, cudaStream_t stream
         return launch_after(kernel, grid, dim3(threads), 0, stream, a, size);
     };
     if (!vec) return go(layer_norm_elements<T, TW, 16>);
+    const auto vectors = [&](auto alone, auto tail) {
+        constexpr bool A = decltype(alone)::value, E = decltype(tail)::value;
+        return whole ? go(layer_norm_vectors<T, TW, A, E, true>)
+                     : go(layer_norm_vectors<T, TW, A, E, false>);
+    };
     if (a.cols % N == 0)
-        return size > 32 ? go(layer_norm_vectors<T, TW, true, false>)
-                         : go(layer_norm_vectors<T, TW, false, false>);
-    return size > 32 ? go(layer_norm_vectors<T, TW, true, true>)
-                     : go(layer_norm_vectors<T, TW, false, true>);
+        return size > 32 ? vectors(Const<true>(), Const<false>())
+                         : vectors(Const<false>(), Const<false>());
+    return size > 32 ? vectors(Const<true>(), Const<true>()) : vectors(Const<false>(), Const<true>());
 }
 
 StagedShape grad_shape(int64_t cols, int type) {
     const int es = type == kGradF32 ? 4 : 2;
-    return staged_shape(cols, 2, 4, es, staged_threads(type, cols * es % 16 != 0));
+    return staged_shape(cols, es, staged_threads(type, cols * es % 16 != 0));
 }
+// Blocks of the backward pass, each of which leaves one row of column sums:
+// at most kNormPieces.
+int norm_pieces(int64_t rows, int64_t cols, int type, bool vec) {
+    const int size = fit_grad(cols, vec);
+    if (rows == 0) return 0;
+    if (size == 0) return static_cast<int>(rows < 64 ? rows : 64);
+    const int groups = vec ? grad_shape(cols, type).groups : kNormThreads / size;
+    const int64_t most = std::min(device_sms(), kNormPieces);
+    const int64_t need = (rows + groups - 1) / groups;
+    return static_cast<int>(need < most ? need : most);
+}
+
 template <int T, int TW>
 cudaError_t go_staged_grad(const NormGradRows& a, int blocks, bool whole, cudaStream_t stream) {
     constexpr int N = Elem<T>::kVec;
@@ -909,17 +827,6 @@ cudaError_t by_types(int type, int w_type, F&& f) {
 }
 
 }  // namespace
-
-// Blocks of the backward pass, each of which leaves one row of column sums.
-int norm_pieces(int64_t rows, int64_t cols, int type, bool vec) {
-    const int size = fit_grad(cols, vec);
-    if (rows == 0) return 0;
-    if (size == 0) return static_cast<int>(rows < 64 ? rows : 64);
-    const int groups = vec ? grad_shape(cols, type).groups : kNormThreads / size;
-    const int64_t most = std::min(device_sms(), kNormPieces);
-    const int64_t need = (rows + groups - 1) / groups;
-    return static_cast<int>(need < most ? need : most);
-}
 
 cudaError_t read_norm_status(unsigned int* status, bool clear) {
     cudaError_t e = cudaMemcpyFromSymbol(status, g_norm_status, sizeof(unsigned int));
