@@ -591,9 +591,9 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                                 (at.col + c) % 64 / 8, sum + c, my.out);
                 }
             }
-            // written, for copies as for loads; then another warp of the matrix is done
+            // written, for copies as for loads; then another warp of the matrix is done (the
+            // release is for all lanes' stores that the warp's barrier puts before it)
             asm volatile("fence.proxy.async.global;" ::: "memory");
-            __threadfence();
             __syncwarp();
             if (lane == 0)
                 asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(x.tiles_done)
