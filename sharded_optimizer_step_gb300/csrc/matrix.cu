@@ -25,13 +25,14 @@
 // 1 / sqrt(m n), the smallest that occurs throughout, has its 22 bits up to m n = 2^30.
 //
 // What bounds it: three products of halves each, 1718 TFLOP/s of them sustained, so 573
-// of the results' own; and the operands, which come from L2 (a 256 x 256 tile's 128 KB
-// in 0.79 us, 12 TB/s over all SMs).  Eight matrices of 2048 x 2048 run at 508 (2.71 ms),
-// 14 of a Llama-1B layer pair at 613 counted round by round (7.7 ms: segments do less).
-// A few small matrices are bound by their chain of 15 to 17 steps, 6 to 8 us each beside
-// the products: 0.75 for the first operands, 0.3 to read the sums, 1 to 2 to turn them
-// into halves, 0.9 for the stores to be seen, 1.5 until another SM knows (256 x 256:
-// 106 us).
+// of the results' own; and the operands: an SM takes in 64 bytes a clock, a 128 x 128
+// tile's 64 KB in 0.49 us, and a pair's ring of three such stages turns one over in 2.4 us
+// (0.79 us for a 256 x 256 tile's 64 of k, 1.0 with all SMs loading).  Eight matrices of
+// 2048 x 2048 run at 512 (2.68 ms), 14 of a Llama-1B layer pair at 617 counted round by
+// round (7.65 ms: segments do less).  A few small matrices are bound by their chain of 15
+// to 17 steps, 5 to 7 us each beside the products: 0.75 for the first operands, 0.3 to read
+// the sums, 1 to 2 to turn them into halves, 0.5 for the stores to be seen, 1.5 until
+// another SM knows (256 x 256: 102 us).
 //
 // Layout.  All operands live in the workspace as the images of what shared memory
 // holds: blocks of 128 rows x 64 columns, 16 KB of hi then 16 KB of lo, rows of 128

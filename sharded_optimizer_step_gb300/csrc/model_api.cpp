@@ -236,15 +236,15 @@ void plan_steps(MatrixCall* call, bool segments) {
     }
 }
 
-constexpr double kTileCost[3] = {0.95, 1.0, 1.6}, kLevelCost[3] = {11.5, 13, 18};
+constexpr double kTileCost[3] = {0.95, 1.0, 1.6}, kLevelCost[3] = {10.5, 12, 17};
 // About how long the steps take, in units of 64 k of a 128 x 128 tile (0.49 us; a
 // 256 x 256 tile takes a pair 0.79 us: it copies half as much per product).  A level of
-// steps takes its longest tile and 7 us from the last results to the next products, or
+// steps takes its longest tile and 6 us from the last results to the next products, or
 // the tiles' share per SM.  So the larger tile is taken where there are enough of them
-// for all pairs (12 matrices of 1024 x 1024 take 627 us with it and 737 and 1257 with
-// the smaller ones, 4 of them 384, 303 and 429, one 360, 254 and 234), and segments for
-// long matrices (1024 x 4096 382 us and 482 without, 2048 x 8192 954 and 1472; but 4 of
-// 1024 x 1024 335 and 303).
+// for all pairs (12 matrices of 1024 x 1024 take 614 us with it and 721 and 1244 with
+// the smaller ones, 4 of them 382, 293 and 423, one 354, 243 and 225), and segments for
+// long matrices (1024 x 4096 370 us and 470 without, 2048 x 8192 937 and 1450; but 4 of
+// 1024 x 1024 320 and 293).
 double steps_cost(const MatrixTable& t, const MatrixCall& call, int shape, int sms) {
     const int64_t high = kMatrixTiles[shape][0], wide = kMatrixTiles[shape][1];
     const double each = kTileCost[shape], units = static_cast<double>(sms / (high / 128));
