@@ -167,6 +167,19 @@ def test_results_in_other_rows_than_the_inputs(rows, cols, out_stride, out_shift
     _backward(d, x, y.mean, y.rstd, None, ss.layer_norm_grad(d, x, y.mean, y.rstd, d_x=d_x))
 
 
+@pytest.mark.parametrize("rows,cols,stride,shift", [
+    # groups of 64, 96, 160, 192, 320, .. threads; rows that end behind the last whole vector a
+    # group holds; single elements in groups of 96, 192, 320
+    (300, 1600, 1600, 0), (41, 2560, 2560, 0), (23, 5120, 5128, 0), (700, 1090, 1096, 0),
+    (9, 16391, 16392, 0), (5, 16387, 16392, 0), (6, 8199, 8200, 0), (7, 8195, 8200, 0),
+    (400, 1027, 1032, 0), (130, 1300, 1301, 0), (50, 2500, 2501, 1), (50, 3900, 3901, 0),
+    (40, 6200, 6200, 1), (3, 8193, 8193, 0)])
+@pytest.mark.parametrize("dt,w_dt", [("bf16", "f32"), ("f16", "f16"), ("f32", "f32")])
+def test_groups_of_any_number_of_warps(rows, cols, stride, shift, dt, w_dt):
+    test_forward_and_backward(rows, cols, stride, shift, dt, w_dt)
+    test_results_in_other_rows_than_the_inputs(rows, cols, cols + 1, 1, dt, w_dt)
+
+
 @pytest.mark.parametrize("cols", [96, 5003, 20000])
 def test_parts_left_out(cols):
     g = _gen(cols)
