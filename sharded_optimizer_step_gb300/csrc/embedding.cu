@@ -45,6 +45,10 @@ constexpr int kSortHeld = 32768;   // tokens whose ids a block keeps after its f
 constexpr int kIdsAhead = 4;       // loads of ids in flight per thread
 constexpr int kRowsAhead = 8;      // rows of d_out in flight per thread
 constexpr int kPiecesAhead = 16;   // of the pieces of a run
+// Rows that take no vectors are zeroed by vectors from their first 16-byte boundary on if
+// they are longer than this (32000 of 2047 fp32: the gradient takes 47 us instead of 79;
+// 50257 of 769 bf16 45 instead of 41).
+constexpr int kShortRow = 1024;
 
 __device__ __forceinline__ int64_t load_id(const void* ids, int ids64, int64_t i) {
     return ids64 ? __ldg(static_cast<const long long*>(ids) + i)
@@ -248,9 +252,21 @@ __global__ void __launch_bounds__(256) embedding_sum(const EmbedArgs a, const Em
             if (start[v] != start[v + 1]) continue;
             typename Elem<TOUT>::Store* row =
                 static_cast<typename Elem<TOUT>::Store*>(a.table) + (v0 + v) * a.table_stride;
-            for (int64_t c = static_cast<int64_t>(threadIdx.x) * N; c < a.dim;
-                 c += static_cast<int64_t>(blockDim.x) * N)
-                store_elems<TOUT, N>(row + c, zero);
+            if (N > 1 || a.dim <= kShortRow) {
+                for (int64_t c = static_cast<int64_t>(threadIdx.x) * N; c < a.dim;
+                     c += static_cast<int64_t>(blockDim.x) * N)
+                    store_elems<TOUT, N>(row + c, zero);
+            } else {       // vectors from the row's first 16-byte boundary on
+                constexpr int V = Elem<TOUT>::kVec;
+                const int64_t skew = reinterpret_cast<uintptr_t>(row) / (16 / V) % V;
+                const int64_t head = skew == 0 ? 0 : a.dim < V - skew ? a.dim : V - skew;
+                const int64_t last = head + (a.dim - head) / V * V;
+                for (int64_t c = head + static_cast<int64_t>(threadIdx.x) * V; c < last;
+                     c += static_cast<int64_t>(blockDim.x) * V)
+                    *reinterpret_cast<uint4*>(row + c) = make_uint4(0, 0, 0, 0);
+                if (threadIdx.x < head) store_elems<TOUT, 1>(row + threadIdx.x, zero);
+                if (last + threadIdx.x < a.dim) store_elems<TOUT, 1>(row + last + threadIdx.x, zero);
+            }
         }
         return;
     }

@@ -137,6 +137,15 @@ def test_gradient(n, dim, vocab, kind, dt, grad_dt, accumulate):
     assert bool((_outside(buf, grad) == 7.0).all())
 
 
+@pytest.mark.parametrize("n,dim,vocab,kind", [
+    (40, 2047, 300, "uniform"), (41, 1031, 90, "uniform"), (2, 1025, 40, "none"),
+    (3, 1026, 60, "uniform"), (12, 1028, 50, "one"), (7, 1036, 64, "skewed")])
+@pytest.mark.parametrize("dt,grad_dt", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+def test_absent_rows_that_start_anywhere(n, dim, vocab, kind, dt, grad_dt):
+    """Zeros by vectors within rows of more than 1024 columns at any alignment."""
+    test_gradient(n, dim, vocab, kind, dt, grad_dt, False)
+
+
 def test_gradient_repeats_to_the_bit_and_needs_no_clean_workspace():
     g = _gen(5)
     n, dim, vocab = 5000, 520, 300
