@@ -1324,7 +1324,7 @@ class _Scratch:
 
     def at_least(self, nbytes: int):
         """(address, bytes) of a workspace of that size."""
-        import torch
+        torch = _torch or _load_torch()
         capturing = torch.cuda.is_current_stream_capturing()
         if self.buf is None or self.buf.numel() < nbytes:
             if self._captured:
@@ -1377,6 +1377,29 @@ def _here(device, stream):
 
 _NOWHERE = contextlib.nullcontext()
 
+# torch, once a call has needed it, and what the calls below ask of it each time: an
+# import statement, a context that changes nothing and a chain of comparisons are a
+# quarter of a small call's time.
+_torch, _codes, _device_now, _raw_stream = None, {}, None, None
+
+
+def _load_torch():
+    global _torch, _device_now, _raw_stream
+    import torch
+    _codes.update({torch.bfloat16: _capi.DTYPE_BF16, torch.float32: _capi.DTYPE_F32,
+                   torch.float16: _capi.DTYPE_F16})
+    _device_now = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _torch = torch
+    return torch
+
+
+def _elsewhere(device, stream):
+    """Whether a call on tensors of that device has to change the current device or
+    stream (``_at``) first."""
+    return stream is not None or device.index != _device_now()
+
 
 def _rows(t, cols, what):
     """(address, rows, row stride) of a matrix with contiguous rows, or of a
@@ -1401,8 +1424,7 @@ def _one_device(device, *tensors):
 
 
 def _id_bytes(ids):
-    import torch
-    size = {torch.int64: 8, torch.int32: 4}.get(ids.dtype)
+    size = ids.element_size() if ids.dtype in (_torch.int64, _torch.int32) else None
     if size is None or not ids.is_cuda or not ids.is_contiguous():
         raise ValueError("ids must be contiguous CUDA int64 or int32")
     return size
@@ -1413,24 +1435,27 @@ def embedding(table, ids, *, scale: float = 1.0, out=None, stream=None):
     times ``scale``, in one launch: ``out`` (table's dtype; [*ids.shape, D], or
     [ids.numel(), D] with rows of any stride; allocated if None).  An id outside
     [0, V), such as a padding of -1, gives a row of zeros."""
-    import torch
+    torch = _torch or _load_torch()
     if table.dim() != 2 or not table.shape[0] or not table.shape[1]:
         raise ValueError("table must be a matrix [vocabulary, features]")
     vocab, dim = table.shape
     at, _, stride = _rows(table, dim, "table")
-    id_bytes, n, dev = _id_bytes(ids), ids.numel(), table.device
-    with _here(dev, stream):
-        if out is None:
-            out = torch.empty(*ids.shape, dim, dtype=table.dtype, device=dev)
-            to, out_stride = out.data_ptr(), dim
-        else:
-            to, rows, out_stride = _rows(out, dim, "out")
-            if out.dtype is not table.dtype or rows != n:
-                raise ValueError(f"out must have {n} rows of the table's dtype")
-        _one_device(dev, ids, out)
-        rc = _capi.lib().token_embedding(at, stride, _dtype_code(table), vocab, dim,
-                                         ids.data_ptr(), id_bytes, n, scale, to, out_stride,
-                                         _stream(stream, dev))
+    id_bytes, n, dev, dtype = _id_bytes(ids), ids.numel(), table.device, table.dtype
+    if _elsewhere(dev, stream):
+        with _at(dev, stream):
+            return embedding(table, ids, scale=scale, out=out)
+    if dtype not in _codes:
+        raise TypeError(f"unsupported dtype {dtype} (bf16, fp16 or fp32)")
+    if out is None:
+        out = torch.empty(*ids.shape, dim, dtype=dtype, device=dev)
+        to, out_stride = out.data_ptr(), dim
+    else:
+        to, rows, out_stride = _rows(out, dim, "out")
+        if out.dtype is not dtype or rows != n:
+            raise ValueError(f"out must have {n} rows of the table's dtype")
+    _one_device(dev, ids, out)
+    rc = _capi.lib().token_embedding(at, stride, _codes[dtype], vocab, dim, ids.data_ptr(),
+                                     id_bytes, n, scale, to, out_stride, _raw_stream(dev.index))
     if rc:
         _capi.check("token_embedding", rc)
     return out
@@ -1445,6 +1470,7 @@ def embedding_grad(d_out, ids, grad, *, scale: float = 1.0, accumulate: bool = F
     that occur and leaves the others alone (a table tied to the head, whose gradient
     is there already; micro-batches), else every row is written.  Rows of ``d_out``
     whose id is outside [0, V) are not read.  Returns ``grad``."""
+    _torch or _load_torch()
     if grad.dim() != 2 or not grad.shape[0] or not grad.shape[1]:
         raise ValueError("grad must be a matrix [vocabulary, features]")
     vocab, dim = grad.shape
@@ -1454,13 +1480,18 @@ def embedding_grad(d_out, ids, grad, *, scale: float = 1.0, accumulate: bool = F
     if rows != n:
         raise ValueError(f"d_out must have {n} rows")
     _one_device(dev, ids, d_out)
+    if _elsewhere(dev, stream):
+        with _at(dev, stream):
+            return embedding_grad(d_out, ids, grad, scale=scale, accumulate=accumulate,
+                                  workspace=workspace)
+    if d_out.dtype not in _codes or grad.dtype not in _codes:
+        raise TypeError("d_out and grad must be bf16, fp16 or fp32")
     lib = _capi.lib()
-    with _here(dev, stream):
-        ws, ws_bytes, held = _scratch(workspace, EmbeddingWorkspace, dev,
-                                      lib.token_embedding_grad_workspace_bytes(n, vocab, dim))
-        rc = lib.token_embedding_grad(at, stride, _dtype_code(d_out), ids.data_ptr(), id_bytes, n,
-                                      scale, to, grad_stride, _dtype_code(grad), vocab, dim,
-                                      int(bool(accumulate)), ws, ws_bytes, _stream(stream, dev))
+    ws, ws_bytes, held = _scratch(workspace, EmbeddingWorkspace, dev,
+                                  lib.token_embedding_grad_workspace_bytes(n, vocab, dim))
+    rc = lib.token_embedding_grad(at, stride, _codes[d_out.dtype], ids.data_ptr(), id_bytes, n,
+                                  scale, to, grad_stride, _codes[grad.dtype], vocab, dim,
+                                  int(bool(accumulate)), ws, ws_bytes, _raw_stream(dev.index))
     if rc:
         _capi.check("token_embedding_grad", rc)
     return grad
@@ -1478,20 +1509,15 @@ class LayerNormGrad(NamedTuple):
     d_bias: object    # or None
 
 
-def _norm_vector(t, cols, dtype, what):
+def _norm_vector(t, cols, x, what):
     """Device address of a weight, bias or gradient of theirs."""
     if t is None:
         return None
     if t.numel() != cols or not t.is_cuda or not t.is_contiguous() or (
-            t.dtype is not dtype and not _is_f32(t)):
+            t.dtype is not x.dtype and t.dtype is not _torch.float32) or t.device != x.device:
         raise ValueError(f"{what} must be a contiguous CUDA tensor of {cols} elements, of x's "
-                         "dtype or fp32")
+                         "dtype or fp32, on x's device")
     return t.data_ptr()
-
-
-def _is_f32(t):
-    import torch
-    return t.dtype is torch.float32
 
 
 def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, out=None,
@@ -1504,33 +1530,34 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, out=None,
     ``weight`` and ``bias`` [cols] are of x's dtype or fp32, both the same (None: 1
     and 0).  ``out`` (x's dtype and shape; allocated if None) may not be ``x``.
     ``mean`` and ``rstd`` (fp32, one per row) are what ``layer_norm_grad`` takes."""
-    import torch
-    if not x.dim() or not x.shape[-1]:
+    torch = _torch or _load_torch()
+    shape, dtype, dev = x.shape, x.dtype, x.device
+    if not shape or not shape[-1]:
         raise ValueError("x must have rows")
-    cols, dev = x.shape[-1], x.device
+    cols = shape[-1]
     at, rows, stride = _rows(x, cols, "x")
-    w = _norm_vector(weight, cols, x.dtype, "weight")
-    b = _norm_vector(bias, cols, x.dtype, "bias")
-    if weight is not None and bias is not None and weight.dtype is not bias.dtype:
+    w, b = _norm_vector(weight, cols, x, "weight"), _norm_vector(bias, cols, x, "bias")
+    of = weight.dtype if w is not None else bias.dtype if b is not None else dtype
+    if b is not None and bias.dtype is not of:
         raise ValueError("weight and bias must have one dtype")
-    given = weight if weight is not None else bias if bias is not None else x
-    code = _dtype_code(x)
-    with _here(dev, stream):
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=dev)
-            to, out_stride = out.data_ptr(), cols
-        else:
-            if out.dtype is not x.dtype or out.shape != x.shape:
-                raise ValueError("out must have x's dtype and shape")
-            to, _, out_stride = _rows(out, cols, "out")
-        _one_device(dev, weight, bias, out)
-        # two tensors, not two views of one: half the host's time
-        mean = torch.empty(rows, dtype=torch.float32, device=dev)
-        rstd = torch.empty(rows, dtype=torch.float32, device=dev)
-        rc = _capi.lib().rows_layer_norm(
-            at, stride, code, rows, cols, w, b,
-            code if given.dtype is x.dtype else _capi.DTYPE_F32, eps, to, out_stride,
-            mean.data_ptr(), rstd.data_ptr(), _stream(stream, dev))
+    if _elsewhere(dev, stream):
+        with _at(dev, stream):
+            return layer_norm(x, weight, bias, eps=eps, out=out)
+    if dtype not in _codes:
+        raise TypeError(f"unsupported dtype {dtype} (bf16, fp16 or fp32)")
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=dev)
+        to, out_stride = out.data_ptr(), cols
+    else:
+        if out.dtype is not dtype or out.shape != shape or out.device != dev:
+            raise ValueError("out must have x's dtype, shape and device")
+        to, _, out_stride = _rows(out, cols, "out")
+    # two tensors, not two views of one: half the host's time
+    mean = torch.empty(rows, dtype=torch.float32, device=dev)
+    rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+    rc = _capi.lib().rows_layer_norm(at, stride, _codes[dtype], rows, cols, w, b, _codes[of], eps,
+                                     to, out_stride, mean.data_ptr(), rstd.data_ptr(),
+                                     _raw_stream(dev.index))
     if rc:
         _capi.check("rows_layer_norm", rc)
     return LayerNorm(out, mean, rstd)
@@ -1549,46 +1576,49 @@ def layer_norm_grad(d_out, x, mean, rstd, weight=None, *, d_x=None, d_weight=Non
     dtype, or x's or fp32 without a weight) receive them; None leaves one out, and
     ``d_x`` None with neither of the others allocates it.  ``accumulate`` adds to
     ``d_weight`` and ``d_bias`` instead (micro-batches)."""
-    import torch
-    if not x.dim() or not x.shape[-1]:
+    torch = _torch or _load_torch()
+    shape, dtype, dev = x.shape, x.dtype, x.device
+    if not shape or not shape[-1]:
         raise ValueError("x must have rows")
-    cols, dev = x.shape[-1], x.device
+    cols = shape[-1]
     at, rows, stride = _rows(x, cols, "x")
-    if d_out.dtype is not x.dtype or d_out.shape != x.shape:
+    if d_out.dtype is not dtype or d_out.shape != shape:
         raise ValueError("d_out must have x's dtype and shape")
     d_at, _, d_stride = _rows(d_out, cols, "d_out")
     for t, what in ((mean, "mean"), (rstd, "rstd")):
         if t.dtype is not torch.float32 or t.numel() != rows or not t.is_cuda or (
                 not t.is_contiguous()):
             raise ValueError(f"{what} must be a contiguous CUDA fp32 tensor of {rows} elements")
-    w = _norm_vector(weight, cols, x.dtype, "weight")
-    dw = _norm_vector(d_weight, cols, x.dtype, "d_weight")
-    db = _norm_vector(d_bias, cols, x.dtype, "d_bias")
-    of = x.dtype                          # of weight, d_weight and d_bias
-    for t in (d_bias, d_weight, weight):
-        if t is not None:
-            of = t.dtype
-    for t in (d_bias, d_weight):
-        if t is not None and t.dtype is not of:
-            raise ValueError("weight, d_weight and d_bias must have one dtype")
-    lib = _capi.lib()
-    code = _dtype_code(x)
-    with _here(dev, stream):
-        if d_x is None and dw is None and db is None:
-            d_x = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        if d_x is not None and (d_x.dtype is not x.dtype or d_x.shape != x.shape):
+    w = _norm_vector(weight, cols, x, "weight")
+    dw, db = _norm_vector(d_weight, cols, x, "d_weight"), _norm_vector(d_bias, cols, x, "d_bias")
+    of = (weight.dtype if w is not None else d_weight.dtype if dw is not None
+          else d_bias.dtype if db is not None else dtype)
+    if (dw is not None and d_weight.dtype is not of) or (
+            db is not None and d_bias.dtype is not of):
+        raise ValueError("weight, d_weight and d_bias must have one dtype")
+    if _elsewhere(dev, stream):
+        with _at(dev, stream):
+            return layer_norm_grad(d_out, x, mean, rstd, weight, d_x=d_x, d_weight=d_weight,
+                                   d_bias=d_bias, accumulate=accumulate, workspace=workspace)
+    if dtype not in _codes:
+        raise TypeError(f"unsupported dtype {dtype} (bf16, fp16 or fp32)")
+    if d_x is None and dw is None and db is None:
+        d_x = torch.empty(shape, dtype=dtype, device=dev)
+    to, to_stride = None, cols
+    if d_x is not None:
+        if d_x.dtype is not dtype or d_x.shape != shape:
             raise ValueError("d_x must have x's dtype and shape")
-        to, _, to_stride = _rows(d_x, cols, "d_x") if d_x is not None else (None, rows, cols)
-        _one_device(dev, d_out, mean, rstd, weight, d_x, d_weight, d_bias)
-        ws, ws_bytes, held = None, 0, None
-        if dw is not None or db is not None:
-            ws, ws_bytes, held = _scratch(workspace, LayerNormWorkspace, dev,
-                                          lib.rows_layer_norm_workspace_bytes(cols))
-        rc = lib.rows_layer_norm_grad(d_at, d_stride, at, stride, code, rows, cols,
-                                      mean.data_ptr(), rstd.data_ptr(), w,
-                                      code if of is x.dtype else _capi.DTYPE_F32, to, to_stride,
-                                      dw, db, int(bool(accumulate)), ws, ws_bytes,
-                                      _stream(stream, dev))
+        to, _, to_stride = _rows(d_x, cols, "d_x")
+    _one_device(dev, d_out, mean, rstd, d_x)
+    lib = _capi.lib()
+    ws, ws_bytes, held = None, 0, None
+    if dw is not None or db is not None:
+        ws, ws_bytes, held = _scratch(workspace, LayerNormWorkspace, dev,
+                                      lib.rows_layer_norm_workspace_bytes(cols))
+    rc = lib.rows_layer_norm_grad(d_at, d_stride, at, stride, _codes[dtype], rows, cols,
+                                  mean.data_ptr(), rstd.data_ptr(), w, _codes[of], to, to_stride,
+                                  dw, db, int(bool(accumulate)), ws, ws_bytes,
+                                  _raw_stream(dev.index))
     if rc:
         _capi.check("rows_layer_norm_grad", rc)
     return LayerNormGrad(d_x, d_weight, d_bias)

@@ -235,6 +235,7 @@ def wrappers(monkeypatch):
             raise AssertionError(f"{name} was reached")
     monkeypatch.setattr(_capi, "lib", lambda: Never())
     monkeypatch.setattr(ss, "_here", lambda device, stream: contextlib.nullcontext())
+    monkeypatch.setattr(ss, "_elsewhere", lambda device, stream: False)
     monkeypatch.setattr(ss._Scratch, "at_least", lambda self, nbytes: (4096, nbytes))
 
 
