@@ -979,8 +979,8 @@ int rows_layer_norm(const void* x, int64_t x_stride, int32_t dtype, int64_t rows
                     void* out, int64_t out_stride, float* mean, float* rstd, void* stream);
 
 /* rows_layer_norm_grad -- device, two launches (one without d_weight and d_bias;
- * three for rows of over 8192 columns, or 4096 where rows are not 16-byte aligned).  With xh = (x - mean) rstd and
- * g = d_out weight:
+ * three for rows of more than some 8192 columns, or 4096 where rows are not 16-byte
+ * aligned).  With xh = (x - mean) rstd and g = d_out weight:
  *     d_x = rstd (g - mean(g) - xh mean(g xh))
  *     d_weight = sum over rows of d_out xh,   d_bias = sum over rows of d_out
  * each left out where NULL; with accumulate != 0 d_weight and d_bias are added to.

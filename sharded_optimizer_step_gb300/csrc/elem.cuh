@@ -1,6 +1,6 @@
 // Elements of the three floating types as fp32, one or a 16-byte vector at a
 // time: what the row kernels (embedding.cu, layer_norm.cu) and the matrix
-// kernels' passes over tensors (muon.cu) share.
+// kernels' passes over tensors (matrix.cu) share.
 #pragma once
 
 #include "common.cuh"

@@ -109,12 +109,6 @@ __device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t 
         "r"(smem_addr(src)), "r"(bytes), "l"(policy)
         : "memory");
 }
-// The same of data that is read again, from a shared address.
-__device__ __forceinline__ void bulk_store_plain(void* dst, uint32_t src, uint32_t bytes) {
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src),
-                 "r"(bytes)
-                 : "memory");
-}
 __device__ __forceinline__ void bulk_commit() {
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
@@ -122,10 +116,6 @@ __device__ __forceinline__ void bulk_commit() {
 template <int N>
 __device__ __forceinline__ void bulk_wait_read() {
     asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
-}
-// Until all of this thread's groups are written.
-__device__ __forceinline__ void bulk_wait_written() {
-    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 // Orders this thread's writes to shared memory before later bulk copies that
 // read it (issued after a barrier by another thread).
