@@ -363,7 +363,9 @@ struct StagedShape {
     int size, groups, depth;
 };
 // WHOLE: d_x's rows take vectors; else consecutive threads write consecutive elements.
-template <int T, int TW, int N, bool TAIL, bool WHOLE>
+// WARPS: each warp is a group (sixteen of them: their sums one after another would take 4 of
+// 16 us at 4096 rows of 768).
+template <int T, int TW, int N, bool TAIL, bool WHOLE, bool WARPS>
 __global__ void __launch_bounds__(staged_threads(T, TAIL), 1)
     layer_norm_staged_grad(const NormGradRows a, const StagedShape sh,
                            unsigned long long limit_ns) {
@@ -374,7 +376,7 @@ __global__ void __launch_bounds__(staged_threads(T, TAIL), 1)
     __shared__ float2 words[2 * kNormThreads / 32];
     __shared__ uint64_t full[kStagedThreads / 32 * 4];     // up to four slots a group
     __shared__ float tails[TAIL ? 2 * N * kStagedThreads / 32 : 1];   // sums of the row's end
-    const int size = sh.size;
+    const int size = WARPS ? 32 : sh.size;
     Group<false> g = group_of<false>(size, words);
     const int t = threadIdx.x % size;
     const int cols = static_cast<int>(a.cols) / N * N;           // in whole vectors
@@ -526,6 +528,43 @@ __global__ void __launch_bounds__(staged_threads(T, TAIL), 1)
             if (!mbar_wait(bar + j % sh.depth, (j / sh.depth) & 1, kDrainNs))
                 atomicOr(&g_norm_status, kStatusDrainTimeout);
     if (a.piece == nullptr) return;
+    if constexpr (WARPS) {
+        // the warps' sums to where their rows were (8 bytes a column: two slots of 16 bits
+        // or one of fp32), then added in the warps' order
+        __syncwarp();
+        float* to = reinterpret_cast<float*>(mine);
+        if (has) {
+            to[tail] = tails[2 * (g.id * N + t)];
+            to[wide + tail] = tails[2 * (g.id * N + t) + 1];
+        }
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int c = (t + k * size) * N;
+            if (c >= cols) continue;
+            float fw[N], fb[N];
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) {
+                fw[2 * i] = floats(dw[k][i]).x;
+                fw[2 * i + 1] = floats(dw[k][i]).y;
+                fb[2 * i] = floats(db[k][i]).x;
+                fb[2 * i + 1] = floats(db[k][i]).y;
+            }
+            store_elems<kGradF32, N>(to + c, fw);
+            store_elems<kGradF32, N>(to + wide + c, fb);
+        }
+        __syncthreads();
+        const float* from = reinterpret_cast<const float*>(slots + (a.w != nullptr ? 4 * wide : 0));
+        const int each = static_cast<int>(sh.depth * 2 * row_bytes / sizeof(float));
+        for (int c = threadIdx.x; c < 2 * wide; c += blockDim.x) {
+            const int col = c < wide ? c : c - wide;
+            if (col >= static_cast<int>(a.cols)) continue;
+            float sum = from[c];
+#pragma unroll 4
+            for (int q = 1; q < sh.groups; ++q) sum += from[q * each + c];
+            a.piece[(2 * static_cast<int64_t>(blockIdx.x) + (c >= wide)) * a.pitch + col] = sum;
+        }
+        return;
+    }
     // the groups' sums, added in the groups' order, where the rows were
     float* sums = reinterpret_cast<float*>(slots + (a.w != nullptr ? 4 * wide : 0));
     float* piece = a.piece + static_cast<int64_t>(blockIdx.x) * 2 * a.pitch;
@@ -779,12 +818,15 @@ template <int T, int TW>
 cudaError_t go_staged_grad(const NormGradRows& a, int blocks, bool whole, cudaStream_t stream) {
     constexpr int N = Elem<T>::kVec;
     const StagedShape s = grad_shape(a.cols, T);
-    if (a.cols % N == 0)
+    const auto go = [&](auto tail, auto warps) {
+        constexpr bool E = decltype(tail)::value, P = decltype(warps)::value;
         return whole
-                   ? go_staged(layer_norm_staged_grad<T, TW, N, false, true>, a, s, blocks, stream)
-                   : go_staged(layer_norm_staged_grad<T, TW, N, false, false>, a, s, blocks, stream);
-    return whole ? go_staged(layer_norm_staged_grad<T, TW, N, true, true>, a, s, blocks, stream)
-                 : go_staged(layer_norm_staged_grad<T, TW, N, true, false>, a, s, blocks, stream);
+                   ? go_staged(layer_norm_staged_grad<T, TW, N, E, true, P>, a, s, blocks, stream)
+                   : go_staged(layer_norm_staged_grad<T, TW, N, E, false, P>, a, s, blocks, stream);
+    };
+    if (a.cols % N == 0)
+        return s.size == 32 ? go(Const<false>(), Const<true>()) : go(Const<false>(), Const<false>());
+    return s.size == 32 ? go(Const<true>(), Const<true>()) : go(Const<true>(), Const<false>());
 }
 template <int T, int TW>
 cudaError_t go_elements_grad(const NormGradRows& a, int size, int blocks, cudaStream_t stream) {
