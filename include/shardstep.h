@@ -1005,9 +1005,11 @@ int rows_layer_norm_grad(const void* d_out, int64_t d_out_stride, const void* x,
  * The singular values of the result are those of X under s -> a s + b s^3 + c s^5,
  * `rounds` times; the usual (3.4445, -4.7750, 2.0315), 5 times, brings all but the
  * smallest to between 0.7 and 1.2.  Products are formed on the tensor cores from
- * values held as two halves each (22 bits): single precision.  For long matrices two
- * or three rounds are taken together, which forms the same polynomial in fewer
- * operations.  A matrix that holds an inf or NaN (or an element whose square passes
+ * values held as two halves each (22 bits), with sums in fp32: errors are those of
+ * 32-bit products to a factor of 2 or so, 4 after a single round (2e-7 of the result's
+ * norm).  For matrices whose sides are all 512 or more and which are long enough, two
+ * rounds are taken together, which forms the same polynomial in fewer operations; the
+ * last is always by itself.  A matrix that holds an inf or NaN (or an element whose square passes
  * fp32's range) gives NaNs.  Squares below fp32's range count as zeros, and |u| of 0
  * with eps 0 gives NaNs.
  *   rounds        1..64.

@@ -540,7 +540,7 @@ struct MatrixCall {
     float a, b, c, eps;
     int rounds, out_type;
     float c_scale, c_diagonal;       // C from A, as the images hold them
-    uint32_t tiles, most;            // of all steps, of one level of them
+    uint32_t tiles, most;            // of all steps, of the largest
     int steps;
     MatrixStep step[kMatrixSteps];
 };

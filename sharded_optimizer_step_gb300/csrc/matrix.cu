@@ -12,27 +12,28 @@
 // would stand at the end of every step: they took 6 of its 12 us).  Everything but X
 // is symmetric: its products compute the tiles on and above the diagonal, and where an
 // operand lies below it, the tile from above is read the other way round.  Rounds of
-// long matrices go three or two at a time without forming X between them (plan_steps
-// in model_api.cpp).
+// long matrices go two at a time without forming X between them (plan_steps in
+// model_api.cpp).
 //
 // The tensor cores multiply halves; to keep single precision each value v is held as
 // two, hi = half(s v) and lo = half(s v - hi) with s a power of two: 22 bits, of which
 // three products hi hi + hi lo + lo hi make a product good to about 2^-21.  One product
 // of single halves loses 2e-3 to 2e-2 of the result's norm over five rounds, these three
-// 4e-6 to 1e-5, as much as 32-bit products do.  s is 2^15 for X and A, whose elements
+// 2e-6 to 1e-5 (1e-4 where it holds one direction), 0.6 to 2 times what 32-bit products do.
+// s is 2^15 for X and A, whose elements
 // stay below sqrt(2) and 2, 2^13 for C, below 8, and 2^14 for P, below 4 (the host
 // checks the coefficients for it): nothing overflows, and an element of rms
 // 1 / sqrt(m n), the smallest that occurs throughout, has its 22 bits up to m n = 2^30.
 //
 // What bounds it: three products of halves each, 1718 TFLOP/s of them sustained, so 573
-// of the results' own; and the operands: an SM takes in 64 bytes a clock, a 128 x 128
-// tile's 64 KB in 0.49 us, and a pair's ring of three such stages turns one over in 2.4 us
-// (0.79 us for a 256 x 256 tile's 64 of k, 1.0 with all SMs loading).  Eight matrices of
-// 2048 x 2048 run at 512 (2.68 ms), 14 of a Llama-1B layer pair at 617 counted round by
-// round (7.65 ms: segments do less).  A few small matrices are bound by their chain of 15
-// to 17 steps, 5 to 7 us each beside the products: 0.75 for the first operands, 0.3 to read
-// the sums, 1 to 2 to turn them into halves, 0.5 for the stores to be seen, 1.5 until
-// another SM knows (256 x 256: 102 us).
+// of the results' own; the operands: an SM takes in 64 bytes a clock, a 128 x 128
+// tile's 64 KB in 0.49 us, and a pair's ring of three such stages turns one over in 2.4 us;
+// and the sums: 64 of k take a 128 x 64 tile 0.61 us, a 128 x 128 one 0.76 (the products
+// 0.45), a pair's 256 x 256 one 1.08 to 1.27.  Eight matrices of 2048 x 2048 run at 459
+// (3.0 ms).  A few small matrices are bound by their chain of 15 to 17 steps, 3 to 5 us each
+// beside the products: 0.75 for the first operands, 0.3 to read the sums, 1 to 2 to turn
+// them into halves, 0.5 for the stores to be seen, 1.5 until another SM knows (256 x 256:
+// 94 to 99 us).
 //
 // Layout.  All operands live in the workspace as the images of what shared memory
 // holds: blocks of 128 rows x 64 columns, 16 KB of hi then 16 KB of lo, rows of 128
@@ -53,13 +54,15 @@ __device__ unsigned int g_matrix_status;
 constexpr int kBlockBytes = 32768;            // 128 x 64 halves, hi and lo
 constexpr int kRingBytes = 196608;            // of the stages
 constexpr int kMostStages = 4;
+constexpr int kMostAccs = 4;
 // Results on their way out: each result warp's 32 rows x 32 columns of hi or lo.
 constexpr int kOutPiece = 2048;
-// The tensor cores cut sums off at fp32's last bit instead of rounding them, so a
-// long sum of positive terms (a row's square) falls behind by K / 16 times half a
-// bit.  A sum over k therefore goes in pieces of this many, which the result warps
-// add up in their registers (rounding to nearest).
-constexpr int kPiece = 256;
+// The tensor cores cut a sum's terms off at its last bits instead of rounding it, so a
+// long sum falls short with every product that is added to it.  A sum over k therefore
+// goes in pieces of 64, a stage each, which the result warps add up in their registers
+// (rounding to nearest), and within a piece the small products, hi lo and lo hi, go
+// first: four additions at its full size.  (256 k to a piece, products in turn: errors 3
+// to 10 times those of 32-bit products, with 128 up to twice.)
 
 // A tile of results: 128 x 128 by one block, 128 x 64 where tiles are few (a step's
 // time is then its last tile's), or 256 x 256 by a pair of blocks, which copies half as
@@ -75,7 +78,8 @@ struct Shape {
     static constexpr int kColumns = COLS == 256 ? 128 : 32;     // of a result warp
     static constexpr int kResultWarps = 4 * COLS / kColumns;
     static constexpr int kThreads = 64 + 32 * kResultWarps;
-    static constexpr int kTmemColumns = 2 * COLS;               // two accumulators
+    static constexpr int kAccs = COLS == 256 ? 2 : 4;           // accumulators
+    static constexpr int kTmemColumns = kAccs * COLS;
     static constexpr int kArrivals = kBlocks * kResultWarps;    // per tile
     // a stage: 128 rows and this block's columns, 64 k of each, hi and lo
     static constexpr int kRightRows = COLS / kBlocks;
@@ -104,7 +108,7 @@ struct Work {
 struct Shared {
     uint64_t full[kMostStages], empty[kMostStages];
     uint64_t peer[kMostStages];               // the other block's stage is full
-    uint64_t done[2], taken[2];               // an accumulator is complete / has been read
+    uint64_t done[kMostAccs], taken[kMostAccs];   // an accumulator is complete / has been read
     uint64_t drain;
     uint32_t tmem;
     Work work[16];                            // of each result warp
@@ -351,8 +355,8 @@ __device__ __forceinline__ void finish(const MatrixItem& x, const MatrixCall& c,
 // work.  (The launch is cooperative: all blocks are resident, and a tile waits for
 // earlier ones only.)
 //
-// Warp 0 copies operands into a ring of stages, warp 1 issues the products into one
-// of two accumulators, the others turn the other into results.  In a pair, each
+// Warp 0 copies operands into a ring of stages, warp 1 issues each stage's products into
+// one of a few accumulators, the others add those up and turn the sums into results.  In a pair, each
 // block copies its half of both operands; the first block's warp 1 issues the
 // products of both, and the second's passes on that its stages are full.  Every
 // wait has a limit: past it the block sets the status word, lets its copies and
@@ -377,7 +381,7 @@ __global__ void __launch_bounds__(F::kThreads, 1)
             mbar_init(&sh.empty[s], 1);
             mbar_init(&sh.peer[s], 1);
         }
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < F::kAccs; ++k) {
             mbar_init(&sh.done[k], 1);
             mbar_init(&sh.taken[k], F::kResultWarps * F::kBlocks);
         }
@@ -434,59 +438,59 @@ __global__ void __launch_bounds__(F::kThreads, 1)
                     atomicOr(&g_matrix_status, kStatusDrainTimeout);
         }
     } else if (!skip && warp == 1 && rank == 0) {
-        if (lane == 0) {
-            uint32_t used = 0, n = 0;                     // stages, pieces
-            bool ok = true;
-            for (uint32_t i = unit; ok && i < tiles; i += units) {
-                const Tile at = tile_at<F>(t, call, i);
-                const int flags = call.step[at.step].flags;
-                for (int k0 = 0; ok && k0 < at.k; k0 += kPiece, ++n) {
-                    const uint32_t d = tmem + n % 2 * F::kCols;
-                    if (n >= 2) {
-                        ok = kPair ? mbar_wait_pair(&sh.taken[n % 2], (n / 2 - 1) & 1, limit_ns)
-                                  : mbar_wait(&sh.taken[n % 2], (n / 2 - 1) & 1, limit_ns);
-                        if (!ok) break;
-                    }
-                    tmem_fence_after();
-                    const int end = at.k - k0 < kPiece ? at.k : k0 + kPiece;
-                    for (int k = k0; k < end; k += 64, ++used) {
-                        const uint32_t s = used % kStages;
-                        const uint32_t a = smem_addr(ring + s * F::kStageBytes);
-                        const uint32_t b = a + kBlockBytes;
-                        const Turned turned = turned_at<F>(at, flags, k);
-                        uint32_t form =
-                            half_product(F::kRows, F::kCols, turned.left, turned.right);
-                        // 16 k are 32 bytes along the rows, or 16 rows of 128 bytes
-                        uint64_t ah = turned.left ? mn_major(a, 8192) : k_major(a);
-                        uint64_t bh = turned.right ? mn_major(b, 8192) : k_major(b);
-                        uint64_t next_a = turned.left ? 2048 / 16 : 32 / 16;
-                        uint64_t next_b = turned.right ? 2048 / 16 : 32 / 16;
-                        // formed before the wait, not after it
-                        asm volatile("" : "+r"(form), "+l"(ah), "+l"(bh), "+l"(next_a),
-                                     "+l"(next_b));
-                        ok = mbar_wait(&sh.full[s], (used / kStages) & 1, limit_ns);
-                        if (kPair && ok)
-                            ok = mbar_wait_pair(&sh.peer[s], (used / kStages) & 1, limit_ns);
-                        if (!ok) break;
-                        tmem_fence_after();
+        // the warp stays together and one lane issues: what the products take is then in
+        // uniform registers (moved there from one lane's, 12 products took it 690 clocks)
+        const bool one = elect_one();
+        uint32_t n = 0;                                   // stages, which are pieces
+        bool ok = true;
+        const auto wait = [&](uint64_t* bar, uint32_t parity, bool far) {
+            return __all_sync(0xFFFFFFFFu, far ? mbar_wait_pair(bar, parity, limit_ns)
+                                               : mbar_wait(bar, parity, limit_ns)) != 0;
+        };
+        for (uint32_t i = unit; ok && i < tiles; i += units) {
+            const Tile at = tile_at<F>(t, call, i);
+            const int flags = call.step[at.step].flags;
+            for (int k = 0; k < at.k; k += 64, ++n) {
+                const uint32_t s = n % kStages;
+                const uint32_t d = tmem + n % F::kAccs * F::kCols;
+                const uint32_t a = smem_addr(ring + s * F::kStageBytes);
+                const uint32_t b = a + kBlockBytes;
+                const Turned turned = turned_at<F>(at, flags, k);
+                const uint32_t form = half_product(F::kRows, F::kCols, turned.left, turned.right);
+                // 16 k are 32 bytes along the rows, or 16 rows of 128 bytes
+                const uint32_t ah = turned.left ? mn_major(a, 8192) : k_major(a);
+                const uint32_t bh = turned.right ? mn_major(b, 8192) : k_major(b);
+                const uint32_t next_a = turned.left ? 2048 / 16 : 32 / 16;
+                const uint32_t next_b = turned.right ? 2048 / 16 : 32 / 16;
+                const uint32_t al = ah + kBlockBytes / 2 / 16, bl = bh + F::kRightHalf / 16;
+                if (n >= F::kAccs)
+                    ok = wait(&sh.taken[n % F::kAccs], (n / F::kAccs - 1) & 1, kPair);
+                if (ok) ok = wait(&sh.full[s], (n / kStages) & 1, false);
+                if (kPair && ok) ok = wait(&sh.peer[s], (n / kStages) & 1, true);
+                if (!ok) break;
+                tmem_fence_after();
+                if (one) {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q, ah += next_a, bh += next_b) {
-                            const uint64_t al = ah + kBlockBytes / 2 / 16;
-                            const uint64_t bl = bh + F::kRightHalf / 16;
-                            mma_half<kPair>(d, ah, bh, form, k > k0 || q > 0);
-                            mma_half<kPair>(d, ah, bl, form, true);
-                            mma_half<kPair>(d, al, bh, form, true);
-                        }
-                        mma_commit<kPair>(&sh.empty[s]);
+                    for (int q = 0; q < 4; ++q) {
+                        mma_half<kPair>(d, ah + q * next_a, bl + q * next_b, form, q > 0);
+                        mma_half<kPair>(d, al + q * next_a, bh + q * next_b, form, true);
                     }
-                    if (ok) mma_commit<kPair>(&sh.done[n % 2]);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        mma_half<kPair>(d, ah + q * next_a, bh + q * next_b, form, true);
+                    mma_commit<kPair>(&sh.empty[s]);
+                    mma_commit<kPair>(&sh.done[n % F::kAccs]);
                 }
+                __syncwarp();
             }
+        }
+        if (one) {
             if (!ok) atomicOr(&g_matrix_status, kStatusConsumerTimeout);
             mma_commit<kPair>(&sh.drain);    // the products in flight end before their memory goes
             if (!mbar_wait(&sh.drain, 0, kDrainNs))
                 atomicOr(&g_matrix_status, kStatusDrainTimeout);
         }
+        __syncwarp();
     } else if (!skip && warp == 1) {
         if (lane == 0) {
             uint32_t used = 0;
@@ -539,25 +543,29 @@ __global__ void __launch_bounds__(F::kThreads, 1)
             uint32_t sum[F::kColumns];                   // fp32, then halves
 #pragma unroll
             for (int k = 0; k < F::kColumns; ++k) sum[k] = 0u;
-            for (int k0 = 0; k0 < at.k; k0 += kPiece, ++n) {
+            for (int k = 0; k < at.k; k += 64, ++n) {
                 // every lane waits, so that all of them see the products
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sh.done[n % 2], (n / 2) & 1, limit_ns));
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sh.done[n % F::kAccs],
+                                                       (n / F::kAccs) & 1, limit_ns));
                 if (!ok) break;
                 tmem_fence_after();
+                constexpr int kWide = F::kColumns == 128 ? 32 : 8;   // more take more registers
+                const uint32_t from = my.lanes + n % F::kAccs * F::kCols;
 #pragma unroll
-                for (int c = 0; c < F::kColumns; c += 8) {
-                    uint32_t acc[8];
-                    tmem_load8(my.lanes + n % 2 * F::kCols + c, acc);
+                for (int c = 0; c < F::kColumns; c += kWide) {
+                    uint32_t acc[kWide];
+                    if constexpr (kWide == 32) tmem_load32(from + c, acc);
+                    else tmem_load8(from + c, acc);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        sum[c + k] = __float_as_uint(__uint_as_float(sum[c + k]) +
-                                                     __uint_as_float(acc[k]));
+                    for (int j = 0; j < kWide; ++j)
+                        sum[c + j] = __float_as_uint(__uint_as_float(sum[c + j]) +
+                                                     __uint_as_float(acc[j]));
                 }
                 tmem_fence_before();
                 __syncwarp();
                 if (lane == 0) {                         // the next products may come
-                    if constexpr (kPair) arrive_at_first(&sh.taken[n % 2]);
-                    else mbar_arrive(&sh.taken[n % 2]);
+                    if constexpr (kPair) tmem_read_at_first(&sh.taken[n % F::kAccs]);
+                    else mbar_arrive(&sh.taken[n % F::kAccs]);
                 }
             }
             const MatrixItem& x = t.item[at.matrix];

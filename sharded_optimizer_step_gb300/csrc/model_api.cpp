@@ -173,29 +173,26 @@ bool take_group(const F& item, int32_t at, int32_t end, MatrixTable* t) {
 }
 
 // The products of all rounds.  One round at a time these are A = X X^T, P = a + A C and
-// X = P X.  Rounds can also be taken two or three at a time without forming X in
-// between, since everything is a polynomial in A: A' = (P X)(P X)^T = (A P) P, the next
-// P from it, and X = P'' P' P X.  That is 2 products with X a segment and 5 to 9 without
-// instead of 2 and 1 a round: for 5 rounds of an m x n matrix 14 m^3 + 6 m^2 n
-// (products of symmetric matrices half) instead of 5 m^3 + 15 m^2 n.  What a round
-// leaves of small singular values grows with their square, so three rounds are the
-// most, and only at the start: errors are then those of round by round (1e-5 of the
-// norm; 3 then 2 rounds 1.3e-5 to 1.7e-5 on decaying spectra, round by round 1.4e-5 to
-// 4.5e-5, 2 then 3 rounds 1e-4).
+// X = P X.  Rounds can also be taken two at a time without forming X in between, since
+// everything is a polynomial in A: A' = (P X)(P X)^T = (A P) P, the next P from it, and
+// X = P' P X.  That is 2 products with X and 5 without instead of 4 and 2: for 5 rounds of
+// an m x n matrix 9 m^2 n + 11 m^3 (products of symmetric matrices half) instead of
+// 15 m^2 n + 5 m^3.  Errors of the products between grow where X's own round would have
+// settled them, so the last round is always by itself: two rounds and then one are off by
+// 0.8 to 1.8 times what 32-bit products are at a short side of 512, 0.5 to 1.2 times from
+// 1024 on (round by round 0.6 to 1), but 2 to 5 times at sides of 64 to 256, and three rounds
+// at once, or two at the end, 2 to 10 times everywhere.
 void plan_steps(MatrixCall* call, bool segments) {
     double scale[kImages];
     scale[kX0] = scale[kX1] = scale[kA] = scale[kZ] = kImageScaleX;
     scale[kC] = kImageScaleX / 4;
-    scale[kP0] = scale[kP1] = scale[kQ] = kImageScaleX / 2;
+    scale[kP0] = scale[kP1] = kImageScaleX / 2;
+    scale[kQ] = kImageScaleX / 8;              // its elements are below 3.9 squared
     call->c_scale = static_cast<float>(call->c * scale[kC] / scale[kA]);
     call->c_diagonal = static_cast<float>(call->b * scale[kC]);
-    int sym = 0, full = 0, sym_level = 0, full_level = 0;
+    int sym = 0, full = 0;
     call->steps = 0;
-    const auto add = [&](int left, int right, int out, int flags, bool same_level = false) {
-        if (!same_level) {
-            sym_level = sym;
-            full_level = full;
-        }
+    const auto add = [&](int left, int right, int out, int flags) {
         MatrixStep& s = call->step[call->steps++];
         s = MatrixStep{};
         s.left = static_cast<uint8_t>(left);
@@ -205,66 +202,55 @@ void plan_steps(MatrixCall* call, bool segments) {
         s.scale = static_cast<float>((flags & kLastStep ? 1.0 : scale[out]) /
                                      (scale[left] * scale[right]));
         s.diagonal = right == kC ? static_cast<float>(call->a * scale[out]) : 0.0f;
-        s.sym_before = static_cast<uint16_t>(sym_level);
-        s.full_before = static_cast<uint16_t>(full_level);
+        s.sym_before = static_cast<uint16_t>(sym);
+        s.full_before = static_cast<uint16_t>(full);
         ++(flags & kSymmetric ? sym : full);
     };
     int x = kX0;
     for (int done = 0; done < call->rounds;) {
-        const int left = call->rounds - done;
-        const int take = !segments ? 1 : done == 0 ? std::min(left, 3) : std::min(left, 2);
+        const int take = segments && call->rounds - done > 2 ? 2 : 1;
         add(x, x, kA, kSymmetric | kLeftX | kWithC);
-        int p = kP0, q = kP0;
-        scale[kP0] = scale[kP1] = kImageScaleX / 2;
-        add(kA, kC, p, kSymmetric);
-        for (int k = 1; k < take; ++k) {
-            add(kA, p, kZ, kSymmetric, k > 1);       // beside the last product of the P
-            add(kZ, p, kA, kSymmetric | kWithC);
-            const int next = p ^ kP0 ^ kP1;
-            scale[next] = kImageScaleX / 2;
-            add(kA, kC, next, kSymmetric);
-            // its elements are below 3.9 to the power of the rounds so far
-            const int to = q == kQ ? p : kQ;         // (p is done with by then)
-            scale[to] = kImageScaleX / (k == 1 ? 8 : 32);
-            add(next, q, to, kSymmetric);
-            q = to;
-            p = next;
+        add(kA, kC, kP0, kSymmetric);
+        if (take == 2) {
+            add(kA, kP0, kZ, kSymmetric);
+            add(kZ, kP0, kA, kSymmetric | kWithC);
+            add(kA, kC, kP1, kSymmetric);
+            add(kP1, kP0, kQ, kSymmetric);
         }
         done += take;
-        add(q, x, x ^ 1, kRightX | (done == call->rounds ? kLastStep : 0));
+        add(take == 2 ? kQ : kP0, x, x ^ 1,
+            kRightX | (done == call->rounds ? kLastStep : 0));
         x ^= 1;
     }
 }
 
-constexpr double kTileCost[3] = {0.95, 1.0, 1.6}, kLevelCost[3] = {10.5, 12, 17};
-// About how long the steps take, in units of 64 k of a 128 x 128 tile (0.49 us; a
-// 256 x 256 tile takes a pair 0.79 us: it copies half as much per product).  A level of
-// steps takes its longest tile and 6 us from the last results to the next products, or
-// the tiles' share per SM.  So the larger tile is taken where there are enough of them
-// for all pairs (12 matrices of 1024 x 1024 take 614 us with it and 721 and 1244 with
-// the smaller ones, 4 of them 382, 293 and 423, one 354, 243 and 225), and segments for
-// long matrices (1024 x 4096 370 us and 470 without, 2048 x 8192 937 and 1450; but 4 of
-// 1024 x 1024 320 and 293).
+constexpr int32_t kSegmentSide = 512;   // the shortest side for rounds in twos
+constexpr double kTileUs[3] = {0.61, 0.76, 1.08}, kLevelUs[3] = {3.2, 4.2, 7.1};
+// About how many microseconds the steps take: a tile's 64 of k kTileUs (a 256 x 256 tile
+// takes a pair 1.08: it copies half as much per product), and a step its longest tile and
+// kLevelUs from the last results to the next products, or the tiles' share per SM; within
+// 3 to 7% of 17 lists measured with each tile and grouping.  So the larger tile is taken
+// where there are enough of them for all pairs (12 matrices of 1024 x 1024 take 679 us with
+// it and 803 and 1179 with the smaller ones, 4 of them 375, 308 and 396, one 347, 249 and
+// 205), and rounds in twos for long matrices (1024 x 4096 403 us and 488 without,
+// 2048 x 8192 1167 and 1540; but 4 of 1024 x 1024 322 and 308).
 double steps_cost(const MatrixTable& t, const MatrixCall& call, int shape, int sms) {
     const int64_t high = kMatrixTiles[shape][0], wide = kMatrixTiles[shape][1];
-    const double each = kTileCost[shape], units = static_cast<double>(sms / (high / 128));
+    const double each = kTileUs[shape], units = static_cast<double>(sms / (high / 128));
     double total = 0.0;
-    for (int s = 0; s < call.steps;) {
+    for (int s = 0; s < call.steps; ++s) {
         double work = 0.0, longest = 0.0;
-        const int level = call.step[s].sym_before + call.step[s].full_before;
-        for (; s < call.steps && call.step[s].sym_before + call.step[s].full_before == level; ++s) {
-            const int flags = call.step[s].flags;
-            for (int j = 0; j < t.count; ++j) {
-                const int64_t mp = padded(t.item[j].m, high), np = padded(t.item[j].n, wide);
-                const double side = static_cast<double>(mp / high);
-                const double k = each * static_cast<double>((flags & kLeftX ? np : mp) / 64);
-                work += k * (flags & kSymmetric
-                                 ? side * (side + 1) / 2 * static_cast<double>(high / wide)
-                                 : side * static_cast<double>(np / wide));
-                longest = std::max(longest, k);
-            }
+        const int flags = call.step[s].flags;
+        for (int j = 0; j < t.count; ++j) {
+            const int64_t mp = padded(t.item[j].m, high), np = padded(t.item[j].n, wide);
+            const double side = static_cast<double>(mp / high);
+            const double k = each * static_cast<double>((flags & kLeftX ? np : mp) / 64);
+            work += k * (flags & kSymmetric
+                             ? side * (side + 1) / 2 * static_cast<double>(high / wide)
+                             : side * static_cast<double>(np / wide));
+            longest = std::max(longest, k);
         }
-        total += std::max(work / units + longest / 3, longest + kLevelCost[shape]);
+        total += std::max(work / units + longest / 3, longest + kLevelUs[shape]);
     }
     return total;
 }
@@ -274,7 +260,10 @@ void lay_out(MatrixTable* t, MatrixCall* call, char* ws) {
     const int sms = device_sms();
     double best = 0.0;
     bool segments = false;
+    int32_t shortest = INT32_MAX;
+    for (int j = 0; j < t->count; ++j) shortest = std::min(shortest, t->item[j].m);
     for (const bool split : {false, true}) {
+        if (split && shortest < kSegmentSide) continue;
         plan_steps(call, split);
         for (int shape = 0; shape < 3; ++shape) {
             const double cost = steps_cost(*t, *call, shape, sms);
@@ -319,16 +308,12 @@ void lay_out(MatrixTable* t, MatrixCall* call, char* ws) {
     t->part0[t->count] = part;
     t->image0[t->count] = image;
     call->tiles = call->most = 0;
-    uint32_t level = 0;
     for (int k = 0; k < call->steps; ++k) {
         MatrixStep& s = call->step[k];
-        s.first = call->tiles;
         const uint32_t tiles = s.flags & kSymmetric ? sym : full;
-        level = k > 0 && s.sym_before == call->step[k - 1].sym_before &&
-                        s.full_before == call->step[k - 1].full_before
-                    ? level + tiles : tiles;
+        s.first = call->tiles;
         call->tiles += tiles;
-        call->most = std::max(call->most, level);
+        call->most = std::max(call->most, tiles);
     }
 }
 
