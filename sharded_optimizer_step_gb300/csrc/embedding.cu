@@ -34,6 +34,8 @@
 // sort 12 us (8 for 4096 tokens; its latency: two passes over the ids, 32 warps a
 // block, a block an SM), the sums 58 (396 MB, 71% of the memory's rate as reads and
 // writes alternate), the join 6.
+#include <atomic>
+
 #include "elem.cuh"
 
 namespace shardstep {
@@ -42,6 +44,8 @@ namespace {
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortHeld = 32768;   // tokens whose ids a block keeps after its first scan
+constexpr int kSortBytes = sizeof(uint32_t) * kSortWarps * kEmbedSortRange +
+                           sizeof(int16_t) * kSortHeld;     // of shared memory at most
 constexpr int kIdsAhead = 4;       // loads of ids in flight per thread
 constexpr int kRowsAhead = 8;      // rows of d_out in flight per thread
 constexpr int kPiecesAhead = 16;   // of the pieces of a run
@@ -407,6 +411,22 @@ EmbedPlan embed_plan(int64_t n, int64_t dim) {
     return p;
 }
 
+// Raises the sort's limit of shared memory to the most that any call takes, once per
+// device: a limit of this call's own would hold for a call of another thread too, and
+// the kernel's own words count towards the 48 KB that need none.
+static cudaError_t allow_sort() {
+    static std::atomic<int> done[256];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool known = dev >= 0 && dev < 256;
+    if (known && done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+    e = cudaFuncSetAttribute(embedding_sort, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kSortBytes);
+    if (e == cudaSuccess && known) done[dev].store(1, std::memory_order_relaxed);
+    return e;
+}
+
 cudaError_t launch_embedding_grad(const EmbedArgs& a, EmbedSort s, int in_type, int out_type,
                                   bool vec, cudaStream_t stream) {
     const int sms = device_sms();
@@ -414,10 +434,7 @@ cudaError_t launch_embedding_grad(const EmbedArgs& a, EmbedSort s, int in_type, 
     s.range = static_cast<int>(fair < kEmbedSortRange ? fair : kEmbedSortRange);
     const size_t smem = sizeof(uint32_t) * kSortWarps * s.range +
                         (a.n <= kSortHeld ? sizeof(int16_t) * a.n : 0);
-    cudaError_t e = cudaSuccess;
-    if (smem > 48 * 1024)
-        e = cudaFuncSetAttribute(embedding_sort, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(smem));
+    cudaError_t e = allow_sort();
     if (e != cudaSuccess) return e;
     e = launch_after(embedding_sort, dim3(static_cast<unsigned>((a.vocab + s.range - 1) / s.range)),
                      dim3(kSortThreads), smem, stream, a, s);
