@@ -1353,8 +1353,10 @@ def _scratch(workspace, kind, device, nbytes):
     """(address, bytes, holder) of a call's workspace: the caller's, or one of its own."""
     if workspace is None:
         workspace = kind(device)
-    elif workspace.buf is not None and workspace.buf.device != device:
-        raise ValueError("the workspace is on another device")
+    else:                                   # one without a buffer yet makes it where it says
+        at = _torch.device(workspace.device) if workspace.buf is None else workspace.buf.device
+        if at.type != device.type or at.index not in (None, device.index):
+            raise ValueError("the workspace is on another device")
     return (*workspace.at_least(nbytes), workspace)
 
 
@@ -1644,7 +1646,7 @@ def orthogonalize(matrices, out=None, *, rounds: int = 5, coefficients=QUINTIC,
     Products run on the tensor cores in single precision.  ``out``: matrices of the
     same shapes, contiguous, of one dtype (None: allocated, of the input's dtype).
     Returns ``out``, a tensor if a tensor was given."""
-    import torch
+    torch = _torch or _load_torch()
     single = isinstance(matrices, torch.Tensor)
     given = [matrices] if single else matrices
     known = isinstance(given, TensorList)

@@ -1,0 +1,82 @@
+"""A caller's workspace on another device than the tensors is refused before anything
+is allocated or launched, whether it holds a buffer yet or not.  No GPU: tensors that
+claim to be on one, and a library that must not be reached."""
+import contextlib
+
+import pytest
+import torch
+
+import sharded_optimizer_step_gb300 as ss
+from sharded_optimizer_step_gb300 import _capi
+
+KINDS = (ss.EmbeddingWorkspace, ss.LayerNormWorkspace, ss.MatrixWorkspace)
+
+
+class _Buffer:
+    def __init__(self, device, nbytes):
+        self.device, self.nbytes = torch.device(device), nbytes
+
+    def numel(self):
+        return self.nbytes
+
+
+class _OnGpu(torch.Tensor):
+    is_cuda = True
+    device = torch.device("cuda:0")
+
+
+def _claim(*shape, dtype=torch.float32):
+    return torch.zeros(*shape, dtype=dtype).as_subclass(_OnGpu)
+
+
+@pytest.fixture(autouse=True)
+def _no_gpu(monkeypatch):
+    class Never:
+        def __getattr__(self, name):
+            if name.endswith("workspace_bytes"):
+                return lambda *a: 64
+            raise AssertionError(f"{name} was reached")
+
+    def at_least(self, nbytes):
+        made.append(torch.device(self.device))
+        return 4096, nbytes
+    made = []
+    ss._load_torch()
+    monkeypatch.setattr(_capi, "lib", lambda: Never())
+    monkeypatch.setattr(ss, "_here", lambda device, stream: contextlib.nullcontext())
+    monkeypatch.setattr(ss, "_elsewhere", lambda device, stream: False)
+    monkeypatch.setattr(ss._Scratch, "at_least", at_least)
+    return made
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_only_the_tensors_device(kind, _no_gpu):
+    dev = torch.device("cuda:1")
+    for where in ("cuda:0", "cpu", torch.device("cuda", 2), 0):
+        with pytest.raises(ValueError):
+            ss._scratch(kind(where), kind, dev, 64)
+        held = kind("cuda")
+        held.buf = _Buffer(torch.device(where), 1 << 20)
+        with pytest.raises(ValueError):
+            ss._scratch(held, kind, dev, 64)
+    assert not _no_gpu                                     # nothing was allocated
+    for where in ("cuda", "cuda:1", dev, 1):
+        assert ss._scratch(kind(where), kind, dev, 64)[:2] == (4096, 64)
+    held = kind("cuda")                                    # made while cuda:1 was current
+    held.buf = _Buffer(dev, 1 << 20)
+    assert ss._scratch(held, kind, dev, 64)[2] is held
+    assert ss._scratch(None, kind, dev, 64)[2].device == dev
+
+
+def test_every_call_that_takes_one():
+    x, mean = _claim(5, 8), _claim(5)
+    ids = _claim(5, dtype=torch.int64)
+    calls = [
+        lambda: ss.embedding_grad(x, ids, _claim(9, 8), workspace=ss.EmbeddingWorkspace("cuda:1")),
+        lambda: ss.layer_norm_grad(x, x, mean, mean, d_weight=_claim(8),
+                                   workspace=ss.LayerNormWorkspace("cuda:1")),
+        lambda: ss.orthogonalize(x, out=_claim(5, 8), workspace=ss.MatrixWorkspace("cuda:1")),
+    ]
+    for call in calls:
+        with pytest.raises(ValueError, match="another device"):
+            call()
