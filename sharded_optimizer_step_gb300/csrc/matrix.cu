@@ -628,10 +628,12 @@ __device__ __forceinline__ float update_of(const MatrixItem& x, const MatrixGrou
     return g.nesterov ? fmaf(g.mu, m, g.one_mu * (grad * coef)) : m;
 }
 
-// N elements from i on: the momentum, and the sum of the update's squares.
+// N elements from i on: the momentum, and the sum of the update's squares, in fp32 up to
+// kSquaresMost (which a warp's 32 sums still take), beyond it each square in double.
+constexpr float kSquaresMost = 0x1p120f;
 template <int T, int N>
 __device__ __forceinline__ void moments_of(const MatrixItem& x, const MatrixGroup& g, float coef,
-                                           int64_t i, float* sum) {
+                                           int64_t i, float* sum, double* large) {
     float d[N], m[N] = {};
     load_elems<T, N>(static_cast<const typename Elem<T>::Store*>(x.grad) + i, d);
     if (x.m_buf != nullptr) {
@@ -640,18 +642,25 @@ __device__ __forceinline__ void moments_of(const MatrixItem& x, const MatrixGrou
         for (int k = 0; k < N; ++k) m[k] = fmaf(g.mu, m[k], g.one_mu * (d[k] * coef));
         store_elems<kGradF32, N>(x.m_buf + i, m);
     }
+    float s = *sum;
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-        const float u = update_of(x, g, coef, d[k], m[k]);
-        *sum = fmaf(u, u, *sum);
+        d[k] = update_of(x, g, coef, d[k], m[k]);
+        s = fmaf(d[k], d[k], s);
     }
+    if (s <= kSquaresMost) {
+        *sum = s;
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) *large += static_cast<double>(d[k] * d[k]);
 }
 
 // The momentum, and each part's sum of the update's squares.
 template <int T>
 __global__ void __launch_bounds__(256) matrix_moments(const __grid_constant__ MatrixTable t,
                                                       const __grid_constant__ MatrixCall call) {
-    __shared__ float warp_sum[8];
+    __shared__ double warp_sum[8];
     pdl_enter();
     if (skip_step(call.skip)) return;
     const int k = find(t.part0, t.count, blockIdx.x);
@@ -664,15 +673,22 @@ __global__ void __launch_bounds__(256) matrix_moments(const __grid_constant__ Ma
     const int64_t first = static_cast<int64_t>(part) * 256 + threadIdx.x;
     const int64_t next = static_cast<int64_t>(parts) * 256;
     float sum = 0.0f;
+    double large = 0.0;
     int64_t at = 0;                              // elements done in vectors
     if (x.flat) {
         at = n / 8 * 8;
-        for (int64_t i = first; i < n / 8; i += next) moments_of<T, 8>(x, g, coef, 8 * i, &sum);
+        for (int64_t i = first; i < n / 8; i += next) 
+            moments_of<T, 8>(x, g, coef, 8 * i, &sum, &large);
     }
-    for (int64_t i = at + first; i < n; i += next) moments_of<T, 1>(x, g, coef, i, &sum);
+    for (int64_t i = at + first; i < n; i += next) 
+        moments_of<T, 1>(x, g, coef, i, &sum, &large);
 #pragma unroll
     for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-    if (threadIdx.x % 32 == 0) warp_sum[threadIdx.x / 32] = sum;
+    if (__any_sync(0xFFFFFFFFu, !(large == 0.0))) {
+#pragma unroll
+        for (int d = 16; d > 0; d /= 2) large += __shfl_xor_sync(0xFFFFFFFFu, large, d);
+    }
+    if (threadIdx.x % 32 == 0) warp_sum[threadIdx.x / 32] = sum + large;
     __syncthreads();
     if (threadIdx.x != 0) return;
     double s = 0.0;                     // in double from warp to warp

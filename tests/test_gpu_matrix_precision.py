@@ -81,3 +81,30 @@ def test_rows_element_by_element(shape):
     want = _quintic(u.double(), 5)
     got = ss.orthogonalize(u).double()
     assert bool(((got - want).abs() <= 300 * 2.0 ** -21 * want.abs()).all())
+
+
+@pytest.mark.parametrize("shape", [(150, 170), (256, 256), (600, 2050), (3, 5)])
+@pytest.mark.parametrize("size", [1e18, 6e18, 1.8e19])
+def test_elements_whose_squares_fit(shape, size):
+    """Squares below 3.4e38 whose sum is not: the norm is formed all the same.  (An
+    element beyond gives NaNs.)"""
+    g = torch.Generator(device=DEV).manual_seed(7)
+    small = torch.randn(*shape, generator=g, device=DEV).clamp(-1, 1)
+    u = small * size
+    want = _quintic(u.double(), 5)
+    off, plain = _off(ss.orthogonalize(u), want), _off(_quintic(small, 5), want)
+    assert off <= 4 * plain + 2.0 ** -22, (off, plain)
+    u[-1, -1] = 1.9e19
+    assert bool(torch.isnan(ss.orthogonalize(u)).all())
+
+
+def test_a_step_on_elements_whose_squares_fit():
+    g = torch.Generator(device=DEV).manual_seed(8)
+    params = [torch.randn(300, 200, generator=g, device=DEV).bfloat16() for _ in range(2)]
+    grad = torch.randn(300, 200, generator=g, device=DEV)
+    opt = ss.TensorMuon(params, ss.Muon(lr=1.0, weight_decay=0.0))
+    before = opt.master.clone()
+    opt.step([grad, grad * 2.0 ** 61])                  # the same direction
+    a, b = (opt.view(opt.master, k) - opt.view(before, k) for k in (0, 1))
+    # the masters' own roundings, 2^-24 of values up to 4, beside the results'
+    assert float((a - b).norm()) <= 1e-5 * float(a.norm()) + 2.0 ** -22 * 245
