@@ -1193,8 +1193,10 @@ double shardstep_comm_counter(int32_t reset);
 
 /* Name of the kernel that the calling thread's last successful streaming
  * call launched (fused steps, accumulation, non-finite check; for the bucket
- * all-reduce, the kernel of its last non-empty bucket), e.g.
- * "rs_adamw_cast_vec4<8, bf16> (register-staged)"; "" before the first.
+ * all-reduce, the kernel of its last non-empty bucket; the operators over tensors
+ * and rows, the kernel that forms most of the result, for matrices the last group's), e.g.
+ * "rs_adamw_cast_vec4<8, bf16> (register-staged)" or
+ * "matrix_rounds<256, 256>, rounds in twos"; "" before the first.
  * Host only; the string stays valid until the thread's next such call. */
 const char* shardstep_last_kernel(void);
 

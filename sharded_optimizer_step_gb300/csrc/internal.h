@@ -480,6 +480,9 @@ cudaError_t launch_layer_norm(const NormRows& a, int type, int w_type, bool vec,
 cudaError_t launch_layer_norm_grad(const NormGradRows& a, int type, int w_type, void* d_w,
                                    void* d_b, int accumulate, bool vec, bool whole,
                                    cudaStream_t stream);
+// The kernels that these launch for the rows.
+const char* layer_norm_kernel(int64_t cols, int type, bool vec, bool whole);
+const char* layer_norm_grad_kernel(const NormGradRows& a, int type, bool vec, bool whole);
 
 // ------------------------------------------------ matrices' updates
 // (matrix.cu; host side in model_api.cpp)
@@ -512,6 +515,7 @@ struct MatrixTable {
     uint32_t image0[kMatrices + 1];  // first image block of x
     int32_t count;
     int32_t shape;                   // of the tiles: kMatrixTiles[shape]
+    int32_t twos;                    // rounds are taken two at a time
 };
 struct MatrixGroup {
     float lr_wd, mu, one_mu;

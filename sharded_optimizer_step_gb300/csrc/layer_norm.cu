@@ -885,6 +885,18 @@ cudaError_t read_norm_status(unsigned int* status, bool clear) {
     return cudaMemcpyToSymbol(g_norm_status, &zero, sizeof(unsigned int));
 }
 
+const char* layer_norm_kernel(int64_t cols, int type, bool vec, bool whole) {
+    if (fit_rows(cols, type, vec) == 0) return "layer_norm_wide";
+    return !vec ? "layer_norm_elements" : whole ? "layer_norm_vectors" : "layer_norm_vectors, turned";
+}
+const char* layer_norm_grad_kernel(const NormGradRows& a, int type, bool vec, bool whole) {
+    if (a.rows == 0) return "layer_norm_columns";
+    if (fit_grad(a.cols, type, vec) == 0)
+        return a.d_x != nullptr ? "layer_norm_wide_grad" : "layer_norm_wide_columns";
+    return !vec    ? "layer_norm_elements_grad"
+           : whole ? "layer_norm_staged_grad" : "layer_norm_staged_grad, by elements";
+}
+
 cudaError_t launch_layer_norm(const NormRows& a, int type, int w_type, bool vec, bool whole,
                               cudaStream_t stream) {
     const cudaError_t e = by_types(type, w_type, [&](auto t, auto w) {

@@ -274,6 +274,7 @@ void lay_out(MatrixTable* t, MatrixCall* call, char* ws) {
         }
     }
     plan_steps(call, segments);
+    t->twos = segments;
     const int64_t high = kMatrixTiles[t->shape][0], across = kMatrixTiles[t->shape][1];
     // the longest tiles first, so that the last ones to end are short
     std::sort(t->item, t->item + t->count, [](const MatrixItem& a, const MatrixItem& b) {
@@ -328,6 +329,8 @@ int run_groups(const S& sides, const F& item, int32_t n, MatrixCall* call, int g
             lay_out(t.get(), call, static_cast<char*>(workspace));
             const cudaError_t e = launch_matrices(*t, *call, grad_dtype, stream);
             if (e != cudaSuccess) return cuda_fail(what, e);
+            record_kernel("matrix_rounds<%d, %d>%s", kMatrixTiles[t->shape][0],
+                          kMatrixTiles[t->shape][1], t->twos ? ", rounds in twos" : "");
         }
         at = end;
     }
@@ -380,7 +383,7 @@ int token_embedding(const void* table, int64_t table_stride, int32_t dtype, int6
                      rows_aligned(out, out_stride, n, es) && dim * es % 16 == 0;
     const cudaError_t e = launch_embedding(a, dtype, vec, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail("embedding", e);
-    record_kernel("embedding_lookup<%s>", dtype_name(dtype));
+    record_kernel("embedding_lookup<%s> (%s)", dtype_name(dtype), vec ? "vectors" : "elements");
     return ready_ok();
 }
 
@@ -441,7 +444,8 @@ int token_embedding_grad(const void* d_out, int64_t d_out_stride, int32_t dtype,
     const cudaError_t e = launch_embedding_grad(a, s, dtype, grad_dtype, vec,
                                                 static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail("embedding gradient", e);
-    record_kernel("embedding_sum<%s, %s>", dtype_name(dtype), dtype_name(grad_dtype));
+    record_kernel("embedding_sum<%s, %s> (%s)", dtype_name(dtype), dtype_name(grad_dtype),
+                  vec ? "vectors" : "elements");
     return ready_ok();
 }
 
@@ -476,11 +480,11 @@ int rows_layer_norm(const void* x, int64_t x_stride, int32_t dtype, int64_t rows
     const NormRows a{x, x_stride, out, out_stride, weight, bias, mean, rstd, rows, cols, eps};
     const bool vec =
         rows_aligned(x, x_stride, rows, es) && aligned(weight, 16) && aligned(bias, 16);
-    const cudaError_t e =
-        launch_layer_norm(a, dtype, weight_dtype, vec, rows_aligned(out, out_stride, rows, es),
-                          static_cast<cudaStream_t>(stream));
+    const bool whole = rows_aligned(out, out_stride, rows, es);
+    const cudaError_t e = launch_layer_norm(a, dtype, weight_dtype, vec, whole,
+                                            static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail("layer norm", e);
-    record_kernel("layer_norm_rows<%s>", dtype_name(dtype));
+    record_kernel("%s <%s>", layer_norm_kernel(cols, dtype, vec, whole), dtype_name(dtype));
     return ready_ok();
 }
 
@@ -536,7 +540,7 @@ int rows_layer_norm_grad(const void* d_out, int64_t d_out_stride, const void* x,
         launch_layer_norm_grad(a, dtype, weight_dtype, d_weight, d_bias, accumulate != 0, vec,
                                whole, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail("layer norm gradient", e);
-    record_kernel("layer_norm_rows_grad<%s>", dtype_name(dtype));
+    record_kernel("%s <%s>", layer_norm_grad_kernel(a, dtype, vec, whole), dtype_name(dtype));
     return ready_ok();
 }
 
@@ -589,7 +593,6 @@ int matrices_orthogonalize(const void* const* in, void* const* out, const int64_
                             static_cast<cudaStream_t>(stream));
         rc != SHARDSTEP_OK)
         return rc;
-    record_kernel("matrix_product<last> (tcgen05)");
     return ready_ok();
 } catch (const std::bad_alloc&) {
     return ready_fail(SHARDSTEP_ERR_CAPACITY, "out of host memory");
@@ -678,7 +681,6 @@ int tensors_muon_step(const shardstep_matrix_t* ms, int32_t n, int32_t grad_dtyp
                             static_cast<cudaStream_t>(stream));
         rc != SHARDSTEP_OK)
         return rc;
-    record_kernel("matrix_product<last> (tcgen05)");
     return ready_ok();
 } catch (const std::bad_alloc&) {
     return ready_fail(SHARDSTEP_ERR_CAPACITY, "out of host memory");
