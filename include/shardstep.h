@@ -1013,9 +1013,10 @@ int rows_layer_norm_grad(const void* d_out, int64_t d_out_stride, const void* x,
  * fp32's range) gives NaNs.  Squares below fp32's range count as zeros, and |u| of 0
  * with eps 0 gives NaNs.
  *   rounds        1..64.
- *   a, b, c       such that, of the singular values s that [0, 1] leads to, none
- *                 passes 1.39 in any round, |b + c s^2| stays below 7.9 and
- *                 |a + b s^2 + c s^4| below 3.9. */
+ *   a, b, c       |a| >= 1 (a smaller one shrinks small values round by round, below
+ *                 what halves hold), and such that, of the singular values s that [0, 1]
+ *                 leads to, none passes 1.39 in any round, |b + c s^2| stays below 7.9
+ *                 and |a + b s^2 + c s^4| below 3.9. */
 typedef struct {
     double a, b, c, eps;
     int32_t rounds;

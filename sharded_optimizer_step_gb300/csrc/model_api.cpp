@@ -135,6 +135,9 @@ int take_quintic(const shardstep_quintic_t* q, MatrixCall* call) {
     if (!std::isfinite(q->a) || !std::isfinite(q->b) || !std::isfinite(q->c) ||
         !(q->eps >= 0) || !std::isfinite(q->eps))
         return ready_fail(SHARDSTEP_ERR_INVALID, "a coefficient or eps is out of range");
+    if (std::fabs(q->a) < 1)      // small singular values shrink by it in every round
+        return ready_fail(SHARDSTEP_ERR_INVALID,
+                          "|a| is below 1: values shrink below what halves hold");
     double hi = 1.0;
     for (int32_t k = 0; k < q->rounds; ++k) {
         // X and A are held times 2^15 in halves, which end at 65504, b + c A times 2^13
