@@ -480,7 +480,9 @@ __global__ void __launch_bounds__(staged_threads(T, TAIL), 1)
             }
         }
         const float2 m = g.sum(floats(s1).x + floats(s1).y, floats(s2).x + floats(s2).y);
-        // all threads are here: none reads the row before any more
+        // all threads are here: none reads the row before any more (a warp's shuffles alone
+        // order no reads of shared memory before the next copy into it)
+        if constexpr (WARPS) __syncwarp();
         if (t == 0 && !late && j > 0 && fetched < rows) fetch(fetched++);
         if (a.d_x != nullptr) {
             // r (f - c1 - xh c2) = r f + (x - mean) (-r r c2) - r c1
