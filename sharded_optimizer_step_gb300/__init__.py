@@ -1184,7 +1184,7 @@ class TensorAdamW:
         with _on(stream, dev) if stream is not None else contextlib.nullcontext():
             self.master = torch.zeros(pos, dtype=torch.float32, device=dev)
             for p, o, n in zip(self.params, self.offsets, self.numels):
-                self.master[o:o + n].copy_(p.reshape(-1))
+                self.master[o:o + n].copy_(p.detach().reshape(-1))
             code = torch.float32 if state_bits == 32 else torch.uint8
             self.m = torch.zeros(pos, dtype=code, device=dev)
             self.v = torch.zeros(pos, dtype=code, device=dev)
@@ -1740,7 +1740,7 @@ class TensorMuon:
         with _here(dev, stream):
             self.master = torch.zeros(pos, dtype=torch.float32, device=dev)
             for p, o, n in zip(self.params, self.offsets, self.numels):
-                self.master[o:o + n].copy_(p.reshape(-1))
+                self.master[o:o + n].copy_(p.detach().reshape(-1))
             self.m = torch.zeros(pos, dtype=torch.float32, device=dev)
         self._param_code = _dtype_code(self.params[0])
         self._table = (_capi.Matrix * len(self.params))()
