@@ -1005,9 +1005,10 @@ int rows_layer_norm_grad(const void* d_out, int64_t d_out_stride, const void* x,
  * The singular values of the result are those of X under s -> a s + b s^3 + c s^5,
  * `rounds` times; the usual (3.4445, -4.7750, 2.0315), 5 times, brings all but the
  * smallest to between 0.7 and 1.2.  Products are formed on the tensor cores from
- * values held as two halves each (22 bits), with sums in fp32: errors are those of
- * 32-bit products to a factor of 2 or so, 4 after a single round (2e-7 of the result's
- * norm).  For matrices whose sides are all 512 or more and which are long enough, two
+ * values held as two halves each (22 bits), with sums in fp32: after five rounds
+ * errors are 0.2 to 2.6 times those of 32-bit products (1e-6 to 1e-5 of the result's
+ * norm, 8e-5 where u is one direction), after one or two up to 5 times (2e-7), after
+ * twelve up to 6.  For matrices whose sides are all 512 or more and which are long enough, two
  * rounds are taken together, which forms the same polynomial in fewer operations; the
  * last is always by itself.  A matrix that holds an inf or NaN (or an element whose square passes
  * fp32's range) gives NaNs.  Squares below fp32's range count as zeros, and |u| of 0
@@ -1025,7 +1026,9 @@ typedef struct {
 
 /* matrices_orthogonalize -- device, three launches for each group of up to 64
  * matrices (up to 2 GB of workspace, or one matrix); the third is cooperative, one
- * block per SM.
+ * block per SM.  The tile and whether rounds go in twos are chosen for a group by its
+ * sizes and the GPU's number of SMs: equal calls give equal bits, but a matrix beside
+ * others, or on another GPU, may come out some 1e-5 of its norm apart.
  *   in[n], out[n]      host arrays of device pointers: contiguous matrices of
  *                      rows[i] x cols[i] elements of in_dtype and out_dtype.
  *   rows, cols         0..2^20; a matrix without elements is left out.

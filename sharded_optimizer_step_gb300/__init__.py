@@ -1643,9 +1643,11 @@ def orthogonalize(matrices, out=None, *, rounds: int = 5, coefficients=QUINTIC,
         X = u / (|u| + eps), transposed if taller than wide
         A = X X^T,  X = a X + (b A + c A A) X      ``rounds`` times
 
-    Products run on the tensor cores in single precision.  ``out``: matrices of the
-    same shapes, contiguous, of one dtype (None: allocated, of the input's dtype).
-    Returns ``out``, a tensor if a tensor was given."""
+    Products run on the tensor cores from two halves a value, as exact as 32-bit ones
+    to a factor of 3 after the usual rounds.  Equal calls give equal bits; a matrix's last ones depend on
+    what else is in the list and on the GPU.  ``out``: matrices of the same shapes,
+    contiguous, of one dtype (None: allocated, of the input's dtype).  Returns ``out``,
+    a tensor if a tensor was given."""
     torch = _torch or _load_torch()
     single = isinstance(matrices, torch.Tensor)
     given = [matrices] if single else matrices
@@ -1698,7 +1700,8 @@ class Muon:
 class TensorMuon:
     """The orthogonalised momentum step over a list of parameter matrices (bf16 or
     fp16, one dtype) with an fp32 master copy and fp32 momentum, beside
-    ``TensorAdamW`` for the vectors and tables:
+    ``TensorAdamW`` for the vectors and tables.  The matrices are whole ones: a flat
+    piece of a sharded unit is not a matrix.
 
         m = momentum m + (1 - momentum) g,  u = momentum m + (1 - momentum) g  (nesterov)
         p = p - lr weight_decay p - lr s orthogonalize(u)

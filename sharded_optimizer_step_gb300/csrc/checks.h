@@ -59,7 +59,6 @@ inline int check_ranges(std::vector<Range>* reads, std::vector<Range>* writes) {
     return SHARDSTEP_OK;
 }
 
-
 // The ranges of a call with a few arrays, without allocations.
 struct FewRanges {
     Range r[16];

@@ -12,15 +12,15 @@
 // Forward, a row stays in registers as it is in memory (layer_norm_vectors: 16384 rows
 // of 4096 bf16 in 58 to 61 us, 4.4 TB/s; 20 instructions an element and 6 blocks a SM,
 // bound by their latency).  Backward, rows come through shared memory some 190 KB ahead
-// (layer_norm_staged_grad: 84 us, 4.8 TB/s; 27 instructions an element, issue slots 53%
-// busy, 16 warps a SM for their registers).  Where only the results' rows take no
-// vectors, consecutive threads write consecutive elements: forward by turning each
-// warp's, backward from the shared rows (with turned ones 27.5 us at 999 x 5003 fp32 and
-// 137 at 16384 x 4096 bf16 instead of 23.7 and 112: there are no registers for it).  A thread holds the same columns of every row
-// it meets, so their d_w and d_b stay in its registers until the block's last row; the
-// blocks' sums then go to the workspace and layer_norm_columns adds them in the blocks'
-// order (6 us).  The grid goes by the sizes and the number of SMs alone, so equal calls
-// give equal bits.
+// (layer_norm_staged_grad and layer_norm_columns: 82 to 85 us together, 4.8 TB/s; 27
+// instructions an element, issue slots 53% busy, 16 warps a SM for their registers).  Where
+// only the results' rows take no vectors, consecutive threads write consecutive elements:
+// forward by turning each warp's, backward from the shared rows (with turned ones 27.5 us at
+// 999 x 5003 fp32 and 137 at 16384 x 4096 bf16 instead of 23.7 and 112: there are no
+// registers for it).  A thread holds the same columns of every row it meets, so their d_w and
+// d_b stay in its registers until the block's last row; the blocks' sums then go to the
+// workspace and layer_norm_columns adds them in the blocks' order.  The grid goes by the
+// sizes and the number of SMs alone, so equal calls give equal bits.
 //
 // Rows that are not 16-byte aligned take single elements (layer_norm_elements, up to
 // 8192 columns forward and 4096 backward); wider rows (over 16384 forward and 8192

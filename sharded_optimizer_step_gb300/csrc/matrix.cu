@@ -19,7 +19,7 @@
 // two, hi = half(s v) and lo = half(s v - hi) with s a power of two: 22 bits, of which
 // three products hi hi + hi lo + lo hi make a product good to about 2^-21.  One product
 // of single halves loses 2e-3 to 2e-2 of the result's norm over five rounds, these three
-// 2e-6 to 1e-5 (1e-4 where it holds one direction), 0.6 to 2 times what 32-bit products do.
+// 1e-6 to 1e-5 (8e-5 where u is one direction), 0.2 to 2.6 times what 32-bit products do.
 // s is 2^15 for X and A, whose elements
 // stay below sqrt(2) and 2, 2^13 for C, below 8, and 2^14 for P, below 4 (the host
 // checks the coefficients for it): nothing overflows, and an element of rms
@@ -29,11 +29,12 @@
 // of the results' own; the operands: an SM takes in 64 bytes a clock, a 128 x 128
 // tile's 64 KB in 0.49 us, and a pair's ring of three such stages turns one over in 2.4 us;
 // and the sums: 64 of k take a 128 x 64 tile 0.61 us, a 128 x 128 one 0.76 (the products
-// 0.45), a pair's 256 x 256 one 1.08 to 1.27.  Eight matrices of 2048 x 2048 run at 459
-// (3.0 ms).  A few small matrices are bound by their chain of 15 to 17 steps, 3 to 5 us each
+// 0.45), a pair's 256 x 256 one 1.08 to 1.27.  Eight matrices of 2048 x 2048 run at 477
+// (2.88 ms), 14 of a Llama-1B layer pair at 524 counted round by round (9.0 ms: rounds in
+// twos do less).  A few small matrices are bound by their chain of 15 to 17 steps, 3 to 5 us each
 // beside the products: 0.75 for the first operands, 0.3 to read the sums, 1 to 2 to turn
 // them into halves, 0.5 for the stores to be seen, 1.5 until another SM knows (256 x 256:
-// 94 to 99 us).
+// 92 to 98 us).
 //
 // Layout.  All operands live in the workspace as the images of what shared memory
 // holds: blocks of 128 rows x 64 columns, 16 KB of hi then 16 KB of lo, rows of 128
@@ -356,11 +357,11 @@ __device__ __forceinline__ void finish(const MatrixItem& x, const MatrixCall& c,
 // earlier ones only.)
 //
 // Warp 0 copies operands into a ring of stages, warp 1 issues each stage's products into
-// one of a few accumulators, the others add those up and turn the sums into results.  In a pair, each
-// block copies its half of both operands; the first block's warp 1 issues the
-// products of both, and the second's passes on that its stages are full.  Every
-// wait has a limit: past it the block sets the status word, lets its copies and
-// products in flight end, frees its tensor memory and returns.
+// one of a few accumulators, the others add those up and turn the sums into results.  In a
+// pair, each block copies its half of both operands; the first block's warp 1 issues the
+// products of both, and the second's passes on that its stages are full.  Every wait has a
+// limit: past it the block sets the status word, lets its copies and products in flight
+// end, frees its tensor memory and returns.
 template <class F>
 __global__ void __launch_bounds__(F::kThreads, 1)
     matrix_rounds(const __grid_constant__ MatrixTable t, const __grid_constant__ MatrixCall call,
@@ -743,7 +744,7 @@ __global__ void __launch_bounds__(256) matrix_image(const __grid_constant__ Matr
 #pragma unroll
         for (int j = 0; j < 8; ++j) u[p][j] = update_of(x, g, coef, u[p][j], m[j]);
     }
-    // by one warp: an SM has few double-precision units (9.4M elements: the pass takes 26 us,
+    // by one warp: an SM has few double-precision units (9.4M elements: the pass takes 27 us,
     // and 37 where every thread forms the scale)
     if (threadIdx.x < 32) {
         const int parts = t.part0[k + 1] - t.part0[k];

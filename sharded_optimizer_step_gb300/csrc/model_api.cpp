@@ -181,10 +181,10 @@ bool take_group(const F& item, int32_t at, int32_t end, MatrixTable* t) {
 // X = P' P X.  That is 2 products with X and 5 without instead of 4 and 2: for 5 rounds of
 // an m x n matrix 9 m^2 n + 11 m^3 (products of symmetric matrices half) instead of
 // 15 m^2 n + 5 m^3.  Errors of the products between grow where X's own round would have
-// settled them, so the last round is always by itself: two rounds and then one are off by
-// 0.8 to 1.8 times what 32-bit products are at a short side of 512, 0.5 to 1.2 times from
-// 1024 on (round by round 0.6 to 1), but 2 to 5 times at sides of 64 to 256, and three rounds
-// at once, or two at the end, 2 to 10 times everywhere.
+// settled them, so the last round is always by itself.  Five rounds are then off by up to
+// 1.8 times what 32-bit products are at a short side of 512 and 1.2 from 1024 on (round by
+// round 0.8), but 2.2 to 5.5 times at sides of 64 to 256 (1 to 2), which go round by round;
+// with two rounds at the end up to 2.7 times, with three at once up to 10.
 void plan_steps(MatrixCall* call, bool segments) {
     double scale[kImages];
     scale[kX0] = scale[kX1] = scale[kA] = scale[kZ] = kImageScaleX;
