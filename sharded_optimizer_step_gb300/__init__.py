@@ -1779,6 +1779,7 @@ class TensorMuon:
                 raise ValueError("a parameter changed its shape or dtype")
             if any(b.dtype != torch.float32 or b.numel() < self.flat for b in state):
                 raise ValueError("a buffer of the state changed its size or dtype")
+            _one_device(self.master.device, *held)
             self._check_groups()
         given, grads = grads, _tensor_list(grads)
         # a flat piece of a bucket is taken, a matrix of another shape is not
@@ -1811,6 +1812,7 @@ class TensorMuon:
         coef = _f32_word(grad_coef, "grad_coef") or None
         grads = self._call(grads)
         dev = self.master.device
+        _one_device(dev, grad_coef, skip)
         hp = (_capi.MuonHP * len(self.hps))(*[
             (h.lr, h.momentum, h.weight_decay, h.match_rms, int(bool(h.nesterov)), 0)
             for h in self.hps])

@@ -1,6 +1,7 @@
-"""A caller's workspace on another device than the tensors is refused before anything
-is allocated or launched, whether it holds a buffer yet or not.  No GPU: tensors that
-claim to be on one, and a library that must not be reached."""
+"""What is on another device than the tensors is refused before anything is allocated or
+launched: a caller's workspace, whether it holds a buffer yet or not, and the words,
+buffers and parameters of a step.  No GPU: tensors that claim to be on one, and a library
+that must not be reached."""
 import contextlib
 
 import pytest
@@ -80,3 +81,47 @@ def test_every_call_that_takes_one():
     for call in calls:
         with pytest.raises(ValueError, match="another device"):
             call()
+
+
+class _OnAnother(torch.Tensor):
+    is_cuda = True
+    device = torch.device("cuda:1")
+
+
+def _other(*shape, dtype=torch.float32):
+    return torch.zeros(*shape, dtype=dtype).as_subclass(_OnAnother)
+
+
+@pytest.fixture
+def muon(monkeypatch):
+    made = torch.zeros                                     # the state, where the parameters are
+    monkeypatch.setattr(torch, "zeros", lambda *a, device=None, **k: made(*a, **k).as_subclass(
+        _OnGpu) if device is not None else made(*a, **k))
+    opt = ss.TensorMuon([_claim(4, 6, dtype=torch.bfloat16) for _ in range(2)], ss.Muon())
+    monkeypatch.undo()
+    return opt
+
+
+def test_a_steps_words_and_buffers(muon, monkeypatch):
+    class Never:
+        def __getattr__(self, name):
+            raise AssertionError(f"{name} was reached")
+    monkeypatch.setattr(_capi, "lib", lambda: Never())
+    monkeypatch.setattr(ss, "_here", lambda device, stream: contextlib.nullcontext())
+    monkeypatch.setattr(ss._Scratch, "at_least", lambda self, nbytes: (4096, nbytes))
+    grads = [_claim(4, 6) for _ in range(2)]
+    with pytest.raises(AssertionError, match="was reached"):
+        muon.step(grads, grad_coef=_claim(1), skip=_claim(1, dtype=torch.int32))
+    with pytest.raises(ValueError, match="different devices"):
+        muon.step(grads, grad_coef=_other(1))
+    with pytest.raises(ValueError, match="different devices"):
+        muon.step(grads, skip=_other(1, dtype=torch.int32))
+    with pytest.raises(ValueError):
+        muon.step([_other(4, 6) for _ in range(2)])
+    for what in ("m", "params"):
+        was = getattr(muon, what)
+        setattr(muon, what, _other(muon.flat) if what == "m" else
+                [was[0], _other(4, 6, dtype=torch.bfloat16)])
+        with pytest.raises(ValueError, match="different devices"):
+            muon.step(grads)
+        setattr(muon, what, was)
