@@ -1008,7 +1008,7 @@ int rows_layer_norm_grad(const void* d_out, int64_t d_out_stride, const void* x,
  * values held as two halves each (22 bits), with sums in fp32: after five rounds
  * errors are 0.2 to 2.6 times those of 32-bit products (1e-6 to 1e-5 of the result's
  * norm, 8e-5 where u is one direction), after one or two up to 5 times (2e-7), after
- * twelve up to 6.  For matrices whose sides are all 512 or more and which are long enough, two
+ * twelve up to 6; with other coefficients up to 4 times and 2^-22 of the norm a round.  For matrices whose sides are all 512 or more and which are long enough, two
  * rounds are taken together, which forms the same polynomial in fewer operations; the
  * last is always by itself.  A matrix that holds an inf or NaN (or an element whose square passes
  * fp32's range) gives NaNs.  Squares below fp32's range count as zeros, and |u| of 0

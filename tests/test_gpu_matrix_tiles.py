@@ -49,8 +49,8 @@ def _only_here():
         pytest.skip("the lists are those of 152 SMs")
 
 
-def _quintic(u, rounds=5):
-    a, b, c = ss.QUINTIC
+def _quintic(u, rounds=5, abc=ss.QUINTIC):
+    a, b, c = abc
     x = u / (u.norm() + 1e-7)
     tall = x.shape[0] > x.shape[1]
     x = x.T if tall else x
@@ -60,9 +60,9 @@ def _quintic(u, rounds=5):
     return x.T if tall else x
 
 
-def _bound(u, want, rounds=5):
+def _bound(u, want, rounds=5, abc=ss.QUINTIC):
     """Of the norm of the error."""
-    plain = float((_quintic(u.float(), rounds).double() - want).norm())
+    plain = float((_quintic(u.float(), rounds, abc).double() - want).norm())
     return 4 * plain + 2.0 ** -22 * float(want.norm())
 
 
@@ -83,6 +83,25 @@ def test_every_tile_and_grouping(which, rounds):
         most = _bound(u, want, rounds) if min(u.shape) > 1 else 300 * 2.0 ** -21 * float(want.norm())
         assert float((o.double() - want).norm()) <= most, u.shape
         assert torch.equal(o, r), u.shape
+
+
+@pytest.mark.parametrize("which", LISTS)
+@pytest.mark.parametrize("rounds,abc", [(8, (1.5, -0.5, 0.0)), (6, (1.875, -1.25, 0.375)),
+                                        (4, (-1.5, 0.5, 0.0)), (2, ss.QUINTIC), (7, ss.QUINTIC)])
+def test_every_tile_with_other_rounds_and_coefficients(which, rounds, abc):
+    """2^-22 in every round.  Of a piece's four additions at full size each is cut off, by
+    2^-24 of what is there by then on average (a quarter, a half, three quarters, all of
+    it): 2.5 2^-24 of the result, towards zero.  One product with X in a round, or one with X
+    and one of the two rounds' factors in two: 2.5 2^-24 a round of all products on X's way,
+    five eighths of 2^-22; the halves' roundings go to either side and take less than the
+    rest.  All rounds' add up, where 32-bit products round to either side."""
+    _only_here()
+    g = _gen(rounds)
+    us = [torch.randn(*s, generator=g, device=DEV) for s in LISTS[which] if min(s) > 2]
+    for u, o in zip(us, ss.orthogonalize(us, rounds=rounds, coefficients=abc)):
+        want = _quintic(u.double(), rounds, abc)
+        most = _bound(u, want, rounds, abc) + (rounds - 1) * 2.0 ** -22 * float(want.norm())
+        assert float((o.double() - want).norm()) <= most, u.shape
 
 
 @pytest.mark.parametrize("which", LISTS)
