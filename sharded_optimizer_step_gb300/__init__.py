@@ -791,6 +791,18 @@ def ddp_allreduce_as_ready(rank_grads, bucket_offsets, out, ready: BucketReadine
 
 # ---------------------------------------------------- losses over tokens
 
+def _workspace_on(workspace, device):
+    """That a caller's workspace is on that device, or will be (one without a buffer yet
+    makes it where it says)."""
+    if workspace.buf is not None:
+        at = workspace.buf.device
+    else:
+        import torch
+        at = torch.device(workspace.device)
+    if at.type != device.type or at.index not in (None, device.index):
+        raise ValueError("the workspace is on another device")
+
+
 class LossWorkspace:
     """Device workspace of the token losses, kept from call to call so that a
     call allocates nothing once it is large enough.  It carries no results;
@@ -873,6 +885,8 @@ def _loss_buffers(workspace, n, pairs, norm, device):
             out[:1].fill_(math.log(2.0) * pairs / (norm or pairs))
     if workspace is None:
         workspace = LossWorkspace(device)
+    else:
+        _workspace_on(workspace, device)
     return out, workspace.at_least(n, pairs)
 
 
@@ -1091,6 +1105,8 @@ def grad_norm_clip(grads, max_norm: float, *, loss_scale=None, found_inf=None, o
         raise ValueError("out must be a contiguous CUDA fp32 tensor of 2 elements")
     if found_inf is not None and (found_inf.element_size() != 4 or not found_inf.is_cuda):
         raise ValueError("found_inf must be a 4-byte CUDA word")
+    if workspace is not None:
+        _workspace_on(workspace, dev)
     ws = workspace if workspace is not None else NormWorkspace(dev)
     _capi.check("tensors_grad_norm", _capi.lib().tensors_grad_norm(
         grads._ptrs, grads._numels, len(grads), grads.dtype, max_norm,
@@ -1353,10 +1369,8 @@ def _scratch(workspace, kind, device, nbytes):
     """(address, bytes, holder) of a call's workspace: the caller's, or one of its own."""
     if workspace is None:
         workspace = kind(device)
-    else:                                   # one without a buffer yet makes it where it says
-        at = _torch.device(workspace.device) if workspace.buf is None else workspace.buf.device
-        if at.type != device.type or at.index not in (None, device.index):
-            raise ValueError("the workspace is on another device")
+    else:
+        _workspace_on(workspace, device)
     return (*workspace.at_least(nbytes), workspace)
 
 

@@ -125,3 +125,32 @@ def test_a_steps_words_and_buffers(muon, monkeypatch):
         with pytest.raises(ValueError, match="different devices"):
             muon.step(grads)
         setattr(muon, what, was)
+
+
+@pytest.mark.parametrize("held", [False, True])
+def test_losses_and_the_norm(held, monkeypatch):
+    monkeypatch.setattr(ss, "_LOSS_HEAD", [64])
+    monkeypatch.setattr(ss, "_on", lambda stream, device: contextlib.nullcontext())
+    monkeypatch.setattr(ss.LossWorkspace, "at_least", lambda self, n, pairs: (4096, 64, None))
+    x, f, ids = _claim(6, 9), _claim(6), _claim(6, dtype=torch.int64)
+    plain = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, device=None, **k: plain(*a, **k))
+
+    def spaces(where):
+        loss, norm = ss.LossWorkspace(where), object.__new__(ss.NormWorkspace)
+        norm.buf = torch.zeros(8)
+        norm.buf = (_other if torch.device(where).index == 1 else _claim)(8)
+        if held:
+            loss.buf = _Buffer(where, 1 << 20)
+        return loss, norm
+
+    def calls(loss, norm):
+        yield lambda: ss.policy_loss(x, ids, f, f, workspace=loss, stream=0)
+        yield lambda: ss.preference_loss(x, ids, [6, 0], f, workspace=loss, stream=0)
+        yield lambda: ss.grad_norm_clip([x], 1.0, out=_claim(2), workspace=norm, stream=0)
+    for call in calls(*spaces("cuda:1")):
+        with pytest.raises(ValueError, match="another device"):
+            call()
+    for call in calls(*spaces("cuda:0")):
+        with pytest.raises(AssertionError, match="was reached"):
+            call()
