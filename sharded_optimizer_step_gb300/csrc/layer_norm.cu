@@ -889,7 +889,8 @@ cudaError_t read_norm_status(unsigned int* status, bool clear) {
 
 const char* layer_norm_kernel(int64_t cols, int type, bool vec, bool whole) {
     if (fit_rows(cols, type, vec) == 0) return "layer_norm_wide";
-    return !vec ? "layer_norm_elements" : whole ? "layer_norm_vectors" : "layer_norm_vectors, turned";
+    return !vec    ? "layer_norm_elements"
+           : whole ? "layer_norm_vectors" : "layer_norm_vectors, turned";
 }
 const char* layer_norm_grad_kernel(const NormGradRows& a, int type, bool vec, bool whole) {
     if (a.rows == 0) return "layer_norm_columns";

@@ -20,10 +20,10 @@
 // three products hi hi + hi lo + lo hi make a product good to about 2^-21.  One product
 // of single halves loses 2e-3 to 2e-2 of the result's norm over five rounds, these three
 // 1e-6 to 1e-5 (8e-5 where u is one direction), 0.2 to 2.6 times what 32-bit products do.
-// s is 2^15 for X and A, whose elements
-// stay below sqrt(2) and 2, 2^13 for C, below 8, and 2^14 for P, below 4 (the host
-// checks the coefficients for it): nothing overflows, and an element of rms
-// 1 / sqrt(m n), the smallest that occurs throughout, has its 22 bits up to m n = 2^30.
+// s is 2^15 for X and A, whose elements stay below sqrt(2) and 2, 2^13 for C, below 8, 2^14
+// for P, below 4, and 2^12 for the product of two of them (the host checks the coefficients
+// for it): nothing overflows, and an element of rms 1 / sqrt(m n), the smallest that occurs
+// throughout (|a| is 1 or more), has its 22 bits up to m n = 2^30.
 //
 // What bounds it: three products of halves each, 1718 TFLOP/s of them sustained, so 573
 // of the results' own; the operands: an SM takes in 64 bytes a clock, a 128 x 128
@@ -31,8 +31,8 @@
 // and the sums: 64 of k take a 128 x 64 tile 0.61 us, a 128 x 128 one 0.76 (the products
 // 0.45), a pair's 256 x 256 one 1.08 to 1.27.  Eight matrices of 2048 x 2048 run at 477
 // (2.88 ms), 14 of a Llama-1B layer pair at 524 counted round by round (9.0 ms: rounds in
-// twos do less).  A few small matrices are bound by their chain of 15 to 17 steps, 3 to 5 us each
-// beside the products: 0.75 for the first operands, 0.3 to read the sums, 1 to 2 to turn
+// twos do less).  A few small matrices are bound by their chain of 15 to 17 steps, 3 to 5 us
+// each beside the products: 0.75 for the first operands, 0.3 to read the sums, 1 to 2 to turn
 // them into halves, 0.5 for the stores to be seen, 1.5 until another SM knows (256 x 256:
 // 92 to 98 us).
 //
@@ -678,10 +678,10 @@ __global__ void __launch_bounds__(256) matrix_moments(const __grid_constant__ Ma
     int64_t at = 0;                              // elements done in vectors
     if (x.flat) {
         at = n / 8 * 8;
-        for (int64_t i = first; i < n / 8; i += next) 
+        for (int64_t i = first; i < n / 8; i += next)
             moments_of<T, 8>(x, g, coef, 8 * i, &sum, &large);
     }
-    for (int64_t i = at + first; i < n; i += next) 
+    for (int64_t i = at + first; i < n; i += next)
         moments_of<T, 1>(x, g, coef, i, &sum, &large);
 #pragma unroll
     for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
